@@ -70,6 +70,10 @@ extern "C" {
 #define DQ4_ERR_LAUNCH 9           /* the CUDA runtime reported an error at launch */
 #define DQ4_ERR_TOO_LARGE 10       /* more scratch needed than given (the static array) */
 #define DQ4_ERR_CUBLAS 11          /* reserved: no entry point calls cuBLAS any more */
+#define DQ4_ERR_HEADS 12           /* head counts or a head size that is not supported */
+#define DQ4_ERR_ROTARY 13          /* the rotation's size or tables do not fit the heads */
+#define DQ4_ERR_PAGE 14            /* tokens per page not 16, 32, 64, 128 or 256 */
+#define DQ4_ERR_WORKSPACE 15       /* the workspace is NULL or smaller than needed */
 
 /* Version of this interface (incremented on any change of a signature). */
 int dq4_abi_version(void);

@@ -1,0 +1,384 @@
+"""ctypes binding of include/dq4_attn.h: argument marshalling only, as in _binding.
+
+The attention around the 4-bit projections: the norm of queries and keys with the position
+rotation (forward and backward), the append to a paged 8-bit key/value cache, and the attention
+that reads it.  Everything is asynchronous on ``stream`` (default: the current one) and reads
+lengths, pages and positions on the device: nothing here waits for the GPU.
+"""
+
+from __future__ import annotations
+
+import ctypes
+import math
+from typing import Optional, Tuple
+
+import torch
+
+from ._binding import _DTYPE_CODE, Dq4Error, _check, _stream_handle, get_lib
+
+_HALF = (torch.float16, torch.bfloat16)
+PAGE_TOKENS = (16, 32, 64, 128, 256)
+HEAD_DIMS = (64, 128)
+
+
+class _Cache(ctypes.Structure):
+    """dq4_kv8_cache of dq4_attn.h."""
+
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("pages", ctypes.c_int64),
+                ("kv_heads", ctypes.c_int32), ("page", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32)]
+
+
+_LIB = None
+
+
+def _lib() -> ctypes.CDLL:
+    global _LIB
+    if _LIB is None:
+        L = get_lib()
+        p, i64, i32, f32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_float
+        L.dq4_qk_norm_rope.argtypes = [p, i64, i64, p, i64, i64, i32, i64, i32, i32, i32, p, p,
+                                       f32, p, p, i64, i32, i32, p, p, p, p, p]
+        L.dq4_qk_norm_rope.restype = ctypes.c_int
+        L.dq4_qk_norm_rope_backward.argtypes = [p, p, p, i64, i64, p, i64, i64, i32, i64, i32,
+                                                i32, i32, p, p, f32, p, p, i64, i32, i32, p, p,
+                                                p, p, p, p, i64, p, p]
+        L.dq4_qk_norm_rope_backward.restype = ctypes.c_int
+        L.dq4_qk_norm_rope_backward_workspace_bytes.argtypes = [i32]
+        L.dq4_qk_norm_rope_backward_workspace_bytes.restype = i64
+        L.dq4_kv8_append.argtypes = [p, p, i64, i64, p, i64, i64, i32, i64, p, i64, i32, p, p,
+                                     i64, p, p, i64, i32, i32, p, p]
+        L.dq4_kv8_append.restype = ctypes.c_int
+        L.dq4_kv8_attention.argtypes = [p, p, i64, i64, i32, i64, i32, p, i64, i32, p, p, i64,
+                                        i32, f32, i32, i32, p, p, p, i64, p, p]
+        L.dq4_kv8_attention.restype = ctypes.c_int
+        L.dq4_kv8_attention_workspace_bytes.argtypes = [i64, i64, i32, i32, i32]
+        L.dq4_kv8_attention_workspace_bytes.restype = i64
+        _LIB = L
+    return _LIB
+
+
+# ------------------------------------------------------------- helpers
+_WORKSPACES = {}
+
+
+def _workspace(need: int, what: str, device, handle) -> torch.Tensor:
+    """The cached zero-filled workspace of (operator, device, stream), grown to `need` bytes."""
+    key = (what, device.index, handle)
+    ws = _WORKSPACES.get(key)
+    if ws is None or ws.numel() < need:
+        ws = torch.zeros(max(need, 1), dtype=torch.uint8, device=device)
+        torch.cuda.synchronize(device)  # zero-filled before any stream uses it
+        _WORKSPACES[key] = ws
+    return ws
+
+
+def _own_workspace(workspace, need: int, what: str, device, handle) -> torch.Tensor:
+    if workspace is None:
+        return _workspace(need, what, device, handle)
+    _check(workspace, "workspace", torch.uint8, need, device)
+    return workspace
+
+
+def _heads(t: torch.Tensor, name: str, dtype, device) -> None:
+    """A tokens x heads x head_dim tensor: any strides, but a head's values contiguous."""
+    if t.device.type != "cuda":
+        raise ValueError(f"{name}: must be a CUDA tensor (the library reads device memory)")
+    if t.device != device:
+        raise ValueError(f"{name}: expected a tensor on {device}, got {t.device}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
+    if t.dim() != 3:
+        raise ValueError(f"{name}: must be tokens x heads x head_dim, got {tuple(t.shape)}")
+    if t.shape[2] > 1 and t.stride(2) != 1 and t.numel():
+        raise ValueError(f"{name}: the values of a head must be contiguous")
+
+
+def _output(out, name: str, shape, dtype, device) -> torch.Tensor:
+    if out is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if tuple(out.shape) != tuple(shape):
+        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(out.shape)}")
+    _check(out, name, dtype, 0, device)
+    return out
+
+
+def _bad(bad, device) -> Optional[int]:
+    if bad is None:
+        return None
+    _check(bad, "bad", torch.int32, 1, device)
+    return bad.data_ptr()
+
+
+def _tables(cos, sin, device) -> Tuple[Optional[int], Optional[int], int, int]:
+    """(cos, sin, rows, rotary) of the rotation's tables."""
+    if (cos is None) != (sin is None):
+        raise ValueError("cos and sin come together")
+    if cos is None:
+        return None, None, 0, 0
+    if cos.dim() != 2 or cos.shape != sin.shape:
+        raise ValueError(f"cos and sin must be positions x rotary / 2 and alike, got "
+                         f"{tuple(cos.shape)} and {tuple(sin.shape)}")
+    _check(cos, "cos", torch.float32, 0, device)
+    _check(sin, "sin", torch.float32, 0, device)
+    return cos.data_ptr(), sin.data_ptr(), cos.shape[0], 2 * cos.shape[1]
+
+
+# ------------------------------------------------------------- norm and rotation
+def _norm_inputs(q, k, q_weight, k_weight, cos, sin, positions):
+    """Checked inputs: (tokens, heads, kv heads, head_dim, tables, positions)."""
+    device, dtype = q.device, q.dtype
+    if dtype not in _DTYPE_CODE:
+        raise TypeError(f"q: unsupported dtype {dtype}")
+    _heads(q, "q", dtype, device)
+    tokens, hq, dim = q.shape
+    hk = 0
+    if k is not None:
+        _heads(k, "k", dtype, device)
+        hk = k.shape[1]
+        if k.shape[0] != tokens or k.shape[2] != dim:
+            raise ValueError(f"k {tuple(k.shape)} does not go with q {tuple(q.shape)}")
+    if k is not None and (q_weight is None) != (k_weight is None):
+        raise ValueError("q_weight and k_weight come together")
+    if q_weight is not None:
+        _check(q_weight, "q_weight", dtype, dim, device)
+        if k is not None:
+            _check(k_weight, "k_weight", dtype, dim, device)
+    tables = _tables(cos, sin, device)
+    if cos is not None:
+        if positions is None:
+            raise ValueError("positions: needed with cos and sin")
+        _check(positions, "positions", torch.int64, tokens, device)
+    return tokens, hq, hk, dim, tables
+
+
+def _norm_args(q, k, q_weight, k_weight, eps, tokens, hq, hk, dim, tables, interleaved,
+               positions):
+    qs = q.stride()
+    ks = k.stride() if k is not None else (0, 0)
+    return (q.data_ptr(), qs[0], qs[1], None if k is None else k.data_ptr(), ks[0], ks[1],
+            _DTYPE_CODE[q.dtype], tokens, hq, hk, dim,
+            None if q_weight is None else q_weight.data_ptr(),
+            None if q_weight is None or k is None else k_weight.data_ptr(), eps, tables[0],
+            tables[1], tables[2], tables[3], interleaved,
+            None if tables[0] is None else positions.data_ptr())
+
+
+def qk_norm_rope(q: torch.Tensor, k: Optional[torch.Tensor], q_weight: Optional[torch.Tensor],
+                 k_weight: Optional[torch.Tensor], cos: Optional[torch.Tensor] = None,
+                 sin: Optional[torch.Tensor] = None, positions: Optional[torch.Tensor] = None,
+                 eps: float = 1e-6, interleaved: bool = False,
+                 q_out: Optional[torch.Tensor] = None, k_out: Optional[torch.Tensor] = None,
+                 bad: Optional[torch.Tensor] = None, stream=None):
+    """Norm and rotation of every head of q and k in one launch; returns (q_out, k_out).
+
+    ``y = R(positions[t]) (w * x / sqrt(mean(x^2) + eps))`` for q (tokens x heads x head_dim)
+    and k (tokens x kv_heads x head_dim, or None), float16, bfloat16 or float32, with any
+    strides between tokens and heads (views of a fused projection).  Without weights there is
+    no norm; without ``cos`` and ``sin`` (float32 tables, positions x rotary / 2) no rotation.
+    ``interleaved`` pairs values 2i and 2i + 1, else i and i + rotary / 2.  A position outside
+    the tables yields zeros, counted into ``bad`` (int32) for each head.
+    """
+    tokens, hq, hk, dim, tables = _norm_inputs(q, k, q_weight, k_weight, cos, sin, positions)
+    device = q.device
+    q_out = _output(q_out, "q_out", (tokens, hq, dim), q.dtype, device)
+    if k is not None:
+        k_out = _output(k_out, "k_out", (tokens, hk, dim), q.dtype, device)
+    st = _lib().dq4_qk_norm_rope(
+        *_norm_args(q, k, q_weight, k_weight, eps, tokens, hq, hk, dim, tables, interleaved,
+                    positions),
+        q_out.data_ptr(), None if k is None else k_out.data_ptr(), _bad(bad, device),
+        _stream_handle(stream, device))
+    if st:
+        raise Dq4Error(st, "dq4_qk_norm_rope")
+    return q_out, k_out
+
+
+def qk_norm_rope_backward(dq_out: torch.Tensor, dk_out: Optional[torch.Tensor],
+                          q: torch.Tensor, k: Optional[torch.Tensor],
+                          q_weight: Optional[torch.Tensor], k_weight: Optional[torch.Tensor],
+                          cos: Optional[torch.Tensor] = None, sin: Optional[torch.Tensor] = None,
+                          positions: Optional[torch.Tensor] = None, eps: float = 1e-6,
+                          interleaved: bool = False, dq: Optional[torch.Tensor] = None,
+                          dk: Optional[torch.Tensor] = None,
+                          workspace: Optional[torch.Tensor] = None,
+                          bad: Optional[torch.Tensor] = None, stream=None):
+    """The gradients of :func:`qk_norm_rope`: (dq, dk, dq_weight, dk_weight).
+
+    ``dq_out`` and ``dk_out`` are the outputs' gradients (contiguous, q's dtype); the weights'
+    gradients are float32 (None without weights), summed in a fixed order.  ``workspace``
+    (uint8, zero-filled before its first use) holds partial sums; by default a cached buffer
+    per (device, stream) is used.
+    """
+    tokens, hq, hk, dim, tables = _norm_inputs(q, k, q_weight, k_weight, cos, sin, positions)
+    device, dtype = q.device, q.dtype
+    _check(dq_out, "dq_out", dtype, tokens * hq * dim, device)
+    if k is not None:
+        if dk_out is None:
+            raise ValueError("dk_out: needed with k")
+        _check(dk_out, "dk_out", dtype, tokens * hk * dim, device)
+    dq = _output(dq, "dq", (tokens, hq, dim), dtype, device)
+    if k is not None:
+        dk = _output(dk, "dk", (tokens, hk, dim), dtype, device)
+    handle = _stream_handle(stream, device)
+    dqw = dkw = ws = None
+    if q_weight is not None:
+        dqw = torch.empty(dim, dtype=torch.float32, device=device)
+        if k is not None:
+            dkw = torch.empty(dim, dtype=torch.float32, device=device)
+        need = _lib().dq4_qk_norm_rope_backward_workspace_bytes(dim)
+        ws = _own_workspace(workspace, need, "norm", device, handle)
+    st = _lib().dq4_qk_norm_rope_backward(
+        dq_out.data_ptr(), None if k is None else dk_out.data_ptr(),
+        *_norm_args(q, k, q_weight, k_weight, eps, tokens, hq, hk, dim, tables, interleaved,
+                    positions),
+        dq.data_ptr(), None if k is None else dk.data_ptr(),
+        None if dqw is None else dqw.data_ptr(), None if dkw is None else dkw.data_ptr(),
+        None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel(),
+        _bad(bad, device), handle)
+    if st:
+        raise Dq4Error(st, "dq4_qk_norm_rope_backward")
+    return dq, dk, dqw, dkw
+
+
+# ------------------------------------------------------------- the cache
+class KV8Cache:
+    """A paged key/value cache in 8 bits: e4m3 codes and one scale for each page and head.
+
+    ``k`` and ``v`` are float8_e4m3fn [pages, kv_heads, page, head_dim], ``k_scale`` and
+    ``v_scale`` float32 [pages, kv_heads]; a stored value is code * scale.  Nothing has to be
+    initialized: slots and scales are read only where tokens were appended.
+    """
+
+    def __init__(self, k: torch.Tensor, v: torch.Tensor, k_scale: torch.Tensor,
+                 v_scale: torch.Tensor):
+        if k.dim() != 4:
+            raise ValueError(f"k: must be pages x kv_heads x page x head_dim, got "
+                             f"{tuple(k.shape)}")
+        pages, heads, page, dim = k.shape
+        if page not in PAGE_TOKENS:
+            raise ValueError(f"k: a page holds {PAGE_TOKENS} tokens, got {page}")
+        if dim not in HEAD_DIMS:
+            raise ValueError(f"k: head_dim must be one of {HEAD_DIMS}, got {dim}")
+        if v.shape != k.shape:
+            raise ValueError(f"v: expected shape {tuple(k.shape)}, got {tuple(v.shape)}")
+        for t, name in ((k, "k"), (v, "v")):
+            _check(t, name, torch.float8_e4m3fn, k.numel(), k.device)
+        for t, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+            if tuple(t.shape) != (pages, heads):
+                raise ValueError(f"{name}: expected shape {(pages, heads)}, got "
+                                 f"{tuple(t.shape)}")
+            _check(t, name, torch.float32, pages * heads, k.device)
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.device, self.kv_heads, self.page, self.head_dim = k.device, heads, page, dim
+        self.c = _Cache(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+                        pages, heads, page, dim)
+        self.ref = ctypes.addressof(self.c)
+
+    @classmethod
+    def empty(cls, pages: int, kv_heads: int, page: int, head_dim: int, device="cuda"):
+        """A cache of its own tensors."""
+        shape = (pages, kv_heads, page, head_dim)
+        codes = [torch.empty(shape, dtype=torch.float8_e4m3fn, device=device) for _ in range(2)]
+        scales = [torch.empty(shape[:2], dtype=torch.float32, device=device) for _ in range(2)]
+        return cls(*codes, *scales)
+
+
+def _batch(cache, tokens: int, block_table, seq_lens, cu):
+    """Checked pointers of the ragged batch: (table, stride, width, lens, cu, sequences)."""
+    device = cache.device
+    if block_table.dim() != 2:
+        raise ValueError(f"block_table: must be sequences x pages, got "
+                         f"{tuple(block_table.shape)}")
+    seqs, width = block_table.shape
+    if block_table.dtype != torch.int32 or block_table.device != device or (
+            width > 1 and block_table.stride(1) != 1):
+        raise ValueError(f"block_table: must be int32 rows on {device}")
+    _check(seq_lens, "seq_lens", torch.int32, seqs, device)
+    if cu is None:
+        if tokens != seqs:
+            raise ValueError(f"{tokens} tokens for {seqs} sequences: cu says how many each has")
+        return block_table.data_ptr(), block_table.stride(0), width, seq_lens.data_ptr(), None, \
+            seqs
+    _check(cu, "cu", torch.int32, seqs + 1, device)
+    return block_table.data_ptr(), block_table.stride(0), width, seq_lens.data_ptr(), \
+        cu.data_ptr(), seqs
+
+
+def kv8_append(cache: KV8Cache, k: torch.Tensor, v: torch.Tensor, block_table: torch.Tensor,
+               seq_lens: torch.Tensor, cu: Optional[torch.Tensor] = None,
+               cos: Optional[torch.Tensor] = None, sin: Optional[torch.Tensor] = None,
+               interleaved: bool = False, bad: Optional[torch.Tensor] = None,
+               stream=None) -> None:
+    """Append tokens to the cache, keys rotated by their positions on the way; one launch.
+
+    k and v are tokens x kv_heads x head_dim (float16 or bfloat16).  Sequence b's are rows
+    ``cu[b] .. cu[b + 1] - 1`` (int32; None: one each), its length with them ``seq_lens[b]``
+    (int32), and page ``block_table[b, j]`` (int32) holds its tokens from j * page on.  Scales
+    are the least powers of two that fit; a page whose scale grows has its earlier codes
+    rescaled.  ``bad`` (int32) counts tokens that have no place.
+    """
+    if k.dtype not in _HALF:
+        raise TypeError("k must be float16 or bfloat16")
+    device = cache.device
+    _heads(k, "k", k.dtype, device)
+    _heads(v, "v", k.dtype, device)
+    tokens = k.shape[0]
+    if k.shape != v.shape or k.shape[1] != cache.kv_heads or k.shape[2] != cache.head_dim:
+        raise ValueError(f"k {tuple(k.shape)} and v {tuple(v.shape)}: expected (tokens, "
+                         f"{cache.kv_heads}, {cache.head_dim})")
+    table, stride, width, lens, cu_ptr, seqs = _batch(cache, tokens, block_table, seq_lens, cu)
+    tables = _tables(cos, sin, device)
+    ks, vs = k.stride(), v.stride()
+    st = _lib().dq4_kv8_append(
+        cache.ref, k.data_ptr(), ks[0], ks[1], v.data_ptr(), vs[0], vs[1], _DTYPE_CODE[k.dtype],
+        tokens, table, stride, width, lens, cu_ptr, seqs, *tables, interleaved,
+        _bad(bad, device), _stream_handle(stream, device))
+    if st:
+        raise Dq4Error(st, "dq4_kv8_append")
+
+
+def kv8_attention(cache: KV8Cache, q: torch.Tensor, block_table: torch.Tensor,
+                  seq_lens: torch.Tensor, cu: Optional[torch.Tensor] = None,
+                  max_new: Optional[int] = None, scale: Optional[float] = None,
+                  causal: bool = True, window: int = 0, out: Optional[torch.Tensor] = None,
+                  return_lse: bool = False, workspace: Optional[torch.Tensor] = None,
+                  bad: Optional[torch.Tensor] = None, stream=None):
+    """Attention of q (tokens x heads x head_dim, float16 or bfloat16) over the cache.
+
+    The batch is given as for :func:`kv8_append`; a token at position p sees its sequence's
+    keys j <= p (all of them if not ``causal``) with j > p - window if ``window`` > 0.
+    ``scale`` defaults to 1 / sqrt(head_dim); ``max_new`` is the most new tokens of a sequence
+    (an estimate will do: it chooses the kernel; default 1, or the mean with ``cu``).  Returns
+    ``out`` (tokens x heads x head_dim), or (out, lse) with the float32 log-sums.  A row that
+    sees no key gets zeros and -inf.  ``workspace`` (uint8, zero-filled before its first use)
+    holds partial results; by default a cached buffer per (device, stream) is used.
+    """
+    if q.dtype not in _HALF:
+        raise TypeError("q must be float16 or bfloat16")
+    device = cache.device
+    _heads(q, "q", q.dtype, device)
+    tokens, heads, dim = q.shape
+    if dim != cache.head_dim or heads % cache.kv_heads:
+        raise ValueError(f"q {tuple(q.shape)}: the cache has {cache.kv_heads} heads of "
+                         f"{cache.head_dim}")
+    table, stride, width, lens, cu_ptr, seqs = _batch(cache, tokens, block_table, seq_lens, cu)
+    if max_new is None:
+        max_new = 1 if cu is None else -(-tokens // max(seqs, 1))
+    out = _output(out, "out", (tokens, heads, dim), q.dtype, device)
+    lse = torch.empty((tokens, heads), dtype=torch.float32, device=device) if return_lse else None
+    handle = _stream_handle(stream, device)
+    L = _lib()
+    need = L.dq4_kv8_attention_workspace_bytes(tokens, seqs, heads, cache.kv_heads, dim)
+    ws = _own_workspace(workspace, need, "attention", device, handle)
+    qs = q.stride()
+    st = L.dq4_kv8_attention(
+        cache.ref, q.data_ptr(), qs[0], qs[1], _DTYPE_CODE[q.dtype], tokens, heads, table,
+        stride, width, lens, cu_ptr, seqs, max_new,
+        1 / math.sqrt(dim) if scale is None else scale, causal, window, out.data_ptr(),
+        None if lse is None else lse.data_ptr(), ws.data_ptr(), ws.numel(), _bad(bad, device),
+        handle)
+    if st:
+        raise Dq4Error(st, "dq4_kv8_attention")
+    return (out, lse) if return_lse else out

@@ -24,7 +24,8 @@ STATUS_NAMES = {
     0: "DQ4_OK", 1: "DQ4_ERR_NULL", 2: "DQ4_ERR_N", 3: "DQ4_ERR_BLOCKSIZE",
     4: "DQ4_ERR_NESTED_BLOCKSIZE", 5: "DQ4_ERR_DTYPE", 6: "DQ4_ERR_ALIGN",
     7: "DQ4_ERR_DEVICE", 8: "DQ4_ERR_ARCH", 9: "DQ4_ERR_LAUNCH", 10: "DQ4_ERR_TOO_LARGE",
-    11: "DQ4_ERR_CUBLAS",
+    11: "DQ4_ERR_CUBLAS", 12: "DQ4_ERR_HEADS", 13: "DQ4_ERR_ROTARY", 14: "DQ4_ERR_PAGE",
+    15: "DQ4_ERR_WORKSPACE",
 }
 
 

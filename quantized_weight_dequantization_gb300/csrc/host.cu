@@ -123,6 +123,10 @@ const char* dq4_status_string(int status) {
       return "the problem needs more scratch than given (DQ4_STATIC_SCRATCH_BLOCKS for the "
              "static array; one row of W for a transient buffer)";
     case DQ4_ERR_CUBLAS: return "reserved (no entry point calls cuBLAS)";
+    case DQ4_ERR_HEADS: return "the head counts or the head size are not supported";
+    case DQ4_ERR_ROTARY: return "the rotation's size or tables do not fit the heads";
+    case DQ4_ERR_PAGE: return "a page must hold 16, 32, 64, 128 or 256 tokens";
+    case DQ4_ERR_WORKSPACE: return "the workspace is NULL or smaller than needed";
     default: return "unknown status";
   }
 }

@@ -1,0 +1,547 @@
+// Norm and rotation of every head of queries and keys, and its gradients:
+// dq4_qk_norm_rope and dq4_qk_norm_rope_backward (dq4_attn.h).
+//
+// Forward, for a head x of D values at position p:
+//   y = R(p) (w x r),  r = 1 / sqrt(mean(x^2) + eps)
+// Backward, with g = R(-p) dy (R is orthogonal, so its transpose is R(-p)), xh = x r:
+//   dx = r (g w - xh mean(g w xh)),   dw = sum over tokens and heads of g xh
+// Both read every value once and write every result once; they are bound by HBM.
+#include "attn.cuh"
+
+namespace dq4d {
+namespace {
+
+constexpr int kNormThreads = 256;  // forward: 8 warps
+constexpr int kBwdThreads = 512;   // backward: 16 warps, each with weight-gradient sums
+constexpr int kMaxPartials = 512;  // CTAs that may leave weight-gradient partials
+constexpr int kMaxDim = 1024;
+constexpr int kAnyWarps = 4;       // warps per CTA of the any-size kernels
+
+struct NormArgs {
+  const void* x[2];        // q, k
+  const void* dy[2];       // backward: gradients of the outputs
+  int64_t token_stride[2], head_stride[2];
+  const void* w[2];        // weights, or null
+  void* out[2];            // outputs; backward: dx
+  int heads[2];
+  int64_t tokens;
+  float eps;
+  const float* cos;
+  const float* sin;
+  int64_t table_rows;
+  int dim, rotary;
+  bool interleaved;
+  const int64_t* positions;
+  int* bad;
+  int chunks[2];           // head chunks of a token, of q and of k
+  int chunk;               // heads in a chunk
+  float* dw[2];
+  int* count;              // backward: CTAs that left their partials
+  float* part;             // backward: [CTA][2][dim]
+};
+
+// The position's row of the tables, or -1 where it is outside them (all lanes alike).
+__device__ __forceinline__ int64_t table_row(const NormArgs& p, int64_t t) {
+  if (p.cos == nullptr) return 0;
+  const int64_t pos = __ldg(p.positions + t);
+  return pos >= 0 && pos < p.table_rows ? pos : -1;
+}
+
+template <int kLanes>
+__device__ __forceinline__ float group_sum(float v) {
+#pragma unroll
+  for (int o = kLanes / 2; o > 0; o >>= 1) v += __shfl_xor_sync(kAllLanes, v, o);
+  return v;
+}
+
+// A warp takes a unit: kRows heads of one token for each of its 32 / kLanes groups of
+// kLanes = kDim / 8 lanes, all of q or all of k.  The position's cosines and sines and the
+// weights stay in registers over the unit, and all its loads are issued before the first
+// use.  kRows = 4 once that still gives every SM its 64 warps; with fewer units
+// one row a lane leaves more warps, and the latency of one row, to each SM (kRows = 4
+// against 1: see the launch).
+template <int DT, int kDim, int kRows>
+__global__ void __launch_bounds__(kNormThreads) dq4_qk_norm_kernel(const NormArgs p) {
+  using T = typename Elem<DT>::T;
+  constexpr int kLanes = kDim / 8, kGroups = 32 / kLanes;
+  wait_for_stream();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int l = lane % kLanes, group = lane / kLanes;
+  const int per_token = p.chunks[0] + p.chunks[1];
+  const int64_t unit = int64_t(blockIdx.x) * (kNormThreads / 32) + warp;
+  const int64_t t = unit / per_token;
+  if (t >= p.tokens) return;
+  int c = int(unit - t * per_token);
+  const int which = c >= p.chunks[0];
+  if (which) c -= p.chunks[0];
+  const int h0 = c * (kRows * kGroups) + group;
+  const int heads = p.heads[which];
+  const LanePlace at = lane_place(l, p.cos ? p.rotary : 0, p.interleaved);
+  const T* x = static_cast<const T*>(p.x[which]) + t * p.token_stride[which];
+  Raw4<DT> ra[kRows], rb[kRows];
+#pragma unroll
+  for (int i = 0; i < kRows; ++i) {
+    const int h = min(h0 + i * kGroups, heads - 1);
+    const T* row = x + h * p.head_stride[which];
+    ra[i] = load4<DT>(row + at.a);
+    rb[i] = load4<DT>(row + at.b);
+  }
+  const bool normed = p.w[which] != nullptr;
+  F4 wa, wb;
+  if (normed) {
+    const T* w = static_cast<const T*>(p.w[which]);
+    wa = widen<DT>(load4<DT>(w + at.a));
+    wb = widen<DT>(load4<DT>(w + at.b));
+  }
+  const int64_t row = table_row(p, t);
+  float4 cs = {}, sn = {};
+  if (at.turned && row >= 0) {
+    cs = __ldg(reinterpret_cast<const float4*>(p.cos + row * (p.rotary / 2) + 4 * l));
+    sn = __ldg(reinterpret_cast<const float4*>(p.sin + row * (p.rotary / 2) + 4 * l));
+  }
+  T* out = static_cast<T*>(p.out[which]) + t * heads * kDim;
+#pragma unroll
+  for (int i = 0; i < kRows; ++i) {
+    const int h = h0 + i * kGroups;
+    F4 a = widen<DT>(ra[i]), b = widen<DT>(rb[i]);
+    if (normed) {
+      float ss = 0.f;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) ss = fmaf(a.v[j], a.v[j], fmaf(b.v[j], b.v[j], ss));
+      const float r = rsqrtf(group_sum<kLanes>(ss) * (1.f / kDim) + p.eps);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        a.v[j] = a.v[j] * r * wa.v[j];
+        b.v[j] = b.v[j] * r * wb.v[j];
+      }
+    }
+    if (at.turned) turn(a, b, cs, sn, p.interleaved);
+    if (row < 0) a = b = F4{};
+    if (h < heads) {
+      store4<DT>(out + h * kDim + at.a, a);
+      store4<DT>(out + h * kDim + at.b, b);
+      if (row < 0 && l == 0 && p.bad) atomicAdd(p.bad, 1);
+    }
+  }
+}
+
+// Sum the CTAs' partial weight gradients, in CTA order within each of the thread groups
+// that share the columns and then in group order, by the last CTA to leave its own: the
+// order does not depend on which CTA that is.  `mine` is this CTA's [2][dim] in shared
+// memory, whose storage holds 2 x blockDim floats at least.
+__device__ void finish_weights(const NormArgs& p, float* mine) {
+  __shared__ bool last;
+  const int cols = 2 * p.dim;
+  float* part = p.part + int64_t(blockIdx.x) * cols;
+  for (int i = threadIdx.x; i < cols; i += blockDim.x) part[i] = mine[i];
+  __threadfence();
+  __syncthreads();
+  if (threadIdx.x == 0) last = atomicAdd(p.count, 1) == int(gridDim.x) - 1;
+  __syncthreads();
+  if (!last) return;
+  __threadfence();
+  const int groups = max(1, int(blockDim.x) / cols);
+  for (int i0 = 0; i0 < cols; i0 += blockDim.x) {
+    const int g = threadIdx.x / min(cols, int(blockDim.x));
+    const int i = i0 + threadIdx.x % min(cols, int(blockDim.x));
+    float s = 0.f;
+    if (i < cols && g < groups)
+      for (int c = g; c < int(gridDim.x); c += groups) s += __ldcg(p.part + int64_t(c) * cols + i);
+    __syncthreads();
+    mine[threadIdx.x] = s;
+    __syncthreads();
+    if (i < cols && g == 0) {
+      for (int o = 1; o < groups; ++o) s += mine[threadIdx.x + o * cols];
+      float* dw = p.dw[i >= p.dim];
+      if (dw) dw[i >= p.dim ? i - p.dim : i] = s;
+    }
+  }
+  if (threadIdx.x == 0) *p.count = 0;  // ready for the next call
+}
+
+// The backward pass in the forward kernel's layout.  A warp walks the units with a fixed
+// stride and keeps, in each lane, the sums of its eight columns of the weight gradients of
+// q and of k; lanes, warps and CTAs are then summed in a fixed order.
+template <int DT, int kDim, int kRows>
+__global__ void __launch_bounds__(kBwdThreads) dq4_qk_norm_backward_kernel(const NormArgs p) {
+  using T = typename Elem<DT>::T;
+  constexpr int kLanes = kDim / 8, kGroups = 32 / kLanes, kWarps = kBwdThreads / 32;
+  __shared__ float sums[kWarps * 2 * kDim];
+  wait_for_stream();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int l = lane % kLanes, group = lane / kLanes;
+  const int per_token = p.chunks[0] + p.chunks[1];
+  const int64_t units = p.tokens * per_token;
+  const LanePlace at = lane_place(l, p.cos ? p.rotary : 0, p.interleaved);
+  F4 dwa[2] = {}, dwb[2] = {};
+  for (int64_t unit = int64_t(blockIdx.x) * kWarps + warp; unit < units;
+       unit += int64_t(gridDim.x) * kWarps) {
+    const int64_t t = unit / per_token;
+    int c = int(unit - t * per_token);
+    const int which = c >= p.chunks[0];
+    if (which) c -= p.chunks[0];
+    const int h0 = c * (kRows * kGroups) + group;
+    const int heads = p.heads[which];
+    const T* x = static_cast<const T*>(p.x[which]) + t * p.token_stride[which];
+    const T* dy = static_cast<const T*>(p.dy[which]) + t * heads * kDim;
+    Raw4<DT> ra[kRows], rb[kRows], ga[kRows], gb[kRows];
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+      const int h = min(h0 + i * kGroups, heads - 1);
+      ra[i] = load4<DT>(x + h * p.head_stride[which] + at.a);
+      rb[i] = load4<DT>(x + h * p.head_stride[which] + at.b);
+      ga[i] = load4<DT>(dy + h * kDim + at.a);
+      gb[i] = load4<DT>(dy + h * kDim + at.b);
+    }
+    const bool normed = p.w[which] != nullptr;
+    F4 wa, wb;
+    if (normed) {
+      const T* w = static_cast<const T*>(p.w[which]);
+      wa = widen<DT>(load4<DT>(w + at.a));
+      wb = widen<DT>(load4<DT>(w + at.b));
+    }
+    const int64_t row = table_row(p, t);
+    float4 cs = {}, sn = {};
+    if (at.turned && row >= 0) {
+      cs = __ldg(reinterpret_cast<const float4*>(p.cos + row * (p.rotary / 2) + 4 * l));
+      sn = __ldg(reinterpret_cast<const float4*>(p.sin + row * (p.rotary / 2) + 4 * l));
+      sn = make_float4(-sn.x, -sn.y, -sn.z, -sn.w);
+    }
+    T* out = static_cast<T*>(p.out[which]) + t * heads * kDim;
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+      const int h = h0 + i * kGroups;
+      const bool real = h < heads && row >= 0;
+      F4 a = widen<DT>(ra[i]), b = widen<DT>(rb[i]);
+      F4 g = widen<DT>(ga[i]), k = widen<DT>(gb[i]);
+      if (at.turned) turn(g, k, cs, sn, p.interleaved);
+      if (normed) {
+        float ss = 0.f;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) ss = fmaf(a.v[j], a.v[j], fmaf(b.v[j], b.v[j], ss));
+        const float r = rsqrtf(group_sum<kLanes>(ss) * (1.f / kDim) + p.eps);
+        float dot = 0.f;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          a.v[j] *= r;  // xh
+          b.v[j] *= r;
+          if (real) {
+            const float ca = g.v[j] * a.v[j], cb = k.v[j] * b.v[j];
+            dwa[0].v[j] += which ? 0.f : ca;
+            dwb[0].v[j] += which ? 0.f : cb;
+            dwa[1].v[j] += which ? ca : 0.f;
+            dwb[1].v[j] += which ? cb : 0.f;
+          }
+          g.v[j] *= wa.v[j];
+          k.v[j] *= wb.v[j];
+          dot = fmaf(g.v[j], a.v[j], fmaf(k.v[j], b.v[j], dot));
+        }
+        const float m = group_sum<kLanes>(dot) * (1.f / kDim);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          g.v[j] = r * fmaf(-a.v[j], m, g.v[j]);
+          k.v[j] = r * fmaf(-b.v[j], m, k.v[j]);
+        }
+      }
+      if (row < 0) g = k = F4{};
+      if (h < heads) {
+        store4<DT>(out + h * kDim + at.a, g);
+        store4<DT>(out + h * kDim + at.b, k);
+        if (row < 0 && l == 0 && p.bad) atomicAdd(p.bad, 1);
+      }
+    }
+  }
+  if (p.dw[0] == nullptr) return;
+#pragma unroll
+  for (int n = 0; n < 2; ++n)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+#pragma unroll
+      for (int o = kLanes; o < 32; o <<= 1) {
+        dwa[n].v[j] += __shfl_xor_sync(kAllLanes, dwa[n].v[j], o);
+        dwb[n].v[j] += __shfl_xor_sync(kAllLanes, dwb[n].v[j], o);
+      }
+      if (group == 0) {
+        sums[(warp * 2 + n) * kDim + at.a + j] = dwa[n].v[j];
+        sums[(warp * 2 + n) * kDim + at.b + j] = dwb[n].v[j];
+      }
+    }
+  __syncthreads();
+  for (int i = threadIdx.x; i < 2 * kDim; i += kBwdThreads) {
+    float s = sums[i];
+    for (int w = 1; w < kWarps; ++w) s += sums[w * 2 * kDim + i];
+    sums[i] = s;
+  }
+  __syncthreads();
+  finish_weights(p, sums);
+}
+
+// Any even head size and rotation, any alignment: a warp per head, values lane, lane + 32
+// and so on, a value's partner read again from memory (L1).
+template <int DT, bool kBackward>
+__global__ void __launch_bounds__(32 * kAnyWarps) dq4_qk_norm_any_kernel(const NormArgs p) {
+  using T = typename Elem<DT>::T;
+  __shared__ float sums[kBackward ? kAnyWarps * 2 * kMaxDim : 1];
+  wait_for_stream();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int all_heads = p.heads[0] + p.heads[1];
+  const int64_t rows = p.tokens * all_heads;
+  const int half = p.rotary / 2;
+  float* mine = sums + (kBackward ? warp * 2 * p.dim : 0);
+  if constexpr (kBackward) {
+    for (int i = lane; i < 2 * p.dim; i += 32) mine[i] = 0.f;
+  }
+  for (int64_t r0 = int64_t(blockIdx.x) * kAnyWarps + warp; r0 < rows;
+       r0 += int64_t(gridDim.x) * kAnyWarps) {
+    const int64_t t = r0 / all_heads;
+    int h = int(r0 - t * all_heads);
+    const int which = h >= p.heads[0];
+    if (which) h -= p.heads[0];
+    const T* x = static_cast<const T*>(p.x[which]) + t * p.token_stride[which] +
+                 h * p.head_stride[which];
+    const int64_t o = (t * p.heads[which] + h) * p.dim;
+    const T* dy = kBackward ? static_cast<const T*>(p.dy[which]) + o : nullptr;
+    const T* w = static_cast<const T*>(p.w[which]);
+    T* out = static_cast<T*>(p.out[which]) + o;
+    const int64_t row = table_row(p, t);
+    float r = 1.f;
+    if (w) {
+      float ss = 0.f;
+      for (int i = lane; i < p.dim; i += 32) {
+        const float v = Elem<DT>::load(x + i);
+        ss = fmaf(v, v, ss);
+      }
+      r = rsqrtf(group_sum<32>(ss) / p.dim + p.eps);
+    }
+    // value i of the rotated (back: sign < 0) vector whose values f gives
+    auto turned = [&](auto f, int i, float sign) {
+      if (p.cos == nullptr || i >= p.rotary) return f(i);
+      const int j = p.interleaved ? i >> 1 : i % half;
+      const bool second = p.interleaved ? i & 1 : i >= half;
+      const int pair = p.interleaved ? i ^ 1 : second ? i - half : i + half;
+      const float c = __ldg(p.cos + row * half + j), s = sign * __ldg(p.sin + row * half + j);
+      const float v = __fmul_rn(f(i), c), u = __fmul_rn(f(pair), s);
+      return second ? __fadd_rn(v, u) : __fsub_rn(v, u);
+    };
+    if (row < 0) {
+      for (int i = lane; i < p.dim; i += 32) out[i] = Elem<DT>::make(0.f);
+      if (lane == 0 && p.bad) atomicAdd(p.bad, 1);
+      continue;
+    }
+    if constexpr (!kBackward) {
+      auto value = [&](int i) {
+        const float v = Elem<DT>::load(x + i);
+        return w ? v * r * Elem<DT>::load(w + i) : v;
+      };
+      for (int i = lane; i < p.dim; i += 32) out[i] = Elem<DT>::make(turned(value, i, 1.f));
+    } else {
+      auto value = [&](int i) { return Elem<DT>::load(dy + i); };
+      float dot = 0.f;
+      if (w) {
+        for (int i = lane; i < p.dim; i += 32) {
+          const float g = turned(value, i, -1.f), xh = Elem<DT>::load(x + i) * r;
+          mine[which * p.dim + i] += g * xh;
+          dot = fmaf(g * Elem<DT>::load(w + i), xh, dot);
+        }
+        dot = group_sum<32>(dot) / p.dim;
+      }
+      for (int i = lane; i < p.dim; i += 32) {
+        float g = turned(value, i, -1.f);
+        if (w) {
+          const float xh = Elem<DT>::load(x + i) * r;
+          g = r * fmaf(-xh, dot, g * Elem<DT>::load(w + i));
+        }
+        out[i] = Elem<DT>::make(g);
+      }
+    }
+  }
+  if constexpr (kBackward) {
+    if (p.dw[0] == nullptr) return;
+    __syncthreads();
+    for (int i = threadIdx.x; i < 2 * p.dim; i += 32 * kAnyWarps) {
+      float s = sums[i];
+      for (int v = 1; v < kAnyWarps; ++v) s += sums[v * 2 * p.dim + i];
+      sums[i] = s;
+    }
+    __syncthreads();
+    finish_weights(p, sums);
+  }
+}
+
+// ------------------------------------------------------------------------ host side
+int check_norm(const NormArgs& p, int32_t dtype) {
+  if (!valid_dtype(dtype, true)) return DQ4_ERR_DTYPE;
+  if (p.tokens < 0) return DQ4_ERR_N;
+  if (p.heads[0] < 1 || p.heads[1] < 0 || p.heads[0] > 65536 || p.heads[1] > 65536 ||
+      p.dim < 2 || p.dim > kMaxDim || p.dim % 2 != 0)
+    return DQ4_ERR_HEADS;
+  if ((p.cos == nullptr) != (p.sin == nullptr)) return DQ4_ERR_NULL;
+  if (p.cos && (p.rotary < 2 || p.rotary > p.dim || p.rotary % 2 != 0 || p.table_rows < 0))
+    return DQ4_ERR_ROTARY;
+  if (p.tokens == 0) return DQ4_OK;
+  if (p.cos && p.positions == nullptr) return DQ4_ERR_NULL;
+  if (p.cos && (misaligned(p.cos, 4) || misaligned(p.sin, 4) || misaligned(p.positions, 8)))
+    return DQ4_ERR_ALIGN;
+  const uintptr_t es = dtype == DQ4_OUT_F32 ? 4 : 2;
+  for (int n = 0; n < 2 && p.heads[n] > 0; ++n) {
+    if (!p.x[n] || !p.out[n]) return DQ4_ERR_NULL;
+    if ((p.w[0] == nullptr) != (p.w[n] == nullptr)) return DQ4_ERR_NULL;
+    if (misaligned(p.x[n], es) || misaligned(p.out[n], es) || misaligned(p.w[n], es))
+      return DQ4_ERR_ALIGN;
+  }
+  if (misaligned(p.bad, 4)) return DQ4_ERR_ALIGN;
+  return DQ4_OK;
+}
+
+// Whether the register kernels take this call (see lane_place and load4).
+bool in_registers(const NormArgs& p, int32_t dtype, bool backward) {
+  if (p.dim != 64 && p.dim != 128 && p.dim != 256) return false;
+  if (p.cos && (p.rotary % 8 != 0 || !aligned(p.cos, 16) || !aligned(p.sin, 16))) return false;
+  const uintptr_t to = dtype == DQ4_OUT_F32 ? 16 : 8;
+  for (int n = 0; n < 2 && p.heads[n] > 0; ++n) {
+    if (p.token_stride[n] % 4 != 0 || p.head_stride[n] % 4 != 0 || !aligned(p.x[n], to) ||
+        !aligned(p.out[n], to) || !aligned(p.w[n], to) || (backward && !aligned(p.dy[n], to)))
+      return false;
+  }
+  return true;
+}
+
+void cut_heads(NormArgs* p, int rows) {
+  p->chunk = rows * 32 / (p->dim / 8);
+  for (int n = 0; n < 2; ++n) p->chunks[n] = (p->heads[n] + p->chunk - 1) / p->chunk;
+}
+
+template <int DT, int kDim>
+int launch_forward(NormArgs p, int sms, cudaStream_t stream) {
+  constexpr int kWarps = kNormThreads / 32;
+  cut_heads(&p, 4);
+  const bool four = p.tokens * (p.chunks[0] + p.chunks[1]) >= int64_t(sms) * 64;
+  if (!four) cut_heads(&p, 1);
+  const int64_t grid = (p.tokens * (p.chunks[0] + p.chunks[1]) + kWarps - 1) / kWarps;
+  if (grid > kMaxGrid) return DQ4_ERR_N;
+  return launch_ordered(four ? dq4_qk_norm_kernel<DT, kDim, 4> : dq4_qk_norm_kernel<DT, kDim, 1>,
+                        dim3(unsigned(grid)), kNormThreads, 0, stream, p);
+}
+
+template <int DT, int kDim>
+int launch_backward(NormArgs p, int sms, cudaStream_t stream) {
+  constexpr int kWarps = kBwdThreads / 32;
+  cut_heads(&p, 2);
+  const int64_t units = p.tokens * (p.chunks[0] + p.chunks[1]);
+  const int64_t want = (units + kWarps - 1) / kWarps;
+  const int grid = int(want < 2 * sms ? want : 2 * sms);
+  return launch_ordered(dq4_qk_norm_backward_kernel<DT, kDim, 2>,
+                        dim3(unsigned(grid < kMaxPartials ? grid : kMaxPartials)), kBwdThreads, 0,
+                        stream, p);
+}
+
+template <int DT>
+int launch_norm(const NormArgs& p, bool backward, int sms, cudaStream_t stream) {
+  if (!in_registers(p, DT, backward)) {
+    const int64_t want = (p.tokens * (p.heads[0] + p.heads[1]) + kAnyWarps - 1) / kAnyWarps;
+    const int64_t most = backward ? kMaxPartials : 16 * sms;
+    const dim3 grid(unsigned(want < most ? want : most));
+    return backward
+               ? launch_ordered(dq4_qk_norm_any_kernel<DT, true>, grid, 32 * kAnyWarps, 0, stream, p)
+               : launch_ordered(dq4_qk_norm_any_kernel<DT, false>, grid, 32 * kAnyWarps, 0, stream,
+                                p);
+  }
+  switch (p.dim) {
+    case 64:
+      return backward ? launch_backward<DT, 64>(p, sms, stream)
+                      : launch_forward<DT, 64>(p, sms, stream);
+    case 128:
+      return backward ? launch_backward<DT, 128>(p, sms, stream)
+                      : launch_forward<DT, 128>(p, sms, stream);
+    default:
+      return backward ? launch_backward<DT, 256>(p, sms, stream)
+                      : launch_forward<DT, 256>(p, sms, stream);
+  }
+}
+
+int run_norm(const NormArgs& p, int32_t dtype, bool backward, void* stream) {
+  int dev, sms;
+  if (const int st = current_device(&dev, &sms)) return st;
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  switch (dtype) {
+    case DQ4_OUT_F16: return launch_norm<DQ4_OUT_F16>(p, backward, sms, s);
+    case DQ4_OUT_BF16: return launch_norm<DQ4_OUT_BF16>(p, backward, sms, s);
+    default: return launch_norm<DQ4_OUT_F32>(p, backward, sms, s);
+  }
+}
+
+}  // namespace
+}  // namespace dq4d
+
+using namespace dq4d;
+
+extern "C" {
+
+int dq4_qk_norm_rope(const void* q, int64_t q_token_stride, int64_t q_head_stride, const void* k,
+                     int64_t k_token_stride, int64_t k_head_stride, int32_t dtype,
+                     int64_t tokens, int32_t q_heads, int32_t k_heads, int32_t head_dim,
+                     const void* q_weight, const void* k_weight, float eps, const float* cos,
+                     const float* sin, int64_t table_rows, int32_t rotary, int32_t interleaved,
+                     const int64_t* positions, void* q_out, void* k_out, int* bad,
+                     void* stream) {
+  NormArgs p = {{q, k}, {}, {q_token_stride, k_token_stride}, {q_head_stride, k_head_stride},
+                {q_weight, k_weight}, {q_out, k_out}, {q_heads, k_heads}, tokens, eps, cos, sin,
+                table_rows, head_dim, rotary, interleaved != 0, positions, bad};
+  if (const int st = check_norm(p, dtype)) return st;
+  if (tokens == 0) return DQ4_OK;
+  return run_norm(p, dtype, false, stream);
+}
+
+int64_t dq4_qk_norm_rope_backward_workspace_bytes(int32_t head_dim) {
+  if (head_dim < 2 || head_dim > kMaxDim) return 0;
+  return 256 + int64_t(kMaxPartials) * 2 * head_dim * 4;
+}
+
+int dq4_qk_norm_rope_backward(const void* dq_out, const void* dk_out, const void* q,
+                              int64_t q_token_stride, int64_t q_head_stride, const void* k,
+                              int64_t k_token_stride, int64_t k_head_stride, int32_t dtype,
+                              int64_t tokens, int32_t q_heads, int32_t k_heads,
+                              int32_t head_dim, const void* q_weight, const void* k_weight,
+                              float eps, const float* cos, const float* sin,
+                              int64_t table_rows, int32_t rotary, int32_t interleaved,
+                              const int64_t* positions, void* dq, void* dk, float* dq_weight,
+                              float* dk_weight, void* workspace, int64_t workspace_bytes,
+                              int* bad, void* stream) {
+  NormArgs p = {{q, k}, {dq_out, dk_out}, {q_token_stride, k_token_stride},
+                {q_head_stride, k_head_stride}, {q_weight, k_weight}, {dq, dk},
+                {q_heads, k_heads}, tokens, eps, cos, sin, table_rows, head_dim, rotary,
+                interleaved != 0, positions, bad};
+  if (const int st = check_norm(p, dtype)) return st;
+  const uintptr_t es = dtype == DQ4_OUT_F32 ? 4 : 2;
+  for (int n = 0; n < 2 && p.heads[n] > 0; ++n) {
+    if (tokens > 0 && !p.dy[n]) return DQ4_ERR_NULL;
+    if (misaligned(p.dy[n], es)) return DQ4_ERR_ALIGN;
+  }
+  if (q_weight) {
+    // k_heads == 0 leaves dk_weight's place unused; its sums are zero
+    if (!dq_weight || (k_heads > 0 && !dk_weight)) return DQ4_ERR_NULL;
+    if (misaligned(dq_weight, 4) || misaligned(dk_weight, 4)) return DQ4_ERR_ALIGN;
+    if (!workspace || workspace_bytes < dq4_qk_norm_rope_backward_workspace_bytes(head_dim))
+      return DQ4_ERR_WORKSPACE;
+    if (misaligned(workspace, 256)) return DQ4_ERR_ALIGN;
+    p.dw[0] = dq_weight;
+    p.dw[1] = dk_weight;
+    p.count = static_cast<int*>(workspace);
+    p.part = reinterpret_cast<float*>(static_cast<char*>(workspace) + 256);
+  }
+  if (tokens == 0) {
+    if (!q_weight) return DQ4_OK;
+    int dev, sms;
+    if (const int st = current_device(&dev, &sms)) return st;
+    for (int n = 0; n < 2; ++n) {
+      if (!p.dw[n]) continue;
+      const cudaError_t e = cudaMemsetAsync(p.dw[n], 0, size_t(head_dim) * 4,
+                                            static_cast<cudaStream_t>(stream));
+      if (e != cudaSuccess) return fail_cuda(DQ4_ERR_LAUNCH, e);
+    }
+    return DQ4_OK;
+  }
+  return run_norm(p, dtype, true, stream);
+}
+
+}  // extern "C"
