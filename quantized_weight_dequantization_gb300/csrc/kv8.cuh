@@ -4,7 +4,6 @@
 #include "attn.cuh"
 
 namespace dq4d {
-namespace {
 
 struct Kv8 {
   uint8_t* codes[2];  // k, v: [pages][kv_heads][page][dim]
@@ -22,6 +21,8 @@ struct Batch {
   const int32_t* cu;  // null: one token each
   int64_t seqs, tokens;
 };
+
+namespace {
 
 // Sequence b's first new token, new tokens, and length with them.  Whatever cu holds, the
 // rows stay inside the call's tokens.

@@ -6,23 +6,10 @@
 // maximum scales what was summed by exp(m_old - m_new).  This form takes a warp for each
 // query head of each token: a lane scores one key of 32, then sums the values of dim / 32
 // columns over the 32 keys.
-#include "kv8.cuh"
+#include "kv8_attend.cuh"
 
 namespace dq4d {
 namespace {
-
-struct AttendArgs {
-  Kv8 c;
-  Batch s;
-  const void* q;
-  int64_t token_stride, head_stride;
-  int heads, group;  // query heads, and of them per kv head
-  float scale;
-  int causal, window;
-  void* out;
-  float* lse;
-  int* bad;
-};
 
 constexpr int kRowWarps = 4;
 
@@ -68,7 +55,7 @@ __global__ void __launch_bounds__(32 * kRowWarps) dq4_kv8_rows_kernel(const Atte
         const uint8_t* k = p.c.codes[0] + (block * p.c.page + (j & (p.c.page - 1))) * kDim;
         float dot = 0.f;
         for (int i = 0; i < kDim; ++i) dot = fmaf(s_q[warp][i], e4m3(k[i]), dot);
-        score = dot * p.c.scale[0][block] * p.scale;
+        score = dot * p.c.scale[0][block] * p.scale_log2;
         vs = p.c.scale[1][block];
       } else {
         met_bad = true;
@@ -79,8 +66,8 @@ __global__ void __launch_bounds__(32 * kRowWarps) dq4_kv8_rows_kernel(const Atte
     const float next = fmaxf(m, top);
     if (!__any_sync(kAllLanes, block >= 0)) continue;
     const float base = next == -INFINITY ? 0.f : next;
-    const float e = block >= 0 ? expf(score - base) : 0.f;
-    const float keep = expf(m - base);
+    const float e = block >= 0 ? exp2f(score - base) : 0.f;
+    const float keep = exp2f(m - base);
     m = next;
     l = l * keep + e;
     for (int i = 0; i < kCols; ++i) o[i] *= keep;
@@ -96,7 +83,7 @@ __global__ void __launch_bounds__(32 * kRowWarps) dq4_kv8_rows_kernel(const Atte
   if (p.bad && __any_sync(kAllLanes, met_bad) && lane == 0) atomicAdd(p.bad, 1);
   T* out = static_cast<T*>(p.out) + r * kDim + lane * kCols;
   for (int i = 0; i < kCols; ++i) out[i] = Elem<DT>::make(l != 0.f ? o[i] / l : 0.f);
-  if (p.lse && lane == 0) p.lse[r] = m + logf(l);
+  if (p.lse && lane == 0) p.lse[r] = fmaf(m, kLn2, logf(l));
 }
 
 }  // namespace
@@ -109,7 +96,7 @@ extern "C" {
 int64_t dq4_kv8_attention_workspace_bytes(int64_t tokens, int64_t seqs, int32_t heads,
                                           int32_t kv_heads, int32_t head_dim) {
   if (tokens <= 0 || seqs <= 0 || heads < 1 || kv_heads < 1 || head_dim < 1) return 0;
-  return 256;
+  return decode_workspace_bytes();
 }
 
 int dq4_kv8_attention(const dq4_kv8_cache* cache, const void* q, int64_t q_token_stride,
@@ -125,7 +112,7 @@ int dq4_kv8_attention(const dq4_kv8_cache* cache, const void* q, int64_t q_token
   if (heads < 1 || heads > 65535 || heads % cache->kv_heads != 0) return DQ4_ERR_HEADS;
   p.s = {block_table, table_stride, table_width, seq_lens, cu, seqs, tokens};
   if (const int st = check_batch(p.s)) return st;
-  if (window < 0 || max_new < 0) return DQ4_ERR_N;
+  if (window < 0 || max_new < 0 || cache->pages * cache->kv_heads > INT32_MAX) return DQ4_ERR_N;
   if (tokens == 0 || seqs == 0) return DQ4_OK;
   if (!q || !out) return DQ4_ERR_NULL;
   if (misaligned(q, 16) || misaligned(out, 16) || q_token_stride % 8 || q_head_stride % 8 ||
@@ -140,7 +127,8 @@ int dq4_kv8_attention(const dq4_kv8_cache* cache, const void* q, int64_t q_token
   p.head_stride = q_head_stride;
   p.heads = heads;
   p.group = heads / cache->kv_heads;
-  p.scale = scale;
+  p.bf16 = dtype == DQ4_OUT_BF16;
+  p.scale_log2 = scale * 1.4426950408889634f;
   p.causal = causal;
   p.window = window;
   p.out = out;
@@ -148,6 +136,9 @@ int dq4_kv8_attention(const dq4_kv8_cache* cache, const void* q, int64_t q_token
   p.bad = bad;
   int dev, sms;
   if (const int st = current_device(&dev, &sms)) return st;
+  if (int64_t(max_new) * p.group <= 64)
+    return launch_decode(p, cache->head_dim, max_new * p.group, sms, workspace,
+                         static_cast<cudaStream_t>(stream));
   const int64_t grid = (tokens * heads + kRowWarps - 1) / kRowWarps;
   if (grid > kMaxGrid) return DQ4_ERR_N;
   const bool bf16 = dtype == DQ4_OUT_BF16, small = cache->head_dim == 64;
