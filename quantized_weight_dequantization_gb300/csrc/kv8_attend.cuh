@@ -109,5 +109,6 @@ __device__ __forceinline__ uint32_t f16_of_e4m3_high(uint32_t w) {
 int launch_decode(const AttendArgs& p, int head_dim, int rows, int sms, void* workspace,
                   cudaStream_t stream);
 int64_t decode_workspace_bytes();
+int launch_prefill(const AttendArgs& p, int head_dim, cudaStream_t stream);
 
 }  // namespace dq4d
