@@ -21,7 +21,8 @@ struct AttendArgs {
   float* lse;
   int* bad;
   int* count;        // decode: arrivals at a shared item
-  float* part;       // decode: partial results
+  float* part;       // decode: unnormalized rows of parts of items,
+  float2* stats;     // and their {m, l}
 };
 
 namespace {
