@@ -35,6 +35,7 @@ constexpr int kTile = 64;          // keys of a unit
 constexpr int kGrans = kTile / 16; // granules of 16 keys, never of two pages
 constexpr int kMaxCtas = 160;      // CTAs the workspace has room for
 constexpr int kMaxRows = 16;       // query rows of an item: 8 NT
+constexpr int kOpening = 1;        // what starting and ending an item costs, in units
 constexpr int kSegs = 8;           // items, or parts of them, that a warp plans at a time
 constexpr int kBatch = 32 / kGrans;  // units whose pages are read ahead together
 // parts: two for each warp, and two for each CTA
@@ -42,8 +43,9 @@ constexpr int kParts = kMaxCtas * (2 * kWarps + 2);
 
 // An item, or the part of it that falls to a warp.
 struct Segment {
-  int64_t item0;  // the item's first unit of all
-  int first;      // this part's first unit, from the warp's first
+  int64_t item0;  // where the item's first unit of keys stands among all units
+  int first;      // this part's first unit, counted over the warp's
+  int count;      // its units
   int tiles;      // units of the whole item
   int tile0;      // this part's first unit within the item
   int b, head;    // sequence and kv head
@@ -68,7 +70,9 @@ struct SeqWork {
 };
 
 // The units of a sequence: its kv heads times its row tiles, times the units of keys
-// that its rows see (one at least, so that rows which see none get their zeros).
+// that its rows see (one at least, so that rows which see none get their zeros).  In the
+// division of the work an item counts kOpening units more, placed before its keys: starting
+// and ending an item takes a warp about as long as a unit does.
 __device__ __forceinline__ SeqWork seq_work(const AttendArgs& p, const Seq& s, int rows_tile) {
   SeqWork w;
   w.held = held_keys(p, s.len);
@@ -206,7 +210,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
   extern __shared__ uint8_t smem_raw[];
   __shared__ int64_t s_sums[kWarps], s_before;
   __shared__ int s_b0;
-  __shared__ bool s_last;
+  __shared__ bool s_last[2];
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
   const uint32_t sbase = smem_u32(base);
@@ -231,7 +235,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
   auto units_of = [&](int64_t b) -> int64_t {
     if (b >= seqs) return 0;
     const SeqWork w = seq_work(p, seq_at(p.s, b), kRows);
-    return int64_t(w.tiles) * w.items;
+    return int64_t(w.tiles + kOpening) * w.items;
   };
   int64_t units = 0, before = 0;
   const int64_t mine = units_of(tid);
@@ -269,8 +273,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
 
   // Rows 2 c + j of O^T (columns g kDim / 8 .. of dim): the result, or a part of it.
   auto flush = [&](const Segment& s) {
-    const int units_here = min(int(v1 - v0) - s.first, s.tiles - s.tile0);
-    const bool whole = units_here == s.tiles;
+    const bool whole = s.count == s.tiles;
     const int part = 2 * warp + (s.first > 0);  // of the warp's first item, or its last
     if (!whole && lane == 0) parts[part] = s;
     const int64_t slot = blockIdx.x * (2 * kWarps) + part;
@@ -359,7 +362,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
 
   // Plan up to kSegs segments from unit u on; plan_b, plan_first: a sequence at or before
   // it, and that one's first unit.  32 sequences at a time, one per lane.
-  int plan_b = s_b0, nseg = 0;
+  int plan_b = s_b0, nseg = 0, planned = 0;
   int64_t plan_first = s_before, plan_u = v0;
   auto plan = [&] {
     int from = -1;
@@ -378,57 +381,87 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
       const int src = plan_b - from;
       const int tiles = __shfl_sync(kAllLanes, w.tiles, src);
       const int items = __shfl_sync(kAllLanes, w.items, src);
-      const int64_t all = int64_t(tiles) * items;
+      const int cost = tiles + kOpening;
+      const int64_t all = int64_t(cost) * items;
       if (plan_u >= plan_first + all) {
         plan_first += all;
         ++plan_b;
         continue;
       }
       const int64_t in = plan_u - plan_first;
-      const int item = int(divide(in, tiles)), tile = int(in - int64_t(item) * tiles);
+      const int item = int(divide(in, cost));
+      const int64_t item0 = plan_first + int64_t(item) * cost + kOpening;
+      const int tile = int(max(int64_t(0), plan_u - item0));
+      plan_u = min(v1, item0 + tiles);
+      const int count = int(plan_u - item0) - tile;
+      if (count <= 0) continue;  // its keys fall to the next warp
       const int per_head = items / p.c.heads;
+      const int r0 = item % per_head * kRows;
       if (lane == src)
-        seg_of[nseg] = Segment{plan_u - tile, int(plan_u - v0), tiles,  tile,
-                               plan_b,        item / per_head,  item % per_head * kRows,
-                               s.n * p.group, w.key0,           w.held, s.len,
-                               s.n,           int(s.row)};
-      plan_u = min(v1, plan_u - tile + tiles);
+        seg_of[nseg] = Segment{item0,  planned,         count,  tiles, tile,  plan_b, item / per_head,
+                               r0,     s.n * p.group,   w.key0, w.held, s.len, s.n,    int(s.row)};
+      planned += count;
+      // its query rows, to L2 before they are needed: a lane for each line of 128 bytes
+      constexpr int kLines = kDim / 64;
+      const int r = r0 + lane / kLines;
+      const int n = __shfl_sync(kAllLanes, s.n, src);
+      const int row = __shfl_sync(kAllLanes, int(s.row), src);
+      if (lane / kLines < kRows && r < n * p.group) {
+        const int tok = r / p.group;
+        const uint16_t* q = static_cast<const uint16_t*>(p.q) + (row + tok) * p.token_stride +
+                            (item / per_head * p.group + r - tok * p.group) * p.head_stride;
+        asm volatile("prefetch.global.L2 [%0];" :: "l"(q + lane % kLines * 64));
+      }
       ++nseg;
     }
     __syncwarp();
   };
 
   // Pages read ahead: lane kGrans t + h holds granule h of unit kBatch batch + t of the plan.
+  // Three batches are on the way, so that no load is used in the batch that issues it: the
+  // page ids of batch + 2, the scales of batch + 1, and the batch that is being used.
   struct Ahead {
-    int seg, key, block;     // block: page * kv_heads + head, or -1
-    float ks, bias, inv;     // K's scale; log2 and inverse of V's
+    int seg, key, id, head;  // id: the page, or -1 where there are no such keys
+    int block;               // page * kv_heads + head, or -1
+    float ks, vs;            // scales
   };
-  int unit0 = 0, unit1 = 0;  // the plan's units, from the warp's first
-  auto read_ahead = [&](int batch) {
-    Ahead a = {0, 0, -1, 0.f, 0.f, 0.f};
+  int unit0 = 0, unit1 = 0;  // the plan's units, counted over the warp's
+  auto read_pages = [&](int batch) {
+    Ahead a = {0, 0, -1, 0, -1, 0.f, 1.f};
     const int i = unit0 + batch * kBatch + lane / kGrans;
     if (i >= unit1) return a;
     int sg = 0;
     while (sg + 1 < nseg && seg_of[sg + 1].first <= i) ++sg;
     const Segment& s = seg_of[sg];
     a.seg = sg;
+    a.head = s.head;
     a.key = s.key0 + (s.tile0 + i - s.first) * kTile + (lane % kGrans) * 16;
     if (a.key < s.held) {
-      const int id = __ldg(p.s.table + s.b * p.s.table_stride + (a.key >> p.c.log2_page));
-      if (id >= 0 && id < p.c.pages) {
-        a.block = id * p.c.heads + s.head;
-        a.ks = p.c.scale[0][a.block];
-        const float vs = used_scale(p.c.scale[1][a.block]);
-        a.bias = log2f(vs);
-        a.inv = 1.f / vs;
-      } else {
-        met_bad = 1;
-      }
+      a.id = __ldg(p.s.table + s.b * p.s.table_stride + (a.key >> p.c.log2_page));
+      a.block = 0;
     }
     if (s.held < s.len) met_bad = 1;
     return a;
   };
-  Ahead now = {}, next = {};
+  auto read_scales = [&](Ahead& a) {
+    if (a.block < 0) return;
+    if (a.id >= 0 && a.id < p.c.pages) {
+      a.block = a.id * p.c.heads + a.head;
+      a.ks = __ldg(p.c.scale[0] + a.block);
+      a.vs = __ldg(p.c.scale[1] + a.block);
+    } else {
+      a.block = -1;
+      met_bad = 1;
+    }
+  };
+  Ahead now = {}, next = {}, later = {};
+  float now_bias = 0.f, now_inv = 0.f;  // log2 and inverse of now.vs
+  auto use = [&](const Ahead& a) {
+    now = a;
+    const float vs = used_scale(a.vs);
+    now_bias = log2f(vs);
+    now_inv = 1.f / vs;
+  };
   const int rows_copy = min(p.c.page, kTile);
   // The next slot of the ring: the keys (which = 0) or values of unit k of the plan, which
   // is in the batch `now` or the one after it.
@@ -468,20 +501,27 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
   };
 
   while (plan_u < v1) {
-    unit0 = int(plan_u - v0);
+    unit0 = planned;
     plan();
-    unit1 = int(plan_u - v0);
+    unit1 = planned;
     const int count = unit1 - unit0;
-    now = read_ahead(0);
-    next = read_ahead(1);
+    if (count == 0) break;
+    now = read_pages(0);
+    next = read_pages(1);
+    later = read_pages(2);
+    read_scales(now);
+    read_scales(next);
     for (int k = 0; k < kSlots; ++k)
       if (k < 2 * count) issue(k / 2, 0, k & 1);
+    use(now);
     int seg = -1, all_lo = 0, all_hi = 0;
     for (int k = 0; k < count; ++k) {
       const int batch = k / kBatch, t = (k % kBatch) * kGrans;
       if (k > 0 && k % kBatch == 0) {
-        now = next;
-        next = read_ahead(batch + 1);
+        use(next);
+        next = later;
+        read_scales(next);
+        later = read_pages(batch + 2);
       }
       const int sg = __shfl_sync(kAllLanes, now.seg, t);
       if (sg != seg) {
@@ -500,8 +540,8 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
 #pragma unroll
       for (int h = 0; h < kGrans; ++h) {
         ks[h] = __shfl_sync(kAllLanes, now.ks, t + h);
-        bias[h] = __shfl_sync(kAllLanes, now.bias, t + h);
-        inv[h] = __shfl_sync(kAllLanes, now.inv, t + h);
+        bias[h] = __shfl_sync(kAllLanes, now_bias, t + h);
+        inv[h] = __shfl_sync(kAllLanes, now_inv, t + h);
         there[h] = __shfl_sync(kAllLanes, now.block, t + h) >= 0;
         all = all && there[h];
       }
@@ -648,53 +688,68 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
   __syncthreads();
 
   // ---- join the warps' parts, item by item, and CTAs' parts of an item
-  for (int i = 0; i < 2 * kWarps;) {
+  // A task is a row of an item; the warps take them in turn.
+  const int64_t own = int64_t(blockIdx.x) * (2 * kWarps);
+  const int64_t cta_slots = int64_t(kMaxCtas) * (2 * kWarps);
+  // An item that a CTA shares stands at its start (slot 0) or runs over its end (slot 1).
+  auto cta_slot = [&](int cta, int64_t begin, const Segment& s) {
+    return cta_slots + 2 * cta + (s.item0 - kOpening <= begin ? 0 : 1);
+  };
+  int shared[2] = {-1, -1};  // parts of the items that other CTAs have parts of, too
+  float v[kCols], top, sum;
+  for (int i = 0, task = 0; i < 2 * kWarps;) {
     if (parts[i].rows == 0) {
       ++i;
       continue;
     }
     const Segment& s = parts[i];
-    // the item's parts in this CTA: which[0] .. which[n - 1], in key order
+    const int64_t to_slot = cta_slot(blockIdx.x, u0, s);
+    const bool alone = s.item0 >= u0 && s.item0 + s.tiles <= u1;
+    if (!alone) shared[to_slot & 1] = i;
+    // the item's parts in this CTA, in key order, four bits each
     uint64_t which = 0;
     int n = 0;
     for (; i < 2 * kWarps && (parts[i].rows == 0 || parts[i].item0 == s.item0); ++i)
       if (parts[i].rows != 0) which |= uint64_t(i) << (4 * n++);
     const int rows = min(kRows, s.rows - s.r0);
-    const bool alone = s.item0 >= u0 && s.item0 + s.tiles <= u1;
-    const int64_t own = int64_t(blockIdx.x) * (2 * kWarps);
-    const int64_t cta_slots = int64_t(kMaxCtas) * (2 * kWarps);
-    const int64_t mine_at = cta_slots + 2 * blockIdx.x + (s.item0 <= u0 ? 0 : 1);
-    float v[kCols], top, sum;
-    for (int r = warp; r < rows; r += kWarps) {
+    for (int r = 0; r < rows; ++r, ++task) {
+      if (task % kWarps != warp) continue;
       join_parts(p, n, r, [&](int k) { return own + int((which >> (4 * k)) & 15); }, v, top, sum);
       if (alone) {
         write_row(p, s, r, v, top, sum);
       } else {
-        float* to = p.part + (mine_at * kMaxRows + r) * kDim + lane * kCols;
+        float* to = p.part + (to_slot * kMaxRows + r) * kDim + lane * kCols;
 #pragma unroll
         for (int k = 0; k < kCols; ++k) to[k] = v[k];
-        if (lane == 0) p.stats[mine_at * kMaxRows + r] = make_float2(top, sum);
+        if (lane == 0) p.stats[to_slot * kMaxRows + r] = make_float2(top, sum);
       }
     }
-    if (alone) continue;
-    // the item's CTAs c0 .. c1, counted where c1's part is
+  }
+  if (shared[0] < 0 && shared[1] < 0) return;
+  // arrivals are counted at the CTA that has the item's last part
+  __syncthreads();
+  if (tid < 2) {
+    s_last[tid] = false;
+    if (shared[tid] >= 0) {
+      const Segment& s = parts[shared[tid]];
+      const int c0 = cta_of(s.item0), c1 = cta_of(s.item0 + s.tiles - 1);
+      s_last[tid] = atomic_add_acq_rel(p.count + c1, 1) == c1 - c0;
+      if (s_last[tid]) p.count[c1] = 0;  // ready for the next call
+    }
+  }
+  __syncthreads();
+  for (int k = 0, task = 0; k < 2; ++k) {
+    if (!s_last[k]) continue;
+    const Segment& s = parts[shared[k]];
     const int c0 = cta_of(s.item0), c1 = cta_of(s.item0 + s.tiles - 1);
-    __syncthreads();
-    if (tid == 0) {
-      s_last = atomic_add_acq_rel(p.count + c1, 1) == c1 - c0;
-      if (s_last) p.count[c1] = 0;  // ready for the next call
+    const int64_t first = cta_slot(c0, begin_of(c0), s);
+    const int rows = min(kRows, s.rows - s.r0);
+    for (int r = 0; r < rows; ++r, ++task) {
+      if (task % kWarps != warp) continue;
+      join_parts(p, c1 - c0 + 1, r,
+                 [&](int x) { return x == 0 ? first : cta_slots + 2 * (c0 + x); }, v, top, sum);
+      write_row(p, s, r, v, top, sum);
     }
-    __syncthreads();
-    if (s_last) {
-      // an item starts at its CTA's first unit, or is that CTA's last
-      const int64_t first = cta_slots + 2 * c0 + (begin_of(c0) == s.item0 ? 0 : 1);
-      for (int r = warp; r < rows; r += kWarps) {
-        join_parts(p, c1 - c0 + 1, r,
-                   [&](int k) { return k == 0 ? first : cta_slots + 2 * (c0 + k); }, v, top, sum);
-        write_row(p, s, r, v, top, sum);
-      }
-    }
-    __syncthreads();  // s_last may be set anew
   }
 }
 
