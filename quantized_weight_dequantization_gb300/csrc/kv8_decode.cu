@@ -52,6 +52,7 @@ struct Segment {
   int r0, rows;   // first query row of the item, and the sequence's rows
   int key0;       // the item's first key, a multiple of kTile
   int held, len, n, row;
+  bool in_ring;   // a part: kept in the warp's ring, not in the workspace
 };
 
 template <int kDim>
@@ -133,49 +134,70 @@ __device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* s_sums, int64_
   return total;
 }
 
-// Row r of the n parts whose slots slot(0) .. slot(n - 1) are: columns kCols lane .. of O
-// and m and l, summed in that order.
-template <int kCols, typename SlotOf>
-__device__ __forceinline__ void join_parts(const AttendArgs& p, int n, int r, SlotOf slot,
-                                           float (&v)[kCols], float& top, float& sum) {
+// A part's rows of O, unnormalized, and their {m, l}: in global or shared memory.
+struct PartAt {
+  const float* o;
+  const float2* stats;
+};
+
+// Rows r and, if two, r2 of the n parts at(0) .. at(n - 1): columns kCols lane .. of O and m
+// and l, summed in that order.  Two rows at a time keep twice the loads on the way.
+template <int kCols, typename At>
+__device__ __forceinline__ void join_parts(int n, int r, int r2, At at, float (&v)[2][kCols],
+                                           float (&top)[2], float (&sum)[2]) {
   const int lane = threadIdx.x & 31;
-  top = -INFINITY;
-  sum = 0.f;
+  const int row[2] = {r, r2};
 #pragma unroll
-  for (int i = 0; i < kCols; ++i) v[i] = 0.f;
+  for (int x = 0; x < 2; ++x) {
+    top[x] = -INFINITY;
+    sum[x] = 0.f;
+#pragma unroll
+    for (int i = 0; i < kCols; ++i) v[x][i] = 0.f;
+  }
   for (int i0 = 0; i0 < n; i0 += 32) {  // 32 parts at a time, one's m and l per lane
-    float2 st = make_float2(-INFINITY, 0.f);
-    if (i0 + lane < n) st = __ldcg(p.stats + slot(i0 + lane) * kMaxRows + r);
-    float t = st.x;
+    float2 st[2];
+    float mine[2];
 #pragma unroll
-    for (int w = 16; w > 0; w >>= 1) t = fmaxf(t, __shfl_xor_sync(kAllLanes, t, w));
-    const float is = fmaxf(top, t), from = is == -INFINITY ? 0.f : is;
-    const float keep = exp2_fast(top - from);
-    const float mine = exp2_fast(st.x - from);
-    sum *= keep;
+    for (int x = 0; x < 2; ++x) {
+      st[x] = make_float2(-INFINITY, 0.f);
+      if (i0 + lane < n) st[x] = at(i0 + lane).stats[row[x]];
+    }
 #pragma unroll
-    for (int i = 0; i < kCols; ++i) v[i] *= keep;
-    top = is;
+    for (int x = 0; x < 2; ++x) {
+      float t = st[x].x;
+#pragma unroll
+      for (int w = 16; w > 0; w >>= 1) t = fmaxf(t, __shfl_xor_sync(kAllLanes, t, w));
+      const float is = fmaxf(top[x], t), from = is == -INFINITY ? 0.f : is;
+      const float keep = exp2_fast(top[x] - from);
+      mine[x] = exp2_fast(st[x].x - from);
+      sum[x] *= keep;
+#pragma unroll
+      for (int i = 0; i < kCols; ++i) v[x][i] *= keep;
+      top[x] = is;
+    }
     const int k1 = min(32, n - i0);
-#pragma unroll 8
+#pragma unroll 4
     for (int k = 0; k < k1; ++k) {
-      const float* row = p.part + (slot(i0 + k) * kMaxRows + r) * (32 * kCols) + lane * kCols;
-      float x[kCols];
-      if constexpr (kCols == 4) {
-        const float4 u = __ldcg(reinterpret_cast<const float4*>(row));
-        x[0] = u.x;
-        x[1] = u.y;
-        x[2] = u.z;
-        x[3] = u.w;
-      } else {
-        const float2 u = __ldcg(reinterpret_cast<const float2*>(row));
-        x[0] = u.x;
-        x[1] = u.y;
-      }
-      const float f = __shfl_sync(kAllLanes, mine, k);
-      sum = fmaf(f, __shfl_sync(kAllLanes, st.y, k), sum);
+      const float* o = at(i0 + k).o + lane * kCols;
 #pragma unroll
-      for (int i = 0; i < kCols; ++i) v[i] = fmaf(f, x[i], v[i]);
+      for (int x = 0; x < 2; ++x) {
+        float u[kCols];
+        if constexpr (kCols == 4) {
+          const float4 y = *reinterpret_cast<const float4*>(o + row[x] * (32 * kCols));
+          u[0] = y.x;
+          u[1] = y.y;
+          u[2] = y.z;
+          u[3] = y.w;
+        } else {
+          const float2 y = *reinterpret_cast<const float2*>(o + row[x] * (32 * kCols));
+          u[0] = y.x;
+          u[1] = y.y;
+        }
+        const float f = __shfl_sync(kAllLanes, mine[x], k);
+        sum[x] = fmaf(f, __shfl_sync(kAllLanes, st[x].y, k), sum[x]);
+#pragma unroll
+        for (int i = 0; i < kCols; ++i) v[x][i] = fmaf(f, u[i], v[x][i]);
+      }
     }
   }
 }
@@ -271,12 +293,29 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
   int issued = 0, taken = 0;  // slots of the ring filled and consumed
   int met_bad = 0;
 
+  // where parts are kept: warp w's two in the workspace, its last in its ring
+  auto own_part = [&](int part) {
+    return p.part + (int64_t(blockIdx.x) * (2 * kWarps) + part) * (kMaxRows * kDim);
+  };
+  auto own_stats = [&](int part) {
+    return p.stats + (int64_t(blockIdx.x) * (2 * kWarps) + part) * kMaxRows;
+  };
+  auto ring_of = [&](int w) { return reinterpret_cast<float*>(base + w * kSlots * S::kSlot); };
+  static_assert(kRows * (kDim * 4 + 8) <= kSlots * S::kSlot, "a part fits the ring");
+  float* ring_part = ring_of(warp);
+  float2* ring_stats = reinterpret_cast<float2*>(ring_part + kRows * kDim);
+
   // Rows 2 c + j of O^T (columns g kDim / 8 .. of dim): the result, or a part of it.
-  auto flush = [&](const Segment& s) {
+  // Parts go to the workspace, but for the warp's last, when its ring is free.
+  auto flush = [&](const Segment& s, bool ring_free) {
     const bool whole = s.count == s.tiles;
     const int part = 2 * warp + (s.first > 0);  // of the warp's first item, or its last
-    if (!whole && lane == 0) parts[part] = s;
-    const int64_t slot = blockIdx.x * (2 * kWarps) + part;
+    if (!whole && lane == 0) {
+      parts[part] = s;
+      parts[part].in_ring = ring_free;
+    }
+    float* part_o = ring_free ? ring_part : own_part(part);
+    float2* part_stats = ring_free ? ring_stats : own_stats(part);
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -302,13 +341,12 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
           if (p.lse && g == 0)
             p.lse[at] = sum == 0.f ? -INFINITY : fmaf(m[nt][j] - kLift, kLn2, logf(sum));
         } else {
-          float4* to = reinterpret_cast<float4*>(p.part + (slot * kMaxRows + r) * kDim +
-                                                 g * (kDim / 8));
+          float4* to = reinterpret_cast<float4*>(part_o + r * kDim + g * (kDim / 8));
 #pragma unroll
           for (int i = 0; i < kSteps; i += 2)
             to[i / 2] = make_float4(o[nt][i][j], o[nt][i][2 + j], o[nt][i + 1][j],
                                     o[nt][i + 1][2 + j]);
-          if (g == 0) p.stats[slot * kMaxRows + r] = make_float2(m[nt][j], sum);
+          if (g == 0) part_stats[r] = make_float2(m[nt][j], sum);
         }
       }
   };
@@ -399,7 +437,8 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
       const int r0 = item % per_head * kRows;
       if (lane == src)
         seg_of[nseg] = Segment{item0,  planned,         count,  tiles, tile,  plan_b, item / per_head,
-                               r0,     s.n * p.group,   w.key0, w.held, s.len, s.n,    int(s.row)};
+                               r0,     s.n * p.group,   w.key0, w.held, s.len, s.n,    int(s.row),
+                               false};
       planned += count;
       // its query rows, to L2 before they are needed: a lane for each line of 128 bytes
       constexpr int kLines = kDim / 64;
@@ -525,7 +564,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
       }
       const int sg = __shfl_sync(kAllLanes, now.seg, t);
       if (sg != seg) {
-        if (seg >= 0) flush(seg_of[seg]);
+        if (seg >= 0) flush(seg_of[seg], false);
         seg = sg;
         const Segment& s = seg_of[seg];
         open(s);
@@ -679,7 +718,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
       if (2 * k + 1 + kSlots < 2 * count && !failed)
         issue((2 * k + 1 + kSlots) / 2, batch, (kSlots + 1) & 1);
     }
-    flush(seg_of[seg]);
+    flush(seg_of[seg], plan_u == v1 && !failed);
   }
   // after a failure: the copies still in flight, before the ring goes away
   for (int i = failed ? max(0, issued - kSlots) : issued; i < issued; ++i)
@@ -688,15 +727,14 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
   __syncthreads();
 
   // ---- join the warps' parts, item by item, and CTAs' parts of an item
-  // A task is a row of an item; the warps take them in turn.
-  const int64_t own = int64_t(blockIdx.x) * (2 * kWarps);
+  // A task is two rows of an item; the warps take them in turn.
   const int64_t cta_slots = int64_t(kMaxCtas) * (2 * kWarps);
   // An item that a CTA shares stands at its start (slot 0) or runs over its end (slot 1).
   auto cta_slot = [&](int cta, int64_t begin, const Segment& s) {
     return cta_slots + 2 * cta + (s.item0 - kOpening <= begin ? 0 : 1);
   };
   int shared[2] = {-1, -1};  // parts of the items that other CTAs have parts of, too
-  float v[kCols], top, sum;
+  float v[2][kCols], top[2], sum[2];
   for (int i = 0, task = 0; i < 2 * kWarps;) {
     if (parts[i].rows == 0) {
       ++i;
@@ -712,16 +750,29 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
     for (; i < 2 * kWarps && (parts[i].rows == 0 || parts[i].item0 == s.item0); ++i)
       if (parts[i].rows != 0) which |= uint64_t(i) << (4 * n++);
     const int rows = min(kRows, s.rows - s.r0);
-    for (int r = 0; r < rows; ++r, ++task) {
+    for (int r = 0; r < rows; r += 2, ++task) {
       if (task % kWarps != warp) continue;
-      join_parts(p, n, r, [&](int k) { return own + int((which >> (4 * k)) & 15); }, v, top, sum);
-      if (alone) {
-        write_row(p, s, r, v, top, sum);
-      } else {
-        float* to = p.part + (to_slot * kMaxRows + r) * kDim + lane * kCols;
+      const int r2 = min(r + 1, rows - 1);
+      join_parts<kCols>(
+          n, r, r2,
+          [&](int k) {
+            const int part = int((which >> (4 * k)) & 15);
+            if (!parts[part].in_ring) return PartAt{own_part(part), own_stats(part)};
+            const float* o = ring_of(part >> 1);
+            return PartAt{o, reinterpret_cast<const float2*>(o + kRows * kDim)};
+          },
+          v, top, sum);
 #pragma unroll
-        for (int k = 0; k < kCols; ++k) to[k] = v[k];
-        if (lane == 0) p.stats[to_slot * kMaxRows + r] = make_float2(top, sum);
+      for (int x = 0; x < 2; ++x) {
+        const int at = x ? r2 : r;
+        if (alone) {
+          write_row(p, s, at, v[x], top[x], sum[x]);
+        } else {
+          float* to = p.part + (to_slot * kMaxRows + at) * kDim + lane * kCols;
+#pragma unroll
+          for (int k = 0; k < kCols; ++k) to[k] = v[x][k];
+          if (lane == 0) p.stats[to_slot * kMaxRows + at] = make_float2(top[x], sum[x]);
+        }
       }
     }
   }
@@ -730,8 +781,9 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
   __syncthreads();
   if (tid < 2) {
     s_last[tid] = false;
-    if (shared[tid] >= 0) {
-      const Segment& s = parts[shared[tid]];
+    const int of = tid == 0 ? shared[0] : shared[1];
+    if (of >= 0) {
+      const Segment& s = parts[of];
       const int c0 = cta_of(s.item0), c1 = cta_of(s.item0 + s.tiles - 1);
       s_last[tid] = atomic_add_acq_rel(p.count + c1, 1) == c1 - c0;
       if (s_last[tid]) p.count[c1] = 0;  // ready for the next call
@@ -740,15 +792,22 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
   __syncthreads();
   for (int k = 0, task = 0; k < 2; ++k) {
     if (!s_last[k]) continue;
-    const Segment& s = parts[shared[k]];
+    const Segment& s = parts[k == 0 ? shared[0] : shared[1]];
     const int c0 = cta_of(s.item0), c1 = cta_of(s.item0 + s.tiles - 1);
     const int64_t first = cta_slot(c0, begin_of(c0), s);
     const int rows = min(kRows, s.rows - s.r0);
-    for (int r = 0; r < rows; ++r, ++task) {
+    for (int r = 0; r < rows; r += 2, ++task) {
       if (task % kWarps != warp) continue;
-      join_parts(p, c1 - c0 + 1, r,
-                 [&](int x) { return x == 0 ? first : cta_slots + 2 * (c0 + x); }, v, top, sum);
-      write_row(p, s, r, v, top, sum);
+      const int r2 = min(r + 1, rows - 1);
+      join_parts<kCols>(
+          c1 - c0 + 1, r, r2,
+          [&](int x) {
+            const int64_t slot = x == 0 ? first : cta_slots + 2 * (c0 + x);
+            return PartAt{p.part + slot * (kMaxRows * kDim), p.stats + slot * kMaxRows};
+          },
+          v, top, sum);
+      write_row(p, s, r, v[0], top[0], sum[0]);
+      write_row(p, s, r2, v[1], top[1], sum[1]);
     }
   }
 }
