@@ -9,6 +9,7 @@ lengths, pages and positions on the device: nothing here waits for the GPU.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 from typing import Optional, Tuple
 
@@ -60,109 +61,117 @@ def _lib() -> ctypes.CDLL:
 
 
 # ------------------------------------------------------------- helpers
+# A call of few tokens is bound by the host, so the checks below first take the short way that a
+# valid argument passes, and look for what is wrong only if it does not.
 _WORKSPACES = {}
 
 
-def _workspace(need: int, what: str, device, handle) -> torch.Tensor:
-    """The cached zero-filled workspace of (operator, device, stream), grown to `need` bytes."""
-    key = (what, device.index, handle)
+def _workspace(workspace, need: int, what: str, like: torch.Tensor, handle) -> torch.Tensor:
+    """The caller's workspace, or the cached zero-filled one of (operator, device, stream), grown
+    to `need` bytes."""
+    if workspace is not None:
+        _check(workspace, "workspace", torch.uint8, need, like.device)
+        return workspace
+    key = (what, like.get_device(), handle)
     ws = _WORKSPACES.get(key)
     if ws is None or ws.numel() < need:
-        ws = torch.zeros(max(need, 1), dtype=torch.uint8, device=device)
-        torch.cuda.synchronize(device)  # zero-filled before any stream uses it
+        ws = torch.zeros(max(need, 1), dtype=torch.uint8, device=like.device)
+        torch.cuda.synchronize(like.device)  # zero-filled before any stream uses it
         _WORKSPACES[key] = ws
     return ws
 
 
-def _own_workspace(workspace, need: int, what: str, device, handle) -> torch.Tensor:
-    if workspace is None:
-        return _workspace(need, what, device, handle)
-    _check(workspace, "workspace", torch.uint8, need, device)
-    return workspace
+def _stream(stream, index: int) -> int:
+    """The handle of `stream`, or of the device's current one."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(index)
+    return _stream_handle(stream, None)
 
 
-def _heads(t: torch.Tensor, name: str, dtype, device) -> None:
+def _flat(t: torch.Tensor, name: str, dtype, numel: int, like: torch.Tensor) -> int:
+    """The address of a contiguous tensor of `dtype` with `numel` elements at least, on like's
+    device."""
+    if (t.dtype is not dtype or t.get_device() != like.get_device() or t.numel() < numel
+            or not t.is_contiguous()):
+        _check(t, name, dtype, numel, like.device)
+    return t.data_ptr()
+
+
+def _heads(t: torch.Tensor, name: str, dtype, like: torch.Tensor) -> None:
     """A tokens x heads x head_dim tensor: any strides, but a head's values contiguous."""
+    if (t.is_cuda and t.dtype is dtype and t.get_device() == like.get_device() and t.dim() == 3
+            and t.stride(2) == 1):
+        return
     if t.device.type != "cuda":
         raise ValueError(f"{name}: must be a CUDA tensor (the library reads device memory)")
-    if t.device != device:
-        raise ValueError(f"{name}: expected a tensor on {device}, got {t.device}")
+    if t.device != like.device:
+        raise ValueError(f"{name}: expected a tensor on {like.device}, got {t.device}")
     if t.dtype != dtype:
         raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
     if t.dim() != 3:
         raise ValueError(f"{name}: must be tokens x heads x head_dim, got {tuple(t.shape)}")
-    if t.shape[2] > 1 and t.stride(2) != 1 and t.numel():
+    if t.shape[2] > 1 and t.numel():
         raise ValueError(f"{name}: the values of a head must be contiguous")
 
 
-def _output(out, name: str, shape, dtype, device) -> torch.Tensor:
+def _output(out, name: str, shape, like: torch.Tensor) -> torch.Tensor:
+    """`out` if given, else a new tensor; contiguous, of like's type."""
     if out is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    if tuple(out.shape) != tuple(shape):
-        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(out.shape)}")
-    _check(out, name, dtype, 0, device)
+        return torch.empty(shape, dtype=like.dtype, device=like.device)
+    if tuple(out.shape) != shape:
+        raise ValueError(f"{name}: expected shape {shape}, got {tuple(out.shape)}")
+    _flat(out, name, like.dtype, 0, like)
     return out
 
 
-def _bad(bad, device) -> Optional[int]:
-    if bad is None:
-        return None
-    _check(bad, "bad", torch.int32, 1, device)
-    return bad.data_ptr()
+def _bad(bad, like) -> Optional[int]:
+    return None if bad is None else _flat(bad, "bad", torch.int32, 1, like)
 
 
-def _tables(cos, sin, device) -> Tuple[Optional[int], Optional[int], int, int]:
+def _tables(cos, sin, like) -> Tuple[Optional[int], Optional[int], int, int]:
     """(cos, sin, rows, rotary) of the rotation's tables."""
-    if (cos is None) != (sin is None):
-        raise ValueError("cos and sin come together")
-    if cos is None:
+    if cos is None and sin is None:
         return None, None, 0, 0
+    if cos is None or sin is None:
+        raise ValueError("cos and sin come together")
     if cos.dim() != 2 or cos.shape != sin.shape:
         raise ValueError(f"cos and sin must be positions x rotary / 2 and alike, got "
                          f"{tuple(cos.shape)} and {tuple(sin.shape)}")
-    _check(cos, "cos", torch.float32, 0, device)
-    _check(sin, "sin", torch.float32, 0, device)
-    return cos.data_ptr(), sin.data_ptr(), cos.shape[0], 2 * cos.shape[1]
+    rows, half = cos.shape
+    return (_flat(cos, "cos", torch.float32, 0, like), _flat(sin, "sin", torch.float32, 0, like),
+            rows, 2 * half)
 
 
 # ------------------------------------------------------------- norm and rotation
-def _norm_inputs(q, k, q_weight, k_weight, cos, sin, positions):
-    """Checked inputs: (tokens, heads, kv heads, head_dim, tables, positions)."""
-    device, dtype = q.device, q.dtype
+def _norm_args(q, k, q_weight, k_weight, cos, sin, positions, eps, interleaved):
+    """Checked arguments of the C entry points, from q to positions."""
+    dtype = q.dtype
     if dtype not in _DTYPE_CODE:
         raise TypeError(f"q: unsupported dtype {dtype}")
-    _heads(q, "q", dtype, device)
+    _heads(q, "q", dtype, q)
     tokens, hq, dim = q.shape
-    hk = 0
+    qs = q.stride()
+    qw = kw = k_ptr = pos = None
+    hk, ks = 0, (0, 0)
     if k is not None:
-        _heads(k, "k", dtype, device)
-        hk = k.shape[1]
-        if k.shape[0] != tokens or k.shape[2] != dim:
+        _heads(k, "k", dtype, q)
+        k_tokens, hk, k_dim = k.shape
+        if k_tokens != tokens or k_dim != dim:
             raise ValueError(f"k {tuple(k.shape)} does not go with q {tuple(q.shape)}")
-    if k is not None and (q_weight is None) != (k_weight is None):
-        raise ValueError("q_weight and k_weight come together")
+        if (q_weight is None) != (k_weight is None):
+            raise ValueError("q_weight and k_weight come together")
+        k_ptr, ks = k.data_ptr(), k.stride()
     if q_weight is not None:
-        _check(q_weight, "q_weight", dtype, dim, device)
+        qw = _flat(q_weight, "q_weight", dtype, dim, q)
         if k is not None:
-            _check(k_weight, "k_weight", dtype, dim, device)
-    tables = _tables(cos, sin, device)
+            kw = _flat(k_weight, "k_weight", dtype, dim, q)
+    tables = _tables(cos, sin, q)
     if cos is not None:
         if positions is None:
             raise ValueError("positions: needed with cos and sin")
-        _check(positions, "positions", torch.int64, tokens, device)
-    return tokens, hq, hk, dim, tables
-
-
-def _norm_args(q, k, q_weight, k_weight, eps, tokens, hq, hk, dim, tables, interleaved,
-               positions):
-    qs = q.stride()
-    ks = k.stride() if k is not None else (0, 0)
-    return (q.data_ptr(), qs[0], qs[1], None if k is None else k.data_ptr(), ks[0], ks[1],
-            _DTYPE_CODE[q.dtype], tokens, hq, hk, dim,
-            None if q_weight is None else q_weight.data_ptr(),
-            None if q_weight is None or k is None else k_weight.data_ptr(), eps, tables[0],
-            tables[1], tables[2], tables[3], interleaved,
-            None if tables[0] is None else positions.data_ptr())
+        pos = _flat(positions, "positions", torch.int64, tokens, q)
+    return (q.data_ptr(), qs[0], qs[1], k_ptr, ks[0], ks[1], _DTYPE_CODE[dtype], tokens, hq, hk,
+            dim, qw, kw, eps, *tables, interleaved, pos)
 
 
 def qk_norm_rope(q: torch.Tensor, k: Optional[torch.Tensor], q_weight: Optional[torch.Tensor],
@@ -180,16 +189,14 @@ def qk_norm_rope(q: torch.Tensor, k: Optional[torch.Tensor], q_weight: Optional[
     ``interleaved`` pairs values 2i and 2i + 1, else i and i + rotary / 2.  A position outside
     the tables yields zeros, counted into ``bad`` (int32) for each head.
     """
-    tokens, hq, hk, dim, tables = _norm_inputs(q, k, q_weight, k_weight, cos, sin, positions)
-    device = q.device
-    q_out = _output(q_out, "q_out", (tokens, hq, dim), q.dtype, device)
+    args = _norm_args(q, k, q_weight, k_weight, cos, sin, positions, eps, interleaved)
+    q_out = _output(q_out, "q_out", tuple(q.shape), q)
+    k_ptr = None
     if k is not None:
-        k_out = _output(k_out, "k_out", (tokens, hk, dim), q.dtype, device)
-    st = _lib().dq4_qk_norm_rope(
-        *_norm_args(q, k, q_weight, k_weight, eps, tokens, hq, hk, dim, tables, interleaved,
-                    positions),
-        q_out.data_ptr(), None if k is None else k_out.data_ptr(), _bad(bad, device),
-        _stream_handle(stream, device))
+        k_out = _output(k_out, "k_out", tuple(k.shape), q)
+        k_ptr = k_out.data_ptr()
+    st = _lib().dq4_qk_norm_rope(*args, q_out.data_ptr(), k_ptr, _bad(bad, q),
+                                 _stream(stream, q.get_device()))
     if st:
         raise Dq4Error(st, "dq4_qk_norm_rope")
     return q_out, k_out
@@ -211,35 +218,36 @@ def qk_norm_rope_backward(dq_out: torch.Tensor, dk_out: Optional[torch.Tensor],
     (uint8, zero-filled before its first use) holds partial sums; by default a cached buffer
     per (device, stream) is used.
     """
-    tokens, hq, hk, dim, tables = _norm_inputs(q, k, q_weight, k_weight, cos, sin, positions)
-    device, dtype = q.device, q.dtype
-    _check(dq_out, "dq_out", dtype, tokens * hq * dim, device)
+    args = _norm_args(q, k, q_weight, k_weight, cos, sin, positions, eps, interleaved)
+    dim = q.shape[2]
+    dq_out_ptr = _flat(dq_out, "dq_out", q.dtype, q.numel(), q)
+    dq = _output(dq, "dq", tuple(q.shape), q)
+    dk_out_ptr = dk_ptr = dqw = dkw = dkw_ptr = None
     if k is not None:
         if dk_out is None:
             raise ValueError("dk_out: needed with k")
-        _check(dk_out, "dk_out", dtype, tokens * hk * dim, device)
-    dq = _output(dq, "dq", (tokens, hq, dim), dtype, device)
-    if k is not None:
-        dk = _output(dk, "dk", (tokens, hk, dim), dtype, device)
-    handle = _stream_handle(stream, device)
-    dqw = dkw = ws = None
+        dk_out_ptr = _flat(dk_out, "dk_out", q.dtype, k.numel(), q)
+        dk = _output(dk, "dk", tuple(k.shape), q)
+        dk_ptr = dk.data_ptr()
+    handle = _stream(stream, q.get_device())
+    weights = (None, None, None, 0)
     if q_weight is not None:
-        dqw = torch.empty(dim, dtype=torch.float32, device=device)
+        dqw = torch.empty(dim, dtype=torch.float32, device=q.device)
         if k is not None:
-            dkw = torch.empty(dim, dtype=torch.float32, device=device)
-        need = _lib().dq4_qk_norm_rope_backward_workspace_bytes(dim)
-        ws = _own_workspace(workspace, need, "norm", device, handle)
-    st = _lib().dq4_qk_norm_rope_backward(
-        dq_out.data_ptr(), None if k is None else dk_out.data_ptr(),
-        *_norm_args(q, k, q_weight, k_weight, eps, tokens, hq, hk, dim, tables, interleaved,
-                    positions),
-        dq.data_ptr(), None if k is None else dk.data_ptr(),
-        None if dqw is None else dqw.data_ptr(), None if dkw is None else dkw.data_ptr(),
-        None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel(),
-        _bad(bad, device), handle)
+            dkw = torch.empty(dim, dtype=torch.float32, device=q.device)
+            dkw_ptr = dkw.data_ptr()
+        ws = _workspace(workspace, _norm_need(dim), "norm", q, handle)
+        weights = (dqw.data_ptr(), dkw_ptr, ws.data_ptr(), ws.numel())
+    st = _lib().dq4_qk_norm_rope_backward(dq_out_ptr, dk_out_ptr, *args, dq.data_ptr(), dk_ptr,
+                                          *weights, _bad(bad, q), handle)
     if st:
         raise Dq4Error(st, "dq4_qk_norm_rope_backward")
     return dq, dk, dqw, dkw
+
+
+@functools.lru_cache(maxsize=64)
+def _norm_need(dim: int) -> int:
+    return _lib().dq4_qk_norm_rope_backward_workspace_bytes(dim)
 
 
 # ------------------------------------------------------------- the cache
@@ -271,7 +279,7 @@ class KV8Cache:
                                  f"{tuple(t.shape)}")
             _check(t, name, torch.float32, pages * heads, k.device)
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
-        self.device, self.kv_heads, self.page, self.head_dim = k.device, heads, page, dim
+        self.kv_heads, self.page, self.head_dim = heads, page, dim
         self.c = _Cache(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
                         pages, heads, page, dim)
         self.ref = ctypes.addressof(self.c)
@@ -287,23 +295,21 @@ class KV8Cache:
 
 def _batch(cache, tokens: int, block_table, seq_lens, cu):
     """Checked pointers of the ragged batch: (table, stride, width, lens, cu, sequences)."""
-    device = cache.device
+    like = cache.k
     if block_table.dim() != 2:
         raise ValueError(f"block_table: must be sequences x pages, got "
                          f"{tuple(block_table.shape)}")
     seqs, width = block_table.shape
-    if block_table.dtype != torch.int32 or block_table.device != device or (
-            width > 1 and block_table.stride(1) != 1):
-        raise ValueError(f"block_table: must be int32 rows on {device}")
-    _check(seq_lens, "seq_lens", torch.int32, seqs, device)
-    if cu is None:
-        if tokens != seqs:
-            raise ValueError(f"{tokens} tokens for {seqs} sequences: cu says how many each has")
-        return block_table.data_ptr(), block_table.stride(0), width, seq_lens.data_ptr(), None, \
-            seqs
-    _check(cu, "cu", torch.int32, seqs + 1, device)
-    return block_table.data_ptr(), block_table.stride(0), width, seq_lens.data_ptr(), \
-        cu.data_ptr(), seqs
+    stride, inner = block_table.stride()
+    if (block_table.dtype is not torch.int32 or block_table.get_device() != like.get_device()
+            or (width > 1 and inner != 1)):
+        raise ValueError(f"block_table: must be int32 rows on {like.device}")
+    lens = _flat(seq_lens, "seq_lens", torch.int32, seqs, like)
+    if cu is not None:
+        cu = _flat(cu, "cu", torch.int32, seqs + 1, like)
+    elif tokens != seqs:
+        raise ValueError(f"{tokens} tokens for {seqs} sequences: cu says how many each has")
+    return block_table.data_ptr(), stride, width, lens, cu, seqs
 
 
 def kv8_append(cache: KV8Cache, k: torch.Tensor, v: torch.Tensor, block_table: torch.Tensor,
@@ -321,20 +327,20 @@ def kv8_append(cache: KV8Cache, k: torch.Tensor, v: torch.Tensor, block_table: t
     """
     if k.dtype not in _HALF:
         raise TypeError("k must be float16 or bfloat16")
-    device = cache.device
-    _heads(k, "k", k.dtype, device)
-    _heads(v, "v", k.dtype, device)
-    tokens = k.shape[0]
-    if k.shape != v.shape or k.shape[1] != cache.kv_heads or k.shape[2] != cache.head_dim:
+    like = cache.k
+    _heads(k, "k", k.dtype, like)
+    _heads(v, "v", k.dtype, like)
+    tokens, heads, dim = k.shape
+    if k.shape != v.shape or heads != cache.kv_heads or dim != cache.head_dim:
         raise ValueError(f"k {tuple(k.shape)} and v {tuple(v.shape)}: expected (tokens, "
                          f"{cache.kv_heads}, {cache.head_dim})")
     table, stride, width, lens, cu_ptr, seqs = _batch(cache, tokens, block_table, seq_lens, cu)
-    tables = _tables(cos, sin, device)
+    tables = _tables(cos, sin, like)
     ks, vs = k.stride(), v.stride()
     st = _lib().dq4_kv8_append(
         cache.ref, k.data_ptr(), ks[0], ks[1], v.data_ptr(), vs[0], vs[1], _DTYPE_CODE[k.dtype],
         tokens, table, stride, width, lens, cu_ptr, seqs, *tables, interleaved,
-        _bad(bad, device), _stream_handle(stream, device))
+        _bad(bad, like), _stream(stream, like.get_device()))
     if st:
         raise Dq4Error(st, "dq4_kv8_append")
 
@@ -357,8 +363,8 @@ def kv8_attention(cache: KV8Cache, q: torch.Tensor, block_table: torch.Tensor,
     """
     if q.dtype not in _HALF:
         raise TypeError("q must be float16 or bfloat16")
-    device = cache.device
-    _heads(q, "q", q.dtype, device)
+    like = cache.k
+    _heads(q, "q", q.dtype, like)
     tokens, heads, dim = q.shape
     if dim != cache.head_dim or heads % cache.kv_heads:
         raise ValueError(f"q {tuple(q.shape)}: the cache has {cache.kv_heads} heads of "
@@ -366,19 +372,25 @@ def kv8_attention(cache: KV8Cache, q: torch.Tensor, block_table: torch.Tensor,
     table, stride, width, lens, cu_ptr, seqs = _batch(cache, tokens, block_table, seq_lens, cu)
     if max_new is None:
         max_new = 1 if cu is None else -(-tokens // max(seqs, 1))
-    out = _output(out, "out", (tokens, heads, dim), q.dtype, device)
-    lse = torch.empty((tokens, heads), dtype=torch.float32, device=device) if return_lse else None
-    handle = _stream_handle(stream, device)
-    L = _lib()
-    need = L.dq4_kv8_attention_workspace_bytes(tokens, seqs, heads, cache.kv_heads, dim)
-    ws = _own_workspace(workspace, need, "attention", device, handle)
+    out = _output(out, "out", (tokens, heads, dim), q)
+    lse = lse_ptr = None
+    if return_lse:
+        lse = torch.empty((tokens, heads), dtype=torch.float32, device=q.device)
+        lse_ptr = lse.data_ptr()
+    handle = _stream(stream, like.get_device())
+    need = _attention_need(tokens, seqs, heads, cache.kv_heads, dim)
+    ws = _workspace(workspace, need, "attention", like, handle)
     qs = q.stride()
-    st = L.dq4_kv8_attention(
+    st = _lib().dq4_kv8_attention(
         cache.ref, q.data_ptr(), qs[0], qs[1], _DTYPE_CODE[q.dtype], tokens, heads, table,
         stride, width, lens, cu_ptr, seqs, max_new,
-        1 / math.sqrt(dim) if scale is None else scale, causal, window, out.data_ptr(),
-        None if lse is None else lse.data_ptr(), ws.data_ptr(), ws.numel(), _bad(bad, device),
-        handle)
+        1 / math.sqrt(dim) if scale is None else scale, causal, window, out.data_ptr(), lse_ptr,
+        ws.data_ptr(), ws.numel(), _bad(bad, like), handle)
     if st:
         raise Dq4Error(st, "dq4_kv8_attention")
     return (out, lse) if return_lse else out
+
+
+@functools.lru_cache(maxsize=256)
+def _attention_need(tokens: int, seqs: int, heads: int, kv_heads: int, dim: int) -> int:
+    return _lib().dq4_kv8_attention_workspace_bytes(tokens, seqs, heads, kv_heads, dim)
