@@ -11,15 +11,20 @@
 // with c the softmax scale times the row's and the key page's scale, and vs the page's V
 // scale, which enters the exponent so that V's codes are the operand as they are.
 //
-// Roles (13 warps):
+// Roles (four groups of four warps):
 //  * warps 0..3 and 4..7: the softmax of tile 0 and 1, one thread a row, no shuffles.  They
 //    first bring the query rows to FP16 in shared memory.  m is the reference of a row, not
 //    always its maximum: it moves, and O and l with it, only when a score passes it by
-//    2^kSlack, so that O is rarely read back;
+//    2^kSlack.  So a step's weights are computed against the reference at hand in one pass
+//    over S, with the maximum found on the way, and kept in registers; only if some row has
+//    to move is S read again;
 //  * warps 8..11: bring keys and values from the cache to FP16 in shared memory (codes are
-//    exact in FP16), loaded a tile ahead into registers;
-//  * warp 12: issues the products.  While a tile's softmax runs, the tensor cores work for
-//    the other tile.
+//    exact in FP16), loaded a step ahead into registers;
+//  * warps 12 and 13: issue the products of tile 0 and 1.  A product holds its issuing thread
+//    longer than the tensor cores take for its 128 x 128 x 16, so one thread would not keep
+//    them busy.  While a tile's softmax runs, the tensor cores work for the other tile.
+// Registers move from the last two groups to the softmax, which holds 64 packed weights and
+// two chunks of S.
 // Q, K and V are held K-major / MN-major with 128-byte swizzle: rows of 64 values.
 #include "kv8_attend.cuh"
 
@@ -31,9 +36,12 @@ constexpr int kCtaRows = 2 * kTileRows;
 constexpr int kKeys = 128;         // keys of a step
 constexpr int kGrans = kKeys / 16; // granules of 16 keys: never of two pages
 constexpr int kLoadThreads = 128;
-constexpr int kPrefillThreads = kCtaRows + kLoadThreads + 32;
+constexpr int kPrefillThreads = kCtaRows + kLoadThreads + 128;
 constexpr int kLoadWarp = kCtaRows / 32;
 constexpr int kIssueWarp = kLoadWarp + kLoadThreads / 32;
+// registers a thread of the softmax, load and issue groups: 128 each at launch
+constexpr int kSoftmaxRegs = 152, kLoadRegs = 128, kIssueRegs = 80;
+static_assert(2 * kSoftmaxRegs + kLoadRegs + kIssueRegs == 4 * 128, "what the launch holds");
 constexpr int kSteps2 = 2;         // steps of keys in shared memory
 // P <= 2^(kTileLift + kSlack) = 2^15 fits FP16
 constexpr float kTileLift = 7.f, kSlack = 8.f;
@@ -75,6 +83,93 @@ __device__ __forceinline__ void commit_to(uint32_t bar) {
                :: "r"(bar) : "memory");
 }
 
+// 32 consecutive columns of this warp's TMEM lanes.  The registers may be read only after
+// tmem_loaded(), and in volatile statements only (scale_pair): the compiler keeps those in
+// order, but knows of no dependence between the wait and the registers.
+__device__ __forceinline__ void tmem_load(uint32_t addr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,"
+      "%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
+        "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
+        "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(addr));
+}
+__device__ __forceinline__ void tmem_loaded() {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+
+// Two FP32 values in a register pair, for the packed fma and add.
+__device__ __forceinline__ uint64_t pair_of(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void split(uint64_t v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+// (a c + d, b c + d) for a and b from a TMEM load, c and d the same in both halves
+__device__ __forceinline__ void scale_pair(uint32_t a, uint32_t b, uint64_t c, uint64_t d, float& x,
+                                           float& y) {
+  asm volatile(
+      "{\n.reg .b64 v;\nmov.b64 v, {%2, %3};\nfma.rn.f32x2 v, v, %4, %5;\n"
+      "mov.b64 {%0, %1}, v;\n}"
+      : "=f"(x), "=f"(y) : "r"(a), "r"(b), "l"(c), "l"(d));
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+// One pass over a row's 128 scores in TMEM (the next 32 loaded while 32 are used): weights
+// 2^x, x = c S + bias - from, packed in FP16 into w; l gets sum 2^x / vs; the largest x is
+// returned.  gran: the step's {ks, log2 vs, 1 / vs} of 16 keys each.  kMasked: only keys lo <=
+// key + i < hi are seen.
+template <bool kMasked>
+__device__ __forceinline__ float softmax_pass(uint32_t scores, uint32_t gran, float cq,
+                                              float from, int key, int lo, int hi, float& l,
+                                              uint32_t (&w)[kKeys / 2]) {
+  float top = -INFINITY;
+  uint32_t s[2][32];
+  tmem_load(scores, s[0]);
+#pragma unroll
+  for (int c = 0; c < kKeys / 32; ++c) {
+    tmem_loaded();
+    if (c + 1 < kKeys / 32) tmem_load(scores + 32 * (c + 1), s[(c + 1) & 1]);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const uint4 gi = lds_v4(gran + (2 * c + h) * 16);
+      const float ck = cq * __uint_as_float(gi.x), add = __uint_as_float(gi.y) - from;
+      const uint64_t ck2 = pair_of(ck, ck), off2 = pair_of(add, add);
+      uint64_t sum2 = 0;
+#pragma unroll
+      for (int i = 0; i < 16; i += 2) {
+        float x, y;
+        scale_pair(s[c & 1][16 * h + i], s[c & 1][16 * h + i + 1], ck2, off2, x, y);
+        if constexpr (kMasked) {
+          const int k = key + 32 * c + 16 * h + i;
+          if (k < lo || k >= hi) x = -INFINITY;
+          if (k + 1 < lo || k + 1 >= hi) y = -INFINITY;
+        }
+        top = fmaxf(fmaxf(x, y), top);
+        x = exp2_fast(x);
+        y = exp2_fast(y);
+        sum2 = add2(sum2, pair_of(x, y));
+        w[16 * c + 8 * h + i / 2] = pack_f16(x, y);
+      }
+      float a, b;
+      split(sum2, a, b);
+      const float sum = a + b;
+      // an unseen granule's scale may be no number
+      if (!kMasked || sum != 0.f) l = fmaf(sum, __uint_as_float(gi.z), l);
+    }
+  }
+  return top;
+}
+
 template <int kDim>
 __global__ void __launch_bounds__(kPrefillThreads, 1) dq4_kv8_prefill_kernel(const AttendArgs p) {
   using S = PrefillSmem<kDim>;
@@ -93,20 +188,22 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) dq4_kv8_prefill_kernel(con
   auto s_full = [&](int t) { return bar0 + 8 * (8 + t); };   // scores of tile t ready
   auto p_full = [&](int t) { return bar0 + 8 * (10 + t); };  // its weights written
   auto o_done = [&](int t) { return bar0 + 8 * (12 + t); };  // its O summed so far
-  const uint32_t q_full = bar0 + 8 * 14, all_done = bar0 + 8 * 15;
+  const uint32_t q_full = bar0 + 8 * 14;
+  auto all_done = [&](int t) { return bar0 + 8 * (15 + t); };
   if (tid == 0) {
     s_abort = 0;
     for (int i = 0; i < 2; ++i) {
       mbar_init(k_full(i), kLoadThreads);
       mbar_init(v_full(i), kLoadThreads);
-      mbar_init(k_empty(i), 1);
-      mbar_init(v_empty(i), 1);
+      mbar_init(k_empty(i), 2);
+      mbar_init(v_empty(i), 2);
       mbar_init(s_full(i), 1);
       mbar_init(p_full(i), kTileRows);
       mbar_init(o_done(i), 1);
     }
     mbar_init(q_full, kCtaRows);
-    mbar_init(all_done, 1);
+    mbar_init(all_done(0), 1);
+    mbar_init(all_done(1), 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   wait_for_stream();
@@ -163,6 +260,7 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) dq4_kv8_prefill_kernel(con
 
   if (warp < kLoadWarp) {
     // ------------------------------------------------------------------ softmax
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" :: "n"(kSoftmaxRegs));
     const int t = warp >> 2;
     const int row = tid & (kTileRows - 1);  // of the tile = its TMEM lane
     const uint32_t lanes = uint32_t((warp & 3) * 32) << 16;
@@ -216,10 +314,12 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) dq4_kv8_prefill_kernel(con
     const int last_r = min(rows, r0 + (t + 1) * kTileRows) - 1;
     const int all_lo = first_key(p, q.len - q.n + last_r / p.group);
     const int all_hi = last_key(p, q.len - q.n + (r0 + t * kTileRows) / p.group, held);
-    float m = -INFINITY, l = 0.f;
+    // from: what is taken off a row's exponents (the reference m less kTileLift)
+    float from = 0.f, l = 0.f;
+    bool fresh = true;  // no key seen yet
     const int n = steps[t];
     bool ok = true;
-    for (int j = 0; j < n && ok; ++j) {
+    for (int j = 0; j < n; ++j) {
       const int slot = j & 1;
       ok = wait_warp(s_full(t), j) && wait_warp(v_full(slot), j >> 1);
       if (!ok) break;
@@ -227,40 +327,23 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) dq4_kv8_prefill_kernel(con
       const uint32_t gran = sbase + S::kGran + slot * kGrans * 16;
       const int key = key0 + j * kKeys;
       const bool masked = key < all_lo || key + kKeys > all_hi;
-      // the largest exponent of the step
-      float top = -INFINITY;
-#pragma unroll
-      for (int c = 0; c < kKeys / 32; ++c) {
-        uint32_t s[32];
-        tmem_ld32(t_s(t) + lanes + 32 * c, s);
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const uint4 gi = lds_v4(gran + (2 * c + h) * 16);
-          const float ck = cq * __uint_as_float(gi.x), bias = __uint_as_float(gi.y);
-          float mx = -INFINITY;
-          if (!masked) {
-#pragma unroll
-            for (int i = 0; i < 16; ++i) mx = fmaxf(mx, __uint_as_float(s[16 * h + i]));
-          } else {
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const int k = key + 32 * c + 16 * h + i;
-              mx = fmaxf(mx, k >= lo && k < hi ? __uint_as_float(s[16 * h + i]) : -INFINITY);
-            }
-          }
-          if (mx != -INFINITY) top = fmaxf(top, fmaf(mx, ck, bias));
-        }
-      }
-      const bool move = top > m + kSlack;  // also from -infinity
+      uint32_t w[kKeys / 2];
+      float more = 0.f;
+      const float top =
+          masked ? softmax_pass<true>(t_s(t) + lanes, gran, cq, from, key, lo, hi, more, w)
+                 : softmax_pass<false>(t_s(t) + lanes, gran, cq, from, key, lo, hi, more, w);
+      const bool move = fresh ? top > -INFINITY : top > kTileLift + kSlack;
       if (__any_sync(kAllLanes, move)) {
-        const float keep = move ? exp2_fast(m - top) : 1.f;
-        if (move) m = top;
+        const float to = move ? from + top - kTileLift : from;
+        const float keep = fresh ? 0.f : exp2_fast(from - to);
+        from = to;
+        fresh = fresh && !move;
         l *= keep;
         if (j > 0) {
           ok = wait_warp(o_done(t), j - 1);
           if (!ok) break;
           asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-#pragma unroll
+#pragma unroll 1
           for (int c = 0; c < kDim / 32; ++c) {
             uint32_t o[32];
             tmem_ld32(t_o(t) + lanes + 32 * c, o);
@@ -268,34 +351,17 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) dq4_kv8_prefill_kernel(con
             for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * keep);
             tmem_st<32>(t_o(t) + lanes + 32 * c, o);
           }
-          asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
         }
+        more = 0.f;
+        softmax_pass<true>(t_s(t) + lanes, gran, cq, from, key, lo, hi, more, w);
       }
-      const float from = m == -INFINITY ? 0.f : m - kTileLift;
+      l += more;
 #pragma unroll
-      for (int c = 0; c < kKeys / 32; ++c) {
-        uint32_t s[32], w[16];
-        tmem_ld32(t_s(t) + lanes + 32 * c, s);
+      for (int c = 0; c < kKeys / 64; ++c) {
+        uint32_t part[32];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const uint4 gi = lds_v4(gran + (2 * c + h) * 16);
-          const float ck = cq * __uint_as_float(gi.x), add = __uint_as_float(gi.y) - from;
-          float sum = 0.f;
-#pragma unroll
-          for (int i = 0; i < 16; i += 2) {
-            float x = exp2_fast(fmaf(__uint_as_float(s[16 * h + i]), ck, add));
-            float y = exp2_fast(fmaf(__uint_as_float(s[16 * h + i + 1]), ck, add));
-            if (masked) {
-              const int k = key + 32 * c + 16 * h + i;
-              if (k < lo || k >= hi) x = 0.f;
-              if (k + 1 < lo || k + 1 >= hi) y = 0.f;
-            }
-            sum += x + y;
-            w[8 * h + i / 2] = pack_f16(x, y);
-          }
-          if (!masked || sum != 0.f) l = fmaf(sum, __uint_as_float(gi.z), l);
-        }
-        tmem_st<16>(t_s(t) + lanes + 16 * c, w);
+        for (int i = 0; i < 32; ++i) part[i] = w[32 * c + i];
+        tmem_st<32>(t_s(t) + lanes + 32 * c, part);
       }
       asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
       asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
@@ -331,168 +397,151 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) dq4_kv8_prefill_kernel(con
         }
       }
       if (real && p.lse)
-        p.lse[at] = l == 0.f ? -INFINITY : fmaf(m - kTileLift, kLn2, logf(l));
+        p.lse[at] = l == 0.f ? -INFINITY : fmaf(from, kLn2, logf(l));
     }
   } else if (warp < kIssueWarp) {
     // --------------------------------------------------- keys and values to FP16
-    // thread: 16 bytes (16 values) at chunk `col` of rows row0 + 16 / rows a pass ..
-    constexpr int kCols = kDim / 16;                    // 16-byte pieces of a row
-    constexpr int kRowsPass = kLoadThreads / kCols;     // rows a pass: 16 or 32
+    // A thread takes 16 bytes (16 values) of a row in each pass: piece `col` of rows row0,
+    // row0 + kRowsPass, ...  Eight neighbouring lanes take four pieces of one 64-value block
+    // in two rows, so that their 16-byte stores meet eight different bank groups.
+    constexpr int kCols = kDim / 16;                 // pieces of a row
+    constexpr int kRowsPass = kLoadThreads / kCols;  // 16 or 32
     constexpr int kPasses = kKeys / kRowsPass;
-    const int lt = tid - kCtaRows;
-    const int col = lt % kCols, row0 = lt / kCols;
+    const int lw = warp - kLoadWarp;
+    const int col = kDim == 128 ? (lane & 3) + ((lane >> 3) & 1) * 4 : lane & 3;
+    const int row0 =
+        kDim == 128 ? lw * 4 + ((lane >> 2) & 1) + ((lane >> 4) & 1) * 2 : lw * 8 + (lane >> 2);
+    const uint32_t line = (col >> 2) * S::kBlock + row0 * 128;
+    const uint32_t to[2] = {line + (((2 * (col & 3)) ^ (row0 & 7)) << 4),
+                            line + (((2 * (col & 3) + 1) ^ (row0 & 7)) << 4)};
     bool met_bad = held < q.len;
     const int32_t* table = p.s.table + b * p.s.table_stride;
-    // the page and head of key `key`, or -1
-    auto block_of = [&](int key) {
-      if (key >= held) return -1;
+    // Lane x holds granule x % kGrans of a step: its page's block (page * kv_heads + head), or
+    // -1 where there are no such keys.
+    auto find_block = [&](int j) {
+      const int key = key0 + j * kKeys + (lane & (kGrans - 1)) * 16;
+      if (j >= nsteps || key >= held) return -1;
       const int id = __ldg(table + (key >> p.c.log2_page));
       if (id >= 0 && id < p.c.pages) return int(id * p.c.heads + head);
       met_bad = true;
       return -1;
     };
     uint4 raw[2][kPasses];
-    int block[kPasses], gblock;
     float gk, gv;
-    auto find_blocks = [&](int j) {
-#pragma unroll
-      for (int i = 0; i < kPasses; ++i)
-        block[i] = j < nsteps ? block_of(key0 + j * kKeys + row0 + i * kRowsPass) : -1;
-      gblock = j < nsteps && lt < kGrans ? block_of(key0 + j * kKeys + lt * 16) : -1;
-    };
-    auto fetch = [&](int j) {
+    const int page_bytes = p.c.page * kDim;
+    auto fetch = [&](int j, int block) {
 #pragma unroll
       for (int i = 0; i < kPasses; ++i) {
-        const int key = key0 + j * kKeys + row0 + i * kRowsPass;
+        const int row = row0 + i * kRowsPass;
+        const int key = key0 + j * kKeys + row;
+        int at = __shfl_sync(kAllLanes, block, row >> 4);
+        if (key >= held) at = -1;  // a slot never written: it may hold no number
         const int64_t off =
-            ((int64_t(block[i]) << p.c.log2_page) + (key & (p.c.page - 1))) * kDim + col * 16;
+            int64_t(at) * page_bytes + ((key & (p.c.page - 1)) * kDim + col * 16);
 #pragma unroll
-        for (int w = 0; w < 2; ++w)
-          raw[w][i] = block[i] < 0 ? make_uint4(0, 0, 0, 0)
-                                   : __ldg(reinterpret_cast<const uint4*>(p.c.codes[w] + off));
+        for (int x = 0; x < 2; ++x)
+          raw[x][i] = at < 0 ? make_uint4(0, 0, 0, 0)
+                             : __ldg(reinterpret_cast<const uint4*>(p.c.codes[x] + off));
       }
-      gk = gblock < 0 ? 0.f : __ldg(p.c.scale[0] + gblock);
-      gv = gblock < 0 ? 0.f : __ldg(p.c.scale[1] + gblock);
-      if (gblock < 0) gv = -1.f;  // no such keys
+      gk = block < 0 ? 0.f : __ldg(p.c.scale[0] + block);
+      gv = block < 0 ? -1.f : __ldg(p.c.scale[1] + block);
     };
-    // 16 codes to two 16-byte pieces of FP16; the second column block's lanes store theirs
-    // in the other order, so that a quarter warp meets 8 different bank groups
-    auto put = [&](uint32_t to, int row, const uint4& v) {
-      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-      uint32_t h[8];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        h[2 * i] = f16_of_e4m3(w[i]);
-        h[2 * i + 1] = f16_of_e4m3_high(w[i]);
-      }
-      const uint32_t line = to + (col / 4) * S::kBlock + row * 128;
-      const int first = (col >> 2) & 1;
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int x = i ^ first;
-        const uint32_t piece = (2 * (col & 3) + x) ^ (row & 7);
-        sts_v4(line + (piece << 4), x ? h[4] : h[0], x ? h[5] : h[1], x ? h[6] : h[2],
-               x ? h[7] : h[3]);
-      }
+    auto put = [&](uint32_t at, const uint4& v) {
+      sts_v4(at + to[0], f16_of_e4m3(v.x), f16_of_e4m3_high(v.x), f16_of_e4m3(v.y),
+             f16_of_e4m3_high(v.y));
+      sts_v4(at + to[1], f16_of_e4m3(v.z), f16_of_e4m3_high(v.z), f16_of_e4m3(v.w),
+             f16_of_e4m3_high(v.w));
     };
-    find_blocks(0);
-    fetch(0);
-    find_blocks(1);
+    fetch(0, find_block(0));
+    int block = find_block(1);
     for (int j = 0; j < nsteps; ++j) {
       const int slot = j & 1;
       bool ok = j < kSteps2 || wait(k_empty(slot), (j >> 1) - 1);
-      if (!ok) break;
+      if (!__all_sync(kAllLanes, ok)) break;
 #pragma unroll
       for (int i = 0; i < kPasses; ++i)
-        put(sbase + S::kK + slot * S::kOperand, row0 + i * kRowsPass, raw[0][i]);
+        put(sbase + S::kK + slot * S::kOperand + i * kRowsPass * 128, raw[0][i]);
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       mbar_arrive(k_full(slot));
       ok = j < kSteps2 || wait(v_empty(slot), (j >> 1) - 1);
-      if (!ok) break;
+      if (!__all_sync(kAllLanes, ok)) break;
 #pragma unroll
       for (int i = 0; i < kPasses; ++i)
-        put(sbase + S::kV + slot * S::kOperand, row0 + i * kRowsPass, raw[1][i]);
-      if (lt < kGrans) {
+        put(sbase + S::kV + slot * S::kOperand + i * kRowsPass * 128, raw[1][i]);
+      if (lw == 0 && lane < kGrans) {
         // keys that are not there: S = 0 and an exponent of -infinity
         const float vs = used_scale(gv);
         const bool none = gv == -1.f;
-        sts_v4(sbase + S::kGran + (slot * kGrans + lt) * 16, __float_as_uint(gk),
+        sts_v4(sbase + S::kGran + (slot * kGrans + lane) * 16, __float_as_uint(gk),
                __float_as_uint(none ? -INFINITY : log2f(vs)), __float_as_uint(none ? 0.f : 1.f / vs),
                0);
       }
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       mbar_arrive(v_full(slot));
       if (j + 1 < nsteps) {
-        fetch(j + 1);
-        find_blocks(j + 2);
+        fetch(j + 1, block);
+        block = find_block(j + 2);
       }
     }
-    if (p.bad && met_bad && lt % 32 == 0) atomicAdd(p.bad, 1);
-  } else if (lane == 0) {
+    if (p.bad && __any_sync(kAllLanes, met_bad) && lane == 0) atomicAdd(p.bad, 1);
+  } else {
     // -------------------------------------------------------------- the products
-    const uint32_t idesc_s = instr_desc_f16<kTileRows, kKeys>(false);
-    const uint32_t idesc_o = instr_desc_f16<kTileRows, kDim>(false) | (1u << 16);  // B: N contiguous
-    auto scores = [&](int t, int j) {  // S_t = Q_t K_j^T
-      const uint32_t a = sbase + S::kQ + t * S::kOperand;
-      const uint32_t k = sbase + S::kK + (j & 1) * S::kOperand;
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(kIssueRegs));
+    const int t = warp - kIssueWarp;
+    if (t < 2 && lane == 0) {
+      const uint32_t idesc_s = instr_desc_f16<kTileRows, kKeys>(false);
+      const uint32_t idesc_o =
+          instr_desc_f16<kTileRows, kDim>(false) | (1u << 16);  // B: N contiguous
+      const int n = steps[t];
+      auto scores = [&](int j) {  // S = Q K_j^T
+        const uint32_t a = sbase + S::kQ + t * S::kOperand;
+        const uint32_t k = sbase + S::kK + (j & 1) * S::kOperand;
 #pragma unroll
-      for (int i = 0; i < kDim / 16; ++i) {
-        const uint32_t off = (i / 4) * S::kBlock + (i % 4) * 32;
-        asm volatile(
-            "{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\n"
-            "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}"
-            :: "r"(t_s(t)), "l"(smem_desc(a + off)), "l"(smem_desc(k + off)), "r"(idesc_s),
-               "r"(i > 0 ? 1u : 0u));
-      }
-      commit_to(s_full(t));
-    };
-    auto values = [&](int t, int j) {  // O_t += P_t V_j
-      const uint32_t v = sbase + S::kV + (j & 1) * S::kOperand;
+        for (int i = 0; i < kDim / 16; ++i) {
+          const uint32_t off = (i / 4) * S::kBlock + (i % 4) * 32;
+          asm volatile(
+              "{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\n"
+              "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}"
+              :: "r"(t_s(t)), "l"(smem_desc(a + off)), "l"(smem_desc(k + off)), "r"(idesc_s),
+                 "r"(i > 0 ? 1u : 0u));
+        }
+        commit_to(s_full(t));
+      };
+      auto values = [&](int j) {  // O += P V_j
+        const uint32_t v = sbase + S::kV + (j & 1) * S::kOperand;
 #pragma unroll
-      for (int i = 0; i < kKeys / 16; ++i) {
-        asm volatile(
-            "{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\n"
-            "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}"
-            :: "r"(t_o(t)), "r"(t_s(t) + 8 * i), "l"(smem_desc_mn(v + i * 2048, S::kBlock)),
-               "r"(idesc_o), "r"(j > 0 || i > 0 ? 1u : 0u));
-      }
-      commit_to(o_done(t));
-    };
-    bool ok = nsteps == 0 || (wait(q_full, 0) && wait(k_full(0), 0));
-    if (nsteps > 0 && ok) {
-      asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-      for (int t = 0; t < 2; ++t)
-        if (steps[t] > 0) scores(t, 0);
-      commit_to(k_empty(0));
-    }
-    for (int j = 0; j < nsteps && ok; ++j) {
-      ok = wait(v_full(j & 1), j >> 1);
-      const bool more = j + 1 < nsteps;
-      bool have_k = false;
-      for (int t = 0; t < 2 && ok; ++t) {
-        if (j < steps[t]) {
-          ok = wait(p_full(t), j);
+        for (int i = 0; i < kKeys / 16; ++i) {
+          asm volatile(
+              "{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\n"
+              "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}"
+              :: "r"(t_o(t)), "r"(t_s(t) + 8 * i), "l"(smem_desc_mn(v + i * 2048, S::kBlock)),
+                 "r"(idesc_o), "r"(j > 0 || i > 0 ? 1u : 0u));
+        }
+        commit_to(o_done(t));
+      };
+      // Both issuers pass every step's barriers, also those past their tile's last step, so
+      // that each slot's phase ends with one arrival of each.
+      bool ok = nsteps > 0 && wait(q_full, 0);
+      for (int j = -1; j < nsteps && ok; ++j) {
+        if (j >= 0) {
+          ok = wait(v_full(j & 1), j >> 1) && (j >= n || wait(p_full(t), j));
           if (!ok) break;
           asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-          values(t, j);
+          if (j < n) values(j);
+          commit_to(v_empty(j & 1));
         }
-        if (j + 1 < steps[t]) {
-          if (!have_k) {
-            ok = wait(k_full((j + 1) & 1), (j + 1) >> 1);
-            if (!ok) break;
-            asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-            have_k = true;
-          }
-          scores(t, j + 1);
+        if (j + 1 < nsteps) {
+          ok = wait(k_full((j + 1) & 1), (j + 1) >> 1);
+          if (!ok) break;
+          asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+          if (j + 1 < n) scores(j + 1);
+          commit_to(k_empty((j + 1) & 1));
         }
       }
-      if (!ok) break;
-      commit_to(v_empty(j & 1));
-      if (more) commit_to(k_empty((j + 1) & 1));
+      // every product issued is done before TMEM and shared memory go
+      commit_to(all_done(t));
+      mbar_wait(all_done(t), 0);
     }
-    // every product issued is done before TMEM and shared memory go
-    commit_to(all_done);
-    mbar_wait(all_done, 0);
   }
   __syncwarp();
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
