@@ -321,7 +321,8 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) dq4_kv8_prefill_kernel(con
     bool ok = true;
     for (int j = 0; j < n; ++j) {
       const int slot = j & 1;
-      ok = wait_warp(s_full(t), j) && wait_warp(v_full(slot), j >> 1);
+      // (the step's scales come with V, long before the scores do)
+      ok = wait_warp(v_full(slot), j >> 1) && wait_warp(s_full(t), j);
       if (!ok) break;
       asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
       const uint32_t gran = sbase + S::kGran + slot * kGrans * 16;
@@ -521,22 +522,19 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) dq4_kv8_prefill_kernel(con
       };
       // Both issuers pass every step's barriers, also those past their tile's last step, so
       // that each slot's phase ends with one arrival of each.
+      // The weights are waited for last: what follows is then issued in one go.
       bool ok = nsteps > 0 && wait(q_full, 0);
       for (int j = -1; j < nsteps && ok; ++j) {
-        if (j >= 0) {
-          ok = wait(v_full(j & 1), j >> 1) && (j >= n || wait(p_full(t), j));
-          if (!ok) break;
-          asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-          if (j < n) values(j);
-          commit_to(v_empty(j & 1));
-        }
-        if (j + 1 < nsteps) {
-          ok = wait(k_full((j + 1) & 1), (j + 1) >> 1);
-          if (!ok) break;
-          asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-          if (j + 1 < n) scores(j + 1);
-          commit_to(k_empty((j + 1) & 1));
-        }
+        const bool more = j + 1 < nsteps;
+        if (j >= 0) ok = wait(v_full(j & 1), j >> 1);
+        if (more) ok = ok && wait(k_full((j + 1) & 1), (j + 1) >> 1);
+        if (j >= 0 && j < n) ok = ok && wait(p_full(t), j);
+        if (!ok) break;
+        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+        if (j >= 0 && j < n) values(j);
+        if (j >= 0) commit_to(v_empty(j & 1));
+        if (j + 1 < n) scores(j + 1);
+        if (more) commit_to(k_empty((j + 1) & 1));
       }
       // every product issued is done before TMEM and shared memory go
       commit_to(all_done(t));
