@@ -17,6 +17,14 @@ __device__ __forceinline__ void wait_for_stream() {
   asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
+// A plain load.  What a kernel before may have written is read with these only: a read-only
+// (non-coherent) load has no place in the order of memory accesses, so that it could be moved
+// ahead of wait_for_stream.
+template <typename T>
+__device__ __forceinline__ T load_global(const T* p) {
+  return *p;
+}
+
 // ------------------------------------------------------------ groups of four values
 struct F4 {
   float v[4];
@@ -57,9 +65,9 @@ template <int DT>
 __device__ __forceinline__ Raw4<DT> load4(const typename Elem<DT>::T* p) {
   Raw4<DT> r;
   if constexpr (DT == DQ4_OUT_F32) {
-    r.u = __ldg(reinterpret_cast<const uint4*>(p));
+    r.u = load_global(reinterpret_cast<const uint4*>(p));
   } else {
-    r.u = __ldg(reinterpret_cast<const uint2*>(p));
+    r.u = load_global(reinterpret_cast<const uint2*>(p));
   }
   return r;
 }

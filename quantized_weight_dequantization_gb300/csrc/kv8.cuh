@@ -33,7 +33,7 @@ struct Seq {
 
 __device__ __forceinline__ int64_t seq_row(const Batch& s, int64_t b) {
   if (s.cu == nullptr) return b;
-  const int64_t r = __ldg(s.cu + b);
+  const int64_t r = load_global(s.cu + b);
   return r < 0 ? 0 : r > s.tokens ? s.tokens : r;
 }
 
@@ -42,7 +42,7 @@ __device__ __forceinline__ Seq seq_at(const Batch& s, int64_t b) {
   q.row = seq_row(s, b);
   const int64_t n = s.cu ? seq_row(s, b + 1) - q.row : 1;
   q.n = n < 0 ? 0 : int(n);
-  q.len = __ldg(s.lens + b);
+  q.len = load_global(s.lens + b);
   return q;
 }
 

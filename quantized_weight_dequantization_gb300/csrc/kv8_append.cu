@@ -86,7 +86,7 @@ __global__ void __launch_bounds__(1024) dq4_kv8_append_kernel(const AppendArgs p
   const int j = (begin >> log2_page) + int(blockIdx.x - u0);  // the page within the sequence
   const int lo = max(begin, j << log2_page), hi = min(q.len, (j + 1) << log2_page);
   if (lo >= hi) return;
-  const int id = j >= 0 && j < p.s.table_width ? __ldg(p.s.table + b * p.s.table_stride + j) : -1;
+  const int id = j >= 0 && j < p.s.table_width ? load_global(p.s.table + b * p.s.table_stride + j) : -1;
   if (id < 0 || id >= p.c.pages) {
     if (p.bad && tid == 0 && head == 0 && which == 0) atomicAdd(p.bad, hi - lo);
     return;
@@ -116,8 +116,8 @@ __global__ void __launch_bounds__(1024) dq4_kv8_append_kernel(const AppendArgs p
       if (p.bad && l == 0 && head == 0) atomicAdd(p.bad, 1);
     } else if (at.turned) {
       const int64_t row0 = int64_t(pos) * (p.rotary / 2) + 4 * l;
-      turn(a[i], c[i], __ldg(reinterpret_cast<const float4*>(p.cos + row0)),
-           __ldg(reinterpret_cast<const float4*>(p.sin + row0)), p.interleaved);
+      turn(a[i], c[i], load_global(reinterpret_cast<const float4*>(p.cos + row0)),
+           load_global(reinterpret_cast<const float4*>(p.sin + row0)), p.interleaved);
     }
 #pragma unroll
     for (int k = 0; k < 4; ++k) {

@@ -27,6 +27,9 @@ struct AttendArgs {
 
 namespace {
 
+// The head of the workspace: arrival counters, of either kernel, zero between calls.
+constexpr int64_t kCounterBytes = 2048;
+
 constexpr float kMinScale = 7.888609052210118e-31f;  // 2^-100, the least scale append writes
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -110,6 +113,8 @@ __device__ __forceinline__ uint32_t f16_of_e4m3_high(uint32_t w) {
 int launch_decode(const AttendArgs& p, int head_dim, int rows, int sms, void* workspace,
                   cudaStream_t stream);
 int64_t decode_workspace_bytes();
-int launch_prefill(const AttendArgs& p, int head_dim, cudaStream_t stream);
+int launch_prefill(const AttendArgs& p, int head_dim, int sms, void* workspace,
+                   cudaStream_t stream);
+int64_t prefill_workspace_bytes(int64_t tokens, int64_t seqs, int64_t group, int head_dim);
 
 }  // namespace dq4d

@@ -19,7 +19,9 @@ extern "C" {
 int64_t dq4_kv8_attention_workspace_bytes(int64_t tokens, int64_t seqs, int32_t heads,
                                           int32_t kv_heads, int32_t head_dim) {
   if (tokens <= 0 || seqs <= 0 || heads < 1 || kv_heads < 1 || head_dim < 1) return 0;
-  return decode_workspace_bytes();
+  const int64_t few = decode_workspace_bytes();
+  const int64_t many = prefill_workspace_bytes(tokens, seqs, heads / kv_heads, head_dim);
+  return few > many ? few : many;
 }
 
 int dq4_kv8_attention(const dq4_kv8_cache* cache, const void* q, int64_t q_token_stride,
@@ -62,7 +64,7 @@ int dq4_kv8_attention(const dq4_kv8_cache* cache, const void* q, int64_t q_token
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   const int64_t rows = int64_t(max_new) * p.group;
   if (rows <= kFewRows) return launch_decode(p, cache->head_dim, int(rows), sms, workspace, s);
-  return launch_prefill(p, cache->head_dim, s);
+  return launch_prefill(p, cache->head_dim, sms, workspace, s);
 }
 
 }  // extern "C"

@@ -366,7 +366,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
                             c * (kDim / 4);
 #pragma unroll
         for (int i = 0; i < kWordsK / 2; ++i)
-          raw[i] = __ldg(reinterpret_cast<const uint4*>(q) + i);
+          raw[i] = load_global(reinterpret_cast<const uint4*>(q) + i);
       }
       const uint32_t* w = reinterpret_cast<const uint32_t*>(raw);
       float top = 0.f;
@@ -476,7 +476,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
     a.head = s.head;
     a.key = s.key0 + (s.tile0 + i - s.first) * kTile + (lane % kGrans) * 16;
     if (a.key < s.held) {
-      a.id = __ldg(p.s.table + s.b * p.s.table_stride + (a.key >> p.c.log2_page));
+      a.id = load_global(p.s.table + s.b * p.s.table_stride + (a.key >> p.c.log2_page));
       a.block = 0;
     }
     if (s.held < s.len) met_bad = 1;
@@ -486,8 +486,8 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
     if (a.block < 0) return;
     if (a.id >= 0 && a.id < p.c.pages) {
       a.block = a.id * p.c.heads + a.head;
-      a.ks = __ldg(p.c.scale[0] + a.block);
-      a.vs = __ldg(p.c.scale[1] + a.block);
+      a.ks = load_global(p.c.scale[0] + a.block);
+      a.vs = load_global(p.c.scale[1] + a.block);
     } else {
       a.block = -1;
       met_bad = 1;
@@ -846,15 +846,17 @@ int launch_one(const AttendArgs& p, int sms, cudaStream_t stream) {
 
 }  // namespace
 
+static_assert(kMaxCtas * 4 <= kCounterBytes, "a counter for each CTA");
+
 int64_t decode_workspace_bytes() {
-  return kMaxCtas * 4 + int64_t(kParts) * kMaxRows * (8 + 128 * 4);
+  return kCounterBytes + int64_t(kParts) * kMaxRows * (8 + 128 * 4);
 }
 
 int launch_decode(const AttendArgs& args, int head_dim, int rows, int sms, void* workspace,
                   cudaStream_t stream) {
   AttendArgs p = args;
   p.count = static_cast<int*>(workspace);
-  p.stats = reinterpret_cast<float2*>(p.count + kMaxCtas);
+  p.stats = reinterpret_cast<float2*>(static_cast<char*>(workspace) + kCounterBytes);
   p.part = reinterpret_cast<float*>(p.stats + int64_t(kParts) * kMaxRows);
   if (head_dim == 64)
     return rows <= 8 ? launch_one<64, 1>(p, sms, stream) : launch_one<64, 2>(p, sms, stream);

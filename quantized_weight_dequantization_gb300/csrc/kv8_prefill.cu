@@ -1,30 +1,34 @@
 // Attention over the 8-bit paged cache for many query rows a kv head (prompts and chunks of
 // them): bound by the tensor cores, 4 dim operations for each pair of a row and a key.
 //
-// A CTA owns 256 query rows of one sequence and kv head (two tiles of 128; row = new token
-// x head of the group, so that grouped heads share the keys) and walks the keys that any
-// of them sees, 128 at a time:
-//   S = Q K^T    (128 x 128, tcgen05, FP16 operands from shared memory, FP32 in TMEM)
+// A unit is 256 query rows of one sequence and kv head: two tiles of 128 (row = new token x
+// head of the group, so that grouped heads share the keys).  It walks the keys that any of
+// its rows sees, 64 at a step:
+//   S = Q K^T    (128 x 64 a tile, tcgen05, FP16 operands from shared memory, FP32 in TMEM)
 //   P = 2^(c S + log2 vs - m + kTileLift)  FP16, written over S in TMEM
 //   O += P V     (A operand P from TMEM, B operand V from shared memory, FP32 in TMEM)
 //   l += P / vs
 // with c the softmax scale times the row's and the key page's scale, and vs the page's V
 // scale, which enters the exponent so that V's codes are the operand as they are.
 //
+// One CTA runs per SM, on an equal run of all units' steps, whatever the lengths are: a
+// planning kernel lists the units and where their steps start.  A unit that several CTAs
+// share is summed from their FP32 parts, in the order of the keys, by the last of them to
+// finish, tile by tile.
+//
 // Roles (four groups of four warps):
 //  * warps 0..3 and 4..7: the softmax of tile 0 and 1, one thread a row, no shuffles.  They
-//    first bring the query rows to FP16 in shared memory.  m is the reference of a row, not
-//    always its maximum: it moves, and O and l with it, only when a score passes it by
-//    2^kSlack.  So a step's weights are computed against the reference at hand in one pass
-//    over S, with the maximum found on the way, and kept in registers; only if some row has
-//    to move is S read again;
+//    first bring a unit's query rows to FP16 in shared memory, and at its end write the
+//    result or the part.  m is the reference of a row, not always its maximum: it moves, and
+//    O and l with it, only when a score passes it by 2^kSlack.  So a step's weights are
+//    computed against the reference at hand in one pass over S, with the maximum found on
+//    the way, and kept in registers; only if some row has to move is S read again;
 //  * warps 8..11: bring keys and values from the cache to FP16 in shared memory (codes are
 //    exact in FP16), loaded a step ahead into registers;
 //  * warps 12 and 13: issue the products of tile 0 and 1.  A product holds its issuing thread
-//    longer than the tensor cores take for its 128 x 128 x 16, so one thread would not keep
-//    them busy.  While a tile's softmax runs, the tensor cores work for the other tile.
-// Registers move from the last two groups to the softmax, which holds 64 packed weights and
-// two chunks of S.
+//    longer than the tensor cores take for it, so one thread would not keep them busy.
+// Each tile has two S buffers: the scores of the next step are computed while the softmax
+// works on this one, and P V of this one while it works on the next.
 // Q, K and V are held K-major / MN-major with 128-byte swizzle: rows of 64 values.
 #include "kv8_attend.cuh"
 
@@ -32,34 +36,50 @@ namespace dq4d {
 namespace {
 
 constexpr int kTileRows = 128;     // query rows of a tile = TMEM lanes
-constexpr int kCtaRows = 2 * kTileRows;
-constexpr int kKeys = 128;         // keys of a step
+constexpr int kUnitRows = 2 * kTileRows;
+constexpr int kKeys = 64;          // keys of a step
 constexpr int kGrans = kKeys / 16; // granules of 16 keys: never of two pages
+constexpr int kSlots = 4;          // steps of keys and of values in shared memory
+// steps whose scales stay in shared memory: a step's are read until its weights are done, by
+// when the keys of no step past the fourth after it have been loaded
+constexpr int kGranSlots = 8;
 constexpr int kLoadThreads = 128;
-constexpr int kPrefillThreads = kCtaRows + kLoadThreads + 128;
-constexpr int kLoadWarp = kCtaRows / 32;
+constexpr int kPrefillThreads = kUnitRows + kLoadThreads + 128;
+constexpr int kLoadWarp = kUnitRows / 32;
 constexpr int kIssueWarp = kLoadWarp + kLoadThreads / 32;
-// registers a thread of the softmax, load and issue groups: 128 each at launch
-constexpr int kSoftmaxRegs = 152, kLoadRegs = 128, kIssueRegs = 80;
-static_assert(2 * kSoftmaxRegs + kLoadRegs + kIssueRegs == 4 * 128, "what the launch holds");
-constexpr int kSteps2 = 2;         // steps of keys in shared memory
+constexpr int kMaxCtas = 160;      // CTAs the workspace has room for
+constexpr int kOpening = 4;        // what starting and ending a unit costs, in steps
+constexpr int kMinSteps = 16;      // steps that a CTA takes at least
+constexpr int kPlanThreads = 1024;
 // P <= 2^(kTileLift + kSlack) = 2^15 fits FP16
 constexpr float kTileLift = 7.f, kSlack = 8.f;
 
+// A unit, as planned.
+struct alignas(16) Unit {
+  int64_t start;     // its first step among a kv head's, kOpening of them before its keys
+  int b, r0, rows;   // sequence, first query row, and the sequence's rows
+  int key0;          // first key, a multiple of kKeys
+  int steps[2];      // of its tiles (0: no rows)
+  int len, n, row;   // the sequence's length, new tokens and first row of q
+  int held;          // its keys that are there
+};
+static_assert(sizeof(Unit) == 48, "read as three 16-byte words");
+
 template <int kDim>
 struct PrefillSmem {
-  static constexpr int kBlocks = kDim / 64;            // 64-value column blocks
-  static constexpr int kBlock = kKeys * 128;           // bytes of one: 128 rows x 128 bytes
+  static constexpr int kBlocks = kDim / 64;         // 64-value column blocks
+  static constexpr int kQBlock = kTileRows * 128;   // bytes of one of Q: 128 rows x 128 bytes
+  static constexpr int kBlock = kKeys * 128;        // and of one of K or V
+  static constexpr int kQTile = kBlocks * kQBlock;
   static constexpr int kOperand = kBlocks * kBlock;
   static constexpr int kQ = 0;
-  static constexpr int kK = 2 * kOperand;
-  static constexpr int kV = kK + kSteps2 * kOperand;
-  static constexpr int kGran = kV + kSteps2 * kOperand;  // [step][granule]{ks, log2 vs, 1 / vs, -}
-  static constexpr int kBars = kGran + kSteps2 * kGrans * 16;
-  static constexpr int kBytes = kBars + 32 * 8 + 1024;   // + alignment slack
+  static constexpr int kK = 2 * kQTile;
+  static constexpr int kV = kK + kSlots * kOperand;
+  static constexpr int kGran = kV + kSlots * kOperand;  // [slot][granule]{ks, log2 vs, 1 / vs, -}
+  static constexpr int kBars = kGran + kGranSlots * kGrans * 16;
+  static constexpr int kBytes = kBars + 32 * 8 + 1024;  // + alignment slack
   static_assert(kBytes + 256 <= 227 * 1024, "shared memory budget");
 };
-static_assert(PrefillSmem<128>::kBytes > 116 * 1024, "one CTA per SM: it takes all of TMEM");
 
 // Shared-memory matrix descriptor of a B operand with N contiguous (MN-major), 128-byte
 // swizzle: blocks of 64 values `block` bytes apart, groups of 8 rows along K 1024 apart.
@@ -124,7 +144,7 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   return r;
 }
 
-// One pass over a row's 128 scores in TMEM (the next 32 loaded while 32 are used): weights
+// One pass over a row's 64 scores in TMEM (the next 32 loaded while 32 are used): weights
 // 2^x, x = c S + bias - from, packed in FP16 into w; l gets sum 2^x / vs; the largest x is
 // returned.  gran: the step's {ks, log2 vs, 1 / vs} of 16 keys each.  kMasked: only keys lo <=
 // key + i < hi are seen.
@@ -170,84 +190,213 @@ __device__ __forceinline__ float softmax_pass(uint32_t scores, uint32_t gran, fl
   return top;
 }
 
+// The call, and where its workspace holds what.
+struct PrefillArgs {
+  AttendArgs a;
+  Unit* units;
+  int64_t max_units;
+  int64_t* total;   // a kv head's steps, all units
+  int* count;       // [CTA][tile] arrivals at a shared unit whose last part the CTA has
+  float2* stats;    // [CTA][2][tile][row]{from, l}
+  float4* part;     // [CTA][2][tile][dim / 4][row] unnormalized O
+};
+
+// List the units: sequence b's stand at index row / 256 + b and on, as many as its rows need;
+// indexes in between are units without rows.
+__global__ void __launch_bounds__(kPlanThreads) dq4_kv8_plan_kernel(const PrefillArgs w) {
+  const AttendArgs& p = w.a;
+  __shared__ int64_t s_sums[32];
+  wait_for_stream();
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  auto first_unit = [&](int64_t b) { return seq_row(p.s, b) * p.group / kUnitRows + b; };
+  int64_t total = 0;
+  for (int64_t u0 = 0; u0 < w.max_units; u0 += kPlanThreads) {
+    const int64_t u = u0 + tid;
+    Unit x = {};
+    int64_t cost = 0;
+    if (u < w.max_units) {
+      int64_t lo = 0, hi = p.s.seqs;  // the last sequence whose first unit is at or before u
+      while (hi - lo > 1) {
+        const int64_t mid = (lo + hi) / 2;
+        if (first_unit(mid) <= u) lo = mid; else hi = mid;
+      }
+      const Seq q = seq_at(p.s, lo);
+      x.b = int(lo);
+      x.rows = q.n * p.group;
+      const int64_t r0 = (u - first_unit(lo)) * kUnitRows;
+      if (r0 < x.rows) {
+        x.r0 = int(r0);
+        x.len = q.len;
+        x.n = q.n;
+        x.row = int(q.row);
+        x.held = held_keys(p, q.len);
+        const int begin = first_key(p, q.len - q.n + x.r0 / p.group) & ~(kKeys - 1);
+        x.key0 = min(begin, x.held & ~(kKeys - 1));
+        for (int t = 0; t < 2; ++t) {
+          const int first = x.r0 + t * kTileRows;
+          if (first >= x.rows) break;
+          const int last = min(x.rows, first + kTileRows) - 1;
+          const int end = last_key(p, q.len - q.n + last / p.group, x.held);
+          // (one at least: rows that see no key get their zeros)
+          x.steps[t] = max(1, (end - x.key0 + kKeys - 1) / kKeys);
+        }
+        cost = max(x.steps[0], x.steps[1]) + kOpening;
+      }
+    }
+    int64_t run = cost;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t up = __shfl_up_sync(kAllLanes, run, o);
+      if (lane >= o) run += up;
+    }
+    __syncthreads();
+    if (lane == 31) s_sums[warp] = run;
+    __syncthreads();
+    int64_t before = total + run - cost;
+    for (int i = 0; i < kPlanThreads / 32; ++i) {
+      if (i < warp) before += s_sums[i];
+      total += s_sums[i];
+    }
+    x.start = before;
+    if (u < w.max_units) w.units[u] = x;
+  }
+  if (tid == 0) *w.total = total;
+}
+
+// A CTA's walk over its run of steps, the same for each of its roles: all kv heads' steps
+// one after the other, each head's units in their order.
+struct Walk {
+  int64_t v, v1;      // next step and end of the run
+  int64_t total;      // a head's steps
+  int64_t u;          // unit of v, or one before it
+  int head;
+  int steps;          // so far
+};
+
+// The steps [a, e) of a unit that fall to this CTA.
+struct Segment {
+  Unit x;
+  int head;
+  int a, e;
+  int step0;      // the CTA's steps before it
+  int64_t item0;  // the unit's first step of keys among all
+};
+
+__device__ __forceinline__ Walk start_walk(const PrefillArgs& w, int64_t v0, int64_t v1,
+                                           int64_t total) {
+  Walk k = {v0, v1, total, 0, int(v0 / total), 0};
+  const int64_t at = v0 - k.head * total;
+  k.u = find_last(w.max_units, at, [&](int64_t i) { return load_global(&w.units[i].start); });
+  return k;
+}
+
+// The next segment, if any (false at the end of the run).
+__device__ __forceinline__ bool next_segment(const PrefillArgs& w, Walk& k, Segment& s) {
+  while (k.v < k.v1) {
+    if (k.u >= w.max_units) {
+      k.u = 0;
+      ++k.head;
+    }
+    const int4* src = reinterpret_cast<const int4*>(w.units + k.u);
+    int4* dst = reinterpret_cast<int4*>(&s.x);
+#pragma unroll
+    for (int i = 0; i < 3; ++i) dst[i] = load_global(src + i);
+    const int steps = max(s.x.steps[0], s.x.steps[1]);
+    s.item0 = k.head * k.total + s.x.start + kOpening;
+    ++k.u;
+    if (steps == 0 || s.item0 + steps <= k.v) continue;
+    s.a = int(max(int64_t(0), k.v - s.item0));
+    k.v = min(k.v1, s.item0 + steps);
+    s.e = int(k.v - s.item0);
+    s.head = k.head;
+    s.step0 = k.steps;
+    if (s.e <= s.a) continue;
+    k.steps += s.e - s.a;
+    return true;
+  }
+  return false;
+}
+
+// The 128 threads of a tile's softmax.
+__device__ __forceinline__ void bar_tile(int t) {
+  if (t == 0) {
+    asm volatile("bar.sync 1, 128;" ::: "memory");
+  } else {
+    asm volatile("bar.sync 2, 128;" ::: "memory");
+  }
+}
+
 template <int kDim>
-__global__ void __launch_bounds__(kPrefillThreads, 1) dq4_kv8_prefill_kernel(const AttendArgs p) {
+__global__ void __launch_bounds__(kPrefillThreads, 1) dq4_kv8_prefill_kernel(const PrefillArgs w) {
   using S = PrefillSmem<kDim>;
+  const AttendArgs& p = w.a;
   extern __shared__ uint8_t smem_raw[];
   __shared__ uint32_t s_tmem;
   __shared__ volatile int s_abort;
+  __shared__ int s_last[2];
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
   const uint32_t sbase = smem_u32(base);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t bar0 = sbase + S::kBars;
   auto k_full = [&](int s) { return bar0 + 8 * s; };
-  auto k_empty = [&](int s) { return bar0 + 8 * (2 + s); };
-  auto v_full = [&](int s) { return bar0 + 8 * (4 + s); };
-  auto v_empty = [&](int s) { return bar0 + 8 * (6 + s); };
-  auto s_full = [&](int t) { return bar0 + 8 * (8 + t); };   // scores of tile t ready
-  auto p_full = [&](int t) { return bar0 + 8 * (10 + t); };  // its weights written
-  auto o_done = [&](int t) { return bar0 + 8 * (12 + t); };  // its O summed so far
-  const uint32_t q_full = bar0 + 8 * 14;
-  auto all_done = [&](int t) { return bar0 + 8 * (15 + t); };
+  auto k_empty = [&](int s) { return bar0 + 8 * (4 + s); };
+  auto v_full = [&](int s) { return bar0 + 8 * (8 + s); };
+  auto v_empty = [&](int s) { return bar0 + 8 * (12 + s); };
+  // tile t: scores ready in buffer u, its weights written there, O summed up to that step; Q
+  // there.  Steps alternate between the buffers' barriers, so that a wait never lags more
+  // than one phase behind its barrier, which a parity could not tell.
+  auto s_full = [&](int t, int u) { return bar0 + 8 * (16 + 2 * t + u); };
+  auto p_full = [&](int t, int u) { return bar0 + 8 * (20 + 2 * t + u); };
+  auto o_done = [&](int t, int u) { return bar0 + 8 * (24 + 2 * t + u); };
+  auto q_full = [&](int t) { return bar0 + 8 * (28 + t); };
+  auto all_done = [&](int t) { return bar0 + 8 * (30 + t); };
   if (tid == 0) {
     s_abort = 0;
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < kSlots; ++i) {
       mbar_init(k_full(i), kLoadThreads);
       mbar_init(v_full(i), kLoadThreads);
       mbar_init(k_empty(i), 2);
       mbar_init(v_empty(i), 2);
-      mbar_init(s_full(i), 1);
-      mbar_init(p_full(i), kTileRows);
-      mbar_init(o_done(i), 1);
     }
-    mbar_init(q_full, kCtaRows);
-    mbar_init(all_done(0), 1);
-    mbar_init(all_done(1), 1);
+    for (int t = 0; t < 2; ++t) {
+      for (int u = 0; u < 2; ++u) {
+        mbar_init(s_full(t, u), 1);
+        mbar_init(p_full(t, u), kTileRows);
+        mbar_init(o_done(t, u), 1);
+      }
+      mbar_init(q_full(t), kTileRows);
+      mbar_init(all_done(t), 1);
+    }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  wait_for_stream();
-
-  // ---- this CTA's rows: heads fastest, then the row tiles from the last one back (with a
-  // causal mask the last rows see the most keys, and the longest work starts first).
-  // Sequence b's tiles start at unit row * group / 256 + b.
-  const int64_t units = gridDim.x / p.c.heads;
-  const int head = blockIdx.x % p.c.heads;
-  const int64_t unit = units - 1 - blockIdx.x / p.c.heads;
-  auto first_unit = [&](int64_t b) { return seq_row(p.s, b) * p.group / kCtaRows + b; };
-  const int64_t b = find_last(p.s.seqs, unit, first_unit);
-  const Seq q = seq_at(p.s, b);
-  const int rows = q.n * p.group;
-  const int r0 = int(unit - first_unit(b)) * kCtaRows;
-  if (r0 >= rows) return;
-  const int held = held_keys(p, q.len);
-  // the steps of keys that tile t's rows see: from step 0 at key0 to steps[t]
-  int steps[2];
-  const int key0 = first_key(p, q.len - q.n + r0 / p.group) & ~(kKeys - 1);
-#pragma unroll
-  for (int t = 0; t < 2; ++t) {
-    const int last = min(rows, r0 + (t + 1) * kTileRows) - 1;
-    const int end = last_key(p, q.len - q.n + last / p.group, held);
-    steps[t] = r0 + t * kTileRows < rows ? max(0, (end - key0 + kKeys - 1) / kKeys) : 0;
-  }
-  const int nsteps = max(steps[0], steps[1]);
-
   if (warp == kIssueWarp) {  // the whole TMEM: S and P of both tiles, then O of both
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;"
                  :: "r"(smem_u32(&s_tmem)) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
   }
+  wait_for_stream();
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
   __syncthreads();
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
   const uint32_t tmem = s_tmem;
-  auto t_s = [&](int t) { return tmem + t * kKeys; };
-  auto t_o = [&](int t) { return tmem + 2 * kKeys + t * kDim; };
+  auto t_s = [&](int t, int u) { return tmem + t * 128 + u * kKeys; };
+  auto t_o = [&](int t) { return tmem + 256 + t * kDim; };
+
+  // ---- this CTA's run of the steps
+  const int64_t total = load_global(w.total), all = total * p.c.heads;
+  const int64_t ctas = max(int64_t(1), min(int64_t(gridDim.x), all / kMinSteps));
+  const int64_t v0 = min(int64_t(blockIdx.x), ctas) * all / ctas;
+  const int64_t v1 = min(int64_t(blockIdx.x) + 1, ctas) * all / ctas;
+  auto begin_of = [&](int64_t cta) { return cta * all / ctas; };
+  auto cta_of = [&](int64_t v) { return int(((v + 1) * ctas - 1) / all); };
+
   auto fail = [&] {
     s_abort = 1;
     if (p.bad) atomicAdd(p.bad, 1);
   };
   auto wait = [&](uint32_t bar, int phase) {
+    if (mbar_test(bar, uint32_t(phase) & 1u)) return true;
     if (s_abort) return false;
     if (mbar_wait(bar, uint32_t(phase) & 1u)) return true;
     fail();
@@ -258,147 +407,202 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) dq4_kv8_prefill_kernel(con
     return bool(__all_sync(kAllLanes, wait(bar, phase)));
   };
 
+  Segment sg;
+  Walk walk = {};
+  if (v0 < v1) walk = start_walk(w, v0, v1, total);
+
   if (warp < kLoadWarp) {
     // ------------------------------------------------------------------ softmax
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" :: "n"(kSoftmaxRegs));
     const int t = warp >> 2;
     const int row = tid & (kTileRows - 1);  // of the tile = its TMEM lane
     const uint32_t lanes = uint32_t((warp & 3) * 32) << 16;
-    const int r = r0 + t * kTileRows + row;
-    const bool real = r < rows;
-    const int tok = min(r, rows - 1) / p.group;
-    const int pos = q.len - q.n + tok;
-    const int64_t at = (q.row + tok) * p.heads + head * p.group + (min(r, rows - 1) - tok * p.group);
-    float cq;
-    {
-      uint4 raw[kDim / 8];
-#pragma unroll
-      for (int i = 0; i < kDim / 8; ++i) raw[i] = make_uint4(0, 0, 0, 0);
-      if (real) {
-        const uint16_t* src = static_cast<const uint16_t*>(p.q) +
-                              (q.row + tok) * p.token_stride +
-                              (head * p.group + r - tok * p.group) * p.head_stride;
-#pragma unroll
-        for (int i = 0; i < kDim / 8; ++i) raw[i] = __ldg(reinterpret_cast<const uint4*>(src) + i);
-      }
-      const uint32_t* w = reinterpret_cast<const uint32_t*>(raw);
-      float top = 0.f;
-#pragma unroll
-      for (int i = 0; i < kDim / 2; ++i) {
-        float x, y;
-        widen2(w[i], p.bf16, x, y);
-        top = fmaxf(top, fmaxf(fabsf(x), fabsf(y)));
-      }
-      float up, down;
-      row_scaling(top, up, down);
-      cq = down * fabsf(p.scale_log2);  // a negative scale turns the row instead
-      if (p.scale_log2 < 0.f) up = -up;
-#pragma unroll
-      for (int i = 0; i < kDim / 8; ++i) {
-        uint32_t h[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          float x, y;
-          widen2(w[4 * i + j], p.bf16, x, y);
-          h[j] = pack_f16(x * up, y * up);
-        }
-        sts_v4(sbase + S::kQ + t * S::kOperand + (i / 8) * S::kBlock + row * 128 +
-                   (((i & 7) ^ (row & 7)) << 4),
-               h[0], h[1], h[2], h[3]);
-      }
-      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-      mbar_arrive(q_full);
-    }
-    const int lo = first_key(p, pos), hi = last_key(p, pos, held);
-    // keys that every row of the tile sees
-    const int last_r = min(rows, r0 + (t + 1) * kTileRows) - 1;
-    const int all_lo = first_key(p, q.len - q.n + last_r / p.group);
-    const int all_hi = last_key(p, q.len - q.n + (r0 + t * kTileRows) / p.group, held);
-    // from: what is taken off a row's exponents (the reference m less kTileLift)
-    float from = 0.f, l = 0.f;
-    bool fresh = true;  // no key seen yet
-    const int n = steps[t];
+    int step = 0;  // the tile's steps so far: buffers and their phases
     bool ok = true;
-    for (int j = 0; j < n; ++j) {
-      const int slot = j & 1;
-      // (the step's scales come with V, long before the scores do)
-      ok = wait_warp(v_full(slot), j >> 1) && wait_warp(s_full(t), j);
+    while (ok && next_segment(w, walk, sg)) {
+      const int count = min(sg.e, sg.x.steps[t]) - sg.a;
+      if (count <= 0) continue;
+      const Unit& x = sg.x;
+      const int first = x.r0 + t * kTileRows;
+      const int r = min(first + row, x.rows - 1);
+      const bool real = first + row < x.rows;
+      const int tok = r / p.group;
+      const int pos = x.len - x.n + tok;
+      const int q_head = sg.head * p.group + r - tok * p.group;
+      const int64_t at = int64_t(x.row + tok) * p.heads + q_head;
+      // ---- the query row, scaled, to shared memory (the unit before has read its own: its
+      // last scores were waited for)
+      float cq;
+      {
+        uint4 raw[kDim / 8];
+        const uint16_t* src = static_cast<const uint16_t*>(p.q) +
+                              int64_t(x.row + tok) * p.token_stride + q_head * p.head_stride;
+#pragma unroll
+        for (int i = 0; i < kDim / 8; ++i) raw[i] = load_global(reinterpret_cast<const uint4*>(src) + i);
+        const uint32_t* h = reinterpret_cast<const uint32_t*>(raw);
+        float top = 0.f;
+#pragma unroll
+        for (int i = 0; i < kDim / 2; ++i) {
+          float y, z;
+          widen2(h[i], p.bf16, y, z);
+          top = fmaxf(top, fmaxf(fabsf(y), fabsf(z)));
+        }
+        float up, down;
+        row_scaling(top, up, down);
+        cq = down * fabsf(p.scale_log2);  // a negative scale turns the row instead
+        if (p.scale_log2 < 0.f) up = -up;
+#pragma unroll
+        for (int i = 0; i < kDim / 8; ++i) {
+          uint32_t f[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            float y, z;
+            widen2(h[4 * i + j], p.bf16, y, z);
+            f[j] = pack_f16(y * up, z * up);
+          }
+          sts_v4(sbase + S::kQ + t * S::kQTile + (i / 8) * S::kQBlock + row * 128 +
+                     (((i & 7) ^ (row & 7)) << 4),
+                 f[0], f[1], f[2], f[3]);
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        mbar_arrive(q_full(t));
+      }
+      const int lo = first_key(p, pos), hi = last_key(p, pos, x.held);
+      // keys that every row of the tile sees
+      const int last_r = min(x.rows, first + kTileRows) - 1;
+      const int all_lo = first_key(p, x.len - x.n + last_r / p.group);
+      const int all_hi = last_key(p, x.len - x.n + first / p.group, x.held);
+      // from: what is taken off a row's exponents (the reference m less kTileLift)
+      float from = 0.f, l = 0.f;
+      bool fresh = true;  // no key seen yet
+      for (int j = 0; j < count; ++j, ++step) {
+        const int u = step & 1;
+        ok = wait_warp(s_full(t, u), step >> 1);  // and with the scores, the step's scales
+        if (!ok) break;
+        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+        const uint32_t gran = sbase + S::kGran + (sg.step0 + j) % kGranSlots * (kGrans * 16);
+        const uint32_t scores = t_s(t, u) + lanes;
+        const int key = x.key0 + (sg.a + j) * kKeys;
+        const bool masked = key < all_lo || key + kKeys > all_hi;
+        uint32_t wt[kKeys / 2];
+        float more = 0.f;
+        const float top = masked ? softmax_pass<true>(scores, gran, cq, from, key, lo, hi, more, wt)
+                                 : softmax_pass<false>(scores, gran, cq, from, key, lo, hi, more, wt);
+        const bool move = fresh ? top > -INFINITY : top > kTileLift + kSlack;
+        if (__any_sync(kAllLanes, move)) {
+          const float to = move ? from + top - kTileLift : from;
+          const float keep = fresh ? 0.f : exp2_fast(from - to);
+          from = to;
+          fresh = fresh && !move;
+          l *= keep;
+          if (j > 0) {
+            ok = wait_warp(o_done(t, u ^ 1), (step - 1) >> 1);
+            if (!ok) break;
+            asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+#pragma unroll 1
+            for (int c = 0; c < kDim / 32; ++c) {
+              uint32_t o[32];
+              tmem_ld32(t_o(t) + lanes + 32 * c, o);
+#pragma unroll
+              for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * keep);
+              tmem_st<32>(t_o(t) + lanes + 32 * c, o);
+            }
+          }
+          more = 0.f;
+          softmax_pass<true>(scores, gran, cq, from, key, lo, hi, more, wt);
+        }
+        l += more;
+        tmem_st<32>(scores, wt);
+        asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+        asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+        mbar_arrive(p_full(t, u));
+      }
+      if (!ok) break;
+      // ---- the unit's end: its result, or the part of it that this CTA has
+      ok = wait_warp(o_done(t, (step - 1) & 1), (step - 1) >> 1);
       if (!ok) break;
       asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-      const uint32_t gran = sbase + S::kGran + slot * kGrans * 16;
-      const int key = key0 + j * kKeys;
-      const bool masked = key < all_lo || key + kKeys > all_hi;
-      uint32_t w[kKeys / 2];
-      float more = 0.f;
-      const float top =
-          masked ? softmax_pass<true>(t_s(t) + lanes, gran, cq, from, key, lo, hi, more, w)
-                 : softmax_pass<false>(t_s(t) + lanes, gran, cq, from, key, lo, hi, more, w);
-      const bool move = fresh ? top > -INFINITY : top > kTileLift + kSlack;
-      if (__any_sync(kAllLanes, move)) {
-        const float to = move ? from + top - kTileLift : from;
-        const float keep = fresh ? 0.f : exp2_fast(from - to);
-        from = to;
-        fresh = fresh && !move;
-        l *= keep;
-        if (j > 0) {
-          ok = wait_warp(o_done(t), j - 1);
-          if (!ok) break;
-          asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-#pragma unroll 1
-          for (int c = 0; c < kDim / 32; ++c) {
-            uint32_t o[32];
-            tmem_ld32(t_o(t) + lanes + 32 * c, o);
-#pragma unroll
-            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * keep);
-            tmem_st<32>(t_o(t) + lanes + 32 * c, o);
-          }
-        }
-        more = 0.f;
-        softmax_pass<true>(t_s(t) + lanes, gran, cq, from, key, lo, hi, more, w);
-      }
-      l += more;
-#pragma unroll
-      for (int c = 0; c < kKeys / 64; ++c) {
-        uint32_t part[32];
-#pragma unroll
-        for (int i = 0; i < 32; ++i) part[i] = w[32 * c + i];
-        tmem_st<32>(t_s(t) + lanes + 32 * c, part);
-      }
-      asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-      asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-      mbar_arrive(p_full(t));
-    }
-    // ---- the rows' results
-    if (n > 0 && ok) {
-      ok = wait_warp(o_done(t), n - 1);
-      asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-    }
-    if (ok) {
-      const float inv = l == 0.f ? 0.f : 1.f / l;
       uint4* out = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + at * kDim);
+      auto put = [&](int c, const float (&o)[8], float inv) {  // columns 8 c .. of the row
+        uint32_t f[4];
 #pragma unroll
+        for (int k = 0; k < 4; ++k) f[k] = pack_out(o[2 * k] * inv, o[2 * k + 1] * inv, p.bf16);
+        if (real) out[c] = make_uint4(f[0], f[1], f[2], f[3]);
+      };
+      auto put_lse = [&](float ref, float sum) {
+        if (real && p.lse) p.lse[at] = sum == 0.f ? -INFINITY : fmaf(ref, kLn2, logf(sum));
+      };
+      const bool whole = sg.a == 0 && count == x.steps[t];
+      const int64_t slot_at = 2 * blockIdx.x + (sg.item0 - kOpening <= v0 ? 0 : 1);
+      auto part_of = [&](int64_t s) { return w.part + (s * 2 + t) * (kDim / 4) * kTileRows + row; };
+      auto stats_of = [&](int64_t s) { return w.stats + (s * 2 + t) * kTileRows + row; };
+#pragma unroll 1
       for (int c = 0; c < kDim / 32; ++c) {
         uint32_t o[32];
-        if (n > 0) {
-          tmem_ld32(t_o(t) + lanes + 32 * c, o);
-        } else {
-#pragma unroll
-          for (int i = 0; i < 32; ++i) o[i] = 0;
-        }
-        if (real) {
+        tmem_ld32(t_o(t) + lanes + 32 * c, o);
+        if (whole) {
+          const float inv = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            uint32_t w[4];
+            float f[8];
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-              w[k] = pack_out(__uint_as_float(o[8 * i + 2 * k]) * inv,
-                              __uint_as_float(o[8 * i + 2 * k + 1]) * inv, p.bf16);
-            out[4 * c + i] = make_uint4(w[0], w[1], w[2], w[3]);
+            for (int k = 0; k < 8; ++k) f[k] = __uint_as_float(o[8 * i + k]);
+            put(4 * c + i, f, inv);
           }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            part_of(slot_at)[(8 * c + i) * kTileRows] =
+                make_float4(__uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1]),
+                            __uint_as_float(o[4 * i + 2]), __uint_as_float(o[4 * i + 3]));
         }
       }
-      if (real && p.lse)
-        p.lse[at] = l == 0.f ? -INFINITY : fmaf(from, kLn2, logf(l));
+      if (whole) {
+        put_lse(from, l);
+        continue;
+      }
+      *stats_of(slot_at) = make_float2(fresh ? -INFINITY : from, l);
+      const int c0 = cta_of(sg.item0), c1 = cta_of(sg.item0 + x.steps[t] - 1);
+      bar_tile(t);
+      if (row == 0) {
+        int* counter = w.count + 2 * c1 + t;
+        s_last[t] = atomic_add_acq_rel(counter, 1) == c1 - c0;
+        if (s_last[t]) *counter = 0;  // ready for the next call
+      }
+      bar_tile(t);
+      if (!s_last[t]) continue;
+      const int64_t slot0 = 2 * c0 + (sg.item0 - kOpening <= begin_of(c0) ? 0 : 1);
+      auto slot_of = [&](int c) { return c == c0 ? slot0 : int64_t(2 * c); };
+      float top = -INFINITY, sum = 0.f;
+      for (int c = c0; c <= c1; ++c) top = fmaxf(top, __ldcg(stats_of(slot_of(c))).x);
+      const float ref = top == -INFINITY ? 0.f : top;
+      for (int c = c0; c <= c1; ++c) {
+        const float2 st = __ldcg(stats_of(slot_of(c)));
+        sum = fmaf(exp2_fast(st.x - ref), st.y, sum);
+      }
+      const float inv = sum == 0.f ? 0.f : 1.f / sum;
+#pragma unroll 1
+      for (int i = 0; i < kDim / 32; ++i) {
+        float4 acc[8] = {};
+        for (int c = c0; c <= c1; ++c) {
+          const float f = exp2_fast(__ldcg(stats_of(slot_of(c))).x - ref);
+          const float4* src = part_of(slot_of(c)) + 8 * i * kTileRows;
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const float4 y = __ldcg(src + k * kTileRows);
+            acc[k].x = fmaf(f, y.x, acc[k].x);
+            acc[k].y = fmaf(f, y.y, acc[k].y);
+            acc[k].z = fmaf(f, y.z, acc[k].z);
+            acc[k].w = fmaf(f, y.w, acc[k].w);
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float4 y = acc[2 * k], z = acc[2 * k + 1];
+          const float f[8] = {y.x, y.y, y.z, y.w, z.x, z.y, z.z, z.w};
+          put(4 * i + k, f, inv);
+        }
+      }
+      put_lse(ref, sum);
     }
   } else if (warp < kIssueWarp) {
     // --------------------------------------------------- keys and values to FP16
@@ -415,37 +619,55 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) dq4_kv8_prefill_kernel(con
     const uint32_t line = (col >> 2) * S::kBlock + row0 * 128;
     const uint32_t to[2] = {line + (((2 * (col & 3)) ^ (row0 & 7)) << 4),
                             line + (((2 * (col & 3) + 1) ^ (row0 & 7)) << 4)};
-    bool met_bad = held < q.len;
-    const int32_t* table = p.s.table + b * p.s.table_stride;
+    const int page_bytes = p.c.page * kDim;
+    bool met_bad = false;
+    // Where the next step to read stands: its segment, and the step within the unit.
+    bool more = next_segment(w, walk, sg);
+    int j = more ? sg.a : 0;
     // Lane x holds granule x % kGrans of a step: its page's block (page * kv_heads + head), or
     // -1 where there are no such keys.
-    auto find_block = [&](int j) {
-      const int key = key0 + j * kKeys + (lane & (kGrans - 1)) * 16;
-      if (j >= nsteps || key >= held) return -1;
-      const int id = __ldg(table + (key >> p.c.log2_page));
-      if (id >= 0 && id < p.c.pages) return int(id * p.c.heads + head);
-      met_bad = true;
-      return -1;
+    struct Step {
+      int key, held, block;  // first key
+    };
+    auto find_step = [&] {
+      Step s = {0, 0, -1};
+      if (!more) return s;
+      s.key = sg.x.key0 + j * kKeys;
+      s.held = sg.x.held;
+      if (s.held < sg.x.len) met_bad = true;
+      const int key = s.key + (lane & (kGrans - 1)) * 16;
+      if (key < s.held) {
+        const int id =
+            load_global(p.s.table + sg.x.b * p.s.table_stride + (key >> p.c.log2_page));
+        if (id >= 0 && id < p.c.pages) {
+          s.block = id * p.c.heads + sg.head;
+        } else {
+          met_bad = true;
+        }
+      }
+      if (++j == sg.e) {
+        more = next_segment(w, walk, sg);
+        j = sg.a;
+      }
+      return s;
     };
     uint4 raw[2][kPasses];
     float gk, gv;
-    const int page_bytes = p.c.page * kDim;
-    auto fetch = [&](int j, int block) {
+    auto fetch = [&](const Step& s) {
 #pragma unroll
       for (int i = 0; i < kPasses; ++i) {
-        const int row = row0 + i * kRowsPass;
-        const int key = key0 + j * kKeys + row;
-        int at = __shfl_sync(kAllLanes, block, row >> 4);
-        if (key >= held) at = -1;  // a slot never written: it may hold no number
+        const int row = row0 + i * kRowsPass, key = s.key + row;
+        int at = __shfl_sync(kAllLanes, s.block, row >> 4);
+        if (key >= s.held) at = -1;  // a slot never written: it may hold no number
         const int64_t off =
             int64_t(at) * page_bytes + ((key & (p.c.page - 1)) * kDim + col * 16);
 #pragma unroll
         for (int x = 0; x < 2; ++x)
           raw[x][i] = at < 0 ? make_uint4(0, 0, 0, 0)
-                             : __ldg(reinterpret_cast<const uint4*>(p.c.codes[x] + off));
+                             : load_global(reinterpret_cast<const uint4*>(p.c.codes[x] + off));
       }
-      gk = block < 0 ? 0.f : __ldg(p.c.scale[0] + block);
-      gv = block < 0 ? -1.f : __ldg(p.c.scale[1] + block);
+      gk = s.block < 0 ? 0.f : load_global(p.c.scale[0] + s.block);
+      gv = s.block < 0 ? -1.f : load_global(p.c.scale[1] + s.block);
     };
     auto put = [&](uint32_t at, const uint4& v) {
       sts_v4(at + to[0], f16_of_e4m3(v.x), f16_of_e4m3_high(v.x), f16_of_e4m3(v.y),
@@ -453,92 +675,111 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) dq4_kv8_prefill_kernel(con
       sts_v4(at + to[1], f16_of_e4m3(v.z), f16_of_e4m3_high(v.z), f16_of_e4m3(v.w),
              f16_of_e4m3_high(v.w));
     };
-    fetch(0, find_block(0));
-    int block = find_block(1);
-    for (int j = 0; j < nsteps; ++j) {
-      const int slot = j & 1;
-      bool ok = j < kSteps2 || wait(k_empty(slot), (j >> 1) - 1);
+    bool have = more;
+    Step s = find_step();
+    fetch(s);
+    bool have_next = more;
+    s = find_step();
+    for (int g = 0; have; ++g) {
+      const int slot = g % kSlots;
+      bool ok = g < kSlots || wait(k_empty(slot), g / kSlots - 1);
       if (!__all_sync(kAllLanes, ok)) break;
 #pragma unroll
       for (int i = 0; i < kPasses; ++i)
         put(sbase + S::kK + slot * S::kOperand + i * kRowsPass * 128, raw[0][i]);
-      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-      mbar_arrive(k_full(slot));
-      ok = j < kSteps2 || wait(v_empty(slot), (j >> 1) - 1);
-      if (!__all_sync(kAllLanes, ok)) break;
-#pragma unroll
-      for (int i = 0; i < kPasses; ++i)
-        put(sbase + S::kV + slot * S::kOperand + i * kRowsPass * 128, raw[1][i]);
       if (lw == 0 && lane < kGrans) {
         // keys that are not there: S = 0 and an exponent of -infinity
         const float vs = used_scale(gv);
         const bool none = gv == -1.f;
-        sts_v4(sbase + S::kGran + (slot * kGrans + lane) * 16, __float_as_uint(gk),
+        sts_v4(sbase + S::kGran + (g % kGranSlots * kGrans + lane) * 16, __float_as_uint(gk),
                __float_as_uint(none ? -INFINITY : log2f(vs)), __float_as_uint(none ? 0.f : 1.f / vs),
                0);
       }
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      mbar_arrive(k_full(slot));
+      ok = g < kSlots || wait(v_empty(slot), g / kSlots - 1);
+      if (!__all_sync(kAllLanes, ok)) break;
+#pragma unroll
+      for (int i = 0; i < kPasses; ++i)
+        put(sbase + S::kV + slot * S::kOperand + i * kRowsPass * 128, raw[1][i]);
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       mbar_arrive(v_full(slot));
-      if (j + 1 < nsteps) {
-        fetch(j + 1, block);
-        block = find_block(j + 2);
+      have = have_next;
+      if (have) {
+        fetch(s);
+        have_next = more;
+        s = find_step();
       }
     }
     if (p.bad && __any_sync(kAllLanes, met_bad) && lane == 0) atomicAdd(p.bad, 1);
   } else {
     // -------------------------------------------------------------- the products
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(kIssueRegs));
     const int t = warp - kIssueWarp;
-    if (t < 2 && lane == 0) {
+    if (t < 2) {
       const uint32_t idesc_s = instr_desc_f16<kTileRows, kKeys>(false);
       const uint32_t idesc_o =
           instr_desc_f16<kTileRows, kDim>(false) | (1u << 16);  // B: N contiguous
-      const int n = steps[t];
-      auto scores = [&](int j) {  // S = Q K_j^T
-        const uint32_t a = sbase + S::kQ + t * S::kOperand;
-        const uint32_t k = sbase + S::kK + (j & 1) * S::kOperand;
+      auto scores = [&](int slot, int u) {  // S = Q K^T
+        const uint32_t a = sbase + S::kQ + t * S::kQTile;
+        const uint32_t k = sbase + S::kK + slot * S::kOperand;
 #pragma unroll
         for (int i = 0; i < kDim / 16; ++i) {
-          const uint32_t off = (i / 4) * S::kBlock + (i % 4) * 32;
           asm volatile(
               "{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\n"
               "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}"
-              :: "r"(t_s(t)), "l"(smem_desc(a + off)), "l"(smem_desc(k + off)), "r"(idesc_s),
+              :: "r"(t_s(t, u)), "l"(smem_desc(a + (i / 4) * S::kQBlock + (i % 4) * 32)),
+                 "l"(smem_desc(k + (i / 4) * S::kBlock + (i % 4) * 32)), "r"(idesc_s),
                  "r"(i > 0 ? 1u : 0u));
         }
-        commit_to(s_full(t));
+        commit_to(s_full(t, u));
       };
-      auto values = [&](int j) {  // O += P V_j
-        const uint32_t v = sbase + S::kV + (j & 1) * S::kOperand;
+      auto values = [&](int slot, int u, bool first) {  // O += P V
+        const uint32_t v = sbase + S::kV + slot * S::kOperand;
 #pragma unroll
         for (int i = 0; i < kKeys / 16; ++i) {
           asm volatile(
               "{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\n"
               "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}"
-              :: "r"(t_o(t)), "r"(t_s(t) + 8 * i), "l"(smem_desc_mn(v + i * 2048, S::kBlock)),
-                 "r"(idesc_o), "r"(j > 0 || i > 0 ? 1u : 0u));
+              :: "r"(t_o(t)), "r"(t_s(t, u) + 8 * i), "l"(smem_desc_mn(v + i * 2048, S::kBlock)),
+                 "r"(idesc_o), "r"(!first || i > 0 ? 1u : 0u));
         }
-        commit_to(o_done(t));
+        commit_to(o_done(t, u));
       };
       // Both issuers pass every step's barriers, also those past their tile's last step, so
       // that each slot's phase ends with one arrival of each.
-      // The weights are waited for last: what follows is then issued in one go.
-      bool ok = nsteps > 0 && wait(q_full, 0);
-      for (int j = -1; j < nsteps && ok; ++j) {
-        const bool more = j + 1 < nsteps;
-        if (j >= 0) ok = wait(v_full(j & 1), j >> 1);
-        if (more) ok = ok && wait(k_full((j + 1) & 1), (j + 1) >> 1);
-        if (j >= 0 && j < n) ok = ok && wait(p_full(t), j);
-        if (!ok) break;
-        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-        if (j >= 0 && j < n) values(j);
-        if (j >= 0) commit_to(v_empty(j & 1));
-        if (j + 1 < n) scores(j + 1);
-        if (more) commit_to(k_empty((j + 1) & 1));
+      int g = 0, step = 0, units = 0;  // steps, this tile's steps, its units so far
+      bool ok = true;
+      while (ok && next_segment(w, walk, sg)) {
+        const int count = sg.e - sg.a;
+        const int n = max(0, min(sg.e, sg.x.steps[t]) - sg.a);  // of this tile
+        if (lane == 0) {
+          if (n > 0) ok = wait(q_full(t), units);
+          // step j's weights are waited for last: P V of j and the scores of j + 2, which take
+          // their place, are then issued in one go
+          for (int j = -2; j < count && ok; ++j) {
+            const int gv = g + j, gk = g + j + 2, sv = step + j, sk = step + j + 2;
+            const bool more = j + 2 < count;
+            if (j >= 0) ok = wait(v_full(gv % kSlots), gv / kSlots);
+            if (more) ok = ok && wait(k_full(gk % kSlots), gk / kSlots);
+            if (j >= 0 && j < n) ok = ok && wait(p_full(t, sv & 1), sv >> 1);
+            if (!ok) break;
+            asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+            if (j >= 0 && j < n) values(gv % kSlots, sv & 1, j == 0);
+            if (j >= 0) commit_to(v_empty(gv % kSlots));
+            if (j + 2 < n) scores(gk % kSlots, sk & 1);
+            if (more) commit_to(k_empty(gk % kSlots));
+          }
+        }
+        ok = __shfl_sync(kAllLanes, int(ok), 0) != 0;
+        g += count;
+        step += n;
+        units += n > 0;
       }
       // every product issued is done before TMEM and shared memory go
-      commit_to(all_done(t));
-      mbar_wait(all_done(t), 0);
+      if (lane == 0) {
+        commit_to(all_done(t));
+        mbar_wait(all_done(t), 0);
+      }
     }
   }
   __syncwarp();
@@ -550,24 +791,51 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) dq4_kv8_prefill_kernel(con
   }
 }
 
+static_assert(kMaxCtas * 2 * 4 <= kCounterBytes, "a counter for each CTA and tile");
+
+int64_t max_units(int64_t tokens, int64_t seqs, int64_t group) {
+  return tokens * group / kUnitRows + seqs;
+}
+
+int64_t plan_bytes(int64_t units) { return 64 + (units + 1) * int64_t(sizeof(Unit)); }
+
 template <int kDim>
-int launch_one(const AttendArgs& p, cudaStream_t stream) {
+int launch_one(const PrefillArgs& w, int sms, cudaStream_t stream) {
+  // more than half an SM's shared memory: one CTA per SM, as it takes all of TMEM
   constexpr int kBytes =
       PrefillSmem<kDim>::kBytes > 117 * 1024 ? PrefillSmem<kDim>::kBytes : 117 * 1024;
-  const int64_t units = p.s.tokens * p.group / kCtaRows + p.s.seqs;
-  if (units * p.c.heads > kMaxGrid) return DQ4_ERR_N;
   auto kernel = dq4_kv8_prefill_kernel<kDim>;
   const cudaError_t e =
       cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes);
   if (e != cudaSuccess) return fail_cuda(DQ4_ERR_LAUNCH, e);
-  return launch_ordered(kernel, dim3(unsigned(units * p.c.heads)), kPrefillThreads, kBytes, stream,
-                        p);
+  if (const int st = launch_ordered(dq4_kv8_plan_kernel, dim3(1), kPlanThreads, 0, stream, w))
+    return st;
+  return launch_ordered(kernel, dim3(unsigned(sms < kMaxCtas ? sms : kMaxCtas)), kPrefillThreads,
+                        kBytes, stream, w);
 }
 
 }  // namespace
 
-int launch_prefill(const AttendArgs& p, int head_dim, cudaStream_t stream) {
-  return head_dim == 64 ? launch_one<64>(p, stream) : launch_one<128>(p, stream);
+int64_t prefill_workspace_bytes(int64_t tokens, int64_t seqs, int64_t group, int head_dim) {
+  return kCounterBytes + int64_t(kMaxCtas) * 4 * kTileRows * (8 + int64_t(head_dim) * 4) +
+         plan_bytes(max_units(tokens, seqs, group)) + 256;
+}
+
+int launch_prefill(const AttendArgs& p, int head_dim, int sms, void* workspace,
+                   cudaStream_t stream) {
+  PrefillArgs w = {};
+  w.a = p;
+  w.max_units = max_units(p.s.tokens, p.s.seqs, p.group);
+  char* at = static_cast<char*>(workspace);
+  w.count = reinterpret_cast<int*>(at);
+  at += kCounterBytes;
+  w.stats = reinterpret_cast<float2*>(at);
+  at += int64_t(kMaxCtas) * 4 * kTileRows * 8;
+  w.part = reinterpret_cast<float4*>(at);
+  at += int64_t(kMaxCtas) * 4 * kTileRows * head_dim * 4;
+  w.total = reinterpret_cast<int64_t*>(at);
+  w.units = reinterpret_cast<Unit*>(at + 64);
+  return head_dim == 64 ? launch_one<64>(w, sms, stream) : launch_one<128>(w, sms, stream);
 }
 
 }  // namespace dq4d

@@ -43,7 +43,7 @@ struct NormArgs {
 // The position's row of the tables, or -1 where it is outside them (all lanes alike).
 __device__ __forceinline__ int64_t table_row(const NormArgs& p, int64_t t) {
   if (p.cos == nullptr) return 0;
-  const int64_t pos = __ldg(p.positions + t);
+  const int64_t pos = load_global(p.positions + t);
   return pos >= 0 && pos < p.table_rows ? pos : -1;
 }
 
@@ -96,8 +96,8 @@ __global__ void __launch_bounds__(kNormThreads) dq4_qk_norm_kernel(const NormArg
   const int64_t row = table_row(p, t);
   float4 cs = {}, sn = {};
   if (at.turned && row >= 0) {
-    cs = __ldg(reinterpret_cast<const float4*>(p.cos + row * (p.rotary / 2) + 4 * l));
-    sn = __ldg(reinterpret_cast<const float4*>(p.sin + row * (p.rotary / 2) + 4 * l));
+    cs = load_global(reinterpret_cast<const float4*>(p.cos + row * (p.rotary / 2) + 4 * l));
+    sn = load_global(reinterpret_cast<const float4*>(p.sin + row * (p.rotary / 2) + 4 * l));
   }
   T* out = static_cast<T*>(p.out[which]) + t * heads * kDim;
 #pragma unroll
@@ -203,8 +203,8 @@ __global__ void __launch_bounds__(kBwdThreads) dq4_qk_norm_backward_kernel(const
     const int64_t row = table_row(p, t);
     float4 cs = {}, sn = {};
     if (at.turned && row >= 0) {
-      cs = __ldg(reinterpret_cast<const float4*>(p.cos + row * (p.rotary / 2) + 4 * l));
-      sn = __ldg(reinterpret_cast<const float4*>(p.sin + row * (p.rotary / 2) + 4 * l));
+      cs = load_global(reinterpret_cast<const float4*>(p.cos + row * (p.rotary / 2) + 4 * l));
+      sn = load_global(reinterpret_cast<const float4*>(p.sin + row * (p.rotary / 2) + 4 * l));
       sn = make_float4(-sn.x, -sn.y, -sn.z, -sn.w);
     }
     T* out = static_cast<T*>(p.out[which]) + t * heads * kDim;
@@ -319,7 +319,7 @@ __global__ void __launch_bounds__(32 * kAnyWarps) dq4_qk_norm_any_kernel(const N
       const int j = p.interleaved ? i >> 1 : i % half;
       const bool second = p.interleaved ? i & 1 : i >= half;
       const int pair = p.interleaved ? i ^ 1 : second ? i - half : i + half;
-      const float c = __ldg(p.cos + row * half + j), s = sign * __ldg(p.sin + row * half + j);
+      const float c = load_global(p.cos + row * half + j), s = sign * load_global(p.sin + row * half + j);
       const float v = __fmul_rn(f(i), c), u = __fmul_rn(f(pair), s);
       return second ? __fadd_rn(v, u) : __fsub_rn(v, u);
     };

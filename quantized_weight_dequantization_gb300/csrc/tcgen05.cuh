@@ -41,6 +41,16 @@ __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity,
   return done != 0;
 }
 
+// Whether the phase has completed, without suspending the thread.
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n.reg .pred p;\nmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+      "selp.u32 %0, 1, 0, p;\n}"
+      : "=r"(done) : "r"(bar), "r"(parity) : "memory");
+  return done != 0;
+}
+
 // Poll two barriers at once (their round trips overlap); true when both phases completed.
 __device__ __forceinline__ bool mbar_try2(uint32_t bar_a, uint32_t par_a, uint32_t bar_b,
                                           uint32_t par_b) {
