@@ -25,8 +25,9 @@
 //    the way, and kept in registers; only if some row has to move is S read again;
 //  * warps 8..11: bring keys and values from the cache to FP16 in shared memory (codes are
 //    exact in FP16), loaded a step ahead into registers;
-//  * warps 12 and 13: issue the products of tile 0 and 1.  A product holds its issuing thread
-//    longer than the tensor cores take for it, so one thread would not keep them busy.
+//  * warps 12 .. 15: issue Q K^T of tile 0 and 1, and P V of tile 0 and 1.  The tensor cores
+//    take a new product about when the last one ends, so that a thread that waits for one
+//    kind's operands would keep them from the other kinds.
 // Each tile has two S buffers: the scores of the next step are computed while the softmax
 // works on this one, and P V of this one while it works on the next.
 // Q, K and V are held K-major / MN-major with 128-byte swizzle: rows of 64 values.
@@ -77,7 +78,7 @@ struct PrefillSmem {
   static constexpr int kV = kK + kSlots * kOperand;
   static constexpr int kGran = kV + kSlots * kOperand;  // [slot][granule]{ks, log2 vs, 1 / vs, -}
   static constexpr int kBars = kGran + kGranSlots * kGrans * 16;
-  static constexpr int kBytes = kBars + 32 * 8 + 1024;  // + alignment slack
+  static constexpr int kBytes = kBars + 34 * 8 + 1024;  // + alignment slack
   static_assert(kBytes + 256 <= 227 * 1024, "shared memory budget");
 };
 
@@ -98,9 +99,27 @@ __device__ __forceinline__ void sts_v4(uint32_t addr, uint32_t a, uint32_t b, ui
                :: "r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
 
-__device__ __forceinline__ void commit_to(uint32_t bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];"
-               :: "r"(bar) : "memory");
+// The products and their commits, by the lane of the warp that leads (the other operands are
+// the same for all lanes).  A from shared memory, or from TMEM.
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add,
+                                       uint32_t leads) {
+  asm volatile(
+      "{\n.reg .pred p, q;\nsetp.ne.b32 p, %4, 0;\nsetp.ne.b32 q, %5, 0;\n"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}"
+      :: "r"(d), "l"(a), "l"(b), "r"(idesc), "r"(uint32_t(add)), "r"(leads));
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add,
+                                       uint32_t leads) {
+  asm volatile(
+      "{\n.reg .pred p, q;\nsetp.ne.b32 p, %4, 0;\nsetp.ne.b32 q, %5, 0;\n"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}"
+      :: "r"(d), "r"(a), "l"(b), "r"(idesc), "r"(uint32_t(add)), "r"(leads));
+}
+__device__ __forceinline__ void commit_if(uint32_t bar, uint32_t leads) {
+  asm volatile(
+      "{\n.reg .pred q;\nsetp.ne.b32 q, %1, 0;\n"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}"
+      :: "r"(bar), "r"(leads) : "memory");
 }
 
 // 32 consecutive columns of this warp's TMEM lanes.  The registers may be read only after
@@ -350,7 +369,7 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) dq4_kv8_prefill_kernel(con
   auto p_full = [&](int t, int u) { return bar0 + 8 * (20 + 2 * t + u); };
   auto o_done = [&](int t, int u) { return bar0 + 8 * (24 + 2 * t + u); };
   auto q_full = [&](int t) { return bar0 + 8 * (28 + t); };
-  auto all_done = [&](int t) { return bar0 + 8 * (30 + t); };
+  auto all_done = [&](int i) { return bar0 + 8 * (30 + i); };
   if (tid == 0) {
     s_abort = 0;
     for (int i = 0; i < kSlots; ++i) {
@@ -367,6 +386,7 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) dq4_kv8_prefill_kernel(con
       }
       mbar_init(q_full(t), kTileRows);
       mbar_init(all_done(t), 1);
+      mbar_init(all_done(2 + t), 1);
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -714,73 +734,60 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) dq4_kv8_prefill_kernel(con
     if (p.bad && __any_sync(kAllLanes, met_bad) && lane == 0) atomicAdd(p.bad, 1);
   } else {
     // -------------------------------------------------------------- the products
-    const int t = warp - kIssueWarp;
-    if (t < 2) {
-      const uint32_t idesc_s = instr_desc_f16<kTileRows, kKeys>(false);
-      const uint32_t idesc_o =
-          instr_desc_f16<kTileRows, kDim>(false) | (1u << 16);  // B: N contiguous
-      auto scores = [&](int slot, int u) {  // S = Q K^T
-        const uint32_t a = sbase + S::kQ + t * S::kQTile;
-        const uint32_t k = sbase + S::kK + slot * S::kOperand;
+    // Warps kIssueWarp + t issue tile t's scores, kIssueWarp + 2 + t its P V.  The whole warp
+    // runs this, one lane issues: the operands are then the same for all lanes, which a
+    // branch on the lane would hide from the compiler.
+    const int role = __shfl_sync(kAllLanes, warp - kIssueWarp, 0), t = role & 1;
+    const uint32_t leads = lane == 0;
+    // (a descriptor's address counts 16 bytes)
+    const uint64_t q_desc = smem_desc(sbase + S::kQ + t * S::kQTile);
+    const uint64_t k_desc = smem_desc(sbase + S::kK);
+    const uint64_t v_desc = smem_desc_mn(sbase + S::kV, S::kBlock);
+    const uint32_t idesc_s = instr_desc_f16<kTileRows, kKeys>(false);
+    const uint32_t idesc_o = instr_desc_f16<kTileRows, kDim>(false) | (1u << 16);  // B: N contiguous
+    // Every step's barriers are passed, also past the tile's last step, so that each slot's
+    // phase ends with one arrival of each tile.
+    int g = 0, step = 0, units = 0;  // steps, this tile's steps, its units so far
+    bool ok = true;
+    while (ok && next_segment(w, walk, sg)) {
+      const int count = sg.e - sg.a;
+      const int n = max(0, min(sg.e, sg.x.steps[t]) - sg.a);  // of this tile
+      if (role < 2 && n > 0) ok = wait_warp(q_full(t), units++);
+      for (int j = 0; j < count && ok; ++j, ++g) {
+        const int slot = g % kSlots, phase = g / kSlots, u = step & 1;
+        if (role < 2) {  // S = Q K^T, once the weights in its buffer have been used
+          ok = wait_warp(k_full(slot), phase) &&
+               (j >= n || step < 2 || wait_warp(o_done(t, u), (step >> 1) - 1));
+          if (!ok) break;
+          asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+          if (j < n) {
+            const uint64_t k = k_desc + slot * (S::kOperand / 16);
 #pragma unroll
-        for (int i = 0; i < kDim / 16; ++i) {
-          asm volatile(
-              "{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\n"
-              "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}"
-              :: "r"(t_s(t, u)), "l"(smem_desc(a + (i / 4) * S::kQBlock + (i % 4) * 32)),
-                 "l"(smem_desc(k + (i / 4) * S::kBlock + (i % 4) * 32)), "r"(idesc_s),
-                 "r"(i > 0 ? 1u : 0u));
-        }
-        commit_to(s_full(t, u));
-      };
-      auto values = [&](int slot, int u, bool first) {  // O += P V
-        const uint32_t v = sbase + S::kV + slot * S::kOperand;
-#pragma unroll
-        for (int i = 0; i < kKeys / 16; ++i) {
-          asm volatile(
-              "{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\n"
-              "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}"
-              :: "r"(t_o(t)), "r"(t_s(t, u) + 8 * i), "l"(smem_desc_mn(v + i * 2048, S::kBlock)),
-                 "r"(idesc_o), "r"(!first || i > 0 ? 1u : 0u));
-        }
-        commit_to(o_done(t, u));
-      };
-      // Both issuers pass every step's barriers, also those past their tile's last step, so
-      // that each slot's phase ends with one arrival of each.
-      int g = 0, step = 0, units = 0;  // steps, this tile's steps, its units so far
-      bool ok = true;
-      while (ok && next_segment(w, walk, sg)) {
-        const int count = sg.e - sg.a;
-        const int n = max(0, min(sg.e, sg.x.steps[t]) - sg.a);  // of this tile
-        if (lane == 0) {
-          if (n > 0) ok = wait(q_full(t), units);
-          // step j's weights are waited for last: P V of j and the scores of j + 2, which take
-          // their place, are then issued in one go
-          for (int j = -2; j < count && ok; ++j) {
-            const int gv = g + j, gk = g + j + 2, sv = step + j, sk = step + j + 2;
-            const bool more = j + 2 < count;
-            if (j >= 0) ok = wait(v_full(gv % kSlots), gv / kSlots);
-            if (more) ok = ok && wait(k_full(gk % kSlots), gk / kSlots);
-            if (j >= 0 && j < n) ok = ok && wait(p_full(t, sv & 1), sv >> 1);
-            if (!ok) break;
-            asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-            if (j >= 0 && j < n) values(gv % kSlots, sv & 1, j == 0);
-            if (j >= 0) commit_to(v_empty(gv % kSlots));
-            if (j + 2 < n) scores(gk % kSlots, sk & 1);
-            if (more) commit_to(k_empty(gk % kSlots));
+            for (int i = 0; i < kDim / 16; ++i)
+              mma_ss(t_s(t, u), q_desc + ((i / 4) * S::kQBlock + (i % 4) * 32) / 16,
+                     k + ((i / 4) * S::kBlock + (i % 4) * 32) / 16, idesc_s, i > 0, leads);
+            commit_if(s_full(t, u), leads);
           }
+          commit_if(k_empty(slot), leads);
+        } else {  // O += P V
+          ok = wait_warp(v_full(slot), phase) && (j >= n || wait_warp(p_full(t, u), step >> 1));
+          if (!ok) break;
+          asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+          if (j < n) {
+            const uint64_t v = v_desc + slot * (S::kOperand / 16);
+#pragma unroll
+            for (int i = 0; i < kKeys / 16; ++i)
+              mma_ts(t_o(t), t_s(t, u) + 8 * i, v + i * (2048 / 16), idesc_o, j > 0 || i > 0, leads);
+            commit_if(o_done(t, u), leads);
+          }
+          commit_if(v_empty(slot), leads);
         }
-        ok = __shfl_sync(kAllLanes, int(ok), 0) != 0;
-        g += count;
-        step += n;
-        units += n > 0;
-      }
-      // every product issued is done before TMEM and shared memory go
-      if (lane == 0) {
-        commit_to(all_done(t));
-        mbar_wait(all_done(t), 0);
+        step += j < n;
       }
     }
+    // every product issued is done before TMEM and shared memory go
+    commit_if(all_done(role), leads);
+    if (lane == 0) mbar_wait(all_done(role), 0);
   }
   __syncwarp();
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
