@@ -24,7 +24,8 @@
 //    computed against the reference at hand in one pass over S, with the maximum found on
 //    the way, and kept in registers; only if some row has to move is S read again;
 //  * warps 8..11: bring keys and values from the cache to FP16 in shared memory (codes are
-//    exact in FP16), loaded a step ahead into registers;
+//    exact in FP16), their codes copied to shared memory some steps ahead, where each thread
+//    takes back what it asked for itself;
 //  * warps 12 .. 15: issue Q K^T of tile 0 and 1, and P V of tile 0 and 1.  The tensor cores
 //    take a new product about when the last one ends, so that a thread that waits for one
 //    kind's operands would keep them from the other kinds.
@@ -40,16 +41,17 @@ constexpr int kTileRows = 128;     // query rows of a tile = TMEM lanes
 constexpr int kUnitRows = 2 * kTileRows;
 constexpr int kKeys = 64;          // keys of a step
 constexpr int kGrans = kKeys / 16; // granules of 16 keys: never of two pages
-constexpr int kSlots = 4;          // steps of keys and of values in shared memory
+constexpr int kSlots = 3;          // steps of keys and of values in shared memory, as FP16
+constexpr int kRawSlots = 4;       // and of their codes
 // steps whose scales stay in shared memory: a step's are read until its weights are done, by
-// when the keys of no step past the fourth after it have been loaded
+// when the keys of no step past the fifth after it have been placed
 constexpr int kGranSlots = 8;
 constexpr int kLoadThreads = 128;
 constexpr int kPrefillThreads = kUnitRows + kLoadThreads + 128;
 constexpr int kLoadWarp = kUnitRows / 32;
 constexpr int kIssueWarp = kLoadWarp + kLoadThreads / 32;
 constexpr int kMaxCtas = 160;      // CTAs the workspace has room for
-constexpr int kOpening = 4;        // what starting and ending a unit costs, in steps
+constexpr int kOpening = 13;       // what starting and ending a unit costs, in steps
 constexpr int kMinSteps = 16;      // steps that a CTA takes at least
 constexpr int kPlanThreads = 1024;
 // P <= 2^(kTileLift + kSlack) = 2^15 fits FP16
@@ -77,7 +79,11 @@ struct PrefillSmem {
   static constexpr int kK = 2 * kQTile;
   static constexpr int kV = kK + kSlots * kOperand;
   static constexpr int kGran = kV + kSlots * kOperand;  // [slot][granule]{ks, log2 vs, 1 / vs, -}
-  static constexpr int kBars = kGran + kGranSlots * kGrans * 16;
+  // codes: [slot][K, V][pass][load thread], 16 bytes each; and {block, ks, vs} of granules
+  static constexpr int kRawPass = kLoadThreads * 16;
+  static constexpr int kRaw = kGran + kGranSlots * kGrans * 16;
+  static constexpr int kNote = kRaw + kRawSlots * 2 * kKeys * kDim;
+  static constexpr int kBars = kNote + kRawSlots * kGrans * 16;
   static constexpr int kBytes = kBars + 34 * 8 + 1024;  // + alignment slack
   static_assert(kBytes + 256 <= 227 * 1024, "shared memory budget");
 };
@@ -336,6 +342,12 @@ __device__ __forceinline__ bool next_segment(const PrefillArgs& w, Walk& k, Segm
   return false;
 }
 
+// mbar_wait where the phase was not complete at first sight: kept out of line, as the roles'
+// loops share the instruction caches.
+__device__ __noinline__ bool wait_longer(uint32_t bar, uint32_t parity) {
+  return mbar_wait(bar, parity);
+}
+
 // The 128 threads of a tile's softmax.
 __device__ __forceinline__ void bar_tile(int t) {
   if (t == 0) {
@@ -359,6 +371,7 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) dq4_kv8_prefill_kernel(con
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t bar0 = sbase + S::kBars;
   auto k_full = [&](int s) { return bar0 + 8 * s; };
+  static_assert(kSlots <= 4, "barriers 0 .. 15");
   auto k_empty = [&](int s) { return bar0 + 8 * (4 + s); };
   auto v_full = [&](int s) { return bar0 + 8 * (8 + s); };
   auto v_empty = [&](int s) { return bar0 + 8 * (12 + s); };
@@ -418,7 +431,7 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) dq4_kv8_prefill_kernel(con
   auto wait = [&](uint32_t bar, int phase) {
     if (mbar_test(bar, uint32_t(phase) & 1u)) return true;
     if (s_abort) return false;
-    if (mbar_wait(bar, uint32_t(phase) & 1u)) return true;
+    if (wait_longer(bar, uint32_t(phase) & 1u)) return true;
     fail();
     return false;
   };
@@ -438,54 +451,74 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) dq4_kv8_prefill_kernel(con
     const uint32_t lanes = uint32_t((warp & 3) * 32) << 16;
     int step = 0;  // the tile's steps so far: buffers and their phases
     bool ok = true;
-    while (ok && next_segment(w, walk, sg)) {
-      const int count = min(sg.e, sg.x.steps[t]) - sg.a;
-      if (count <= 0) continue;
-      const Unit& x = sg.x;
-      const int first = x.r0 + t * kTileRows;
-      const int r = min(first + row, x.rows - 1);
-      const bool real = first + row < x.rows;
-      const int tok = r / p.group;
-      const int pos = x.len - x.n + tok;
-      const int q_head = sg.head * p.group + r - tok * p.group;
-      const int64_t at = int64_t(x.row + tok) * p.heads + q_head;
-      // ---- the query row, scaled, to shared memory (the unit before has read its own: its
-      // last scores were waited for)
-      float cq;
-      {
-        uint4 raw[kDim / 8];
-        const uint16_t* src = static_cast<const uint16_t*>(p.q) +
-                              int64_t(x.row + tok) * p.token_stride + q_head * p.head_stride;
+    // A unit as this thread's row sees it.
+    struct Row {
+      int64_t at;   // token and head, as of q and out
+      int pos;
+      bool real;
+    };
+    auto count_of = [&](const Segment& s) { return min(s.e, s.x.steps[t]) - s.a; };
+    auto next_of_tile = [&](Segment& s) {
+      while (next_segment(w, walk, s))
+        if (count_of(s) > 0) return true;
+      return false;
+    };
+    auto row_at = [&](const Segment& s, int64_t& src) {
+      const int first = s.x.r0 + t * kTileRows;
+      const int r = min(first + row, s.x.rows - 1);
+      const int tok = r / p.group, q_head = s.head * p.group + r - tok * p.group;
+      src = int64_t(s.x.row + tok) * p.token_stride + q_head * p.head_stride;
+      return Row{int64_t(s.x.row + tok) * p.heads + q_head, s.x.len - s.x.n + tok,
+                 first + row < s.x.rows};
+    };
+    // The query row, scaled, to shared memory; its factor for the scores.  (The unit before
+    // has no more use for its own: its last scores were waited for.)
+    auto load_query = [&](int64_t src) {
+      uint4 raw[kDim / 8];
 #pragma unroll
-        for (int i = 0; i < kDim / 8; ++i) raw[i] = load_global(reinterpret_cast<const uint4*>(src) + i);
-        const uint32_t* h = reinterpret_cast<const uint32_t*>(raw);
-        float top = 0.f;
+      for (int i = 0; i < kDim / 8; ++i)
+        raw[i] = load_global(
+            reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) + src) + i);
+      const uint32_t* h = reinterpret_cast<const uint32_t*>(raw);
+      float top = 0.f;
 #pragma unroll
-        for (int i = 0; i < kDim / 2; ++i) {
-          float y, z;
-          widen2(h[i], p.bf16, y, z);
-          top = fmaxf(top, fmaxf(fabsf(y), fabsf(z)));
-        }
-        float up, down;
-        row_scaling(top, up, down);
-        cq = down * fabsf(p.scale_log2);  // a negative scale turns the row instead
-        if (p.scale_log2 < 0.f) up = -up;
-#pragma unroll
-        for (int i = 0; i < kDim / 8; ++i) {
-          uint32_t f[4];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            float y, z;
-            widen2(h[4 * i + j], p.bf16, y, z);
-            f[j] = pack_f16(y * up, z * up);
-          }
-          sts_v4(sbase + S::kQ + t * S::kQTile + (i / 8) * S::kQBlock + row * 128 +
-                     (((i & 7) ^ (row & 7)) << 4),
-                 f[0], f[1], f[2], f[3]);
-        }
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        mbar_arrive(q_full(t));
+      for (int i = 0; i < kDim / 2; ++i) {
+        float y, z;
+        widen2(h[i], p.bf16, y, z);
+        top = fmaxf(top, fmaxf(fabsf(y), fabsf(z)));
       }
+      float up, down;
+      row_scaling(top, up, down);
+      if (p.scale_log2 < 0.f) up = -up;  // a negative scale turns the row instead
+#pragma unroll
+      for (int i = 0; i < kDim / 8; ++i) {
+        uint32_t f[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          float y, z;
+          widen2(h[4 * i + j], p.bf16, y, z);
+          f[j] = pack_f16(y * up, z * up);
+        }
+        sts_v4(sbase + S::kQ + t * S::kQTile + (i / 8) * S::kQBlock + row * 128 +
+                   (((i & 7) ^ (row & 7)) << 4),
+               f[0], f[1], f[2], f[3]);
+      }
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      mbar_arrive(q_full(t));
+      return down * fabsf(p.scale_log2);
+    };
+    bool have = next_of_tile(sg);
+    int64_t src = 0;
+    Row me = {};
+    float cq = 0.f;
+    if (have) {
+      me = row_at(sg, src);
+      cq = load_query(src);
+    }
+    while (have) {
+      const Unit& x = sg.x;
+      const int count = count_of(sg), first = x.r0 + t * kTileRows;
+      const int pos = me.pos;
       const int lo = first_key(p, pos), hi = last_key(p, pos, x.held);
       // keys that every row of the tile sees
       const int last_r = min(x.rows, first + kTileRows) - 1;
@@ -537,7 +570,17 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) dq4_kv8_prefill_kernel(con
         mbar_arrive(p_full(t, u));
       }
       if (!ok) break;
-      // ---- the unit's end: its result, or the part of it that this CTA has
+      // ---- the next unit's query row goes first: its scores are computed while this unit's
+      // result, or the part of it that this CTA has, is written
+      const Segment was = sg;
+      const Row mine = me;
+      const int64_t at = mine.at;
+      const bool real = mine.real;
+      have = next_of_tile(sg);
+      if (have) {
+        me = row_at(sg, src);
+        cq = load_query(src);
+      }
       ok = wait_warp(o_done(t, (step - 1) & 1), (step - 1) >> 1);
       if (!ok) break;
       asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
@@ -551,8 +594,8 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) dq4_kv8_prefill_kernel(con
       auto put_lse = [&](float ref, float sum) {
         if (real && p.lse) p.lse[at] = sum == 0.f ? -INFINITY : fmaf(ref, kLn2, logf(sum));
       };
-      const bool whole = sg.a == 0 && count == x.steps[t];
-      const int64_t slot_at = 2 * blockIdx.x + (sg.item0 - kOpening <= v0 ? 0 : 1);
+      const bool whole = was.a == 0 && count == was.x.steps[t];
+      const int64_t slot_at = 2 * blockIdx.x + (was.item0 - kOpening <= v0 ? 0 : 1);
       auto part_of = [&](int64_t s) { return w.part + (s * 2 + t) * (kDim / 4) * kTileRows + row; };
       auto stats_of = [&](int64_t s) { return w.stats + (s * 2 + t) * kTileRows + row; };
 #pragma unroll 1
@@ -581,7 +624,7 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) dq4_kv8_prefill_kernel(con
         continue;
       }
       *stats_of(slot_at) = make_float2(fresh ? -INFINITY : from, l);
-      const int c0 = cta_of(sg.item0), c1 = cta_of(sg.item0 + x.steps[t] - 1);
+      const int c0 = cta_of(was.item0), c1 = cta_of(was.item0 + was.x.steps[t] - 1);
       bar_tile(t);
       if (row == 0) {
         int* counter = w.count + 2 * c1 + t;
@@ -590,7 +633,7 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) dq4_kv8_prefill_kernel(con
       }
       bar_tile(t);
       if (!s_last[t]) continue;
-      const int64_t slot0 = 2 * c0 + (sg.item0 - kOpening <= begin_of(c0) ? 0 : 1);
+      const int64_t slot0 = 2 * c0 + (was.item0 - kOpening <= begin_of(c0) ? 0 : 1);
       auto slot_of = [&](int c) { return c == c0 ? slot0 : int64_t(2 * c); };
       float top = -INFINITY, sum = 0.f;
       for (int c = c0; c <= c1; ++c) top = fmaxf(top, __ldcg(stats_of(slot_of(c))).x);
@@ -671,23 +714,44 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) dq4_kv8_prefill_kernel(con
       }
       return s;
     };
-    uint4 raw[2][kPasses];
-    float gk, gv;
-    auto fetch = [&](const Step& s) {
+    const int lt = tid - kUnitRows;
+    int brought = 0, g = 0;  // steps asked for, and placed
+    auto note_at = [&](int step) {
+      return sbase + S::kNote + (step % kRawSlots * kGrans + (lane & (kGrans - 1))) * 16;
+    };
+    // Ask for a step's codes and scales; an empty group of copies past the last step.
+    auto fetch = [&](bool valid, const Step& s) {
+      if (valid) {
+        const uint32_t dst = sbase + S::kRaw + brought % kRawSlots * (2 * kKeys * kDim) + lt * 16;
 #pragma unroll
-      for (int i = 0; i < kPasses; ++i) {
-        const int row = row0 + i * kRowsPass, key = s.key + row;
-        int at = __shfl_sync(kAllLanes, s.block, row >> 4);
-        if (key >= s.held) at = -1;  // a slot never written: it may hold no number
-        const int64_t off =
-            int64_t(at) * page_bytes + ((key & (p.c.page - 1)) * kDim + col * 16);
+        for (int i = 0; i < kPasses; ++i) {
+          const int row = row0 + i * kRowsPass, key = s.key + row;
+          const int at = __shfl_sync(kAllLanes, s.block, row >> 4);
+          // a slot never written may hold no number: zeros
+          const int size = at >= 0 && key < s.held ? 16 : 0;
+          const int64_t off =
+              int64_t(at) * page_bytes + ((key & (p.c.page - 1)) * kDim + col * 16);
 #pragma unroll
-        for (int x = 0; x < 2; ++x)
-          raw[x][i] = at < 0 ? make_uint4(0, 0, 0, 0)
-                             : load_global(reinterpret_cast<const uint4*>(p.c.codes[x] + off));
+          for (int x = 0; x < 2; ++x) {
+            const void* src = size ? static_cast<const void*>(p.c.codes[x] + off) : w.units;
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;"
+                         :: "r"(dst + (x * kPasses + i) * S::kRawPass), "l"(src), "r"(size)
+                         : "memory");
+          }
+        }
+        if (lw == 0 && lane < kGrans) {
+          const uint32_t note = note_at(brought);
+          asm volatile("st.shared.b32 [%0], %1;" :: "r"(note), "r"(s.block) : "memory");
+          if (s.block >= 0) {
+#pragma unroll
+            for (int x = 0; x < 2; ++x)
+              asm volatile("cp.async.ca.shared.global [%0], [%1], 4;"
+                           :: "r"(note + 4 + 4 * x), "l"(p.c.scale[x] + s.block) : "memory");
+          }
+        }
+        ++brought;
       }
-      gk = s.block < 0 ? 0.f : load_global(p.c.scale[0] + s.block);
-      gv = s.block < 0 ? -1.f : load_global(p.c.scale[1] + s.block);
+      asm volatile("cp.async.commit_group;" ::: "memory");
     };
     auto put = [&](uint32_t at, const uint4& v) {
       sts_v4(at + to[0], f16_of_e4m3(v.x), f16_of_e4m3_high(v.x), f16_of_e4m3(v.y),
@@ -695,42 +759,48 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) dq4_kv8_prefill_kernel(con
       sts_v4(at + to[1], f16_of_e4m3(v.z), f16_of_e4m3_high(v.z), f16_of_e4m3(v.w),
              f16_of_e4m3_high(v.w));
     };
+    for (int i = 0; i < kRawSlots; ++i) {
+      const bool valid = more;
+      fetch(valid, find_step());
+    }
     bool have = more;
     Step s = find_step();
-    fetch(s);
-    bool have_next = more;
-    s = find_step();
-    for (int g = 0; have; ++g) {
-      const int slot = g % kSlots;
-      bool ok = g < kSlots || wait(k_empty(slot), g / kSlots - 1);
-      if (!__all_sync(kAllLanes, ok)) break;
+    for (; g < brought; ++g) {
+      const int slot = g % kSlots, phase = g / kSlots;
+      asm volatile("cp.async.wait_group %0;" :: "n"(kRawSlots - 1) : "memory");
+      const uint32_t from = sbase + S::kRaw + g % kRawSlots * (2 * kKeys * kDim) + lt * 16;
+      uint4 codes[2][kPasses];
+#pragma unroll
+      for (int x = 0; x < 2; ++x)
+#pragma unroll
+        for (int i = 0; i < kPasses; ++i)
+          codes[x][i] = lds_v4(from + (x * kPasses + i) * S::kRawPass);
+      if (phase > 0 && !wait_warp(k_empty(slot), phase - 1)) break;
 #pragma unroll
       for (int i = 0; i < kPasses; ++i)
-        put(sbase + S::kK + slot * S::kOperand + i * kRowsPass * 128, raw[0][i]);
+        put(sbase + S::kK + slot * S::kOperand + i * kRowsPass * 128, codes[0][i]);
       if (lw == 0 && lane < kGrans) {
         // keys that are not there: S = 0 and an exponent of -infinity
-        const float vs = used_scale(gv);
-        const bool none = gv == -1.f;
-        sts_v4(sbase + S::kGran + (g % kGranSlots * kGrans + lane) * 16, __float_as_uint(gk),
-               __float_as_uint(none ? -INFINITY : log2f(vs)), __float_as_uint(none ? 0.f : 1.f / vs),
-               0);
+        const uint4 note = lds_v4(note_at(g));
+        const float vs = used_scale(__uint_as_float(note.z));
+        const bool none = int(note.x) < 0;
+        sts_v4(sbase + S::kGran + (g % kGranSlots * kGrans + lane) * 16, none ? 0 : note.y,
+               __float_as_uint(none ? -INFINITY : __log2f(vs)),
+               __float_as_uint(none ? 0.f : __fdividef(1.f, vs)), 0);
       }
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       mbar_arrive(k_full(slot));
-      ok = g < kSlots || wait(v_empty(slot), g / kSlots - 1);
-      if (!__all_sync(kAllLanes, ok)) break;
+      if (phase > 0 && !wait_warp(v_empty(slot), phase - 1)) break;
 #pragma unroll
       for (int i = 0; i < kPasses; ++i)
-        put(sbase + S::kV + slot * S::kOperand + i * kRowsPass * 128, raw[1][i]);
+        put(sbase + S::kV + slot * S::kOperand + i * kRowsPass * 128, codes[1][i]);
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       mbar_arrive(v_full(slot));
-      have = have_next;
-      if (have) {
-        fetch(s);
-        have_next = more;
-        s = find_step();
-      }
+      fetch(have, s);
+      have = more;
+      s = find_step();
     }
+    asm volatile("cp.async.wait_all;" ::: "memory");
     if (p.bad && __any_sync(kAllLanes, met_bad) && lane == 0) atomicAdd(p.bad, 1);
   } else {
     // -------------------------------------------------------------- the products
