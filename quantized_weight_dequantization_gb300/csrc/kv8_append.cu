@@ -7,8 +7,10 @@
 // Scales are powers of two, so that a page that grows its scale loses nothing but what
 // falls below e4m3's smallest step: rounding does not pile up over a page's tokens.
 //
-// A CTA owns one page and head of K or of V, so nothing is shared between CTAs: it
-// reads its tokens once into registers (rotated in FP32), reduces max|x|, and writes codes.
+// A group of page * dim / 32 threads owns one page and head of K or of V, so nothing is shared
+// between groups: it reads its tokens once into registers (rotated in FP32), reduces max|x|,
+// and writes codes.  A CTA has the groups of a few heads of one page, so that finding the page
+// is paid for once.
 // Two bytes a value in, one out: bound by HBM for prompts, by the chain of dependent loads
 // (length, page id, scale; tokens) for single tokens.
 #include "kv8.cuh"
@@ -27,9 +29,11 @@ struct AppendArgs {
   int rotary;
   bool interleaved;
   int* bad;
+  int group;  // threads of a page and head
 };
 
-constexpr int kPasses = 4;  // 8-value groups of lanes a thread handles: page * dim / 32 threads
+constexpr int kPasses = 4;  // 8-value pieces a thread handles
+constexpr int kCtaThreads = 256;  // a CTA takes heads up to about as many threads
 
 __device__ __forceinline__ uint32_t e4m3x4(const F4& f) {
   uint16_t lo, hi;
@@ -68,9 +72,12 @@ __global__ void __launch_bounds__(1024) dq4_kv8_append_kernel(const AppendArgs p
   constexpr int kLanes = kDim / 8;
   __shared__ float s_max[32];
   wait_for_stream();
-  const int head = blockIdx.y, which = blockIdx.z;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int l = tid % kLanes, first = tid / kLanes, step = blockDim.x / kLanes;
+  const int which = blockIdx.z, lane = threadIdx.x & 31;
+  const int heads = blockDim.x / p.group;  // of this CTA
+  const int mine = threadIdx.x / p.group, tid = threadIdx.x - mine * p.group;
+  const bool real = blockIdx.y * heads + mine < p.c.heads;
+  const int head = min(blockIdx.y * heads + mine, p.c.heads - 1);
+  const int l = tid % kLanes, first = tid / kLanes, step = p.group / kLanes;
   const int page = p.c.page, log2_page = p.c.log2_page;
   // The sequence and the page within it.  Sequence b's pages start at unit
   // row / page + 2 b: n tokens touch at most n / page + 2 pages, and the units of the
@@ -88,7 +95,7 @@ __global__ void __launch_bounds__(1024) dq4_kv8_append_kernel(const AppendArgs p
   if (lo >= hi) return;
   const int id = j >= 0 && j < p.s.table_width ? load_global(p.s.table + b * p.s.table_stride + j) : -1;
   if (id < 0 || id >= p.c.pages) {
-    if (p.bad && tid == 0 && head == 0 && which == 0) atomicAdd(p.bad, hi - lo);
+    if (p.bad && threadIdx.x == 0 && blockIdx.y == 0 && which == 0) atomicAdd(p.bad, hi - lo);
     return;
   }
   const int64_t block = int64_t(id) * p.c.heads + head;
@@ -113,7 +120,7 @@ __global__ void __launch_bounds__(1024) dq4_kv8_append_kernel(const AppendArgs p
     c[i] = widen<DT>(load4<DT>(row + at.b));
     if (turning && pos >= p.table_rows) {
       a[i] = c[i] = F4{};
-      if (p.bad && l == 0 && head == 0) atomicAdd(p.bad, 1);
+      if (p.bad && l == 0 && head == 0 && real) atomicAdd(p.bad, 1);
     } else if (at.turned) {
       const int64_t row0 = int64_t(pos) * (p.rotary / 2) + 4 * l;
       turn(a[i], c[i], load_global(reinterpret_cast<const float4*>(p.cos + row0)),
@@ -128,9 +135,11 @@ __global__ void __launch_bounds__(1024) dq4_kv8_append_kernel(const AppendArgs p
   if (unordered) amax = __uint_as_float(0x7F800000u);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(kAllLanes, amax, o));
-  if (lane == 0) s_max[warp] = amax;
+  if (lane == 0) s_max[threadIdx.x >> 5] = amax;
   __syncthreads();  // also: every thread has read the old scale
-  amax = s_max[lane < int(blockDim.x >> 5) ? lane : 0];
+  if (!real) return;
+  const int warps = p.group >> 5;
+  amax = s_max[mine * warps + (lane < warps ? lane : 0)];
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(kAllLanes, amax, o));
 
@@ -157,7 +166,7 @@ __global__ void __launch_bounds__(1024) dq4_kv8_append_kernel(const AppendArgs p
     const float ratio = old / scale;
     const int words = (lo - (j << log2_page)) * (kDim / 16);
     uint4* at16 = reinterpret_cast<uint4*>(codes);
-    for (int i = tid; i < words; i += blockDim.x) {
+    for (int i = tid; i < words; i += p.group) {
       uint4 w = at16[i];
       w.x = rescale4(w.x, ratio);
       w.y = rescale4(w.y, ratio);
@@ -169,10 +178,13 @@ __global__ void __launch_bounds__(1024) dq4_kv8_append_kernel(const AppendArgs p
 }
 
 template <int DT, int kDim>
-int launch_append(const AppendArgs& p, int64_t units, cudaStream_t stream) {
+int launch_append(AppendArgs p, int64_t units, cudaStream_t stream) {
+  p.group = p.c.page * kDim / (8 * kPasses);  // 32 .. 1024
+  const int most = kCtaThreads / p.group > 1 ? kCtaThreads / p.group : 1;
+  const int heads = most < p.c.heads ? most : p.c.heads;
   return launch_ordered(dq4_kv8_append_kernel<DT, kDim>,
-                        dim3(unsigned(units), unsigned(p.c.heads), 2),
-                        p.c.page * kDim / (8 * kPasses), 0, stream, p);
+                        dim3(unsigned(units), unsigned((p.c.heads + heads - 1) / heads), 2),
+                        p.group * heads, 0, stream, p);
 }
 
 }  // namespace

@@ -12,8 +12,12 @@ namespace dq4d {
 namespace {
 
 constexpr int kNormThreads = 256;  // forward: 8 warps
-constexpr int kBwdThreads = 512;   // backward: 16 warps, each with weight-gradient sums
+constexpr int kBwdThreads = 256;   // backward: 8 warps, each with weight-gradient sums
+constexpr int kBwdCtas = 2;        // and CTAs per SM
+constexpr int kBwdRows = 4;        // and heads of a lane at a time
 constexpr int kMaxPartials = 512;  // CTAs that may leave weight-gradient partials
+constexpr int kPartGroup = 16;     // of them summed together first
+static_assert((1 + kMaxPartials / kPartGroup) * 4 <= 256, "counters at the workspace's head");
 constexpr int kMaxDim = 1024;
 constexpr int kAnyWarps = 4;       // warps per CTA of the any-size kernels
 
@@ -125,147 +129,185 @@ __global__ void __launch_bounds__(kNormThreads) dq4_qk_norm_kernel(const NormArg
   }
 }
 
-// Sum the CTAs' partial weight gradients, in CTA order within each of the thread groups
-// that share the columns and then in group order, by the last CTA to leave its own: the
-// order does not depend on which CTA that is.  `mine` is this CTA's [2][dim] in shared
-// memory, whose storage holds 2 x blockDim floats at least.
-__device__ void finish_weights(const NormArgs& p, float* mine) {
-  __shared__ bool last;
-  const int cols = 2 * p.dim;
-  float* part = p.part + int64_t(blockIdx.x) * cols;
-  for (int i = threadIdx.x; i < cols; i += blockDim.x) part[i] = mine[i];
-  __threadfence();
-  __syncthreads();
-  if (threadIdx.x == 0) last = atomicAdd(p.count, 1) == int(gridDim.x) - 1;
-  __syncthreads();
-  if (!last) return;
-  __threadfence();
-  const int groups = max(1, int(blockDim.x) / cols);
-  for (int i0 = 0; i0 < cols; i0 += blockDim.x) {
-    const int g = threadIdx.x / min(cols, int(blockDim.x));
-    const int i = i0 + threadIdx.x % min(cols, int(blockDim.x));
-    float s = 0.f;
-    if (i < cols && g < groups)
-      for (int c = g; c < int(gridDim.x); c += groups) s += __ldcg(p.part + int64_t(c) * cols + i);
-    __syncthreads();
-    mine[threadIdx.x] = s;
-    __syncthreads();
-    if (i < cols && g == 0) {
-      for (int o = 1; o < groups; ++o) s += mine[threadIdx.x + o * cols];
-      float* dw = p.dw[i >= p.dim];
-      if (dw) dw[i >= p.dim ? i - p.dim : i] = s;
-    }
+// Column i of the sum of the n rows of `cols` floats at src, in order, kAhead loads at a time.
+__device__ __forceinline__ float sum_rows(const float* src, int n, int cols) {
+  constexpr int kAhead = 16;
+  float s = 0.f;
+  for (int c0 = 0; c0 < n; c0 += kAhead) {
+    float v[kAhead];
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) v[k] = c0 + k < n ? __ldcg(src + int64_t(c0 + k) * cols) : 0.f;
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) s += v[k];
   }
-  if (threadIdx.x == 0) *p.count = 0;  // ready for the next call
+  return s;
 }
 
-// The backward pass in the forward kernel's layout.  A warp walks the units with a fixed
-// stride and keeps, in each lane, the sums of its eight columns of the weight gradients of
-// q and of k; lanes, warps and CTAs are then summed in a fixed order.
+// Sum the CTAs' partial weight gradients (`mine`, [2][dim]): the last CTA of each kPartGroup to
+// leave its own sums the group's, and the last group's the groups', always in CTA order.  (One
+// CTA summing all of them took 12 us for 304 partials.)
+__device__ void finish_weights(const NormArgs& p, const float* mine) {
+  __shared__ bool last;
+  const int cols = 2 * p.dim, group = blockIdx.x / kPartGroup;
+  const int groups = (gridDim.x + kPartGroup - 1) / kPartGroup;
+  const int members = min(kPartGroup, int(gridDim.x) - group * kPartGroup);
+  float* part = p.part + int64_t(blockIdx.x) * cols;
+  float* sums = p.part + int64_t(kMaxPartials) * cols;  // the groups'
+  for (int i = threadIdx.x; i < cols; i += blockDim.x) part[i] = mine[i];
+  for (int level = 0; level < 2; ++level) {
+    __threadfence();
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      int* count = p.count + (level == 0 ? 1 + group : 0);
+      last = atomicAdd(count, 1) == (level == 0 ? members : groups) - 1;
+      if (last) *count = 0;  // ready for the next call
+    }
+    __syncthreads();
+    if (!last) return;
+    __threadfence();
+    for (int i = threadIdx.x; i < cols; i += blockDim.x) {
+      if (level == 0) {
+        sums[int64_t(group) * cols + i] =
+            sum_rows(p.part + int64_t(group) * kPartGroup * cols + i, members, cols);
+      } else {
+        const float s = sum_rows(sums + i, groups, cols);
+        float* dw = p.dw[i >= p.dim];
+        if (dw) dw[i >= p.dim ? i - p.dim : i] = s;
+      }
+    }
+  }
+}
+
+// The backward pass in the forward kernel's layout: first all of q's units, then k's.  A warp
+// walks them with a fixed stride, all of a unit's loads on the way at once, and keeps, in each lane, the sums of its eight columns of the weight's gradient; lanes,
+// warps and CTAs are then summed in a fixed order.  With r the row's factor and m' = mean(g w x),
+//   dx = r g w - x r^3 m',   dw += r g x
+// so that both sums over a row, of x^2 and of g w x, go through the lanes together.
 template <int DT, int kDim, int kRows>
-__global__ void __launch_bounds__(kBwdThreads) dq4_qk_norm_backward_kernel(const NormArgs p) {
+__global__ void __launch_bounds__(kBwdThreads, kBwdCtas)
+    dq4_qk_norm_backward_kernel(const NormArgs p) {
   using T = typename Elem<DT>::T;
   constexpr int kLanes = kDim / 8, kGroups = 32 / kLanes, kWarps = kBwdThreads / 32;
   __shared__ float sums[kWarps * 2 * kDim];
   wait_for_stream();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int l = lane % kLanes, group = lane / kLanes;
-  const int per_token = p.chunks[0] + p.chunks[1];
-  const int64_t units = p.tokens * per_token;
   const LanePlace at = lane_place(l, p.cos ? p.rotary : 0, p.interleaved);
-  F4 dwa[2] = {}, dwb[2] = {};
-  for (int64_t unit = int64_t(blockIdx.x) * kWarps + warp; unit < units;
-       unit += int64_t(gridDim.x) * kWarps) {
-    const int64_t t = unit / per_token;
-    int c = int(unit - t * per_token);
-    const int which = c >= p.chunks[0];
-    if (which) c -= p.chunks[0];
-    const int h0 = c * (kRows * kGroups) + group;
-    const int heads = p.heads[which];
-    const T* x = static_cast<const T*>(p.x[which]) + t * p.token_stride[which];
-    const T* dy = static_cast<const T*>(p.dy[which]) + t * heads * kDim;
-    Raw4<DT> ra[kRows], rb[kRows], ga[kRows], gb[kRows];
-#pragma unroll
-    for (int i = 0; i < kRows; ++i) {
-      const int h = min(h0 + i * kGroups, heads - 1);
-      ra[i] = load4<DT>(x + h * p.head_stride[which] + at.a);
-      rb[i] = load4<DT>(x + h * p.head_stride[which] + at.b);
-      ga[i] = load4<DT>(dy + h * kDim + at.a);
-      gb[i] = load4<DT>(dy + h * kDim + at.b);
-    }
-    const bool normed = p.w[which] != nullptr;
-    F4 wa, wb;
-    if (normed) {
-      const T* w = static_cast<const T*>(p.w[which]);
-      wa = widen<DT>(load4<DT>(w + at.a));
-      wb = widen<DT>(load4<DT>(w + at.b));
-    }
-    const int64_t row = table_row(p, t);
-    float4 cs = {}, sn = {};
-    if (at.turned && row >= 0) {
-      cs = load_global(reinterpret_cast<const float4*>(p.cos + row * (p.rotary / 2) + 4 * l));
-      sn = load_global(reinterpret_cast<const float4*>(p.sin + row * (p.rotary / 2) + 4 * l));
-      sn = make_float4(-sn.x, -sn.y, -sn.z, -sn.w);
-    }
-    T* out = static_cast<T*>(p.out[which]) + t * heads * kDim;
-#pragma unroll
-    for (int i = 0; i < kRows; ++i) {
-      const int h = h0 + i * kGroups;
-      const bool real = h < heads && row >= 0;
-      F4 a = widen<DT>(ra[i]), b = widen<DT>(rb[i]);
-      F4 g = widen<DT>(ga[i]), k = widen<DT>(gb[i]);
-      if (at.turned) turn(g, k, cs, sn, p.interleaved);
+  const int64_t unit0 = int64_t(blockIdx.x) * kWarps + warp;
+  const int64_t stride = int64_t(gridDim.x) * kWarps;
+  const bool normed = p.w[0] != nullptr;
+  struct Rows {
+    Raw4<DT> xa[kRows], xb[kRows], ga[kRows], gb[kRows];
+  };
+#pragma unroll 1
+  for (int which = 0; which < 2; ++which) {
+    const int heads = p.heads[which], chunks = p.chunks[which];
+    F4 dwa = {}, dwb = {}, wa = {}, wb = {};
+    if (heads > 0) {
+      const T* x = static_cast<const T*>(p.x[which]);
+      const T* dy = static_cast<const T*>(p.dy[which]);
+      T* out = static_cast<T*>(p.out[which]);
+      const int64_t token_stride = p.token_stride[which], head_stride = p.head_stride[which];
       if (normed) {
-        float ss = 0.f;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) ss = fmaf(a.v[j], a.v[j], fmaf(b.v[j], b.v[j], ss));
-        const float r = rsqrtf(group_sum<kLanes>(ss) * (1.f / kDim) + p.eps);
-        float dot = 0.f;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          a.v[j] *= r;  // xh
-          b.v[j] *= r;
-          if (real) {
-            const float ca = g.v[j] * a.v[j], cb = k.v[j] * b.v[j];
-            dwa[0].v[j] += which ? 0.f : ca;
-            dwb[0].v[j] += which ? 0.f : cb;
-            dwa[1].v[j] += which ? ca : 0.f;
-            dwb[1].v[j] += which ? cb : 0.f;
-          }
-          g.v[j] *= wa.v[j];
-          k.v[j] *= wb.v[j];
-          dot = fmaf(g.v[j], a.v[j], fmaf(k.v[j], b.v[j], dot));
-        }
-        const float m = group_sum<kLanes>(dot) * (1.f / kDim);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          g.v[j] = r * fmaf(-a.v[j], m, g.v[j]);
-          k.v[j] = r * fmaf(-b.v[j], m, k.v[j]);
-        }
+        const T* w = static_cast<const T*>(p.w[which]);
+        wa = widen<DT>(load4<DT>(w + at.a));
+        wb = widen<DT>(load4<DT>(w + at.b));
       }
-      if (row < 0) g = k = F4{};
-      if (h < heads) {
-        store4<DT>(out + h * kDim + at.a, g);
-        store4<DT>(out + h * kDim + at.b, k);
-        if (row < 0 && l == 0 && p.bad) atomicAdd(p.bad, 1);
+      // a unit: head chunk c of token t
+      const int64_t t_step = stride / chunks;
+      const int c_step = int(stride - t_step * chunks);
+      auto load = [&](int64_t t, int c, Rows& r) {
+        if (t >= p.tokens) return;
+#pragma unroll
+        for (int i = 0; i < kRows; ++i) {
+          const int h = min((c * kRows + i) * kGroups + group, heads - 1);
+          const T* xr = x + t * token_stride + h * head_stride;
+          const T* gr = dy + (t * heads + h) * kDim;
+          r.xa[i] = load4<DT>(xr + at.a);
+          r.xb[i] = load4<DT>(xr + at.b);
+          r.ga[i] = load4<DT>(gr + at.a);
+          r.gb[i] = load4<DT>(gr + at.b);
+        }
+      };
+      int64_t t = unit0 / chunks;
+      int c = int(unit0 - t * chunks);
+      Rows now;
+      load(t, c, now);
+      while (t < p.tokens) {
+        const int64_t row = table_row(p, t);
+        int64_t t2 = t + t_step;
+        int c2 = c + c_step;
+        if (c2 >= chunks) {
+          c2 -= chunks;
+          ++t2;
+        }
+        float4 cs = {}, sn = {};
+        if (at.turned && row >= 0) {
+          cs = load_global(reinterpret_cast<const float4*>(p.cos + row * (p.rotary / 2) + 4 * l));
+          sn = load_global(reinterpret_cast<const float4*>(p.sin + row * (p.rotary / 2) + 4 * l));
+          sn = make_float4(-sn.x, -sn.y, -sn.z, -sn.w);
+        }
+#pragma unroll
+        for (int i = 0; i < kRows; ++i) {
+          const int h = (c * kRows + i) * kGroups + group;
+          F4 a = widen<DT>(now.xa[i]), b = widen<DT>(now.xb[i]);
+          F4 g = widen<DT>(now.ga[i]), k = widen<DT>(now.gb[i]);
+          if (at.turned) turn(g, k, cs, sn, p.interleaved);
+          if (row < 0) g = k = F4{};
+          if (normed) {
+            float ss = 0.f, dot = 0.f;
+            F4 ga, gb;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              ss = fmaf(a.v[j], a.v[j], fmaf(b.v[j], b.v[j], ss));
+              ga.v[j] = g.v[j] * a.v[j];
+              gb.v[j] = k.v[j] * b.v[j];
+              dot = fmaf(ga.v[j], wa.v[j], fmaf(gb.v[j], wb.v[j], dot));
+            }
+#pragma unroll
+            for (int o = kLanes / 2; o > 0; o >>= 1) {
+              ss += __shfl_xor_sync(kAllLanes, ss, o);
+              dot += __shfl_xor_sync(kAllLanes, dot, o);
+            }
+            const float r = rsqrtf(ss * (1.f / kDim) + p.eps);
+            const float m = -(dot * (1.f / kDim)) * r * r * r;
+            const float real = h < heads ? r : 0.f;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              dwa.v[j] = fmaf(ga.v[j], real, dwa.v[j]);
+              dwb.v[j] = fmaf(gb.v[j], real, dwb.v[j]);
+              g.v[j] = fmaf(g.v[j] * wa.v[j], r, a.v[j] * m);
+              k.v[j] = fmaf(k.v[j] * wb.v[j], r, b.v[j] * m);
+            }
+            if (row < 0) g = k = F4{};
+          }
+          if (h < heads) {
+            T* o = out + (t * heads + h) * kDim;
+            store4<DT>(o + at.a, g);
+            store4<DT>(o + at.b, k);
+            if (row < 0 && l == 0 && p.bad) atomicAdd(p.bad, 1);
+          }
+        }
+        t = t2;
+        c = c2;
+        load(t, c, now);
       }
     }
-  }
-  if (p.dw[0] == nullptr) return;
-#pragma unroll
-  for (int n = 0; n < 2; ++n)
+    if (p.dw[0] == nullptr) continue;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
 #pragma unroll
       for (int o = kLanes; o < 32; o <<= 1) {
-        dwa[n].v[j] += __shfl_xor_sync(kAllLanes, dwa[n].v[j], o);
-        dwb[n].v[j] += __shfl_xor_sync(kAllLanes, dwb[n].v[j], o);
+        dwa.v[j] += __shfl_xor_sync(kAllLanes, dwa.v[j], o);
+        dwb.v[j] += __shfl_xor_sync(kAllLanes, dwb.v[j], o);
       }
       if (group == 0) {
-        sums[(warp * 2 + n) * kDim + at.a + j] = dwa[n].v[j];
-        sums[(warp * 2 + n) * kDim + at.b + j] = dwb[n].v[j];
+        sums[(warp * 2 + which) * kDim + at.a + j] = dwa.v[j];
+        sums[(warp * 2 + which) * kDim + at.b + j] = dwb.v[j];
       }
     }
+  }
+  if (p.dw[0] == nullptr) return;
   __syncthreads();
   for (int i = threadIdx.x; i < 2 * kDim; i += kBwdThreads) {
     float s = sums[i];
@@ -426,13 +468,12 @@ int launch_forward(NormArgs p, int sms, cudaStream_t stream) {
 template <int DT, int kDim>
 int launch_backward(NormArgs p, int sms, cudaStream_t stream) {
   constexpr int kWarps = kBwdThreads / 32;
-  cut_heads(&p, 2);
+  cut_heads(&p, kBwdRows);
   const int64_t units = p.tokens * (p.chunks[0] + p.chunks[1]);
   const int64_t want = (units + kWarps - 1) / kWarps;
-  const int grid = int(want < 2 * sms ? want : 2 * sms);
-  return launch_ordered(dq4_qk_norm_backward_kernel<DT, kDim, 2>,
-                        dim3(unsigned(grid < kMaxPartials ? grid : kMaxPartials)), kBwdThreads, 0,
-                        stream, p);
+  const int most = kBwdCtas * sms < kMaxPartials ? kBwdCtas * sms : kMaxPartials;
+  return launch_ordered(dq4_qk_norm_backward_kernel<DT, kDim, kBwdRows>,
+                        dim3(unsigned(want < most ? want : most)), kBwdThreads, 0, stream, p);
 }
 
 template <int DT>
@@ -494,7 +535,7 @@ int dq4_qk_norm_rope(const void* q, int64_t q_token_stride, int64_t q_head_strid
 
 int64_t dq4_qk_norm_rope_backward_workspace_bytes(int32_t head_dim) {
   if (head_dim < 2 || head_dim > kMaxDim) return 0;
-  return 256 + int64_t(kMaxPartials) * 2 * head_dim * 4;
+  return 256 + int64_t(kMaxPartials + kMaxPartials / kPartGroup) * 2 * head_dim * 4;
 }
 
 int dq4_qk_norm_rope_backward(const void* dq_out, const void* dk_out, const void* q,
