@@ -72,6 +72,18 @@ __device__ __forceinline__ Raw4<DT> load4(const typename Elem<DT>::T* p) {
   return r;
 }
 
+// The same for what is read, or written, once: it leaves the caches first.
+template <int DT>
+__device__ __forceinline__ Raw4<DT> load4_once(const typename Elem<DT>::T* p) {
+  Raw4<DT> r;
+  if constexpr (DT == DQ4_OUT_F32) {
+    r.u = __ldcs(reinterpret_cast<const uint4*>(p));
+  } else {
+    r.u = __ldcs(reinterpret_cast<const uint2*>(p));
+  }
+  return r;
+}
+
 template <int DT>
 __device__ __forceinline__ F4 widen(const Raw4<DT>& r) {
   F4 f;
@@ -104,6 +116,16 @@ __device__ __forceinline__ void store4(typename Elem<DT>::T* p, const F4& f) {
   } else {
     *reinterpret_cast<uint2*>(p) =
         make_uint2(pack2<DT>(f.v[0], f.v[1]), pack2<DT>(f.v[2], f.v[3]));
+  }
+}
+
+template <int DT>
+__device__ __forceinline__ void store4_once(typename Elem<DT>::T* p, const F4& f) {
+  if constexpr (DT == DQ4_OUT_F32) {
+    __stcs(reinterpret_cast<float4*>(p), make_float4(f.v[0], f.v[1], f.v[2], f.v[3]));
+  } else {
+    __stcs(reinterpret_cast<uint2*>(p),
+           make_uint2(pack2<DT>(f.v[0], f.v[1]), pack2<DT>(f.v[2], f.v[3])));
   }
 }
 

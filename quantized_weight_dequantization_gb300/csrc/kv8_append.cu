@@ -93,7 +93,22 @@ __global__ void __launch_bounds__(1024) dq4_kv8_append_kernel(const AppendArgs p
   const int j = (begin >> log2_page) + int(blockIdx.x - u0);  // the page within the sequence
   const int lo = max(begin, j << log2_page), hi = min(q.len, (j + 1) << log2_page);
   if (lo >= hi) return;
-  const int id = j >= 0 && j < p.s.table_width ? load_global(p.s.table + b * p.s.table_stride + j) : -1;
+  // (the page id is on its way while the tokens are read)
+  const int id = j >= 0 && j < p.s.table_width
+                     ? load_global(p.s.table + b * p.s.table_stride + j) : -1;
+
+  const bool turning = which == 0 && p.cos != nullptr;
+  const LanePlace at = lane_place(l, turning ? p.rotary : 0, p.interleaved);
+  const T* x = static_cast<const T*>(p.x[which]) + head * p.head_stride[which];
+  Raw4<DT> ra[kPasses], rb[kPasses];
+#pragma unroll
+  for (int i = 0; i < kPasses; ++i) {
+    const int pos = (j << log2_page) + first + i * step;
+    if (pos < lo || pos >= hi) continue;
+    const T* row = x + (q.row + (pos - begin)) * p.token_stride[which];
+    ra[i] = load4_once<DT>(row + at.a);
+    rb[i] = load4_once<DT>(row + at.b);
+  }
   if (id < 0 || id >= p.c.pages) {
     if (p.bad && threadIdx.x == 0 && blockIdx.y == 0 && which == 0) atomicAdd(p.bad, hi - lo);
     return;
@@ -104,9 +119,6 @@ __global__ void __launch_bounds__(1024) dq4_kv8_append_kernel(const AppendArgs p
   const bool earlier = lo > (j << log2_page);
   const float old = earlier ? *scale_at : 0.f;
 
-  const bool turning = which == 0 && p.cos != nullptr;
-  const LanePlace at = lane_place(l, turning ? p.rotary : 0, p.interleaved);
-  const T* x = static_cast<const T*>(p.x[which]) + head * p.head_stride[which];
   F4 a[kPasses], c[kPasses];
   float amax = 0.f;
   bool unordered = false;
@@ -115,9 +127,8 @@ __global__ void __launch_bounds__(1024) dq4_kv8_append_kernel(const AppendArgs p
     const int pos = (j << log2_page) + first + i * step;
     a[i] = c[i] = F4{};
     if (pos < lo || pos >= hi) continue;
-    const T* row = x + (q.row + (pos - begin)) * p.token_stride[which];
-    a[i] = widen<DT>(load4<DT>(row + at.a));
-    c[i] = widen<DT>(load4<DT>(row + at.b));
+    a[i] = widen<DT>(ra[i]);
+    c[i] = widen<DT>(rb[i]);
     if (turning && pos >= p.table_rows) {
       a[i] = c[i] = F4{};
       if (p.bad && l == 0 && head == 0 && real) atomicAdd(p.bad, 1);

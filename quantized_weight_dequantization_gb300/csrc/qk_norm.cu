@@ -87,8 +87,8 @@ __global__ void __launch_bounds__(kNormThreads) dq4_qk_norm_kernel(const NormArg
   for (int i = 0; i < kRows; ++i) {
     const int h = min(h0 + i * kGroups, heads - 1);
     const T* row = x + h * p.head_stride[which];
-    ra[i] = load4<DT>(row + at.a);
-    rb[i] = load4<DT>(row + at.b);
+    ra[i] = load4_once<DT>(row + at.a);
+    rb[i] = load4_once<DT>(row + at.b);
   }
   const bool normed = p.w[which] != nullptr;
   F4 wa, wb;
@@ -223,10 +223,10 @@ __global__ void __launch_bounds__(kBwdThreads, kBwdCtas)
           const int h = min((c * kRows + i) * kGroups + group, heads - 1);
           const T* xr = x + t * token_stride + h * head_stride;
           const T* gr = dy + (t * heads + h) * kDim;
-          r.xa[i] = load4<DT>(xr + at.a);
-          r.xb[i] = load4<DT>(xr + at.b);
-          r.ga[i] = load4<DT>(gr + at.a);
-          r.gb[i] = load4<DT>(gr + at.b);
+          r.xa[i] = load4_once<DT>(xr + at.a);
+          r.xb[i] = load4_once<DT>(xr + at.b);
+          r.ga[i] = load4_once<DT>(gr + at.a);
+          r.gb[i] = load4_once<DT>(gr + at.b);
         }
       };
       int64_t t = unit0 / chunks;
@@ -283,8 +283,8 @@ __global__ void __launch_bounds__(kBwdThreads, kBwdCtas)
           }
           if (h < heads) {
             T* o = out + (t * heads + h) * kDim;
-            store4<DT>(o + at.a, g);
-            store4<DT>(o + at.b, k);
+            store4_once<DT>(o + at.a, g);
+            store4_once<DT>(o + at.b, k);
             if (row < 0 && l == 0 && p.bad) atomicAdd(p.bad, 1);
           }
         }
