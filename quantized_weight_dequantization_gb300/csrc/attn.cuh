@@ -223,6 +223,19 @@ int launch_ordered(void (*kernel)(KArgs...), dim3 grid, int threads, size_t smem
   return DQ4_OK;
 }
 
+// Let `kernel` have `bytes` of dynamic shared memory, once for each device (bit dev of
+// *allowed; devices past 63 every time).
+template <typename Kernel>
+int allow_smem(Kernel kernel, int bytes, int dev, std::atomic<uint64_t>* allowed) {
+  const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
+  if (allowed->load(std::memory_order_relaxed) & bit) return DQ4_OK;
+  const cudaError_t e =
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e != cudaSuccess) return fail_cuda(DQ4_ERR_LAUNCH, e);
+  allowed->fetch_or(bit, std::memory_order_relaxed);
+  return DQ4_OK;
+}
+
 inline bool valid_dtype(int32_t dtype, bool with_f32) {
   return dtype == DQ4_OUT_F16 || dtype == DQ4_OUT_BF16 || (with_f32 && dtype == DQ4_OUT_F32);
 }

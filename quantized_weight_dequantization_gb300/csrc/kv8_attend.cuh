@@ -110,10 +110,10 @@ __device__ __forceinline__ uint32_t f16_of_e4m3_high(uint32_t w) {
 }  // namespace
 
 // The two kernels (kv8_decode.cu, kv8_prefill.cu).
-int launch_decode(const AttendArgs& p, int head_dim, int rows, int sms, void* workspace,
+int launch_decode(const AttendArgs& p, int head_dim, int rows, int dev, int sms, void* workspace,
                   cudaStream_t stream);
 int64_t decode_workspace_bytes();
-int launch_prefill(const AttendArgs& p, int head_dim, int sms, void* workspace,
+int launch_prefill(const AttendArgs& p, int head_dim, int dev, int sms, void* workspace,
                    cudaStream_t stream);
 int64_t prefill_workspace_bytes(int64_t tokens, int64_t seqs, int64_t group, int head_dim);
 

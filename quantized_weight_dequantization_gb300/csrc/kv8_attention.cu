@@ -63,8 +63,8 @@ int dq4_kv8_attention(const dq4_kv8_cache* cache, const void* q, int64_t q_token
   if (const int st = current_device(&dev, &sms)) return st;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   const int64_t rows = int64_t(max_new) * p.group;
-  if (rows <= kFewRows) return launch_decode(p, cache->head_dim, int(rows), sms, workspace, s);
-  return launch_prefill(p, cache->head_dim, sms, workspace, s);
+  if (rows <= kFewRows) return launch_decode(p, cache->head_dim, int(rows), dev, sms, workspace, s);
+  return launch_prefill(p, cache->head_dim, dev, sms, workspace, s);
 }
 
 }  // extern "C"

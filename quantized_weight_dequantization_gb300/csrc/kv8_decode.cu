@@ -4,7 +4,7 @@
 // The call's work is cut into units of 64 keys of one item (a sequence, a kv head and up to
 // 8 NT query rows of it: new tokens x heads of the group).  One CTA runs per SM, on an equal
 // run of the units whatever the lengths are, and each of its 8 warps on an eighth of that
-// run.  Items that fall to one warp alone are written by it; for the others each warp leaves
+// run (for few short items, a CTA on one item).  Items that fall to one warp alone are written by it; for the others each warp leaves
 // FP32 parts (at most two: of its first and of its last item), which the CTA joins once, at
 // its end, and the last CTA of an item joins across CTAs.  Parts are always summed in the
 // order of their keys, so results do not depend on timing.
@@ -36,6 +36,7 @@ constexpr int kGrans = kTile / 16; // granules of 16 keys, never of two pages
 constexpr int kMaxCtas = 160;      // CTAs the workspace has room for
 constexpr int kMaxRows = 16;       // query rows of an item: 8 NT
 constexpr int kOpening = 1;        // what starting and ending an item costs, in units
+constexpr int kItemUnits = 24;     // units of an item that a CTA takes alone
 constexpr int kSegs = 8;           // items, or parts of them, that a warp plans at a time
 constexpr int kBatch = 32 / kGrans;  // units whose pages are read ahead together
 // parts: two for each warp, and two for each CTA
@@ -230,7 +231,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
   constexpr int kWordsV = kDim / 32;    // and of a value
   constexpr int kCols = kDim / 32;      // columns a lane takes where parts are joined
   extern __shared__ uint8_t smem_raw[];
-  __shared__ int64_t s_sums[kWarps], s_before;
+  __shared__ int64_t s_sums[kWarps], s_before, s_run[2];
   __shared__ int s_b0;
   __shared__ bool s_last[2];
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -264,25 +265,52 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
   for (int64_t b = tid; b - tid < seqs; b += kDecodeThreads)
     units += block_scan(b == tid ? mine : units_of(b), s_sums, before);
   if (units == 0) return;
-  const int64_t ctas = min(int64_t(gridDim.x), units);
-  if (blockIdx.x >= ctas) return;
-  auto begin_of = [&](int64_t cta) { return divide(cta * units, ctas); };
-  auto cta_of = [&](int64_t u) { return int(divide((u + 1) * ctas - 1, units)); };
-  const int64_t u0 = begin_of(blockIdx.x), u1 = begin_of(blockIdx.x + 1);
-  int64_t passed = 0;
-  for (int64_t b = tid; b - tid < seqs; b += kDecodeThreads) {
-    const int64_t v = b == tid ? mine : units_of(b);
-    int64_t total = units;
-    if (seqs > kDecodeThreads) total = block_scan(v, s_sums, before);
-    const int64_t at = passed + before;
-    if (at <= u0 && u0 < at + v) {
-      s_b0 = int(b);
-      s_before = at;
+  // With no more items than CTAs, and few units in each, a CTA takes one item: one more unit
+  // for its warps is sooner done than a join of several CTAs' parts.
+  if (seqs <= kDecodeThreads) {
+    SeqWork w = {};
+    if (tid < seqs) w = seq_work(p, seq_at(p.s, tid), kRows);
+    int64_t first;
+    const int64_t items = block_scan(w.items, s_sums, first);
+    const bool each = items <= gridDim.x;
+    if (!__syncthreads_or(w.items > 0 && w.tiles > kItemUnits) && each) {
+      if (blockIdx.x >= items) return;
+      if (first <= blockIdx.x && blockIdx.x < first + w.items) {
+        s_b0 = tid;
+        s_before = before;
+        s_run[0] = before + (blockIdx.x - first) * (w.tiles + kOpening);
+        s_run[1] = s_run[0] + w.tiles + kOpening;
+      }
+    } else if (tid == 0) {
+      s_run[1] = -1;
     }
-    passed += total;
-    if (passed > u0) break;  // the same for every thread
+  } else if (tid == 0) {
+    s_run[1] = -1;
   }
   __syncthreads();
+  const int64_t ctas = min(int64_t(gridDim.x), units);
+  auto begin_of = [&](int64_t cta) { return divide(cta * units, ctas); };
+  auto cta_of = [&](int64_t u) { return int(divide((u + 1) * ctas - 1, units)); };
+  int64_t u0 = s_run[0], u1 = s_run[1];
+  if (u1 < 0) {
+    if (blockIdx.x >= ctas) return;
+    u0 = begin_of(blockIdx.x);
+    u1 = begin_of(blockIdx.x + 1);
+    int64_t passed = 0;
+    for (int64_t b = tid; b - tid < seqs; b += kDecodeThreads) {
+      const int64_t v = b == tid ? mine : units_of(b);
+      int64_t total = units;
+      if (seqs > kDecodeThreads) total = block_scan(v, s_sums, before);
+      const int64_t at = passed + before;
+      if (at <= u0 && u0 < at + v) {
+        s_b0 = int(b);
+        s_before = at;
+      }
+      passed += total;
+      if (passed > u0) break;  // the same for every thread
+    }
+    __syncthreads();
+  }
   const int64_t v0 = u0 + (u1 - u0) * warp / kWarps, v1 = u0 + (u1 - u0) * (warp + 1) / kWarps;
 
   // ---- state of the segment a warp is in
@@ -831,15 +859,14 @@ int make_map(CUtensorMap* map, const Kv8& c, int which, int dim, void* any) {
 }
 
 template <int kDim, int NT>
-int launch_one(const AttendArgs& p, int sms, cudaStream_t stream) {
+int launch_one(const AttendArgs& p, int dev, int sms, cudaStream_t stream) {
   constexpr int kBytes = DecodeSmem<kDim>::kBytes;
   CUtensorMap k, v;
   if (const int st = make_map(&k, p.c, 0, kDim, p.count)) return st;
   if (const int st = make_map(&v, p.c, 1, kDim, p.count)) return st;
   auto kernel = dq4_kv8_decode_kernel<kDim, NT>;
-  const cudaError_t e =
-      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes);
-  if (e != cudaSuccess) return fail_cuda(DQ4_ERR_LAUNCH, e);
+  static std::atomic<uint64_t> allowed{0};
+  if (const int st = allow_smem(kernel, kBytes, dev, &allowed)) return st;
   return launch_ordered(kernel, dim3(unsigned(sms < kMaxCtas ? sms : kMaxCtas)), kDecodeThreads,
                         kBytes, stream, k, v, p);
 }
@@ -852,15 +879,15 @@ int64_t decode_workspace_bytes() {
   return kCounterBytes + int64_t(kParts) * kMaxRows * (8 + 128 * 4);
 }
 
-int launch_decode(const AttendArgs& args, int head_dim, int rows, int sms, void* workspace,
-                  cudaStream_t stream) {
+int launch_decode(const AttendArgs& args, int head_dim, int rows, int dev, int sms,
+                  void* workspace, cudaStream_t stream) {
   AttendArgs p = args;
   p.count = static_cast<int*>(workspace);
   p.stats = reinterpret_cast<float2*>(static_cast<char*>(workspace) + kCounterBytes);
   p.part = reinterpret_cast<float*>(p.stats + int64_t(kParts) * kMaxRows);
   if (head_dim == 64)
-    return rows <= 8 ? launch_one<64, 1>(p, sms, stream) : launch_one<64, 2>(p, sms, stream);
-  return rows <= 8 ? launch_one<128, 1>(p, sms, stream) : launch_one<128, 2>(p, sms, stream);
+    return rows <= 8 ? launch_one<64, 1>(p, dev, sms, stream) : launch_one<64, 2>(p, dev, sms, stream);
+  return rows <= 8 ? launch_one<128, 1>(p, dev, sms, stream) : launch_one<128, 2>(p, dev, sms, stream);
 }
 
 }  // namespace dq4d

@@ -877,14 +877,13 @@ int64_t max_units(int64_t tokens, int64_t seqs, int64_t group) {
 int64_t plan_bytes(int64_t units) { return 64 + (units + 1) * int64_t(sizeof(Unit)); }
 
 template <int kDim>
-int launch_one(const PrefillArgs& w, int sms, cudaStream_t stream) {
+int launch_one(const PrefillArgs& w, int dev, int sms, cudaStream_t stream) {
   // more than half an SM's shared memory: one CTA per SM, as it takes all of TMEM
   constexpr int kBytes =
       PrefillSmem<kDim>::kBytes > 117 * 1024 ? PrefillSmem<kDim>::kBytes : 117 * 1024;
   auto kernel = dq4_kv8_prefill_kernel<kDim>;
-  const cudaError_t e =
-      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes);
-  if (e != cudaSuccess) return fail_cuda(DQ4_ERR_LAUNCH, e);
+  static std::atomic<uint64_t> allowed{0};
+  if (const int st = allow_smem(kernel, kBytes, dev, &allowed)) return st;
   if (const int st = launch_ordered(dq4_kv8_plan_kernel, dim3(1), kPlanThreads, 0, stream, w))
     return st;
   return launch_ordered(kernel, dim3(unsigned(sms < kMaxCtas ? sms : kMaxCtas)), kPrefillThreads,
@@ -898,7 +897,7 @@ int64_t prefill_workspace_bytes(int64_t tokens, int64_t seqs, int64_t group, int
          plan_bytes(max_units(tokens, seqs, group)) + 256;
 }
 
-int launch_prefill(const AttendArgs& p, int head_dim, int sms, void* workspace,
+int launch_prefill(const AttendArgs& p, int head_dim, int dev, int sms, void* workspace,
                    cudaStream_t stream) {
   PrefillArgs w = {};
   w.a = p;
@@ -912,7 +911,7 @@ int launch_prefill(const AttendArgs& p, int head_dim, int sms, void* workspace,
   at += int64_t(kMaxCtas) * 4 * kTileRows * head_dim * 4;
   w.total = reinterpret_cast<int64_t*>(at);
   w.units = reinterpret_cast<Unit*>(at + 64);
-  return head_dim == 64 ? launch_one<64>(w, sms, stream) : launch_one<128>(w, sms, stream);
+  return head_dim == 64 ? launch_one<64>(w, dev, sms, stream) : launch_one<128>(w, dev, sms, stream);
 }
 
 }  // namespace dq4d
