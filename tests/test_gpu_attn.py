@@ -581,3 +581,12 @@ def test_binding_refusals(dq):
     with pytest.raises(ValueError, match="CUDA tensor"):
         dq.qk_norm_rope(x.cpu(), None, None, None)
     torch.cuda.synchronize()
+
+
+def test_example_layer(dq):
+    """The example's layer, with 4-bit projections around these operators.  A value of the cache
+    is off by half a step of e4m3 at most, 2^-4 of it and 2^-5.8 in the mean square; outputs add
+    many of them, so that their difference stays below the largest of one."""
+    from examples import attention_layer
+
+    assert max(attention_layer.main(steps=2, prompts=(200, 3, 64))) < 2.0 ** -4
