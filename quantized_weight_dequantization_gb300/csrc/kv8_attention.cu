@@ -5,9 +5,19 @@
 namespace dq4d {
 namespace {
 
-// Query rows of a kv head (new tokens of a sequence x heads of the group) up to which a call
-// goes to the kernel that reads each key once for few rows.
-constexpr int kFewRows = 64;
+// Whether a call goes to the kernel for many query rows a kv head.  The one for few reads a
+// unit of 64 keys in about a third of the time that the other takes for its 256 rows, but once
+// for each 16 rows; the other starts about 15 us later (two launches, longer units).  With
+// `keys` the most that a sequence can hold or see, both measured at 8 kv heads of 128, in us:
+//   rows   1 x 1000   1 x 20000   8 x 2000   8 x 10000   32 x 1000   32 x 5000   (seqs x keys)
+//     32    15 / 30     34 / 60    31 / 41    117 / 95     52 / 59    225 / 169  (few / many)
+//     64    15 / 31     51 / 62    47 / 41    201 / 98     84 / 62    316 / 172
+//    128    15 / 32     88 / 63    81 / 44    361 / 102   146 / 66    758 / 185
+//    512    32 / 40    305 / 84   258 / 71   1198 / 207   539 / 148  2340 / 398
+bool many_rows(int64_t rows, int64_t seqs, int64_t kv_heads, int64_t keys) {
+  const int64_t units = seqs * kv_heads * ((keys + 63) / 64), tiles = (rows + 15) / 16;
+  return tiles > 2 && (tiles - 2) * units > 6000;
+}
 
 }  // namespace
 }  // namespace dq4d
@@ -63,8 +73,12 @@ int dq4_kv8_attention(const dq4_kv8_cache* cache, const void* q, int64_t q_token
   if (const int st = current_device(&dev, &sms)) return st;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   const int64_t rows = int64_t(max_new) * p.group;
-  if (rows <= kFewRows) return launch_decode(p, cache->head_dim, int(rows), dev, sms, workspace, s);
-  return launch_prefill(p, cache->head_dim, dev, sms, workspace, s);
+  int64_t keys = int64_t(table_width) * cache->page;
+  if (window > 0 && keys > int64_t(window) + max_new) keys = int64_t(window) + max_new;
+  if (many_rows(rows, seqs, cache->kv_heads, keys))
+    return launch_prefill(p, cache->head_dim, dev, sms, workspace, s);
+  return launch_decode(p, cache->head_dim, int(rows < 65536 ? rows : 65536), dev, sms, workspace,
+                       s);
 }
 
 }  // extern "C"

@@ -331,8 +331,13 @@ def test_append_counts_tokens_without_a_place(dq):
 
 
 # ------------------------------------------------------------------------ attention
+MANY = 1 << 20  # as max_new: the kernel for many rows, whatever the sizes; 1: the one for few
+
+
 def check_attend(dq, b, new, heads, dtype, causal=True, window=0, scale=None, max_new=None,
                  use_cu=True, q_scale=1.0, strided=False, lens=None, stream=None):
+    """Both kernels, and the one that the call would choose, against the definition; returns the
+    outputs."""
     lens = b.lens if lens is None else lens
     cu = np.concatenate([[0], np.cumsum(new)]).astype(np.int32)
     x = b.rng.standard_normal((int(cu[-1]), heads, b.dim)).astype(np.float32) * q_scale
@@ -340,23 +345,26 @@ def check_attend(dq, b, new, heads, dtype, causal=True, window=0, scale=None, ma
     if strided:
         q = torch.cat([q, q[:, :1], q[:, :1]], 1)[:, :heads]
     scale = b.dim ** -0.5 if scale is None else scale
-    bad = torch.zeros(1, dtype=torch.int32, device="cuda")
-    out, lse = dq.kv8_attention(b.cache, q, dev(b.table), dev(np.array(lens, np.int32)),
-                                dev(cu) if use_cu else None, max_new, scale, causal, window,
-                                return_lse=True, bad=bad, stream=stream)
-    if stream is not None:
-        stream.synchronize()
     want, want_lse, size, reach = oracle_attn.attend(
         host(q), b.codes[0], b.codes[1], b.scales[0], b.scales[1], b.table, lens, cu, scale,
         causal, window)
     if dtype == "f16":  # past the type's range an output is infinite
         want = np.where(np.abs(want) < 65520, want, np.copysign(np.inf, want))
     delta = 2.0 ** -18 * reach
-    close(host(out), want, (2.0 ** -10 + 2 * delta[..., None]) * size + U[dtype] * np.abs(want)
-          + TINY[dtype], "out")
-    close(lse.cpu().numpy(), want_lse, delta + 2.0 ** -18, "lse")
-    assert int(bad.item()) == 0
-    return out
+    outs = []
+    for hint in (max_new, 1, MANY):
+        bad = torch.zeros(1, dtype=torch.int32, device="cuda")
+        out, lse = dq.kv8_attention(b.cache, q, dev(b.table), dev(np.array(lens, np.int32)),
+                                    dev(cu) if use_cu else None, hint, scale, causal, window,
+                                    return_lse=True, bad=bad, stream=stream)
+        if stream is not None:
+            stream.synchronize()
+        close(host(out), want, (2.0 ** -10 + 2 * delta[..., None]) * size
+              + U[dtype] * np.abs(want) + TINY[dtype], ("out", hint))
+        close(lse.cpu().numpy(), want_lse, delta + 2.0 ** -18, ("lse", hint))
+        assert int(bad.item()) == 0
+        outs.append(out)
+    return outs
 
 
 LENS = [1, 0, 15, 16, 31, 33, 64, 65, 127, 300, 2]
@@ -441,7 +449,8 @@ def test_attend_on_another_stream_repeats_bit_for_bit(dq, new):
         runs.append(check_attend(dq, b, [new] * 3, 8, "bf16", stream=stream))
     torch.cuda.synchronize()
     for r in runs[1:]:
-        assert torch.equal(r, runs[0])
+        for x, y in zip(r, runs[0]):
+            assert torch.equal(x, y)
 
 
 @pytest.mark.parametrize("new", [1, 60])
@@ -451,7 +460,8 @@ def test_attend_page_that_holds_no_number_reaches_only_rows_that_see_it(dq, new)
     b.cache.v_scale[int(b.table[0, 5]), 1] = float("nan")  # keys 80 .. 95 of sequence 0
     q = dev(b.rng.standard_normal((2 * new, 4, 64)).astype(np.float32), torch.bfloat16)
     cu = dev(np.array([0, new, 2 * new], np.int32))
-    out = dq.kv8_attention(b.cache, q, dev(b.table), dev(np.array([96, 96], np.int32)), cu)
+    out = dq.kv8_attention(b.cache, q, dev(b.table), dev(np.array([96, 96], np.int32)), cu,
+                           1 if new == 1 else MANY)
     seen = torch.arange(2 * new, device="cuda") < new
     seen &= torch.arange(2 * new, device="cuda") + 96 - new >= 80
     broken = out.isnan().any(-1)
@@ -466,17 +476,19 @@ def test_attend_pages_that_do_not_exist_are_not_seen_and_counted(dq, new):
     q = dev(b.rng.standard_normal((new, 2, 64)).astype(np.float32), torch.bfloat16)
     cu = dev(np.array([0, new], np.int32))
     bad = torch.zeros(1, dtype=torch.int32, device="cuda")
-    want, lse = dq.kv8_attention(b.cache, q, dev(b.table), lens, cu, return_lse=True, bad=bad)
+    hint = 1 if new == 1 else MANY
+    want, lse = dq.kv8_attention(b.cache, q, dev(b.table), lens, cu, hint, return_lse=True,
+                                 bad=bad)
     assert int(bad.item()) == 0
     for hole in (-1, b.pages, 1 << 30):
         t = b.table.copy()
         t[0, 2] = hole
-        got, lse2 = dq.kv8_attention(b.cache, q, dev(t), lens, cu, return_lse=True, bad=bad)
+        got, lse2 = dq.kv8_attention(b.cache, q, dev(t), lens, cu, hint, return_lse=True, bad=bad)
         assert int(bad.item()) > 0
         bad.zero_()
         assert torch.isfinite(got.float()).all() and (lse2 < lse).all()
     # a table narrower than the sequence
-    got, lse2 = dq.kv8_attention(b.cache, q, dev(b.table[:, :4]), lens, cu, return_lse=True,
+    got, lse2 = dq.kv8_attention(b.cache, q, dev(b.table[:, :4]), lens, cu, hint, return_lse=True,
                                  bad=bad)
     assert int(bad.item()) > 0 and torch.isfinite(got.float()).all() and (lse2 < lse).all()
 
@@ -496,7 +508,7 @@ def test_cache_past_4_gib(dq):
     small = dq.KV8Cache.empty(6, kv, page, dim)
     near = np.array([[5, 3, 4], [2, 1, 0]], np.int32)
     dq.kv8_append(small, x[0], x[1], dev(near), dev(lens), dev(cu))
-    for q, c, n in ((x[2], dev(cu), 150), (x[2][[149, 219]], None, 1)):
+    for q, c, n in ((x[2], dev(cu), MANY), (x[2], dev(cu), 1), (x[2][[149, 219]], None, 1)):
         a = dq.kv8_attention(cache, q, dev(table), dev(lens), c, n)
         b = dq.kv8_attention(small, q, dev(near), dev(lens), c, n)
         assert torch.isfinite(a.float()).all() and torch.equal(a, b)
