@@ -64,17 +64,22 @@ def _lib() -> ctypes.CDLL:
 # A call of few tokens is bound by the host, so the checks below first take the short way that a
 # valid argument passes, and look for what is wrong only if it does not.
 _WORKSPACES = {}
+_OUTGROWN = []  # captured graphs may still use them
 
 
 def _workspace(workspace, need: int, what: str, like: torch.Tensor, handle) -> torch.Tensor:
     """The caller's workspace, or the cached zero-filled one of (operator, device, stream), grown
-    to `need` bytes."""
+    to `need` bytes, and to twice its size at least, so that all outgrown ones together stay
+    below the one in use."""
     if workspace is not None:
         _check(workspace, "workspace", torch.uint8, need, like.device)
         return workspace
     key = (what, like.get_device(), handle)
     ws = _WORKSPACES.get(key)
     if ws is None or ws.numel() < need:
+        if ws is not None:
+            _OUTGROWN.append(ws)
+            need = max(need, 2 * ws.numel())
         ws = torch.zeros(max(need, 1), dtype=torch.uint8, device=like.device)
         torch.cuda.synchronize(like.device)  # zero-filled before any stream uses it
         _WORKSPACES[key] = ws

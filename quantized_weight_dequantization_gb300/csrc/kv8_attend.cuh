@@ -20,8 +20,8 @@ struct AttendArgs {
   void* out;
   float* lse;
   int* bad;
-  int* count;        // decode: arrivals at a shared item
-  float* part;       // decode: unnormalized rows of parts of items,
+  int* count;        // few rows: arrivals at a shared item
+  float* part;       // few rows: unnormalized rows of parts of items,
   float2* stats;     // and their {m, l}
 };
 
@@ -79,8 +79,7 @@ __device__ __forceinline__ void widen2(uint32_t u, bool bf16, float& a, float& b
 // A row with an infinity or a NaN gets a NaN inverse.
 __device__ __forceinline__ void row_scaling(float top, float& up, float& down) {
   const int e = int(__float_as_uint(top) >> 23);  // biased; 0 also for subnormal rows
-  // exponents -14 .. of 127 - (14 - (e - 127)) kept normal: e in [1, 254] gives up in
-  // [2^-113, 2^126] after the clamp
+  // 2^k and 2^-k both normal: only rows whose largest is below 2^-112 miss the range
   const int k = min(max(14 - (e - 127), -126), 126);
   up = __uint_as_float(uint32_t(k + 127) << 23);
   down = __uint_as_float(uint32_t(127 - k) << 23);
@@ -110,8 +109,9 @@ __device__ __forceinline__ uint32_t f16_of_e4m3_high(uint32_t w) {
 }  // namespace
 
 // The two kernels (kv8_decode.cu, kv8_prefill.cu).
-int launch_decode(const AttendArgs& p, int head_dim, int rows, int dev, int sms, void* workspace,
-                  cudaStream_t stream);
+// rows: query rows a kv head; keys: the most that a sequence holds or sees (estimates, both)
+int launch_decode(const AttendArgs& p, int head_dim, int64_t rows, int64_t keys, int dev, int sms,
+                  void* workspace, cudaStream_t stream);
 int64_t decode_workspace_bytes();
 int launch_prefill(const AttendArgs& p, int head_dim, int dev, int sms, void* workspace,
                    cudaStream_t stream);

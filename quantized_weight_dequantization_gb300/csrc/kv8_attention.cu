@@ -5,17 +5,19 @@
 namespace dq4d {
 namespace {
 
-// Whether a call goes to the kernel for many query rows a kv head.  The one for few reads a
-// unit of 64 keys in about a third of the time that the other takes for its 256 rows, but once
-// for each 16 rows; the other starts about 15 us later (two launches, longer units).  With
-// `keys` the most that a sequence can hold or see, both measured at 8 kv heads of 128, in us:
+// Whether a call goes to the kernel for many query rows a kv head.  The one for few takes
+// about a third of the time for a unit of 64 keys that the other takes for its 256 rows, but
+// once for each 8 or 16 rows; the other starts about 15 us later (two launches, longer units).
+// With `keys` the most that a sequence can hold or see, both measured at 8 kv heads of 128, in
+// us (few / many):
 //   rows   1 x 1000   1 x 20000   8 x 2000   8 x 10000   32 x 1000   32 x 5000   (seqs x keys)
-//     32    15 / 30     34 / 60    31 / 41    117 / 95     52 / 59    225 / 169  (few / many)
-//     64    15 / 31     51 / 62    47 / 41    201 / 98     84 / 62    316 / 172
-//    128    15 / 32     88 / 63    81 / 44    361 / 102   146 / 66    758 / 185
-//    512    32 / 40    305 / 84   258 / 71   1198 / 207   539 / 148  2340 / 398
+//     32    15 / 31     34 / 73    26 / 41     78 / 95     49 / 59    135 / 169
+//     64    15 / 32     46 / 71    43 / 42    130 / 98     79 / 62    243 / 172
+//    128    15 / 33     70 / 63    68 / 44    232 / 103   133 / 65    444 / 184
+//    512    33 / 40    221 / 89   206 / 71    832 / 204   449 / 146  1680 / 398
 bool many_rows(int64_t rows, int64_t seqs, int64_t kv_heads, int64_t keys) {
-  const int64_t units = seqs * kv_heads * ((keys + 63) / 64), tiles = (rows + 15) / 16;
+  const double units = double(seqs * kv_heads) * double((keys + 63) / 64);  // may be huge
+  const double tiles = double((rows + 15) / 16);
   return tiles > 2 && (tiles - 2) * units > 6000;
 }
 
@@ -77,8 +79,7 @@ int dq4_kv8_attention(const dq4_kv8_cache* cache, const void* q, int64_t q_token
   if (window > 0 && keys > int64_t(window) + max_new) keys = int64_t(window) + max_new;
   if (many_rows(rows, seqs, cache->kv_heads, keys))
     return launch_prefill(p, cache->head_dim, dev, sms, workspace, s);
-  return launch_decode(p, cache->head_dim, int(rows < 65536 ? rows : 65536), dev, sms, workspace,
-                       s);
+  return launch_decode(p, cache->head_dim, rows, keys, dev, sms, workspace, s);
 }
 
 }  // extern "C"

@@ -36,7 +36,7 @@ constexpr int kGrans = kTile / 16; // granules of 16 keys, never of two pages
 constexpr int kMaxCtas = 160;      // CTAs the workspace has room for
 constexpr int kMaxRows = 16;       // query rows of an item: 8 NT
 constexpr int kOpening = 1;        // what starting and ending an item costs, in units
-constexpr int kItemUnits = 24;     // units of an item that a CTA takes alone
+constexpr int kItemUnits = 18;     // units of an item that a CTA takes alone (see `each`)
 constexpr int kSegs = 8;           // items, or parts of them, that a warp plans at a time
 constexpr int kBatch = 32 / kGrans;  // units whose pages are read ahead together
 // parts: two for each warp, and two for each CTA
@@ -265,15 +265,21 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
   for (int64_t b = tid; b - tid < seqs; b += kDecodeThreads)
     units += block_scan(b == tid ? mine : units_of(b), s_sums, before);
   if (units == 0) return;
-  // With no more items than CTAs, and few units in each, a CTA takes one item: one more unit
-  // for its warps is sooner done than a join of several CTAs' parts.
+  // With no more items than CTAs, a CTA takes one item each, if none is longer than an equal
+  // share of the units by more than kItemUnits: a unit takes a CTA 0.26 us, and a join of
+  // several CTAs' parts about 5 us.  Equal shares / an item each, in us, 8 kv heads of 128:
+  //   keys of a sequence   256         1024        1536        2048        3000
+  //    1 sequence          12.6 / 9.8  14.4 / 13.8 15.5 / 16.0 15.6 / 18.2 15.6 / 21.3
+  //    8                   13.5 / 9.7  14.7 / 14.3 16.8 / 16.5 17.3 / 18.7 19.9 / 21.6
+  //   18                   14.3 / 9.9  18.4 / 14.6 19.6 / 16.8 21.5 / 19.0 28.0 / 24.1
   if (seqs <= kDecodeThreads) {
     SeqWork w = {};
     if (tid < seqs) w = seq_work(p, seq_at(p.s, tid), kRows);
     int64_t first;
     const int64_t items = block_scan(w.items, s_sums, first);
     const bool each = items <= gridDim.x;
-    if (!__syncthreads_or(w.items > 0 && w.tiles > kItemUnits) && each) {
+    const bool longer = w.items > 0 && int64_t(w.tiles - kItemUnits) * gridDim.x > units;
+    if (!__syncthreads_or(longer) && each) {
       if (blockIdx.x >= items) return;
       if (first <= blockIdx.x && blockIdx.x < first + w.items) {
         s_b0 = tid;
@@ -871,6 +877,23 @@ int launch_one(const AttendArgs& p, int dev, int sms, cudaStream_t stream) {
                         kBytes, stream, k, v, p);
 }
 
+// Query rows of an item, 8 or 16, for calls with more than 8 a kv head.  A unit takes a CTA
+// 0.26 us with 8 rows and 0.47 with 16, but 8 read each key twice as often.  While the keys
+// stay in L2 that is for nothing; past half of its 129 MB (other data passes through it, too)
+// 16 rows are taken, and also where they make the items few enough for a CTA each.  8 / 16, in
+// us, 8 kv heads of 128 (64):
+//   seqs x keys   1 x 2000                   4 x 8000                   64 x 1000                  64 x 4000
+//    16 rows     14.5 / 18.3 (13.2 / 16.5)  28.6 / 31.4 (24.3 / 25.3)  53.7 / 56.9 (42.3 / 38.9)  186 / 114 (111 / 85)
+//    24          15.6 / 17.2 (14.3 / 15.2)  36.4 / 38.6 (29.8 / 31.0)  72.0 / 78.6 (55.9 / 55.6)
+// and with a CTA each, 16 rows, 16 x 2000 keys: 29.7 / 25.6 (25.0 / 20.2).
+bool wide_items(const AttendArgs& p, int64_t rows, int64_t keys, int dim, int sms) {
+  const double blocks = double(p.s.seqs * p.c.heads);  // (double: estimates may be huge)
+  const double narrow = double((rows + 7) / 8), wide = double((rows + 15) / 16);
+  if (rows <= 8) return false;
+  if (blocks * wide <= sms && sms < blocks * narrow) return true;
+  return blocks * double(keys) * (2 * dim) > 64.5e6;
+}
+
 }  // namespace
 
 static_assert(kMaxCtas * 4 <= kCounterBytes, "a counter for each CTA");
@@ -879,15 +902,16 @@ int64_t decode_workspace_bytes() {
   return kCounterBytes + int64_t(kParts) * kMaxRows * (8 + 128 * 4);
 }
 
-int launch_decode(const AttendArgs& args, int head_dim, int rows, int dev, int sms,
-                  void* workspace, cudaStream_t stream) {
+int launch_decode(const AttendArgs& args, int head_dim, int64_t rows, int64_t keys, int dev,
+                  int sms, void* workspace, cudaStream_t stream) {
   AttendArgs p = args;
   p.count = static_cast<int*>(workspace);
   p.stats = reinterpret_cast<float2*>(static_cast<char*>(workspace) + kCounterBytes);
   p.part = reinterpret_cast<float*>(p.stats + int64_t(kParts) * kMaxRows);
+  const bool wide = wide_items(p, rows, keys, head_dim, sms);
   if (head_dim == 64)
-    return rows <= 8 ? launch_one<64, 1>(p, dev, sms, stream) : launch_one<64, 2>(p, dev, sms, stream);
-  return rows <= 8 ? launch_one<128, 1>(p, dev, sms, stream) : launch_one<128, 2>(p, dev, sms, stream);
+    return wide ? launch_one<64, 2>(p, dev, sms, stream) : launch_one<64, 1>(p, dev, sms, stream);
+  return wide ? launch_one<128, 2>(p, dev, sms, stream) : launch_one<128, 1>(p, dev, sms, stream);
 }
 
 }  // namespace dq4d

@@ -61,9 +61,11 @@ __device__ __forceinline__ float group_sum(float v) {
 // A warp takes a unit: kRows heads of one token for each of its 32 / kLanes groups of
 // kLanes = kDim / 8 lanes, all of q or all of k.  The position's cosines and sines and the
 // weights stay in registers over the unit, and all its loads are issued before the first
-// use.  kRows = 4 once that still gives every SM its 64 warps; with fewer units
-// one row a lane leaves more warps, and the latency of one row, to each SM (kRows = 4
-// against 1: see the launch).
+// use.  kRows = 4 once that gives every SM 16 warps; with fewer units one row a lane leaves
+// more warps, and the latency of one row, to each SM.  kRows = 1 / 4, in us, BF16:
+//   tokens            64         256        512        1024       2048        8192
+//   40 heads of 128   2.0 / 2.6  2.8 / 3.0  4.1 / 3.6  6.7 / 5.1  12.2 / 8.1  52.4 / 32.1
+//   20 heads of 64    1.8 / 2.4  2.0 / 2.5  2.1 / 2.5  2.8 / 3.0   4.1 / 4.2  12.2 / 11.1
 template <int DT, int kDim, int kRows>
 __global__ void __launch_bounds__(kNormThreads) dq4_qk_norm_kernel(const NormArgs p) {
   using T = typename Elem<DT>::T;
@@ -457,7 +459,7 @@ template <int DT, int kDim>
 int launch_forward(NormArgs p, int sms, cudaStream_t stream) {
   constexpr int kWarps = kNormThreads / 32;
   cut_heads(&p, 4);
-  const bool four = p.tokens * (p.chunks[0] + p.chunks[1]) >= int64_t(sms) * 64;
+  const bool four = p.tokens * (p.chunks[0] + p.chunks[1]) >= int64_t(sms) * 16;
   if (!four) cut_heads(&p, 1);
   const int64_t grid = (p.tokens * (p.chunks[0] + p.chunks[1]) + kWarps - 1) / kWarps;
   if (grid > kMaxGrid) return DQ4_ERR_N;

@@ -435,6 +435,49 @@ def test_attend_scales_that_are_not_powers_of_two(dq, new):
     check_attend(dq, b, [new, new], 8, "bf16")
 
 
+@pytest.mark.parametrize("new", [1, 60])
+def test_attend_pages_of_zeros_keep_their_weight(dq, new):
+    """Values appended as zeros stand at the least scale; their keys count all the same."""
+    b = Batch(dq, [210, 70], 2, 128, 16, seed=14)
+    b.fill()
+    for at in b.table[0, 2:9]:
+        b.codes[1][at] = np.where(np.isnan(b.codes[1][at]), np.nan, 0.0)
+        b.scales[1][at] = 2.0 ** -100
+    b.cache.v.copy_(dev(b.codes[1].astype(np.float32)).to(torch.float8_e4m3fn))
+    b.cache.v_scale.copy_(dev(b.scales[1]))
+    check_attend(dq, b, [new, new], 4, "bf16")
+    check_attend(dq, b, [new, new], 4, "bf16", window=100)
+
+
+@pytest.mark.parametrize("new", [1, 40])
+def test_attend_captured_graph_outlives_a_larger_call(dq, new):
+    """A larger call grows the stream's workspace; a graph captured before keeps its own."""
+    b = Batch(dq, [700, 90], 2, 128, 64, seed=15)
+    b.fill()
+    q = dev(b.rng.standard_normal((2 * new, 4, 128)).astype(np.float32), torch.bfloat16)
+    table, lens = dev(b.table), dev(np.array(b.lens, np.int32))
+    cu = dev(np.array([0, new, 2 * new], np.int32))
+    hint = 1 if new == 1 else MANY
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        want = dq.kv8_attention(b.cache, q, table, lens, cu, hint)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=side):
+            out = dq.kv8_attention(b.cache, q, table, lens, cu, hint)
+        many = torch.zeros(100000, 4, 128, dtype=torch.bfloat16, device="cuda")
+        far = dev(np.array([0, 99990, 100000], np.int32))
+        dq.kv8_attention(b.cache, many, table, lens, far, MANY)
+        torch.cuda.synchronize()
+        spoil = [torch.full((20 << 20,), 0x7F, dtype=torch.uint8, device="cuda")
+                 for _ in range(4)]  # what was given back would be taken by these
+        graph.replay()
+        torch.cuda.synchronize()
+    assert torch.equal(out, want)
+    assert all(bool((x == 0x7F).all()) for x in spoil)
+
+
 @pytest.mark.parametrize("new", [1, 5, 70])
 def test_attend_on_another_stream_repeats_bit_for_bit(dq, new):
     b = Batch(dq, [3000, 90, 1500], 2, 128, 64, seed=8)
