@@ -142,13 +142,17 @@ int dq4_kv8_append(const dq4_kv8_cache* cache, const void* k, int64_t k_token_st
  *   out             contiguous tokens x heads x head_dim of `dtype`, 16-byte aligned
  *   lse             optional FP32 tokens x heads (NULL to skip)
  *   max_new         the most new tokens of any sequence, or an estimate: it chooses the
- *                   kernel, and the result does not depend on it
+ *                   kernel, and what the result means does not depend on it (its rounding
+ *                   does)
  *   workspace       device memory, 256-byte aligned, of at least
  *                   dq4_kv8_attention_workspace_bytes bytes, zero-filled before its first
  *                   use; a completed call leaves it ready for later calls of any shape
  *                   that it is large enough for, in the same stream (not for concurrent
  *                   calls).
- * The result does not depend on the order in which the SMs work.  Keys past the table's
+ * The result does not depend on the order in which the SMs work.  A key counts with its weight
+ * times its page's V scale down to 2^-120 of the row's largest such product; below that it
+ * counts as nothing, in lse too (V scales of one sequence would have to lie 2^100 apart).
+ * pages * kv_heads: at most 2^31 - 1.  Keys past the table's
  * table_width pages, and pages with an id outside [0, pages), are not seen; bad is
  * incremented for each part of the work that met one, and for a wait that ran out (never
  * expected; the workspace must then be zero-filled again).

@@ -1,7 +1,9 @@
-// Shared pieces of the attention-side kernels (dq4_attn.h): typed 4-value groups, the
-// rotation of a lane's eight values, the search of a sequence by its first unit of work,
+// Shared pieces of the attention-side kernels (dq4_attn.h): typed groups of values, the
+// rotation of a lane's two groups, the search of a sequence by its first unit of work,
 // and the launch with programmatic stream serialization.
 #pragma once
+
+#include <type_traits>
 
 #include "common.cuh"
 #include "dq4_attn.h"
@@ -25,11 +27,7 @@ __device__ __forceinline__ T load_global(const T* p) {
   return *p;
 }
 
-// ------------------------------------------------------------ groups of four values
-struct F4 {
-  float v[4];
-};
-
+// ------------------------------------------------------------------ element types
 template <int DT>
 struct Elem;
 template <>
@@ -51,130 +49,148 @@ struct Elem<DQ4_OUT_F32> {
   static __device__ __forceinline__ T make(float f) { return f; }
 };
 
-// Raw bits of four consecutive values: 8 bytes (16-bit types) or 16 (FP32).
-template <int DT>
-struct Raw4 {
-  uint2 u;
-};
-template <>
-struct Raw4<DQ4_OUT_F32> {
-  uint4 u;
+// ----------------------------------------------------------------- groups of values
+// Raw bits of a group of V consecutive values: 8 or 16 bytes.
+template <int DT, int V>
+struct Raw {
+  static constexpr int kBytes = V * int(sizeof(typename Elem<DT>::T));
+  static_assert(kBytes == 8 || kBytes == 16, "one load");
+  std::conditional_t<kBytes == 8, uint2, uint4> u;
 };
 
-template <int DT>
-__device__ __forceinline__ Raw4<DT> load4(const typename Elem<DT>::T* p) {
-  Raw4<DT> r;
-  if constexpr (DT == DQ4_OUT_F32) {
-    r.u = load_global(reinterpret_cast<const uint4*>(p));
-  } else {
-    r.u = load_global(reinterpret_cast<const uint2*>(p));
-  }
-  return r;
+template <int DT, int V>
+__device__ __forceinline__ Raw<DT, V> load_group(const typename Elem<DT>::T* p) {
+  return {load_global(reinterpret_cast<const decltype(Raw<DT, V>::u)*>(p))};
 }
 
 // The same for what is read, or written, once: it leaves the caches first.
-template <int DT>
-__device__ __forceinline__ Raw4<DT> load4_once(const typename Elem<DT>::T* p) {
-  Raw4<DT> r;
-  if constexpr (DT == DQ4_OUT_F32) {
-    r.u = __ldcs(reinterpret_cast<const uint4*>(p));
-  } else {
-    r.u = __ldcs(reinterpret_cast<const uint2*>(p));
-  }
-  return r;
+template <int DT, int V>
+__device__ __forceinline__ Raw<DT, V> load_group_once(const typename Elem<DT>::T* p) {
+  return {__ldcs(reinterpret_cast<const decltype(Raw<DT, V>::u)*>(p))};
 }
 
-template <int DT>
-__device__ __forceinline__ F4 widen(const Raw4<DT>& r) {
-  F4 f;
-  if constexpr (DT == DQ4_OUT_F32) {
-    f.v[0] = __uint_as_float(r.u.x);
-    f.v[1] = __uint_as_float(r.u.y);
-    f.v[2] = __uint_as_float(r.u.z);
-    f.v[3] = __uint_as_float(r.u.w);
-  } else if constexpr (DT == DQ4_OUT_BF16) {
-    f.v[0] = __uint_as_float(r.u.x << 16);
-    f.v[1] = __uint_as_float(r.u.x & 0xFFFF0000u);
-    f.v[2] = __uint_as_float(r.u.y << 16);
-    f.v[3] = __uint_as_float(r.u.y & 0xFFFF0000u);
-  } else {
-    __half2 a, b;
-    memcpy(&a, &r.u.x, 4);
-    memcpy(&b, &r.u.y, 4);
-    f.v[0] = __low2float(a);
-    f.v[1] = __high2float(a);
-    f.v[2] = __low2float(b);
-    f.v[3] = __high2float(b);
+// A lane's two groups in FP32: values 0 .. V - 1 are group a of lane_place, the others b.
+template <int V>
+struct Vals {
+  float v[2 * V];
+};
+
+template <int DT, int V>
+__device__ __forceinline__ Vals<V> widen(const Raw<DT, V>& ra, const Raw<DT, V>& rb) {
+  Vals<V> f;
+#pragma unroll
+  for (int half = 0; half < 2; ++half) {
+    uint32_t w[Raw<DT, V>::kBytes / 4];
+    memcpy(w, half ? &rb.u : &ra.u, sizeof(w));
+    float* to = f.v + half * V;
+#pragma unroll
+    for (int i = 0; i < V; i += 2) {
+      if constexpr (DT == DQ4_OUT_F32) {
+        to[i] = __uint_as_float(w[i]);
+        to[i + 1] = __uint_as_float(w[i + 1]);
+      } else if constexpr (DT == DQ4_OUT_BF16) {
+        to[i] = __uint_as_float(w[i / 2] << 16);
+        to[i + 1] = __uint_as_float(w[i / 2] & 0xFFFF0000u);
+      } else {
+        __half2 h;
+        memcpy(&h, &w[i / 2], 4);
+        to[i] = __low2float(h);
+        to[i + 1] = __high2float(h);
+      }
+    }
   }
   return f;
 }
 
-template <int DT>
-__device__ __forceinline__ void store4(typename Elem<DT>::T* p, const F4& f) {
-  if constexpr (DT == DQ4_OUT_F32) {
-    *reinterpret_cast<float4*>(p) = make_float4(f.v[0], f.v[1], f.v[2], f.v[3]);
-  } else {
-    *reinterpret_cast<uint2*>(p) =
-        make_uint2(pack2<DT>(f.v[0], f.v[1]), pack2<DT>(f.v[2], f.v[3]));
+// Group a (half 0) or b of a lane's values, in the element type.
+template <int DT, int V>
+__device__ __forceinline__ Raw<DT, V> narrow(const Vals<V>& x, int half) {
+  uint32_t w[Raw<DT, V>::kBytes / 4];
+  const float* from = x.v + half * V;
+#pragma unroll
+  for (int i = 0; i < V; i += 2) {
+    if constexpr (DT == DQ4_OUT_F32) {
+      w[i] = __float_as_uint(from[i]);
+      w[i + 1] = __float_as_uint(from[i + 1]);
+    } else {
+      w[i / 2] = pack2<DT>(from[i], from[i + 1]);
+    }
   }
+  Raw<DT, V> r;
+  memcpy(&r.u, w, sizeof(w));
+  return r;
 }
 
-template <int DT>
-__device__ __forceinline__ void store4_once(typename Elem<DT>::T* p, const F4& f) {
-  if constexpr (DT == DQ4_OUT_F32) {
-    __stcs(reinterpret_cast<float4*>(p), make_float4(f.v[0], f.v[1], f.v[2], f.v[3]));
-  } else {
-    __stcs(reinterpret_cast<uint2*>(p),
-           make_uint2(pack2<DT>(f.v[0], f.v[1]), pack2<DT>(f.v[2], f.v[3])));
-  }
+template <int DT, int V>
+__device__ __forceinline__ void store_group(typename Elem<DT>::T* p, const Raw<DT, V>& r) {
+  *reinterpret_cast<decltype(Raw<DT, V>::u)*>(p) = r.u;
+}
+template <int DT, int V>
+__device__ __forceinline__ void store_group_once(typename Elem<DT>::T* p, const Raw<DT, V>& r) {
+  __stcs(reinterpret_cast<decltype(Raw<DT, V>::u)*>(p), r.u);
 }
 
 // ------------------------------------------------------------------- the rotation
-// A head of kDim values is held by kDim / 8 lanes, eight values each: two groups of four,
-// at values 4 a and 4 b, so chosen that both values of every rotated pair sit in one lane
-// and no lane needs another's.  Half-split pairs (i, i + rotary / 2): lane l < rotary / 8
-// takes groups l and l + rotary / 8, the others two neighbouring groups past rotary.
-// Neighbours paired: groups 2 l and 2 l + 1.  Either way lane l turns with the table
-// entries 4 l .. 4 l + 3 of its position's row.
+// A head of kDim values is held by kDim / 2 V lanes, two groups of V values each, so chosen
+// that both values of every rotated pair sit in one lane and no lane needs another's.
+// Half-split pairs (i, i + rotary / 2): lane l < rotary / 2 V takes groups l and
+// l + rotary / 2 V, the others two neighbouring groups past rotary.  Neighbours paired: groups
+// 2 l and 2 l + 1.  Either way lane l turns with the table entries V l .. V l + V - 1 of its
+// position's row.  rotary is a multiple of 2 V.
 struct LanePlace {
   int a, b;     // first values of the two groups
   bool turned;  // whether the lane's values are rotated
 };
 
+template <int V>
 __device__ __forceinline__ LanePlace lane_place(int l, int rotary, bool interleaved) {
   LanePlace p;
-  p.turned = 8 * l < rotary;
+  p.turned = 2 * V * l < rotary;
   if (interleaved || !p.turned) {
-    p.a = 8 * l;
-    p.b = 8 * l + 4;
+    p.a = 2 * V * l;
+    p.b = 2 * V * l + V;
   } else {
-    p.a = 4 * l;
-    p.b = 4 * l + rotary / 2;
+    p.a = V * l;
+    p.b = V * l + rotary / 2;
   }
   return p;
 }
 
-// (x, y) -> (x c - y s, y c + x s), every product and sum rounded on its own
-__device__ __forceinline__ void turn_pair(float& x, float& y, float c, float s) {
-  const float xc = __fmul_rn(x, c), ys = __fmul_rn(y, s);
-  const float yc = __fmul_rn(y, c), xs = __fmul_rn(x, s);
-  x = __fsub_rn(xc, ys);
-  y = __fadd_rn(yc, xs);
+// A lane's V entries of a row of a table.
+template <int V>
+__device__ __forceinline__ void load_entries(const float* p, float (&x)[V]) {
+#pragma unroll
+  for (int i = 0; i < V; i += 4) {
+    const float4 f = load_global(reinterpret_cast<const float4*>(p + i));
+    x[i] = f.x;
+    x[i + 1] = f.y;
+    x[i + 2] = f.z;
+    x[i + 3] = f.w;
+  }
 }
 
-__device__ __forceinline__ void turn(F4& a, F4& b, const float4& c, const float4& s,
-                                     bool interleaved) {
-  if (interleaved) {
-    turn_pair(a.v[0], a.v[1], c.x, s.x);
-    turn_pair(a.v[2], a.v[3], c.y, s.y);
-    turn_pair(b.v[0], b.v[1], c.z, s.z);
-    turn_pair(b.v[2], b.v[3], c.w, s.w);
-  } else {
-    turn_pair(a.v[0], b.v[0], c.x, s.x);
-    turn_pair(a.v[1], b.v[1], c.y, s.y);
-    turn_pair(a.v[2], b.v[2], c.z, s.z);
-    turn_pair(a.v[3], b.v[3], c.w, s.w);
+// Value i of a lane turns with its partner y by entry turn_entry of the lane's cosines and sines:
+// x c - y s, or x c + y s if turn_adds (the second of a pair).
+template <bool kInterleaved, int V>
+__device__ __forceinline__ constexpr int partner(int i) { return kInterleaved ? i ^ 1 : i ^ V; }
+template <bool kInterleaved, int V>
+__device__ __forceinline__ constexpr int turn_entry(int i) { return kInterleaved ? i / 2 : i % V; }
+template <bool kInterleaved, int V>
+__device__ __forceinline__ constexpr bool turn_adds(int i) { return kInterleaved ? i & 1 : i >= V; }
+
+// A lane's values turned (kBack: turned back), every product and sum rounded on its own.
+template <bool kInterleaved, bool kBack, int V>
+__device__ __forceinline__ Vals<V> turned(const Vals<V>& x, const float (&c)[V],
+                                          const float (&s)[V]) {
+  Vals<V> r;
+#pragma unroll
+  for (int i = 0; i < 2 * V; ++i) {
+    const int e = turn_entry<kInterleaved, V>(i);
+    const float xc = __fmul_rn(x.v[i], c[e]);
+    const float ys = __fmul_rn(x.v[partner<kInterleaved, V>(i)], s[e]);
+    r.v[i] = turn_adds<kInterleaved, V>(i) != kBack ? __fadd_rn(xc, ys) : __fsub_rn(xc, ys);
   }
+  return r;
 }
 
 // --------------------------------------------------------------- ragged sequences

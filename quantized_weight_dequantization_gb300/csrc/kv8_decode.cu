@@ -4,10 +4,10 @@
 // The call's work is cut into units of 64 keys of one item (a sequence, a kv head and up to
 // 8 NT query rows of it: new tokens x heads of the group).  One CTA runs per SM, on an equal
 // run of the units whatever the lengths are, and each of its 8 warps on an eighth of that
-// run (for few short items, a CTA on one item).  Items that fall to one warp alone are written by it; for the others each warp leaves
-// FP32 parts (at most two: of its first and of its last item), which the CTA joins once, at
-// its end, and the last CTA of an item joins across CTAs.  Parts are always summed in the
-// order of their keys, so results do not depend on timing.
+// run (for few short items, a CTA on one item).  Items that fall to one warp alone are written
+// by it; for the others each warp leaves FP32 parts (at most two: of its first and of its last
+// item), which the CTA joins once, at its end, and the last CTA of an item joins across CTAs.
+// Parts are always summed in the order of their keys, so results do not depend on timing.
 //
 // A warp has a ring of shared-memory slots of its own, each 64 keys or 64 values of one
 // head, filled by TMA (swizzled); lane 0 issues, all lanes consume, and a slot is refilled as
@@ -24,6 +24,12 @@
 // leave the N side of 8 to the few query rows.  The order of dim inside K Q^T, and of dim
 // inside O^T, is free: a lane takes 16 or 32 consecutive bytes of a key for the first product
 // and dim / 8 of a value for the second, so shared memory is read in 16-byte words.
+//
+// Measured (kv heads of 128): 64 sequences of 100 .. 8192 keys, 4 rows a head, 101 us (541 MB,
+// 5.3 TB/s; the loop itself runs at 7, the rest is the start, the joins and SMs that end 20 us
+// apart on equal work); 2 sequences of up to 131071 keys, 8 rows, 85 us (465 MB, 5.4 TB/s).
+// Short calls are a chain of latencies: one sequence of 777 keys takes 12 us, 2 of them to find
+// the work, 2 to the first keys, 4 in the loop and the rest in the joins and the launch.
 #include "kv8_attend.cuh"
 
 namespace dq4d {
@@ -882,9 +888,11 @@ int launch_one(const AttendArgs& p, int dev, int sms, cudaStream_t stream) {
 // stay in L2 that is for nothing; past half of its 129 MB (other data passes through it, too)
 // 16 rows are taken, and also where they make the items few enough for a CTA each.  8 / 16, in
 // us, 8 kv heads of 128 (64):
-//   seqs x keys   1 x 2000                   4 x 8000                   64 x 1000                  64 x 4000
-//    16 rows     14.5 / 18.3 (13.2 / 16.5)  28.6 / 31.4 (24.3 / 25.3)  53.7 / 56.9 (42.3 / 38.9)  186 / 114 (111 / 85)
-//    24          15.6 / 17.2 (14.3 / 15.2)  36.4 / 38.6 (29.8 / 31.0)  72.0 / 78.6 (55.9 / 55.6)
+//   seqs x keys   16 rows                    24 rows
+//    1 x 2000     14.5 / 18.3 (13.2 / 16.5)  15.6 / 17.2 (14.3 / 15.2)
+//    4 x 8000     28.6 / 31.4 (24.3 / 25.3)  36.4 / 38.6 (29.8 / 31.0)
+//   64 x 1000     53.7 / 56.9 (42.3 / 38.9)  72.0 / 78.6 (55.9 / 55.6)
+//   64 x 4000      186 / 114  (111 / 85)
 // and with a CTA each, 16 rows, 16 x 2000 keys: 29.7 / 25.6 (25.0 / 20.2).
 bool wide_items(const AttendArgs& p, int64_t rows, int64_t keys, int dim, int sms) {
   const double blocks = double(p.s.seqs * p.c.heads);  // (double: estimates may be huge)

@@ -5,16 +5,23 @@
 //   y = R(p) (w x r),  r = 1 / sqrt(mean(x^2) + eps)
 // Backward, with g = R(-p) dy (R is orthogonal, so its transpose is R(-p)), xh = x r:
 //   dx = r (g w - xh mean(g w xh)),   dw = sum over tokens and heads of g xh
-// Both read every value once and write every result once; they are bound by HBM.
+// Both read every value once and write every result once.  Measured, 32 + 8 heads of 128, BF16:
+// forward 8191 tokens 32 us (172 MB, 5.4 TB/s), backward 16384 tokens 104 us (512 MB, 4.9 TB/s),
+// against 6.8 TB/s of a copy; 4 tokens take 1.8 us.  What holds them back from the copy is the
+// instructions of 8 values a lane and the latency of a warp's chain (position, tables, rows, the
+// sums over the lanes) at the occupancy that the rows in registers allow.  Tried and slower: 16
+// values a lane (fewer instructions, fewer warps: 40 us and 110 us), rows through shared memory
+// by asynchronous copies two units ahead (36 and 106 us), packed FP32 pairs (33 and 105 us).
 #include "attn.cuh"
 
 namespace dq4d {
 namespace {
 
+constexpr int V = 4;               // values of a lane's groups (lane_place)
 constexpr int kNormThreads = 256;  // forward: 8 warps
+constexpr int kNormCtas = 4;       // and CTAs per SM (3, with all registers: 36 us for 32)
 constexpr int kBwdThreads = 256;   // backward: 8 warps, each with weight-gradient sums
 constexpr int kBwdCtas = 2;        // and CTAs per SM
-constexpr int kBwdRows = 4;        // and heads of a lane at a time
 constexpr int kMaxPartials = 512;  // CTAs that may leave weight-gradient partials
 constexpr int kPartGroup = 16;     // of them summed together first
 static_assert((1 + kMaxPartials / kPartGroup) * 4 <= 256, "counters at the workspace's head");
@@ -58,76 +65,107 @@ __device__ __forceinline__ float group_sum(float v) {
   return v;
 }
 
+struct Turn {
+  float c[V], s[V];
+};
+
+// The cosines and sines of lane l at a row of the tables.
+__device__ __forceinline__ Turn load_turn(const NormArgs& p, bool turned, int64_t row, int l) {
+  Turn t = {};
+  if (turned && row >= 0) {
+    load_entries(p.cos + row * (p.rotary / 2) + V * l, t.c);
+    load_entries(p.sin + row * (p.rotary / 2) + V * l, t.s);
+  }
+  return t;
+}
+
 // A warp takes a unit: kRows heads of one token for each of its 32 / kLanes groups of
-// kLanes = kDim / 8 lanes, all of q or all of k.  The position's cosines and sines and the
-// weights stay in registers over the unit, and all its loads are issued before the first
-// use.  kRows = 4 once that gives every SM 16 warps; with fewer units one row a lane leaves
-// more warps, and the latency of one row, to each SM.  kRows = 1 / 4, in us, BF16:
+// kLanes = kDim / 2 V lanes, all of q or all of k.  The position's cosines and sines and the
+// weights stay in registers over the unit, multiplied:
+//   R(w x r) = r (x (w C) + y (w' S)),  y and w' the partners of x and w,
+// and all its loads are issued before the first use.  kRows = 4 once that gives every SM 16
+// warps; with fewer units one row a lane leaves more warps, and the latency of one row, to each
+// SM.  kRows = 1 / 4, in us, BF16:
 //   tokens            64         256        512        1024       2048        8192
 //   40 heads of 128   2.0 / 2.6  2.8 / 3.0  4.1 / 3.6  6.7 / 5.1  12.2 / 8.1  52.4 / 32.1
 //   20 heads of 64    1.8 / 2.4  2.0 / 2.5  2.1 / 2.5  2.8 / 3.0   4.1 / 4.2  12.2 / 11.1
 template <int DT, int kDim, int kRows>
-__global__ void __launch_bounds__(kNormThreads) dq4_qk_norm_kernel(const NormArgs p) {
+__global__ void __launch_bounds__(kNormThreads, kNormCtas) dq4_qk_norm_kernel(const NormArgs p) {
   using T = typename Elem<DT>::T;
-  constexpr int kLanes = kDim / 8, kGroups = 32 / kLanes;
+  constexpr int kLanes = kDim / (2 * V), kGroups = 32 / kLanes;
   wait_for_stream();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int l = lane % kLanes, group = lane / kLanes;
   const int per_token = p.chunks[0] + p.chunks[1];
   const int64_t unit = int64_t(blockIdx.x) * (kNormThreads / 32) + warp;
-  const int64_t t = unit / per_token;
+  const int64_t t = unit >> 32 ? unit / per_token : int64_t(uint32_t(unit) / uint32_t(per_token));
   if (t >= p.tokens) return;
   int c = int(unit - t * per_token);
   const int which = c >= p.chunks[0];
   if (which) c -= p.chunks[0];
   const int h0 = c * (kRows * kGroups) + group;
   const int heads = p.heads[which];
-  const LanePlace at = lane_place(l, p.cos ? p.rotary : 0, p.interleaved);
+  const LanePlace at = lane_place<V>(l, p.cos ? p.rotary : 0, p.interleaved);
   const T* x = static_cast<const T*>(p.x[which]) + t * p.token_stride[which];
-  Raw4<DT> ra[kRows], rb[kRows];
+  Raw<DT, V> ra[kRows], rb[kRows];
 #pragma unroll
   for (int i = 0; i < kRows; ++i) {
     const int h = min(h0 + i * kGroups, heads - 1);
     const T* row = x + h * p.head_stride[which];
-    ra[i] = load4_once<DT>(row + at.a);
-    rb[i] = load4_once<DT>(row + at.b);
+    ra[i] = load_group_once<DT, V>(row + at.a);
+    rb[i] = load_group_once<DT, V>(row + at.b);
   }
   const bool normed = p.w[which] != nullptr;
-  F4 wa, wb;
+  Vals<V> w = {};
   if (normed) {
-    const T* w = static_cast<const T*>(p.w[which]);
-    wa = widen<DT>(load4<DT>(w + at.a));
-    wb = widen<DT>(load4<DT>(w + at.b));
+    const T* from = static_cast<const T*>(p.w[which]);
+    w = widen<DT, V>(load_group<DT, V>(from + at.a), load_group<DT, V>(from + at.b));
   }
   const int64_t row = table_row(p, t);
-  float4 cs = {}, sn = {};
-  if (at.turned && row >= 0) {
-    cs = load_global(reinterpret_cast<const float4*>(p.cos + row * (p.rotary / 2) + 4 * l));
-    sn = load_global(reinterpret_cast<const float4*>(p.sin + row * (p.rotary / 2) + 4 * l));
-  }
-  T* out = static_cast<T*>(p.out[which]) + t * heads * kDim;
+  const Turn turn = load_turn(p, at.turned, row, l);
+  T* out = static_cast<T*>(p.out[which]) + (t * heads + h0) * kDim;
+  auto rows = [&](auto interleaved) {
+    constexpr bool kInterleaved = decltype(interleaved)::value;
+    float wc[2 * V], ws[2 * V];
 #pragma unroll
-  for (int i = 0; i < kRows; ++i) {
-    const int h = h0 + i * kGroups;
-    F4 a = widen<DT>(ra[i]), b = widen<DT>(rb[i]);
-    if (normed) {
-      float ss = 0.f;
+    for (int j = 0; j < 2 * V; ++j) {
+      const int e = turn_entry<kInterleaved, V>(j);
+      const float s = w.v[partner<kInterleaved, V>(j)] * turn.s[e];
+      wc[j] = at.turned ? w.v[j] * turn.c[e] : w.v[j];
+      ws[j] = turn_adds<kInterleaved, V>(j) ? s : -s;
+    }
 #pragma unroll
-      for (int j = 0; j < 4; ++j) ss = fmaf(a.v[j], a.v[j], fmaf(b.v[j], b.v[j], ss));
-      const float r = rsqrtf(group_sum<kLanes>(ss) * (1.f / kDim) + p.eps);
+    for (int i = 0; i < kRows; ++i) {
+      Vals<V> v = widen<DT, V>(ra[i], rb[i]);
+      if (normed) {
+        float ss = 0.f;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        a.v[j] = a.v[j] * r * wa.v[j];
-        b.v[j] = b.v[j] * r * wb.v[j];
+        for (int j = 0; j < 2 * V; ++j) ss = fmaf(v.v[j], v.v[j], ss);
+        const float r = rsqrtf(group_sum<kLanes>(ss) * (1.f / kDim) + p.eps);
+        Vals<V> y;
+#pragma unroll
+        for (int j = 0; j < 2 * V; ++j) {
+          y.v[j] = v.v[j] * wc[j];
+          if (at.turned) y.v[j] = fmaf(v.v[partner<kInterleaved, V>(j)], ws[j], y.v[j]);
+          y.v[j] *= r;
+        }
+        v = y;
+      } else if (at.turned) {
+        v = turned<kInterleaved, false>(v, turn.c, turn.s);
       }
+      if (h0 + i * kGroups >= heads) continue;
+      if (row < 0) {
+        v = Vals<V>{};
+        if (l == 0 && p.bad) atomicAdd(p.bad, 1);
+      }
+      store_group<DT, V>(out + i * (kGroups * kDim) + at.a, narrow<DT, V>(v, 0));
+      store_group<DT, V>(out + i * (kGroups * kDim) + at.b, narrow<DT, V>(v, 1));
     }
-    if (at.turned) turn(a, b, cs, sn, p.interleaved);
-    if (row < 0) a = b = F4{};
-    if (h < heads) {
-      store4<DT>(out + h * kDim + at.a, a);
-      store4<DT>(out + h * kDim + at.b, b);
-      if (row < 0 && l == 0 && p.bad) atomicAdd(p.bad, 1);
-    }
+  };
+  if (p.interleaved) {
+    rows(std::true_type{});
+  } else {
+    rows(std::false_type{});
   }
 }
 
@@ -181,39 +219,40 @@ __device__ void finish_weights(const NormArgs& p, const float* mine) {
 }
 
 // The backward pass in the forward kernel's layout: first all of q's units, then k's.  A warp
-// walks them with a fixed stride, all of a unit's loads on the way at once, and keeps, in each lane, the sums of its eight columns of the weight's gradient; lanes,
-// warps and CTAs are then summed in a fixed order.  With r the row's factor and m' = mean(g w x),
+// walks them with a fixed stride, all of a unit's loads on the way at once, and keeps, in each
+// lane, the sums of its columns of the weight's gradient; lanes, warps and CTAs are then summed
+// in a fixed order.  With r the row's factor and m' = mean(g w x),
 //   dx = r g w - x r^3 m',   dw += r g x
 // so that both sums over a row, of x^2 and of g w x, go through the lanes together.
 template <int DT, int kDim, int kRows>
 __global__ void __launch_bounds__(kBwdThreads, kBwdCtas)
     dq4_qk_norm_backward_kernel(const NormArgs p) {
   using T = typename Elem<DT>::T;
-  constexpr int kLanes = kDim / 8, kGroups = 32 / kLanes, kWarps = kBwdThreads / 32;
+  constexpr int kLanes = kDim / (2 * V), kGroups = 32 / kLanes, kWarps = kBwdThreads / 32;
   __shared__ float sums[kWarps * 2 * kDim];
   wait_for_stream();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int l = lane % kLanes, group = lane / kLanes;
-  const LanePlace at = lane_place(l, p.cos ? p.rotary : 0, p.interleaved);
+  const LanePlace at = lane_place<V>(l, p.cos ? p.rotary : 0, p.interleaved);
   const int64_t unit0 = int64_t(blockIdx.x) * kWarps + warp;
   const int64_t stride = int64_t(gridDim.x) * kWarps;
   const bool normed = p.w[0] != nullptr;
   struct Rows {
-    Raw4<DT> xa[kRows], xb[kRows], ga[kRows], gb[kRows];
+    Raw<DT, V> xa[kRows], xb[kRows], ga[kRows], gb[kRows];
   };
 #pragma unroll 1
   for (int which = 0; which < 2; ++which) {
     const int heads = p.heads[which], chunks = p.chunks[which];
-    F4 dwa = {}, dwb = {}, wa = {}, wb = {};
+    Vals<V> dw = {};
     if (heads > 0) {
       const T* x = static_cast<const T*>(p.x[which]);
       const T* dy = static_cast<const T*>(p.dy[which]);
       T* out = static_cast<T*>(p.out[which]);
       const int64_t token_stride = p.token_stride[which], head_stride = p.head_stride[which];
+      Vals<V> w = {};
       if (normed) {
-        const T* w = static_cast<const T*>(p.w[which]);
-        wa = widen<DT>(load4<DT>(w + at.a));
-        wb = widen<DT>(load4<DT>(w + at.b));
+        const T* from = static_cast<const T*>(p.w[which]);
+        w = widen<DT, V>(load_group<DT, V>(from + at.a), load_group<DT, V>(from + at.b));
       }
       // a unit: head chunk c of token t
       const int64_t t_step = stride / chunks;
@@ -225,10 +264,10 @@ __global__ void __launch_bounds__(kBwdThreads, kBwdCtas)
           const int h = min((c * kRows + i) * kGroups + group, heads - 1);
           const T* xr = x + t * token_stride + h * head_stride;
           const T* gr = dy + (t * heads + h) * kDim;
-          r.xa[i] = load4_once<DT>(xr + at.a);
-          r.xb[i] = load4_once<DT>(xr + at.b);
-          r.ga[i] = load4_once<DT>(gr + at.a);
-          r.gb[i] = load4_once<DT>(gr + at.b);
+          r.xa[i] = load_group_once<DT, V>(xr + at.a);
+          r.xb[i] = load_group_once<DT, V>(xr + at.b);
+          r.ga[i] = load_group_once<DT, V>(gr + at.a);
+          r.gb[i] = load_group_once<DT, V>(gr + at.b);
         }
       };
       int64_t t = unit0 / chunks;
@@ -243,52 +282,48 @@ __global__ void __launch_bounds__(kBwdThreads, kBwdCtas)
           c2 -= chunks;
           ++t2;
         }
-        float4 cs = {}, sn = {};
-        if (at.turned && row >= 0) {
-          cs = load_global(reinterpret_cast<const float4*>(p.cos + row * (p.rotary / 2) + 4 * l));
-          sn = load_global(reinterpret_cast<const float4*>(p.sin + row * (p.rotary / 2) + 4 * l));
-          sn = make_float4(-sn.x, -sn.y, -sn.z, -sn.w);
-        }
+        const Turn turn = load_turn(p, at.turned, row, l);
 #pragma unroll
         for (int i = 0; i < kRows; ++i) {
           const int h = (c * kRows + i) * kGroups + group;
-          F4 a = widen<DT>(now.xa[i]), b = widen<DT>(now.xb[i]);
-          F4 g = widen<DT>(now.ga[i]), k = widen<DT>(now.gb[i]);
-          if (at.turned) turn(g, k, cs, sn, p.interleaved);
-          if (row < 0) g = k = F4{};
+          Vals<V> g = widen<DT, V>(now.ga[i], now.gb[i]);
           if (normed) {
-            float ss = 0.f, dot = 0.f;
-            F4 ga, gb;
+            const Vals<V> v = widen<DT, V>(now.xa[i], now.xb[i]);
+            if (at.turned)
+              g = p.interleaved ? turned<true, true>(g, turn.c, turn.s)
+                                : turned<false, true>(g, turn.c, turn.s);
+            float ss = 0.f, gwx = 0.f;
+            Vals<V> gx;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              ss = fmaf(a.v[j], a.v[j], fmaf(b.v[j], b.v[j], ss));
-              ga.v[j] = g.v[j] * a.v[j];
-              gb.v[j] = k.v[j] * b.v[j];
-              dot = fmaf(ga.v[j], wa.v[j], fmaf(gb.v[j], wb.v[j], dot));
+            for (int j = 0; j < 2 * V; ++j) {
+              gx.v[j] = g.v[j] * v.v[j];
+              ss = fmaf(v.v[j], v.v[j], ss);
+              gwx = fmaf(gx.v[j], w.v[j], gwx);
             }
 #pragma unroll
             for (int o = kLanes / 2; o > 0; o >>= 1) {
               ss += __shfl_xor_sync(kAllLanes, ss, o);
-              dot += __shfl_xor_sync(kAllLanes, dot, o);
+              gwx += __shfl_xor_sync(kAllLanes, gwx, o);
             }
             const float r = rsqrtf(ss * (1.f / kDim) + p.eps);
-            const float m = -(dot * (1.f / kDim)) * r * r * r;
-            const float real = h < heads ? r : 0.f;
+            const float m = -(gwx * (1.f / kDim)) * r * r * r;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              dwa.v[j] = fmaf(ga.v[j], real, dwa.v[j]);
-              dwb.v[j] = fmaf(gb.v[j], real, dwb.v[j]);
-              g.v[j] = fmaf(g.v[j] * wa.v[j], r, a.v[j] * m);
-              k.v[j] = fmaf(k.v[j] * wb.v[j], r, b.v[j] * m);
+            for (int j = 0; j < 2 * V; ++j) {
+              if (h < heads && row >= 0) dw.v[j] = fmaf(gx.v[j], r, dw.v[j]);
+              g.v[j] = fmaf(g.v[j] * w.v[j], r, v.v[j] * m);
             }
-            if (row < 0) g = k = F4{};
+          } else if (at.turned) {
+            g = p.interleaved ? turned<true, true>(g, turn.c, turn.s)
+                              : turned<false, true>(g, turn.c, turn.s);
           }
-          if (h < heads) {
-            T* o = out + (t * heads + h) * kDim;
-            store4_once<DT>(o + at.a, g);
-            store4_once<DT>(o + at.b, k);
-            if (row < 0 && l == 0 && p.bad) atomicAdd(p.bad, 1);
+          if (h >= heads) continue;
+          if (row < 0) {
+            g = Vals<V>{};
+            if (l == 0 && p.bad) atomicAdd(p.bad, 1);
           }
+          T* o = out + (t * heads + h) * kDim;
+          store_group_once<DT, V>(o + at.a, narrow<DT, V>(g, 0));
+          store_group_once<DT, V>(o + at.b, narrow<DT, V>(g, 1));
         }
         t = t2;
         c = c2;
@@ -297,16 +332,11 @@ __global__ void __launch_bounds__(kBwdThreads, kBwdCtas)
     }
     if (p.dw[0] == nullptr) continue;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int j = 0; j < 2 * V; ++j) {
 #pragma unroll
-      for (int o = kLanes; o < 32; o <<= 1) {
-        dwa.v[j] += __shfl_xor_sync(kAllLanes, dwa.v[j], o);
-        dwb.v[j] += __shfl_xor_sync(kAllLanes, dwb.v[j], o);
-      }
-      if (group == 0) {
-        sums[(warp * 2 + which) * kDim + at.a + j] = dwa.v[j];
-        sums[(warp * 2 + which) * kDim + at.b + j] = dwb.v[j];
-      }
+      for (int o = kLanes; o < 32; o <<= 1) dw.v[j] += __shfl_xor_sync(kAllLanes, dw.v[j], o);
+      if (group == 0)
+        sums[(warp * 2 + which) * kDim + (j < V ? at.a + j : at.b + j - V)] = dw.v[j];
     }
   }
   if (p.dw[0] == nullptr) return;
@@ -321,7 +351,9 @@ __global__ void __launch_bounds__(kBwdThreads, kBwdCtas)
 }
 
 // Any even head size and rotation, any alignment: a warp per head, values lane, lane + 32
-// and so on, a value's partner read again from memory (L1).
+// and so on, a value's partner read again from memory (L1).  For shapes that the kernels above
+// could take it needs, forward and backward, 25 and 86 us for 5 and 15 (1024 tokens, 40 heads of
+// 128, BF16).
 template <int DT, bool kBackward>
 __global__ void __launch_bounds__(32 * kAnyWarps) dq4_qk_norm_any_kernel(const NormArgs p) {
   using T = typename Elem<DT>::T;
@@ -437,13 +469,15 @@ int check_norm(const NormArgs& p, int32_t dtype) {
   return DQ4_OK;
 }
 
-// Whether the register kernels take this call (see lane_place and load4).
-bool in_registers(const NormArgs& p, int32_t dtype, bool backward) {
+// Whether the kernels that hold a head in groups of V values take this call (see lane_place and
+// load_group).
+bool in_groups(const NormArgs& p, int32_t dtype, bool backward) {
   if (p.dim != 64 && p.dim != 128 && p.dim != 256) return false;
-  if (p.cos && (p.rotary % 8 != 0 || !aligned(p.cos, 16) || !aligned(p.sin, 16))) return false;
-  const uintptr_t to = dtype == DQ4_OUT_F32 ? 16 : 8;
+  if (p.cos && (p.rotary % (2 * V) != 0 || !aligned(p.cos, 16) || !aligned(p.sin, 16)))
+    return false;
+  const uintptr_t to = V * (dtype == DQ4_OUT_F32 ? 4 : 2);
   for (int n = 0; n < 2 && p.heads[n] > 0; ++n) {
-    if (p.token_stride[n] % 4 != 0 || p.head_stride[n] % 4 != 0 || !aligned(p.x[n], to) ||
+    if (p.token_stride[n] % V != 0 || p.head_stride[n] % V != 0 || !aligned(p.x[n], to) ||
         !aligned(p.out[n], to) || !aligned(p.w[n], to) || (backward && !aligned(p.dy[n], to)))
       return false;
   }
@@ -451,36 +485,43 @@ bool in_registers(const NormArgs& p, int32_t dtype, bool backward) {
 }
 
 void cut_heads(NormArgs* p, int rows) {
-  p->chunk = rows * 32 / (p->dim / 8);
+  p->chunk = rows * 32 / (p->dim / (2 * V));
   for (int n = 0; n < 2; ++n) p->chunks[n] = (p->heads[n] + p->chunk - 1) / p->chunk;
 }
 
 template <int DT, int kDim>
 int launch_forward(NormArgs p, int sms, cudaStream_t stream) {
-  constexpr int kWarps = kNormThreads / 32;
-  cut_heads(&p, 4);
-  const bool four = p.tokens * (p.chunks[0] + p.chunks[1]) >= int64_t(sms) * 16;
-  if (!four) cut_heads(&p, 1);
+  constexpr int kWarps = kNormThreads / 32, kRows = 32 / Raw<DT, V>::kBytes;  // 64 bytes of a lane
+  cut_heads(&p, kRows);
+  const bool more = p.tokens * (p.chunks[0] + p.chunks[1]) >= int64_t(sms) * 16;
+  if (!more) cut_heads(&p, 1);
   const int64_t grid = (p.tokens * (p.chunks[0] + p.chunks[1]) + kWarps - 1) / kWarps;
   if (grid > kMaxGrid) return DQ4_ERR_N;
-  return launch_ordered(four ? dq4_qk_norm_kernel<DT, kDim, 4> : dq4_qk_norm_kernel<DT, kDim, 1>,
-                        dim3(unsigned(grid)), kNormThreads, 0, stream, p);
+  return launch_ordered(
+      more ? dq4_qk_norm_kernel<DT, kDim, kRows> : dq4_qk_norm_kernel<DT, kDim, 1>,
+      dim3(unsigned(grid)), kNormThreads, 0, stream, p);
 }
 
 template <int DT, int kDim>
 int launch_backward(NormArgs p, int sms, cudaStream_t stream) {
-  constexpr int kWarps = kBwdThreads / 32;
-  cut_heads(&p, kBwdRows);
+  constexpr int kWarps = kBwdThreads / 32, kRows = 32 / Raw<DT, V>::kBytes;  // 128 bytes of a lane
+  cut_heads(&p, kRows);
   const int64_t units = p.tokens * (p.chunks[0] + p.chunks[1]);
   const int64_t want = (units + kWarps - 1) / kWarps;
   const int most = kBwdCtas * sms < kMaxPartials ? kBwdCtas * sms : kMaxPartials;
-  return launch_ordered(dq4_qk_norm_backward_kernel<DT, kDim, kBwdRows>,
+  return launch_ordered(dq4_qk_norm_backward_kernel<DT, kDim, kRows>,
                         dim3(unsigned(want < most ? want : most)), kBwdThreads, 0, stream, p);
+}
+
+template <int DT, int kDim>
+int launch_dim(const NormArgs& p, bool backward, int sms, cudaStream_t stream) {
+  return backward ? launch_backward<DT, kDim>(p, sms, stream)
+                  : launch_forward<DT, kDim>(p, sms, stream);
 }
 
 template <int DT>
 int launch_norm(const NormArgs& p, bool backward, int sms, cudaStream_t stream) {
-  if (!in_registers(p, DT, backward)) {
+  if (!in_groups(p, DT, backward)) {
     const int64_t want = (p.tokens * (p.heads[0] + p.heads[1]) + kAnyWarps - 1) / kAnyWarps;
     const int64_t most = backward ? kMaxPartials : 16 * sms;
     const dim3 grid(unsigned(want < most ? want : most));
@@ -490,15 +531,9 @@ int launch_norm(const NormArgs& p, bool backward, int sms, cudaStream_t stream) 
                                 p);
   }
   switch (p.dim) {
-    case 64:
-      return backward ? launch_backward<DT, 64>(p, sms, stream)
-                      : launch_forward<DT, 64>(p, sms, stream);
-    case 128:
-      return backward ? launch_backward<DT, 128>(p, sms, stream)
-                      : launch_forward<DT, 128>(p, sms, stream);
-    default:
-      return backward ? launch_backward<DT, 256>(p, sms, stream)
-                      : launch_forward<DT, 256>(p, sms, stream);
+    case 64: return launch_dim<DT, 64>(p, backward, sms, stream);
+    case 128: return launch_dim<DT, 128>(p, backward, sms, stream);
+    default: return launch_dim<DT, 256>(p, backward, sms, stream);
   }
 }
 
