@@ -23,7 +23,7 @@ sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
 import quantized_weight_dequantization_gb300 as dq  # noqa: E402
 
 DEV = torch.device("cuda")
-HIDDEN, HEADS, KV_HEADS, DIM, PAGE = 2048, 16, 4, 128, 64
+HIDDEN, HEADS, KV_HEADS, DIM, PAGE = 2048, 16, 8, 128, 64
 DTYPE = torch.bfloat16
 
 

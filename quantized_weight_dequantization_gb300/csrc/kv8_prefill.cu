@@ -237,8 +237,8 @@ struct PrefillArgs {
 
 // List the units: sequence b's stand at index row / 256 + b and on, as many as its rows need;
 // indexes in between are units without rows.  One CTA, as the list is short (a unit for 256 rows)
-// and each unit's start needs the sum before it: 4 us or so, before the other kernel's 30 at
-// least.
+// and each unit's start needs the sum before it: 5.5 us for 4 sequences from cold caches,
+// where the other kernel takes 38.
 __global__ void __launch_bounds__(kPlanThreads) dq4_kv8_plan_kernel(const PrefillArgs w) {
   const AttendArgs& p = w.a;
   __shared__ int64_t s_sums[32];
