@@ -281,6 +281,27 @@ def test_append_prompts_then_tokens(dq, page, dim, dtype, rotary, inter):
     b.check()
 
 
+@pytest.mark.parametrize("pad", [4, 8])
+@pytest.mark.parametrize("dim,rotary,inter", [(128, 128, False), (64, 32, True), (64, 8, False)])
+def test_append_tokens_aligned_to_8_or_16_bytes(dq, pad, dim, rotary, inter):
+    """Rows a multiple of 4 or of 8 values apart, the first 8 bytes past a 16-byte boundary."""
+    b = Batch(dq, [100, 37], 3, dim, 32, seed=16)
+    buf = b.rng.standard_normal((2, 137, 3, dim + pad)).astype(np.float32)
+    flat = [torch.zeros(buf[0].size + 8, dtype=torch.bfloat16, device="cuda")[4:-4]
+            for _ in range(2)]
+    xs = []
+    for t, x in zip(flat, buf):
+        t.copy_(dev(x.ravel(), torch.bfloat16))
+        xs.append(t.view(137, 3, dim + pad)[:, :, :dim])
+    cos, sin = tables(101, rotary, b.rng)
+    lens, cu = np.array([100, 37], np.int32), np.array([0, 100, 137], np.int32)
+    dq.kv8_append(b.cache, *xs, dev(b.table), dev(lens), dev(cu), dev(cos), dev(sin), inter)
+    for i in range(2):
+        oracle_attn.append(b.codes[i], b.scales[i], host(xs[i]), cos if i == 0 else None, sin,
+                           b.table, lens, cu, inter)
+    b.check()
+
+
 def test_append_scales_grow_shrink_and_hit_their_limits(dq):
     b = Batch(dq, [64] * 6, 2, 64, 64, seed=9)
     sizes = [1.0, 448.0, 449.0, 1e-38, 6e4, 0.0]
