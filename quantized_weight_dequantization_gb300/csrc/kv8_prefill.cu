@@ -63,8 +63,11 @@ constexpr int kMaxCtas = 160;      // CTAs the workspace has room for
 constexpr int kOpening = 13;       // what starting and ending a unit costs, in steps
 constexpr int kMinSteps = 16;      // steps that a CTA takes at least
 constexpr int kPlanThreads = 1024;
-// P <= 2^(kTileLift + kSlack) = 2^15 fits FP16
-constexpr float kTileLift = 7.f, kSlack = 8.f;
+// P <= 2^(kTileLift + kSlack) = 2^15 fits FP16.  A row's reference is set at its first keys, 2^2
+// for the largest of them; weights down to 2^-14 (2^-16 of it) have all their bits, smaller
+// ones a step of 2^-24.  The slack is what a row's maximum may grow by before its step is computed
+// again and O rescaled: with 2^7 and 2^8 a prompt of 8192 takes 651 us, with 2^2 and 2^13 607.
+constexpr float kTileLift = 2.f, kSlack = 13.f;
 
 // A unit, as planned.
 struct alignas(16) Unit {
