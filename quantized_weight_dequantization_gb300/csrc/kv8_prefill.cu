@@ -33,14 +33,16 @@
 // works on this one, and P V of this one while it works on the next.
 // Q, K and V are held K-major / MN-major with 128-byte swizzle: rows of 64 values.
 //
-// Measured: a causal prompt of 8192 tokens, 32 heads over 8 of 128, BF16, 651 us (550 GFLOP, 845
-// TFLOP/s, 0.44 of a library GEMM's rate); 5 chunks of up to 1025 tokens over up to 16411 keys,
-// 16 heads over 8 of 64, 353 us (186 GFLOP, 527 TFLOP/s; at 64 a key takes as many exponentials
-// and scores for half the operations).  A step takes 1800 to 2100 cycles for 1300 of the tensor
-// cores': the conversion of the codes, and roles that share the issue slots and the instruction
-// caches.  Dropped after measuring: one thread that issues all products, the softmax tiles taking
-// turns, codes by TMA (each within 5 %), issue code with all operands static (1954 us: it no
-// longer fits the instruction caches).
+// Measured: a causal prompt of 8192 tokens, 32 heads over 8 of 128, BF16, 528 to 562 us by its
+// data (550 GFLOP, 1.0 PFLOP/s, 0.53 of a library GEMM's rate), 627 where one head's scores spread
+// so widely that its rows move often; 5 chunks of up to 1025 tokens over up to 16411 keys,
+// 16 heads over 8 of 64, 340 us (186 GFLOP, 546 TFLOP/s; at 64 a key takes as many exponentials
+// and scores for half the operations).  A step takes about 2000 cycles for 1300 of the tensor
+// cores': the conversion of the codes, and roles that share the issue slots (half of them busy)
+// and the instruction caches; starting and ending a unit takes about nine steps more.  Dropped
+// after measuring: one thread that issues all products, the softmax tiles taking turns, codes by
+// TMA (each within 5 %), the next unit's query rows prefetched to L2 (605 us for 607), issue code
+// with all operands static (1954 us: it no longer fits the instruction caches).
 #include "kv8_attend.cuh"
 
 namespace dq4d {
@@ -60,13 +62,17 @@ constexpr int kPrefillThreads = kUnitRows + kLoadThreads + 128;
 constexpr int kLoadWarp = kUnitRows / 32;
 constexpr int kIssueWarp = kLoadWarp + kLoadThreads / 32;
 constexpr int kMaxCtas = 160;      // CTAs the workspace has room for
-constexpr int kOpening = 13;       // what starting and ending a unit costs, in steps
+// What starting and ending a unit counts for in the division of the work, in steps: about 9 by
+// the cycles of most runs, more where rows move often.  A prompt of 8192 takes 536 to 560 us
+// with 13, 528 to 562 with 10 and 520 to 571 with 8, by its data, one of 2048 78, 75 and 74.
+constexpr int kOpening = 10;
 constexpr int kMinSteps = 16;      // steps that a CTA takes at least
 constexpr int kPlanThreads = 1024;
 // P <= 2^(kTileLift + kSlack) = 2^15 fits FP16.  A row's reference is set at its first keys, 2^2
 // for the largest of them; weights down to 2^-14 (2^-16 of it) have all their bits, smaller
-// ones a step of 2^-24.  The slack is what a row's maximum may grow by before its step is computed
-// again and O rescaled: with 2^7 and 2^8 a prompt of 8192 takes 651 us, with 2^2 and 2^13 607.
+// ones a step of 2^-24.  The slack is what a row's maximum may grow by before its step is
+// computed again and O rescaled: with 2^7 and 2^8 a prompt of 8192 with one head of widely spread
+// scores takes 651 us, with 2^2 and 2^13 607 (both with kOpening 13).
 constexpr float kTileLift = 2.f, kSlack = 13.f;
 
 // A unit, as planned.
@@ -488,11 +494,25 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) dq4_kv8_prefill_kernel(con
     // The query row, scaled, to shared memory; its factor for the scores.  (The unit before
     // has no more use for its own: its last scores were waited for.)
     auto load_query = [&](int64_t src) {
-      uint4 raw[kDim / 8];
+      // a warp copies its rows, whole lines at a time, and each thread then takes its own
+      constexpr int kPieces = kDim / 8;  // of 16 bytes
+      auto piece_at = [&](int row, int i) {
+        return sbase + S::kQ + t * S::kQTile + (i / 8) * S::kQBlock + row * 128 +
+               (((i & 7) ^ (row & 7)) << 4);
+      };
+#pragma unroll 1
+      for (int i = 0; i < kPieces; ++i) {
+        const int r = i * (32 / kPieces) + lane / kPieces, piece = lane % kPieces;
+        const uint16_t* from = static_cast<const uint16_t*>(p.q) +
+                               __shfl_sync(kAllLanes, src, r) + piece * 8;
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;"
+                     :: "r"(piece_at((warp & 3) * 32 + r, piece)), "l"(from) : "memory");
+      }
+      asm volatile("cp.async.wait_all;" ::: "memory");
+      __syncwarp();
+      uint4 raw[kPieces];
 #pragma unroll
-      for (int i = 0; i < kDim / 8; ++i)
-        raw[i] = load_global(
-            reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) + src) + i);
+      for (int i = 0; i < kPieces; ++i) raw[i] = lds_v4(piece_at(row, i));
       const uint32_t* h = reinterpret_cast<const uint32_t*>(raw);
       float top = 0.f;
 #pragma unroll
@@ -513,9 +533,7 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) dq4_kv8_prefill_kernel(con
           widen2(h[4 * i + j], p.bf16, y, z);
           f[j] = pack_f16(y * up, z * up);
         }
-        sts_v4(sbase + S::kQ + t * S::kQTile + (i / 8) * S::kQBlock + row * 128 +
-                   (((i & 7) ^ (row & 7)) << 4),
-               f[0], f[1], f[2], f[3]);
+        sts_v4(piece_at(row, i), f[0], f[1], f[2], f[3]);
       }
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       mbar_arrive(q_full(t));
