@@ -6,8 +6,8 @@
 // Backward, with g = R(-p) dy (R is orthogonal, so its transpose is R(-p)), xh = x r:
 //   dx = r (g w - xh mean(g w xh)),   dw = sum over tokens and heads of g xh
 // Both read every value once and write every result once.  Measured, 32 + 8 heads of 128, BF16:
-// forward 8191 tokens 32 us (172 MB, 5.4 TB/s), backward 16384 tokens 104 us (512 MB, 4.9 TB/s),
-// against 6.8 TB/s of a copy; 4 tokens take 1.8 us.  What holds them back from the copy is the
+// forward 8191 tokens 31 us (172 MB, 5.5 TB/s), backward 16384 tokens 101 us (512 MB, 5.0 TB/s),
+// against 6.8 TB/s of a copy; 4 tokens take 1.7 us.  What holds them back from the copy is the
 // instructions of 8 values a lane and the latency of a warp's chain (position, tables, rows, the
 // sums over the lanes) at the occupancy that the rows in registers allow.  Tried and slower: 16
 // values a lane (fewer instructions, fewer warps: 40 us and 110 us), rows through shared memory
@@ -18,12 +18,14 @@ namespace dq4d {
 namespace {
 
 constexpr int V = 4;               // values of a lane's groups (lane_place)
-constexpr int kNormThreads = 256;  // forward: 8 warps
-constexpr int kNormCtas = 4;       // and CTAs per SM (3, with all registers: 36 us for 32)
+// Forward: 4 warps a CTA (8191 tokens: 31.0 us; with 8 warps 32.0, with 16 33.9), and 32 warps
+// per SM (24, with all the registers that a lane would take: 36 us).
+constexpr int kNormThreads = 128;
+constexpr int kNormCtas = 8;
 constexpr int kBwdThreads = 256;   // backward: 8 warps, each with weight-gradient sums
 constexpr int kBwdCtas = 2;        // and CTAs per SM
 constexpr int kMaxPartials = 512;  // CTAs that may leave weight-gradient partials
-constexpr int kPartGroup = 16;     // of them summed together first
+constexpr int kPartGroup = 24;     // of them summed together first
 static_assert((1 + kMaxPartials / kPartGroup) * 4 <= 256, "counters at the workspace's head");
 constexpr int kMaxDim = 1024;
 constexpr int kAnyWarps = 4;       // warps per CTA of the any-size kernels
