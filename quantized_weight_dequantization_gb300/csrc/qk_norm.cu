@@ -26,7 +26,8 @@ constexpr int kBwdThreads = 256;   // backward: 8 warps, each with weight-gradie
 constexpr int kBwdCtas = 2;        // and CTAs per SM
 constexpr int kMaxPartials = 512;  // CTAs that may leave weight-gradient partials
 constexpr int kPartGroup = 24;     // of them summed together first
-static_assert((1 + kMaxPartials / kPartGroup) * 4 <= 256, "counters at the workspace's head");
+constexpr int kMaxGroups = (kMaxPartials + kPartGroup - 1) / kPartGroup;
+static_assert((1 + kMaxGroups) * 4 <= 256, "counters at the workspace's head");
 constexpr int kMaxDim = 1024;
 constexpr int kAnyWarps = 4;       // warps per CTA of the any-size kernels
 
@@ -574,7 +575,7 @@ int dq4_qk_norm_rope(const void* q, int64_t q_token_stride, int64_t q_head_strid
 
 int64_t dq4_qk_norm_rope_backward_workspace_bytes(int32_t head_dim) {
   if (head_dim < 2 || head_dim > kMaxDim) return 0;
-  return 256 + int64_t(kMaxPartials + kMaxPartials / kPartGroup) * 2 * head_dim * 4;
+  return 256 + int64_t(kMaxPartials + kMaxGroups) * 2 * head_dim * 4;
 }
 
 int dq4_qk_norm_rope_backward(const void* dq_out, const void* dk_out, const void* q,

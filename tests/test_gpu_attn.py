@@ -186,6 +186,29 @@ def test_norm_positions_outside_the_tables_give_zeros_and_are_counted(dq, dim):
         torch.testing.assert_close(x, y, rtol=1e-5, atol=1e-5)
 
 
+def guarded(need):
+    """A zero-filled workspace of just `need` bytes, and the bytes that follow it."""
+    buf = torch.zeros(need + 65536, dtype=torch.uint8, device="cuda")
+    buf[need:] = 0xA5
+    return buf[:need], buf[need:]
+
+
+@pytest.mark.parametrize("dim,pad", [(128, 0), (64, 3), (80, 0), (256, 3)])
+def test_norm_backward_stays_in_its_workspace(dq, dim, pad):
+    """As many CTAs as there can be leave sums: pad 3 and dim 80 take the any-size kernel."""
+    from quantized_weight_dequantization_gb300 import _attention
+    q, k, w, cos, sin, pos, rng = norm_problem(900, 6, 3, dim, 64, "bf16", 4, pad)
+    grads = [dev(rng.standard_normal(x.shape).astype(np.float32), torch.bfloat16) for x in (q, k)]
+    ws, after = guarded(_attention._norm_need(dim))
+    got = dq.qk_norm_rope_backward(*grads, q, k, *w, dev(cos), dev(sin), dev(pos), 1e-5,
+                                   workspace=ws)
+    assert bool((after == 0xA5).all()) and not bool(ws[:256].any())
+    for i, (x, dy) in enumerate(zip((q, k), grads)):
+        _, _, dw, dw_size = oracle_attn.norm_rope_backward(host(dy), host(x), host(w[i]), cos, sin,
+                                                           pos, 1e-5, False)
+        close(host(got[2 + i]), dw, 2.0 ** -15 * dw_size + 1e-30, "dw")
+
+
 # ----------------------------------------------------------------------- the cache
 class Batch:
     """A ragged batch on pages in random order, slots and scales never written left as NaN."""
@@ -468,6 +491,22 @@ def test_attend_pages_of_zeros_keep_their_weight(dq, new):
     b.cache.v_scale.copy_(dev(b.scales[1]))
     check_attend(dq, b, [new, new], 4, "bf16")
     check_attend(dq, b, [new, new], 4, "bf16", window=100)
+
+
+@pytest.mark.parametrize("hint", [1, MANY])
+@pytest.mark.parametrize("dim", [64, 128])
+def test_attend_stays_in_its_workspace(dq, dim, hint):
+    from quantized_weight_dequantization_gb300 import _attention
+    b = Batch(dq, [2000, 300, 1, 700], 4, dim, 32, seed=17)
+    b.fill()
+    new = [150, 40, 1, 0]
+    q = dev(b.rng.standard_normal((191, 12, dim)).astype(np.float32), torch.bfloat16)
+    cu = dev(np.concatenate([[0], np.cumsum(new)]).astype(np.int32))
+    args = (b.cache, q, dev(b.table), dev(np.array(b.lens, np.int32)), cu, hint)
+    ws, after = guarded(_attention._attention_need(191, 4, 12, 4, dim))
+    out = dq.kv8_attention(*args, workspace=ws)
+    assert bool((after == 0xA5).all()) and not bool(ws[:2048].any())
+    assert torch.equal(out, dq.kv8_attention(*args))
 
 
 @pytest.mark.parametrize("new", [1, 40])
