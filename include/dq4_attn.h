@@ -155,7 +155,9 @@ int dq4_kv8_append(const dq4_kv8_cache* cache, const void* k, int64_t k_token_st
  * pages * kv_heads: at most 2^31 - 1.  Keys past the table's
  * table_width pages, and pages with an id outside [0, pages), are not seen; bad is
  * incremented for each part of the work that met one, and for a wait that ran out (never
- * expected; the workspace must then be zero-filled again).
+ * expected; the workspace must then be zero-filled again).  Pages that lie wholly before
+ * the windows of all of the sequence's rows are not looked at: they may have been given
+ * back, their ids and what they hold may be anything.
  */
 int dq4_kv8_attention(const dq4_kv8_cache* cache, const void* q, int64_t q_token_stride,
                       int64_t q_head_stride, int32_t dtype, int64_t tokens, int32_t heads,

@@ -500,11 +500,12 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
   // Three batches are on the way, so that no load is used in the batch that issues it: the
   // page ids of batch + 2, the scales of batch + 1, and the batch that is being used.
   struct Ahead {
-    int seg, key, id, head;  // id: the page, or -1 where there are no such keys
+    int seg, key, id, head;  // id: the page, or -1 where there are no such keys, or none sees them
     int block;               // page * kv_heads + head, or -1
     float ks, vs;            // scales
   };
   int unit0 = 0, unit1 = 0;  // the plan's units, counted over the warp's
+  const int rows_copy = min(p.c.page, kTile);
   auto read_pages = [&](int batch) {
     Ahead a = {0, 0, -1, 0, -1, 0.f, 1.f};
     const int i = unit0 + batch * kBatch + lane / kGrans;
@@ -515,7 +516,8 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
     a.seg = sg;
     a.head = s.head;
     a.key = s.key0 + (s.tile0 + i - s.first) * kTile + (lane % kGrans) * 16;
-    if (a.key < s.held) {
+    // (copies take rows_copy keys; one of which no row of the sequence sees any is left out)
+    if (a.key < s.held && (a.key | (rows_copy - 1)) >= first_key(p, s.len - s.n)) {
       a.id = load_global(p.s.table + s.b * p.s.table_stride + (a.key >> p.c.log2_page));
       a.block = 0;
     }
@@ -541,7 +543,6 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
     now_bias = log2f(vs);
     now_inv = 1.f / vs;
   };
-  const int rows_copy = min(p.c.page, kTile);
   // The next slot of the ring: the keys (which = 0) or values of unit k of the plan, which
   // is in the batch `now` or the one after it.
   auto issue = [&](int k, int batch, int which) {

@@ -81,8 +81,9 @@ struct alignas(16) Unit {
   int b, r0, rows;   // sequence, first query row, and the sequence's rows
   int key0;          // first key, a multiple of kKeys
   int steps[2];      // of its tiles (0: no rows)
-  int len, n, row;   // the sequence's length, new tokens and first row of q
-  int held;          // its keys that are there
+  int pos, row;      // the sequence's first new token: its position, and its row of q
+  int held;          // the sequence's keys that are there
+  int seen;          // the first key that the rows see: pages before it are not looked at
 };
 static_assert(sizeof(Unit) == 48, "read as three 16-byte words");
 
@@ -271,17 +272,17 @@ __global__ void __launch_bounds__(kPlanThreads) dq4_kv8_plan_kernel(const Prefil
       const int64_t r0 = (u - first_unit(lo)) * kUnitRows;
       if (r0 < x.rows) {
         x.r0 = int(r0);
-        x.len = q.len;
-        x.n = q.n;
+        x.pos = q.len - q.n;
         x.row = int(q.row);
         x.held = held_keys(p, q.len);
-        const int begin = first_key(p, q.len - q.n + x.r0 / p.group) & ~(kKeys - 1);
-        x.key0 = min(begin, x.held & ~(kKeys - 1));
+        x.seen = first_key(p, x.pos + x.r0 / p.group);
+        x.key0 = min(x.seen, x.held) & ~(kKeys - 1);
+        if (x.held < q.len && p.bad) atomicAdd(p.bad, 1);
         for (int t = 0; t < 2; ++t) {
           const int first = x.r0 + t * kTileRows;
           if (first >= x.rows) break;
           const int last = min(x.rows, first + kTileRows) - 1;
-          const int end = last_key(p, q.len - q.n + last / p.group, x.held);
+          const int end = last_key(p, x.pos + last / p.group, x.held);
           // (one at least: rows that see no key get their zeros)
           x.steps[t] = max(1, (end - x.key0 + kKeys - 1) / kKeys);
         }
@@ -488,7 +489,7 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) dq4_kv8_prefill_kernel(con
       const int r = min(first + row, s.x.rows - 1);
       const int tok = r / p.group, q_head = s.head * p.group + r - tok * p.group;
       src = int64_t(s.x.row + tok) * p.token_stride + q_head * p.head_stride;
-      return Row{int64_t(s.x.row + tok) * p.heads + q_head, s.x.len - s.x.n + tok,
+      return Row{int64_t(s.x.row + tok) * p.heads + q_head, s.x.pos + tok,
                  first + row < s.x.rows};
     };
     // The query row, scaled, to shared memory; its factor for the scores.  (The unit before
@@ -554,8 +555,8 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) dq4_kv8_prefill_kernel(con
       const int lo = first_key(p, pos), hi = last_key(p, pos, x.held);
       // keys that every row of the tile sees
       const int last_r = min(x.rows, first + kTileRows) - 1;
-      const int all_lo = first_key(p, x.len - x.n + last_r / p.group);
-      const int all_hi = last_key(p, x.len - x.n + first / p.group, x.held);
+      const int all_lo = first_key(p, x.pos + last_r / p.group);
+      const int all_hi = last_key(p, x.pos + first / p.group, x.held);
       // from: what is taken off a row's exponents (the reference m less kTileLift)
       float from = 0.f, l = 0.f;
       bool fresh = true;  // no key seen yet
@@ -729,9 +730,8 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) dq4_kv8_prefill_kernel(con
       if (!more) return s;
       s.key = sg.x.key0 + j * kKeys;
       s.held = sg.x.held;
-      if (s.held < sg.x.len) met_bad = true;
       const int key = s.key + (lane & (kGrans - 1)) * 16;
-      if (key < s.held) {
+      if (key < s.held && (key | (p.c.page - 1)) >= sg.x.seen) {
         const int id =
             load_global(p.s.table + sg.x.b * p.s.table_stride + (key >> p.c.log2_page));
         if (id >= 0 && id < p.c.pages) {
