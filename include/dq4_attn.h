@@ -158,6 +158,10 @@ int dq4_kv8_append(const dq4_kv8_cache* cache, const void* k, int64_t k_token_st
  * expected; the workspace must then be zero-filled again).  Pages that lie wholly before
  * the windows of all of the sequence's rows are not looked at: they may have been given
  * back, their ids and what they hold may be anything.
+ * A NaN code or scale of K or V reaches the rows that see its key, and no others.  Of V, a
+ * scale that is NaN (append's mark of a page with a value that is not finite) makes out and
+ * lse of such a row NaN; a NaN code beside a number (append writes none) makes the row's
+ * value of that column NaN, or the whole row and its lse.
  */
 int dq4_kv8_attention(const dq4_kv8_cache* cache, const void* q, int64_t q_token_stride,
                       int64_t q_head_stride, int32_t dtype, int64_t tokens, int32_t heads,

@@ -74,6 +74,37 @@ __device__ __forceinline__ void widen2(uint32_t u, bool bf16, float& a, float& b
   }
 }
 
+// Codes that are no numbers among four e4m3 codes: 0x80 in the byte of each.
+__device__ __forceinline__ uint32_t nan_codes(uint32_t w) {
+  return ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
+}
+__device__ __forceinline__ uint32_t nan_codes(uint4 v) {
+  return nan_codes(v.x) | nan_codes(v.y) | nan_codes(v.z) | nan_codes(v.w);
+}
+// The same codes with zeros in their place.
+__device__ __forceinline__ uint4 without_nan(uint4 v) {
+  auto clean = [](uint32_t w) { return w & ~((nan_codes(w) >> 7) * 0xFFu); };
+  return make_uint4(clean(v.x), clean(v.y), clean(v.z), clean(v.w));
+}
+
+// The same of two FP16 values, 0x8000 in the place of each; and their larger values, or NaN.
+__device__ __forceinline__ uint32_t nan_halves(uint32_t w) {
+  return ((w & 0x7FFF7FFFu) + 0x03FF03FFu) & 0x80008000u;
+}
+__device__ __forceinline__ uint32_t larger_f16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+// The keys lo <= key + i < hi of 64, one bit each.
+__device__ __forceinline__ uint64_t seen_keys(int key, int lo, int hi) {
+  const int a = max(lo - key, 0), b = min(hi - key, 64);
+  return a < b ? ~uint64_t(0) >> (64 - (b - a)) << a : 0;
+}
+
+constexpr uint32_t kNaN = 0x7FC00000u;
+
 // The power of two that brings a row's largest magnitude into [2^14, 2^15), and its inverse.
 // FP16 then holds a BF16 or FP16 row as it is, but for values below 2^-38 of its largest.
 // A row with an infinity or a NaN gets a NaN inverse.
@@ -104,6 +135,23 @@ __device__ __forceinline__ uint32_t f16_of_e4m3_high(uint32_t w) {
   asm("{\n.reg .b16 lo, hi;\nmov.b32 {lo, hi}, %1;\ncvt.rn.f16x2.e4m3x2 %0, hi;\n}"
       : "=r"(r) : "r"(w));
   return r;
+}
+
+__device__ __forceinline__ void sts_v4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c,
+                                       uint32_t d) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};"
+               :: "r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+__device__ __forceinline__ void sts_b32(uint32_t addr, uint32_t v) {
+  asm volatile("st.shared.b32 [%0], %1;" :: "r"(addr), "r"(v) : "memory");
+}
+__device__ __forceinline__ uint32_t lds_b32(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(addr));
+  return v;
+}
+__device__ __forceinline__ void sts_v4(uint32_t addr, const uint4& v) {
+  sts_v4(addr, v.x, v.y, v.z, v.w);
 }
 
 }  // namespace

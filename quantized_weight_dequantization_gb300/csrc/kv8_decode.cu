@@ -716,6 +716,49 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
 
       // ---- O^T += V^T P^T: keys 2 c, 2 c + 1, + 8 and + 9 of each 16, dims g kDim / 8 ..
       const uint32_t values = arrive();
+      // A weight of 0 does not keep a value that is no number from its row.  So where some row
+      // does not see a key, such codes become zeros, and l brings them to the rows that do.
+      if (!all && (key < all_lo || min(key + kTile, seg_of[seg].held) > all_hi)) {
+        auto piece = [&](int row, int i) {
+          return values + row * kDim + (i ^ (lane & (kDim / 16 - 1))) * 16;
+        };
+        uint32_t any = 0;
+#pragma unroll
+        for (int i = 0; i < kDim / 16; ++i) {
+          const uint4 x = lds_v4(piece(lane, i)), y = lds_v4(piece(lane + 32, i));
+          any |= nan_codes(x) | nan_codes(y);
+        }
+        if (__any_sync(kAllLanes, any != 0)) {
+          uint64_t nan = 0;  // the keys that have such codes
+#pragma unroll 1
+          for (int row = lane; row < kTile; row += 32) {
+            bool found = false;
+#pragma unroll 1
+            for (int i = 0; i < kDim / 16; ++i) {
+              const uint4 v = lds_v4(piece(row, i));
+              if (nan_codes(v) == 0) continue;
+              found = true;
+              sts_v4(piece(row, i), without_nan(v));
+            }
+            nan |= uint64_t(__ballot_sync(kAllLanes, found)) << (row & 32);
+          }
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // (the slot's next copy)
+          __syncwarp();
+#pragma unroll
+          for (int h = 0; h < kGrans; ++h)
+            if (!there[h]) nan &= ~(uint64_t(0xFFFF) << (16 * h));
+          const Segment& s = seg_of[seg];
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              const int r = min(s.rows - 1, s.r0 + nt * 8 + 2 * c + j);
+              const int pos = s.len - s.n + r / p.group;
+              if (nan & seen_keys(key, first_key(p, pos), last_key(p, pos, s.held)))
+                l[nt][j] = __uint_as_float(kNaN);
+            }
+        }
+      }
 #pragma unroll
       for (int h = 0; h < kGrans; ++h) {
         uint32_t w[4][kWordsV];

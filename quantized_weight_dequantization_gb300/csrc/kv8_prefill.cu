@@ -83,9 +83,10 @@ struct alignas(16) Unit {
   int steps[2];      // of its tiles (0: no rows)
   int pos, row;      // the sequence's first new token: its position, and its row of q
   int held;          // the sequence's keys that are there
-  int seen;          // the first key that the rows see: pages before it are not looked at
+  int first;         // the first key of the pages that hold a key which some row sees
+  int all_lo, all_hi;  // the keys that every row sees
 };
-static_assert(sizeof(Unit) == 48, "read as three 16-byte words");
+static_assert(sizeof(Unit) == 64, "read as 16-byte words");
 
 template <int kDim>
 struct PrefillSmem {
@@ -102,7 +103,10 @@ struct PrefillSmem {
   static constexpr int kRawPass = kLoadThreads * 16;
   static constexpr int kRaw = kGran + kGranSlots * kGrans * 16;
   static constexpr int kNote = kRaw + kRawSlots * 2 * kKeys * kDim;
-  static constexpr int kBars = kNote + kRawSlots * kGrans * 16;
+  // [tile][step % 4] keys of a mixed step with NaN codes of V; [tile] rows that see such, a bit each
+  static constexpr int kNan = kNote + kRawSlots * kGrans * 16;
+  static constexpr int kLost = kNan + 2 * 4 * 16;
+  static constexpr int kBars = kLost + 2 * 16;
   static constexpr int kBytes = kBars + 34 * 8 + 1024;  // + alignment slack
   static_assert(kBytes + 256 <= 227 * 1024, "shared memory budget");
 };
@@ -116,12 +120,6 @@ __device__ __forceinline__ uint64_t smem_desc_mn(uint32_t addr, uint32_t block) 
   d |= static_cast<uint64_t>(1) << 46;
   d |= static_cast<uint64_t>(2) << 61;
   return d;
-}
-
-__device__ __forceinline__ void sts_v4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c,
-                                       uint32_t d) {
-  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};"
-               :: "r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
 
 // The products and their commits, by the lane of the warp that leads (the other operands are
@@ -234,6 +232,50 @@ __device__ __forceinline__ float softmax_pass(uint32_t scores, uint32_t gran, fl
   return top;
 }
 
+// A step's V as FP16 at `values`: what is no number becomes zero, and the keys that had such are
+// returned, a bit each.  Either tile's warp looks for itself, so what it finds it notes (`mine`:
+// {keys, step}) before it goes, for the other one (`other`), which may come too late to see it.
+template <int kDim>
+__device__ __noinline__ uint64_t clean_values(uint32_t values, uint32_t mine, uint32_t other, int g) {
+  const int lane = threadIdx.x & 31;
+  constexpr int kPieces = kDim / 8;  // of 16 bytes, of a key
+  auto piece_at = [&](int key, int i) {
+    return values + (i / 8) * PrefillSmem<kDim>::kBlock + key * 128 + (((i ^ key) & 7) << 4);
+  };
+  uint64_t keys = 0;
+#pragma unroll 1
+  for (int key = lane; key < kKeys; key += 32) {
+    uint32_t top = 0;  // the largest of each half, or NaN if one is
+#pragma unroll 4
+    for (int i = 0; i < kPieces; ++i) {
+      const uint4 v = lds_v4(piece_at(key, i));
+      top = larger_f16x2(larger_f16x2(larger_f16x2(top, v.x), larger_f16x2(v.y, v.z)), v.w);
+    }
+    keys |= uint64_t(__ballot_sync(kAllLanes, nan_halves(top) != 0)) << (key & 32);
+  }
+  if (keys != 0) {
+    if (lane == 0) sts_v4(mine, uint32_t(keys), uint32_t(keys >> 32), uint32_t(g), 0);
+    __threadfence_block();
+    __syncwarp();
+#pragma unroll 1
+    for (int key = lane; key < kKeys; key += 32) {
+      if (!(keys >> key & 1)) continue;
+#pragma unroll 1
+      for (int i = 0; i < kPieces; ++i) {
+        const uint4 v = lds_v4(piece_at(key, i));
+        auto clean = [](uint32_t w) { return w & ~((nan_halves(w) >> 15) * 0xFFFFu); };
+        sts_v4(piece_at(key, i), clean(v.x), clean(v.y), clean(v.z), clean(v.w));
+      }
+    }
+  }
+  // (also for what the other warp wrote, and this one has seen)
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  __threadfence_block();
+  __syncwarp();
+  const uint4 note = lds_v4(other);
+  return int(note.z) == g ? keys | note.x | uint64_t(note.y) << 32 : keys;
+}
+
 // The call, and where its workspace holds what.
 struct PrefillArgs {
   AttendArgs a;
@@ -275,8 +317,11 @@ __global__ void __launch_bounds__(kPlanThreads) dq4_kv8_plan_kernel(const Prefil
         x.pos = q.len - q.n;
         x.row = int(q.row);
         x.held = held_keys(p, q.len);
-        x.seen = first_key(p, x.pos + x.r0 / p.group);
-        x.key0 = min(x.seen, x.held) & ~(kKeys - 1);
+        const int first_pos = x.pos + x.r0 / p.group;
+        x.first = first_key(p, first_pos) & -p.c.page;
+        x.key0 = min(first_key(p, first_pos), x.held) & ~(kKeys - 1);
+        x.all_lo = first_key(p, x.pos + (min(x.rows, x.r0 + kUnitRows) - 1) / p.group);
+        x.all_hi = last_key(p, first_pos, x.held);
         if (x.held < q.len && p.bad) atomicAdd(p.bad, 1);
         for (int t = 0; t < 2; ++t) {
           const int first = x.r0 + t * kTileRows;
@@ -307,6 +352,30 @@ __global__ void __launch_bounds__(kPlanThreads) dq4_kv8_plan_kernel(const Prefil
     if (u < w.max_units) w.units[u] = x;
   }
   if (tid == 0) *w.total = total;
+}
+
+// A step of a unit is mixed if some row does not see one of its keys.  A weight of 0 does not
+// keep a value that is no number from its row, so in such steps V's codes that are none become
+// zeros before the product, and l brings them to the rows that see their keys.
+__device__ __forceinline__ bool mixed_step(int all_lo, int all_hi, int key) {
+  return key < all_lo || key + kKeys > all_hi;
+}
+
+// The rows of a tile that see a key of `nan` (bits of the keys from `key` on) are noted at
+// `lost`, after all rows have read what was noted of the unit before.  By one warp.
+__device__ __noinline__ void lose_rows(const AttendArgs& p, const Unit& x, int t, int key,
+                                       uint64_t nan, uint32_t lost) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll 1
+  for (int i = 0; i < kTileRows / 32; ++i) {
+    const int r = min(x.r0 + t * kTileRows + i * 32 + lane, x.rows - 1), pos = x.pos + r / p.group;
+    const bool sees = nan & seen_keys(key, first_key(p, pos), last_key(p, pos, x.held));
+    const uint32_t rows = __ballot_sync(kAllLanes, sees);
+    if (lane == 0 && rows)
+      asm volatile("red.shared.or.b32 [%0], %1;" :: "r"(lost + 4 * i), "r"(rows) : "memory");
+  }
+  __threadfence_block();
+  __syncwarp();
 }
 
 // A CTA's walk over its run of steps, the same for each of its roles: all kv heads' steps
@@ -346,7 +415,7 @@ __device__ __forceinline__ bool next_segment(const PrefillArgs& w, Walk& k, Segm
     const int4* src = reinterpret_cast<const int4*>(w.units + k.u);
     int4* dst = reinterpret_cast<int4*>(&s.x);
 #pragma unroll
-    for (int i = 0; i < 3; ++i) dst[i] = load_global(src + i);
+    for (int i = 0; i < int(sizeof(Unit) / 16); ++i) dst[i] = load_global(src + i);
     const int steps = max(s.x.steps[0], s.x.steps[1]);
     s.item0 = k.head * k.total + s.x.start + kOpening;
     ++k.u;
@@ -404,6 +473,8 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) dq4_kv8_prefill_kernel(con
   auto o_done = [&](int t, int u) { return bar0 + 8 * (24 + 2 * t + u); };
   auto q_full = [&](int t) { return bar0 + 8 * (28 + t); };
   auto all_done = [&](int i) { return bar0 + 8 * (30 + i); };
+  if (tid < 8) sts_v4(sbase + S::kNan + 16 * tid, 0, 0, uint32_t(-1), 0);
+  if (tid < 2) sts_v4(sbase + S::kLost + 16 * tid, 0, 0, 0, 0);
   if (tid == 0) {
     s_abort = 0;
     for (int i = 0; i < kSlots; ++i) {
@@ -550,13 +621,10 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) dq4_kv8_prefill_kernel(con
     }
     while (have) {
       const Unit& x = sg.x;
-      const int count = count_of(sg), first = x.r0 + t * kTileRows;
+      const int count = count_of(sg);
       const int pos = me.pos;
       const int lo = first_key(p, pos), hi = last_key(p, pos, x.held);
-      // keys that every row of the tile sees
-      const int last_r = min(x.rows, first + kTileRows) - 1;
-      const int all_lo = first_key(p, x.pos + last_r / p.group);
-      const int all_hi = last_key(p, x.pos + first / p.group, x.held);
+      const int all_lo = x.all_lo, all_hi = x.all_hi;
       // from: what is taken off a row's exponents (the reference m less kTileLift)
       float from = 0.f, l = 0.f;
       bool fresh = true;  // no key seen yet
@@ -568,7 +636,7 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) dq4_kv8_prefill_kernel(con
         const uint32_t gran = sbase + S::kGran + (sg.step0 + j) % kGranSlots * (kGrans * 16);
         const uint32_t scores = t_s(t, u) + lanes;
         const int key = x.key0 + (sg.a + j) * kKeys;
-        const bool masked = key < all_lo || key + kKeys > all_hi;
+        const bool masked = mixed_step(all_lo, all_hi, key);
         uint32_t wt[kKeys / 2];
         float more = 0.f;
         const float top = masked ? softmax_pass<true>(scores, gran, cq, from, key, lo, hi, more, wt)
@@ -617,6 +685,13 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) dq4_kv8_prefill_kernel(con
       ok = wait_warp(o_done(t, (step - 1) & 1), (step - 1) >> 1);
       if (!ok) break;
       asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+      const uint32_t lost_at = sbase + S::kLost + 16 * t + 4 * (warp & 3);
+      const uint32_t lost = lds_b32(lost_at);
+      if (lost != 0) {
+        if (lost >> lane & 1) l = __uint_as_float(kNaN);
+        __syncwarp();
+        if (lane == 0) sts_b32(lost_at, 0);
+      }
       uint4* out = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + at * kDim);
       auto put = [&](int c, const float (&o)[8], float inv) {  // columns 8 c .. of the row
         uint32_t f[4];
@@ -731,7 +806,8 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) dq4_kv8_prefill_kernel(con
       s.key = sg.x.key0 + j * kKeys;
       s.held = sg.x.held;
       const int key = s.key + (lane & (kGrans - 1)) * 16;
-      if (key < s.held && (key | (p.c.page - 1)) >= sg.x.seen) {
+      // (pages before the rows' windows are not looked at)
+      if (key < s.held && key >= sg.x.first) {
         const int id =
             load_global(p.s.table + sg.x.b * p.s.table_stride + (key >> p.c.log2_page));
         if (id >= 0 && id < p.c.pages) {
@@ -869,11 +945,14 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) dq4_kv8_prefill_kernel(con
     const uint32_t idesc_o = instr_desc_f16<kTileRows, kDim>(false) | (1u << 16);  // B: N contiguous
     // Every step's barriers are passed, also past the tile's last step, so that each slot's
     // phase ends with one arrival of each tile.
+    auto nan_at = [&](int t, int g) { return sbase + S::kNan + (t * 4 + (g & 3)) * 16; };
     int g = 0, step = 0, units = 0;  // steps, this tile's steps, its units so far
     bool ok = true;
     while (ok && next_segment(w, walk, sg)) {
       const int count = sg.e - sg.a;
       const int n = max(0, min(sg.e, sg.x.steps[t]) - sg.a);  // of this tile
+      const int key = sg.x.key0 + sg.a * kKeys;
+      const int all_lo = sg.x.all_lo, all_hi = sg.x.all_hi;
       if (role < 2 && n > 0) ok = wait_warp(q_full(t), units++);
       for (int j = 0; j < count && ok; ++j, ++g) {
         const int slot = g % kSlots, phase = g / kSlots, u = step & 1;
@@ -892,8 +971,15 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) dq4_kv8_prefill_kernel(con
           }
           commit_if(k_empty(slot), leads);
         } else {  // O += P V
-          ok = wait_warp(v_full(slot), phase) && (j >= n || wait_warp(p_full(t, u), step >> 1));
+          ok = wait_warp(v_full(slot), phase);
           if (!ok) break;
+          uint64_t nan = 0;
+          if (j < n && mixed_step(all_lo, all_hi, key + j * kKeys))
+            nan = clean_values<kDim>(sbase + S::kV + slot * S::kOperand, nan_at(t, g), nan_at(1 - t, g),
+                                     g);
+          ok = j >= n || wait_warp(p_full(t, u), step >> 1);
+          if (!ok) break;
+          if (nan != 0) lose_rows(p, sg.x, t, key + j * kKeys, nan, sbase + S::kLost + 16 * t);
           asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
           if (j < n) {
             const uint64_t v = v_desc + slot * (S::kOperand / 16);

@@ -1,13 +1,41 @@
-"""Attention over the 8-bit cache where values are no numbers; definitions and tolerances as in
-test_gpu_attn."""
+"""Attention over the 8-bit cache where values are no numbers, scores lie far apart, sums are
+large, and arguments are at their ends; definitions and tolerances as in test_gpu_attn."""
+
+import sys
 
 import numpy as np
 import pytest
 import torch
 
-from tests.test_gpu_attn import Batch, check_attend, dq  # noqa: F401
+from oracle import attention as oracle_attn
+from tests.test_gpu_attn import (DT, MANY, TINY, U, Batch, check_attend, close, dev, dq,  # noqa: F401
+                                 host)
 
 pytestmark = pytest.mark.gpu
+
+
+def both(dq, b, q, new, causal=True, window=0, scale=None, lens=None):
+    """(hint, out, lse, bad) of either kernel."""
+    cu = dev(np.concatenate([[0], np.cumsum(new)]).astype(np.int32))
+    lens = dev(np.array(b.lens if lens is None else lens, np.int32))
+    for hint in (1, MANY):
+        bad = torch.zeros(1, dtype=torch.int32, device="cuda")
+        out, lse = dq.kv8_attention(b.cache, q, dev(b.table), lens, cu, hint, scale, causal,
+                                    window, return_lse=True, bad=bad)
+        yield hint, out, lse, int(bad.item())
+
+
+def definition(b, q, new, scale, causal=True, window=0):
+    cu = np.concatenate([[0], np.cumsum(new)])
+    with np.errstate(invalid="ignore"):
+        return oracle_attn.attend(host(q), b.codes[0], b.codes[1], b.scales[0], b.scales[1],
+                                  b.table, b.lens, cu, scale, causal, window)
+
+
+def tolerance(want, size, reach, dtype):
+    """As derived in test_gpu_attn."""
+    return ((2.0 ** -10 + 2.0 ** -17 * reach[..., None]) * size + U[dtype] * np.abs(want)
+            + TINY[dtype])
 
 
 # ------------------------------------------------------- values that are no numbers
@@ -42,3 +70,51 @@ def test_attend_pages_before_the_window_need_not_exist(dq, new, dim, page, windo
         b.scales = [np.concatenate([s, np.full_like(s[:6], np.nan)]) if len(s) == b.pages else s
                     for s in b.scales]
     check_attend(dq, b, [new] * 3, 4, "bf16", True, window)
+
+
+@pytest.mark.parametrize("dim,heads,kv,page", [(64, 2, 2, 16), (128, 4, 2, 64), (128, 2, 2, 32)])
+@pytest.mark.parametrize("lens,new", [([200, 90], [200, 90]), ([200, 90], [102, 8]),
+                                      ([167, 90], [6, 3]), ([164, 81], [6, 4])])
+def test_attend_rows_before_a_value_that_is_not_finite(dq, dim, heads, kv, page, lens, new):
+    """What the append makes of an infinite value of V reaches the rows that see its page; lse
+    is as good as out."""
+    b = Batch(dq, lens, kv, dim, page, seed=23)
+
+    def make(i, x):
+        if i == 1:
+            x[min(162, lens[0] - 1), 0, 5] = np.inf  # sequence 0
+            x[lens[0] + 80, 1, 0] = np.nan           # sequence 1
+
+    b.append(dq, lens, lens, "bf16", 0, False, make=make)
+    assert sum(np.isnan(b.scales[1][t]).sum() for row in b.table for t in row if t >= 0) == 2
+    q = dev(b.rng.standard_normal((sum(new), heads, dim)).astype(np.float32), torch.bfloat16)
+    want, want_lse, size, reach = definition(b, q, new, dim ** -0.5)
+    seen = np.isnan(want).any(-1)
+    assert seen.any() and not seen.all()
+    for hint, out, lse, bad in both(dq, b, q, new):
+        close(host(out), want, tolerance(want, size, reach, "bf16"), ("out", hint))
+        close(lse.cpu().numpy()[~seen], want_lse[~seen], 2.0 ** -18 * reach[~seen] + 2.0 ** -18,
+              ("lse", hint))
+        assert bad == 0
+
+
+@pytest.mark.parametrize("dim,heads,kv,page", [(64, 2, 2, 16), (128, 8, 2, 64)])
+@pytest.mark.parametrize("new", [4, 77])
+@pytest.mark.parametrize("causal,window", [(True, 0), (True, 50), (False, 50)])
+def test_attend_codes_that_are_no_numbers_beside_scales_that_are(dq, dim, heads, kv, page, new,
+                                                                 causal, window):
+    """A NaN code of a key or a value reaches the rows that see it, and no others."""
+    b = Batch(dq, [300, 140], kv, dim, page, seed=24)
+    b.fill()
+    for i, key, g in ((1, 299, 0), (1, 240, 1), (0, 298, 1), (1, 246, 0)):
+        b.codes[i][b.table[0, key // page], g, key % page] = np.nan
+    for i, t in ((0, b.cache.k), (1, b.cache.v)):
+        t.copy_(dev(b.codes[i].astype(np.float32)).to(torch.float8_e4m3fn))
+    q = dev(b.rng.standard_normal((2 * new, heads, dim)).astype(np.float32), torch.bfloat16)
+    want, want_lse, size, reach = definition(b, q, [new] * 2, dim ** -0.5, causal, window)
+    seen = np.isnan(want).any(-1)
+    assert seen.any() and not seen.all()
+    for hint, out, lse, _ in both(dq, b, q, [new] * 2, causal, window):
+        close(host(out), want, tolerance(want, size, reach, "bf16"), ("out", hint))
+        close(lse.cpu().numpy()[~seen], want_lse[~seen], 2.0 ** -18 * reach[~seen] + 2.0 ** -18,
+              ("lse", hint))
