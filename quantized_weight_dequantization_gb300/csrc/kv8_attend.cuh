@@ -38,6 +38,19 @@ constexpr float kLn2 = 0.6931471805599453f;
 // to 2^-38 is not lost.
 constexpr float kLift = 14.f;
 
+// The sum l of the weights over the pages' V scales is held in units of 2^16.  A weight is at most
+// 2^15 and a scale 2^-100 to 2^120, so that 2^28 keys at the least scale stay below 2^128 (they
+// are log n in lse), and the largest weight of a row alone, 2^kLift or 2^kTileLift, above 2^-126
+// or little below it at the largest scale.
+constexpr float kSumUnit = 1.f / 65536;
+constexpr float kLogSumUnit = 16 * kLn2;
+
+// The factor of O that makes a row's result, and its log-sum: of sum l, with weights 2^(x - ref).
+__device__ __forceinline__ float inverse_sum(float l) { return l == 0.f ? 0.f : kSumUnit / l; }
+__device__ __forceinline__ float log_sum(float ref, float l) {
+  return l == 0.f ? -INFINITY : fmaf(ref, kLn2, logf(l) + kLogSumUnit);
+}
+
 __device__ __forceinline__ float exp2_fast(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));

@@ -216,13 +216,13 @@ __device__ __forceinline__ void write_row(const AttendArgs& p, const Segment& s,
   const int lane = threadIdx.x & 31;
   const int tok = (s.r0 + r) / p.group;
   const int64_t at = int64_t(s.row + tok) * p.heads + s.head * p.group + s.r0 + r - tok * p.group;
-  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  const float inv = inverse_sum(sum);
   uint32_t* out = static_cast<uint32_t*>(p.out) + (at * 32 + lane) * (kCols / 2);
 #pragma unroll
   for (int i = 0; i < kCols / 2; ++i)
     out[i] = pack_out(v[2 * i] * inv, v[2 * i + 1] * inv, p.bf16);
   if (p.lse && lane == 0)
-    p.lse[at] = sum == 0.f ? -INFINITY : fmaf(top - kLift, kLn2, logf(sum));
+    p.lse[at] = log_sum(top - kLift, sum);
 }
 
 template <int kDim, int NT>
@@ -369,7 +369,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
           const int tok = (s.r0 + r) / p.group;
           const int64_t at =
               int64_t(s.row + tok) * p.heads + s.head * p.group + s.r0 + r - tok * p.group;
-          const float inv = sum == 0.f ? 0.f : 1.f / sum;
+          const float inv = inverse_sum(sum);
           uint4* out = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + at * kDim +
                                                 g * (kDim / 8));
 #pragma unroll
@@ -379,7 +379,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
                                     pack_out(o[nt][i + 2][j] * inv, o[nt][i + 2][2 + j] * inv, p.bf16),
                                     pack_out(o[nt][i + 3][j] * inv, o[nt][i + 3][2 + j] * inv, p.bf16));
           if (p.lse && g == 0)
-            p.lse[at] = sum == 0.f ? -INFINITY : fmaf(m[nt][j] - kLift, kLn2, logf(sum));
+            p.lse[at] = log_sum(m[nt][j] - kLift, sum);
         } else {
           float4* to = reinterpret_cast<float4*>(part_o + r * kDim + g * (kDim / 8));
 #pragma unroll
@@ -536,12 +536,12 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
     }
   };
   Ahead now = {}, next = {}, later = {};
-  float now_bias = 0.f, now_inv = 0.f;  // log2 and inverse of now.vs
+  float now_bias = 0.f, now_inv = 0.f;  // log2 and inverse (in kSumUnit) of now.vs
   auto use = [&](const Ahead& a) {
     now = a;
     const float vs = used_scale(a.vs);
     now_bias = log2f(vs);
-    now_inv = 1.f / vs;
+    now_inv = kSumUnit / vs;
   };
   // The next slot of the ring: the keys (which = 0) or values of unit k of the plan, which
   // is in the batch `now` or the one after it.

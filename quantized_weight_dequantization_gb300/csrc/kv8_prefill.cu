@@ -98,7 +98,7 @@ struct PrefillSmem {
   static constexpr int kQ = 0;
   static constexpr int kK = 2 * kQTile;
   static constexpr int kV = kK + kSlots * kOperand;
-  static constexpr int kGran = kV + kSlots * kOperand;  // [slot][granule]{ks, log2 vs, 1 / vs, -}
+  static constexpr int kGran = kV + kSlots * kOperand;  // [slot][granule]{ks, log2 vs, kSumUnit / vs, -}
   // codes: [slot][K, V][pass][load thread], 16 bytes each; and {block, ks, vs} of granules
   static constexpr int kRawPass = kLoadThreads * 16;
   static constexpr int kRaw = kGran + kGranSlots * kGrans * 16;
@@ -188,7 +188,7 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
 
 // One pass over a row's 64 scores in TMEM (the next 32 loaded while 32 are used): weights
 // 2^x, x = c S + bias - from, packed in FP16 into w; l gets sum 2^x / vs; the largest x is
-// returned.  gran: the step's {ks, log2 vs, 1 / vs} of 16 keys each.  kMasked: only keys lo <=
+// returned.  gran: the step's {ks, log2 vs, kSumUnit / vs} of 16 keys each.  kMasked: only keys lo <=
 // key + i < hi are seen.
 template <bool kMasked>
 __device__ __forceinline__ float softmax_pass(uint32_t scores, uint32_t gran, float cq,
@@ -700,7 +700,7 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) dq4_kv8_prefill_kernel(con
         if (real) out[c] = make_uint4(f[0], f[1], f[2], f[3]);
       };
       auto put_lse = [&](float ref, float sum) {
-        if (real && p.lse) p.lse[at] = sum == 0.f ? -INFINITY : fmaf(ref, kLn2, logf(sum));
+        if (real && p.lse) p.lse[at] = log_sum(ref, sum);
       };
       const bool whole = was.a == 0 && count == was.x.steps[t];
       const int64_t slot_at = 2 * blockIdx.x + (was.item0 - kOpening <= v0 ? 0 : 1);
@@ -711,7 +711,7 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) dq4_kv8_prefill_kernel(con
         uint32_t o[32];
         tmem_ld32(t_o(t) + lanes + 32 * c, o);
         if (whole) {
-          const float inv = l == 0.f ? 0.f : 1.f / l;
+          const float inv = inverse_sum(l);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             float f[8];
@@ -750,7 +750,7 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) dq4_kv8_prefill_kernel(con
         const float2 st = __ldcg(stats_of(slot_of(c)));
         sum = fmaf(exp2_fast(st.x - ref), st.y, sum);
       }
-      const float inv = sum == 0.f ? 0.f : 1.f / sum;
+      const float inv = inverse_sum(sum);
 #pragma unroll 1
       for (int i = 0; i < kDim / 32; ++i) {
         float4 acc[8] = {};
@@ -914,7 +914,7 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) dq4_kv8_prefill_kernel(con
         const bool none = int(note.x) < 0;
         sts_v4(sbase + S::kGran + (g % kGranSlots * kGrans + lane) * 16, none ? 0 : note.y,
                __float_as_uint(none ? -INFINITY : __log2f(vs)),
-               __float_as_uint(none ? 0.f : __fdividef(1.f, vs)), 0);
+               __float_as_uint(none ? 0.f : __fdividef(kSumUnit, vs)), 0);
       }
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       mbar_arrive(k_full(slot));

@@ -118,3 +118,43 @@ def test_attend_codes_that_are_no_numbers_beside_scales_that_are(dq, dim, heads,
         close(host(out), want, tolerance(want, size, reach, "bf16"), ("out", hint))
         close(lse.cpu().numpy()[~seen], want_lse[~seen], 2.0 ** -18 * reach[~seen] + 2.0 ** -18,
               ("lse", hint))
+
+
+# ------------------------------------------------------------------ sums and weights
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("rise", [0.0, 8.5])
+@pytest.mark.parametrize("keys,new", [(20000, 40), (70000, 1)])
+def test_attend_many_keys_whose_values_are_zeros(dq, dim, rise, keys, new):
+    """All of V at the least scale; the keys after the first 64 score `rise` more: the sum is
+    n e^s whatever the scales are.  (Scores are exact, so that lse is good to 2^-18.)"""
+    page = 256
+    b = Batch(dq, [keys], 1, dim, page, seed=25)
+    b.fill()
+    for i in range(2):
+        b.codes[i] = np.where(np.isnan(b.codes[i]), np.nan, 0.0)
+    used = b.table[0, :-(-keys // page)]
+    b.codes[0][used, 0, :, 0] = np.where(np.isnan(b.codes[0][used, 0, :, 0]), np.nan, 1.0)
+    b.codes[0][b.table[0, 0], 0, :64, 0] = 0.0
+    b.scales[0][used], b.scales[1][used] = 1.0, 2.0 ** -100
+    for i, (t, s) in enumerate(((b.cache.k, b.cache.k_scale), (b.cache.v, b.cache.v_scale))):
+        t.copy_(dev(b.codes[i].astype(np.float32)).to(torch.float8_e4m3fn))
+        s.copy_(dev(b.scales[i]))
+    q = torch.zeros((new, 4, dim), dtype=torch.bfloat16, device="cuda")
+    q[:, :, 0] = rise
+    seen = np.arange(keys - new, keys) + 1
+    want = np.log(64 + (seen - 64) * np.exp(rise))[:, None].repeat(4, 1)
+    for hint, out, lse, bad in both(dq, b, q, [new], scale=1.0):
+        assert not bool(out.any()), hint
+        close(lse.cpu().numpy(), want, 2.0 ** -18 * rise + 2.0 ** -18 * np.abs(want), hint)
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("v_exp", [-100, 0, 110])
+def test_attend_values_at_the_ends_of_the_scales(dq, dim, v_exp):
+    """V at the least scale that append writes, and near the largest; BF16 holds the results."""
+    b = Batch(dq, [3000, 65], 2, dim, 64, seed=26)
+    b.fill()
+    b.scales[1] = np.where(np.isnan(b.scales[1]), np.nan, 2.0 ** v_exp).astype(np.float32)
+    b.cache.v_scale.copy_(dev(b.scales[1]))
+    check_attend(dq, b, [1, 1], 4, "bf16")
+    check_attend(dq, b, [130, 40], 4, "bf16")
