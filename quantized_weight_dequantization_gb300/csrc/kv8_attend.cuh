@@ -38,10 +38,10 @@ constexpr float kLn2 = 0.6931471805599453f;
 // to 2^-38 is not lost.
 constexpr float kLift = 14.f;
 
-// The sum l of the weights over the pages' V scales is held in units of 2^16.  A weight is at most
-// 2^15 and a scale 2^-100 to 2^120, so that 2^28 keys at the least scale stay below 2^128 (they
-// are log n in lse), and the largest weight of a row alone, 2^kLift or 2^kTileLift, above 2^-126
-// or little below it at the largest scale.
+// The sum l of the weights over the pages' V scales is held in units of 2^16.  A weight is below
+// 2^16 and a scale 2^-100 to 2^120, so that 2^27 keys at the least scale stay below 2^128 (they
+// are log n in lse), and the largest weight of a row alone, 2^14 (few rows) or 2^10 at least
+// (many), is 2^-126 or more at the largest scale.
 constexpr float kSumUnit = 1.f / 65536;
 constexpr float kLogSumUnit = 16 * kLn2;
 

@@ -20,9 +20,9 @@
 //  * warps 0..3 and 4..7: the softmax of tile 0 and 1, one thread a row, no shuffles.  They
 //    first bring a unit's query rows to FP16 in shared memory, and at its end write the
 //    result or the part.  m is the reference of a row, not always its maximum: it moves, and
-//    O and l with it, only when a score passes it by 2^kSlack.  So a step's weights are
-//    computed against the reference at hand in one pass over S, with the maximum found on
-//    the way, and kept in registers; only if some row has to move is S read again;
+//    O and l with it, only when a score passes it by 2^kSlack.  So one pass over S gives a
+//    step's weights: the maximum of 32 scores is looked at before their exponentials, and if
+//    some row has to move, the weights before them are scaled by a power of two;
 //  * warps 8..11: bring keys and values from the cache to FP16 in shared memory (codes are
 //    exact in FP16), their codes copied to shared memory some steps ahead, where each thread
 //    takes back what it asked for itself;
@@ -68,12 +68,13 @@ constexpr int kMaxCtas = 160;      // CTAs the workspace has room for
 constexpr int kOpening = 10;
 constexpr int kMinSteps = 16;      // steps that a CTA takes at least
 constexpr int kPlanThreads = 1024;
-// P <= 2^(kTileLift + kSlack) = 2^15 fits FP16.  A row's reference is set at its first keys, 2^2
-// for the largest of them; weights down to 2^-14 (2^-16 of it) have all their bits, smaller
-// ones a step of 2^-24.  The slack is what a row's maximum may grow by before its step is
-// computed again and O rescaled: with 2^7 and 2^8 a prompt of 8192 with one head of widely spread
-// scores takes 651 us, with 2^2 and 2^13 607 (both with kOpening 13).
-constexpr float kTileLift = 2.f, kSlack = 13.f;
+// P <= 2^(kTileLift + kSlack) < 65504 fits FP16.  A row's reference is set so that its largest
+// weight so far is 2^13 to 2^14: weights down to 2^-14, 2^-27 of the largest, have all their bits, smaller
+// ones a step of 2^-24.  (That shows where one key dominates that has no values.)  The slack is
+// what a row's maximum may grow by before the rows of its warp move.  A prompt of 8192, by its
+// data (two draws of one distribution), and chunks over 16k at dim 64: 578, 562 and 334 us.  With the moves found after the exponentials, which are then computed again, 681, 644 and
+// 380, and 583, 529 and 342 with 2^2 and 2^13, where small weights lose eleven bits.
+constexpr float kTileLift = 13.f, kSlack = 2.9f;
 
 // A unit, as planned.
 struct alignas(16) Unit {
@@ -186,50 +187,93 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   return r;
 }
 
+// A row's sums: weights are 2^(s - from) of its scores s in base 2.
+struct RowSum {
+  float from = 0.f;
+  float peak = -INFINITY;  // log2 of the largest weight so far
+  float l = 0.f;
+  bool fresh = true;       // no key seen yet
+};
+
 // One pass over a row's 64 scores in TMEM (the next 32 loaded while 32 are used): weights
-// 2^x, x = c S + bias - from, packed in FP16 into w; l gets sum 2^x / vs; the largest x is
-// returned.  gran: the step's {ks, log2 vs, kSumUnit / vs} of 16 keys each.  kMasked: only keys lo <=
-// key + i < hi are seen.
+// 2^x, x = c S + bias - from, packed in FP16 into w; l gets sum 2^x / vs.  gran: the step's {ks,
+// log2 vs, kSumUnit / vs} of 16 keys each.  kMasked: only keys lo <= key + i < hi are seen.
+// If some row's weights would grow past 2^(kTileLift + kSlack), all rows of the warp move their
+// references to their maxima, and what has been summed by powers of two: the 32 scores at hand
+// before their exponentials, the weights before them and l here, O by the caller (returns whether
+// they moved, and the factor in keep).
 template <bool kMasked>
-__device__ __forceinline__ float softmax_pass(uint32_t scores, uint32_t gran, float cq,
-                                              float from, int key, int lo, int hi, float& l,
-                                              uint32_t (&w)[kKeys / 2]) {
-  float top = -INFINITY;
-  uint32_t s[2][32];
+__device__ __forceinline__ bool softmax_pass(uint32_t scores, uint32_t gran, float cq, int key,
+                                             int lo, int hi, RowSum& r, float& keep,
+                                             uint32_t (&w)[kKeys / 2]) {
+  bool moved = false;
+  keep = 1.f;
+  uint32_t s[kKeys / 32][32];
   tmem_load(scores, s[0]);
 #pragma unroll
   for (int c = 0; c < kKeys / 32; ++c) {
     tmem_loaded();
-    if (c + 1 < kKeys / 32) tmem_load(scores + 32 * (c + 1), s[(c + 1) & 1]);
+    float x[32], inverse[2];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const uint4 gi = lds_v4(gran + (2 * c + h) * 16);
-      const float ck = cq * __uint_as_float(gi.x), add = __uint_as_float(gi.y) - from;
+      const float ck = cq * __uint_as_float(gi.x), add = __uint_as_float(gi.y) - r.from;
       const uint64_t ck2 = pair_of(ck, ck), off2 = pair_of(add, add);
+      inverse[h] = __uint_as_float(gi.z);
+#pragma unroll
+      for (int i = 16 * h; i < 16 * h + 16; i += 2) {
+        scale_pair(s[c][i], s[c][i + 1], ck2, off2, x[i], x[i + 1]);
+        if constexpr (kMasked) {
+          const int k = key + 32 * c + i;
+          if (k < lo || k >= hi) x[i] = -INFINITY;
+          if (k + 1 < lo || k + 1 >= hi) x[i + 1] = -INFINITY;
+        }
+        r.peak = fmaxf(fmaxf(x[i], x[i + 1]), r.peak);
+      }
+    }
+    if (__any_sync(kAllLanes, r.peak > (r.fresh ? -INFINITY : kTileLift + kSlack))) {
+      // (of a fresh row nothing has been summed, and its peak may be anything)
+      const float over = r.peak - kTileLift;
+      const float by = !r.fresh ? fmaxf(0.f, floorf(over)) : r.peak > -INFINITY ? over : 0.f;
+      const float factor = r.fresh ? 1.f : exp2_fast(-by);
+      r.from += by;
+      r.peak -= by;
+      r.l *= factor;
+      keep *= factor;
+      moved = true;
+#pragma unroll
+      for (int i = 0; i < 32; ++i) x[i] -= by;
+      // (in two factors, as FP16 holds no power below 2^-24)
+      const float most = fminf(by, 15.f);
+      const __half2 f1 = __float2half2_rn(r.fresh ? 1.f : exp2_fast(-most));
+      const __half2 f2 = __float2half2_rn(r.fresh ? 1.f : exp2_fast(most - by));
+#pragma unroll
+      for (int i = 0; i < 16 * c; ++i) {
+        __half2 v;
+        memcpy(&v, &w[i], 4);
+        v = __hmul2(__hmul2(v, f1), f2);
+        memcpy(&w[i], &v, 4);
+      }
+      r.fresh = r.fresh && !(r.peak > -INFINITY);
+    }
+    if (c + 1 < kKeys / 32) tmem_load(scores + 32 * (c + 1), s[c + 1]);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
       uint64_t sum2 = 0;
 #pragma unroll
-      for (int i = 0; i < 16; i += 2) {
-        float x, y;
-        scale_pair(s[c & 1][16 * h + i], s[c & 1][16 * h + i + 1], ck2, off2, x, y);
-        if constexpr (kMasked) {
-          const int k = key + 32 * c + 16 * h + i;
-          if (k < lo || k >= hi) x = -INFINITY;
-          if (k + 1 < lo || k + 1 >= hi) y = -INFINITY;
-        }
-        top = fmaxf(fmaxf(x, y), top);
-        x = exp2_fast(x);
-        y = exp2_fast(y);
-        sum2 = add2(sum2, pair_of(x, y));
-        w[16 * c + 8 * h + i / 2] = pack_f16(x, y);
+      for (int i = 16 * h; i < 16 * h + 16; i += 2) {
+        const float y = exp2_fast(x[i]), z = exp2_fast(x[i + 1]);
+        sum2 = add2(sum2, pair_of(y, z));
+        w[16 * c + i / 2] = pack_f16(y, z);
       }
-      float a, b;
-      split(sum2, a, b);
-      const float sum = a + b;
+      float y, z;
+      split(sum2, y, z);
+      const float sum = y + z;
       // an unseen granule's scale may be no number
-      if (!kMasked || sum != 0.f) l = fmaf(sum, __uint_as_float(gi.z), l);
+      if (!kMasked || sum != 0.f) r.l = fmaf(sum, inverse[h], r.l);
     }
   }
-  return top;
+  return moved;
 }
 
 // A step's V as FP16 at `values`: what is no number becomes zero, and the keys that had such are
@@ -625,9 +669,7 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) dq4_kv8_prefill_kernel(con
       const int pos = me.pos;
       const int lo = first_key(p, pos), hi = last_key(p, pos, x.held);
       const int all_lo = x.all_lo, all_hi = x.all_hi;
-      // from: what is taken off a row's exponents (the reference m less kTileLift)
-      float from = 0.f, l = 0.f;
-      bool fresh = true;  // no key seen yet
+      RowSum sum;
       for (int j = 0; j < count; ++j, ++step) {
         const int u = step & 1;
         ok = wait_warp(s_full(t, u), step >> 1);  // and with the scores, the step's scales
@@ -638,34 +680,23 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) dq4_kv8_prefill_kernel(con
         const int key = x.key0 + (sg.a + j) * kKeys;
         const bool masked = mixed_step(all_lo, all_hi, key);
         uint32_t wt[kKeys / 2];
-        float more = 0.f;
-        const float top = masked ? softmax_pass<true>(scores, gran, cq, from, key, lo, hi, more, wt)
-                                 : softmax_pass<false>(scores, gran, cq, from, key, lo, hi, more, wt);
-        const bool move = fresh ? top > -INFINITY : top > kTileLift + kSlack;
-        if (__any_sync(kAllLanes, move)) {
-          const float to = move ? from + top - kTileLift : from;
-          const float keep = fresh ? 0.f : exp2_fast(from - to);
-          from = to;
-          fresh = fresh && !move;
-          l *= keep;
-          if (j > 0) {
-            ok = wait_warp(o_done(t, u ^ 1), (step - 1) >> 1);
-            if (!ok) break;
-            asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-#pragma unroll 1
-            for (int c = 0; c < kDim / 32; ++c) {
-              uint32_t o[32];
-              tmem_ld32(t_o(t) + lanes + 32 * c, o);
-#pragma unroll
-              for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * keep);
-              tmem_st<32>(t_o(t) + lanes + 32 * c, o);
-            }
-          }
-          more = 0.f;
-          softmax_pass<true>(scores, gran, cq, from, key, lo, hi, more, wt);
-        }
-        l += more;
+        float keep;
+        const bool moved = masked ? softmax_pass<true>(scores, gran, cq, key, lo, hi, sum, keep, wt)
+                                  : softmax_pass<false>(scores, gran, cq, key, lo, hi, sum, keep, wt);
         tmem_st<32>(scores, wt);
+        if (moved && j > 0) {
+          ok = wait_warp(o_done(t, u ^ 1), (step - 1) >> 1);
+          if (!ok) break;
+          asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+#pragma unroll 1
+          for (int c = 0; c < kDim / 32; ++c) {
+            uint32_t o[32];
+            tmem_ld32(t_o(t) + lanes + 32 * c, o);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * keep);
+            tmem_st<32>(t_o(t) + lanes + 32 * c, o);
+          }
+        }
         asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
         asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
         mbar_arrive(p_full(t, u));
@@ -688,7 +719,7 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) dq4_kv8_prefill_kernel(con
       const uint32_t lost_at = sbase + S::kLost + 16 * t + 4 * (warp & 3);
       const uint32_t lost = lds_b32(lost_at);
       if (lost != 0) {
-        if (lost >> lane & 1) l = __uint_as_float(kNaN);
+        if (lost >> lane & 1) sum.l = __uint_as_float(kNaN);
         __syncwarp();
         if (lane == 0) sts_b32(lost_at, 0);
       }
@@ -699,8 +730,8 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) dq4_kv8_prefill_kernel(con
         for (int k = 0; k < 4; ++k) f[k] = pack_out(o[2 * k] * inv, o[2 * k + 1] * inv, p.bf16);
         if (real) out[c] = make_uint4(f[0], f[1], f[2], f[3]);
       };
-      auto put_lse = [&](float ref, float sum) {
-        if (real && p.lse) p.lse[at] = log_sum(ref, sum);
+      auto put_lse = [&](float ref, float l) {
+        if (real && p.lse) p.lse[at] = log_sum(ref, l);
       };
       const bool whole = was.a == 0 && count == was.x.steps[t];
       const int64_t slot_at = 2 * blockIdx.x + (was.item0 - kOpening <= v0 ? 0 : 1);
@@ -711,7 +742,7 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) dq4_kv8_prefill_kernel(con
         uint32_t o[32];
         tmem_ld32(t_o(t) + lanes + 32 * c, o);
         if (whole) {
-          const float inv = inverse_sum(l);
+          const float inv = inverse_sum(sum.l);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             float f[8];
@@ -728,10 +759,10 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) dq4_kv8_prefill_kernel(con
         }
       }
       if (whole) {
-        put_lse(from, l);
+        put_lse(sum.from, sum.l);
         continue;
       }
-      *stats_of(slot_at) = make_float2(fresh ? -INFINITY : from, l);
+      *stats_of(slot_at) = make_float2(sum.fresh ? -INFINITY : sum.from, sum.l);
       const int c0 = cta_of(was.item0), c1 = cta_of(was.item0 + was.x.steps[t] - 1);
       bar_tile(t);
       if (row == 0) {
@@ -743,14 +774,14 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) dq4_kv8_prefill_kernel(con
       if (!s_last[t]) continue;
       const int64_t slot0 = 2 * c0 + (was.item0 - kOpening <= begin_of(c0) ? 0 : 1);
       auto slot_of = [&](int c) { return c == c0 ? slot0 : int64_t(2 * c); };
-      float top = -INFINITY, sum = 0.f;
+      float top = -INFINITY, l = 0.f;
       for (int c = c0; c <= c1; ++c) top = fmaxf(top, __ldcg(stats_of(slot_of(c))).x);
       const float ref = top == -INFINITY ? 0.f : top;
       for (int c = c0; c <= c1; ++c) {
         const float2 st = __ldcg(stats_of(slot_of(c)));
-        sum = fmaf(exp2_fast(st.x - ref), st.y, sum);
+        l = fmaf(exp2_fast(st.x - ref), st.y, l);
       }
-      const float inv = inverse_sum(sum);
+      const float inv = inverse_sum(l);
 #pragma unroll 1
       for (int i = 0; i < kDim / 32; ++i) {
         float4 acc[8] = {};
@@ -773,7 +804,7 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) dq4_kv8_prefill_kernel(con
           put(4 * i + k, f, inv);
         }
       }
-      put_lse(ref, sum);
+      put_lse(ref, l);
     }
   } else if (warp < kIssueWarp) {
     // --------------------------------------------------- keys and values to FP16

@@ -158,3 +158,33 @@ def test_attend_values_at_the_ends_of_the_scales(dq, dim, v_exp):
     b.cache.v_scale.copy_(dev(b.scales[1]))
     check_attend(dq, b, [1, 1], 4, "bf16")
     check_attend(dq, b, [130, 40], 4, "bf16")
+
+
+@pytest.mark.parametrize("dim,heads", [(64, 4), (128, 32)])
+@pytest.mark.parametrize("above", [0, 3])
+def test_attend_values_beside_one_dominant_key_of_zeros(dq, dim, heads, above):
+    """The first key scores 12 to 17 nats above the others and has no values, so that the result
+    is what the small weights give (`above`: some later keys pass the first one by 1.5 nats, with
+    no values either).  The others' scores are equal: their roundings do not average out."""
+    n, page, kv = 700, 64, 2
+    b = Batch(dq, [n], kv, dim, page, seed=27)
+    b.fill()
+    for i in range(2):
+        b.codes[i] = np.where(np.isnan(b.codes[i]), np.nan, np.abs(b.codes[i]))
+    for t in b.table[0]:
+        b.scales[0][t], b.scales[1][t] = 1.0, 256.0
+        b.codes[0][t] = np.where(np.isnan(b.codes[0][t]), np.nan, 0.0)
+    for key, code in [(0, 1.0)] + [(100 + 70 * i, 1.125) for i in range(above)]:
+        b.codes[0][b.table[0, key // page], :, key % page, 0] = code
+        b.codes[1][b.table[0, key // page], :, key % page] = 0.0
+    for i, (t, s) in enumerate(((b.cache.k, b.cache.k_scale), (b.cache.v, b.cache.v_scale))):
+        t.copy_(dev(b.codes[i].astype(np.float32)).to(torch.float8_e4m3fn))
+        s.copy_(dev(b.scales[i]))
+    new = 150
+    q = np.zeros((new, heads, dim), np.float32)
+    q[:, :, 0] = np.linspace(12, 17, new * heads).reshape(new, heads)
+    q = dev(q, torch.float16)
+    want, want_lse, size, reach = definition(b, q, [new], 1.0)
+    for hint, out, lse, bad in both(dq, b, q, [new], scale=1.0):
+        close(host(out), want, tolerance(want, size, reach, "f16"), ("out", hint))
+        close(lse.cpu().numpy(), want_lse, 2.0 ** -18 * reach + 2.0 ** -18, ("lse", hint))
