@@ -55,7 +55,10 @@ constexpr int kGrans = kKeys / 16; // granules of 16 keys: never of two pages
 constexpr int kSlots = 3;          // steps of keys and of values in shared memory, as FP16
 constexpr int kRawSlots = 4;       // and of their codes
 // steps whose scales stay in shared memory: a step's are read until its weights are done, by
-// when the keys of no step past the fifth after it have been placed
+// when the keys of no step past the fifth after it have been placed.  (A slot of keys is free
+// again once both tiles have passed its step.  With steps of its own a tile passes none before
+// the weights of the second step before it; without, none past the second after its last step
+// before that one's weights: see `last`.)
 constexpr int kGranSlots = 8;
 constexpr int kLoadThreads = 128;
 constexpr int kPrefillThreads = kUnitRows + kLoadThreads + 128;
@@ -978,6 +981,7 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) dq4_kv8_prefill_kernel(con
     // phase ends with one arrival of each tile.
     auto nan_at = [&](int t, int g) { return sbase + S::kNan + (t * 4 + (g & 3)) * 16; };
     int g = 0, step = 0, units = 0;  // steps, this tile's steps, its units so far
+    int last = -kGranSlots;          // this tile's last step, among all
     bool ok = true;
     while (ok && next_segment(w, walk, sg)) {
       const int count = sg.e - sg.a;
@@ -989,7 +993,8 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) dq4_kv8_prefill_kernel(con
         const int slot = g % kSlots, phase = g / kSlots, u = step & 1;
         if (role < 2) {  // S = Q K^T, once the weights in its buffer have been used
           ok = wait_warp(k_full(slot), phase) &&
-               (j >= n || step < 2 || wait_warp(o_done(t, u), (step >> 1) - 1));
+               (j < n ? step < 2 || wait_warp(o_done(t, u), (step >> 1) - 1)
+                      : g - last != 3 || wait_warp(p_full(t, u ^ 1), (step - 1) >> 1));
           if (!ok) break;
           asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
           if (j < n) {
@@ -999,6 +1004,7 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) dq4_kv8_prefill_kernel(con
               mma_ss(t_s(t, u), q_desc + ((i / 4) * S::kQBlock + (i % 4) * 32) / 16,
                      k + ((i / 4) * S::kBlock + (i % 4) * 32) / 16, idesc_s, i > 0, leads);
             commit_if(s_full(t, u), leads);
+            last = g;
           }
           commit_if(k_empty(slot), leads);
         } else {  // O += P V

@@ -188,3 +188,24 @@ def test_attend_values_beside_one_dominant_key_of_zeros(dq, dim, heads, above):
     for hint, out, lse, bad in both(dq, b, q, [new], scale=1.0):
         close(host(out), want, tolerance(want, size, reach, "f16"), ("out", hint))
         close(lse.cpu().numpy(), want_lse, 2.0 ** -18 * reach + 2.0 ** -18, ("lse", hint))
+
+
+# ---------------------------------------------------------------- uneven sequences
+@pytest.mark.parametrize("dim,heads,kv", [(128, 4, 1), (64, 4, 2)])
+def test_attend_sequences_of_one_tile_after_sequences_of_two(dq, dim, heads, kv):
+    """Long chunks that many CTAs share, then prompts of two tiles and a step or two, then single
+    tokens, which have no rows in the second tile: it must not fall behind the first by more
+    steps than scales are kept for."""
+    lens, new = [], []
+    for i in range(6):
+        lens += [6000 + 300 * i, 40, 90] + [500 + 90 * i] * 4
+        new += [130, 40, 70] + [1] * 4
+    b = Batch(dq, lens, kv, dim, 64, seed=30)
+    b.fill()
+    first = check_attend(dq, b, new, heads, "bf16", max_new=MANY)
+    b.rng = np.random.default_rng(31)
+    state = b.rng.bit_generator.state
+    for _ in range(3):
+        b.rng.bit_generator.state = state
+        again = check_attend(dq, b, new, heads, "bf16", max_new=MANY)
+        assert torch.equal(again[0], again[2]) and len(first) == 3
