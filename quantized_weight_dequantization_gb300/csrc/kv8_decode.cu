@@ -575,12 +575,13 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
   };
   auto arrive = [&] {  // the next slot of the ring, once its copies are in
     const int slot = taken % kSlots;
-    if (!failed && !mbar_wait(bars + 8 * slot, uint32_t(taken / kSlots) & 1u)) failed = true;
+    // (for the warp as a whole: what follows a wait that ran out is collective)
+    failed = !__all_sync(kAllLanes, !failed && mbar_wait(bars + 8 * slot, uint32_t(taken / kSlots) & 1u));
     ++taken;
     return ring + slot * S::kSlot;
   };
 
-  while (plan_u < v1) {
+  while (plan_u < v1 && !failed) {
     unit0 = planned;
     plan();
     unit1 = planned;
