@@ -111,7 +111,7 @@ struct PrefillSmem {
   static constexpr int kNan = kNote + kRawSlots * kGrans * 16;
   static constexpr int kLost = kNan + 2 * 4 * 16;
   static constexpr int kBars = kLost + 2 * 16;
-  static constexpr int kBytes = kBars + 34 * 8 + 1024;  // + alignment slack
+  static constexpr int kBytes = kBars + 38 * 8 + 1024;  // + alignment slack
   static_assert(kBytes + 256 <= 227 * 1024, "shared memory budget");
 };
 
@@ -485,15 +485,6 @@ __device__ __noinline__ bool wait_longer(uint32_t bar, uint32_t parity) {
   return mbar_wait(bar, parity);
 }
 
-// The 128 threads of a tile's softmax.
-__device__ __forceinline__ void bar_tile(int t) {
-  if (t == 0) {
-    asm volatile("bar.sync 1, 128;" ::: "memory");
-  } else {
-    asm volatile("bar.sync 2, 128;" ::: "memory");
-  }
-}
-
 template <int kDim>
 __global__ void __launch_bounds__(kPrefillThreads, 1) dq4_kv8_prefill_kernel(const PrefillArgs w) {
   using S = PrefillSmem<kDim>;
@@ -501,7 +492,7 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) dq4_kv8_prefill_kernel(con
   extern __shared__ uint8_t smem_raw[];
   __shared__ uint32_t s_tmem;
   __shared__ volatile int s_abort;
-  __shared__ int s_last[2];
+  __shared__ volatile int s_last[2];
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
   const uint32_t sbase = smem_u32(base);
@@ -520,6 +511,9 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) dq4_kv8_prefill_kernel(con
   auto o_done = [&](int t, int u) { return bar0 + 8 * (24 + 2 * t + u); };
   auto q_full = [&](int t) { return bar0 + 8 * (28 + t); };
   auto all_done = [&](int i) { return bar0 + 8 * (30 + i); };
+  // tile t, where a unit is shared: its part is written; whether it was the last part is known
+  auto part_full = [&](int t) { return bar0 + 8 * (34 + t); };
+  auto last_full = [&](int t) { return bar0 + 8 * (36 + t); };
   if (tid < 8) sts_v4(sbase + S::kNan + 16 * tid, 0, 0, uint32_t(-1), 0);
   if (tid < 2) sts_v4(sbase + S::kLost + 16 * tid, 0, 0, 0, 0);
   if (tid == 0) {
@@ -539,6 +533,8 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) dq4_kv8_prefill_kernel(con
       mbar_init(q_full(t), kTileRows);
       mbar_init(all_done(t), 1);
       mbar_init(all_done(2 + t), 1);
+      mbar_init(part_full(t), kTileRows);
+      mbar_init(last_full(t), 1);
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -588,7 +584,8 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) dq4_kv8_prefill_kernel(con
     const int t = warp >> 2;
     const int row = tid & (kTileRows - 1);  // of the tile = its TMEM lane
     const uint32_t lanes = uint32_t((warp & 3) * 32) << 16;
-    int step = 0;  // the tile's steps so far: buffers and their phases
+    int step = 0;   // the tile's steps so far: buffers and their phases
+    int joins = 0;  // and its shared units
     bool ok = true;
     // A unit as this thread's row sees it.
     struct Row {
@@ -767,13 +764,16 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) dq4_kv8_prefill_kernel(con
       }
       *stats_of(slot_at) = make_float2(sum.fresh ? -INFINITY : sum.from, sum.l);
       const int c0 = cta_of(was.item0), c1 = cta_of(was.item0 + was.x.steps[t] - 1);
-      bar_tile(t);
-      if (row == 0) {
+      // (barriers whose waits have a limit, as any other of a thread may have run out)
+      mbar_arrive(part_full(t));
+      if (row == 0 && wait(part_full(t), joins)) {
         int* counter = w.count + 2 * c1 + t;
         s_last[t] = atomic_add_acq_rel(counter, 1) == c1 - c0;
         if (s_last[t]) *counter = 0;  // ready for the next call
+        mbar_arrive(last_full(t));
       }
-      bar_tile(t);
+      ok = wait_warp(last_full(t), joins++);
+      if (!ok) break;
       if (!s_last[t]) continue;
       const int64_t slot0 = 2 * c0 + (was.item0 - kOpening <= begin_of(c0) ? 0 : 1);
       auto slot_of = [&](int c) { return c == c0 ? slot0 : int64_t(2 * c); };
