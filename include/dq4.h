@@ -230,8 +230,9 @@ int dq4_int8_correction_prep(const uint16_t* A, const int8_t* CB, const float* S
  *                    (as many as fill the GPU and whose cols x ncols FP32
  *                    partial tiles fit the buffer); a second kernel then
  *                    adds the partial tiles in range order, so the result is
- *                    deterministic.  NULL or too small: one row range,
- *                    written straight to dst.
+ *                    deterministic.  Host threads that share a workspace
+ *                    make their calls one at a time.  NULL or too small: one
+ *                    row range, written straight to dst.
  *                    dq4_nested_out_prod_workspace_bytes gives the size that
  *                    fills the current device.
  *   bad              optional device int: incremented when a wait inside the

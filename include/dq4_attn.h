@@ -6,7 +6,9 @@
  *
  * Conventions are those of dq4.h: DEVICE pointers owned by the caller, no allocation and
  * no synchronization inside, work enqueued on `stream`, a status code returned (nothing is
- * enqueued on an error other than DQ4_ERR_LAUNCH), host threads may call concurrently.
+ * enqueued on an error other than DQ4_ERR_LAUNCH), host threads may call concurrently, but
+ * calls that share a workspace one at a time: dq4_kv8_attention may take two launches, which
+ * have to follow each other in the stream.
  * Element types are DQ4_OUT_F16 / DQ4_OUT_BF16 / DQ4_OUT_F32 (`dtype`).  Strides count
  * elements.  Sums, softmax statistics and norms are FP32.
  *

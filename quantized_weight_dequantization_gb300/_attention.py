@@ -15,7 +15,7 @@ from typing import Optional, Tuple
 
 import torch
 
-from ._binding import _DTYPE_CODE, Dq4Error, _check, _stream_handle, get_lib
+from ._binding import _DTYPE_CODE, Dq4Error, _call_lock, _check, _stream_handle, get_lib
 
 _HALF = (torch.float16, torch.bfloat16)
 PAGE_TOKENS = (16, 32, 64, 128, 256)
@@ -234,17 +234,19 @@ def qk_norm_rope_backward(dq_out: torch.Tensor, dk_out: Optional[torch.Tensor],
         dk_out_ptr = _flat(dk_out, "dk_out", q.dtype, k.numel(), q)
         dk = _output(dk, "dk", tuple(k.shape), q)
         dk_ptr = dk.data_ptr()
+    bad_ptr = _bad(bad, q)
     handle = _stream(stream, q.get_device())
     weights = (None, None, None, 0)
-    if q_weight is not None:
-        dqw = torch.empty(dim, dtype=torch.float32, device=q.device)
-        if k is not None:
-            dkw = torch.empty(dim, dtype=torch.float32, device=q.device)
-            dkw_ptr = dkw.data_ptr()
-        ws = _workspace(workspace, _norm_need(dim), "norm", q, handle)
-        weights = (dqw.data_ptr(), dkw_ptr, ws.data_ptr(), ws.numel())
-    st = _lib().dq4_qk_norm_rope_backward(dq_out_ptr, dk_out_ptr, *args, dq.data_ptr(), dk_ptr,
-                                          *weights, _bad(bad, q), handle)
+    with _call_lock(q.get_device(), handle):
+        if q_weight is not None:
+            dqw = torch.empty(dim, dtype=torch.float32, device=q.device)
+            if k is not None:
+                dkw = torch.empty(dim, dtype=torch.float32, device=q.device)
+                dkw_ptr = dkw.data_ptr()
+            ws = _workspace(workspace, _norm_need(dim), "norm", q, handle)
+            weights = (dqw.data_ptr(), dkw_ptr, ws.data_ptr(), ws.numel())
+        st = _lib().dq4_qk_norm_rope_backward(dq_out_ptr, dk_out_ptr, *args, dq.data_ptr(),
+                                              dk_ptr, *weights, bad_ptr, handle)
     if st:
         raise Dq4Error(st, "dq4_qk_norm_rope_backward")
     return dq, dk, dqw, dkw
@@ -382,15 +384,17 @@ def kv8_attention(cache: KV8Cache, q: torch.Tensor, block_table: torch.Tensor,
     if return_lse:
         lse = torch.empty((tokens, heads), dtype=torch.float32, device=q.device)
         lse_ptr = lse.data_ptr()
+    bad_ptr = _bad(bad, like)
     handle = _stream(stream, like.get_device())
     need = _attention_need(tokens, seqs, heads, cache.kv_heads, dim)
-    ws = _workspace(workspace, need, "attention", like, handle)
     qs = q.stride()
-    st = _lib().dq4_kv8_attention(
-        cache.ref, q.data_ptr(), qs[0], qs[1], _DTYPE_CODE[q.dtype], tokens, heads, table,
-        stride, width, lens, cu_ptr, seqs, max_new,
-        1 / math.sqrt(dim) if scale is None else scale, causal, window, out.data_ptr(), lse_ptr,
-        ws.data_ptr(), ws.numel(), _bad(bad, like), handle)
+    with _call_lock(like.get_device(), handle):
+        ws = _workspace(workspace, need, "attention", like, handle)
+        st = _lib().dq4_kv8_attention(
+            cache.ref, q.data_ptr(), qs[0], qs[1], _DTYPE_CODE[q.dtype], tokens, heads, table,
+            stride, width, lens, cu_ptr, seqs, max_new,
+            1 / math.sqrt(dim) if scale is None else scale, causal, window, out.data_ptr(),
+            lse_ptr, ws.data_ptr(), ws.numel(), bad_ptr, handle)
     if st:
         raise Dq4Error(st, "dq4_kv8_attention")
     return (out, lse) if return_lse else out

@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import threading
 from typing import Optional
 
 import torch
@@ -104,6 +105,21 @@ def __getattr__(name):
 # ------------------------------------------------------------- helpers
 def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
     return None if t is None else t.data_ptr()
+
+
+_CALL_LOCKS = {}
+
+
+def _call_lock(index: int, handle: int) -> threading.Lock:
+    """Held by a call from the choice of its workspace until all its work is in the stream.
+
+    Calls on one (device, stream) share the cached workspaces, and the stream's order keeps them
+    apart only if a call's launches stand together in it: ctypes releases the interpreter for
+    the C call, so that another thread's call could come between two launches.
+    """
+    key = (index, handle)
+    lock = _CALL_LOCKS.get(key)
+    return lock if lock is not None else _CALL_LOCKS.setdefault(key, threading.Lock())
 
 
 _WORKSPACES = {}
@@ -234,20 +250,21 @@ def dq4_nested_host(packed: torch.Tensor, scale_codes: torch.Tensor,
         out = torch.empty(n, dtype=out_dtype, pin_memory=True)
     _check_host(out, "out", out_dtype, n)
     handle = _stream_handle(stream, device)
-    if scratch is None:
-        need = int(get_lib().dq4_nested_host_scratch_bytes(n, blocksize, nested_blocksize,
-                                                          _DTYPE_CODE[out_dtype]))
-        key = (device.index, handle)
-        scratch = _SCRATCH.get(key)
-        if scratch is None or scratch.numel() < need:
-            scratch = torch.empty(max(need, 1), dtype=torch.uint8, device=device)
-            _SCRATCH[key] = scratch
-    elif scratch.device != device or scratch.dtype != torch.uint8:
+    if scratch is not None and (scratch.device != device or scratch.dtype != torch.uint8):
         raise ValueError("scratch must be a uint8 tensor on the device")
-    st = get_lib().dq4_nested_host(_ptr(packed), _ptr(scale_codes), _ptr(nested_absmax),
-                                   _ptr(scale_codebook), _ptr(value_codebook), float(offset), n,
-                                   blocksize, nested_blocksize, _DTYPE_CODE[out_dtype],
-                                   _ptr(out), _ptr(scratch), scratch.numel(), handle)
+    with _call_lock(device.index, handle):
+        if scratch is None:
+            need = int(get_lib().dq4_nested_host_scratch_bytes(n, blocksize, nested_blocksize,
+                                                              _DTYPE_CODE[out_dtype]))
+            key = (device.index, handle)
+            scratch = _SCRATCH.get(key)
+            if scratch is None or scratch.numel() < need:
+                scratch = torch.empty(max(need, 1), dtype=torch.uint8, device=device)
+                _SCRATCH[key] = scratch
+        st = get_lib().dq4_nested_host(_ptr(packed), _ptr(scale_codes), _ptr(nested_absmax),
+                                       _ptr(scale_codebook), _ptr(value_codebook), float(offset),
+                                       n, blocksize, nested_blocksize, _DTYPE_CODE[out_dtype],
+                                       _ptr(out), _ptr(scratch), scratch.numel(), handle)
     if st:
         raise Dq4Error(st, "dq4_nested_host")
     return out
@@ -469,15 +486,16 @@ def out_prod(packed: torch.Tensor, scale_codes: torch.Tensor, nested_absmax: tor
     if bad is not None:
         _check(bad, "bad", torch.int32, 1, device)
     handle = _stream_handle(stream, device)
-    if workspace is None:
-        workspace = _out_prod_workspace(rows, cols, ncols, device, handle)
-    elif workspace.numel() > 0:
+    if workspace is not None and workspace.numel() > 0:
         _check(workspace, "workspace", torch.float32, 1, device)
-    st = get_lib().dq4_nested_out_prod(
-        _ptr(packed), _ptr(scale_codes), _ptr(nested_absmax), _ptr(scale_codebook),
-        _ptr(value_codebook), float(offset), rows, cols, blocksize, nested_blocksize, _ptr(G),
-        ncols, _ptr(dst), _ptr(workspace) if workspace.numel() > 0 else None,
-        workspace.numel() * 4, _ptr(bad), handle)
+    with _call_lock(device.index, handle):
+        if workspace is None:
+            workspace = _out_prod_workspace(rows, cols, ncols, device, handle)
+        st = get_lib().dq4_nested_out_prod(
+            _ptr(packed), _ptr(scale_codes), _ptr(nested_absmax), _ptr(scale_codebook),
+            _ptr(value_codebook), float(offset), rows, cols, blocksize, nested_blocksize, _ptr(G),
+            ncols, _ptr(dst), _ptr(workspace) if workspace.numel() > 0 else None,
+            workspace.numel() * 4, _ptr(bad), handle)
     if st:
         raise Dq4Error(st, "dq4_nested_out_prod")
     return dst
@@ -523,17 +541,18 @@ def linear(X: torch.Tensor, packed: torch.Tensor, scale_codes: torch.Tensor,
     if bad is not None:
         _check(bad, "bad", torch.int32, 1, device)
     handle = _stream_handle(stream, device)
-    if workspace is None:
-        workspace = _linear_workspace(M, N, K, device, handle)
-    elif workspace.numel() > 0:
+    if workspace is not None and workspace.numel() > 0:
         if workspace.device != device or workspace.dtype != torch.uint8:
             raise ValueError("workspace must be a uint8 tensor on X's device")
-    st = get_lib().dq4_nested_linear(
-        _ptr(X), _DTYPE_CODE[X.dtype], _ptr(packed), _ptr(scale_codes), _ptr(nested_absmax),
-        _ptr(scale_codebook), _ptr(value_codebook), float(offset), M, N, K, blocksize,
-        nested_blocksize, _DTYPE_CODE[out_dtype], _ptr(Y),
-        _ptr(workspace) if workspace.numel() > 0 else None, workspace.numel(), _ptr(bad),
-        handle)
+    with _call_lock(device.index, handle):
+        if workspace is None:
+            workspace = _linear_workspace(M, N, K, device, handle)
+        st = get_lib().dq4_nested_linear(
+            _ptr(X), _DTYPE_CODE[X.dtype], _ptr(packed), _ptr(scale_codes), _ptr(nested_absmax),
+            _ptr(scale_codebook), _ptr(value_codebook), float(offset), M, N, K, blocksize,
+            nested_blocksize, _DTYPE_CODE[out_dtype], _ptr(Y),
+            _ptr(workspace) if workspace.numel() > 0 else None, workspace.numel(), _ptr(bad),
+            handle)
     if st:
         raise Dq4Error(st, "dq4_nested_linear")
     return Y
