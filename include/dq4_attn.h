@@ -64,8 +64,9 @@ int dq4_qk_norm_rope(const void* q, int64_t q_token_stride, int64_t q_head_strid
  *   dq, dk          contiguous, `dtype`, as q_out and k_out
  *   dq_weight, dk_weight  FP32[head_dim] (both NULL without weights, when dx = g)
  *   workspace       dq4_qk_norm_rope_backward_workspace_bytes(head_dim) bytes, 256-byte
- *                   aligned, zero-filled before its first use; a completed call leaves it
- *                   ready for the next in the same stream (not for concurrent calls).
+ *                   aligned, the first 256 zero before its first use; a completed call leaves
+ *                   it ready for the next in the same stream (not for concurrent calls or
+ *                   replays of captured ones).
  *                   Not used without weights.
  * The sums over tokens are taken in a fixed order: the same call gives the same bits.
  */
@@ -147,17 +148,17 @@ int dq4_kv8_append(const dq4_kv8_cache* cache, const void* k, int64_t k_token_st
  *                   kernel, and what the result means does not depend on it (its rounding
  *                   does)
  *   workspace       device memory, 256-byte aligned, of at least
- *                   dq4_kv8_attention_workspace_bytes bytes, zero-filled before its first
- *                   use; a completed call leaves it ready for later calls of any shape
- *                   that it is large enough for, in the same stream (not for concurrent
- *                   calls).
+ *                   dq4_kv8_attention_workspace_bytes bytes, the first 2048 zero before
+ *                   its first use; a completed call leaves it ready for later calls of any
+ *                   shape that it is large enough for, in the same stream (not for concurrent
+ *                   calls or replays of captured ones).
  * The result does not depend on the order in which the SMs work.  A key counts with its weight
  * times its page's V scale down to 2^-120 of the row's largest such product; below that it
  * counts as nothing, in lse too (V scales of one sequence would have to lie 2^100 apart).
  * pages * kv_heads: at most 2^31 - 1.  Keys past the table's
  * table_width pages, and pages with an id outside [0, pages), are not seen; bad is
  * incremented for each part of the work that met one, and for a wait that ran out (never
- * expected; the workspace must then be zero-filled again).  Pages that lie wholly before
+ * expected; the workspace must then be cleared again).  Pages that lie wholly before
  * the windows of all of the sequence's rows are not looked at: they may have been given
  * back, their ids and what they hold may be anything.
  * A NaN code or scale of K or V reaches the rows that see its key, and no others.  Of V, a

@@ -64,24 +64,38 @@ def _lib() -> ctypes.CDLL:
 # A call of few tokens is bound by the host, so the checks below first take the short way that a
 # valid argument passes, and look for what is wrong only if it does not.
 _WORKSPACES = {}
-_OUTGROWN = []  # captured graphs may still use them
+_COUNTERS = {"attention": 2048, "norm": 256}  # bytes that have to be zero at first, at the head
 
 
 def _workspace(workspace, need: int, what: str, like: torch.Tensor, handle) -> torch.Tensor:
-    """The caller's workspace, or the cached zero-filled one of (operator, device, stream), grown
-    to `need` bytes, and to twice its size at least, so that all outgrown ones together stay
-    below the one in use."""
+    """The caller's workspace, or the stream's (_stream_workspace).  Memory of the latter comes from
+    the stream that uses it."""
     if workspace is not None:
         _check(workspace, "workspace", torch.uint8, need, like.device)
         return workspace
-    key = (what, like.get_device(), handle)
+    index = like.get_device()
+    if handle == torch._C._cuda_getCurrentRawStream(index):
+        return _stream_workspace(need, what, like, index, handle)
+    stream = (torch.cuda.ExternalStream(handle, index) if handle else
+              torch.cuda.default_stream(index))
+    with torch.cuda.stream(stream):
+        return _stream_workspace(need, what, like, index, handle)
+
+
+def _stream_workspace(need: int, what: str, like: torch.Tensor, index: int, handle):
+    """The cached zero-filled workspace of (operator, device, current stream), grown to `need`
+    bytes, and to twice its size at least.  In a capture: one of the graph's own memory, whose
+    counters the graph itself clears, so that its replays share nothing with other calls."""
+    if torch._C._cuda_isCurrentStreamCapturing():
+        ws = torch.empty(need, dtype=torch.uint8, device=like.device)
+        ws[:_COUNTERS[what]].zero_()
+        return ws
+    key = (what, index, handle)
     ws = _WORKSPACES.get(key)
     if ws is None or ws.numel() < need:
         if ws is not None:
-            _OUTGROWN.append(ws)
             need = max(need, 2 * ws.numel())
         ws = torch.zeros(max(need, 1), dtype=torch.uint8, device=like.device)
-        torch.cuda.synchronize(like.device)  # zero-filled before any stream uses it
         _WORKSPACES[key] = ws
     return ws
 
@@ -221,7 +235,8 @@ def qk_norm_rope_backward(dq_out: torch.Tensor, dk_out: Optional[torch.Tensor],
     ``dq_out`` and ``dk_out`` are the outputs' gradients (contiguous, q's dtype); the weights'
     gradients are float32 (None without weights), summed in a fixed order.  ``workspace``
     (uint8, zero-filled before its first use) holds partial sums; by default a cached buffer
-    per (device, stream) is used.
+    per (device, stream) is used, and in ``torch.cuda.graph`` memory of the graph's own (a
+    workspace that is given belongs to one call or replay at a time).
     """
     args = _norm_args(q, k, q_weight, k_weight, cos, sin, positions, eps, interleaved)
     dim = q.shape[2]
@@ -366,7 +381,9 @@ def kv8_attention(cache: KV8Cache, q: torch.Tensor, block_table: torch.Tensor,
     (an estimate will do: it chooses the kernel; default 1, or the mean with ``cu``).  Returns
     ``out`` (tokens x heads x head_dim), or (out, lse) with the float32 log-sums.  A row that
     sees no key gets zeros and -inf.  ``workspace`` (uint8, zero-filled before its first use)
-    holds partial results; by default a cached buffer per (device, stream) is used.
+    holds partial results; by default a cached buffer per (device, stream) is used, and in
+    ``torch.cuda.graph`` memory of the graph's own, cleared in the graph (1.2 us a call).  A
+    workspace that is given belongs to one call, or replay of a captured one, at a time.
     """
     if q.dtype not in _HALF:
         raise TypeError("q must be float16 or bfloat16")

@@ -209,3 +209,66 @@ def test_attend_sequences_of_one_tile_after_sequences_of_two(dq, dim, heads, kv)
         b.rng.bit_generator.state = state
         again = check_attend(dq, b, new, heads, "bf16", max_new=MANY)
         assert torch.equal(again[0], again[2]) and len(first) == 3
+
+
+# --------------------------------------------------------------------- captured calls
+def captured(fn, stream=None):
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=stream):
+        out = fn()
+    return graph, out
+
+
+@pytest.mark.parametrize("hint", [1, MANY])
+def test_attend_and_norm_backward_captured_without_a_call_before(dq, hint):
+    """On the capture's own stream, which no call has used."""
+    b = Batch(dq, [700, 90], 2, 128, 64, seed=32)
+    b.fill()
+    q = dev(b.rng.standard_normal((60, 4, 128)).astype(np.float32), torch.bfloat16)
+    cu = dev(np.array([0, 30, 60], np.int32))
+    args = (b.cache, q, dev(b.table), dev(np.array(b.lens, np.int32)), cu, hint)
+    w = torch.ones(128, dtype=torch.bfloat16, device="cuda")
+    norm = (q, q, q, q, w, w)
+    want, grads = dq.kv8_attention(*args), dq.qk_norm_rope_backward(*norm)
+    side = torch.cuda.Stream()
+    for stream in (None, side):
+        graph, out = captured(lambda: (dq.kv8_attention(*args), dq.kv8_attention(*args),
+                                       *dq.qk_norm_rope_backward(*norm)), stream)
+        for _ in range(3):
+            for o in out:
+                o.zero_()
+            graph.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(out[0], want) and torch.equal(out[1], want)
+            assert all(torch.equal(x, y) for x, y in zip(out[2:], grads))
+
+
+@pytest.mark.parametrize("hint", [1, MANY])
+def test_captured_calls_share_no_workspace(dq, hint):
+    """Two graphs captured on one stream, replayed side by side with calls of other shapes."""
+    b = Batch(dq, [9000, 90, 4000], 2, 64, 64, seed=33)
+    b.fill()
+    table, lens = dev(b.table), dev(np.array(b.lens, np.int32))
+    w = torch.ones(64, dtype=torch.bfloat16, device="cuda")
+    calls = []
+    for new in (40, 25, 60):
+        q = dev(b.rng.standard_normal((3 * new, 4, 64)).astype(np.float32), torch.bfloat16)
+        cu = dev(np.arange(4, dtype=np.int32) * new)
+        calls.append(lambda q=q, cu=cu: (dq.kv8_attention(b.cache, q, table, lens, cu, hint),
+                                         *dq.qk_norm_rope_backward(q, q, q, q, w, w)))
+    want = [call() for call in calls]
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        calls[2]()  # the stream has a workspace of its own
+    torch.cuda.synchronize()
+    graphs = [captured(call, side) for call in calls[:2]]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(20):
+        for (graph, _), stream in zip(graphs, streams):
+            with torch.cuda.stream(stream):
+                graph.replay()
+        with torch.cuda.stream(side):
+            eager = calls[2]()
+        torch.cuda.synchronize()
+        for got, expected in zip([g[1] for g in graphs] + [eager], want):
+            assert all(torch.equal(x, y) for x, y in zip(got, expected))
