@@ -147,6 +147,9 @@ def _bad(bad, like) -> Optional[int]:
     return None if bad is None else _flat(bad, "bad", torch.int32, 1, like)
 
 
+_NO_ROWS = 256  # an address: empty tensors have none, and none means no rotation
+
+
 def _tables(cos, sin, like) -> Tuple[Optional[int], Optional[int], int, int]:
     """(cos, sin, rows, rotary) of the rotation's tables."""
     if cos is None and sin is None:
@@ -157,8 +160,10 @@ def _tables(cos, sin, like) -> Tuple[Optional[int], Optional[int], int, int]:
         raise ValueError(f"cos and sin must be positions x rotary / 2 and alike, got "
                          f"{tuple(cos.shape)} and {tuple(sin.shape)}")
     rows, half = cos.shape
-    return (_flat(cos, "cos", torch.float32, 0, like), _flat(sin, "sin", torch.float32, 0, like),
-            rows, 2 * half)
+    c, s = (_flat(t, n, torch.float32, 0, like) for t, n in ((cos, "cos"), (sin, "sin")))
+    if rows == 0 and half > 0:  # tables all the same, with no position in them: never followed
+        c = s = _NO_ROWS
+    return c, s, rows, 2 * half
 
 
 # ------------------------------------------------------------- norm and rotation

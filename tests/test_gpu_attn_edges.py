@@ -272,3 +272,31 @@ def test_captured_calls_share_no_workspace(dq, hint):
         torch.cuda.synchronize()
         for got, expected in zip([g[1] for g in graphs] + [eager], want):
             assert all(torch.equal(x, y) for x, y in zip(got, expected))
+
+
+# ---------------------------------------------------------------- ends of arguments
+@pytest.mark.parametrize("dim", [64, 72])
+def test_tables_without_rows_have_no_position(dq, dim):
+    """Tables of no rows are not "no tables": every position is outside them."""
+    x = torch.randn((3, 2, dim), device="cuda").bfloat16()
+    w = torch.ones(dim, dtype=torch.bfloat16, device="cuda")
+    t = torch.empty((0, dim // 2), device="cuda")
+    pos = torch.zeros(3, dtype=torch.int64, device="cuda")
+    bad = torch.zeros(1, dtype=torch.int32, device="cuda")
+    q, k = dq.qk_norm_rope(x, x, w, w, t, t, pos, bad=bad)
+    assert not bool(q.any()) and not bool(k.any()) and int(bad.item()) == 12
+    bad.zero_()
+    grads = dq.qk_norm_rope_backward(x, x, x, x, w, w, t, t, pos, bad=bad)
+    assert not any(bool(g.any()) for g in grads) and int(bad.item()) == 12
+
+
+def test_append_tables_without_rows_store_zeros(dq):
+    b = Batch(dq, [3], 2, 64, 16, seed=28)
+    x = torch.randn((3, 2, 64), device="cuda").bfloat16()
+    t = torch.empty((0, 32), device="cuda")
+    bad = torch.zeros(1, dtype=torch.int32, device="cuda")
+    dq.kv8_append(b.cache, x, x, dev(b.table), dev(np.array([3], np.int32)),
+                  dev(np.array([0, 3], np.int32)), t, t, bad=bad)
+    at = int(b.table[0, 0])
+    assert int(bad.item()) == 3 and not bool(b.cache.k[at, :, :3].float().any())
+    assert bool(b.cache.v[at, :, :3].float().any())
