@@ -20,6 +20,7 @@ from ._binding import _DTYPE_CODE, Dq4Error, _call_lock, _check, _stream_handle,
 _HALF = (torch.float16, torch.bfloat16)
 PAGE_TOKENS = (16, 32, 64, 128, 256)
 HEAD_DIMS = (64, 128)
+_INT_MAX = 2 ** 31 - 1
 
 
 class _Cache(ctypes.Structure):
@@ -401,6 +402,8 @@ def kv8_attention(cache: KV8Cache, q: torch.Tensor, block_table: torch.Tensor,
     table, stride, width, lens, cu_ptr, seqs = _batch(cache, tokens, block_table, seq_lens, cu)
     if max_new is None:
         max_new = 1 if cu is None else -(-tokens // max(seqs, 1))
+    # (the library takes 32 bits: no sequence is longer)
+    window, max_new = max(-1, min(window, _INT_MAX)), max(-1, min(max_new, _INT_MAX))
     out = _output(out, "out", (tokens, heads, dim), q)
     lse = lse_ptr = None
     if return_lse:

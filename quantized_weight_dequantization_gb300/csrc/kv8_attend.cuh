@@ -68,7 +68,7 @@ __device__ __forceinline__ int held_keys(const AttendArgs& p, int len) {
 
 // The keys [lo, hi) that a query at position pos sees.
 __device__ __forceinline__ int first_key(const AttendArgs& p, int pos) {
-  return p.window > 0 ? max(0, pos - p.window + 1) : 0;
+  return p.window > 0 && pos >= p.window ? pos - p.window + 1 : 0;
 }
 __device__ __forceinline__ int last_key(const AttendArgs& p, int pos, int held) {
   return p.causal ? min(held, pos + 1) : held;

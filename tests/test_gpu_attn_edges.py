@@ -300,3 +300,16 @@ def test_append_tables_without_rows_store_zeros(dq):
     at = int(b.table[0, 0])
     assert int(bad.item()) == 3 and not bool(b.cache.k[at, :, :3].float().any())
     assert bool(b.cache.v[at, :, :3].float().any())
+
+
+@pytest.mark.parametrize("window", [2 ** 31 - 1, 2 ** 31, 2 ** 32 + 5, sys.maxsize])
+def test_attend_windows_longer_than_any_sequence(dq, window):
+    b = Batch(dq, [300, 140, 3], 2, 64, 16, seed=29)
+    b.fill()
+    q = dev(b.rng.standard_normal((45, 4, 64)).astype(np.float32), torch.bfloat16)
+    cu = dev(np.array([0, 20, 40, 45], np.int32))  # (two rows lie before sequence 2's start)
+    args = (b.cache, q, dev(b.table), dev(np.array(b.lens, np.int32)), cu)
+    for hint in (1, MANY, 2 ** 31, 2 ** 40):
+        for causal in (True, False):
+            assert torch.equal(dq.kv8_attention(*args, hint, causal=causal, window=window),
+                               dq.kv8_attention(*args, hint, causal=causal))
