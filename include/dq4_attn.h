@@ -155,7 +155,7 @@ int dq4_kv8_append(const dq4_kv8_cache* cache, const void* k, int64_t k_token_st
  * The result does not depend on the order in which the SMs work.  A key counts with its weight
  * times its page's V scale down to 2^-120 of the row's largest such product; below that it
  * counts as nothing, in lse too (V scales of one sequence would have to lie 2^100 apart).
- * pages * kv_heads: at most 2^31 - 1.  Keys past the table's
+ * pages * kv_heads and tokens * heads / kv_heads: at most 2^31 - 1.  Keys past the table's
  * table_width pages, and pages with an id outside [0, pages), are not seen; bad is
  * incremented for each part of the work that met one, and for a wait that ran out (never
  * expected; the workspace must then be cleared again).  Pages that lie wholly before

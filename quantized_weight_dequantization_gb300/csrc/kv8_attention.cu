@@ -49,7 +49,10 @@ int dq4_kv8_attention(const dq4_kv8_cache* cache, const void* q, int64_t q_token
   if (heads < 1 || heads > 65535 || heads % cache->kv_heads != 0) return DQ4_ERR_HEADS;
   p.s = {block_table, table_stride, table_width, seq_lens, cu, seqs, tokens};
   if (const int st = check_batch(p.s)) return st;
-  if (window < 0 || max_new < 0 || cache->pages * cache->kv_heads > INT32_MAX) return DQ4_ERR_N;
+  // (query rows of a kv head, and blocks of the cache, are counted in 32 bits)
+  if (window < 0 || max_new < 0 || cache->pages * cache->kv_heads > INT32_MAX ||
+      tokens * (heads / cache->kv_heads) > INT32_MAX)
+    return DQ4_ERR_N;
   if (tokens == 0 || seqs == 0) return DQ4_OK;
   if (!q || !out) return DQ4_ERR_NULL;
   if (misaligned(q, 16) || misaligned(out, 16) || q_token_stride % 8 || q_head_stride % 8 ||
