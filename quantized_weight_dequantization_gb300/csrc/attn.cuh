@@ -27,6 +27,25 @@ __device__ __forceinline__ T load_global(const T* p) {
   return *p;
 }
 
+// Loads from L2 of what other CTAs of the same kernel have written, in order after the atomic
+// that says so.
+__device__ __forceinline__ float load_l2(const float* p) {
+  float f;
+  asm volatile("ld.global.cg.f32 %0, [%1];" : "=f"(f) : "l"(p) : "memory");
+  return f;
+}
+__device__ __forceinline__ float2 load_l2(const float2* p) {
+  float2 f;
+  asm volatile("ld.global.cg.v2.f32 {%0, %1}, [%2];" : "=f"(f.x), "=f"(f.y) : "l"(p) : "memory");
+  return f;
+}
+__device__ __forceinline__ float4 load_l2(const float4* p) {
+  float4 f;
+  asm volatile("ld.global.cg.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(f.x), "=f"(f.y), "=f"(f.z), "=f"(f.w) : "l"(p) : "memory");
+  return f;
+}
+
 // ------------------------------------------------------------------ element types
 template <int DT>
 struct Elem;
@@ -63,10 +82,19 @@ __device__ __forceinline__ Raw<DT, V> load_group(const typename Elem<DT>::T* p) 
   return {load_global(reinterpret_cast<const decltype(Raw<DT, V>::u)*>(p))};
 }
 
-// The same for what is read, or written, once: it leaves the caches first.
+// The same for what is read, or written, once: it leaves the caches first.  (Volatile and with
+// a memory clobber: this load, too, keeps its place after wait_for_stream.)
 template <int DT, int V>
 __device__ __forceinline__ Raw<DT, V> load_group_once(const typename Elem<DT>::T* p) {
-  return {__ldcs(reinterpret_cast<const decltype(Raw<DT, V>::u)*>(p))};
+  Raw<DT, V> r;
+  if constexpr (sizeof(r.u) == 8) {
+    asm volatile("ld.global.cs.v2.b32 {%0, %1}, [%2];"
+                 : "=r"(r.u.x), "=r"(r.u.y) : "l"(p) : "memory");
+  } else {
+    asm volatile("ld.global.cs.v4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r.u.x), "=r"(r.u.y), "=r"(r.u.z), "=r"(r.u.w) : "l"(p) : "memory");
+  }
+  return r;
 }
 
 // A lane's two groups in FP32: values 0 .. V - 1 are group a of lane_place, the others b.

@@ -778,10 +778,10 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) dq4_kv8_prefill_kernel(con
       const int64_t slot0 = 2 * c0 + (was.item0 - kOpening <= begin_of(c0) ? 0 : 1);
       auto slot_of = [&](int c) { return c == c0 ? slot0 : int64_t(2 * c); };
       float top = -INFINITY, l = 0.f;
-      for (int c = c0; c <= c1; ++c) top = fmaxf(top, __ldcg(stats_of(slot_of(c))).x);
+      for (int c = c0; c <= c1; ++c) top = fmaxf(top, load_l2(stats_of(slot_of(c))).x);
       const float ref = top == -INFINITY ? 0.f : top;
       for (int c = c0; c <= c1; ++c) {
-        const float2 st = __ldcg(stats_of(slot_of(c)));
+        const float2 st = load_l2(stats_of(slot_of(c)));
         l = fmaf(exp2_fast(st.x - ref), st.y, l);
       }
       const float inv = inverse_sum(l);
@@ -789,11 +789,11 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) dq4_kv8_prefill_kernel(con
       for (int i = 0; i < kDim / 32; ++i) {
         float4 acc[8] = {};
         for (int c = c0; c <= c1; ++c) {
-          const float f = exp2_fast(__ldcg(stats_of(slot_of(c))).x - ref);
+          const float f = exp2_fast(load_l2(stats_of(slot_of(c))).x - ref);
           const float4* src = part_of(slot_of(c)) + 8 * i * kTileRows;
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
-            const float4 y = __ldcg(src + k * kTileRows);
+            const float4 y = load_l2(src + k * kTileRows);
             acc[k].x = fmaf(f, y.x, acc[k].x);
             acc[k].y = fmaf(f, y.y, acc[k].y);
             acc[k].z = fmaf(f, y.z, acc[k].z);

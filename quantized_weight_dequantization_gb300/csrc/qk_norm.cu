@@ -179,7 +179,7 @@ __device__ __forceinline__ float sum_rows(const float* src, int n, int cols) {
   for (int c0 = 0; c0 < n; c0 += kAhead) {
     float v[kAhead];
 #pragma unroll
-    for (int k = 0; k < kAhead; ++k) v[k] = c0 + k < n ? __ldcg(src + int64_t(c0 + k) * cols) : 0.f;
+    for (int k = 0; k < kAhead; ++k) v[k] = c0 + k < n ? load_l2(src + int64_t(c0 + k) * cols) : 0.f;
 #pragma unroll
     for (int k = 0; k < kAhead; ++k) s += v[k];
   }
