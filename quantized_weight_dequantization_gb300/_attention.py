@@ -293,6 +293,8 @@ class KV8Cache:
             raise ValueError(f"k: must be pages x kv_heads x page x head_dim, got "
                              f"{tuple(k.shape)}")
         pages, heads, page, dim = k.shape
+        if heads < 1:
+            raise ValueError("k: the cache needs one kv head at least")
         if page not in PAGE_TOKENS:
             raise ValueError(f"k: a page holds {PAGE_TOKENS} tokens, got {page}")
         if dim not in HEAD_DIMS:

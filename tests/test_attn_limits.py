@@ -1,7 +1,10 @@
-"""Sizes that the attention's kernels count in 32 bits are refused past them, on the host."""
+"""Sizes at their ends, without a GPU: what the attention's kernels count in 32 bits is refused
+past them, and a cache has heads."""
 
 import pytest
+import torch
 
+from quantized_weight_dequantization_gb300 import KV8Cache
 from tests.test_attn_abi import P, _cache, lib  # noqa: F401
 
 
@@ -17,3 +20,10 @@ def test_blocks_of_the_cache(lib):  # noqa: F811
     status = lib.dq4_kv8_attention(_cache(pages=1 << 30, kv_heads=2), P, 256, 64, 1, 5, 4, P, 3, 3,
                                    P, P, 2, 4, 0.1, 1, 0, P, None, P, 1 << 62, None, None)
     assert status == 2
+
+
+def test_cache_without_heads():
+    codes = torch.zeros((4, 0, 16, 64), dtype=torch.float8_e4m3fn)
+    scales = torch.zeros((4, 0))
+    with pytest.raises(ValueError, match="one kv head"):
+        KV8Cache(codes, codes, scales, scales)
