@@ -17,8 +17,9 @@
  * (table_rows x rotary / 2, row-major):
  *   interleaved == 0: values i and i + rotary / 2 are a pair;
  *   interleaved != 0: values 2 i and 2 i + 1 are a pair;
- *   (a, b) -> (RN32(a c) - RN32(b s), RN32(b c) + RN32(a s)), each rounded to FP32.
- * The other values pass.  cos == sin == NULL: no rotation.
+ *   (a, b) -> (a c - b s, b c + a s) in FP32, every product and sum rounded on its own, but
+ *   for dq4_qk_norm_rope with weights, which may multiply a value's factors in another order.
+ * The other values pass.  cos == sin == NULL: no rotation (tables of no rows are tables).
  *
  * `bad` is an optional device int (NULL to skip) that counts what a call could not do,
  * as each entry point says; it stays 0 for valid inputs.
@@ -152,9 +153,11 @@ int dq4_kv8_append(const dq4_kv8_cache* cache, const void* k, int64_t k_token_st
  *                   its first use; a completed call leaves it ready for later calls of any
  *                   shape that it is large enough for, in the same stream (not for concurrent
  *                   calls or replays of captured ones).
- * The result does not depend on the order in which the SMs work.  A key counts with its weight
- * times its page's V scale down to 2^-120 of the row's largest such product; below that it
- * counts as nothing, in lse too (V scales of one sequence would have to lie 2^100 apart).
+ * The result does not depend on the order in which the SMs work.  Weights e_j times their pages'
+ * V scales are FP16 in the product with V: relative to the row's largest, one has all its 11
+ * bits down to 2^-27, a fixed step of 2^-37 below, and is nothing below 2^-38.  lse and the
+ * sum in out's denominator take them in FP32, down to 2^-138 of the largest (what is less would
+ * matter only with V scales of one sequence 2^100 apart).
  * pages * kv_heads and tokens * heads / kv_heads: at most 2^31 - 1.  Keys past the table's
  * table_width pages, and pages with an id outside [0, pages), are not seen; bad is
  * incremented for each part of the work that met one, and for a wait that ran out (never

@@ -34,7 +34,7 @@ constexpr float kMinScale = 7.888609052210118e-31f;  // 2^-100, the least scale 
 constexpr float kLn2 = 0.6931471805599453f;
 
 // Weights are 2^(s - m + kLift): the largest sits near the top of FP16's range (V's codes are
-// summed in FP32), so that a weight 2^-24 of the largest still has all its bits and one down
+// summed in FP32), so that a weight 2^-28 of the largest still has all its bits and one down
 // to 2^-38 is not lost.
 constexpr float kLift = 14.f;
 
@@ -119,7 +119,8 @@ __device__ __forceinline__ uint64_t seen_keys(int key, int lo, int hi) {
 constexpr uint32_t kNaN = 0x7FC00000u;
 
 // The power of two that brings a row's largest magnitude into [2^14, 2^15), and its inverse.
-// FP16 then holds a BF16 or FP16 row as it is, but for values below 2^-38 of its largest.
+// FP16 then holds a BF16 row as it is down to 2^-31 of its largest, an FP16 row down to 2^-28;
+// smaller values are rounded to 2^-38 of it, below what the FP32 sum of the products holds.
 // A row with an infinity or a NaN gets a NaN inverse.
 __device__ __forceinline__ void row_scaling(float top, float& up, float& down) {
   const int e = int(__float_as_uint(top) >> 23);  // biased; 0 also for subnormal rows

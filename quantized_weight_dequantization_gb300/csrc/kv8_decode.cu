@@ -18,7 +18,7 @@
 //   S^T (keys x rows)  = K (keys x dim) Q^T      codes of K as FP16, exact
 //   P   = 2^(c S + log2 vs - m + kLift)          c: softmax scale, page scale and row scale
 //   O^T (dim x rows)  += V^T (dim x keys) P^T
-//   l  += P / vs
+//   l  += P / vs   (in units of 2^16)
 // The page's V scale vs enters the exponent, so that P V needs no scaled V and the weights
 // keep their precision whatever the scales are; l takes it out again.  Keys on the M side
 // leave the N side of 8 to the few query rows.  The order of dim inside K Q^T, and of dim
@@ -27,7 +27,7 @@
 //
 // Measured (kv heads of 128): 64 sequences of 100 .. 8192 keys, 4 rows a head, 101 us (541 MB,
 // 5.3 TB/s; the loop itself runs at 7, the rest is the start, the joins and SMs that end 20 us
-// apart on equal work); 2 sequences of up to 131071 keys, 8 rows, 85 us (465 MB, 5.4 TB/s).
+// apart on equal work); 2 sequences of up to 131071 keys, 8 rows, 86 to 87 us (465 MB, 5.4 TB/s).
 // Short calls are a chain of latencies: one sequence of 777 keys takes 12 us, 2 of them to find
 // the work, 2 to the first keys, 4 in the loop and the rest in the joins and the launch.
 #include "kv8_attend.cuh"
@@ -719,6 +719,8 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
       const uint32_t values = arrive();
       // A weight of 0 does not keep a value that is no number from its row.  So where some row
       // does not see a key, such codes become zeros, and l brings them to the rows that do.
+      // (24 sequences x 5 tokens under a window: 22.3 -> 23.2 us.  Looked for on the way into the
+      // product instead, 22.3, but 8 x 128 tokens over 10000 keys take 1302 us for 1223.)
       if (!all && (key < all_lo || min(key + kTile, seg_of[seg].held) > all_hi)) {
         auto piece = [&](int row, int i) {
           return values + row * kDim + (i ^ (lane & (kDim / 16 - 1))) * 16;

@@ -7,7 +7,7 @@
 //   S = Q K^T    (128 x 64 a tile, tcgen05, FP16 operands from shared memory, FP32 in TMEM)
 //   P = 2^(c S + log2 vs - m + kTileLift)  FP16, written over S in TMEM
 //   O += P V     (A operand P from TMEM, B operand V from shared memory, FP32 in TMEM)
-//   l += P / vs
+//   l += P / vs   (in units of 2^16)
 // with c the softmax scale times the row's and the key page's scale, and vs the page's V
 // scale, which enters the exponent so that V's codes are the operand as they are.
 //
@@ -33,16 +33,16 @@
 // works on this one, and P V of this one while it works on the next.
 // Q, K and V are held K-major / MN-major with 128-byte swizzle: rows of 64 values.
 //
-// Measured: a causal prompt of 8192 tokens, 32 heads over 8 of 128, BF16, 528 to 562 us by its
-// data (550 GFLOP, 1.0 PFLOP/s, 0.53 of a library GEMM's rate), 627 where one head's scores spread
-// so widely that its rows move often; 5 chunks of up to 1025 tokens over up to 16411 keys,
-// 16 heads over 8 of 64, 340 us (186 GFLOP, 546 TFLOP/s; at 64 a key takes as many exponentials
-// and scores for half the operations).  A step takes about 2000 cycles for 1300 of the tensor
+// Measured: a causal prompt of 8192 tokens, 32 heads over 8 of 128, BF16, 564 to 576 us by its
+// data (550 GFLOP, 0.96 PFLOP/s, 0.51 of a library GEMM's rate); 5 chunks of up to 1025 tokens
+// over up to 16411 keys, 16 heads over 8 of 64, 340 us (186 GFLOP, 548 TFLOP/s; at 64 a key takes
+// as many exponentials and scores for half the operations).  A step takes about 2000 cycles for 1300 of the tensor
 // cores': the conversion of the codes, and roles that share the issue slots (half of them busy)
 // and the instruction caches; starting and ending a unit takes about nine steps more.  Dropped
 // after measuring: one thread that issues all products, the softmax tiles taking turns, codes by
 // TMA (each within 5 %), the next unit's query rows prefetched to L2 (605 us for 607), issue code
-// with all operands static (1954 us: it no longer fits the instruction caches).
+// with all operands static (1954 us: it no longer fits the instruction caches).  Times of
+// dropped forms are those of their day, to be compared with each other.
 #include "kv8_attend.cuh"
 
 namespace dq4d {
@@ -66,8 +66,8 @@ constexpr int kLoadWarp = kUnitRows / 32;
 constexpr int kIssueWarp = kLoadWarp + kLoadThreads / 32;
 constexpr int kMaxCtas = 160;      // CTAs the workspace has room for
 // What starting and ending a unit counts for in the division of the work, in steps: about 9 by
-// the cycles of most runs, more where rows move often.  A prompt of 8192 takes 536 to 560 us
-// with 13, 528 to 562 with 10 and 520 to 571 with 8, by its data, one of 2048 78, 75 and 74.
+// the cycles of most runs.  When it was chosen, a prompt of 8192 took 536 to 560 us with 13, 528 to
+// 562 with 10 and 520 to 571 with 8, by its data, one of 2048 78, 75 and 74.
 constexpr int kOpening = 10;
 constexpr int kMinSteps = 16;      // steps that a CTA takes at least
 constexpr int kPlanThreads = 1024;
@@ -403,7 +403,9 @@ __global__ void __launch_bounds__(kPlanThreads) dq4_kv8_plan_kernel(const Prefil
 
 // A step of a unit is mixed if some row does not see one of its keys.  A weight of 0 does not
 // keep a value that is no number from its row, so in such steps V's codes that are none become
-// zeros before the product, and l brings them to the rows that see their keys.
+// zeros before the product, and l brings them to the rows that see their keys.  (By the warps
+// that issue P V, which have the time: a prompt of 8192 takes 531 -> 544 us.  By those that bring
+// the values, or by the softmax, 550 to 573.)
 __device__ __forceinline__ bool mixed_step(int all_lo, int all_hi, int key) {
   return key < all_lo || key + kKeys > all_hi;
 }

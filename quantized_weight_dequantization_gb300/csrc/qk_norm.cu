@@ -6,8 +6,8 @@
 // Backward, with g = R(-p) dy (R is orthogonal, so its transpose is R(-p)), xh = x r:
 //   dx = r (g w - xh mean(g w xh)),   dw = sum over tokens and heads of g xh
 // Both read every value once and write every result once.  Measured, 32 + 8 heads of 128, BF16:
-// forward 8191 tokens 31 us (172 MB, 5.5 TB/s), backward 16384 tokens 101 us (512 MB, 5.0 TB/s),
-// against 6.8 TB/s of a copy; 4 tokens take 1.7 us.  What holds them back from the copy is the
+// forward 8191 tokens 31 us (172 MB, 5.5 TB/s), backward 16384 tokens 103 us (512 MB, 5.0 TB/s),
+// against 6.8 TB/s of a copy; 4 tokens take 1.8 us.  What holds them back from the copy is the
 // instructions of 8 values a lane and the latency of a warp's chain (position, tables, rows, the
 // sums over the lanes) at the occupancy that the rows in registers allow.  Tried and slower: 16
 // values a lane (fewer instructions, fewer warps: 40 us and 110 us), rows through shared memory
