@@ -1,8 +1,8 @@
 """Fused nested 4-bit weight dequantization for NVIDIA GB300 (sm_103a).
 
 The computation lives in the CUDA library ``libdq4.so`` (C ABI in
-``include/dq4.h`` and, for the attention around the 4-bit projections,
-``include/dq4_attn.h``); this package is its thin Python binding.  The first use
+``include/dq4.h``; for the attention around the 4-bit projections
+``include/dq4_attn.h``, for layers with 8-bit weights ``include/dq4_int8.h``); this package is its thin Python binding.  The first use
 of the library raises ImportError if it has not been built (see ``build``):
 there is no CPU fallback.
 """
@@ -31,6 +31,13 @@ from ._binding import (  # noqa: F401
     out_prod,
     sizes,
 )
+from ._int8 import (  # noqa: F401
+    Int8Rows,
+    int8_linear,
+    int8_linear_backward,
+    int8_moe,
+    int8_quantize,
+)
 
 
 def __getattr__(name):
@@ -42,4 +49,5 @@ def __getattr__(name):
 __all__ = ["dq4_nested", "dq4_nested_host", "dq4_nested_transposed", "dq4",
            "dq4_nested_unfused", "dq4_nested_unfused_static", "Dq4Error", "get_lib", "sizes",
            "int8_correction_prep", "out_prod", "linear", "OUT_F16", "OUT_BF16", "OUT_F32",
-           "KV8Cache", "kv8_append", "kv8_attention", "qk_norm_rope", "qk_norm_rope_backward"]
+           "KV8Cache", "kv8_append", "kv8_attention", "qk_norm_rope", "qk_norm_rope_backward",
+           "Int8Rows", "int8_quantize", "int8_linear", "int8_linear_backward", "int8_moe"]

@@ -1,0 +1,323 @@
+"""ctypes binding of include/dq4_int8.h: argument marshalling only, as in _binding.
+
+Layers with 8-bit weights: the row quantizer of LLM.int8 with its outlier columns, the 8-bit
+product, the gradient of its input, and a mixture-of-experts layer for few tokens.  Everything is
+asynchronous on ``stream`` (default: the current one): nothing here waits for the GPU.
+"""
+
+from __future__ import annotations
+
+import ctypes
+import functools
+from typing import NamedTuple, Optional
+
+import torch
+
+from ._attention import _COUNTERS, _HALF, _bad, _flat, _stream, _workspace
+from ._binding import _DTYPE_CODE, Dq4Error, _call_lock, get_lib
+
+# bytes of a new workspace that have to be zero (None: all of them)
+_COUNTERS.update({"int8 quantize": None, "int8 linear": 4096, "int8 backward": 4096,
+                  "int8 moe": 4096})
+
+_LIB = None
+
+
+def _lib() -> ctypes.CDLL:
+    global _LIB
+    if _LIB is None:
+        L = get_lib()
+        p, i64, i32, f32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_float
+        L.dq4_int8_quantize.argtypes = [p, i64, i32, i64, i64, f32, p, p, p, i32, p, p, p, i64, p]
+        L.dq4_int8_quantize.restype = ctypes.c_int
+        L.dq4_int8_quantize_workspace_bytes.argtypes = [i64]
+        L.dq4_int8_quantize_workspace_bytes.restype = i64
+        L.dq4_int8_linear.argtypes = [p, p, p, p, i64, i64, i64, p, i32, p, i32, p, i32, p, p, i64,
+                                      p, p]
+        L.dq4_int8_linear.restype = ctypes.c_int
+        L.dq4_int8_linear_workspace_bytes.argtypes = [i64, i64, i64, i32]
+        L.dq4_int8_linear_workspace_bytes.restype = i64
+        L.dq4_int8_linear_backward.argtypes = [p, i32, p, p, i64, i64, i64, p, p, i64, p, p]
+        L.dq4_int8_linear_backward.restype = ctypes.c_int
+        L.dq4_int8_linear_backward_workspace_bytes.argtypes = [i64, i64, i64]
+        L.dq4_int8_linear_backward_workspace_bytes.restype = i64
+        L.dq4_int8_moe.argtypes = [p, i64, i32, i64, i64, i64, i64, p, i32, i32, p, p, p, p, p, p,
+                                   p, p, i64, p]
+        L.dq4_int8_moe.restype = ctypes.c_int
+        L.dq4_int8_moe_workspace_bytes.argtypes = [i64, i64, i64, i32]
+        L.dq4_int8_moe_workspace_bytes.restype = i64
+        _LIB = L
+    return _LIB
+
+
+# Workspace sizes depend on shapes (and, for the products, the device's SMs) alone; a device that
+# could not be asked (a negative answer) is not remembered.
+@functools.lru_cache(maxsize=256)
+def _need_of(index: int, name: str, *shape) -> int:
+    with torch.cuda.device(index):
+        need = getattr(_lib(), f"dq4_int8_{name}_workspace_bytes")(*shape)
+    if need < 0:
+        raise Dq4Error(-need, f"dq4_int8_{name}_workspace_bytes")
+    return need
+
+
+class _on:
+    """The device of a call's tensors made current for it (nothing if it is already)."""
+
+    def __init__(self, index: int):
+        self.index = index
+
+    def __enter__(self):
+        self.was = torch.cuda.current_device()
+        if self.was != self.index:
+            torch.cuda.set_device(self.index)
+
+    def __exit__(self, *exc):
+        if self.was != self.index:
+            torch.cuda.set_device(self.was)
+
+
+def _on_gpu(t: torch.Tensor, name: str) -> None:
+    if t.device.type != "cuda":
+        raise ValueError(f"{name}: must be a CUDA tensor (the library reads device memory)")
+
+
+def _rows(t: torch.Tensor, name: str) -> None:
+    """A matrix of rows: any stride between them, a row's values contiguous."""
+    _on_gpu(t, name)
+    if t.dtype not in _HALF:
+        raise TypeError(f"{name}: must be float16 or bfloat16, got {t.dtype}")
+    if t.dim() != 2:
+        raise ValueError(f"{name}: must be 2-D, got {tuple(t.shape)}")
+    if t.shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name}: the values of a row must be contiguous")
+
+
+def _shape(t: torch.Tensor, name: str, shape) -> None:
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+
+
+def _weight(CB: torch.Tensor, SCB: torch.Tensor, like: torch.Tensor, name: str, dims: int):
+    """Checked addresses of a weight's codes and scales."""
+    if CB.dim() != dims:
+        raise ValueError(f"{name}: must be {dims}-D, got {tuple(CB.shape)}")
+    _shape(SCB, f"{name}'s scales", CB.shape[:-1])
+    return (_flat(CB, name, torch.int8, 0, like),
+            _flat(SCB, f"{name}'s scales", torch.float32, 0, like))
+
+
+# ------------------------------------------------------------- rows in 8 bits
+class Int8Rows(NamedTuple):
+    """Activations in 8 bits: a value is codes * scales[:, None] / 127, but for the columns
+    ``cols``, whose values are ``outliers``.
+
+    ``codes`` int8 [M, K], ``scales`` float32 [M]; ``cols`` int64 [L] (ascending, -1 for none),
+    ``outliers`` float16 or bfloat16 [M, L] and ``count`` int32 [1] are None without outlier
+    columns.
+    """
+
+    codes: torch.Tensor
+    scales: torch.Tensor
+    cols: Optional[torch.Tensor] = None
+    outliers: Optional[torch.Tensor] = None
+    count: Optional[torch.Tensor] = None
+
+
+def int8_quantize(X: torch.Tensor, threshold: float = 0.0, max_outliers: int = 64,
+                  workspace: Optional[torch.Tensor] = None, stream=None) -> Int8Rows:
+    """Rows of X (M x K, float16 or bfloat16, any row stride) in 8 bits, as LLM.int8 has them.
+
+    A row's scale is its largest magnitude below ``threshold`` (0: of all values).  Columns with
+    a value at or above the threshold are outliers: the first ``max_outliers`` of them (1 .. 128)
+    have codes of 0 and their values in ``outliers``; ``count`` says how many there are, and
+    those past the maximum keep codes that end at +-127.  ``cols`` is what
+    :func:`int8_correction_prep` takes, ``outliers`` its subA.  A row with a NaN has a scale of
+    NaN.  ``workspace`` (uint8, zero-filled before its first use) is needed with a threshold; by
+    default a cached buffer per (device, stream) is used, and in ``torch.cuda.graph`` memory of
+    the graph's own.
+    """
+    _rows(X, "X")
+    M, K = X.shape
+    device = X.device
+    codes = torch.empty((M, K), dtype=torch.int8, device=device)
+    scales = torch.empty(M, dtype=torch.float32, device=device)
+    index = X.get_device()
+    handle = _stream(stream, index)
+    args = (X.data_ptr(), X.stride(0), _DTYPE_CODE[X.dtype], M, K, threshold, codes.data_ptr(),
+            scales.data_ptr())
+    with _on(index):
+        if threshold == 0:
+            st = _lib().dq4_int8_quantize(*args, None, 0, None, None, None, 0, handle)
+            rows = Int8Rows(codes, scales)
+        else:
+            if not 1 <= max_outliers <= 128:
+                raise ValueError(f"max_outliers must be 1 .. 128, got {max_outliers}")
+            cols = torch.empty(max_outliers, dtype=torch.int64, device=device)
+            outliers = torch.empty((M, max_outliers), dtype=X.dtype, device=device)
+            count = torch.empty(1, dtype=torch.int32, device=device)
+            rows = Int8Rows(codes, scales, cols, outliers, count)
+            need = _need_of(index, "quantize", K)
+            with _call_lock(index, handle):
+                ws = _workspace(workspace, need, "int8 quantize", X, handle)
+                st = _lib().dq4_int8_quantize(*args, cols.data_ptr(), max_outliers,
+                                              outliers.data_ptr(), count.data_ptr(),
+                                              ws.data_ptr(), ws.numel(), handle)
+    if st:
+        raise Dq4Error(st, "dq4_int8_quantize")
+    return rows
+
+
+# ------------------------------------------------------------- the product
+def int8_linear(X: Int8Rows, CB: torch.Tensor, SCB: torch.Tensor,
+                bias: Optional[torch.Tensor] = None, out_dtype: torch.dtype = torch.float16,
+                Y: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                bad: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Y = X W^T + bias with rows X in 8 bits (:func:`int8_quantize`) and W (N x K) in 8 bits:
+    CB int8 codes, SCB float32 scales of its rows, a value CB * SCB / 127.
+
+    Outlier columns of X multiply W's values as the 16-bit numbers they are.  ``bias`` ([N]) and
+    Y are of ``out_dtype`` (float16, bfloat16 or float32).  K must be a multiple of 16.
+    ``workspace`` (uint8, zero-filled before its first use) holds X in 16 bits and partial sums;
+    by default a cached buffer per (device, stream) is used, and in ``torch.cuda.graph`` memory
+    of the graph's own.  ``bad`` (int32) counts columns that cannot be used.
+    """
+    codes = X.codes
+    _on_gpu(codes, "codes")
+    if codes.dim() != 2 or CB.dim() != 2 or codes.shape[1] != CB.shape[1]:
+        raise ValueError(f"codes {tuple(codes.shape)} do not go with CB {tuple(CB.shape)}")
+    M, K = codes.shape
+    N = CB.shape[0]
+    codes_ptr = _flat(codes, "codes", torch.int8, 0, codes)
+    _shape(X.scales, "scales", (M,))
+    scales_ptr = _flat(X.scales, "scales", torch.float32, 0, codes)
+    cb_ptr, scb_ptr = _weight(CB, SCB, codes, "CB", 2)
+    if Y is not None:
+        out_dtype = Y.dtype
+    if out_dtype not in _DTYPE_CODE:
+        raise TypeError(f"out_dtype: unsupported {out_dtype}")
+    cols_ptr = outliers_ptr = bias_ptr = None
+    L = kind = 0
+    if (X.cols is None) != (X.outliers is None):
+        raise ValueError("cols and outliers come together")
+    if X.cols is not None:
+        if X.cols.dim() != 1 or X.cols.numel() > 128:
+            raise ValueError(f"cols: must be 1-D, 128 at most, got {tuple(X.cols.shape)}")
+        L = X.cols.numel()
+        if X.outliers.dtype not in _HALF:
+            raise TypeError(f"outliers: must be float16 or bfloat16, got {X.outliers.dtype}")
+        _shape(X.outliers, "outliers", (M, L))
+        kind = _DTYPE_CODE[X.outliers.dtype]
+        cols_ptr = _flat(X.cols, "cols", torch.int64, 0, codes)
+        outliers_ptr = _flat(X.outliers, "outliers", X.outliers.dtype, 0, codes)
+    if bias is not None:
+        _shape(bias, "bias", (N,))
+        bias_ptr = _flat(bias, "bias", out_dtype, 0, codes)
+    if Y is None:
+        Y = torch.empty((M, N), dtype=out_dtype, device=codes.device)
+    else:
+        _shape(Y, "Y", (M, N))
+    y_ptr = _flat(Y, "Y", out_dtype, 0, codes)
+    bad_ptr = _bad(bad, codes)
+    index = codes.get_device()
+    handle = _stream(stream, index)
+    need = _need_of(index, "linear", M, N, K, L)
+    with _on(index), _call_lock(index, handle):
+        ws_ptr, ws_bytes = _scratch(workspace, need, "int8 linear", codes, handle)
+        st = _lib().dq4_int8_linear(codes_ptr, scales_ptr, cb_ptr, scb_ptr, M, N, K, cols_ptr, L,
+                                    outliers_ptr, kind, bias_ptr, _DTYPE_CODE[out_dtype], y_ptr,
+                                    ws_ptr, ws_bytes, bad_ptr, handle)
+    if st:
+        raise Dq4Error(st, "dq4_int8_linear")
+    return Y
+
+
+def _scratch(workspace, need: int, what: str, like: torch.Tensor, handle):
+    """Address and size of the call's workspace; none if it needs none."""
+    if need == 0 and workspace is None:
+        return None, 0
+    ws = _workspace(workspace, need, what, like, handle)
+    return ws.data_ptr(), ws.numel()
+
+
+def int8_linear_backward(dY: torch.Tensor, CB: torch.Tensor, SCB: torch.Tensor,
+                         dX: Optional[torch.Tensor] = None,
+                         workspace: Optional[torch.Tensor] = None,
+                         bad: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """dX = dY W: the gradient of :func:`int8_linear`'s input, its rounding to 8 bits taken as
+    the identity.
+
+    dY is M x N (float16 or bfloat16, contiguous); W's values are rounded to its type, as
+    :func:`int8_correction_prep` has them.  N must be a multiple of 8, K of 16.  ``workspace``
+    and ``bad`` as for :func:`int8_linear`.
+    """
+    _on_gpu(dY, "dY")
+    if dY.dtype not in _HALF:
+        raise TypeError(f"dY: must be float16 or bfloat16, got {dY.dtype}")
+    if dY.dim() != 2 or CB.dim() != 2 or dY.shape[1] != CB.shape[0]:
+        raise ValueError(f"dY {tuple(dY.shape)} does not go with CB {tuple(CB.shape)}")
+    M, N = dY.shape
+    K = CB.shape[1]
+    dy_ptr = _flat(dY, "dY", dY.dtype, 0, dY)
+    cb_ptr, scb_ptr = _weight(CB, SCB, dY, "CB", 2)
+    if dX is None:
+        dX = torch.empty((M, K), dtype=dY.dtype, device=dY.device)
+    else:
+        _shape(dX, "dX", (M, K))
+    dx_ptr = _flat(dX, "dX", dY.dtype, 0, dY)
+    bad_ptr = _bad(bad, dY)
+    index = dY.get_device()
+    handle = _stream(stream, index)
+    need = _need_of(index, "linear_backward", M, N, K)
+    with _on(index), _call_lock(index, handle):
+        ws_ptr, ws_bytes = _scratch(workspace, need, "int8 backward", dY, handle)
+        st = _lib().dq4_int8_linear_backward(dy_ptr, _DTYPE_CODE[dY.dtype], cb_ptr, scb_ptr, M, N,
+                                             K, dx_ptr, ws_ptr, ws_bytes, bad_ptr, handle)
+    if st:
+        raise Dq4Error(st, "dq4_int8_linear_backward")
+    return dX
+
+
+# ------------------------------------------------------------- mixture of experts
+def int8_moe(X: torch.Tensor, logits: torch.Tensor, w1: torch.Tensor, s1: torch.Tensor,
+             w2: torch.Tensor, s2: torch.Tensor, top_k: int, renormalize: bool = True,
+             return_routing: bool = False, workspace: Optional[torch.Tensor] = None, stream=None):
+    """A mixture-of-experts layer for few tokens (256 at most) over 8-bit weights.
+
+    X is T x H (float16 or bfloat16), ``logits`` T x E (float32).  Each token goes through the
+    ``top_k`` experts (16 at most) with its largest logits, the lower index first where they are
+    equal, weighted by their softmax over the chosen ones (``renormalize``) or over all:
+    ``y = sum p_e W2_e (silu(Wg_e x) * (Wu_e x))``.  ``w1`` int8 [E, 2 I, H] holds the rows of
+    Wg, then those of Wu, ``w2`` int8 [E, H, I]; ``s1`` [E, 2 I] and ``s2`` [E, H] are float32
+    scales of their rows, a value w * s / 127.  H and I are multiples of 16.  Returns Y (T x H,
+    X's dtype), or (Y, ids, weights) with the choices, int32 and float32 [T, top_k].
+    ``workspace`` (uint8, zero-filled before its first use) holds the rows between the launches;
+    by default a cached buffer per (device, stream) is used, and in ``torch.cuda.graph`` memory
+    of the graph's own.
+    """
+    _rows(X, "X")
+    T, H = X.shape
+    w1_ptr, s1_ptr = _weight(w1, s1, X, "w1", 3)
+    w2_ptr, s2_ptr = _weight(w2, s2, X, "w2", 3)
+    E, I = w1.shape[0], w2.shape[2]
+    _shape(w1, "w1", (E, 2 * I, H))
+    _shape(w2, "w2", (E, H, I))
+    _shape(logits, "logits", (T, E))
+    logits_ptr = _flat(logits, "logits", torch.float32, 0, X)
+    if not 1 <= top_k <= min(E, 16):
+        raise ValueError(f"top_k must be 1 .. {min(E, 16)}, got {top_k}")
+    ids = torch.empty((T, top_k), dtype=torch.int32, device=X.device)
+    weights = torch.empty((T, top_k), dtype=torch.float32, device=X.device)
+    Y = torch.empty((T, H), dtype=X.dtype, device=X.device)
+    index = X.get_device()
+    handle = _stream(stream, index)
+    need = _need_of(index, "moe", T, H, I, top_k)
+    with _on(index), _call_lock(index, handle):
+        ws_ptr, ws_bytes = _scratch(workspace, need, "int8 moe", X, handle)
+        st = _lib().dq4_int8_moe(X.data_ptr(), X.stride(0), _DTYPE_CODE[X.dtype], T, H, I, E,
+                                 logits_ptr, top_k, renormalize, w1_ptr, s1_ptr, w2_ptr, s2_ptr,
+                                 ids.data_ptr(), weights.data_ptr(), Y.data_ptr(), ws_ptr,
+                                 ws_bytes, handle)
+    if st:
+        raise Dq4Error(st, "dq4_int8_moe")
+    return (Y, ids, weights) if return_routing else Y
