@@ -14,10 +14,11 @@ CSRC = os.path.join(PKG, "csrc")
 SOURCES = [os.path.join(CSRC, f) for f in
            ("flat.cu", "transposed.cu", "int8_prep.cu", "out_prod.cu", "linear.cu",
             "host_pipeline.cu", "qk_norm.cu", "kv8_append.cu", "kv8_attention.cu",
-            "kv8_decode.cu", "kv8_prefill.cu", "int8_quantize.cu", "int8_linear.cu", "int8_backward.cu", "int8_moe.cu",
-            "host.cu")]
+            "kv8_decode.cu", "kv8_prefill.cu", "int8_quantize.cu", "int8_linear.cu",
+            "int8_backward.cu", "int8_gemm.cu", "int8_moe.cu", "host.cu")]
 HEADERS = [os.path.join(ROOT, "include", "dq4.h"), os.path.join(ROOT, "include", "dq4_attn.h"),
            os.path.join(ROOT, "include", "dq4_int8.h"), os.path.join(CSRC, "int8.cuh"),
+           os.path.join(CSRC, "int8_gemm.cuh"),
            os.path.join(CSRC, "common.cuh"), os.path.join(CSRC, "attn.cuh"),
            os.path.join(CSRC, "kv8.cuh"), os.path.join(CSRC, "kv8_attend.cuh"), os.path.join(CSRC, "tcgen05.cuh"),
            os.path.join(CSRC, "tmap.cuh")]

@@ -1,49 +1,17 @@
-// The gradient of the 8-bit product's input: dq4_int8_linear_backward (dq4_int8.h).
-#include "int8.cuh"
-
-namespace dq4d {
-namespace {
-
-constexpr int kThreadsBack = 128, kRowsBack = 8;
-
-struct BackArgs {
-  const void* dY;
-  bool bf16;
-  const int8_t* CB;
-  const float* SCB;
-  int64_t M, N, K;
-  void* dX;
-};
-
-// A thread a column of dX, 8 rows of it.
-__global__ void __launch_bounds__(kThreadsBack) dq4_int8_backward_kernel(const BackArgs p) {
-  wait_for_stream();
-  const int64_t k = int64_t(blockIdx.x) * kThreadsBack + threadIdx.x;
-  if (k >= p.K) return;
-  for (int64_t m0 = int64_t(blockIdx.y) * kRowsBack; m0 < p.M; m0 += int64_t(gridDim.y) * kRowsBack) {
-    float sum[kRowsBack] = {};
-    for (int64_t n = 0; n < p.N; ++n) {
-      float w = __fmul_rn(__fmul_rn(float(p.CB[n * p.K + k]), p.SCB[n]), kRecip127);
-      w = p.bf16 ? __bfloat162float(__float2bfloat16_rn(w)) : __half2float(__float2half_rn(w));
-#pragma unroll
-      for (int i = 0; i < kRowsBack; ++i)
-        if (m0 + i < p.M) sum[i] = fmaf(load_16(p.dY, (m0 + i) * p.N + n, p.bf16), w, sum[i]);
-    }
-#pragma unroll
-    for (int i = 0; i < kRowsBack; ++i)
-      if (m0 + i < p.M)
-        store_any(p.dX, (m0 + i) * p.K + k, sum[i], p.bf16 ? DQ4_OUT_BF16 : DQ4_OUT_F16);
-  }
-}
-
-}  // namespace
-}  // namespace dq4d
+// The gradient of the 8-bit product's input, dq4_int8_linear_backward (dq4_int8.h): the entry
+// point.  The kernel is the product's (int8_gemm.cu), the weight's columns its rows.
+#include "int8_gemm.cuh"
 
 using namespace dq4d;
 
 extern "C" {
 
-int64_t dq4_int8_linear_backward_workspace_bytes(int64_t M, int64_t N, int64_t K) { return 0; }
+int64_t dq4_int8_linear_backward_workspace_bytes(int64_t M, int64_t N, int64_t K) {
+  if (M <= 0 || N <= 0 || K <= 0 || M > INT32_MAX || N > INT32_MAX || K > INT32_MAX) return 0;
+  int dev, sms;
+  if (current_device(&dev, &sms) != DQ4_OK) return -DQ4_ERR_DEVICE;
+  return int8_backward_workspace(M, N, K, sms);
+}
 
 int dq4_int8_linear_backward(const void* dY, int32_t dtype, const int8_t* CB, const float* SCB,
                              int64_t M, int64_t N, int64_t K, void* dX, void* workspace,
@@ -60,11 +28,16 @@ int dq4_int8_linear_backward(const void* dY, int32_t dtype, const int8_t* CB, co
     return DQ4_ERR_ALIGN;
   int dev, sms;
   if (const int st = current_device(&dev, &sms)) return st;
-  const BackArgs p = {dY, dtype == DQ4_OUT_BF16, CB, SCB, M, N, K, dX};
-  const int64_t y = (M + kRowsBack - 1) / kRowsBack;
-  const dim3 grid(unsigned((K + kThreadsBack - 1) / kThreadsBack), unsigned(y < 65535 ? y : 65535));
-  return launch_ordered(dq4_int8_backward_kernel, grid, kThreadsBack, 0,
-                        static_cast<cudaStream_t>(stream), p);
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (N == 0) {
+    const cudaError_t e = cudaMemsetAsync(dX, 0, size_t(M) * size_t(K) * 2, s);
+    return e == cudaSuccess ? DQ4_OK : fail_cuda(DQ4_ERR_LAUNCH, e);
+  }
+  if (!workspace || workspace_bytes < int8_backward_workspace(M, N, K, sms))
+    return DQ4_ERR_WORKSPACE;
+  if (misaligned(workspace, 256)) return DQ4_ERR_ALIGN;
+  const Int8Backward p = {dY, dtype == DQ4_OUT_BF16, CB, SCB, M, N, K, dX, bad};
+  return launch_int8_backward(p, dev, sms, workspace, s);
 }
 
 }  // extern "C"

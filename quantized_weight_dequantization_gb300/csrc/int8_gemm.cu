@@ -1,0 +1,870 @@
+// Products of many rows with an 8-bit weight on tcgen05: Y = X W^T (dq4_int8_linear) and
+// dX = dY W (dq4_int8_linear_backward).
+//
+// The weight is the MMA's A operand: 128 of its rows (or, for the gradient, columns) are the
+// lanes of TMEM, where its 16-bit values are written a stage of 128 at a time; BX rows of the
+// activations are B, read by TMA from their 16-bit form.  For the product that form is made by a
+// kernel of its own (int8_rows_kernel: codes as FP16, outliers in place of their codes), which
+// costs 3 bytes a value once, where converting inside would cost every weight tile the same again.
+//
+// A CTA takes items (a tile, or a part of a tile's sum where there are few) in turn:
+//   warps 0..7    two groups that take alternate stages: codes from shared memory to 16-bit values
+//                 in TMEM, a thread a lane
+//   warps 8..15   read a finished tile out of TMEM, scale, store (or leave a part of the sum; the
+//                 last part's CTA adds them all, in their order)
+//   then          one or two warps that issue the MMAs (alternate stages, accumulators of their
+//                 own: issuing takes a thread about 120 cycles, whatever BX is), the warp that
+//                 copies the weight's codes, the warp that copies the activations
+// Waits are bounded; one that runs out counts into *bad, raises a flag of the CTA, and every
+// role lets its copies and MMAs finish and ends.
+#include "int8_gemm.cuh"
+#include "tcgen05.cuh"
+#include "tmap.cuh"
+
+namespace dq4d {
+namespace {
+
+constexpr int kStep = 64;            // values of a K step: 128 bytes of 16-bit values
+constexpr int kStage = 2 * kStep;    // of a stage
+constexpr int kTileW = 128;          // weight rows (columns) of a tile: TMEM lanes
+constexpr int kRawSlot = kTileW * kStage;  // bytes of a stage's codes
+constexpr int kRawSlots = 4;
+constexpr int kRing = 4;             // stages in TMEM
+constexpr uint32_t kRingCol = 256;   // where they start; the accumulators lie before
+constexpr uint32_t kTmemColumns = 512;
+constexpr int kProducers = 8, kReaders = 8;
+
+template <int BX>
+struct Gemm {
+  static constexpr int kIssuers = BX < 256 ? 2 : 1;
+  static constexpr int kBuffers = 256 / (BX * kIssuers);  // accumulators of an issuer
+  // a slot of activations is a stage for two issuers (so that stage g's slot is always taken
+  // by the same one), a step for one
+  static constexpr int kSlotSteps = kIssuers;
+  static constexpr int kStepBytes = BX * kStep * 2;
+  static constexpr int kSlot = kSlotSteps * kStepBytes;
+  static constexpr int kSlots = BX == 256 ? 5 : BX == 128 ? 4 : 6;
+  static_assert(kIssuers == 1 || kSlots % 2 == 0, "a slot belongs to one issuer");
+  static constexpr int kThreads = 32 * (kProducers + kReaders + kIssuers + 2);
+  static constexpr int kRawAt = kSlots * kSlot;
+  static constexpr int kBarsAt = kRawAt + kRawSlots * kRawSlot;
+  static constexpr int kBars = 2 * kSlots + 2 * kRawSlots + 2 * kRing + 2 * kBuffers + 1;
+  static constexpr int kBytes = kBarsAt + 8 * kBars + 1024;  // + alignment slack
+  static_assert(kBytes + 1600 <= 227 * 1024, "shared memory budget");
+  static_assert(kBytes > 116 * 1024, "one CTA per SM: the TMEM allocation never waits");
+};
+
+struct GemmArgs {
+  int64_t lanes, rows;   // of the output: weight rows (columns), activation rows
+  int steps, code_steps; // K steps, and of them with codes from CB (the rest: outlier columns)
+  int tiles_x;           // tiles along the activations
+  int64_t tiles;
+  int parts;             // of a tile's sum
+  int64_t items;         // tiles * parts
+  const int8_t* CB;
+  const float* SCB;
+  int64_t K, N;
+  const int32_t* cols;   // the outlier columns that are used, -1 for none
+  const float* units;    // of the activation rows
+  const void* bias;
+  int out_dtype;
+  void* out;             // [rows][lanes]
+  float* part;           // [items][BX][128]
+  int* count;            // [tiles]
+  int* bad;
+};
+
+__device__ __forceinline__ void bar_readers() {
+  asm volatile("bar.sync 1, %0;" :: "n"(32 * kReaders) : "memory");
+}
+__device__ __forceinline__ bool all_readers(bool v) {
+  uint32_t r;
+  asm volatile(
+      "{\n.reg .pred p, q;\nsetp.ne.u32 p, %1, 0;\nbar.red.and.pred q, 1, %2, p;\n"
+      "selp.u32 %0, 1, 0, q;\n}"
+      : "=r"(r) : "r"(uint32_t(v)), "n"(32 * kReaders) : "memory");
+  return r != 0;
+}
+__device__ __forceinline__ void commit(uint32_t bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];"
+               :: "r"(bar) : "memory");
+}
+__device__ __forceinline__ uint32_t lds_u8(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(addr));
+  return v;
+}
+// {a, b} + {c, c} and {a, b} * {c, d}, each rounded on its own.
+__device__ __forceinline__ uint64_t pair_of(uint32_t a, uint32_t b) {
+  return uint64_t(b) << 32 | a;
+}
+__device__ __forceinline__ uint64_t add_pair(uint64_t x, uint64_t y) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul_pair(uint64_t x, uint64_t y) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
+  return r;
+}
+
+// A ring's place and the parity of its phase, by the number of its uses.
+template <int kDepth>
+struct Place {
+  int slot = 0;
+  uint32_t phase = 0;
+  __device__ __forceinline__ void next() {
+    if (++slot == kDepth) {
+      slot = 0;
+      phase ^= 1u;
+    }
+  }
+};
+
+// kBack: lanes are columns of the weight, the sum runs over its rows.  kBF16: 16-bit values are
+// BF16 (the gradient's), else FP16.
+template <int BX, bool kBack, bool kBF16>
+__global__ void __launch_bounds__(Gemm<BX>::kThreads, 1)
+    dq4_int8_gemm_kernel(const __grid_constant__ CUtensorMap map_w,
+                         const __grid_constant__ CUtensorMap map_x, const GemmArgs p) {
+  using S = Gemm<BX>;
+  constexpr int kIssuers = S::kIssuers, kBuffers = S::kBuffers, kSlots = S::kSlots;
+  constexpr int kOut = kBF16 ? DQ4_OUT_BF16 : DQ4_OUT_F16;
+  constexpr int kMmaWarp = kProducers + kReaders;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ uint32_t s_tmem;
+  __shared__ volatile int s_abort;
+  __shared__ bool s_last;
+  __shared__ int s_cols[kMaxOutliers];
+  __shared__ __align__(16) float s_scale[kBack ? 4 * kStage : 4];  // two stages of each group
+  uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~uintptr_t(1023));
+  const uint32_t sbase = smem_u32(base);
+  const uint32_t bar0 = sbase + S::kBarsAt;
+  auto x_full = [&](int s) { return bar0 + 8 * s; };
+  auto x_empty = [&](int s) { return bar0 + 8 * (kSlots + s); };
+  auto raw_full = [&](int s) { return bar0 + 8 * (2 * kSlots + s); };
+  auto raw_empty = [&](int s) { return bar0 + 8 * (2 * kSlots + kRawSlots + s); };
+  auto w_full = [&](int s) { return bar0 + 8 * (2 * kSlots + 2 * kRawSlots + s); };
+  auto w_empty = [&](int s) { return bar0 + 8 * (2 * kSlots + 2 * kRawSlots + kRing + s); };
+  auto acc_full = [&](int b) {
+    return bar0 + 8 * (2 * kSlots + 2 * kRawSlots + 2 * kRing + b);
+  };
+  auto acc_empty = [&](int b) { return acc_full(kBuffers + b); };
+  const uint32_t all_done = acc_full(2 * kBuffers);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  volatile int* aborted = &s_abort;
+  auto fail = [&] {
+    *aborted = 1;
+    if (p.bad) atomicAdd(p.bad, 1);
+  };
+
+  // ---- setup: touches no global memory, so it overlaps the kernel before this one
+  if (warp == kMmaWarp) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;"
+                 :: "r"(smem_u32(&s_tmem)), "r"(kTmemColumns));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    if (lane == 0) {
+      for (int s = 0; s < kSlots; ++s) {
+        mbar_init(x_full(s), 1);
+        mbar_init(x_empty(s), 1);
+      }
+      for (int s = 0; s < kRawSlots; ++s) {
+        mbar_init(raw_full(s), 1);
+        mbar_init(raw_empty(s), kProducers / 2);
+      }
+      for (int s = 0; s < kRing; ++s) {
+        mbar_init(w_full(s), kProducers / 2);
+        mbar_init(w_empty(s), 1);
+      }
+      for (int b = 0; b < kBuffers; ++b) {
+        mbar_init(acc_full(b), kIssuers);
+        mbar_init(acc_empty(b), kReaders);
+      }
+      mbar_init(all_done, kIssuers);
+      *aborted = 0;
+      asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+      asm volatile("prefetch.tensormap [%0];" :: "l"(reinterpret_cast<uint64_t>(&map_w)));
+      asm volatile("prefetch.tensormap [%0];" :: "l"(reinterpret_cast<uint64_t>(&map_x)));
+    }
+  }
+  wait_for_stream();
+  asm volatile("griddepcontrol.launch_dependents;");
+  if (!kBack && p.cols)
+    for (int l = tid; l < kMaxOutliers; l += S::kThreads) s_cols[l] = load_global(p.cols + l);
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+  __syncthreads();
+  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+  const uint32_t tmem = s_tmem;
+
+  // An item: its tile's lanes and rows, its stages.  Every role walks the CTA's items; stages are
+  // counted over all of them (g), and stage g is group and issuer g % 2's, in slot g % depth.
+  struct Item {
+    int64_t lane0, row0;
+    int begin, end;  // stages
+  };
+  const int stages = (p.steps + 1) / 2;
+  auto item_at = [&](int64_t i) {
+    Item it;
+    const int64_t tile = i / p.parts;
+    const int part = int(i - tile * p.parts);
+    const int64_t tw = tile / p.tiles_x;
+    it.lane0 = tw * kTileW;
+    it.row0 = (tile - tw * p.tiles_x) * BX;
+    it.begin = int(int64_t(stages) * part / p.parts);
+    it.end = int(int64_t(stages) * (part + 1) / p.parts);
+    return it;
+  };
+  auto steps_of = [&](int stage) { return min(2, p.steps - 2 * stage); };
+
+  if (warp == kMmaWarp + kIssuers) {
+    if (lane == 0) {
+      // ---- the weight's codes: 128 rows of 128 bytes a stage
+      const uint64_t map = reinterpret_cast<uint64_t>(&map_w);
+      Place<kRawSlots> at;
+      int g = 0;
+      bool stop = false;
+      for (int64_t i = blockIdx.x; i < p.items && !stop; i += gridDim.x) {
+        const Item it = item_at(i);
+        for (int s = it.begin; s < it.end; ++s, ++g, at.next()) {
+          if (g >= kRawSlots && (*aborted || !mbar_wait(raw_empty(at.slot), at.phase ^ 1u))) {
+            if (!*aborted) fail();
+            stop = true;
+            break;
+          }
+          const bool codes = kBack || 2 * s < p.code_steps;
+          mbar_expect(raw_full(at.slot), codes ? kRawSlot : 0);
+          if (codes)
+            tma_load_2d(sbase + S::kRawAt + at.slot * kRawSlot, map,
+                        kBack ? int(it.lane0) : s * kStage, kBack ? s * kStage : int(it.lane0),
+                        raw_full(at.slot));
+        }
+      }
+      if (*aborted)  // copies in flight land before the CTA leaves
+        for (int j = g - 1; j >= 0 && j >= g - kRawSlots; --j)
+          mbar_wait(raw_full(j % kRawSlots), (j / kRawSlots) & 1);
+    }
+  } else if (warp == kMmaWarp + kIssuers + 1) {
+    if (lane == 0) {
+      // ---- the activations: BX rows of 64 values a step
+      const uint64_t map = reinterpret_cast<uint64_t>(&map_x);
+      Place<kSlots> at;
+      int q = 0;
+      bool stop = false;
+      for (int64_t i = blockIdx.x; i < p.items && !stop; i += gridDim.x) {
+        const Item it = item_at(i);
+        for (int s = it.begin; s < it.end && !stop; ++s) {
+          const int n = steps_of(s);
+          for (int sub = 0; sub < n; sub += S::kSlotSteps, ++q, at.next()) {
+            if (q >= kSlots && (*aborted || !mbar_wait(x_empty(at.slot), at.phase ^ 1u))) {
+              if (!*aborted) fail();
+              stop = true;
+              break;
+            }
+            const int here = min(S::kSlotSteps, n - sub);
+            mbar_expect(x_full(at.slot), here * S::kStepBytes);
+            for (int k = 0; k < here; ++k)
+              tma_load_2d(sbase + at.slot * S::kSlot + k * S::kStepBytes, map,
+                          (2 * s + sub + k) * kStep, int(it.row0), x_full(at.slot));
+          }
+        }
+      }
+      if (*aborted)
+        for (int j = q - 1; j >= 0 && j >= q - kSlots; --j)
+          mbar_wait(x_full(j % kSlots), (j / kSlots) & 1);
+    }
+  } else if (warp >= kMmaWarp) {
+    if (lane == 0) {
+      // ---- the MMAs: issuer `mine` takes the stages g with g % kIssuers == mine
+      const int mine = warp - kMmaWarp;
+      const uint32_t idesc = instr_desc_f16<kTileW, BX>(kBF16);
+      Place<kRing> wp;
+      Place<kSlots> xp;
+      int g = 0, buffer = 0, turn = 0;
+      bool stop = false;
+      for (int64_t i = blockIdx.x; i < p.items && !stop; i += gridDim.x, ++turn) {
+        const Item it = item_at(i);
+        buffer = turn % kBuffers;
+        if (turn >= kBuffers && (*aborted || !mbar_wait(acc_empty(buffer),
+                                                        uint32_t(turn / kBuffers - 1) & 1u))) {
+          if (!*aborted) fail();
+          break;
+        }
+        const uint32_t acc = tmem + (mine * kBuffers + buffer) * BX;
+        uint32_t more = 0;  // whether the accumulator holds something
+        for (int s = it.begin; s < it.end; ++s, ++g, wp.next()) {
+          const int n = steps_of(s);
+          if (kIssuers > 1 && (g & 1) != mine) {
+            xp.next();
+            continue;
+          }
+          if (*aborted || !mbar_wait(w_full(wp.slot), wp.phase)) {
+            if (!*aborted) fail();
+            stop = true;
+            break;
+          }
+          for (int sub = 0; sub < n; ++sub) {
+            const int in_slot = sub % S::kSlotSteps;
+            if (in_slot == 0 && !mbar_wait(x_full(xp.slot), xp.phase)) {
+              fail();
+              stop = true;
+              break;
+            }
+            asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+            const uint32_t a = tmem + kRingCol + (wp.slot * 2 + sub) * 32;
+            const uint32_t b = sbase + xp.slot * S::kSlot + in_slot * S::kStepBytes;
+#pragma unroll
+            for (int k = 0; k < kStep / 16; ++k) {
+              asm volatile(
+                  "{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\n"
+                  "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}"
+                  :: "r"(acc), "r"(a + k * 8), "l"(smem_desc(b + k * 32)), "r"(idesc), "r"(more));
+              more = 1;
+            }
+            if (in_slot == S::kSlotSteps - 1 || sub == n - 1) {
+              commit(x_empty(xp.slot));
+              xp.next();
+            }
+          }
+          if (stop) break;
+          commit(w_empty(wp.slot));
+        }
+        if (stop) break;
+        commit(acc_full(buffer));
+      }
+      // every MMA issued above has finished before the TMEM is freed
+      commit(all_done);
+      mbar_wait(all_done, 0);
+    }
+  } else if (warp < kProducers) {
+    // ---- the weight's 16-bit values: thread r of a group is lane r of TMEM
+    const int group = warp / 4, quad = warp & 3, r = quad * 32 + lane;
+    const uint32_t to0 = tmem + (uint32_t(quad * 32) << 16) + kRingCol;
+    Place<kRing> wp;
+    Place<kRawSlots> rp;
+    int g = 0;
+    bool stop = false, given_up = false;
+    // the scale of row r of this group's next stage of an item, loaded a stage of the group ahead
+    float scale = 0.f;
+    int loaded = -1, scale_turn = 0;  // (loaded: the stage whose scale that is)
+    auto scale_of = [&](int s) {
+      const int64_t n = int64_t(s) * kStage + r;
+      return n < p.N ? load_global(p.SCB + n) : 0.f;
+    };
+    for (int64_t i = blockIdx.x; i < p.items && !stop; i += gridDim.x) {
+      const Item it = item_at(i);
+      for (int s = it.begin; s < it.end; ++s, ++g, wp.next(), rp.next()) {
+        if ((g & 1) != group) continue;
+        if constexpr (kBack) {
+          if (loaded != s) scale = scale_of(s);
+          s_scale[(group * 2 + scale_turn) * kStage + r] = scale;
+          // The group's scales are there; and if one of its warps gave up on its last stage, all
+          // of them end here.
+          uint32_t go;
+          asm volatile(
+              "{\n.reg .pred p, q;\nsetp.ne.u32 p, %1, 0;\nbar.red.and.pred q, %2, %3, p;\n"
+              "selp.u32 %0, 1, 0, q;\n}"
+              : "=r"(go) : "r"(uint32_t(!given_up)), "r"(2 + group), "n"(32 * kProducers / 2)
+              : "memory");
+          if (go == 0) {
+            stop = true;
+            break;
+          }
+          loaded = s + 2 < it.end ? s + 2 : -1;
+          if (loaded >= 0) scale = scale_of(loaded);
+        }
+        const bool ok = !*aborted &&
+                        (mbar_try2(raw_full(rp.slot), rp.phase, w_empty(wp.slot),
+                                   g >= kRing ? wp.phase ^ 1u : 1u) ||
+                         (mbar_wait(raw_full(rp.slot), rp.phase) &&
+                          (g < kRing || mbar_wait(w_empty(wp.slot), wp.phase ^ 1u))));
+        if (!__all_sync(kAllLanes, ok)) {
+          if (lane == 0 && !*aborted) fail();
+          if constexpr (kBack) {
+            given_up = true;
+            continue;
+          }
+          stop = true;
+          break;
+        }
+        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+        const int n = steps_of(s);
+        const uint32_t raw = sbase + S::kRawAt + rp.slot * kRawSlot;
+#pragma unroll 1
+        for (int sub = 0; sub < n; ++sub) {
+          const uint32_t to = to0 + (wp.slot * 2 + sub) * 32;
+          if constexpr (kBack) {
+            // column r of 64 rows: consecutive lanes read consecutive bytes
+            const uint32_t from = raw + sub * kStep * kTileW + r;
+            const float* sc = s_scale + (group * 2 + scale_turn) * kStage + sub * kStep;
+            const uint64_t off = pair_of(0xCB000080u, 0xCB000080u);  // -(2^23 + 128)
+            const uint32_t r127 = __float_as_uint(kRecip127);
+            uint32_t o[32];
+#pragma unroll
+            for (int j = 0; j < 32; j += 2) {
+              const float4 f = *reinterpret_cast<const float4*>(sc + 2 * j);
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                // 2^23 + (code + 128), exactly
+                const uint64_t u = pair_of(lds_u8(from + (2 * (j + h)) * kTileW) ^ 0x4B000080u,
+                                           lds_u8(from + (2 * (j + h) + 1) * kTileW) ^ 0x4B000080u);
+                const uint64_t w = mul_pair(
+                    mul_pair(add_pair(u, off), h ? pair_of(__float_as_uint(f.z), __float_as_uint(f.w))
+                                                 : pair_of(__float_as_uint(f.x), __float_as_uint(f.y))),
+                    pair_of(r127, r127));
+                o[j + h] = pack2<kOut>(__uint_as_float(uint32_t(w)), __uint_as_float(uint32_t(w >> 32)));
+              }
+            }
+            tmem_st<32>(to, o);
+          } else {
+            const int step = 2 * s + sub;
+            if (step < p.code_steps) {
+              uint32_t o[32];
+#pragma unroll
+              for (int c = 0; c < 4; ++c) {
+                const uint4 w = lds_v4(raw + r * kStage + (((4 * sub + c) ^ (r & 7)) << 4));
+                codes_f16(w.x, o[8 * c], o[8 * c + 1]);
+                codes_f16(w.y, o[8 * c + 2], o[8 * c + 3]);
+                codes_f16(w.z, o[8 * c + 4], o[8 * c + 5]);
+                codes_f16(w.w, o[8 * c + 6], o[8 * c + 7]);
+              }
+              tmem_st<32>(to, o);
+            } else {
+              // what the outliers' lower halves multiply: their columns, gathered
+              const int8_t* row = p.CB + (it.lane0 + r) * p.K;
+              const bool in = it.lane0 + r < p.N;
+#pragma unroll 1
+              for (int c = 0; c < 4; ++c) {
+                uint32_t o[8];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                  uint32_t w = 0;
+#pragma unroll
+                  for (int b = 0; b < 4; ++b) {
+                    const int col = s_cols[(step - p.code_steps) * kStep + 16 * c + 4 * j + b];
+                    if (in && col >= 0) w |= uint32_t(uint8_t(load_global(row + col))) << (8 * b);
+                  }
+                  codes_f16(w, o[2 * j], o[2 * j + 1]);
+                }
+                tmem_st<8>(to + 8 * c, o);
+              }
+            }
+          }
+        }
+        if constexpr (kBack) scale_turn ^= 1;
+        asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+        asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(w_full(wp.slot));
+          mbar_arrive(raw_empty(rp.slot));
+        }
+      }
+    }
+  } else {
+    // ---- finished tiles: lane = weight row (column), 32 columns of activation rows at a time
+    constexpr int kHalf = BX / 2, kChunks = kHalf / 32;
+    const int quad = warp & 3, half = (warp - kProducers) >> 2;
+    const bool f32 = p.out_dtype == DQ4_OUT_F32, bf16 = p.out_dtype == DQ4_OUT_BF16;
+    // two lanes exchange a value, so that a store takes four bytes
+    const bool pairs = !f32 && p.lanes % 2 == 0 && (reinterpret_cast<uintptr_t>(p.out) & 3) == 0;
+    int turn = 0, g = 0;
+    for (int64_t i = blockIdx.x; i < p.items; i += gridDim.x, ++turn) {
+      const Item it = item_at(i);
+      const int buffer = turn % kBuffers;
+      const int64_t n = it.lane0 + quad * 32 + lane, m0 = it.row0 + half * kHalf;
+      float scale = 1.f, bias = 0.f, unit[kChunks];
+      if constexpr (!kBack) {
+        if (n < p.lanes) {
+          scale = load_global(p.SCB + n) * kRecip127;
+          if (p.bias) bias = load_any(p.bias, n, p.out_dtype);
+        }
+#pragma unroll
+        for (int c = 0; c < kChunks; ++c)
+          unit[c] = m0 + 32 * c + lane < p.rows ? load_global(p.units + m0 + 32 * c + lane) : 0.f;
+      }
+      const bool ok = !*aborted && mbar_wait(acc_full(buffer), uint32_t(turn / kBuffers) & 1u) &&
+                      !*aborted;
+      if (!all_readers(ok)) {
+        if (!ok && lane == 0 && !*aborted) fail();
+        break;
+      }
+      asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+      const uint32_t at = tmem + (uint32_t(quad * 32) << 16) + buffer * BX + half * kHalf;
+      // the accumulators that have a stage of the item: the first stage's issuer, and with
+      // two stages both
+      const int first = kIssuers > 1 ? g & 1 : 0;
+      const bool both = kIssuers > 1 && it.end - it.begin > 1;
+      g += it.end - it.begin;
+      auto read = [&](int c, uint32_t (&v)[32]) {
+        tmem_ld32(at + first * kBuffers * BX + 32 * c, v);
+        if (kIssuers > 1 && both) {
+          uint32_t w[32];
+          tmem_ld32(at + (first ^ 1) * kBuffers * BX + 32 * c, w);
+#pragma unroll
+          for (int j = 0; j < 32; ++j)
+            v[j] = __float_as_uint(__uint_as_float(v[j]) + __uint_as_float(w[j]));
+        }
+      };
+      auto release = [&] {
+        asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) mbar_arrive(acc_empty(buffer));
+      };
+      auto finish = [&](float acc, int c, int j) {
+        if constexpr (kBack) return acc;
+        else return acc * __shfl_sync(kAllLanes, unit[c], j) * scale + bias;
+      };
+      auto store = [&](int c, int j, float y) {  // one value
+        const int64_t m = m0 + 32 * c + j;
+        if (m < p.rows && n < p.lanes) store_any(p.out, m * p.lanes + n, y, p.out_dtype);
+      };
+      if (p.parts == 1) {
+        if (f32) {
+#pragma unroll
+          for (int c = 0; c < kChunks; ++c) {
+            uint32_t v[32];
+            read(c, v);
+#pragma unroll
+            for (int j = 0; j < 32; ++j) store(c, j, finish(__uint_as_float(v[j]), c, j));
+          }
+          release();
+        } else {
+          // all of the tile to registers, so that the next one can start, then the stores
+          uint32_t keep[kHalf / 2];
+#pragma unroll
+          for (int c = 0; c < kChunks; ++c) {
+            uint32_t v[32];
+            read(c, v);
+#pragma unroll
+            for (int j = 0; j < 32; j += 2) {
+              const float a = finish(__uint_as_float(v[j]), c, j);
+              const float b = finish(__uint_as_float(v[j + 1]), c, j + 1);
+              keep[16 * c + j / 2] = bf16 ? pack2<DQ4_OUT_BF16>(a, b) : pack2<DQ4_OUT_F16>(a, b);
+            }
+          }
+          release();
+          uint16_t* out = static_cast<uint16_t*>(p.out);
+#pragma unroll
+          for (int j = 0; j < kHalf / 2; ++j) {
+            const int64_t m = m0 + 2 * j;
+            if (pairs) {
+              const uint32_t other = __shfl_xor_sync(kAllLanes, keep[j], 1);
+              const uint32_t v = lane & 1 ? __byte_perm(other, keep[j], 0x7632)
+                                          : __byte_perm(keep[j], other, 0x5410);
+              const int64_t row = m + (lane & 1);
+              if (row < p.rows && n < p.lanes)
+                *reinterpret_cast<uint32_t*>(out + row * p.lanes + (n & ~int64_t(1))) = v;
+            } else if (n < p.lanes) {
+              if (m < p.rows) out[m * p.lanes + n] = uint16_t(keep[j]);
+              if (m + 1 < p.rows) out[(m + 1) * p.lanes + n] = uint16_t(keep[j] >> 16);
+            }
+          }
+        }
+        continue;
+      }
+      // ---- a part of the sum; the last of a tile's parts adds them in their order
+      float* part = p.part + (i * BX + half * kHalf) * kTileW + quad * 32 + lane;
+#pragma unroll 1
+      for (int c = 0; c < kChunks; ++c) {
+        uint32_t v[32];
+        read(c, v);
+#pragma unroll
+        for (int j = 0; j < 32; ++j) part[(32 * c + j) * kTileW] = __uint_as_float(v[j]);
+      }
+      release();
+      bar_readers();
+      const int64_t tile = i / p.parts;
+      if (tid == 32 * kProducers) {
+        s_last = atomic_add_acq_rel(p.count + tile, 1) == p.parts - 1;
+        if (s_last) p.count[tile] = 0;  // ready for the next call
+      }
+      bar_readers();
+      if (!s_last) continue;
+      const float* from = p.part + (tile * p.parts * BX + half * kHalf) * kTileW + quad * 32 + lane;
+#pragma unroll
+      for (int c = 0; c < kChunks; ++c) {
+        float sum[32];
+#pragma unroll
+        for (int j = 0; j < 32; ++j) sum[j] = load_l2(from + (32 * c + j) * kTileW);
+        for (int q = 1; q < p.parts; ++q)
+#pragma unroll
+          for (int j = 0; j < 32; ++j)
+            sum[j] += load_l2(from + (int64_t(q) * BX + 32 * c + j) * kTileW);
+#pragma unroll
+        for (int j = 0; j < 32; ++j) store(c, j, finish(sum[j], c, j));
+      }
+    }
+  }
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;"
+                 :: "r"(tmem), "r"(kTmemColumns));
+  }
+}
+
+// ------------------------------------------------------------ rows in FP16 for the product
+struct RowArgs {
+  const int8_t* codes;
+  const float* scales;
+  int64_t M, K, width;  // width: of a row in FP16
+  const int64_t* cols;
+  const void* outliers;
+  int L;
+  bool bf16;
+  uint16_t* X;     // [M][width]
+  float* units;    // [M]
+  int32_t* used;   // [kMaxOutliers]
+  int* bad;
+};
+
+// A row's FP16 values are its codes, times the row's unit u = scale / 127.  An outlier x takes
+// the place of its code as x / u, in two FP16 terms, the second in a column of its own past K,
+// where the weight's column is gathered again.  FP16 ends at 65504: where an outlier is above
+// 2^15 u, the unit is 2^-15 of it, and codes are rounded to FP16 with what they are in it.
+__global__ void __launch_bounds__(256) int8_rows_kernel(const RowArgs p) {
+  __shared__ int64_t s_cols[kMaxOutliers];
+  __shared__ uint32_t s_top[8];
+  wait_for_stream();
+  asm volatile("griddepcontrol.launch_dependents;");
+  const int t = threadIdx.x;
+  int64_t col = -1;  // of entry t, if it is used
+  if (p.L > 0) {
+    if (t < kMaxOutliers) s_cols[t] = t < p.L ? load_global(p.cols + t) : -1;
+    __syncthreads();
+    int wrong = 0;
+    if (t < kMaxOutliers) {
+      int64_t top = -1;
+      for (int l = 0; l < min(t, p.L); ++l)
+        if (s_cols[l] < p.K) top = max(top, s_cols[l]);
+      const int64_t c = s_cols[t];
+      if (c > top && c < p.K) col = c;
+      wrong = col < 0 && c != -1;
+      if (blockIdx.x == 0) p.used[t] = int32_t(col);
+    }
+    if (blockIdx.x == 0 && wrong && p.bad) atomicAdd(p.bad, 1);
+  }
+  const int64_t codes_end = (p.K + kStep - 1) / kStep * kStep;
+  for (int64_t row = blockIdx.x; row < p.M; row += gridDim.x) {
+    float unit = load_global(p.scales + row) * kRecip127, ratio = 1.f, x = 0.f;
+    if (p.L > 0) {
+      if (col >= 0) x = load_16(p.outliers, row * p.L + t, p.bf16);
+      uint32_t top = __reduce_max_sync(kAllLanes, __float_as_uint(x) & 0x7FFFFFFFu);
+      __syncthreads();  // (the last row's has been read)
+      if ((t & 31) == 0) s_top[t >> 5] = top;
+      __syncthreads();
+      for (int w = 0; w < 8; ++w) top = max(top, s_top[w]);
+      const float own = unit;
+      if (top < 0x7F800000u) {
+        unit = fmaxf(fmaxf(unit, __uint_as_float(top) * 3.0517578125e-05f), 7.888609052210118e-31f);
+        ratio = own == unit ? 1.f : __fdiv_rn(own, unit);
+        if (own != own) unit = own;
+      } else {
+        unit = __uint_as_float(0x7FC00000u);
+      }
+    }
+    uint16_t* to = p.X + row * p.width;
+    const int8_t* from = p.codes + row * p.K;
+    for (int64_t k = t * 16; k < codes_end; k += 256 * 16) {
+      uint4 c = make_uint4(0, 0, 0, 0);
+      if (k < p.K) c = load_global(reinterpret_cast<const uint4*>(from + k));
+      const uint32_t* w = reinterpret_cast<const uint32_t*>(&c);
+      uint32_t o[8];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) codes_f16(w[j], o[2 * j], o[2 * j + 1]);
+      if (ratio != 1.f) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          __half2 h;
+          memcpy(&h, &o[j], 4);
+          o[j] = pack2<DQ4_OUT_F16>(__low2float(h) * ratio, __high2float(h) * ratio);
+        }
+      }
+      uint4* y = reinterpret_cast<uint4*>(to + k);
+      y[0] = make_uint4(o[0], o[1], o[2], o[3]);
+      y[1] = make_uint4(o[4], o[5], o[6], o[7]);
+    }
+    if (t == 0) p.units[row] = unit;
+    if (p.L > 0) {
+      __syncthreads();  // the codes are there
+      if (codes_end + t < p.width) {
+        const float v = col >= 0 ? __fdiv_rn(x, unit) : 0.f;
+        const __half high = __float2half_rn(v);
+        if (col >= 0) to[col] = __half_as_ushort(high);
+        to[codes_end + t] = __half_as_ushort(__float2half_rn(v - __half2float(high)));
+      }
+    }
+  }
+}
+
+// ------------------------------------------------------------------------ host side
+int64_t up256(int64_t n) { return (n + 255) / 256 * 256; }
+
+struct Plan {
+  int bx;
+  int64_t tiles_x, tiles;
+  int parts;
+};
+
+// The tile's width and the parts of its sum, by the estimated time, in cycles: a stage takes
+// about 560 at BX 64 (the issuers), 640 at 128 and 1120 at 256 (the MMAs), an item about 5000
+// more to fill the pipeline and read out, and parts have to be written and added.
+Plan plan_gemm(int64_t lanes, int64_t rows, int steps, int sms) {
+  Plan best = {};
+  double best_cost = 1e300;
+  const int stages = (steps + 1) / 2;
+  for (int bx = 64; bx <= 256; bx *= 2) {
+    const int64_t tiles_x = (rows + bx - 1) / bx;
+    const int64_t tiles = tiles_x * ((lanes + kTileW - 1) / kTileW);
+    const double stage = bx == 64 ? 560 : bx == 128 ? 640 : 1120;
+    for (int parts = 1; parts <= 16 && parts <= stages; ++parts) {
+      if (parts > 1 && (tiles * parts > sms || tiles * 4 > kInt8Counters)) break;
+      const double rounds = double((tiles * parts + sms - 1) / sms);
+      double cost = rounds * ((stages + parts - 1) / parts * stage + 5000 + 8.0 * bx);
+      if (parts > 1) cost += 3000 + bx * (20.0 + 6.0 * parts);
+      if (cost < best_cost) {
+        best_cost = cost;
+        best = {bx, tiles_x, tiles, parts};
+      }
+    }
+  }
+  return best;
+}
+
+int encode_2d(CUtensorMap* map, CUtensorMapDataType type, const void* base, int64_t width,
+              int64_t height, int64_t stride_bytes, int box_w, int box_h, bool swizzle) {
+  const EncodeTiled encode = tensor_map_encoder();
+  if (!encode) return fail_cuda(DQ4_ERR_LAUNCH, cudaErrorNotSupported);
+  const cuuint64_t size[2] = {cuuint64_t(width), cuuint64_t(height)};
+  const cuuint64_t stride[1] = {cuuint64_t(stride_bytes)};
+  const cuuint32_t box[2] = {cuuint32_t(box_w), cuuint32_t(box_h)};
+  const cuuint32_t step[2] = {1, 1};
+  const CUresult r =
+      encode(map, type, 2, const_cast<void*>(base), size, stride, box, step,
+             CU_TENSOR_MAP_INTERLEAVE_NONE,
+             swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? DQ4_OK : fail_cuda(DQ4_ERR_LAUNCH, cudaErrorInvalidValue);
+}
+
+template <int BX, bool kBack, bool kBF16>
+int launch_one(const CUtensorMap& w, const CUtensorMap& x, const GemmArgs& p, int dev, int sms,
+               cudaStream_t stream) {
+  auto kernel = dq4_int8_gemm_kernel<BX, kBack, kBF16>;
+  static std::atomic<uint64_t> allowed{0};
+  if (const int st = allow_smem(kernel, Gemm<BX>::kBytes, dev, &allowed)) return st;
+  const unsigned grid = unsigned(p.items < sms ? p.items : sms);
+  return launch_ordered(kernel, dim3(grid), Gemm<BX>::kThreads, Gemm<BX>::kBytes, stream, w, x, p);
+}
+
+template <bool kBack, bool kBF16>
+int launch_bx(int bx, const CUtensorMap& w, const CUtensorMap& x, const GemmArgs& p, int dev,
+              int sms, cudaStream_t stream) {
+  if (bx == 64) return launch_one<64, kBack, kBF16>(w, x, p, dev, sms, stream);
+  if (bx == 128) return launch_one<128, kBack, kBF16>(w, x, p, dev, sms, stream);
+  return launch_one<256, kBack, kBF16>(w, x, p, dev, sms, stream);
+}
+
+// The steps of a row in FP16: of its codes, and of its outliers' second terms.
+int code_steps(int64_t K) { return int((K + kStep - 1) / kStep); }
+int all_steps(int64_t K, int L) { return code_steps(K) + (L + kStep - 1) / kStep; }
+
+int64_t part_bytes(const Plan& pl) {
+  return pl.parts > 1 ? pl.tiles * pl.parts * pl.bx * kTileW * 4 : 0;
+}
+
+}  // namespace
+
+int64_t int8_gemm_workspace(int64_t M, int64_t N, int64_t K, int L, int sms) {
+  const Plan pl = plan_gemm(N, M, all_steps(K, L), sms);
+  return kInt8Counters + up256(kMaxOutliers * 4) + up256(M * 4) +
+         up256(M * all_steps(K, L) * kStep * 2) + part_bytes(pl);
+}
+
+int launch_int8_gemm(const Int8Linear& a, int dev, int sms, void* workspace, cudaStream_t stream) {
+  const int steps = all_steps(a.K, a.L);
+  const Plan pl = plan_gemm(a.N, a.M, steps, sms);
+  char* at = static_cast<char*>(workspace);
+  int* count = reinterpret_cast<int*>(at);
+  at += kInt8Counters;
+  int32_t* used = reinterpret_cast<int32_t*>(at);
+  at += up256(kMaxOutliers * 4);
+  float* units = reinterpret_cast<float*>(at);
+  at += up256(a.M * 4);
+  uint16_t* X = reinterpret_cast<uint16_t*>(at);
+  const int64_t width = int64_t(steps) * kStep;
+  at += up256(a.M * width * 2);
+  CUtensorMap w, x;
+  if (const int st = encode_2d(&w, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.CB, a.K, a.N, a.K, kStage,
+                               kTileW, true))
+    return st;
+  if (const int st = encode_2d(&x, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, X, width, a.M, width * 2, kStep,
+                               pl.bx, true))
+    return st;
+  const RowArgs r = {a.codes, a.scales, a.M, a.K, width, a.cols, a.outliers, a.L, a.outliers_bf16,
+                     X, units, used, a.bad};
+  const int64_t row_ctas = a.M < 8 * sms ? a.M : 8 * sms;
+  if (const int st = launch_ordered(int8_rows_kernel, dim3(unsigned(row_ctas)), 256, 0, stream, r))
+    return st;
+  GemmArgs p = {};
+  p.lanes = p.N = a.N;
+  p.rows = a.M;
+  p.steps = steps;
+  p.code_steps = code_steps(a.K);
+  p.tiles_x = int(pl.tiles_x);
+  p.tiles = pl.tiles;
+  p.parts = pl.parts;
+  p.items = pl.tiles * pl.parts;
+  p.CB = a.CB;
+  p.SCB = a.SCB;
+  p.K = a.K;
+  p.cols = a.L > 0 ? used : nullptr;
+  p.units = units;
+  p.bias = a.bias;
+  p.out_dtype = a.out_dtype;
+  p.out = a.Y;
+  p.part = reinterpret_cast<float*>(at);
+  p.count = count;
+  p.bad = a.bad;
+  return launch_bx<false, false>(pl.bx, w, x, p, dev, sms, stream);
+}
+
+int64_t int8_backward_workspace(int64_t M, int64_t N, int64_t K, int sms) {
+  return kInt8Counters + part_bytes(plan_gemm(K, M, code_steps(N), sms));
+}
+
+int launch_int8_backward(const Int8Backward& a, int dev, int sms, void* workspace,
+                         cudaStream_t stream) {
+  const Plan pl = plan_gemm(a.K, a.M, code_steps(a.N), sms);
+  CUtensorMap w, x;
+  if (const int st = encode_2d(&w, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.CB, a.K, a.N, a.K, kTileW,
+                               kStage, false))
+    return st;
+  if (const int st = encode_2d(&x, a.bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                          : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+                               a.dY, a.N, a.M, a.N * 2, kStep, pl.bx, true))
+    return st;
+  GemmArgs p = {};
+  p.lanes = p.K = a.K;
+  p.N = a.N;
+  p.rows = a.M;
+  p.steps = p.code_steps = code_steps(a.N);
+  p.tiles_x = int(pl.tiles_x);
+  p.tiles = pl.tiles;
+  p.parts = pl.parts;
+  p.items = pl.tiles * pl.parts;
+  p.CB = a.CB;
+  p.SCB = a.SCB;
+  p.out_dtype = a.bf16 ? DQ4_OUT_BF16 : DQ4_OUT_F16;
+  p.out = a.dX;
+  p.part = reinterpret_cast<float*>(static_cast<char*>(workspace) + kInt8Counters);
+  p.count = static_cast<int*>(workspace);
+  p.bad = a.bad;
+  return a.bf16 ? launch_bx<true, true>(pl.bx, w, x, p, dev, sms, stream)
+                : launch_bx<true, false>(pl.bx, w, x, p, dev, sms, stream);
+}
+
+}  // namespace dq4d

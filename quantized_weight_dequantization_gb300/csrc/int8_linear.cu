@@ -4,7 +4,7 @@
 // Few rows are bound by the weight's bytes, each read once: a CTA takes 16 RT weight rows, its
 // warps take turns at chunks of 64 of K, and all operands go from global memory to registers
 // (the rows' codes come from L2, and all CTAs read the same).  Outlier columns are added in FP32.
-#include "int8.cuh"
+#include "int8_gemm.cuh"
 
 namespace dq4d {
 namespace {
@@ -78,6 +78,9 @@ __global__ void __launch_bounds__(32 * kWarps, 2) dq4_int8_few_kernel(const Int8
   }
 }
 
+// Whether a product goes to the kernel for few rows.
+bool few_rows(int64_t M, int64_t K) { return M <= 32 || K == 0; }
+
 template <int RT, int NT, int U>
 int launch_few(const Int8Linear& p, cudaStream_t stream) {
   const dim3 grid(unsigned((p.N + 16 * RT - 1) / (16 * RT)), unsigned((p.M + 8 * NT - 1) / (8 * NT)));
@@ -92,7 +95,12 @@ using namespace dq4d;
 extern "C" {
 
 int64_t dq4_int8_linear_workspace_bytes(int64_t M, int64_t N, int64_t K, int32_t L) {
-  return 0;
+  if (M <= 0 || N <= 0 || K < 0 || L < 0 || L > kMaxOutliers || M > INT32_MAX || N > INT32_MAX ||
+      K > INT32_MAX || few_rows(M, K))
+    return 0;
+  int dev, sms;
+  if (current_device(&dev, &sms) != DQ4_OK) return -DQ4_ERR_DEVICE;
+  return int8_gemm_workspace(M, N, K, L, sms);
 }
 
 int dq4_int8_linear(const int8_t* codes, const float* scales, const int8_t* CB, const float* SCB,
@@ -118,6 +126,12 @@ int dq4_int8_linear(const int8_t* codes, const float* scales, const int8_t* CB, 
   const Int8Linear p = {codes, scales, CB, SCB, M, N, K, cols, outliers, L,
                         L > 0 && outlier_dtype == DQ4_OUT_BF16, bias, out_dtype, Y, bad};
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (!few_rows(M, K)) {
+    if (!workspace || workspace_bytes < int8_gemm_workspace(M, N, K, L, sms))
+      return DQ4_ERR_WORKSPACE;
+    if (misaligned(workspace, 256)) return DQ4_ERR_ALIGN;
+    return launch_int8_gemm(p, dev, sms, workspace, s);
+  }
   if (M <= 8) return launch_few<1, 1, 4>(p, s);
   if (M <= 16) return launch_few<1, 2, 4>(p, s);
   return launch_few<2, 4, 2>(p, s);
