@@ -113,14 +113,14 @@ int64_t dq4_int8_linear_backward_workspace_bytes(int64_t M, int64_t N, int64_t K
  * Activations are FP16 in the products, a power of two for each row keeping them in its range
  * (BF16 rows lose nothing down to 2^-31 of their largest value); the inner values are
  * rounded to FP16's 11 bits.
- * T 0 .. 256, E 1 .. 1024, top_k 1 .. min(E, 32), H % 16 == 0, I % 16 == 0, E * I * H < 2^47;
- * weights 16-byte aligned, X 16-byte aligned with row_stride % 8 == 0.
+ * T 0 .. 256, E 1 .. 1024, top_k 1 .. min(E, 16), H up to 32768 and I up to 2^20, both multiples
+ * of 16, E * I * H < 2^47; weights 16-byte aligned, X 16-byte aligned with row_stride % 8 == 0.
  */
 int dq4_int8_moe(const void* X, int64_t row_stride, int32_t dtype, int64_t T, int64_t H, int64_t I,
                  int64_t E, const float* logits, int32_t top_k, int32_t renormalize,
                  const int8_t* W1, const float* S1, const int8_t* W2, const float* S2,
                  int32_t* ids, float* weights, void* Y, void* workspace,
-                 int64_t workspace_bytes, void* stream);
+                 int64_t workspace_bytes, int* bad, void* stream);
 int64_t dq4_int8_moe_workspace_bytes(int64_t T, int64_t H, int64_t I, int32_t top_k);
 
 #ifdef __cplusplus

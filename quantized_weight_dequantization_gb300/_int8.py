@@ -42,7 +42,7 @@ def _lib() -> ctypes.CDLL:
         L.dq4_int8_linear_backward_workspace_bytes.argtypes = [i64, i64, i64]
         L.dq4_int8_linear_backward_workspace_bytes.restype = i64
         L.dq4_int8_moe.argtypes = [p, i64, i32, i64, i64, i64, i64, p, i32, i32, p, p, p, p, p, p,
-                                   p, p, i64, p]
+                                   p, p, i64, p, p]
         L.dq4_int8_moe.restype = ctypes.c_int
         L.dq4_int8_moe_workspace_bytes.argtypes = [i64, i64, i64, i32]
         L.dq4_int8_moe_workspace_bytes.restype = i64
@@ -281,7 +281,8 @@ def int8_linear_backward(dY: torch.Tensor, CB: torch.Tensor, SCB: torch.Tensor,
 # ------------------------------------------------------------- mixture of experts
 def int8_moe(X: torch.Tensor, logits: torch.Tensor, w1: torch.Tensor, s1: torch.Tensor,
              w2: torch.Tensor, s2: torch.Tensor, top_k: int, renormalize: bool = True,
-             return_routing: bool = False, workspace: Optional[torch.Tensor] = None, stream=None):
+             return_routing: bool = False, workspace: Optional[torch.Tensor] = None,
+             bad: Optional[torch.Tensor] = None, stream=None):
     """A mixture-of-experts layer for few tokens (256 at most) over 8-bit weights.
 
     X is T x H (float16 or bfloat16), ``logits`` T x E (float32).  Each token goes through the
@@ -309,6 +310,7 @@ def int8_moe(X: torch.Tensor, logits: torch.Tensor, w1: torch.Tensor, s1: torch.
     ids = torch.empty((T, top_k), dtype=torch.int32, device=X.device)
     weights = torch.empty((T, top_k), dtype=torch.float32, device=X.device)
     Y = torch.empty((T, H), dtype=X.dtype, device=X.device)
+    bad_ptr = _bad(bad, X)
     index = X.get_device()
     handle = _stream(stream, index)
     need = _need_of(index, "moe", T, H, I, top_k)
@@ -317,7 +319,7 @@ def int8_moe(X: torch.Tensor, logits: torch.Tensor, w1: torch.Tensor, s1: torch.
         st = _lib().dq4_int8_moe(X.data_ptr(), X.stride(0), _DTYPE_CODE[X.dtype], T, H, I, E,
                                  logits_ptr, top_k, renormalize, w1_ptr, s1_ptr, w2_ptr, s2_ptr,
                                  ids.data_ptr(), weights.data_ptr(), Y.data_ptr(), ws_ptr,
-                                 ws_bytes, handle)
+                                 ws_bytes, bad_ptr, handle)
     if st:
         raise Dq4Error(st, "dq4_int8_moe")
     return (Y, ids, weights) if return_routing else Y

@@ -18,8 +18,6 @@
 // Waits are bounded; one that runs out counts into *bad, raises a flag of the CTA, and every
 // role lets its copies and MMAs finish and ends.
 #include "int8_gemm.cuh"
-#include "tcgen05.cuh"
-#include "tmap.cuh"
 
 namespace dq4d {
 namespace {
@@ -34,7 +32,7 @@ constexpr uint32_t kRingCol = 256;   // where they start; the accumulators lie b
 constexpr uint32_t kTmemColumns = 512;
 constexpr int kProducers = 8, kReaders = 8;
 
-template <int BX>
+template <int BX, bool kBack>
 struct Gemm {
   static constexpr int kIssuers = BX < 256 ? 2 : 1;
   static constexpr int kBuffers = 256 / (BX * kIssuers);  // accumulators of an issuer
@@ -43,14 +41,15 @@ struct Gemm {
   static constexpr int kSlotSteps = kIssuers;
   static constexpr int kStepBytes = BX * kStep * 2;
   static constexpr int kSlot = kSlotSteps * kStepBytes;
-  static constexpr int kSlots = BX == 256 ? 5 : BX == 128 ? 4 : 6;
+  static constexpr int kSlots = BX == 256 ? (kBack ? 4 : 5) : BX == 128 ? 4 : 6;
   static_assert(kIssuers == 1 || kSlots % 2 == 0, "a slot belongs to one issuer");
   static constexpr int kThreads = 32 * (kProducers + kReaders + kIssuers + 2);
   static constexpr int kRawAt = kSlots * kSlot;
   static constexpr int kBarsAt = kRawAt + kRawSlots * kRawSlot;
   static constexpr int kBars = 2 * kSlots + 2 * kRawSlots + 2 * kRing + 2 * kBuffers + 1;
   static constexpr int kBytes = kBarsAt + 8 * kBars + 1024;  // + alignment slack
-  static_assert(kBytes + 1600 <= 227 * 1024, "shared memory budget");
+  static constexpr int kStatic = kBack ? 16 * kStage + 64 : 4 * kMaxOutliers + 64;
+  static_assert(kBytes + kStatic <= 227 * 1024, "shared memory budget");
   static_assert(kBytes > 116 * 1024, "one CTA per SM: the TMEM allocation never waits");
 };
 
@@ -125,10 +124,10 @@ struct Place {
 // kBack: lanes are columns of the weight, the sum runs over its rows.  kBF16: 16-bit values are
 // BF16 (the gradient's), else FP16.
 template <int BX, bool kBack, bool kBF16>
-__global__ void __launch_bounds__(Gemm<BX>::kThreads, 1)
+__global__ void __launch_bounds__(Gemm<BX, kBack>::kThreads, 1)
     dq4_int8_gemm_kernel(const __grid_constant__ CUtensorMap map_w,
                          const __grid_constant__ CUtensorMap map_x, const GemmArgs p) {
-  using S = Gemm<BX>;
+  using S = Gemm<BX, kBack>;
   constexpr int kIssuers = S::kIssuers, kBuffers = S::kBuffers, kSlots = S::kSlots;
   constexpr int kOut = kBF16 ? DQ4_OUT_BF16 : DQ4_OUT_F16;
   constexpr int kMmaWarp = kProducers + kReaders;
@@ -136,7 +135,7 @@ __global__ void __launch_bounds__(Gemm<BX>::kThreads, 1)
   __shared__ uint32_t s_tmem;
   __shared__ volatile int s_abort;
   __shared__ bool s_last;
-  __shared__ int s_cols[kMaxOutliers];
+  __shared__ int s_cols[kBack ? 1 : kMaxOutliers];
   __shared__ __align__(16) float s_scale[kBack ? 4 * kStage : 4];  // two stages of each group
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
@@ -734,30 +733,14 @@ Plan plan_gemm(int64_t lanes, int64_t rows, int steps, int sms) {
   return best;
 }
 
-int encode_2d(CUtensorMap* map, CUtensorMapDataType type, const void* base, int64_t width,
-              int64_t height, int64_t stride_bytes, int box_w, int box_h, bool swizzle) {
-  const EncodeTiled encode = tensor_map_encoder();
-  if (!encode) return fail_cuda(DQ4_ERR_LAUNCH, cudaErrorNotSupported);
-  const cuuint64_t size[2] = {cuuint64_t(width), cuuint64_t(height)};
-  const cuuint64_t stride[1] = {cuuint64_t(stride_bytes)};
-  const cuuint32_t box[2] = {cuuint32_t(box_w), cuuint32_t(box_h)};
-  const cuuint32_t step[2] = {1, 1};
-  const CUresult r =
-      encode(map, type, 2, const_cast<void*>(base), size, stride, box, step,
-             CU_TENSOR_MAP_INTERLEAVE_NONE,
-             swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
-             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS ? DQ4_OK : fail_cuda(DQ4_ERR_LAUNCH, cudaErrorInvalidValue);
-}
-
 template <int BX, bool kBack, bool kBF16>
 int launch_one(const CUtensorMap& w, const CUtensorMap& x, const GemmArgs& p, int dev, int sms,
                cudaStream_t stream) {
   auto kernel = dq4_int8_gemm_kernel<BX, kBack, kBF16>;
   static std::atomic<uint64_t> allowed{0};
-  if (const int st = allow_smem(kernel, Gemm<BX>::kBytes, dev, &allowed)) return st;
+  if (const int st = allow_smem(kernel, Gemm<BX, kBack>::kBytes, dev, &allowed)) return st;
   const unsigned grid = unsigned(p.items < sms ? p.items : sms);
-  return launch_ordered(kernel, dim3(grid), Gemm<BX>::kThreads, Gemm<BX>::kBytes, stream, w, x, p);
+  return launch_ordered(kernel, dim3(grid), Gemm<BX, kBack>::kThreads, Gemm<BX, kBack>::kBytes, stream, w, x, p);
 }
 
 template <bool kBack, bool kBF16>
@@ -799,10 +782,10 @@ int launch_int8_gemm(const Int8Linear& a, int dev, int sms, void* workspace, cud
   at += up256(a.M * width * 2);
   CUtensorMap w, x;
   if (const int st = encode_2d(&w, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.CB, a.K, a.N, a.K, kStage,
-                               kTileW, true))
+                               kTileW, CU_TENSOR_MAP_SWIZZLE_128B))
     return st;
   if (const int st = encode_2d(&x, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, X, width, a.M, width * 2, kStep,
-                               pl.bx, true))
+                               pl.bx, CU_TENSOR_MAP_SWIZZLE_128B))
     return st;
   const RowArgs r = {a.codes, a.scales, a.M, a.K, width, a.cols, a.outliers, a.L, a.outliers_bf16,
                      X, units, used, a.bad};
@@ -841,11 +824,11 @@ int launch_int8_backward(const Int8Backward& a, int dev, int sms, void* workspac
   const Plan pl = plan_gemm(a.K, a.M, code_steps(a.N), sms);
   CUtensorMap w, x;
   if (const int st = encode_2d(&w, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.CB, a.K, a.N, a.K, kTileW,
-                               kStage, false))
+                               kStage, CU_TENSOR_MAP_SWIZZLE_NONE))
     return st;
   if (const int st = encode_2d(&x, a.bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
                                           : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
-                               a.dY, a.N, a.M, a.N * 2, kStep, pl.bx, true))
+                               a.dY, a.N, a.M, a.N * 2, kStep, pl.bx, CU_TENSOR_MAP_SWIZZLE_128B))
     return st;
   GemmArgs p = {};
   p.lanes = p.K = a.K;

@@ -8,7 +8,6 @@
 // The maximum is taken on the bits of |x|, two values an instruction: for values that are not
 // negative the order of the bits is that of the numbers, infinity and NaN last.
 #include "int8.cuh"
-#include "tcgen05.cuh"
 
 namespace dq4d {
 namespace {

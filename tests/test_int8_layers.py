@@ -96,12 +96,12 @@ def test_moe_refusals(lib):
         assert lib.dq4_int8_moe_workspace_bytes(*shape) == 0
 
     def call(X=P, stride=64, dt=0, T=4, H=64, I=32, E=8, logits=P, k=2, w1=P, s1=P, w2=P, s2=P,
-             ids=P, weights=P, Y=P, ws=P, nbytes=need):
+             ids=P, weights=P, Y=P, ws=P, nbytes=need, bad=P):
         return lib.dq4_int8_moe(X, stride, dt, T, H, I, E, logits, k, 1, w1, s1, w2, s2, ids,
-                                weights, Y, ws, nbytes, None)
+                                weights, Y, ws, nbytes, bad, None)
     for kw in ({"T": -1}, {"T": 257}, {"E": 0}, {"E": 1025}, {"k": 0}, {"k": 17, "E": 32},
                {"k": 9}, {"H": 72}, {"I": 40}, {"H": 1 << 16}, {"I": 0},
-               {"E": 1024, "H": 1 << 15, "I": 1 << 24}):
+               {"E": 1024, "H": 1 << 15, "I": 1 << 21}):
         assert call(**kw) == N_, kw
     assert call(dt=2) == DTYPE
     assert call(T=0, X=None) == OK
@@ -109,7 +109,7 @@ def test_moe_refusals(lib):
         assert call(**{name: None}) == NULL, name
     for kw in ({"X": P + 8}, {"stride": 68}, {"logits": P + 2}, {"w1": P + 8}, {"w2": P + 8},
                {"s1": P + 2}, {"s2": P + 2}, {"ids": P + 2}, {"weights": P + 2}, {"Y": P + 1},
-               {"ws": P + 16}):
+               {"ws": P + 16}, {"bad": P + 2}):
         assert call(**kw) == ALIGN, kw
     assert call(ws=None) == WORKSPACE and call(nbytes=need - 1) == WORKSPACE
 
