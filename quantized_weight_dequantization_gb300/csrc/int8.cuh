@@ -287,8 +287,9 @@ struct Streamed {
   }
 
   // The barriers of this warp's ring: before anything else.
-  static __device__ __forceinline__ void setup(uint8_t* smem) {
+  static __device__ __forceinline__ void setup(uint8_t* smem, const CUtensorMap& map_w) {
     if ((threadIdx.x & 31) == 0) {
+      asm volatile("prefetch.tensormap [%0];" :: "l"(reinterpret_cast<uint64_t>(&map_w)));
       const uint32_t bars = smem_u32(smem) + kBarsAt + (threadIdx.x >> 5) * kDepth * 8;
       for (int i = 0; i < kDepth; ++i) mbar_init(bars + 8 * i, 1);
       asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");

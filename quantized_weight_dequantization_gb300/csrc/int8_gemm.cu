@@ -58,18 +58,17 @@ struct GemmArgs {
   int steps, code_steps; // K steps, and of them with codes from CB (the rest: outlier columns)
   int tiles_x;           // tiles along the activations
   int64_t tiles;
-  int parts;             // of a tile's sum
-  int64_t items;         // tiles * parts
+  int64_t units;         // tiles * stages, if CTAs take equal runs of them; 0: whole tiles in turn
   const int8_t* CB;
   const float* SCB;
   int64_t K, N;
   const int32_t* cols;   // the outlier columns that are used, -1 for none
-  const float* units;    // of the activation rows
+  const float* row_units;  // of the activation rows
   const void* bias;
   int out_dtype;
   void* out;             // [rows][lanes]
-  float* part;           // [items][BX][128]
-  int* count;            // [tiles]
+  float4* part;          // [CTAs][2][BX / 4][128]: a CTA's parts of its first and its last tile
+  int* count;            // [CTAs] parts of the tile whose last one the CTA has
   int* bad;
 };
 
@@ -197,23 +196,36 @@ __global__ void __launch_bounds__(Gemm<BX, kBack>::kThreads, 1)
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
   const uint32_t tmem = s_tmem;
 
-  // An item: its tile's lanes and rows, its stages.  Every role walks the CTA's items; stages are
-  // counted over all of them (g), and stage g is group and issuer g % 2's, in slot g % depth.
+  // An item: a tile, or the part of it that falls to this CTA.  Every role walks the CTA's items;
+  // stages are counted over all of them (g), and stage g is group and issuer g % 2's, in slot
+  // g % depth.
   struct Item {
-    int64_t lane0, row0;
+    int64_t tile, lane0, row0;
     int begin, end;  // stages
   };
   const int stages = (p.steps + 1) / 2;
-  auto item_at = [&](int64_t i) {
-    Item it;
-    const int64_t tile = i / p.parts;
-    const int part = int(i - tile * p.parts);
-    const int64_t tw = tile / p.tiles_x;
+  const int64_t ctas = gridDim.x;
+  auto begin_of = [&](int64_t cta) { return cta * p.units / ctas; };
+  auto cta_of = [&](int64_t u) { return ((u + 1) * ctas - 1) / p.units; };
+  const int64_t walk0 = p.units ? begin_of(blockIdx.x) : blockIdx.x;
+  const int64_t walk1 = p.units ? begin_of(blockIdx.x + 1) : p.tiles;
+  auto next_item = [&](int64_t& at, Item& it) {
+    if (at >= walk1) return false;
+    it.tile = at;
+    it.begin = 0;
+    it.end = stages;
+    if (p.units) {
+      it.tile = at / stages;
+      it.begin = int(at - it.tile * stages);
+      it.end = int(min(int64_t(stages), it.begin + walk1 - at));
+      at += it.end - it.begin;
+    } else {
+      at += ctas;
+    }
+    const int64_t tw = it.tile / p.tiles_x;
     it.lane0 = tw * kTileW;
-    it.row0 = (tile - tw * p.tiles_x) * BX;
-    it.begin = int(int64_t(stages) * part / p.parts);
-    it.end = int(int64_t(stages) * (part + 1) / p.parts);
-    return it;
+    it.row0 = (it.tile - tw * p.tiles_x) * BX;
+    return true;
   };
   auto steps_of = [&](int stage) { return min(2, p.steps - 2 * stage); };
 
@@ -224,8 +236,8 @@ __global__ void __launch_bounds__(Gemm<BX, kBack>::kThreads, 1)
       Place<kRawSlots> at;
       int g = 0;
       bool stop = false;
-      for (int64_t i = blockIdx.x; i < p.items && !stop; i += gridDim.x) {
-        const Item it = item_at(i);
+      Item it;
+      for (int64_t walk = walk0; !stop && next_item(walk, it);) {
         for (int s = it.begin; s < it.end; ++s, ++g, at.next()) {
           if (g >= kRawSlots && (*aborted || !mbar_wait(raw_empty(at.slot), at.phase ^ 1u))) {
             if (!*aborted) fail();
@@ -251,8 +263,8 @@ __global__ void __launch_bounds__(Gemm<BX, kBack>::kThreads, 1)
       Place<kSlots> at;
       int q = 0;
       bool stop = false;
-      for (int64_t i = blockIdx.x; i < p.items && !stop; i += gridDim.x) {
-        const Item it = item_at(i);
+      Item it;
+      for (int64_t walk = walk0; !stop && next_item(walk, it);) {
         for (int s = it.begin; s < it.end && !stop; ++s) {
           const int n = steps_of(s);
           for (int sub = 0; sub < n; sub += S::kSlotSteps, ++q, at.next()) {
@@ -282,8 +294,8 @@ __global__ void __launch_bounds__(Gemm<BX, kBack>::kThreads, 1)
       Place<kSlots> xp;
       int g = 0, buffer = 0, turn = 0;
       bool stop = false;
-      for (int64_t i = blockIdx.x; i < p.items && !stop; i += gridDim.x, ++turn) {
-        const Item it = item_at(i);
+      Item it;
+      for (int64_t walk = walk0; !stop && next_item(walk, it); ++turn) {
         buffer = turn % kBuffers;
         if (turn >= kBuffers && (*aborted || !mbar_wait(acc_empty(buffer),
                                                         uint32_t(turn / kBuffers - 1) & 1u))) {
@@ -298,19 +310,33 @@ __global__ void __launch_bounds__(Gemm<BX, kBack>::kThreads, 1)
             xp.next();
             continue;
           }
-          if (*aborted || !mbar_wait(w_full(wp.slot), wp.phase)) {
-            if (!*aborted) fail();
-            stop = true;
-            break;
-          }
-          for (int sub = 0; sub < n; ++sub) {
-            const int in_slot = sub % S::kSlotSteps;
-            if (in_slot == 0 && !mbar_wait(x_full(xp.slot), xp.phase)) {
-              fail();
+          // the weight's values and the activations, looked at together first: a look costs the
+          // issuing thread about 40 cycles, a wait for what is there 110, and the MMAs wait with it
+          constexpr int kLooks = kIssuers == 1 ? 2 : 1;
+          Place<kSlots> xn = xp;
+          bool ready = mbar_test(w_full(wp.slot), wp.phase);
+#pragma unroll
+          for (int k = 0; k < kLooks; ++k)
+            if (k < n) {
+              ready &= mbar_test(x_full(xn.slot), xn.phase);
+              xn.next();
+            }
+          if (!ready) {
+            xn = xp;
+            bool ok = !*aborted && mbar_wait(w_full(wp.slot), wp.phase);
+            for (int k = 0; k < kLooks && k < n && ok; ++k, xn.next())
+              ok = mbar_wait(x_full(xn.slot), xn.phase);
+            if (!ok) {
+              if (!*aborted) fail();
               stop = true;
               break;
             }
-            asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+          }
+          asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+#pragma unroll
+          for (int sub = 0; sub < 2; ++sub) {
+            if (sub >= n) break;
+            const int in_slot = sub % S::kSlotSteps;
             const uint32_t a = tmem + kRingCol + (wp.slot * 2 + sub) * 32;
             const uint32_t b = sbase + xp.slot * S::kSlot + in_slot * S::kStepBytes;
 #pragma unroll
@@ -326,7 +352,6 @@ __global__ void __launch_bounds__(Gemm<BX, kBack>::kThreads, 1)
               xp.next();
             }
           }
-          if (stop) break;
           commit(w_empty(wp.slot));
         }
         if (stop) break;
@@ -351,8 +376,8 @@ __global__ void __launch_bounds__(Gemm<BX, kBack>::kThreads, 1)
       const int64_t n = int64_t(s) * kStage + r;
       return n < p.N ? load_global(p.SCB + n) : 0.f;
     };
-    for (int64_t i = blockIdx.x; i < p.items && !stop; i += gridDim.x) {
-      const Item it = item_at(i);
+    Item it;
+    for (int64_t walk = walk0; !stop && next_item(walk, it);) {
       for (int s = it.begin; s < it.end; ++s, ++g, wp.next(), rp.next()) {
         if ((g & 1) != group) continue;
         if constexpr (kBack) {
@@ -469,8 +494,8 @@ __global__ void __launch_bounds__(Gemm<BX, kBack>::kThreads, 1)
     // two lanes exchange a value, so that a store takes four bytes
     const bool pairs = !f32 && p.lanes % 2 == 0 && (reinterpret_cast<uintptr_t>(p.out) & 3) == 0;
     int turn = 0, g = 0;
-    for (int64_t i = blockIdx.x; i < p.items; i += gridDim.x, ++turn) {
-      const Item it = item_at(i);
+    Item it;
+    for (int64_t walk = walk0; next_item(walk, it); ++turn) {
       const int buffer = turn % kBuffers;
       const int64_t n = it.lane0 + quad * 32 + lane, m0 = it.row0 + half * kHalf;
       float scale = 1.f, bias = 0.f, unit[kChunks];
@@ -481,7 +506,7 @@ __global__ void __launch_bounds__(Gemm<BX, kBack>::kThreads, 1)
         }
 #pragma unroll
         for (int c = 0; c < kChunks; ++c)
-          unit[c] = m0 + 32 * c + lane < p.rows ? load_global(p.units + m0 + 32 * c + lane) : 0.f;
+          unit[c] = m0 + 32 * c + lane < p.rows ? load_global(p.row_units + m0 + 32 * c + lane) : 0.f;
       }
       const bool ok = !*aborted && mbar_wait(acc_full(buffer), uint32_t(turn / kBuffers) & 1u) &&
                       !*aborted;
@@ -511,22 +536,52 @@ __global__ void __launch_bounds__(Gemm<BX, kBack>::kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(acc_empty(buffer));
       };
-      auto finish = [&](float acc, int c, int j) {
-        if constexpr (kBack) return acc;
-        else return acc * __shfl_sync(kAllLanes, unit[c], j) * scale + bias;
+      auto finish = [&](uint32_t acc, int c, int j) {
+        if constexpr (kBack) return __uint_as_float(acc);
+        else return __uint_as_float(acc) * __shfl_sync(kAllLanes, unit[c], j) * scale + bias;
       };
-      auto store = [&](int c, int j, float y) {  // one value
-        const int64_t m = m0 + 32 * c + j;
-        if (m < p.rows && n < p.lanes) store_any(p.out, m * p.lanes + n, y, p.out_dtype);
+      // 32 columns (activation rows) from c on: to the output's type, two in a word
+      auto pack = [&](const uint32_t (&v)[32], int c, uint32_t* to) {
+#pragma unroll
+        for (int j = 0; j < 32; j += 2) {
+          const float a = finish(v[j], c, j), b = finish(v[j + 1], c, j + 1);
+          to[j / 2] = bf16 ? pack2<DQ4_OUT_BF16>(a, b) : pack2<DQ4_OUT_F16>(a, b);
+        }
       };
-      if (p.parts == 1) {
+      auto store = [&](const uint32_t* from, int c) {
+        uint16_t* out = static_cast<uint16_t*>(p.out);
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+          const int64_t m = m0 + 32 * c + 2 * j;
+          if (pairs) {
+            const uint32_t other = __shfl_xor_sync(kAllLanes, from[j], 1);
+            const uint32_t v = lane & 1 ? __byte_perm(other, from[j], 0x7632)
+                                        : __byte_perm(from[j], other, 0x5410);
+            const int64_t row = m + (lane & 1);
+            if (row < p.rows && n < p.lanes)
+              *reinterpret_cast<uint32_t*>(out + row * p.lanes + (n & ~int64_t(1))) = v;
+          } else if (n < p.lanes) {
+            if (m < p.rows) out[m * p.lanes + n] = uint16_t(from[j]);
+            if (m + 1 < p.rows) out[(m + 1) * p.lanes + n] = uint16_t(from[j] >> 16);
+          }
+        }
+      };
+      auto store_f32 = [&](const uint32_t (&v)[32], int c) {
+        float* out = static_cast<float*>(p.out);
+#pragma unroll
+        for (int j = 0; j < 32; ++j) {
+          const int64_t m = m0 + 32 * c + j;
+          const float y = finish(v[j], c, j);
+          if (m < p.rows && n < p.lanes) out[m * p.lanes + n] = y;
+        }
+      };
+      if (it.begin == 0 && it.end == stages) {
         if (f32) {
 #pragma unroll
           for (int c = 0; c < kChunks; ++c) {
             uint32_t v[32];
             read(c, v);
-#pragma unroll
-            for (int j = 0; j < 32; ++j) store(c, j, finish(__uint_as_float(v[j]), c, j));
+            store_f32(v, c);
           }
           release();
         } else {
@@ -536,63 +591,68 @@ __global__ void __launch_bounds__(Gemm<BX, kBack>::kThreads, 1)
           for (int c = 0; c < kChunks; ++c) {
             uint32_t v[32];
             read(c, v);
-#pragma unroll
-            for (int j = 0; j < 32; j += 2) {
-              const float a = finish(__uint_as_float(v[j]), c, j);
-              const float b = finish(__uint_as_float(v[j + 1]), c, j + 1);
-              keep[16 * c + j / 2] = bf16 ? pack2<DQ4_OUT_BF16>(a, b) : pack2<DQ4_OUT_F16>(a, b);
-            }
+            pack(v, c, keep + 16 * c);
           }
           release();
-          uint16_t* out = static_cast<uint16_t*>(p.out);
 #pragma unroll
-          for (int j = 0; j < kHalf / 2; ++j) {
-            const int64_t m = m0 + 2 * j;
-            if (pairs) {
-              const uint32_t other = __shfl_xor_sync(kAllLanes, keep[j], 1);
-              const uint32_t v = lane & 1 ? __byte_perm(other, keep[j], 0x7632)
-                                          : __byte_perm(keep[j], other, 0x5410);
-              const int64_t row = m + (lane & 1);
-              if (row < p.rows && n < p.lanes)
-                *reinterpret_cast<uint32_t*>(out + row * p.lanes + (n & ~int64_t(1))) = v;
-            } else if (n < p.lanes) {
-              if (m < p.rows) out[m * p.lanes + n] = uint16_t(keep[j]);
-              if (m + 1 < p.rows) out[(m + 1) * p.lanes + n] = uint16_t(keep[j] >> 16);
-            }
-          }
+          for (int c = 0; c < kChunks; ++c) store(keep + 16 * c, c);
         }
         continue;
       }
-      // ---- a part of the sum; the last of a tile's parts adds them in their order
-      float* part = p.part + (i * BX + half * kHalf) * kTileW + quad * 32 + lane;
+      // ---- a part of the sum (the CTA's first if the tile began before it, else its last); the
+      // last of a tile's parts adds them, in their order
+      auto part_at = [&](int64_t cta, int which) {
+        return p.part + ((cta * 2 + which) * (BX / 4) + half * (kHalf / 4)) * kTileW + quad * 32 + lane;
+      };
+      float4* part = part_at(blockIdx.x, it.begin == 0);
 #pragma unroll 1
       for (int c = 0; c < kChunks; ++c) {
         uint32_t v[32];
         read(c, v);
 #pragma unroll
-        for (int j = 0; j < 32; ++j) part[(32 * c + j) * kTileW] = __uint_as_float(v[j]);
+        for (int j = 0; j < 8; ++j)
+          part[(8 * c + j) * kTileW] =
+              make_float4(__uint_as_float(v[4 * j]), __uint_as_float(v[4 * j + 1]),
+                          __uint_as_float(v[4 * j + 2]), __uint_as_float(v[4 * j + 3]));
       }
       release();
       bar_readers();
-      const int64_t tile = i / p.parts;
+      const int64_t cta0 = cta_of(it.tile * stages), cta1 = cta_of((it.tile + 1) * stages - 1);
       if (tid == 32 * kProducers) {
-        s_last = atomic_add_acq_rel(p.count + tile, 1) == p.parts - 1;
-        if (s_last) p.count[tile] = 0;  // ready for the next call
+        s_last = atomic_add_acq_rel(p.count + cta1, 1) == int(cta1 - cta0);
+        if (s_last) p.count[cta1] = 0;  // ready for the next call
       }
       bar_readers();
       if (!s_last) continue;
-      const float* from = p.part + (tile * p.parts * BX + half * kHalf) * kTileW + quad * 32 + lane;
 #pragma unroll
       for (int c = 0; c < kChunks; ++c) {
-        float sum[32];
+        float4 sum[8];
+        const float4* from = part_at(cta0, 1) + 8 * c * kTileW;
 #pragma unroll
-        for (int j = 0; j < 32; ++j) sum[j] = load_l2(from + (32 * c + j) * kTileW);
-        for (int q = 1; q < p.parts; ++q)
+        for (int j = 0; j < 8; ++j) sum[j] = load_l2(from + j * kTileW);
+#pragma unroll 1
+        for (int64_t cta = cta0 + 1; cta <= cta1; ++cta) {
+          from = part_at(cta, 0) + 8 * c * kTileW;
+          float4 more[8];
 #pragma unroll
-          for (int j = 0; j < 32; ++j)
-            sum[j] += load_l2(from + (int64_t(q) * BX + 32 * c + j) * kTileW);
+          for (int j = 0; j < 8; ++j) more[j] = load_l2(from + j * kTileW);
 #pragma unroll
-        for (int j = 0; j < 32; ++j) store(c, j, finish(sum[j], c, j));
+          for (int j = 0; j < 8; ++j) {
+            sum[j].x += more[j].x;
+            sum[j].y += more[j].y;
+            sum[j].z += more[j].z;
+            sum[j].w += more[j].w;
+          }
+        }
+        uint32_t v[32];
+        memcpy(v, sum, sizeof(v));
+        if (f32) {
+          store_f32(v, c);
+        } else {
+          uint32_t keep[16];
+          pack(v, c, keep);
+          store(keep, c);
+        }
       }
     }
   }
@@ -703,14 +763,16 @@ __global__ void __launch_bounds__(256) int8_rows_kernel(const RowArgs p) {
 int64_t up256(int64_t n) { return (n + 255) / 256 * 256; }
 
 struct Plan {
-  int bx;
+  int bx, stages;
   int64_t tiles_x, tiles;
-  int parts;
+  int ctas;
+  bool split;  // equal runs of stages, else whole tiles
 };
 
-// The tile's width and the parts of its sum, by the estimated time, in cycles: a stage takes
-// about 560 at BX 64 (the issuers), 640 at 128 and 1120 at 256 (the MMAs), an item about 5000
-// more to fill the pipeline and read out, and parts have to be written and added.
+// The tile's width, and whether CTAs take whole tiles or equal runs of stages, by the estimated
+// time in cycles: a stage takes about 560 at BX 64 (the issuers), 640 at 128 and 1120 at 256 (the
+// MMAs), the end of a tile some more where its accumulator is the only one, a CTA 5000 to start
+// and end, and parts of tiles have to be written and added.
 Plan plan_gemm(int64_t lanes, int64_t rows, int steps, int sms) {
   Plan best = {};
   double best_cost = 1e300;
@@ -719,36 +781,44 @@ Plan plan_gemm(int64_t lanes, int64_t rows, int steps, int sms) {
     const int64_t tiles_x = (rows + bx - 1) / bx;
     const int64_t tiles = tiles_x * ((lanes + kTileW - 1) / kTileW);
     const double stage = bx == 64 ? 560 : bx == 128 ? 640 : 1120;
-    for (int parts = 1; parts <= 16 && parts <= stages; ++parts) {
-      if (parts > 1 && (tiles * parts > sms || tiles * 4 > kInt8Counters)) break;
-      const double rounds = double((tiles * parts + sms - 1) / sms);
-      double cost = rounds * ((stages + parts - 1) / parts * stage + 5000 + 8.0 * bx);
-      if (parts > 1) cost += 3000 + bx * (20.0 + 6.0 * parts);
-      if (cost < best_cost) {
-        best_cost = cost;
-        best = {bx, tiles_x, tiles, parts};
-      }
+    const double end = bx == 64 ? 200 : bx == 128 ? 1500 : 1500;
+    const double rounds = double((tiles + sms - 1) / sms);
+    double cost = rounds * (stages * stage + end) + 5000;
+    if (cost < best_cost) {
+      best_cost = cost;
+      best = {bx, stages, tiles_x, tiles, int(tiles < sms ? tiles : sms), false};
+    }
+    const int64_t units = tiles * stages;
+    const int ctas = int(units < sms ? units : sms);
+    const double run = double(units) / ctas, sharers = stages / run + 1;
+    cost = (run + 1) * stage + (run / stages + 1) * end + 5000 + 4000 + bx * (15 + 5 * sharers);
+    if (cost < best_cost) {
+      best_cost = cost;
+      best = {bx, stages, tiles_x, tiles, ctas, true};
     }
   }
   return best;
 }
 
 template <int BX, bool kBack, bool kBF16>
-int launch_one(const CUtensorMap& w, const CUtensorMap& x, const GemmArgs& p, int dev, int sms,
+int launch_one(const CUtensorMap& w, const CUtensorMap& x, const GemmArgs& p, int dev, int ctas,
                cudaStream_t stream) {
   auto kernel = dq4_int8_gemm_kernel<BX, kBack, kBF16>;
   static std::atomic<uint64_t> allowed{0};
   if (const int st = allow_smem(kernel, Gemm<BX, kBack>::kBytes, dev, &allowed)) return st;
-  const unsigned grid = unsigned(p.items < sms ? p.items : sms);
-  return launch_ordered(kernel, dim3(grid), Gemm<BX, kBack>::kThreads, Gemm<BX, kBack>::kBytes, stream, w, x, p);
+  return launch_ordered(kernel, dim3(unsigned(ctas)), Gemm<BX, kBack>::kThreads, Gemm<BX, kBack>::kBytes, stream, w, x, p);
 }
 
 template <bool kBack, bool kBF16>
-int launch_bx(int bx, const CUtensorMap& w, const CUtensorMap& x, const GemmArgs& p, int dev,
-              int sms, cudaStream_t stream) {
-  if (bx == 64) return launch_one<64, kBack, kBF16>(w, x, p, dev, sms, stream);
-  if (bx == 128) return launch_one<128, kBack, kBF16>(w, x, p, dev, sms, stream);
-  return launch_one<256, kBack, kBF16>(w, x, p, dev, sms, stream);
+int launch_plan(const Plan& pl, const CUtensorMap& w, const CUtensorMap& x, GemmArgs p, int dev,
+                void* part, cudaStream_t stream) {
+  p.tiles_x = int(pl.tiles_x);
+  p.tiles = pl.tiles;
+  p.units = pl.split ? pl.tiles * pl.stages : 0;
+  p.part = static_cast<float4*>(part);
+  if (pl.bx == 64) return launch_one<64, kBack, kBF16>(w, x, p, dev, pl.ctas, stream);
+  if (pl.bx == 128) return launch_one<128, kBack, kBF16>(w, x, p, dev, pl.ctas, stream);
+  return launch_one<256, kBack, kBF16>(w, x, p, dev, pl.ctas, stream);
 }
 
 // The steps of a row in FP16: of its codes, and of its outliers' second terms.
@@ -756,7 +826,7 @@ int code_steps(int64_t K) { return int((K + kStep - 1) / kStep); }
 int all_steps(int64_t K, int L) { return code_steps(K) + (L + kStep - 1) / kStep; }
 
 int64_t part_bytes(const Plan& pl) {
-  return pl.parts > 1 ? pl.tiles * pl.parts * pl.bx * kTileW * 4 : 0;
+  return pl.split ? int64_t(pl.ctas) * 2 * pl.bx * kTileW * 4 : 0;
 }
 
 }  // namespace
@@ -797,22 +867,17 @@ int launch_int8_gemm(const Int8Linear& a, int dev, int sms, void* workspace, cud
   p.rows = a.M;
   p.steps = steps;
   p.code_steps = code_steps(a.K);
-  p.tiles_x = int(pl.tiles_x);
-  p.tiles = pl.tiles;
-  p.parts = pl.parts;
-  p.items = pl.tiles * pl.parts;
   p.CB = a.CB;
   p.SCB = a.SCB;
   p.K = a.K;
   p.cols = a.L > 0 ? used : nullptr;
-  p.units = units;
+  p.row_units = units;
   p.bias = a.bias;
   p.out_dtype = a.out_dtype;
   p.out = a.Y;
-  p.part = reinterpret_cast<float*>(at);
   p.count = count;
   p.bad = a.bad;
-  return launch_bx<false, false>(pl.bx, w, x, p, dev, sms, stream);
+  return launch_plan<false, false>(pl, w, x, p, dev, at, stream);
 }
 
 int64_t int8_backward_workspace(int64_t M, int64_t N, int64_t K, int sms) {
@@ -835,19 +900,15 @@ int launch_int8_backward(const Int8Backward& a, int dev, int sms, void* workspac
   p.N = a.N;
   p.rows = a.M;
   p.steps = p.code_steps = code_steps(a.N);
-  p.tiles_x = int(pl.tiles_x);
-  p.tiles = pl.tiles;
-  p.parts = pl.parts;
-  p.items = pl.tiles * pl.parts;
   p.CB = a.CB;
   p.SCB = a.SCB;
   p.out_dtype = a.bf16 ? DQ4_OUT_BF16 : DQ4_OUT_F16;
   p.out = a.dX;
-  p.part = reinterpret_cast<float*>(static_cast<char*>(workspace) + kInt8Counters);
   p.count = static_cast<int*>(workspace);
   p.bad = a.bad;
-  return a.bf16 ? launch_bx<true, true>(pl.bx, w, x, p, dev, sms, stream)
-                : launch_bx<true, false>(pl.bx, w, x, p, dev, sms, stream);
+  char* part = static_cast<char*>(workspace) + kInt8Counters;
+  return a.bf16 ? launch_plan<true, true>(pl, w, x, p, dev, part, stream)
+                : launch_plan<true, false>(pl, w, x, p, dev, part, stream);
 }
 
 }  // namespace dq4d

@@ -1,8 +1,9 @@
 // The product of rows in 8 bits with a weight in 8 bits, dq4_int8_linear (dq4_int8.h): the entry
 // point, and the kernel for few rows.
 //
-// Few rows are bound by the weight's bytes, each read once (Streamed in int8.cuh; the rows' codes
-// come from L2, and all CTAs read the same).  Outlier columns are added in FP32.
+// Few rows are bound by the weight's bytes, each read once, by TMA, and multiplied on the tensor
+// cores in FP16 (the integer products of four, dp4a, run at 16 lanes a clock here: 1 row took 41
+// us at 28672 x 8192, 4 rows 91).  Outlier columns are added in FP32.
 #include "int8_gemm.cuh"
 
 namespace dq4d {
@@ -47,120 +48,209 @@ __device__ __forceinline__ void list_columns(const Int8Linear& p, FewColumns* s)
   }
 }
 
-template <int RT, int NT, int kDepth>
-struct FewJobs {
-  using S = Streamed<RT, NT, 1, 2, false, kDepth>;
-  static constexpr int kRows = 16 * RT, kTokens = 8 * NT;
-  static constexpr int kAhead = 4;  // outlier codes of a row loaded ahead
-  const Int8Linear& p;
-  FewColumns* s;
-  float* coef;  // [used columns][M]: what a column's codes have to be multiplied by
-  int64_t tiles_m;  // (more than one only without codes, K = 0)
-  float sn, bias;   // of this thread's row
-  uint32_t ahead[kAhead];
+constexpr int kFewRows = 16;  // weight rows of a job
+constexpr int kAhead = 4;     // outlier columns whose codes are loaded ahead
 
-  __device__ __forceinline__ int64_t row_of(int64_t job, int t, int64_t& m0) const {
-    const int64_t tn = tiles_m == 1 ? job : job / tiles_m;
-    m0 = (job - tn * tiles_m) * kTokens;
-    return tn * kRows + t % kRows;
+// A job is 16 weight rows and 8 NT tokens (all there are), shared by `group` warps of a CTA, which
+// take turns at chunks of 128 of K; one job a group, so that there is little code to fetch (with
+// jobs in turn, as in int8.cuh, a call took 4 to 5 us more).  The order of K in a product is
+// free: lane (g, c) takes 32 consecutive codes of rows g and g + 8, and of token g of each 8.
+template <int NT, int kFewDepth>
+__global__ void __launch_bounds__(kStreamThreads, kFewDepth == 2 ? 3 : 2)
+    dq4_int8_few_kernel(const __grid_constant__ CUtensorMap map_w, const Int8Linear p,
+                        const int group) {
+  constexpr int kTokens = 8 * NT, kStage = kFewRows * kChunk;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ FewColumns s_cols;
+  __shared__ uint64_t s_bars[kStreamWarps][kFewDepth];
+  __shared__ float s_part[kStreamWarps][kFewRows * kTokens];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
+  const int in_cta = warp / group, member = warp - in_cta * group;
+  const int64_t n0 = (int64_t(blockIdx.x) * (kStreamWarps / group) + in_cta) * kFewRows;
+  uint8_t* rings = aligned_1024(smem_raw);
+  float* coef = reinterpret_cast<float*>(rings + kStreamWarps * kFewDepth * kStage);
+  const uint32_t ring = smem_u32(rings) + warp * kFewDepth * kStage, bars = smem_u32(s_bars[warp]);
+  const uint64_t map = reinterpret_cast<uint64_t>(&map_w);
+  // this warp's chunks, member + i * group for i < mine, in turn from `i0` on: warps that went
+  // through the tokens side by side would queue at single lines of L2
+  const int chunks = n0 < p.N ? int((p.K + kChunk - 1) / kChunk) : 0;
+  const int mine = chunks > member ? (chunks - member + group - 1) / group : 0;
+  const int i0 = mine > 0 ? int((uint32_t(n0) / kFewRows) % uint32_t(mine)) : 0;
+  auto chunk = [&](int i) { return member + (i0 + i < mine ? i0 + i : i0 + i - mine) * group; };
+  if (lane == 0) {
+    for (int i = 0; i < kFewDepth; ++i) mbar_init(bars + 8 * i, 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    // the first chunks to L2, while the kernel before this one ends (nothing is read of them yet)
+#pragma unroll 1
+    for (int i = 0; i < kFewDepth && i < mine; ++i)
+      asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global [%0, {%1, %2}];"
+                   :: "l"(map), "r"(chunk(i) * kChunk), "r"(int(n0)) : "memory");
   }
-  __device__ __forceinline__ void places(int64_t job, int (&y)[1]) const { y[0] = int(job * kRows); }
-  __device__ __forceinline__ void tokens(int64_t, const uint8_t* (&tok)[NT]) const {
-    const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-      tok[nt] = reinterpret_cast<const uint8_t*>(p.codes + min(int64_t(8 * nt + g), p.M - 1) * p.K +
-                                                 32 * c);
-  }
-  __device__ __forceinline__ void start() {
-    if (p.L == 0) return;
-    if (threadIdx.x < 32) list_columns(p, s);
+  wait_for_stream();
+  asm volatile("griddepcontrol.launch_dependents;");
+  auto copy = [&](int i, int slot) {
+    mbar_expect(bars + 8 * slot, kStage);
+    tma_load_2d(ring + slot * kStage, map, chunk(i) * kChunk, int(n0), bars + 8 * slot);
+  };
+  if (lane == 0)
+#pragma unroll 1
+    for (int i = 0; i < kFewDepth && i < mine; ++i) copy(i, i);
+  __syncwarp();
+  // the outputs that this thread finishes are all of one row
+  const int t = 32 * member + lane, threads = 32 * group;
+  const int64_t n = n0 + t % kFewRows, n_in = min(n, p.N - 1);
+  const float sn = load_ahead(p.SCB + n_in);
+  uint32_t ahead[kAhead];
+  int used = 0;
+  if (p.L > 0) {  // (while the first codes are on their way)
+    if (warp == 0) list_columns(p, &s_cols);
     __syncthreads();
-    const int n = s->count * int(p.M);
-    for (int i = threadIdx.x; i < n; i += kStreamThreads) {
+    used = s_cols.count;
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      ahead[u] = 0;
+      if (u < used)
+        asm volatile("ld.global.s8 %0, [%1];"
+                     : "=r"(ahead[u]) : "l"(p.CB + n_in * p.K + s_cols.col[u]) : "memory");
+    }
+    for (int i = threadIdx.x; i < used * int(p.M); i += kStreamThreads) {
       const int u = i / int(p.M), m = i - u * int(p.M);
-      const float x = load_16(p.outliers, int64_t(m) * p.L + s->entry[u], p.outliers_bf16);
-      const float code = p.codes[m * p.K + s->col[u]];
+      const float x = load_16(p.outliers, int64_t(m) * p.L + s_cols.entry[u], p.outliers_bf16);
+      const float code = p.codes[m * p.K + s_cols.col[u]];
       // in the place of its code's value; not finite: NaN
       coef[i] = x + (x - x) - code * (load_global(p.scales + m) * kRecip127);
     }
     __syncthreads();
   }
-  __device__ __forceinline__ void begin(int64_t job, int t) {
-    int64_t m0;
-    const int64_t n = min(row_of(job, t, m0), p.N - 1);
-    sn = load_ahead(p.SCB + n);
-    bias = p.bias ? load_any(p.bias, n, p.out_dtype) : 0.f;
-    if (p.L > 0) {
+  const int8_t* tok[NT];
 #pragma unroll
-      for (int u = 0; u < kAhead; ++u) {
-        ahead[u] = 0;
-        if (u < s->count)
-          asm volatile("ld.global.s8 %0, [%1];"
-                       : "=r"(ahead[u]) : "l"(p.CB + n * p.K + s->col[u]) : "memory");
+  for (int nt = 0; nt < NT; ++nt) tok[nt] = p.codes + min(int64_t(8 * nt + g), p.M - 1) * p.K + 32 * c;
+  float acc[NT][4] = {};
+  bool ok = true;
+  int slot = 0, i = 0;
+  uint32_t phase = 0;
+  // the tokens' codes, from L2, a chunk ahead
+  uint4 next[NT][2];
+  auto fetch = [&](int i) {
+    const int64_t k = int64_t(chunk(i)) * kChunk;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        next[nt][h] = make_uint4(0, 0, 0, 0);
+        if (i < mine && k + 32 * c + 16 * h < p.K)
+          next[nt][h] = load_ahead(reinterpret_cast<const uint4*>(tok[nt] + k) + h);
+      }
+  };
+  fetch(0);
+#pragma unroll 1
+  for (; i < mine; ++i) {
+    uint4 x[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      x[nt][0] = next[nt][0];
+      x[nt][1] = next[nt][1];
+    }
+    fetch(i + 1);
+    ok = __all_sync(kAllLanes, mbar_wait(bars + 8 * slot, phase));
+    if (!ok) break;
+    const uint32_t at = ring + slot * kStage + g * kChunk;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {  // 128-byte rows, their 16-byte pieces in place i ^ row % 8
+      const uint4 w0 = lds_v4(at + (((2 * c + h) ^ g) << 4));
+      const uint4 w1 = lds_v4(at + 8 * kChunk + (((2 * c + h) ^ g) << 4));
+#pragma unroll
+      for (int s = 0; s < 4; ++s) {
+        uint32_t a0, a1, a2, a3;
+        codes_f16(reinterpret_cast<const uint32_t*>(&w0)[s], a0, a2);
+        codes_f16(reinterpret_cast<const uint32_t*>(&w1)[s], a1, a3);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          uint32_t b0, b1;
+          codes_f16(reinterpret_cast<const uint32_t*>(&x[nt][h])[s], b0, b1);
+          mma_16816(acc[nt], a0, a1, a2, a3, b0, b1);
+        }
+      }
+    }
+    __syncwarp();  // every lane has read the chunk
+    if (lane == 0 && i + kFewDepth < mine) copy(i + kFewDepth, slot);
+    if (++slot == kFewDepth) {
+      slot = 0;
+      phase ^= 1u;
+    }
+  }
+  if (!ok) {  // copies in flight land before the CTA leaves
+    if (lane == 0 && p.bad) atomicAdd(p.bad, 1);
+    for (int k = 0; k < kFewDepth && i < mine; ++k, ++i) {
+      mbar_wait(bars + 8 * slot, phase);
+      if (++slot == kFewDepth) {
+        slot = 0;
+        phase ^= 1u;
       }
     }
   }
-  __device__ __forceinline__ void finish(int64_t job, const float* part, int warps, int t,
-                                         int threads) const {
-    int64_t m0;
-    const int64_t n = row_of(job, t, m0);  // (a thread's outputs are all of one row)
-    if (n >= p.N) return;
-    const float s_n = sn * kRecip127;
-#pragma unroll 2
-    for (int j = t / kRows; j < kTokens && m0 + j < p.M; j += threads / kRows) {
-      const float s_m = load_global(p.scales + m0 + j) * kRecip127;
-      float y = S::sum(part, warps, j, t % kRows) * s_m * s_n;
-      if (p.L > 0) {
-        float more = 0.f;
 #pragma unroll
-        for (int u = 0; u < kAhead; ++u)
-          if (u < s->count) more += float(int(ahead[u])) * coef[u * int(p.M) + j];
-        for (int u = kAhead; u < s->count; ++u)
-          more += float(load_global(p.CB + n * p.K + s->col[u])) * coef[u * int(p.M) + j];
-        y += more * s_n;
-      }
-      store_any(p.Y, (m0 + j) * p.N + n, y + bias, p.out_dtype);
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      s_part[warp][(8 * nt + 2 * c + (i & 1)) * kFewRows + 8 * (i >> 1) + g] = acc[nt][i];
+  if (group == 1) __syncwarp();
+  else asm volatile("bar.sync %0, %1;" :: "r"(1 + in_cta), "r"(threads) : "memory");
+  if (n >= p.N) return;
+  const float s_n = sn * kRecip127;
+  const float bias = p.bias ? load_any(p.bias, n, p.out_dtype) : 0.f;
+#pragma unroll 1
+  for (int m = t / kFewRows; m < p.M; m += threads / kFewRows) {
+    float sum = 0.f;
+    if (m < kTokens)  // (more rows only without codes, K = 0)
+      for (int w = 0; w < group; ++w) sum += s_part[in_cta * group + w][m * kFewRows + t % kFewRows];
+    float y = sum * (load_global(p.scales + m) * kRecip127) * s_n;
+    if (used > 0) {
+      float more = 0.f;
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u)
+        if (u < used) more += float(int(ahead[u])) * coef[u * int(p.M) + m];
+      for (int u = kAhead; u < used; ++u)
+        more += float(load_global(p.CB + n * p.K + s_cols.col[u])) * coef[u * int(p.M) + m];
+      y += more * s_n;
     }
+    store_any(p.Y, m * p.N + n, y + bias, p.out_dtype);
   }
-};
-
-template <int RT, int NT, int kDepth, int kCtas>
-__global__ void __launch_bounds__(kStreamThreads, kCtas)
-    dq4_int8_few_kernel(const __grid_constant__ CUtensorMap map_w, const Int8Linear p) {
-  extern __shared__ uint8_t smem_raw[];
-  __shared__ FewColumns s_cols;
-  using Jobs = FewJobs<RT, NT, kDepth>;
-  uint8_t* smem = aligned_1024(smem_raw);
-  Jobs::S::setup(smem);
-  wait_for_stream();
-  asm volatile("griddepcontrol.launch_dependents;");
-  Jobs jobs = {p, &s_cols, reinterpret_cast<float*>(smem + Jobs::S::kBytes),
-               (p.M + 8 * NT - 1) / (8 * NT)};
-  Jobs::S::run(jobs, smem, (p.N + 16 * RT - 1) / (16 * RT) * jobs.tiles_m, p.K, map_w, p.bad);
 }
 
 // Whether a product goes to the kernel for few rows.
-bool few_rows(int64_t M, int64_t K) { return M <= 32 || K == 0; }
+bool few_rows(int64_t M, int64_t K) { return M <= 8 || K == 0; }
 
-template <int RT, int NT, int kDepth, int kCtas>
+template <int NT, int kFewDepth>
+int launch_few_depth(const CUtensorMap& w, const Int8Linear& p, int64_t grid, int group, int dev,
+                     cudaStream_t stream) {
+  auto kernel = dq4_int8_few_kernel<NT, kFewDepth>;
+  constexpr int kRings = kStreamWarps * kFewDepth * kFewRows * kChunk + 1024;
+  static std::atomic<uint64_t> allowed{0};
+  if (const int st = allow_smem(kernel, kRings + 8 * NT * kMaxOutliers * 4, dev, &allowed)) return st;
+  return launch_ordered(kernel, dim3(unsigned(grid)), kStreamThreads, kRings + int(p.M < 8 * NT ? p.M : 8 * NT) * p.L * 4,
+                        stream, w, p, group);
+}
+
+template <int NT>
 int launch_few(const Int8Linear& p, int dev, int sms, cudaStream_t stream) {
-  auto kernel = dq4_int8_few_kernel<RT, NT, kDepth, kCtas>;
-  constexpr int kRings = FewJobs<RT, NT, kDepth>::S::kBytes + 1024;
-  constexpr int kMost = kRings + 8 * NT * kMaxOutliers * 4;
-  static_assert(kMost + int(sizeof(FewColumns)) + 1024 <= 227 * 1024, "shared memory");
   CUtensorMap w = {};  // (without codes, K = 0, nothing is copied)
   if (p.K > 0)
     if (const int st = encode_2d(&w, CU_TENSOR_MAP_DATA_TYPE_UINT8, p.CB, p.K, p.N, p.K, kChunk,
-                                 16 * RT, CU_TENSOR_MAP_SWIZZLE_128B))
+                                 kFewRows, CU_TENSOR_MAP_SWIZZLE_128B))
       return st;
-  static std::atomic<uint64_t> allowed{0};
-  if (const int st = allow_smem(kernel, kMost, dev, &allowed)) return st;
-  const int bytes = kRings + (p.M <= 8 * NT ? int(p.M) * p.L * 4 : 0);
-  const int64_t jobs = (p.N + 16 * RT - 1) / (16 * RT) * ((p.M + 8 * NT - 1) / (8 * NT));
-  // (a CTA takes a job at least)
-  const int64_t grid = jobs < kCtas * sms ? jobs : kCtas * sms;
-  return launch_ordered(kernel, dim3(unsigned(grid)), kStreamThreads, bytes, stream, w, p);
+  const int64_t jobs = (p.N + kFewRows - 1) / kFewRows, chunks = (p.K + kChunk - 1) / kChunk;
+  // warps of a job: enough for all that the SMs hold (three CTAs), with two chunks each at least
+  int group = 1;
+  while (group < kStreamWarps && jobs * group * 2 <= 3 * kStreamWarps * sms && chunks >= 4 * group)
+    group *= 2;
+  const int64_t grid = (jobs * group + kStreamWarps - 1) / kStreamWarps;
+  // Shared memory is taken from the L1 that the tokens are read through: rings of two chunks
+  // where an SM gets three CTAs, of four where it gets two at most and its warps need more each on
+  // their way.  Two / four chunks, one row, in us: 4096 x 4096 5.8 / 5.5, 14336 to 4096 16.6 / 13.0,
+  // 4096 to 11008 11.1 / 13.6, 8192 to 28672 37 / 44.
+  if (grid <= 2 * sms) return launch_few_depth<NT, 4>(w, p, grid, group, dev, stream);
+  return launch_few_depth<NT, 2>(w, p, grid, group, dev, stream);
 }
 
 }  // namespace
@@ -208,9 +298,7 @@ int dq4_int8_linear(const int8_t* codes, const float* scales, const int8_t* CB, 
     if (misaligned(workspace, 256)) return DQ4_ERR_ALIGN;
     return launch_int8_gemm(p, dev, sms, workspace, s);
   }
-  if (M <= 8) return launch_few<1, 1, 4, 3>(p, dev, sms, s);
-  if (M <= 16) return launch_few<1, 2, 4, 3>(p, dev, sms, s);
-  return launch_few<2, 4, 2, 2>(p, dev, sms, s);
+  return M <= 8 ? launch_few<1>(p, dev, sms, s) : launch_few<2>(p, dev, sms, s);
 }
 
 }  // extern "C"

@@ -352,7 +352,7 @@ __global__ void __launch_bounds__(kStreamThreads, kCtas)
   extern __shared__ uint8_t smem_raw[];
   using Jobs = UpJobs<NT, kDepth>;
   uint8_t* smem = aligned_1024(smem_raw);
-  Jobs::S::setup(smem);
+  Jobs::S::setup(smem, map_w);
   wait_for_stream();
   asm volatile("griddepcontrol.launch_dependents;");
   Jobs jobs = {p, load_entries<false>(p, smem + Jobs::S::kBytes)};
@@ -433,7 +433,7 @@ __global__ void __launch_bounds__(kStreamThreads, kCtas)
   extern __shared__ uint8_t smem_raw[];
   using Jobs = DownJobs<NT, kDepth>;
   uint8_t* smem = aligned_1024(smem_raw);
-  Jobs::S::setup(smem);
+  Jobs::S::setup(smem, map_w);
   wait_for_stream();
   asm volatile("griddepcontrol.launch_dependents;");
   Jobs jobs = {p, load_entries<true>(p, smem + Jobs::S::kBytes)};
