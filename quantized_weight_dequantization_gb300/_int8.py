@@ -50,31 +50,29 @@ def _lib() -> ctypes.CDLL:
     return _LIB
 
 
-# Workspace sizes depend on shapes (and, for the products, the device's SMs) alone; a device that
-# could not be asked (a negative answer) is not remembered.
+# Workspace sizes depend on shapes (and, for the products, the SMs of the current device, which is
+# the one of `index`) alone; a device that could not be asked (a negative answer) is not remembered.
 @functools.lru_cache(maxsize=256)
 def _need_of(index: int, name: str, *shape) -> int:
-    with torch.cuda.device(index):
-        need = getattr(_lib(), f"dq4_int8_{name}_workspace_bytes")(*shape)
+    need = getattr(_lib(), f"dq4_int8_{name}_workspace_bytes")(*shape)
     if need < 0:
         raise Dq4Error(-need, f"dq4_int8_{name}_workspace_bytes")
     return need
 
 
-class _on:
-    """The device of a call's tensors made current for it (nothing if it is already)."""
+_current_device = torch._C._cuda_getDevice
 
-    def __init__(self, index: int):
-        self.index = index
 
-    def __enter__(self):
-        self.was = torch.cuda.current_device()
-        if self.was != self.index:
-            torch.cuda.set_device(self.index)
-
-    def __exit__(self, *exc):
-        if self.was != self.index:
-            torch.cuda.set_device(self.was)
+def _on_its_device(call):
+    """A call whose tensors are on another device than the current one, with that made current."""
+    @functools.wraps(call)
+    def wrapper(first, *args, **kwargs):
+        like = first[0] if isinstance(first, tuple) else first
+        if like.is_cuda and like.get_device() != _current_device():
+            with torch.cuda.device(like.get_device()):
+                return call(first, *args, **kwargs)
+        return call(first, *args, **kwargs)
+    return wrapper
 
 
 def _on_gpu(t: torch.Tensor, name: str) -> None:
@@ -137,35 +135,38 @@ def int8_quantize(X: torch.Tensor, threshold: float = 0.0, max_outliers: int = 6
     default a cached buffer per (device, stream) is used, and in ``torch.cuda.graph`` memory of
     the graph's own.
     """
-    _rows(X, "X")
+    if not (X.is_cuda and X.dtype in _HALF and X.dim() == 2 and X.stride(1) == 1):
+        _rows(X, "X")
     M, K = X.shape
-    device = X.device
+    index, device = X.get_device(), X.device  # (a device by its index takes torch.empty 2 us more)
+    if index != _current_device():
+        with torch.cuda.device(index):
+            return int8_quantize(X, threshold, max_outliers, workspace, stream)
+    handle = _stream(stream, index)
     codes = torch.empty((M, K), dtype=torch.int8, device=device)
     scales = torch.empty(M, dtype=torch.float32, device=device)
-    index = X.get_device()
-    handle = _stream(stream, index)
-    args = (X.data_ptr(), X.stride(0), _DTYPE_CODE[X.dtype], M, K, threshold, codes.data_ptr(),
-            scales.data_ptr())
-    with _on(index):
-        if threshold == 0:
-            st = _lib().dq4_int8_quantize(*args, None, 0, None, None, None, 0, handle)
-            rows = Int8Rows(codes, scales)
-        else:
-            if not 1 <= max_outliers <= 128:
-                raise ValueError(f"max_outliers must be 1 .. 128, got {max_outliers}")
-            cols = torch.empty(max_outliers, dtype=torch.int64, device=device)
-            outliers = torch.empty((M, max_outliers), dtype=X.dtype, device=device)
-            count = torch.empty(1, dtype=torch.int32, device=device)
-            rows = Int8Rows(codes, scales, cols, outliers, count)
-            need = _need_of(index, "quantize", K)
-            with _call_lock(index, handle):
-                ws = _workspace(workspace, need, "int8 quantize", X, handle)
-                st = _lib().dq4_int8_quantize(*args, cols.data_ptr(), max_outliers,
-                                              outliers.data_ptr(), count.data_ptr(),
-                                              ws.data_ptr(), ws.numel(), handle)
+    if threshold == 0:
+        st = _lib().dq4_int8_quantize(X.data_ptr(), X.stride(0), _DTYPE_CODE[X.dtype], M, K, 0.0,
+                                      codes.data_ptr(), scales.data_ptr(), None, 0, None, None,
+                                      None, 0, handle)
+        if st:
+            raise Dq4Error(st, "dq4_int8_quantize")
+        return Int8Rows(codes, scales)
+    if not 1 <= max_outliers <= 128:
+        raise ValueError(f"max_outliers must be 1 .. 128, got {max_outliers}")
+    cols = torch.empty(max_outliers, dtype=torch.int64, device=device)
+    outliers = torch.empty((M, max_outliers), dtype=X.dtype, device=device)
+    count = torch.empty(1, dtype=torch.int32, device=device)
+    need = _need_of(index, "quantize", K)
+    with _call_lock(index, handle):
+        ws_ptr, ws_bytes = _scratch(workspace, need, "int8 quantize", X, handle)
+        st = _lib().dq4_int8_quantize(X.data_ptr(), X.stride(0), _DTYPE_CODE[X.dtype], M, K,
+                                      threshold, codes.data_ptr(), scales.data_ptr(),
+                                      cols.data_ptr(), max_outliers, outliers.data_ptr(),
+                                      count.data_ptr(), ws_ptr, ws_bytes, handle)
     if st:
         raise Dq4Error(st, "dq4_int8_quantize")
-    return rows
+    return Int8Rows(codes, scales, cols, outliers, count)
 
 
 # ------------------------------------------------------------- the product
@@ -182,34 +183,46 @@ def int8_linear(X: Int8Rows, CB: torch.Tensor, SCB: torch.Tensor,
     by default a cached buffer per (device, stream) is used, and in ``torch.cuda.graph`` memory
     of the graph's own.  ``bad`` (int32) counts columns that cannot be used.
     """
-    codes = X.codes
-    _on_gpu(codes, "codes")
-    if codes.dim() != 2 or CB.dim() != 2 or codes.shape[1] != CB.shape[1]:
-        raise ValueError(f"codes {tuple(codes.shape)} do not go with CB {tuple(CB.shape)}")
-    M, K = codes.shape
-    N = CB.shape[0]
-    codes_ptr = _flat(codes, "codes", torch.int8, 0, codes)
-    _shape(X.scales, "scales", (M,))
-    scales_ptr = _flat(X.scales, "scales", torch.float32, 0, codes)
-    cb_ptr, scb_ptr = _weight(CB, SCB, codes, "CB", 2)
+    codes, scales, cols, outliers, _ = X
+    M, K = codes.shape if codes.dim() == 2 else (-1, -1)
+    N = CB.shape[0] if CB.dim() == 2 else -1
+    index = codes.get_device()
+    # (a call of few rows is the host's: first the short way that valid arguments pass)
+    if not (codes.is_cuda and CB.is_cuda and codes.dtype is torch.int8 and CB.dtype is torch.int8
+            and codes.is_contiguous() and CB.is_contiguous() and CB.get_device() == index
+            and scales.shape == (M,) and SCB.shape == (N,) and CB.shape[1] == K
+            and scales.dtype is torch.float32 and SCB.dtype is torch.float32
+            and scales.is_contiguous() and SCB.is_contiguous()
+            and scales.get_device() == index and SCB.get_device() == index):
+        _on_gpu(codes, "codes")
+        if M < 0 or N < 0 or CB.shape[1] != K:
+            raise ValueError(f"codes {tuple(codes.shape)} do not go with CB {tuple(CB.shape)}")
+        _flat(codes, "codes", torch.int8, 0, codes)
+        _shape(scales, "scales", (M,))
+        _flat(scales, "scales", torch.float32, 0, codes)
+        _weight(CB, SCB, codes, "CB", 2)
+    if index != _current_device():
+        with torch.cuda.device(index):
+            return int8_linear(X, CB, SCB, bias, out_dtype, Y, workspace, bad, stream)
     if Y is not None:
         out_dtype = Y.dtype
-    if out_dtype not in _DTYPE_CODE:
+    kind = _DTYPE_CODE.get(out_dtype)
+    if kind is None:
         raise TypeError(f"out_dtype: unsupported {out_dtype}")
-    cols_ptr = outliers_ptr = bias_ptr = None
-    L = kind = 0
-    if (X.cols is None) != (X.outliers is None):
+    cols_ptr = outliers_ptr = bias_ptr = bad_ptr = None
+    L = outlier_kind = 0
+    if (cols is None) != (outliers is None):
         raise ValueError("cols and outliers come together")
-    if X.cols is not None:
-        if X.cols.dim() != 1 or X.cols.numel() > 128:
-            raise ValueError(f"cols: must be 1-D, 128 at most, got {tuple(X.cols.shape)}")
-        L = X.cols.numel()
-        if X.outliers.dtype not in _HALF:
-            raise TypeError(f"outliers: must be float16 or bfloat16, got {X.outliers.dtype}")
-        _shape(X.outliers, "outliers", (M, L))
-        kind = _DTYPE_CODE[X.outliers.dtype]
-        cols_ptr = _flat(X.cols, "cols", torch.int64, 0, codes)
-        outliers_ptr = _flat(X.outliers, "outliers", X.outliers.dtype, 0, codes)
+    if cols is not None:
+        if cols.dim() != 1 or cols.numel() > 128:
+            raise ValueError(f"cols: must be 1-D, 128 at most, got {tuple(cols.shape)}")
+        L = cols.numel()
+        if outliers.dtype not in _HALF:
+            raise TypeError(f"outliers: must be float16 or bfloat16, got {outliers.dtype}")
+        _shape(outliers, "outliers", (M, L))
+        outlier_kind = _DTYPE_CODE[outliers.dtype]
+        cols_ptr = _flat(cols, "cols", torch.int64, 0, codes)
+        outliers_ptr = _flat(outliers, "outliers", outliers.dtype, 0, codes)
     if bias is not None:
         _shape(bias, "bias", (N,))
         bias_ptr = _flat(bias, "bias", out_dtype, 0, codes)
@@ -217,16 +230,23 @@ def int8_linear(X: Int8Rows, CB: torch.Tensor, SCB: torch.Tensor,
         Y = torch.empty((M, N), dtype=out_dtype, device=codes.device)
     else:
         _shape(Y, "Y", (M, N))
-    y_ptr = _flat(Y, "Y", out_dtype, 0, codes)
-    bad_ptr = _bad(bad, codes)
-    index = codes.get_device()
+        _flat(Y, "Y", out_dtype, 0, codes)
+    if bad is not None:
+        bad_ptr = _bad(bad, codes)
     handle = _stream(stream, index)
     need = _need_of(index, "linear", M, N, K, L)
-    with _on(index), _call_lock(index, handle):
-        ws_ptr, ws_bytes = _scratch(workspace, need, "int8 linear", codes, handle)
-        st = _lib().dq4_int8_linear(codes_ptr, scales_ptr, cb_ptr, scb_ptr, M, N, K, cols_ptr, L,
-                                    outliers_ptr, kind, bias_ptr, _DTYPE_CODE[out_dtype], y_ptr,
-                                    ws_ptr, ws_bytes, bad_ptr, handle)
+    if need == 0 and workspace is None:  # one launch
+        st = _lib().dq4_int8_linear(codes.data_ptr(), scales.data_ptr(), CB.data_ptr(),
+                                    SCB.data_ptr(), M, N, K, cols_ptr, L, outliers_ptr,
+                                    outlier_kind, bias_ptr, kind, Y.data_ptr(), None, 0, bad_ptr,
+                                    handle)
+    else:
+        with _call_lock(index, handle):
+            ws_ptr, ws_bytes = _scratch(workspace, need, "int8 linear", codes, handle)
+            st = _lib().dq4_int8_linear(codes.data_ptr(), scales.data_ptr(), CB.data_ptr(),
+                                        SCB.data_ptr(), M, N, K, cols_ptr, L, outliers_ptr,
+                                        outlier_kind, bias_ptr, kind, Y.data_ptr(), ws_ptr,
+                                        ws_bytes, bad_ptr, handle)
     if st:
         raise Dq4Error(st, "dq4_int8_linear")
     return Y
@@ -240,6 +260,7 @@ def _scratch(workspace, need: int, what: str, like: torch.Tensor, handle):
     return ws.data_ptr(), ws.numel()
 
 
+@_on_its_device
 def int8_linear_backward(dY: torch.Tensor, CB: torch.Tensor, SCB: torch.Tensor,
                          dX: Optional[torch.Tensor] = None,
                          workspace: Optional[torch.Tensor] = None,
@@ -269,7 +290,7 @@ def int8_linear_backward(dY: torch.Tensor, CB: torch.Tensor, SCB: torch.Tensor,
     index = dY.get_device()
     handle = _stream(stream, index)
     need = _need_of(index, "linear_backward", M, N, K)
-    with _on(index), _call_lock(index, handle):
+    with _call_lock(index, handle):
         ws_ptr, ws_bytes = _scratch(workspace, need, "int8 backward", dY, handle)
         st = _lib().dq4_int8_linear_backward(dy_ptr, _DTYPE_CODE[dY.dtype], cb_ptr, scb_ptr, M, N,
                                              K, dx_ptr, ws_ptr, ws_bytes, bad_ptr, handle)
@@ -279,6 +300,7 @@ def int8_linear_backward(dY: torch.Tensor, CB: torch.Tensor, SCB: torch.Tensor,
 
 
 # ------------------------------------------------------------- mixture of experts
+@_on_its_device
 def int8_moe(X: torch.Tensor, logits: torch.Tensor, w1: torch.Tensor, s1: torch.Tensor,
              w2: torch.Tensor, s2: torch.Tensor, top_k: int, renormalize: bool = True,
              return_routing: bool = False, workspace: Optional[torch.Tensor] = None,
@@ -314,7 +336,7 @@ def int8_moe(X: torch.Tensor, logits: torch.Tensor, w1: torch.Tensor, s1: torch.
     index = X.get_device()
     handle = _stream(stream, index)
     need = _need_of(index, "moe", T, H, I, top_k)
-    with _on(index), _call_lock(index, handle):
+    with _call_lock(index, handle):
         ws_ptr, ws_bytes = _scratch(workspace, need, "int8 moe", X, handle)
         st = _lib().dq4_int8_moe(X.data_ptr(), X.stride(0), _DTYPE_CODE[X.dtype], T, H, I, E,
                                  logits_ptr, top_k, renormalize, w1_ptr, s1_ptr, w2_ptr, s2_ptr,

@@ -231,7 +231,7 @@ using namespace dq4d;
 extern "C" {
 
 int64_t dq4_int8_quantize_workspace_bytes(int64_t K) {
-  return K <= 0 ? 0 : kMaskAt + (K + 31) / 32 * 4;
+  return K < 0 ? 0 : kMaskAt + (K + 31) / 32 * 4;
 }
 
 int dq4_int8_quantize(const void* X, int64_t row_stride, int32_t dtype, int64_t M, int64_t K,

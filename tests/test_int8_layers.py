@@ -53,7 +53,7 @@ def test_quantize_refusals(lib):
                {"count": P + 2}, {"ws": P + 16}):
         assert call(**kw) == ALIGN, kw
     need = lib.dq4_int8_quantize_workspace_bytes(64)
-    assert need > 0 and lib.dq4_int8_quantize_workspace_bytes(0) == 0
+    assert need > 0 and lib.dq4_int8_quantize_workspace_bytes(-1) == 0
     assert call(ws=None) == WORKSPACE and call(nbytes=need - 1) == WORKSPACE
 
 
