@@ -102,26 +102,7 @@ __global__ void __launch_bounds__(kStreamThreads, kFewDepth == 2 ? 3 : 2)
   const float sn = load_ahead(p.SCB + n_in);
   uint32_t ahead[kAhead];
   int used = 0;
-  if (p.L > 0) {  // (while the first codes are on their way)
-    if (warp == 0) list_columns(p, &s_cols);
-    __syncthreads();
-    used = s_cols.count;
-#pragma unroll
-    for (int u = 0; u < kAhead; ++u) {
-      ahead[u] = 0;
-      if (u < used)
-        asm volatile("ld.global.s8 %0, [%1];"
-                     : "=r"(ahead[u]) : "l"(p.CB + n_in * p.K + s_cols.col[u]) : "memory");
-    }
-    for (int i = threadIdx.x; i < used * int(p.M); i += kStreamThreads) {
-      const int u = i / int(p.M), m = i - u * int(p.M);
-      const float x = load_16(p.outliers, int64_t(m) * p.L + s_cols.entry[u], p.outliers_bf16);
-      const float code = p.codes[m * p.K + s_cols.col[u]];
-      // in the place of its code's value; not finite: NaN
-      coef[i] = x + (x - x) - code * (load_global(p.scales + m) * kRecip127);
-    }
-    __syncthreads();
-  }
+  if (p.L > 0 && warp == 0) list_columns(p, &s_cols);  // (while the first codes are on their way)
   const int8_t* tok[NT];
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) tok[nt] = p.codes + min(int64_t(8 * nt + g), p.M - 1) * p.K + 32 * c;
@@ -194,8 +175,29 @@ __global__ void __launch_bounds__(kStreamThreads, kFewDepth == 2 ? 3 : 2)
 #pragma unroll
     for (int i = 0; i < 4; ++i)
       s_part[warp][(8 * nt + 2 * c + (i & 1)) * kFewRows + 8 * (i >> 1) + g] = acc[nt][i];
-  if (group == 1) __syncwarp();
-  else asm volatile("bar.sync %0, %1;" :: "r"(1 + in_cta), "r"(threads) : "memory");
+  if (p.L > 0) {
+    __syncthreads();
+    used = s_cols.count;
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      ahead[u] = 0;
+      if (u < used)
+        asm volatile("ld.global.s8 %0, [%1];"
+                     : "=r"(ahead[u]) : "l"(p.CB + n_in * p.K + s_cols.col[u]) : "memory");
+    }
+    for (int i = threadIdx.x; i < used * int(p.M); i += kStreamThreads) {
+      const int u = i / int(p.M), m = i - u * int(p.M);
+      const float x = load_16(p.outliers, int64_t(m) * p.L + s_cols.entry[u], p.outliers_bf16);
+      const float code = p.codes[m * p.K + s_cols.col[u]];
+      // in the place of its code's value; not finite: NaN
+      coef[i] = x + (x - x) - code * (load_global(p.scales + m) * kRecip127);
+    }
+    __syncthreads();
+  } else if (group == 1) {
+    __syncwarp();
+  } else {
+    asm volatile("bar.sync %0, %1;" :: "r"(1 + in_cta), "r"(threads) : "memory");
+  }
   if (n >= p.N) return;
   const float s_n = sn * kRecip127;
   const float bias = p.bias ? load_any(p.bias, n, p.out_dtype) : 0.f;

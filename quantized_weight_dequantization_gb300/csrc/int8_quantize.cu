@@ -2,9 +2,11 @@
 //
 // Bound by memory: 2 bytes a value in, 1 out.  A row lies in the registers of a warp (up to 1024
 // values) or of a CTA, is read once, and its codes are written as if there were no outlier
-// columns; values past the threshold only set their column's bit in a mask.  A second, small
-// launch lists the mask's columns, takes their codes out and copies their values: 2 M L
-// scattered accesses instead of a second pass over X.
+// columns; values past the threshold only mark their column (their own codes are nothing yet).  A
+// second, small launch lists the marked columns, takes their codes out and copies their values:
+// 2 M L scattered accesses instead of a second pass over X.  A mark is a bit set by an atomic that
+// nothing waits for, in one of 16 copies: one word takes an atomic (or a store) every 2 to 3 ns, and
+// 16384 x 1024 with 5 such columns took 31 to 37 us with a single copy.
 // The maximum is taken on the bits of |x|, two values an instruction: for values that are not
 // negative the order of the bits is that of the numbers, infinity and NaN last.
 #include "int8.cuh"
@@ -13,6 +15,7 @@ namespace dq4d {
 namespace {
 
 constexpr int kRowThreads = 256;  // of a CTA
+constexpr int kCopies = 16;       // of the marks
 
 struct QuantArgs {
   const uint16_t* X;
@@ -20,7 +23,7 @@ struct QuantArgs {
   uint32_t loud;  // the least |x| that is an outlier, as 16 bits
   int8_t* codes;
   float* scales;
-  uint32_t* mask;  // a bit for each column
+  uint32_t* marks;  // [kCopies][K / 32 words]: a bit for each column
 };
 
 template <bool kBf16>
@@ -29,11 +32,28 @@ __device__ __forceinline__ float widen(uint32_t bits) {
   else return __half2float(__ushort_as_half(uint16_t(bits)));
 }
 
-// x * inverse to the nearest integer, in the low byte: 1.5 * 2^23 leaves no bits behind the point.
-__device__ __forceinline__ uint32_t code_of(float x, float inverse, bool limit) {
-  float v = __fmul_rn(x, inverse);
-  if (limit) v = fminf(fmaxf(v, -127.f), 127.f);
-  return __float_as_uint(__fadd_rn(v, 12582912.f));
+// Two values of 16 bits as FP32.
+template <bool kBf16>
+__device__ __forceinline__ float2 widen2(uint32_t w) {
+  if constexpr (kBf16) {
+    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+  } else {
+    __half2 h;
+    memcpy(&h, &w, 4);
+    return __half22float2(h);
+  }
+}
+
+// x * inverse to the nearest integer, in the low byte of each half: 1.5 * 2^23 leaves no bits behind
+// the point.  (Two values an instruction.  The product is rounded on its own: ptxas makes one
+// instruction of a packed product and sum, whatever their modifiers, so the sum is an FMA by 1.)
+__device__ __forceinline__ uint64_t codes_of(float2 x, uint64_t inverse2) {
+  const uint64_t magic2 = 0x4B4000004B400000ull, one2 = 0x3F8000003F800000ull;
+  uint64_t v;
+  memcpy(&v, &x, 8);
+  asm("mul.rn.f32x2 %0, %0, %1;" : "+l"(v) : "l"(inverse2));
+  asm("fma.rn.f32x2 %0, %0, %1, %2;" : "+l"(v) : "l"(one2), "l"(magic2));
+  return v;
 }
 
 // kRow threads a row, kGroups groups of 8 values for each at a time.  kVec: groups are whole and
@@ -49,6 +69,7 @@ __global__ void __launch_bounds__(kRowThreads) int8_quantize_kernel(const QuantA
   const int64_t row = int64_t(blockIdx.x) * (kRowThreads / kRow) + threadIdx.x / kRow;
   if (row >= p.M) return;  // (whole warps: a warp's row, or the CTA's only one)
   const uint16_t* x = p.X + row * p.row_stride;
+  uint32_t* marks = p.marks + (blockIdx.x % kCopies) * ((p.K + 31) / 32);
   uint4 v[kGroups];
   auto load = [&](int64_t base) {
 #pragma unroll
@@ -72,16 +93,21 @@ __global__ void __launch_bounds__(kRowThreads) int8_quantize_kernel(const QuantA
   uint32_t top = 0;
   for (int64_t base = 0; base < p.K; base += kSpan) {
     load(base);
-    uint32_t m = 0;
+    uint32_t most = 0, hot = 0;  // hot: groups with outliers
 #pragma unroll
-    for (int g = 0; g < kGroups; ++g)
+    for (int g = 0; g < kGroups; ++g) {
+      const uint32_t m = __vmaxu2(__vmaxu2(v[g].x & 0x7FFF7FFFu, v[g].y & 0x7FFF7FFFu),
+                                  __vmaxu2(v[g].z & 0x7FFF7FFFu, v[g].w & 0x7FFF7FFFu));
+      const uint32_t mg = max(m & 0xFFFFu, m >> 16);
+      if (kThr && mg >= p.loud)
+        hot |= 1u << g;
+      else
+        most = max(most, mg);
+    }
+    if (kThr && hot) {  // seldom: which values, and the largest of the others
 #pragma unroll
-      for (int i = 0; i < 4; ++i) m = __vmaxu2(m, word(g, i) & 0x7FFF7FFFu);
-    uint32_t most = max(m & 0xFFFFu, m >> 16);
-    if (kThr && most >= p.loud) {  // seldom: which, and the largest of the others
-      most = 0;
-#pragma unroll
-      for (int g = 0; g < kGroups; ++g)
+      for (int g = 0; g < kGroups; ++g) {
+        if (!(hot >> g & 1)) continue;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           const uint32_t b = word(g, i / 2) >> (16 * (i & 1)) & 0x7FFFu;
@@ -89,11 +115,10 @@ __global__ void __launch_bounds__(kRowThreads) int8_quantize_kernel(const QuantA
             most = max(most, b);
           } else {
             const int64_t col = base + (int64_t(g) * kRow + t) * 8 + i;
-            const uint32_t bit = 1u << (col & 31);
-            uint32_t* at = p.mask + (col >> 5);
-            if (!(*reinterpret_cast<volatile uint32_t*>(at) & bit)) atomicOr(at, bit);
+            atomicOr(marks + (col >> 5), 1u << (col & 31));
           }
         }
+      }
     }
     top = max(top, most);
   }
@@ -111,29 +136,28 @@ __global__ void __launch_bounds__(kRowThreads) int8_quantize_kernel(const QuantA
 
   // ---- the codes
   const float inverse = scale > 0.f ? __fdiv_rn(127.f, scale) : 0.f;
+  const uint64_t inverse2 = uint64_t(__float_as_uint(inverse)) << 32 | __float_as_uint(inverse);
   int8_t* to = p.codes + row * p.K;
   for (int64_t base = 0; base < p.K; base += kSpan) {
     if (p.K > kSpan) load(base);
 #pragma unroll
     for (int g = 0; g < kGroups; ++g) {
       const int64_t e = base + (int64_t(g) * kRow + t) * 8;
-      uint32_t c[8];
+      uint32_t c[2];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const uint32_t w = word(g, i / 2);
-        c[i] = code_of(widen<kBf16>(i & 1 ? w >> 16 : w & 0xFFFFu), inverse, kThr);
+      for (int h = 0; h < 2; ++h) {
+        const uint64_t a = codes_of(widen2<kBf16>(word(g, 2 * h)), inverse2);
+        const uint64_t b = codes_of(widen2<kBf16>(word(g, 2 * h + 1)), inverse2);
+        c[h] = __byte_perm(__byte_perm(uint32_t(a), uint32_t(a >> 32), 0x0040),
+                           __byte_perm(uint32_t(b), uint32_t(b >> 32), 0x0040), 0x5410);
+        if (!(scale > 0.f)) c[h] = 0;
       }
-      uint32_t lo = __byte_perm(__byte_perm(c[0], c[1], 0x0040), __byte_perm(c[2], c[3], 0x0040),
-                                0x5410);
-      uint32_t hi = __byte_perm(__byte_perm(c[4], c[5], 0x0040), __byte_perm(c[6], c[7], 0x0040),
-                                0x5410);
-      if (!(scale > 0.f)) lo = hi = 0;
       if constexpr (kVec) {
-        if (e < p.K) __stcs(reinterpret_cast<uint2*>(to + e), make_uint2(lo, hi));
+        if (e < p.K) __stcs(reinterpret_cast<uint2*>(to + e), make_uint2(c[0], c[1]));
       } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-          if (e + i < p.K) to[e + i] = int8_t((i < 4 ? lo : hi) >> (8 * (i & 3)));
+          if (e + i < p.K) to[e + i] = int8_t(c[i / 4] >> (8 * (i & 3)));
       }
     }
   }
@@ -142,19 +166,22 @@ __global__ void __launch_bounds__(kRowThreads) int8_quantize_kernel(const QuantA
 struct OutlierArgs {
   const uint16_t* X;
   int64_t row_stride, M, K;
+  uint32_t loud;
   int8_t* codes;
+  const float* scales;
   int64_t* cols;
   int max_cols;
   uint16_t* outliers;
   int32_t* count;
-  uint32_t* mask;
-  int* done;  // CTAs that have read the mask
+  uint32_t* marks;
+  int* done;  // CTAs that have read the marks
   int64_t rows;  // of a CTA
 };
 
-// The mask's columns, listed by every CTA for itself (K / 32 words from L2), their values and
-// codes for its rows; the last CTA to have read the mask clears it.
+// The marked columns, listed by every CTA for itself (from L2), their values and codes for
+// its rows; the last CTA to have read the marks clears them.
 __global__ void __launch_bounds__(kRowThreads) int8_outliers_kernel(const OutlierArgs p) {
+  constexpr int kAtOnce = 8;
   __shared__ int64_t s_cols[kMaxOutliers];
   __shared__ int s_sums[kRowThreads / 32];
   __shared__ bool s_last;
@@ -162,10 +189,16 @@ __global__ void __launch_bounds__(kRowThreads) int8_outliers_kernel(const Outlie
   asm volatile("griddepcontrol.launch_dependents;");
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
   const int64_t words = (p.K + 31) / 32;
+  auto marks_of = [&](int64_t w) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < kCopies; ++i) m |= load_global(p.marks + i * words + w);
+    return m;
+  };
   int found = 0;
   for (int64_t w0 = 0; w0 < words; w0 += kRowThreads) {
-    uint32_t bits = w0 + t < words ? load_global(p.mask + w0 + t) : 0;
-    const int mine = __popc(bits);
+    uint32_t m = w0 + t < words ? marks_of(w0 + t) : 0;
+    const int mine = __popc(m);
     int run = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -180,36 +213,62 @@ __global__ void __launch_bounds__(kRowThreads) int8_outliers_kernel(const Outlie
       if (w < warp) at += s_sums[w];
       found += s_sums[w];
     }
-    for (; bits != 0 && at < p.max_cols; bits &= bits - 1, ++at)
-      s_cols[at] = (w0 + t) * 32 + __ffs(bits) - 1;
+    for (; m != 0 && at < p.max_cols; m &= m - 1, ++at) s_cols[at] = (w0 + t) * 32 + __ffs(m) - 1;
     __syncthreads();
   }
-  if (t == 0) s_last = atomic_add_acq_rel(p.done, 1) == int(gridDim.x) - 1;
   const int kept = min(found, p.max_cols);
   if (blockIdx.x == 0) {
     for (int l = t; l < p.max_cols; l += kRowThreads) p.cols[l] = l < kept ? s_cols[l] : -1;
     if (t == 0) *p.count = found;
   }
   const int64_t row0 = blockIdx.x * p.rows;
-  const int64_t n = min(p.rows, p.M - row0) * p.max_cols;
-  for (int64_t i = t; i < n; i += kRowThreads) {
-    const int64_t row = row0 + i / p.max_cols;
-    const int l = int(i % p.max_cols);
-    uint16_t v = 0;
-    if (l < kept) {
-      v = load_global(p.X + row * p.row_stride + s_cols[l]);
-      p.codes[row * p.K + s_cols[l]] = 0;
+  const int rows = int(min(p.rows, p.M - row0));
+  // (a thread keeps to one of the columns: 128 at most, a power of two of threads for each row)
+  const int wide = p.max_cols <= 32 ? 32 : p.max_cols <= 64 ? 64 : 128;
+  const int l = t % wide, step = kRowThreads / wide;
+  if (l < p.max_cols) {
+    const int64_t col = l < kept ? s_cols[l] : -1;
+    for (int r0 = t / wide; r0 < rows; r0 += step * kAtOnce) {
+      uint16_t v[kAtOnce];
+#pragma unroll
+      for (int i = 0; i < kAtOnce; ++i) {
+        const int r = r0 + i * step;
+        v[i] = 0;
+        if (col >= 0 && r < rows) v[i] = load_global(p.X + (row0 + r) * p.row_stride + col);
+      }
+#pragma unroll
+      for (int i = 0; i < kAtOnce; ++i) {
+        const int64_t row = row0 + r0 + i * step;
+        if (r0 + i * step >= rows) break;
+        if (col >= 0) p.codes[row * p.K + col] = 0;
+        p.outliers[row * p.max_cols + l] = v[i];
+      }
     }
-    p.outliers[row * p.max_cols + l] = v;
+  }
+  // Seldom: outlier columns past the last that is kept.  Their outliers' codes end at +-127 (they
+  // are above the scale).
+  if (found > p.max_cols) {
+    for (int64_t col = s_cols[p.max_cols - 1] + 1; col < p.K; ++col) {
+      if (!(marks_of(col >> 5) >> (col & 31) & 1)) continue;
+      for (int r = t; r < rows; r += kRowThreads) {
+        const uint32_t b = load_global(p.X + (row0 + r) * p.row_stride + col);
+        if ((b & 0x7FFFu) >= p.loud && load_global(p.scales + row0 + r) > 0.f)
+          p.codes[(row0 + r) * p.K + col] = b & 0x8000u ? -127 : 127;
+      }
+    }
   }
   __syncthreads();
+  if (t == 0) s_last = atomic_add_acq_rel(p.done, 1) == int(gridDim.x) - 1;
+  __syncthreads();
   if (s_last) {
-    for (int64_t w = t; w < words; w += kRowThreads) p.mask[w] = 0;
+    for (int64_t w = t; w < kCopies * words; w += kRowThreads) p.marks[w] = 0;
     if (t == 0) *p.done = 0;
   }
 }
 
-constexpr int64_t kMaskAt = 256;  // bytes of the workspace before the mask
+constexpr int64_t kMarksAt = 256;  // bytes of the workspace before the marks
+
+int64_t mark_bytes(int64_t K) { return kCopies * ((K + 31) / 32) * 4; }
 
 template <bool kBf16, bool kThr>
 int launch_rows(const QuantArgs& p, bool vec, cudaStream_t stream) {
@@ -231,7 +290,7 @@ using namespace dq4d;
 extern "C" {
 
 int64_t dq4_int8_quantize_workspace_bytes(int64_t K) {
-  return K < 0 ? 0 : kMaskAt + (K + 31) / 32 * 4;
+  return K < 0 ? 0 : kMarksAt + mark_bytes(K);
 }
 
 int dq4_int8_quantize(const void* X, int64_t row_stride, int32_t dtype, int64_t M, int64_t K,
@@ -251,7 +310,7 @@ int dq4_int8_quantize(const void* X, int64_t row_stride, int32_t dtype, int64_t 
       misaligned(outliers, 2) || misaligned(count, 4))
     return DQ4_ERR_ALIGN;
   if (thr) {
-    if (!workspace || workspace_bytes < kMaskAt + (K + 31) / 32 * 4) return DQ4_ERR_WORKSPACE;
+    if (!workspace || workspace_bytes < kMarksAt + mark_bytes(K)) return DQ4_ERR_WORKSPACE;
     if (misaligned(workspace, 256)) return DQ4_ERR_ALIGN;
   }
   int dev, sms;
@@ -268,7 +327,7 @@ int dq4_int8_quantize(const void* X, int64_t row_stride, int32_t dtype, int64_t 
     } else {
       p.loud = __half_as_ushort(__float2half_ru(threshold));
     }
-    p.mask = reinterpret_cast<uint32_t*>(static_cast<char*>(workspace) + kMaskAt);
+    p.marks = reinterpret_cast<uint32_t*>(static_cast<char*>(workspace) + kMarksAt);
   }
   const bool vec = K % 8 == 0 && row_stride % 8 == 0 && !misaligned(X, 16) && !misaligned(codes, 8);
   if (M > 0) {
@@ -278,8 +337,8 @@ int dq4_int8_quantize(const void* X, int64_t row_stride, int32_t dtype, int64_t 
                                : launch_rows<false, false>(p, vec, s));
     if (st || !thr) return st;
   }
-  OutlierArgs o = {p.X, row_stride, M, K, codes, cols, max_cols, static_cast<uint16_t*>(outliers),
-                   count, p.mask, static_cast<int*>(workspace), 1};
+  OutlierArgs o = {p.X, row_stride, M, K, p.loud, codes, scales, cols, max_cols,
+                   static_cast<uint16_t*>(outliers), count, p.marks, static_cast<int*>(workspace), 1};
   // rows of a CTA: one wave of the SMs, two CTAs each
   o.rows = (M + 2 * sms - 1) / (2 * sms);
   if (o.rows < 1) o.rows = 1;
