@@ -268,13 +268,17 @@ int launch_ordered(void (*kernel)(KArgs...), dim3 grid, int threads, size_t smem
 }
 
 // Let `kernel` have `bytes` of dynamic shared memory, once for each device (bit dev of
-// *allowed; devices past 63 every time).
+// *allowed; devices past 63 every time).  carveout: the share of an SM's 256 KB that becomes shared
+// memory rather than L1, in percent (-1: the driver's choice, what as many CTAs as fit need).
 template <typename Kernel>
-int allow_smem(Kernel kernel, int bytes, int dev, std::atomic<uint64_t>* allowed) {
+int allow_smem(Kernel kernel, int bytes, int dev, std::atomic<uint64_t>* allowed,
+               int carveout = -1) {
   const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
   if (allowed->load(std::memory_order_relaxed) & bit) return DQ4_OK;
-  const cudaError_t e =
+  cudaError_t e =
       cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess && carveout >= 0)
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout, carveout);
   if (e != cudaSuccess) return fail_cuda(DQ4_ERR_LAUNCH, e);
   allowed->fetch_or(bit, std::memory_order_relaxed);
   return DQ4_OK;

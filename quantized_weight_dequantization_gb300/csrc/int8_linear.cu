@@ -229,7 +229,9 @@ int launch_few_depth(const CUtensorMap& w, const Int8Linear& p, int64_t grid, in
   auto kernel = dq4_int8_few_kernel<NT, kFewDepth>;
   constexpr int kRings = kStreamWarps * kFewDepth * kFewRows * kChunk + 1024;
   static std::atomic<uint64_t> allowed{0};
-  if (const int st = allow_smem(kernel, kRings + 8 * NT * kMaxOutliers * 4, dev, &allowed)) return st;
+  if (const int st = allow_smem(kernel, kRings + 8 * NT * kMaxOutliers * 4, dev, &allowed,
+                                kFewDepth == 2 ? 50 : 70))
+    return st;
   return launch_ordered(kernel, dim3(unsigned(grid)), kStreamThreads, kRings + int(p.M < 8 * NT ? p.M : 8 * NT) * p.L * 4,
                         stream, w, p, group);
 }
@@ -248,9 +250,10 @@ int launch_few(const Int8Linear& p, int dev, int sms, cudaStream_t stream) {
     group *= 2;
   const int64_t grid = (jobs * group + kStreamWarps - 1) / kStreamWarps;
   // Shared memory is taken from the L1 that the tokens are read through: rings of two chunks
-  // where an SM gets three CTAs, of four where it gets two at most and its warps need more each on
-  // their way.  Two / four chunks, one row, in us: 4096 x 4096 5.8 / 5.5, 14336 to 4096 16.6 / 13.0,
-  // 4096 to 11008 11.1 / 13.6, 8192 to 28672 37 / 44.
+  // where an SM gets three CTAs (half of the 256 KB), of four where it gets two at most and its
+  // warps need more each on their way (70 %; by the driver's choice 8.2 and 26 us instead of the
+  // first two).  Two / four chunks, one row, in us: 4096 x 4096 5.8 / 5.5, 14336 to 4096
+  // 16.6 / 12.8, 4096 to 11008 11.1 / 13.6, 8192 to 28672 37 / 44.
   if (grid <= 2 * sms) return launch_few_depth<NT, 4>(w, p, grid, group, dev, stream);
   return launch_few_depth<NT, 2>(w, p, grid, group, dev, stream);
 }

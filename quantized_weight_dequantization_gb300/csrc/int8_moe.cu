@@ -567,8 +567,8 @@ int dq4_int8_moe(const void* X, int64_t row_stride, int32_t dtype, int64_t T, in
   at += T * top_k * up256(I / 4);
   p.out = reinterpret_cast<float*>(at);
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (T * top_k <= 6 * E) return launch_moe<1, 3, 2, 3, 2>(p, dev, sms, s);
-  return launch_moe<2, 3, 2, 3, 2>(p, dev, sms, s);
+  if (T * top_k <= 6 * E) return launch_moe<1, 2, 2, 2, 2>(p, dev, sms, s);
+  return launch_moe<2, 2, 2, 2, 2>(p, dev, sms, s);
 }
 
 }  // extern "C"
