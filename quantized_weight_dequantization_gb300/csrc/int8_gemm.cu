@@ -46,7 +46,10 @@ struct Gemm {
   static constexpr int kThreads = 32 * (kProducers + kReaders + kIssuers + 2);
   static constexpr int kRawAt = kSlots * kSlot;
   static constexpr int kBarsAt = kRawAt + kRawSlots * kRawSlot;
-  static constexpr int kBars = 2 * kSlots + 2 * kRawSlots + 2 * kRing + 2 * kBuffers + 1;
+  // where parts of a tile are joined: pieces of 32 rows (both readers' halves) in the idle rings
+  static constexpr int kPiece = 2 * 32 * kTileW * 4;
+  static constexpr int kPieces = kBarsAt / kPiece;
+  static constexpr int kBars = 2 * kSlots + 2 * kRawSlots + 2 * kRing + 2 * kBuffers + 1 + kPieces;
   static constexpr int kBytes = kBarsAt + 8 * kBars + 1024;  // + alignment slack
   static constexpr int kStatic = kBack ? 16 * kStage + 64 : 4 * kMaxOutliers + 64;
   static_assert(kBytes + kStatic <= 227 * 1024, "shared memory budget");
@@ -151,6 +154,7 @@ __global__ void __launch_bounds__(Gemm<BX, kBack>::kThreads, 1)
   };
   auto acc_empty = [&](int b) { return acc_full(kBuffers + b); };
   const uint32_t all_done = acc_full(2 * kBuffers);
+  auto piece_full = [&](int s) { return acc_full(2 * kBuffers + 1 + s); };
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   volatile int* aborted = &s_abort;
   auto fail = [&] {
@@ -181,6 +185,7 @@ __global__ void __launch_bounds__(Gemm<BX, kBack>::kThreads, 1)
         mbar_init(acc_empty(b), kReaders);
       }
       mbar_init(all_done, kIssuers);
+      for (int s = 0; s < S::kPieces; ++s) mbar_init(piece_full(s), 1);
       *aborted = 0;
       asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
       asm volatile("prefetch.tensormap [%0];" :: "l"(reinterpret_cast<uint64_t>(&map_w)));
@@ -624,18 +629,56 @@ __global__ void __launch_bounds__(Gemm<BX, kBack>::kThreads, 1)
       }
       bar_readers();
       if (!s_last) continue;
+      const int sharers = int(cta1 - cta0) + 1;
+      // The CTA's last item: the rings are idle, and the parts are copied into them, many at once.
+      const bool idle = walk >= walk1;
+      const int pieces = kChunks * sharers;  // piece i: 32 columns i / sharers of part i % sharers
+      auto copy = [&](int i) {
+        const int c = i / sharers, q = i - c * sharers;
+        const uint32_t dst = sbase + i % S::kPieces * S::kPiece, bar = piece_full(i % S::kPieces);
+        const float4* from = p.part + ((cta0 + q) * 2 + (q == 0)) * (BX / 4 * kTileW);
+        mbar_expect(bar, S::kPiece);
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          asm volatile(
+              "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+              :: "r"(dst + h * (S::kPiece / 2)), "l"(from + (h * (kHalf / 4) + 8 * c) * kTileW),
+                 "r"(S::kPiece / 2), "r"(bar) : "memory");
+      };
+      if (idle && tid == 32 * kProducers) {
+        // (the parts were written by ordinary stores, and are read by the copies' own path)
+        asm volatile("fence.proxy.async;" ::: "memory");
+        for (int i = 0; i < pieces && i < S::kPieces; ++i) copy(i);
+      }
+      int at_piece = 0;
+      bool here = true;
 #pragma unroll
       for (int c = 0; c < kChunks; ++c) {
         float4 sum[8];
-        const float4* from = part_at(cta0, 1) + 8 * c * kTileW;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) sum[j] = load_l2(from + j * kTileW);
+        for (int j = 0; j < 8; ++j) sum[j] = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 1
-        for (int64_t cta = cta0 + 1; cta <= cta1; ++cta) {
-          from = part_at(cta, 0) + 8 * c * kTileW;
+        for (int q = 0; q < sharers; ++q, ++at_piece) {
           float4 more[8];
+          if (idle) {
+            here = here && mbar_wait(piece_full(at_piece % S::kPieces),
+                                     uint32_t(at_piece / S::kPieces) & 1u);
+            const uint32_t from = sbase + at_piece % S::kPieces * S::kPiece + half * (S::kPiece / 2) +
+                                  (quad * 32 + lane) * 16;
 #pragma unroll
-          for (int j = 0; j < 8; ++j) more[j] = load_l2(from + j * kTileW);
+            for (int j = 0; j < 8; ++j) {
+              const uint4 v = lds_v4(from + j * kTileW * 16);
+              memcpy(&more[j], &v, 16);
+            }
+            if (at_piece + S::kPieces < pieces) {  // its place, for a later piece
+              bar_readers();
+              if (tid == 32 * kProducers) copy(at_piece + S::kPieces);
+            }
+          } else {
+            const float4* from = part_at(cta0 + q, q == 0) + 8 * c * kTileW;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) more[j] = load_l2(from + j * kTileW);
+          }
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
             sum[j].x += more[j].x;
@@ -654,6 +697,7 @@ __global__ void __launch_bounds__(Gemm<BX, kBack>::kThreads, 1)
           store(keep, c);
         }
       }
+      if (!here && lane == 0) fail();
     }
   }
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
@@ -770,18 +814,19 @@ struct Plan {
 };
 
 // The tile's width, and whether CTAs take whole tiles or equal runs of stages, by the estimated
-// time in cycles: a stage takes about 560 at BX 64 (the issuers), 640 at 128 and 1120 at 256 (the
-// MMAs), the end of a tile some more where its accumulator is the only one, a CTA 5000 to start
-// and end, and parts of tiles have to be written and added.
-Plan plan_gemm(int64_t lanes, int64_t rows, int steps, int sms) {
+// time in cycles: a stage takes about 1000 at BX 64 and 128 and 1500 at 256 (the MMAs: 122 each,
+// at 256 181), for the gradient 1300 to 1800 (columns of codes to values); the end of a tile some
+// more where its accumulator is the only one, a CTA 5000 to start and end, and parts of tiles
+// have to be written and added.
+Plan plan_gemm(int64_t lanes, int64_t rows, int steps, bool back, int sms) {
   Plan best = {};
   double best_cost = 1e300;
   const int stages = (steps + 1) / 2;
   for (int bx = 64; bx <= 256; bx *= 2) {
     const int64_t tiles_x = (rows + bx - 1) / bx;
     const int64_t tiles = tiles_x * ((lanes + kTileW - 1) / kTileW);
-    const double stage = bx == 64 ? 560 : bx == 128 ? 640 : 1120;
-    const double end = bx == 64 ? 200 : bx == 128 ? 1500 : 1500;
+    const double stage = bx < 256 ? (back ? 1300 : 1000) : (back ? 1800 : 1500);
+    const double end = bx == 64 ? 200 : 1500;
     const double rounds = double((tiles + sms - 1) / sms);
     double cost = rounds * (stages * stage + end) + 5000;
     if (cost < best_cost) {
@@ -791,7 +836,7 @@ Plan plan_gemm(int64_t lanes, int64_t rows, int steps, int sms) {
     const int64_t units = tiles * stages;
     const int ctas = int(units < sms ? units : sms);
     const double run = double(units) / ctas, sharers = stages / run + 1;
-    cost = (run + 1) * stage + (run / stages + 1) * end + 5000 + 4000 + bx * (15 + 5 * sharers);
+    cost = (run + 1) * stage + (run / stages + 1) * end + 5000 + 4000 + bx * (8 + 4 * sharers);
     if (cost < best_cost) {
       best_cost = cost;
       best = {bx, stages, tiles_x, tiles, ctas, true};
@@ -832,14 +877,14 @@ int64_t part_bytes(const Plan& pl) {
 }  // namespace
 
 int64_t int8_gemm_workspace(int64_t M, int64_t N, int64_t K, int L, int sms) {
-  const Plan pl = plan_gemm(N, M, all_steps(K, L), sms);
+  const Plan pl = plan_gemm(N, M, all_steps(K, L), false, sms);
   return kInt8Counters + up256(kMaxOutliers * 4) + up256(M * 4) +
          up256(M * all_steps(K, L) * kStep * 2) + part_bytes(pl);
 }
 
 int launch_int8_gemm(const Int8Linear& a, int dev, int sms, void* workspace, cudaStream_t stream) {
   const int steps = all_steps(a.K, a.L);
-  const Plan pl = plan_gemm(a.N, a.M, steps, sms);
+  const Plan pl = plan_gemm(a.N, a.M, steps, false, sms);
   char* at = static_cast<char*>(workspace);
   int* count = reinterpret_cast<int*>(at);
   at += kInt8Counters;
@@ -881,12 +926,12 @@ int launch_int8_gemm(const Int8Linear& a, int dev, int sms, void* workspace, cud
 }
 
 int64_t int8_backward_workspace(int64_t M, int64_t N, int64_t K, int sms) {
-  return kInt8Counters + part_bytes(plan_gemm(K, M, code_steps(N), sms));
+  return kInt8Counters + part_bytes(plan_gemm(K, M, code_steps(N), true, sms));
 }
 
 int launch_int8_backward(const Int8Backward& a, int dev, int sms, void* workspace,
                          cudaStream_t stream) {
-  const Plan pl = plan_gemm(a.K, a.M, code_steps(a.N), sms);
+  const Plan pl = plan_gemm(a.K, a.M, code_steps(a.N), true, sms);
   CUtensorMap w, x;
   if (const int st = encode_2d(&w, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.CB, a.K, a.N, a.K, kTileW,
                                kStage, CU_TENSOR_MAP_SWIZZLE_NONE))

@@ -56,7 +56,7 @@ constexpr int kAhead = 4;     // outlier columns whose codes are loaded ahead
 // jobs in turn, as in int8.cuh, a call took 4 to 5 us more).  The order of K in a product is
 // free: lane (g, c) takes 32 consecutive codes of rows g and g + 8, and of token g of each 8.
 template <int NT, int kFewDepth>
-__global__ void __launch_bounds__(kStreamThreads, kFewDepth == 2 ? 3 : 2)
+__global__ void __launch_bounds__(kStreamThreads, kFewDepth == 2 && NT < 4 ? 3 : 2)
     dq4_int8_few_kernel(const __grid_constant__ CUtensorMap map_w, const Int8Linear p,
                         const int group) {
   constexpr int kTokens = 8 * NT, kStage = kFewRows * kChunk;
@@ -220,8 +220,14 @@ __global__ void __launch_bounds__(kStreamThreads, kFewDepth == 2 ? 3 : 2)
   }
 }
 
-// Whether a product goes to the kernel for few rows.
-bool few_rows(int64_t M, int64_t K) { return M <= 8 || K == 0; }
+// Whether a product goes to the kernel for few rows: up to 16, and up to 32 where the weight is
+// small.  Few / many, in us:
+//   rows          4096 x 4096    4096 to 11008   14336 to 4096   8192 to 28672
+//     16          6.6 / 16.9     14.9 / 22.7     16.1 / 30.5      50 / 60
+//     32         12.3 / 17.1     23.4 / 22.6     29.8 / 30.3      75 / 60
+bool few_rows(int64_t M, int64_t N, int64_t K) {
+  return M <= 16 || (M <= 32 && N * K <= 32 << 20) || K == 0;
+}
 
 template <int NT, int kFewDepth>
 int launch_few_depth(const CUtensorMap& w, const Int8Linear& p, int64_t grid, int group, int dev,
@@ -267,7 +273,7 @@ extern "C" {
 
 int64_t dq4_int8_linear_workspace_bytes(int64_t M, int64_t N, int64_t K, int32_t L) {
   if (M <= 0 || N <= 0 || K < 0 || L < 0 || L > kMaxOutliers || M > INT32_MAX || N > INT32_MAX ||
-      K > INT32_MAX || few_rows(M, K))
+      K > INT32_MAX || few_rows(M, N, K))
     return 0;
   int dev, sms;
   if (current_device(&dev, &sms) != DQ4_OK) return -DQ4_ERR_DEVICE;
@@ -297,13 +303,13 @@ int dq4_int8_linear(const int8_t* codes, const float* scales, const int8_t* CB, 
   const Int8Linear p = {codes, scales, CB, SCB, M, N, K, cols, outliers, L,
                         L > 0 && outlier_dtype == DQ4_OUT_BF16, bias, out_dtype, Y, bad};
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (!few_rows(M, K)) {
+  if (!few_rows(M, N, K)) {
     if (!workspace || workspace_bytes < int8_gemm_workspace(M, N, K, L, sms))
       return DQ4_ERR_WORKSPACE;
     if (misaligned(workspace, 256)) return DQ4_ERR_ALIGN;
     return launch_int8_gemm(p, dev, sms, workspace, s);
   }
-  return M <= 8 ? launch_few<1>(p, dev, sms, s) : launch_few<2>(p, dev, sms, s);
+  return M <= 8 ? launch_few<1>(p, dev, sms, s) : M <= 16 ? launch_few<2>(p, dev, sms, s) : launch_few<4>(p, dev, sms, s);
 }
 
 }  // extern "C"

@@ -567,8 +567,10 @@ int dq4_int8_moe(const void* X, int64_t row_stride, int32_t dtype, int64_t T, in
   at += T * top_k * up256(I / 4);
   p.out = reinterpret_cast<float*>(at);
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (T * top_k <= 6 * E) return launch_moe<1, 2, 2, 2, 2>(p, dev, sms, s);
-  return launch_moe<2, 2, 2, 2, 2>(p, dev, sms, s);
+  // (entries of 16 pairs, two products for each weight's conversion, took more: for 64 tokens
+  // through 2 of 8 experts of 4096 x 14336, 16 pairs each, 443 us, in eights, which read the weights
+  // twice from L2, 409; for 23 tokens 302 and 237)
+  return launch_moe<1, 2, 2, 2, 2>(p, dev, sms, s);
 }
 
 }  // extern "C"
