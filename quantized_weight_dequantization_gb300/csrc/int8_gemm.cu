@@ -463,18 +463,27 @@ __global__ void __launch_bounds__(Gemm<BX, kBack>::kThreads, 1)
               // what the outliers' lower halves multiply: their columns, gathered
               const int8_t* row = p.CB + (it.lane0 + r) * p.K;
               const bool in = it.lane0 + r < p.N;
+              const int* cols = s_cols + (step - p.code_steps) * kStep;
 #pragma unroll 1
-              for (int c = 0; c < 4; ++c) {
-                uint32_t o[8];
+              for (int c = 0; c < 4; ++c, cols += 16) {
+                int col[16], most = -1;
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                  uint32_t w = 0;
+                for (int j = 0; j < 16; ++j) {
+                  col[j] = cols[j];
+                  most = max(most, col[j]);
+                }
+                uint32_t o[8] = {};
+                if (most >= 0) {
+                  uint32_t code[16];
 #pragma unroll
-                  for (int b = 0; b < 4; ++b) {
-                    const int col = s_cols[(step - p.code_steps) * kStep + 16 * c + 4 * j + b];
-                    if (in && col >= 0) w |= uint32_t(uint8_t(load_global(row + col))) << (8 * b);
+                  for (int j = 0; j < 16; ++j) {
+                    code[j] = 0;
+                    if (in && col[j] >= 0) code[j] = uint8_t(load_global(row + col[j]));
                   }
-                  codes_f16(w, o[2 * j], o[2 * j + 1]);
+#pragma unroll
+                  for (int j = 0; j < 4; ++j)
+                    codes_f16(code[4 * j] | code[4 * j + 1] << 8 | code[4 * j + 2] << 16 |
+                                  code[4 * j + 3] << 24, o[2 * j], o[2 * j + 1]);
                 }
                 tmem_st<8>(to + 8 * c, o);
               }
@@ -541,15 +550,15 @@ __global__ void __launch_bounds__(Gemm<BX, kBack>::kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(acc_empty(buffer));
       };
-      auto finish = [&](uint32_t acc, int c, int j) {
+      // 32 columns (activation rows) in the output's type, two in a word; u: their units, a lane each
+      auto finish = [&](uint32_t acc, float u, int j) {
         if constexpr (kBack) return __uint_as_float(acc);
-        else return __uint_as_float(acc) * __shfl_sync(kAllLanes, unit[c], j) * scale + bias;
+        else return __uint_as_float(acc) * __shfl_sync(kAllLanes, u, j) * scale + bias;
       };
-      // 32 columns (activation rows) from c on: to the output's type, two in a word
-      auto pack = [&](const uint32_t (&v)[32], int c, uint32_t* to) {
+      auto pack = [&](const uint32_t (&v)[32], float u, uint32_t* to) {
 #pragma unroll
         for (int j = 0; j < 32; j += 2) {
-          const float a = finish(v[j], c, j), b = finish(v[j + 1], c, j + 1);
+          const float a = finish(v[j], u, j), b = finish(v[j + 1], u, j + 1);
           to[j / 2] = bf16 ? pack2<DQ4_OUT_BF16>(a, b) : pack2<DQ4_OUT_F16>(a, b);
         }
       };
@@ -571,44 +580,31 @@ __global__ void __launch_bounds__(Gemm<BX, kBack>::kThreads, 1)
           }
         }
       };
-      auto store_f32 = [&](const uint32_t (&v)[32], int c) {
-        float* out = static_cast<float*>(p.out);
+      const bool whole = it.begin == 0 && it.end == stages;
+      if (whole && !f32) {
+        // all of the tile to registers, so that the next one can start, then the stores
+        uint32_t keep[kHalf / 2];
 #pragma unroll
-        for (int j = 0; j < 32; ++j) {
-          const int64_t m = m0 + 32 * c + j;
-          const float y = finish(v[j], c, j);
-          if (m < p.rows && n < p.lanes) out[m * p.lanes + n] = y;
+        for (int c = 0; c < kChunks; ++c) {
+          uint32_t v[32];
+          read(c, v);
+          pack(v, unit[c], keep + 16 * c);
         }
-      };
-      if (it.begin == 0 && it.end == stages) {
-        if (f32) {
+        release();
 #pragma unroll
-          for (int c = 0; c < kChunks; ++c) {
-            uint32_t v[32];
-            read(c, v);
-            store_f32(v, c);
-          }
-          release();
-        } else {
-          // all of the tile to registers, so that the next one can start, then the stores
-          uint32_t keep[kHalf / 2];
-#pragma unroll
-          for (int c = 0; c < kChunks; ++c) {
-            uint32_t v[32];
-            read(c, v);
-            pack(v, c, keep + 16 * c);
-          }
-          release();
-#pragma unroll
-          for (int c = 0; c < kChunks; ++c) store(keep + 16 * c, c);
-        }
+        for (int c = 0; c < kChunks; ++c) store(keep + 16 * c, c);
         continue;
       }
+      // (What follows runs once or twice in a CTA: loops, as code that is fetched for the first time
+      // takes longer than its instructions.  Unrolled, a join of three 64 KB parts took 14 us.)
       // ---- a part of the sum (the CTA's first if the tile began before it, else its last); the
       // last of a tile's parts adds them, in their order
       auto part_at = [&](int64_t cta, int which) {
         return p.part + ((cta * 2 + which) * (BX / 4) + half * (kHalf / 4)) * kTileW + quad * 32 + lane;
       };
+      int64_t cta0 = 0;
+      int sharers = 0;
+      if (!whole) {
       float4* part = part_at(blockIdx.x, it.begin == 0);
 #pragma unroll 1
       for (int c = 0; c < kChunks; ++c) {
@@ -622,81 +618,89 @@ __global__ void __launch_bounds__(Gemm<BX, kBack>::kThreads, 1)
       }
       release();
       bar_readers();
-      const int64_t cta0 = cta_of(it.tile * stages), cta1 = cta_of((it.tile + 1) * stages - 1);
+      const int64_t cta1 = cta_of((it.tile + 1) * stages - 1);
+      cta0 = cta_of(it.tile * stages);
+      sharers = int(cta1 - cta0) + 1;
       if (tid == 32 * kProducers) {
         s_last = atomic_add_acq_rel(p.count + cta1, 1) == int(cta1 - cta0);
         if (s_last) p.count[cta1] = 0;  // ready for the next call
       }
       bar_readers();
       if (!s_last) continue;
-      const int sharers = int(cta1 - cta0) + 1;
-      // The CTA's last item: the rings are idle, and the parts are copied into them, many at once.
-      const bool idle = walk >= walk1;
-      const int pieces = kChunks * sharers;  // piece i: 32 columns i / sharers of part i % sharers
-      auto copy = [&](int i) {
-        const int c = i / sharers, q = i - c * sharers;
-        const uint32_t dst = sbase + i % S::kPieces * S::kPiece, bar = piece_full(i % S::kPieces);
-        const float4* from = p.part + ((cta0 + q) * 2 + (q == 0)) * (BX / 4 * kTileW);
-        mbar_expect(bar, S::kPiece);
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
+      }
+      // The CTA's last item: the rings are idle, and the parts are copied into them, 32 columns of
+      // all of them at a time (which the first reader warp issues), the next ones ahead.
+      const bool idle = !whole && walk >= walk1 && sharers <= S::kPieces;
+      const int depth = idle ? S::kPieces / sharers : 1;
+      auto copy = [&](int c) {
+        const uint32_t bar = piece_full(c % depth);
+        if (lane == 0) mbar_expect(bar, sharers * S::kPiece);
+        __syncwarp();
+        const int q = lane >> 1, h = lane & 1;
+        if (q < sharers)
           asm volatile(
               "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
-              :: "r"(dst + h * (S::kPiece / 2)), "l"(from + (h * (kHalf / 4) + 8 * c) * kTileW),
+              :: "r"(sbase + (c % depth * sharers + q) * S::kPiece + h * (S::kPiece / 2)),
+                 "l"(p.part + ((cta0 + q) * 2 + (q == 0)) * (BX / 4 * kTileW) +
+                     (h * (kHalf / 4) + 8 * c) * kTileW),
                  "r"(S::kPiece / 2), "r"(bar) : "memory");
       };
-      if (idle && tid == 32 * kProducers) {
+      if (idle && warp == kProducers) {
         // (the parts were written by ordinary stores, and are read by the copies' own path)
         asm volatile("fence.proxy.async;" ::: "memory");
-        for (int i = 0; i < pieces && i < S::kPieces; ++i) copy(i);
+        for (int c = 0; c < kChunks && c < depth; ++c) copy(c);
       }
-      int at_piece = 0;
       bool here = true;
-#pragma unroll
-      for (int c = 0; c < kChunks; ++c) {
-        float4 sum[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) sum[j] = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 1
-        for (int q = 0; q < sharers; ++q, ++at_piece) {
-          float4 more[8];
-          if (idle) {
-            here = here && mbar_wait(piece_full(at_piece % S::kPieces),
-                                     uint32_t(at_piece / S::kPieces) & 1u);
-            const uint32_t from = sbase + at_piece % S::kPieces * S::kPiece + half * (S::kPiece / 2) +
-                                  (quad * 32 + lane) * 16;
+      for (int c = 0; c < kChunks; ++c) {
+        uint32_t v[32];
+        if (whole) {
+          read(c, v);
+        } else {
+          if (idle) here = here && mbar_wait(piece_full(c % depth), uint32_t(c / depth) & 1u);
+          uint32_t at = sbase + c % depth * sharers * S::kPiece + half * (S::kPiece / 2) +
+                        (quad * 32 + lane) * 16;
+          float sum[32] = {};
+#pragma unroll 1
+          for (int q = 0; q < sharers; ++q, at += S::kPiece) {
+            const float4* from = part_at(cta0 + q, q == 0) + 8 * c * kTileW;
+            float more[32];
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-              const uint4 v = lds_v4(from + j * kTileW * 16);
-              memcpy(&more[j], &v, 16);
+              if (idle) {
+                const uint4 w = lds_v4(at + j * kTileW * 16);
+                memcpy(&more[4 * j], &w, 16);
+              } else {
+                const float4 w = load_l2(from + j * kTileW);
+                memcpy(&more[4 * j], &w, 16);
+              }
             }
-            if (at_piece + S::kPieces < pieces) {  // its place, for a later piece
-              bar_readers();
-              if (tid == 32 * kProducers) copy(at_piece + S::kPieces);
-            }
-          } else {
-            const float4* from = part_at(cta0 + q, q == 0) + 8 * c * kTileW;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) more[j] = load_l2(from + j * kTileW);
+            for (int j = 0; j < 32; ++j) sum[j] += more[j];
           }
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            sum[j].x += more[j].x;
-            sum[j].y += more[j].y;
-            sum[j].z += more[j].z;
-            sum[j].w += more[j].w;
+          memcpy(v, sum, sizeof(v));
+          if (idle && c + depth < kChunks) {  // their place, for later ones
+            bar_readers();
+            if (warp == kProducers) copy(c + depth);
           }
         }
-        uint32_t v[32];
-        memcpy(v, sum, sizeof(v));
+        float u = 0.f;
+        if constexpr (!kBack)
+          if (m0 + 32 * c + lane < p.rows) u = load_global(p.row_units + m0 + 32 * c + lane);
         if (f32) {
-          store_f32(v, c);
+          float* out = static_cast<float*>(p.out) + (m0 + 32 * c) * p.lanes + n;
+#pragma unroll
+          for (int j = 0; j < 32; ++j) {
+            const float y = finish(v[j], u, j);
+            if (m0 + 32 * c + j < p.rows && n < p.lanes) out[j * p.lanes] = y;
+          }
         } else {
           uint32_t keep[16];
-          pack(v, c, keep);
+          pack(v, u, keep);
           store(keep, c);
         }
       }
+      if (whole) release();
       if (!here && lane == 0) fail();
     }
   }
@@ -729,25 +733,29 @@ struct RowArgs {
 // where the weight's column is gathered again.  FP16 ends at 65504: where an outlier is above
 // 2^15 u, the unit is 2^-15 of it, and codes are rounded to FP16 with what they are in it.
 __global__ void __launch_bounds__(256) int8_rows_kernel(const RowArgs p) {
-  __shared__ int64_t s_cols[kMaxOutliers];
+  __shared__ int64_t s_most[8];
   __shared__ uint32_t s_top[8];
   wait_for_stream();
   asm volatile("griddepcontrol.launch_dependents;");
   const int t = threadIdx.x;
   int64_t col = -1;  // of entry t, if it is used
   if (p.L > 0) {
-    if (t < kMaxOutliers) s_cols[t] = t < p.L ? load_global(p.cols + t) : -1;
-    __syncthreads();
-    int wrong = 0;
-    if (t < kMaxOutliers) {
-      int64_t top = -1;
-      for (int l = 0; l < min(t, p.L); ++l)
-        if (s_cols[l] < p.K) top = max(top, s_cols[l]);
-      const int64_t c = s_cols[t];
-      if (c > top && c < p.K) col = c;
-      wrong = col < 0 && c != -1;
-      if (blockIdx.x == 0) p.used[t] = int32_t(col);
+    // used: in range and above all before it (the largest so far, by warps and then over them)
+    const int64_t c = t < p.L ? load_global(p.cols + t) : -1;
+    int64_t run = c < p.K ? c : -1;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t up = __shfl_up_sync(kAllLanes, run, o);
+      if ((t & 31) >= o && up > run) run = up;
     }
+    if ((t & 31) == 31) s_most[t >> 5] = run;
+    int64_t top = __shfl_up_sync(kAllLanes, run, 1);
+    if ((t & 31) == 0) top = -1;
+    __syncthreads();
+    for (int w = 0; w < t >> 5; ++w) top = max(top, s_most[w]);
+    if (c > top && c < p.K && c >= 0) col = c;
+    const int wrong = col < 0 && c != -1;
+    if (t < kMaxOutliers && blockIdx.x == 0) p.used[t] = int32_t(col);
     if (blockIdx.x == 0 && wrong && p.bad) atomicAdd(p.bad, 1);
   }
   const int64_t codes_end = (p.K + kStep - 1) / kStep * kStep;
@@ -806,6 +814,8 @@ __global__ void __launch_bounds__(256) int8_rows_kernel(const RowArgs p) {
 // ------------------------------------------------------------------------ host side
 int64_t up256(int64_t n) { return (n + 255) / 256 * 256; }
 
+constexpr double kBackStage = 300;  // columns of codes to values
+
 struct Plan {
   int bx, stages;
   int64_t tiles_x, tiles;
@@ -814,10 +824,12 @@ struct Plan {
 };
 
 // The tile's width, and whether CTAs take whole tiles or equal runs of stages, by the estimated
-// time in cycles: a stage takes about 1000 at BX 64 and 128 and 1500 at 256 (the MMAs: 122 each,
-// at 256 181), for the gradient 1300 to 1800 (columns of codes to values); the end of a tile some
-// more where its accumulator is the only one, a CTA 5000 to start and end, and parts of tiles
-// have to be written and added.
+// time in cycles.  A stage takes about 1000 at BX 64 and 128 and 1500 at 256 (the MMAs: 122 each,
+// at 256 181), for the gradient kBackStage more; the end of a tile 1500 where its accumulator is the
+// only one.  Parts of tiles cost their writing (40 bytes a cycle), the count (3000), and the reading
+// of all parts of a tile by one CTA, at 56 bytes a cycle: for wide tiles that few stages share,
+// more than the SMs that whole tiles leave idle.  512 rows through 4096 x 4096, in us: 256 wide in
+// parts 37, whole 25.
 Plan plan_gemm(int64_t lanes, int64_t rows, int steps, bool back, int sms) {
   Plan best = {};
   double best_cost = 1e300;
@@ -825,10 +837,10 @@ Plan plan_gemm(int64_t lanes, int64_t rows, int steps, bool back, int sms) {
   for (int bx = 64; bx <= 256; bx *= 2) {
     const int64_t tiles_x = (rows + bx - 1) / bx;
     const int64_t tiles = tiles_x * ((lanes + kTileW - 1) / kTileW);
-    const double stage = bx < 256 ? (back ? 1300 : 1000) : (back ? 1800 : 1500);
-    const double end = bx == 64 ? 200 : 1500;
+    const double stage = (bx < 256 ? 1000 : 1500) + (back ? kBackStage : 0);
+    const double end = bx == 64 ? 200 : 1500, last = bx / 64 * 700 + 5000;
     const double rounds = double((tiles + sms - 1) / sms);
-    double cost = rounds * (stages * stage + end) + 5000;
+    double cost = rounds * (stages * stage + end) + last;
     if (cost < best_cost) {
       best_cost = cost;
       best = {bx, stages, tiles_x, tiles, int(tiles < sms ? tiles : sms), false};
@@ -836,7 +848,8 @@ Plan plan_gemm(int64_t lanes, int64_t rows, int steps, bool back, int sms) {
     const int64_t units = tiles * stages;
     const int ctas = int(units < sms ? units : sms);
     const double run = double(units) / ctas, sharers = stages / run + 1;
-    cost = (run + 1) * stage + (run / stages + 1) * end + 5000 + 4000 + bx * (8 + 4 * sharers);
+    cost = (run + 1) * stage + (run / stages + 1) * end + last + bx / 64 * 600 + 3000 +
+           bx * (13 + 9 * sharers);
     if (cost < best_cost) {
       best_cost = cost;
       best = {bx, stages, tiles_x, tiles, ctas, true};
