@@ -51,21 +51,20 @@ struct Gemm {
   static constexpr int kPieces = kBarsAt / kPiece;
   static constexpr int kBars = 2 * kSlots + 2 * kRawSlots + 2 * kRing + 2 * kBuffers + 1 + kPieces;
   static constexpr int kBytes = kBarsAt + 8 * kBars + 1024;  // + alignment slack
-  static constexpr int kStatic = kBack ? 16 * kStage + 64 : 4 * kMaxOutliers + 64;
+  static constexpr int kStatic = kBack ? 16 * kStage + 64 : 64;
   static_assert(kBytes + kStatic <= 227 * 1024, "shared memory budget");
   static_assert(kBytes > 116 * 1024, "one CTA per SM: the TMEM allocation never waits");
 };
 
 struct GemmArgs {
   int64_t lanes, rows;   // of the output: weight rows (columns), activation rows
-  int steps, code_steps; // K steps, and of them with codes from CB (the rest: outlier columns)
+  int steps, code_steps; // K steps, and of them with codes from CB (the rest: outlier columns, from
+                         // their own matrix)
   int tiles_x;           // tiles along the activations
   int64_t tiles;
   int64_t units;         // tiles * stages, if CTAs take equal runs of them; 0: whole tiles in turn
-  const int8_t* CB;
   const float* SCB;
-  int64_t K, N;
-  const int32_t* cols;   // the outlier columns that are used, -1 for none
+  int64_t N;             // weight rows
   const float* row_units;  // of the activation rows
   const void* bias;
   int out_dtype;
@@ -90,10 +89,20 @@ __device__ __forceinline__ void commit(uint32_t bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];"
                :: "r"(bar) : "memory");
 }
-__device__ __forceinline__ uint32_t lds_u8(uint32_t addr) {
-  uint32_t v;
-  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(addr));
-  return v;
+// Four 8 x 8 matrices of 16-bit elements, transposed; a thread gives the address of a row.
+__device__ __forceinline__ void load_transposed(uint32_t addr, uint32_t* m) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(m[0]), "=r"(m[1]), "=r"(m[2]), "=r"(m[3]) : "r"(addr) : "memory");
+}
+// 16 lanes of TMEM, 32 columns: words 4i, 4i + 1 of a thread are columns 8i + 2 (lane % 4) and
+// the next of lane / 4, words 4i + 2, 4i + 3 those of lane / 4 + 8.
+__device__ __forceinline__ void tmem_st_16(uint32_t taddr, const uint32_t (&v)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.16x256b.x4.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
+      "%14,%15,%16};"
+      :: "r"(taddr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]),
+         "r"(v[7]), "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]),
+         "r"(v[14]), "r"(v[15]));
 }
 // {a, b} + {c, c} and {a, b} * {c, d}, each rounded on its own.
 __device__ __forceinline__ uint64_t pair_of(uint32_t a, uint32_t b) {
@@ -128,7 +137,8 @@ struct Place {
 template <int BX, bool kBack, bool kBF16>
 __global__ void __launch_bounds__(Gemm<BX, kBack>::kThreads, 1)
     dq4_int8_gemm_kernel(const __grid_constant__ CUtensorMap map_w,
-                         const __grid_constant__ CUtensorMap map_x, const GemmArgs p) {
+                         const __grid_constant__ CUtensorMap map_x,
+                         const __grid_constant__ CUtensorMap map_cols, const GemmArgs p) {
   using S = Gemm<BX, kBack>;
   constexpr int kIssuers = S::kIssuers, kBuffers = S::kBuffers, kSlots = S::kSlots;
   constexpr int kOut = kBF16 ? DQ4_OUT_BF16 : DQ4_OUT_F16;
@@ -137,7 +147,6 @@ __global__ void __launch_bounds__(Gemm<BX, kBack>::kThreads, 1)
   __shared__ uint32_t s_tmem;
   __shared__ volatile int s_abort;
   __shared__ bool s_last;
-  __shared__ int s_cols[kBack ? 1 : kMaxOutliers];
   __shared__ __align__(16) float s_scale[kBack ? 4 * kStage : 4];  // two stages of each group
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
@@ -194,8 +203,6 @@ __global__ void __launch_bounds__(Gemm<BX, kBack>::kThreads, 1)
   }
   wait_for_stream();
   asm volatile("griddepcontrol.launch_dependents;");
-  if (!kBack && p.cols)
-    for (int l = tid; l < kMaxOutliers; l += S::kThreads) s_cols[l] = load_global(p.cols + l);
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
   __syncthreads();
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
@@ -238,6 +245,7 @@ __global__ void __launch_bounds__(Gemm<BX, kBack>::kThreads, 1)
     if (lane == 0) {
       // ---- the weight's codes: 128 rows of 128 bytes a stage
       const uint64_t map = reinterpret_cast<uint64_t>(&map_w);
+      const uint64_t cols = reinterpret_cast<uint64_t>(&map_cols);
       Place<kRawSlots> at;
       int g = 0;
       bool stop = false;
@@ -249,11 +257,14 @@ __global__ void __launch_bounds__(Gemm<BX, kBack>::kThreads, 1)
             stop = true;
             break;
           }
-          const bool codes = kBack || 2 * s < p.code_steps;
-          mbar_expect(raw_full(at.slot), codes ? kRawSlot : 0);
-          if (codes)
-            tma_load_2d(sbase + S::kRawAt + at.slot * kRawSlot, map,
-                        kBack ? int(it.lane0) : s * kStage, kBack ? s * kStage : int(it.lane0),
+          const uint32_t to = sbase + S::kRawAt + at.slot * kRawSlot;
+          mbar_expect(raw_full(at.slot), kRawSlot);
+          if constexpr (kBack)
+            tma_load_2d(to, map, int(it.lane0), s * kStage, raw_full(at.slot));
+          else if (2 * s < p.code_steps)
+            tma_load_2d(to, map, s * kStage, int(it.lane0), raw_full(at.slot));
+          else
+            tma_load_2d(to, cols, s * kStage - p.code_steps * kStep, int(it.lane0),
                         raw_full(at.slot));
         }
       }
@@ -424,70 +435,57 @@ __global__ void __launch_bounds__(Gemm<BX, kBack>::kThreads, 1)
         for (int sub = 0; sub < n; ++sub) {
           const uint32_t to = to0 + (wp.slot * 2 + sub) * 32;
           if constexpr (kBack) {
-            // column r of 64 rows: consecutive lanes read consecutive bytes
-            const uint32_t from = raw + sub * kStep * kTileW + r;
-            const float* sc = s_scale + (group * 2 + scale_turn) * kStage + sub * kStep;
+            // Rows are 128 bytes, their 16-byte pieces at place ^ row % 8.  A matrix of the load is
+            // 8 rows of 8 pairs of columns; transposed, a thread has pair lane / 4 of two rows.
+            // With rows 0, 1, 4, 5, 8, ... in one and 2, 3, 6, 7, ... in the next it has four rows
+            // that follow one another, which is what it stores of a TMEM lane; columns 2c and 2c +
+            // 1 become lanes c and c + 8.  (A byte at a time, a column a thread: 64 loads a step in
+            // place of 4, and 2047 rows through 11008 x 4096 took 160 us; so 150.)
+            const float* sc =
+                s_scale + (group * 2 + scale_turn) * kStage + sub * kStep + 4 * (lane & 3);
+            const int row = sub * kStep + (lane >> 4) * 16 + (lane >> 3 & 1) * 2 +
+                            (lane >> 1 & 3) * 4 + (lane & 1);
+            const uint32_t from = raw + row * kTileW;
             const uint64_t off = pair_of(0xCB000080u, 0xCB000080u);  // -(2^23 + 128)
-            const uint32_t r127 = __float_as_uint(kRecip127);
+            const uint64_t r127 = pair_of(__float_as_uint(kRecip127), __float_as_uint(kRecip127));
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              uint32_t o[16], m[8];
+              const uint32_t piece = ((2 * quad + h) ^ (row & 7)) << 4;
+              load_transposed(from + piece, m);
+              load_transposed(from + 32 * kTileW + piece, m + 4);
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const float4 f = *reinterpret_cast<const float4*>(sc + 16 * i);
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                  const uint32_t x = m[2 * i + j] ^ 0x80808080u;
+                  const uint64_t scale2 = j ? pair_of(__float_as_uint(f.z), __float_as_uint(f.w))
+                                            : pair_of(__float_as_uint(f.x), __float_as_uint(f.y));
+#pragma unroll
+                  for (int c = 0; c < 2; ++c) {
+                    // 2^23 + (code + 128), exactly
+                    const uint64_t u = pair_of(__byte_perm(x, 0x4B000000u, c ? 0x7651 : 0x7650),
+                                               __byte_perm(x, 0x4B000000u, c ? 0x7653 : 0x7652));
+                    const uint64_t w = mul_pair(mul_pair(add_pair(u, off), scale2), r127);
+                    o[4 * i + 2 * c + j] = pack2<kOut>(__uint_as_float(uint32_t(w)),
+                                                       __uint_as_float(uint32_t(w >> 32)));
+                  }
+                }
+              }
+              tmem_st_16(to + (uint32_t(16 * h) << 16), o);
+            }
+          } else {
             uint32_t o[32];
 #pragma unroll
-            for (int j = 0; j < 32; j += 2) {
-              const float4 f = *reinterpret_cast<const float4*>(sc + 2 * j);
-#pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                // 2^23 + (code + 128), exactly
-                const uint64_t u = pair_of(lds_u8(from + (2 * (j + h)) * kTileW) ^ 0x4B000080u,
-                                           lds_u8(from + (2 * (j + h) + 1) * kTileW) ^ 0x4B000080u);
-                const uint64_t w = mul_pair(
-                    mul_pair(add_pair(u, off), h ? pair_of(__float_as_uint(f.z), __float_as_uint(f.w))
-                                                 : pair_of(__float_as_uint(f.x), __float_as_uint(f.y))),
-                    pair_of(r127, r127));
-                o[j + h] = pack2<kOut>(__uint_as_float(uint32_t(w)), __uint_as_float(uint32_t(w >> 32)));
-              }
+            for (int c = 0; c < 4; ++c) {
+              const uint4 w = lds_v4(raw + r * kStage + (((4 * sub + c) ^ (r & 7)) << 4));
+              codes_f16(w.x, o[8 * c], o[8 * c + 1]);
+              codes_f16(w.y, o[8 * c + 2], o[8 * c + 3]);
+              codes_f16(w.z, o[8 * c + 4], o[8 * c + 5]);
+              codes_f16(w.w, o[8 * c + 6], o[8 * c + 7]);
             }
             tmem_st<32>(to, o);
-          } else {
-            const int step = 2 * s + sub;
-            if (step < p.code_steps) {
-              uint32_t o[32];
-#pragma unroll
-              for (int c = 0; c < 4; ++c) {
-                const uint4 w = lds_v4(raw + r * kStage + (((4 * sub + c) ^ (r & 7)) << 4));
-                codes_f16(w.x, o[8 * c], o[8 * c + 1]);
-                codes_f16(w.y, o[8 * c + 2], o[8 * c + 3]);
-                codes_f16(w.z, o[8 * c + 4], o[8 * c + 5]);
-                codes_f16(w.w, o[8 * c + 6], o[8 * c + 7]);
-              }
-              tmem_st<32>(to, o);
-            } else {
-              // what the outliers' lower halves multiply: their columns, gathered
-              const int8_t* row = p.CB + (it.lane0 + r) * p.K;
-              const bool in = it.lane0 + r < p.N;
-              const int* cols = s_cols + (step - p.code_steps) * kStep;
-#pragma unroll 1
-              for (int c = 0; c < 4; ++c, cols += 16) {
-                int col[16], most = -1;
-#pragma unroll
-                for (int j = 0; j < 16; ++j) {
-                  col[j] = cols[j];
-                  most = max(most, col[j]);
-                }
-                uint32_t o[8] = {};
-                if (most >= 0) {
-                  uint32_t code[16];
-#pragma unroll
-                  for (int j = 0; j < 16; ++j) {
-                    code[j] = 0;
-                    if (in && col[j] >= 0) code[j] = uint8_t(load_global(row + col[j]));
-                  }
-#pragma unroll
-                  for (int j = 0; j < 4; ++j)
-                    codes_f16(code[4 * j] | code[4 * j + 1] << 8 | code[4 * j + 2] << 16 |
-                                  code[4 * j + 3] << 24, o[2 * j], o[2 * j + 1]);
-                }
-                tmem_st<8>(to + 8 * c, o);
-              }
-            }
           }
         }
         if constexpr (kBack) scale_turn ^= 1;
@@ -505,13 +503,16 @@ __global__ void __launch_bounds__(Gemm<BX, kBack>::kThreads, 1)
     constexpr int kHalf = BX / 2, kChunks = kHalf / 32;
     const int quad = warp & 3, half = (warp - kProducers) >> 2;
     const bool f32 = p.out_dtype == DQ4_OUT_F32, bf16 = p.out_dtype == DQ4_OUT_BF16;
+    // the column of this lane (see the gradient's values above)
+    const int column = quad * 32 + (kBack ? (lane & 16) + (lane & 7) * 2 + (lane >> 3 & 1) : lane);
     // two lanes exchange a value, so that a store takes four bytes
+    constexpr int kNext = kBack ? 8 : 1;
     const bool pairs = !f32 && p.lanes % 2 == 0 && (reinterpret_cast<uintptr_t>(p.out) & 3) == 0;
     int turn = 0, g = 0;
     Item it;
     for (int64_t walk = walk0; next_item(walk, it); ++turn) {
       const int buffer = turn % kBuffers;
-      const int64_t n = it.lane0 + quad * 32 + lane, m0 = it.row0 + half * kHalf;
+      const int64_t n = it.lane0 + column, m0 = it.row0 + half * kHalf;
       float scale = 1.f, bias = 0.f, unit[kChunks];
       if constexpr (!kBack) {
         if (n < p.lanes) {
@@ -520,7 +521,8 @@ __global__ void __launch_bounds__(Gemm<BX, kBack>::kThreads, 1)
         }
 #pragma unroll
         for (int c = 0; c < kChunks; ++c)
-          unit[c] = m0 + 32 * c + lane < p.rows ? load_global(p.row_units + m0 + 32 * c + lane) : 0.f;
+          unit[c] =
+              m0 + 32 * c + lane < p.rows ? load_global(p.row_units + m0 + 32 * c + lane) : 0.f;
       }
       const bool ok = !*aborted && mbar_wait(acc_full(buffer), uint32_t(turn / kBuffers) & 1u) &&
                       !*aborted;
@@ -550,7 +552,8 @@ __global__ void __launch_bounds__(Gemm<BX, kBack>::kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(acc_empty(buffer));
       };
-      // 32 columns (activation rows) in the output's type, two in a word; u: their units, a lane each
+      // 32 columns (activation rows) in the output's type, two in a word; u: their units, a lane
+      // each
       auto finish = [&](uint32_t acc, float u, int j) {
         if constexpr (kBack) return __uint_as_float(acc);
         else return __uint_as_float(acc) * __shfl_sync(kAllLanes, u, j) * scale + bias;
@@ -568,10 +571,10 @@ __global__ void __launch_bounds__(Gemm<BX, kBack>::kThreads, 1)
         for (int j = 0; j < 16; ++j) {
           const int64_t m = m0 + 32 * c + 2 * j;
           if (pairs) {
-            const uint32_t other = __shfl_xor_sync(kAllLanes, from[j], 1);
-            const uint32_t v = lane & 1 ? __byte_perm(other, from[j], 0x7632)
-                                        : __byte_perm(from[j], other, 0x5410);
-            const int64_t row = m + (lane & 1);
+            const uint32_t other = __shfl_xor_sync(kAllLanes, from[j], kNext);
+            const uint32_t v = column & 1 ? __byte_perm(other, from[j], 0x7632)
+                                          : __byte_perm(from[j], other, 0x5410);
+            const int64_t row = m + (column & 1);
             if (row < p.rows && n < p.lanes)
               *reinterpret_cast<uint32_t*>(out + row * p.lanes + (n & ~int64_t(1))) = v;
           } else if (n < p.lanes) {
@@ -595,38 +598,40 @@ __global__ void __launch_bounds__(Gemm<BX, kBack>::kThreads, 1)
         for (int c = 0; c < kChunks; ++c) store(keep + 16 * c, c);
         continue;
       }
-      // (What follows runs once or twice in a CTA: loops, as code that is fetched for the first time
-      // takes longer than its instructions.  Unrolled, a join of three 64 KB parts took 14 us.)
+      // (What follows runs once or twice in a CTA: loops, as code that is fetched for the first
+      // time takes longer than its instructions.  Unrolled, a join of three 64 KB parts took 14
+      // us.)
       // ---- a part of the sum (the CTA's first if the tile began before it, else its last); the
       // last of a tile's parts adds them, in their order
       auto part_at = [&](int64_t cta, int which) {
-        return p.part + ((cta * 2 + which) * (BX / 4) + half * (kHalf / 4)) * kTileW + quad * 32 + lane;
+        return p.part + ((cta * 2 + which) * (BX / 4) + half * (kHalf / 4)) * kTileW + quad * 32 +
+               lane;
       };
       int64_t cta0 = 0;
       int sharers = 0;
       if (!whole) {
-      float4* part = part_at(blockIdx.x, it.begin == 0);
+        float4* part = part_at(blockIdx.x, it.begin == 0);
 #pragma unroll 1
-      for (int c = 0; c < kChunks; ++c) {
-        uint32_t v[32];
-        read(c, v);
+        for (int c = 0; c < kChunks; ++c) {
+          uint32_t v[32];
+          read(c, v);
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-          part[(8 * c + j) * kTileW] =
-              make_float4(__uint_as_float(v[4 * j]), __uint_as_float(v[4 * j + 1]),
-                          __uint_as_float(v[4 * j + 2]), __uint_as_float(v[4 * j + 3]));
-      }
-      release();
-      bar_readers();
-      const int64_t cta1 = cta_of((it.tile + 1) * stages - 1);
-      cta0 = cta_of(it.tile * stages);
-      sharers = int(cta1 - cta0) + 1;
-      if (tid == 32 * kProducers) {
-        s_last = atomic_add_acq_rel(p.count + cta1, 1) == int(cta1 - cta0);
-        if (s_last) p.count[cta1] = 0;  // ready for the next call
-      }
-      bar_readers();
-      if (!s_last) continue;
+          for (int j = 0; j < 8; ++j)
+            part[(8 * c + j) * kTileW] =
+                make_float4(__uint_as_float(v[4 * j]), __uint_as_float(v[4 * j + 1]),
+                            __uint_as_float(v[4 * j + 2]), __uint_as_float(v[4 * j + 3]));
+        }
+        release();
+        bar_readers();
+        const int64_t cta1 = cta_of((it.tile + 1) * stages - 1);
+        cta0 = cta_of(it.tile * stages);
+        sharers = int(cta1 - cta0) + 1;
+        if (tid == 32 * kProducers) {
+          s_last = atomic_add_acq_rel(p.count + cta1, 1) == int(cta1 - cta0);
+          if (s_last) p.count[cta1] = 0;  // ready for the next call
+        }
+        bar_readers();
+        if (!s_last) continue;
       }
       // The CTA's last item: the rings are idle, and the parts are copied into them, 32 columns of
       // all of them at a time (which the first reader warp issues), the next ones ahead.
@@ -639,7 +644,8 @@ __global__ void __launch_bounds__(Gemm<BX, kBack>::kThreads, 1)
         const int q = lane >> 1, h = lane & 1;
         if (q < sharers)
           asm volatile(
-              "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+              "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes "
+              "[%0], [%1], %2, [%3];"
               :: "r"(sbase + (c % depth * sharers + q) * S::kPiece + h * (S::kPiece / 2)),
                  "l"(p.part + ((cta0 + q) * 2 + (q == 0)) * (BX / 4 * kTileW) +
                      (h * (kHalf / 4) + 8 * c) * kTileW),
@@ -717,23 +723,30 @@ __global__ void __launch_bounds__(Gemm<BX, kBack>::kThreads, 1)
 struct RowArgs {
   const int8_t* codes;
   const float* scales;
-  int64_t M, K, width;  // width: of a row in FP16
+  int64_t M, K, width;   // width: of a row in FP16
+  int64_t codes_end;     // where the outliers' second terms start in it
+  int64_t row_ctas;
+  const int8_t* CB;
+  int64_t N;
   const int64_t* cols;
   const void* outliers;
   int L;
   bool bf16;
   uint16_t* X;     // [M][width]
   float* units;    // [M]
-  int32_t* used;   // [kMaxOutliers]
+  int8_t* columns; // [N][width - codes_end] the weight's columns of the outliers' second terms
   int* bad;
 };
 
 // A row's FP16 values are its codes, times the row's unit u = scale / 127.  An outlier x takes
 // the place of its code as x / u, in two FP16 terms, the second in a column of its own past K,
-// where the weight's column is gathered again.  FP16 ends at 65504: where an outlier is above
-// 2^15 u, the unit is 2^-15 of it, and codes are rounded to FP16 with what they are in it.
+// where the weight's column stands again: the CTAs past row_ctas gather those columns (gathered
+// in the product itself, for each tile again, 4096 rows with 13 such columns through 4096 x 11008
+// took 293 us; so 274).  FP16 ends at 65504: where an outlier is above 2^15 u, the unit is 2^-15 of
+// it, and codes are rounded to FP16 with what they are in it.
 __global__ void __launch_bounds__(256) int8_rows_kernel(const RowArgs p) {
   __shared__ int64_t s_most[8];
+  __shared__ int s_col[256];
   __shared__ uint32_t s_top[8];
   wait_for_stream();
   asm volatile("griddepcontrol.launch_dependents;");
@@ -755,11 +768,30 @@ __global__ void __launch_bounds__(256) int8_rows_kernel(const RowArgs p) {
     for (int w = 0; w < t >> 5; ++w) top = max(top, s_most[w]);
     if (c > top && c < p.K && c >= 0) col = c;
     const int wrong = col < 0 && c != -1;
-    if (t < kMaxOutliers && blockIdx.x == 0) p.used[t] = int32_t(col);
+    s_col[t] = int(col);
     if (blockIdx.x == 0 && wrong && p.bad) atomicAdd(p.bad, 1);
   }
-  const int64_t codes_end = (p.K + kStep - 1) / kStep * kStep;
-  for (int64_t row = blockIdx.x; row < p.M; row += gridDim.x) {
+  const int64_t codes_end = p.codes_end;
+  if (blockIdx.x >= p.row_ctas) {
+    __syncthreads();
+    const int64_t extra = p.width - codes_end, pieces = p.N * extra / 16;
+    const int64_t step = (gridDim.x - p.row_ctas) * 256;
+    for (int64_t i = (blockIdx.x - p.row_ctas) * 256 + t; i < pieces; i += step) {
+      const int64_t n = i * 16 / extra;
+      const int* cols = s_col + (i * 16 - n * extra);
+      uint32_t code[16];
+#pragma unroll
+      for (int j = 0; j < 16; ++j)
+        code[j] = cols[j] >= 0 ? uint8_t(load_global(p.CB + n * p.K + cols[j])) : 0;
+      uint32_t o[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        o[j] = code[4 * j] | code[4 * j + 1] << 8 | code[4 * j + 2] << 16 | code[4 * j + 3] << 24;
+      *reinterpret_cast<uint4*>(p.columns + i * 16) = make_uint4(o[0], o[1], o[2], o[3]);
+    }
+    return;
+  }
+  for (int64_t row = blockIdx.x; row < p.M; row += p.row_ctas) {
     float unit = load_global(p.scales + row) * kRecip127, ratio = 1.f, x = 0.f;
     if (p.L > 0) {
       if (col >= 0) x = load_16(p.outliers, row * p.L + t, p.bf16);
@@ -814,8 +846,6 @@ __global__ void __launch_bounds__(256) int8_rows_kernel(const RowArgs p) {
 // ------------------------------------------------------------------------ host side
 int64_t up256(int64_t n) { return (n + 255) / 256 * 256; }
 
-constexpr double kBackStage = 300;  // columns of codes to values
-
 struct Plan {
   int bx, stages;
   int64_t tiles_x, tiles;
@@ -825,19 +855,18 @@ struct Plan {
 
 // The tile's width, and whether CTAs take whole tiles or equal runs of stages, by the estimated
 // time in cycles.  A stage takes about 1000 at BX 64 and 128 and 1500 at 256 (the MMAs: 122 each,
-// at 256 181), for the gradient kBackStage more; the end of a tile 1500 where its accumulator is the
-// only one.  Parts of tiles cost their writing (40 bytes a cycle), the count (3000), and the reading
-// of all parts of a tile by one CTA, at 56 bytes a cycle: for wide tiles that few stages share,
-// more than the SMs that whole tiles leave idle.  512 rows through 4096 x 4096, in us: 256 wide in
-// parts 37, whole 25.
-Plan plan_gemm(int64_t lanes, int64_t rows, int steps, bool back, int sms) {
+// at 256 181); the end of a tile 1500 where its accumulator is the only one.  Parts of tiles cost
+// their writing (40 bytes a cycle), the count (3000), and the reading of all parts of a tile by one
+// CTA, at 56 bytes a cycle: for wide tiles that few stages share, more than the SMs that whole
+// tiles leave idle.  512 rows through 4096 x 4096, in us: 256 wide in parts 37, whole 25.
+Plan plan_gemm(int64_t lanes, int64_t rows, int steps, int sms) {
   Plan best = {};
   double best_cost = 1e300;
   const int stages = (steps + 1) / 2;
   for (int bx = 64; bx <= 256; bx *= 2) {
     const int64_t tiles_x = (rows + bx - 1) / bx;
     const int64_t tiles = tiles_x * ((lanes + kTileW - 1) / kTileW);
-    const double stage = (bx < 256 ? 1000 : 1500) + (back ? kBackStage : 0);
+    const double stage = bx < 256 ? 1000 : 1500;
     const double end = bx == 64 ? 200 : 1500, last = bx / 64 * 700 + 5000;
     const double rounds = double((tiles + sms - 1) / sms);
     double cost = rounds * (stages * stage + end) + last;
@@ -859,29 +888,32 @@ Plan plan_gemm(int64_t lanes, int64_t rows, int steps, bool back, int sms) {
 }
 
 template <int BX, bool kBack, bool kBF16>
-int launch_one(const CUtensorMap& w, const CUtensorMap& x, const GemmArgs& p, int dev, int ctas,
-               cudaStream_t stream) {
+int launch_one(const CUtensorMap& w, const CUtensorMap& x, const CUtensorMap& cols,
+               const GemmArgs& p, int dev, int ctas, cudaStream_t stream) {
   auto kernel = dq4_int8_gemm_kernel<BX, kBack, kBF16>;
   static std::atomic<uint64_t> allowed{0};
   if (const int st = allow_smem(kernel, Gemm<BX, kBack>::kBytes, dev, &allowed)) return st;
-  return launch_ordered(kernel, dim3(unsigned(ctas)), Gemm<BX, kBack>::kThreads, Gemm<BX, kBack>::kBytes, stream, w, x, p);
+  return launch_ordered(kernel, dim3(unsigned(ctas)), Gemm<BX, kBack>::kThreads,
+                        Gemm<BX, kBack>::kBytes, stream, w, x, cols, p);
 }
 
 template <bool kBack, bool kBF16>
-int launch_plan(const Plan& pl, const CUtensorMap& w, const CUtensorMap& x, GemmArgs p, int dev,
-                void* part, cudaStream_t stream) {
+int launch_plan(const Plan& pl, const CUtensorMap& w, const CUtensorMap& x,
+                const CUtensorMap& cols, GemmArgs p, int dev, void* part, cudaStream_t stream) {
   p.tiles_x = int(pl.tiles_x);
   p.tiles = pl.tiles;
   p.units = pl.split ? pl.tiles * pl.stages : 0;
   p.part = static_cast<float4*>(part);
-  if (pl.bx == 64) return launch_one<64, kBack, kBF16>(w, x, p, dev, pl.ctas, stream);
-  if (pl.bx == 128) return launch_one<128, kBack, kBF16>(w, x, p, dev, pl.ctas, stream);
-  return launch_one<256, kBack, kBF16>(w, x, p, dev, pl.ctas, stream);
+  if (pl.bx == 64) return launch_one<64, kBack, kBF16>(w, x, cols, p, dev, pl.ctas, stream);
+  if (pl.bx == 128) return launch_one<128, kBack, kBF16>(w, x, cols, p, dev, pl.ctas, stream);
+  return launch_one<256, kBack, kBF16>(w, x, cols, p, dev, pl.ctas, stream);
 }
 
 // The steps of a row in FP16: of its codes, and of its outliers' second terms.
-int code_steps(int64_t K) { return int((K + kStep - 1) / kStep); }
-int all_steps(int64_t K, int L) { return code_steps(K) + (L + kStep - 1) / kStep; }
+// (with outliers the codes end with a stage: its codes come from one matrix)
+int k_steps(int64_t K) { return int((K + kStep - 1) / kStep); }
+int code_steps(int64_t K, int L) { return L > 0 ? (k_steps(K) + 1) / 2 * 2 : k_steps(K); }
+int all_steps(int64_t K, int L) { return code_steps(K, L) + k_steps(L); }
 
 int64_t part_bytes(const Plan& pl) {
   return pl.split ? int64_t(pl.ctas) * 2 * pl.bx * kTileW * 4 : 0;
@@ -890,83 +922,103 @@ int64_t part_bytes(const Plan& pl) {
 }  // namespace
 
 int64_t int8_gemm_workspace(int64_t M, int64_t N, int64_t K, int L, int sms) {
-  const Plan pl = plan_gemm(N, M, all_steps(K, L), false, sms);
-  return kInt8Counters + up256(kMaxOutliers * 4) + up256(M * 4) +
+  const Plan pl = plan_gemm(N, M, all_steps(K, L), sms);
+  return kInt8Counters + up256(N * k_steps(L) * kStep) + up256(M * 4) +
          up256(M * all_steps(K, L) * kStep * 2) + part_bytes(pl);
 }
 
 int launch_int8_gemm(const Int8Linear& a, int dev, int sms, void* workspace, cudaStream_t stream) {
   const int steps = all_steps(a.K, a.L);
-  const Plan pl = plan_gemm(a.N, a.M, steps, false, sms);
+  const Plan pl = plan_gemm(a.N, a.M, steps, sms);
   char* at = static_cast<char*>(workspace);
   int* count = reinterpret_cast<int*>(at);
   at += kInt8Counters;
-  int32_t* used = reinterpret_cast<int32_t*>(at);
-  at += up256(kMaxOutliers * 4);
+  int8_t* columns = reinterpret_cast<int8_t*>(at);
+  const int64_t extra = k_steps(a.L) * kStep;
+  at += up256(a.N * extra);
   float* units = reinterpret_cast<float*>(at);
   at += up256(a.M * 4);
   uint16_t* X = reinterpret_cast<uint16_t*>(at);
   const int64_t width = int64_t(steps) * kStep;
   at += up256(a.M * width * 2);
-  CUtensorMap w, x;
+  CUtensorMap w, x, cols;
   if (const int st = encode_2d(&w, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.CB, a.K, a.N, a.K, kStage,
                                kTileW, CU_TENSOR_MAP_SWIZZLE_128B))
     return st;
+  cols = w;  // (not read without outliers)
+  if (a.L > 0)
+    if (const int st = encode_2d(&cols, CU_TENSOR_MAP_DATA_TYPE_UINT8, columns, extra, a.N, extra,
+                                 kStage, kTileW, CU_TENSOR_MAP_SWIZZLE_128B))
+      return st;
   if (const int st = encode_2d(&x, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, X, width, a.M, width * 2, kStep,
                                pl.bx, CU_TENSOR_MAP_SWIZZLE_128B))
     return st;
-  const RowArgs r = {a.codes, a.scales, a.M, a.K, width, a.cols, a.outliers, a.L, a.outliers_bf16,
-                     X, units, used, a.bad};
-  const int64_t row_ctas = a.M < 8 * sms ? a.M : 8 * sms;
-  if (const int st = launch_ordered(int8_rows_kernel, dim3(unsigned(row_ctas)), 256, 0, stream, r))
+  RowArgs r = {};
+  r.codes = a.codes;
+  r.scales = a.scales;
+  r.M = a.M;
+  r.K = a.K;
+  r.width = width;
+  r.codes_end = int64_t(code_steps(a.K, a.L)) * kStep;
+  r.row_ctas = a.M < 8 * sms ? a.M : 8 * sms;
+  r.CB = a.CB;
+  r.N = a.N;
+  r.cols = a.cols;
+  r.outliers = a.outliers;
+  r.L = a.L;
+  r.bf16 = a.outliers_bf16;
+  r.X = X;
+  r.units = units;
+  r.columns = columns;
+  r.bad = a.bad;
+  const int64_t gathers = (a.N * extra / 16 + 255) / 256;
+  const int64_t row_kernel_ctas = r.row_ctas + (gathers < 4 * sms ? gathers : 4 * sms);
+  if (const int st = launch_ordered(int8_rows_kernel, dim3(unsigned(row_kernel_ctas)), 256, 0,
+                                    stream, r))
     return st;
   GemmArgs p = {};
   p.lanes = p.N = a.N;
   p.rows = a.M;
   p.steps = steps;
-  p.code_steps = code_steps(a.K);
-  p.CB = a.CB;
+  p.code_steps = code_steps(a.K, a.L);
   p.SCB = a.SCB;
-  p.K = a.K;
-  p.cols = a.L > 0 ? used : nullptr;
   p.row_units = units;
   p.bias = a.bias;
   p.out_dtype = a.out_dtype;
   p.out = a.Y;
   p.count = count;
   p.bad = a.bad;
-  return launch_plan<false, false>(pl, w, x, p, dev, at, stream);
+  return launch_plan<false, false>(pl, w, x, cols, p, dev, at, stream);
 }
 
 int64_t int8_backward_workspace(int64_t M, int64_t N, int64_t K, int sms) {
-  return kInt8Counters + part_bytes(plan_gemm(K, M, code_steps(N), true, sms));
+  return kInt8Counters + part_bytes(plan_gemm(K, M, k_steps(N), sms));
 }
 
 int launch_int8_backward(const Int8Backward& a, int dev, int sms, void* workspace,
                          cudaStream_t stream) {
-  const Plan pl = plan_gemm(a.K, a.M, code_steps(a.N), true, sms);
+  const Plan pl = plan_gemm(a.K, a.M, k_steps(a.N), sms);
   CUtensorMap w, x;
   if (const int st = encode_2d(&w, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.CB, a.K, a.N, a.K, kTileW,
-                               kStage, CU_TENSOR_MAP_SWIZZLE_NONE))
+                               kStage, CU_TENSOR_MAP_SWIZZLE_128B))
     return st;
   if (const int st = encode_2d(&x, a.bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
                                           : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
                                a.dY, a.N, a.M, a.N * 2, kStep, pl.bx, CU_TENSOR_MAP_SWIZZLE_128B))
     return st;
   GemmArgs p = {};
-  p.lanes = p.K = a.K;
+  p.lanes = a.K;
   p.N = a.N;
   p.rows = a.M;
-  p.steps = p.code_steps = code_steps(a.N);
-  p.CB = a.CB;
+  p.steps = p.code_steps = k_steps(a.N);
   p.SCB = a.SCB;
   p.out_dtype = a.bf16 ? DQ4_OUT_BF16 : DQ4_OUT_F16;
   p.out = a.dX;
   p.count = static_cast<int*>(workspace);
   p.bad = a.bad;
   char* part = static_cast<char*>(workspace) + kInt8Counters;
-  return a.bf16 ? launch_plan<true, true>(pl, w, x, p, dev, part, stream)
-                : launch_plan<true, false>(pl, w, x, p, dev, part, stream);
+  return a.bf16 ? launch_plan<true, true>(pl, w, x, w, p, dev, part, stream)
+                : launch_plan<true, false>(pl, w, x, w, p, dev, part, stream);
 }
 
 }  // namespace dq4d

@@ -53,7 +53,7 @@ constexpr int kAhead = 4;     // outlier columns whose codes are loaded ahead
 
 // A job is 16 weight rows and 8 NT tokens (all there are), shared by `group` warps of a CTA, which
 // take turns at chunks of 128 of K; one job a group, so that there is little code to fetch (with
-// jobs in turn, as in int8.cuh, a call took 4 to 5 us more).  The order of K in a product is
+// jobs in turn, as in int8_moe.cu, a call took 4 to 5 us more).  The order of K in a product is
 // free: lane (g, c) takes 32 consecutive codes of rows g and g + 8, and of token g of each 8.
 template <int NT, int kFewDepth>
 __global__ void __launch_bounds__(kStreamThreads, kFewDepth == 2 && NT < 4 ? 3 : 2)
@@ -105,7 +105,8 @@ __global__ void __launch_bounds__(kStreamThreads, kFewDepth == 2 && NT < 4 ? 3 :
   if (p.L > 0 && warp == 0) list_columns(p, &s_cols);  // (while the first codes are on their way)
   const int8_t* tok[NT];
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt) tok[nt] = p.codes + min(int64_t(8 * nt + g), p.M - 1) * p.K + 32 * c;
+  for (int nt = 0; nt < NT; ++nt)
+    tok[nt] = p.codes + min(int64_t(8 * nt + g), p.M - 1) * p.K + 32 * c;
   float acc[NT][4] = {};
   bool ok = true;
   int slot = 0, i = 0;
@@ -205,7 +206,8 @@ __global__ void __launch_bounds__(kStreamThreads, kFewDepth == 2 && NT < 4 ? 3 :
   for (int m = t / kFewRows; m < p.M; m += threads / kFewRows) {
     float sum = 0.f;
     if (m < kTokens)  // (more rows only without codes, K = 0)
-      for (int w = 0; w < group; ++w) sum += s_part[in_cta * group + w][m * kFewRows + t % kFewRows];
+      for (int w = 0; w < group; ++w)
+        sum += s_part[in_cta * group + w][m * kFewRows + t % kFewRows];
     float y = sum * (load_global(p.scales + m) * kRecip127) * s_n;
     if (used > 0) {
       float more = 0.f;
@@ -238,7 +240,8 @@ int launch_few_depth(const CUtensorMap& w, const Int8Linear& p, int64_t grid, in
   if (const int st = allow_smem(kernel, kRings + 8 * NT * kMaxOutliers * 4, dev, &allowed,
                                 kFewDepth == 2 ? 50 : 70))
     return st;
-  return launch_ordered(kernel, dim3(unsigned(grid)), kStreamThreads, kRings + int(p.M < 8 * NT ? p.M : 8 * NT) * p.L * 4,
+  const int tokens = int(p.M < 8 * NT ? p.M : 8 * NT);  // (more only with K = 0: none is used then)
+  return launch_ordered(kernel, dim3(unsigned(grid)), kStreamThreads, kRings + tokens * p.L * 4,
                         stream, w, p, group);
 }
 
@@ -309,7 +312,8 @@ int dq4_int8_linear(const int8_t* codes, const float* scales, const int8_t* CB, 
     if (misaligned(workspace, 256)) return DQ4_ERR_ALIGN;
     return launch_int8_gemm(p, dev, sms, workspace, s);
   }
-  return M <= 8 ? launch_few<1>(p, dev, sms, s) : M <= 16 ? launch_few<2>(p, dev, sms, s) : launch_few<4>(p, dev, sms, s);
+  if (M <= 8) return launch_few<1>(p, dev, sms, s);
+  return M <= 16 ? launch_few<2>(p, dev, sms, s) : launch_few<4>(p, dev, sms, s);
 }
 
 }  // extern "C"

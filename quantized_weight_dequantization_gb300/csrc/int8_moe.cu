@@ -2,7 +2,7 @@
 //
 // Bound by the bytes of the chosen experts' weights, each read once.  Four launches:
 //   route   one CTA chooses the experts and lists each one's (token, choice) pairs, by entries of
-//           up to 8 NT; one CTA a token brings its row to FP16, scaled by a power of two
+//           up to 8; one CTA a token brings its row to FP16, scaled by a power of two
 //   up      a job is 16 inner places of an entry's expert, gate and up rows together: inner =
 //           silu(g) * u in FP16, scaled by a power of two for each 16 places of a pair, and the
 //           largest of each pair's row
@@ -18,7 +18,8 @@ namespace {
 constexpr int kRouteThreads = 512;
 constexpr int kMaxTokens = 256, kMaxExperts = 1024, kMaxTopK = 16;
 constexpr int kMaxPairs = kMaxTokens * kMaxTopK;
-constexpr int kMaxEntries = kMaxExperts + kMaxPairs / 8;
+constexpr int kEntry = 8;  // pairs of an entry at most
+constexpr int kMaxEntries = kMaxExperts + kMaxPairs / kEntry;
 constexpr int kUpPlaces = 16, kDownPlaces = 32;
 constexpr int64_t kMaxInner = 1 << 20;
 constexpr int64_t kMaxHidden = 1 << 15;
@@ -26,7 +27,7 @@ constexpr int64_t kMaxHidden = 1 << 15;
 // What `route` finds out, at the head of the workspace.  Pairs (token, choice) stand in the order
 // of their experts: `place` is a pair's there, and rows of xs, inner and out are by place.
 struct Routed {
-  int entries;                      // experts with pairs, one for each 8 NT of them
+  int entries;                      // experts with pairs, one for each 8 of them
   uint16_t expert[kMaxEntries];     // of each
   uint16_t first[kMaxEntries + 1];  // and its first place
   uint16_t place[kMaxPairs];        // of token * top_k + choice
@@ -38,7 +39,7 @@ struct MoeArgs {
   const void* X;
   int64_t row_stride;
   bool bf16;
-  int T, E, top_k, renormalize, most;  // most: tokens of an entry
+  int T, E, top_k, renormalize;
   int64_t H, I;
   const float* logits;
   const int8_t *W1, *W2;
@@ -76,8 +77,8 @@ __device__ __forceinline__ float logit_of(uint32_t key) {
   return __uint_as_float(key & 0x80000000u ? key & 0x7FFFFFFFu : ~key);
 }
 
-// Every CTA finds out the whole routing for itself (the warps' tokens side by side, so that it takes
-// no longer than one token's); CTA t then writes token t's row, and CTA 0 the lists.
+// Every CTA finds out the whole routing for itself (the warps' tokens side by side, so that it
+// takes no longer than one token's); CTA t then writes token t's row, and CTA 0 the lists.
 __global__ void __launch_bounds__(kRouteThreads) dq4_moe_route_kernel(const MoeArgs p) {
   __shared__ uint16_t s_ids[kMaxPairs];
   __shared__ int s_count[kMaxExperts];
@@ -169,7 +170,7 @@ __global__ void __launch_bounds__(kRouteThreads) dq4_moe_route_kernel(const MoeA
 #pragma unroll
   for (int k = 0; k < kEach; ++k) {
     counts[k] = s_count[t * kEach + k];
-    both += uint32_t(counts[k]) | uint32_t((counts[k] + p.most - 1) / p.most) << 16;
+    both += uint32_t(counts[k]) | uint32_t((counts[k] + kEntry - 1) / kEntry) << 16;
   }
   uint32_t run = both;
 #pragma unroll
@@ -190,7 +191,7 @@ __global__ void __launch_bounds__(kRouteThreads) dq4_moe_route_kernel(const MoeA
     const int e = t * kEach + k;
     s_count[e] = first;  // (from here on: the expert's first place)
     if (lists)
-      for (int done = 0; done < counts[k]; done += p.most, ++entry) {
+      for (int done = 0; done < counts[k]; done += kEntry, ++entry) {
         p.r->expert[entry] = uint16_t(e);
         p.r->first[entry] = uint16_t(first + done);
       }
@@ -243,6 +244,239 @@ __global__ void __launch_bounds__(kRouteThreads) dq4_moe_route_kernel(const MoeA
   }
 }
 
+// ------------------------------------------------ products of weight rows and an entry's tokens
+// Warps take jobs (32 weight rows, up to 8 tokens) in turn: alone, or 2, 4 or 8 of a CTA together
+// (a group), which then take turns at the chunks of 128 of K and add their sums at the end.  The
+// order of K inside a product is free: lane (g, c) = (lane / 4, lane % 4) takes 32 consecutive
+// codes of rows g and g + 8 of each 16, and the same places of token g, and eight products take
+// them four at a time.  The weights come by TMA into a ring of the warp's own in shared memory, two
+// chunks ahead, across the ends of jobs (lane 0 issues, all lanes consume); the tokens, which every
+// job of an entry reads, from L2 into registers, a chunk ahead.  Nothing else synchronizes warps
+// before a job's end.  A job starts at a chunk of its own, so that warps do not go through the
+// tokens side by side and queue at single lines of L2. Copies of 128-byte rows: the TMA takes about
+// 3.5 cycles for a row whatever its width, and at 64 bytes a row that bounds the weight's bytes
+// (one token through 11008 x 4096, whose weight alone takes 10.4 us to read: 23.7 us).  Copies of
+// 16 bytes a lane, cp.async, took 13.4 us there.  Rings of four chunks leave the tokens less of L1:
+// 16 tokens, 6 of 64 experts, took 97 us, so 92.
+//
+// kBoxes: boxes of weight rows of a chunk.  kScaled: tokens have factors, one for each 16 values.
+// Jobs:
+//   places(job, y)          the first row of each box of weights
+//   tokens(job)             this lane's token (for one that is not there any other, whose results
+//                           are not used), advanced to its 32 c
+//   scales(job, k, f)       with kScaled: the factors of values k .. k + 15 and the 16 after them
+//   begin(job, t)           before a job's products, thread t of its group
+//   finish(job, part, ...)  the group's sums (sum(part, warps, token, row)), thread t of `threads`
+constexpr int kJobRows = 32;
+// (Entries of 16 pairs, two products for each weight's conversion, took more: 64 tokens through 2
+// of 8 experts of 4096 x 14336, 16 pairs each, 443 us, in eights, which read the weights twice from
+// L2, 409; 23 tokens 302 and 237.)
+constexpr int kDepth = 2;  // chunks of a ring
+constexpr int kCtas = 2;   // of an SM
+
+// The warps of a group: of 1, 2, 4 and 8, what takes the fewest chunks in the longest warp, where
+// the end of a job costs about as much as 2.
+__device__ __forceinline__ int group_warps(uint32_t jobs, uint32_t chunks, uint32_t warps) {
+  int best = 1;
+  uint32_t least = 0xFFFFFFFFu;
+#pragma unroll
+  for (int n = 1; n <= kStreamWarps; n *= 2) {
+    const uint32_t rounds = (jobs + warps / n - 1) / (warps / n);
+    const uint32_t cost = rounds * ((chunks + n - 1) / n + 2);
+    if (cost < least) {
+      least = cost;
+      best = n;
+    }
+  }
+  return best;
+}
+
+template <int kBoxes, bool kScaled>
+struct Streamed {
+  static constexpr int kStage = kJobRows * kChunk;
+  static constexpr int kPart = kJobRows * kEntry;  // sums of a warp
+  static constexpr int kBarsAt = kStreamWarps * kDepth * kStage;
+  static constexpr int kPartsAt = kBarsAt + kStreamWarps * kDepth * 8;
+  static constexpr int kBytes = kPartsAt + kStreamWarps * kPart * 4;  // + 1024 to align
+
+  template <typename Jobs>
+  static __device__ __forceinline__ void run(Jobs& jobs, uint8_t* smem, int64_t all, int64_t K,
+                                             const CUtensorMap& map_w, int* bad) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
+    const int chunks = int((K + kChunk - 1) / kChunk);
+    const int group = group_warps(uint32_t(all), uint32_t(chunks), gridDim.x * kStreamWarps);
+    const int in_cta = warp / group, member = warp - in_cta * group;
+    const int64_t first = int64_t(blockIdx.x) * (kStreamWarps / group) + in_cta;
+    const int64_t stride = int64_t(gridDim.x) * (kStreamWarps / group);
+    float* part = reinterpret_cast<float*>(smem + kPartsAt) + in_cta * group * kPart;
+    const uint32_t ring = smem_u32(smem) + warp * kDepth * kStage;
+    const uint32_t bars = smem_u32(smem) + kBarsAt + warp * kDepth * 8;
+    const int mine = chunks > member ? (chunks - member + group - 1) / group : 0;
+    const uint64_t tw = reinterpret_cast<uint64_t>(&map_w);
+    // ---- the weights' copies: of the next chunk of the next job
+    int y[kBoxes];
+    int64_t ahead = mine > 0 ? first : all;
+    int ahead_chunk = 0, left = mine, slot_in = 0, in_flight = 0;
+    auto start_of = [&](int64_t job) { return int(uint32_t(job) % uint32_t(mine)); };
+    auto open = [&] {
+      if (ahead >= all) return;
+      jobs.places(ahead, y);
+      ahead_chunk = start_of(ahead);
+    };
+    open();
+    auto issue = [&] {
+      if (ahead >= all) return;
+      if (lane == 0) {
+        const int k = (member + ahead_chunk * group) * kChunk;
+        const uint32_t dst = ring + slot_in * kStage, bar = bars + 8 * slot_in;
+        mbar_expect(bar, kStage);
+#pragma unroll
+        for (int i = 0; i < kBoxes; ++i)
+          tma_load_2d(dst + i * (kStage / kBoxes), tw, k, y[i], bar);
+      }
+      ++in_flight;
+      if (++slot_in == kDepth) slot_in = 0;
+      if (++ahead_chunk == mine) ahead_chunk = 0;
+      if (--left == 0) {
+        left = mine;
+        ahead += stride;
+        open();
+      }
+    };
+#pragma unroll 1
+    for (int i = 0; i < kDepth; ++i) issue();
+    // ---- the tokens: those of the next chunk
+    const uint16_t* tok;
+    uint4 x[4];
+    float f[2];
+    int64_t tok_job = mine > 0 ? first : all;
+    int tok_chunk = 0, tok_left = mine;
+    auto tok_open = [&] {
+      if (tok_job >= all) return;
+      tok = jobs.tokens(tok_job);
+      tok_chunk = start_of(tok_job);
+    };
+    tok_open();
+    auto fetch = [&] {
+      if (tok_job >= all) return;
+      const int64_t k = int64_t(member + tok_chunk * group) * kChunk;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        x[i] = make_uint4(0, 0, 0, 0);  // (past the end)
+        if (k + 32 * c + 8 * i < K) x[i] = load_ahead(reinterpret_cast<const uint4*>(tok + k) + i);
+      }
+      if constexpr (kScaled) jobs.scales(tok_job, k + 32 * c, f);
+      if (++tok_chunk == mine) tok_chunk = 0;
+      if (--tok_left == 0) {
+        tok_left = mine;
+        tok_job += stride;
+        tok_open();
+      }
+    };
+    fetch();
+    auto join = [&] {  // the group's threads
+      if (group == 1)
+        __syncwarp();
+      else
+        asm volatile("bar.sync %0, %1;" :: "r"(1 + in_cta), "r"(32 * group) : "memory");
+    };
+    int slot = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    for (int64_t job = first; job < all; job += stride) {
+      jobs.begin(job, 32 * member + lane);
+      float acc[2][4] = {};
+#pragma unroll 1
+      for (int i = 0; i < mine && ok; ++i) {
+        // the tokens' operand words, which frees the registers for the next chunk's
+        uint32_t b[16];
+#pragma unroll
+        for (int s = 0; s < 16; ++s) {
+          b[s] = reinterpret_cast<const uint32_t*>(x)[s];
+          if constexpr (kScaled) {
+            __half2 v;
+            memcpy(&v, &b[s], 4);
+            v = __hmul2(v, __float2half2_rn(f[s >> 3]));
+            memcpy(&b[s], &v, 4);
+          }
+        }
+        fetch();
+        ok = __all_sync(kAllLanes, mbar_wait(bars + 8 * slot, phase));
+        if (!ok) break;
+        const uint32_t at = ring + slot * kStage;
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          // 128-byte rows, their 16-byte pieces in place i ^ row % 8
+          uint4 w[2][2];
+#pragma unroll
+          for (int rt = 0; rt < 2; ++rt)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+              w[rt][h] = lds_v4(at + (16 * rt + 8 * h + g) * kChunk + (((2 * c + half) ^ g) << 4));
+#pragma unroll
+          for (int s = 0; s < 4; ++s)
+#pragma unroll
+            for (int rt = 0; rt < 2; ++rt) {
+              uint32_t a[4];
+              codes_f16(reinterpret_cast<const uint32_t*>(&w[rt][0])[s], a[0], a[2]);
+              codes_f16(reinterpret_cast<const uint32_t*>(&w[rt][1])[s], a[1], a[3]);
+              mma_16816(acc[rt], a[0], a[1], a[2], a[3], b[8 * half + 2 * s],
+                        b[8 * half + 2 * s + 1]);
+            }
+        }
+        __syncwarp();  // every lane has read the chunk
+        --in_flight;
+        issue();
+        if (++slot == kDepth) {
+          slot = 0;
+          phase ^= 1u;
+        }
+      }
+      float* to = part + member * kPart;
+#pragma unroll
+      for (int rt = 0; rt < 2; ++rt)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          to[place(2 * c + (i & 1), 16 * rt + 8 * (i >> 1) + g)] = acc[rt][i];
+      join();
+      jobs.finish(job, part, group, 32 * member + lane, 32 * group);
+      join();  // the sums have been read
+    }
+    if (!ok) {  // copies in flight land before the CTA leaves
+      if (lane == 0 && bad) atomicAdd(bad, 1);
+      for (; in_flight > 0; --in_flight) {
+        mbar_wait(bars + 8 * slot, phase);
+        if (++slot == kDepth) {
+          slot = 0;
+          phase ^= 1u;
+        }
+      }
+    }
+  }
+
+  // The barriers of this warp's ring: before anything else.
+  static __device__ __forceinline__ void setup(uint8_t* smem, const CUtensorMap& map_w) {
+    if ((threadIdx.x & 31) == 0) {
+      asm volatile("prefetch.tensormap [%0];" :: "l"(reinterpret_cast<uint64_t>(&map_w)));
+      const uint32_t bars = smem_u32(smem) + kBarsAt + (threadIdx.x >> 5) * kDepth * 8;
+      for (int i = 0; i < kDepth; ++i) mbar_init(bars + 8 * i, 1);
+      asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    __syncwarp();
+  }
+
+  // Where a token's and row's sum lies: the rows of a token in turn, those of every second token
+  // 8 further on, so that the lanes that store or read together use different banks.
+  static __device__ __forceinline__ int place(int token, int row) {
+    return token * kJobRows + (row ^ (token >> 1 & 3) * 8);
+  }
+  static __device__ __forceinline__ float sum(const float* part, int warps, int token, int row) {
+    float v = 0.f;
+    for (int w = 0; w < warps; ++w) v += part[w * kPart + place(token, row)];
+    return v;
+  }
+};
+
 // What the other two kernels hold of it in shared memory, behind their rings.
 struct Entries {
   float *up, *down;  // of a place's token: xs's `down`, or the scaling of its inner row
@@ -250,9 +484,7 @@ struct Entries {
   int count;
 };
 int64_t entry_bytes(int64_t entries, int64_t pairs) { return pairs * 8 + entries * 4 + 2; }
-int64_t most_entries(int64_t E, int64_t pairs, int64_t most) {
-  return (E < pairs ? E : pairs) + pairs / most;
-}
+int64_t most_entries(int64_t E, int64_t pairs) { return (E < pairs ? E : pairs) + pairs / kEntry; }
 
 template <bool kInner>
 __device__ __forceinline__ Entries load_entries(const MoeArgs& p, uint8_t* smem) {
@@ -278,9 +510,8 @@ __device__ __forceinline__ Entries load_entries(const MoeArgs& p, uint8_t* smem)
 }
 
 // ---------------------------------------------------------------------------- up
-template <int NT, int kDepth>
 struct UpJobs {
-  using S = Streamed<2, NT, 2, 4, false, kDepth>;
+  using S = Streamed<2, false>;
   const MoeArgs& p;
   Entries s;
   float s_gate, s_up;  // scales of this thread's place
@@ -297,16 +528,12 @@ struct UpJobs {
     y[0] = int(s.expert[entry] * 2 * p.I) + tile * kUpPlaces;
     y[1] = y[0] + int(p.I);
   }
-  __device__ __forceinline__ void tokens(int64_t job, const uint8_t* (&tok)[NT]) const {
+  __device__ __forceinline__ const uint16_t* tokens(int64_t job) const {
     const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
     int tile;
     const int entry = entry_of(job, tile);
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-      tok[nt] = reinterpret_cast<const uint8_t*>(
-          p.xs + min(s.first[entry] + 8 * nt + g, s.first[entry + 1] - 1) * p.H + 32 * c);
+    return p.xs + min(s.first[entry] + g, s.first[entry + 1] - 1) * p.H + 32 * c;
   }
-  __device__ __forceinline__ void start() const {}
   __device__ __forceinline__ void begin(int64_t job, int t) {
     int tile;
     const int entry = entry_of(job, tile);
@@ -346,11 +573,10 @@ struct UpJobs {
   }
 };
 
-template <int NT, int kDepth, int kCtas>
 __global__ void __launch_bounds__(kStreamThreads, kCtas)
     dq4_moe_up_kernel(const __grid_constant__ CUtensorMap map_w, const MoeArgs p) {
   extern __shared__ uint8_t smem_raw[];
-  using Jobs = UpJobs<NT, kDepth>;
+  using Jobs = UpJobs;
   uint8_t* smem = aligned_1024(smem_raw);
   Jobs::S::setup(smem, map_w);
   wait_for_stream();
@@ -360,9 +586,8 @@ __global__ void __launch_bounds__(kStreamThreads, kCtas)
 }
 
 // -------------------------------------------------------------------------- down
-template <int NT, int kDepth>
 struct DownJobs {
-  using S = Streamed<2, NT, 1, 4, true, kDepth>;
+  using S = Streamed<1, true>;
   const MoeArgs& p;
   Entries s;
   float s_place;  // scale of this thread's place
@@ -379,33 +604,23 @@ struct DownJobs {
     const int entry = entry_of(job, tile);
     y[0] = int(s.expert[entry] * p.H) + tile * kDownPlaces;
   }
-  __device__ __forceinline__ int pair_of(int entry, int nt) const {
-    return min(s.first[entry] + 8 * nt + (int(threadIdx.x & 31) >> 2), s.first[entry + 1] - 1);
-  }
-  __device__ __forceinline__ void tokens(int64_t job, const uint8_t* (&tok)[NT]) const {
+  __device__ __forceinline__ int pair_of(int64_t job) const {
     int tile;
     const int entry = entry_of(job, tile);
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-      tok[nt] = reinterpret_cast<const uint8_t*>(p.inner + pair_of(entry, nt) * p.I +
-                                                 32 * (threadIdx.x & 3));
+    return min(s.first[entry] + (int(threadIdx.x & 31) >> 2), s.first[entry + 1] - 1);
+  }
+  __device__ __forceinline__ const uint16_t* tokens(int64_t job) const {
+    return p.inner + pair_of(job) * p.I + 32 * (threadIdx.x & 3);
   }
   // A tile's FP16 values in the row's unit: powers of two, both.
-  __device__ __forceinline__ void scales(int64_t job, int64_t k, float (&f)[2 * NT]) const {
-    int tile;
-    const int entry = entry_of(job, tile);
+  __device__ __forceinline__ void scales(int64_t job, int64_t k, float (&f)[2]) const {
+    const int at = pair_of(job);
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      const int at = pair_of(entry, nt);
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-        f[2 * nt + h] = k + 16 * h < p.I
-                            ? load_ahead(p.inner_by + at * (p.I / kUpPlaces) + k / kUpPlaces + h) *
-                                  s.up[at]
-                            : 0.f;
-    }
+    for (int h = 0; h < 2; ++h)
+      f[h] = k + 16 * h < p.I
+                 ? load_ahead(p.inner_by + at * (p.I / kUpPlaces) + k / kUpPlaces + h) * s.up[at]
+                 : 0.f;
   }
-  __device__ __forceinline__ void start() const {}
   __device__ __forceinline__ void begin(int64_t job, int t) {
     int tile;
     const int entry = entry_of(job, tile);
@@ -427,11 +642,10 @@ struct DownJobs {
   }
 };
 
-template <int NT, int kDepth, int kCtas>
 __global__ void __launch_bounds__(kStreamThreads, kCtas)
     dq4_moe_down_kernel(const __grid_constant__ CUtensorMap map_w, const MoeArgs p) {
   extern __shared__ uint8_t smem_raw[];
-  using Jobs = DownJobs<NT, kDepth>;
+  using Jobs = DownJobs;
   uint8_t* smem = aligned_1024(smem_raw);
   Jobs::S::setup(smem, map_w);
   wait_for_stream();
@@ -470,50 +684,47 @@ __global__ void __launch_bounds__(kCombineThreads) dq4_moe_combine_kernel(const 
 
 int64_t up256(int64_t n) { return (n + 255) / 256 * 256; }
 
-// NT: tokens of an entry, by eights; depths of the rings, CTAs of an SM.
-template <int NT, int kUpDepth, int kUpCtas, int kDownDepth, int kDownCtas>
-int launch_moe(MoeArgs p, int dev, int sms, cudaStream_t s) {
-  p.most = 8 * NT;
-  auto up = dq4_moe_up_kernel<NT, kUpDepth, kUpCtas>;
-  auto down = dq4_moe_down_kernel<NT, kDownDepth, kDownCtas>;
+int launch_moe(const MoeArgs& p, int dev, int sms, cudaStream_t s) {
   const int pairs = p.T * p.top_k;
-  const int64_t entries = most_entries(p.E, pairs, p.most);
+  const int64_t entries = most_entries(p.E, pairs);
   const int more = int(entry_bytes(entries, pairs));
-  constexpr int kMore = kMaxPairs * 8 + (kMaxExperts + kMaxPairs / 8) * 4 + 2;
-  constexpr int kUpBytes = UpJobs<NT, kUpDepth>::S::kBytes + 1024;
-  constexpr int kDownBytes = DownJobs<NT, kDownDepth>::S::kBytes + 1024;
-  static_assert(kUpBytes + kMore <= 227 * 1024 && kDownBytes + kMore <= 227 * 1024, "shared memory");
+  constexpr int kMore = kMaxPairs * 8 + kMaxEntries * 4 + 2;
+  constexpr int kUpBytes = UpJobs::S::kBytes + 1024, kDownBytes = DownJobs::S::kBytes + 1024;
+  static_assert(kUpBytes + kMore <= 227 * 1024 && kDownBytes + kMore <= 227 * 1024,
+                "shared memory");
   const int keys = kRouteThreads / 32 * p.E * 4;
   static std::atomic<uint64_t> allowed_route{0}, allowed_up{0}, allowed_down{0};
   if (const int st = allow_smem(dq4_moe_route_kernel, kRouteThreads / 32 * kMaxExperts * 4, dev,
                                 &allowed_route))
     return st;
-  if (const int st = allow_smem(up, kUpBytes + kMore, dev, &allowed_up)) return st;
-  if (const int st = allow_smem(down, kDownBytes + kMore, dev, &allowed_down)) return st;
+  if (const int st = allow_smem(dq4_moe_up_kernel, kUpBytes + kMore, dev, &allowed_up)) return st;
+  if (const int st = allow_smem(dq4_moe_down_kernel, kDownBytes + kMore, dev, &allowed_down))
+    return st;
   CUtensorMap w1, w2;
   if (const int st = encode_2d(&w1, CU_TENSOR_MAP_DATA_TYPE_UINT8, p.W1, p.H, 2 * p.I * p.E, p.H,
                                kChunk, kUpPlaces, CU_TENSOR_MAP_SWIZZLE_128B))
     return st;
-  if (const int st = encode_2d(&w2, CU_TENSOR_MAP_DATA_TYPE_UINT8, p.W2, p.I, p.H * p.E, p.I, kChunk,
-                               kDownPlaces, CU_TENSOR_MAP_SWIZZLE_128B))
+  if (const int st = encode_2d(&w2, CU_TENSOR_MAP_DATA_TYPE_UINT8, p.W2, p.I, p.H * p.E, p.I,
+                               kChunk, kDownPlaces, CU_TENSOR_MAP_SWIZZLE_128B))
     return st;
-  if (const int st = launch_ordered(dq4_moe_route_kernel, dim3(unsigned(p.T)), kRouteThreads, keys, s,
-                                    p))
+  if (const int st = launch_ordered(dq4_moe_route_kernel, dim3(unsigned(p.T)), kRouteThreads,
+                                    keys, s, p))
     return st;
   // (jobs are known on the device only; no more than entries times the tiles of places)
-  auto grid = [&](int64_t places, int64_t tile, int ctas) {
+  auto grid = [&](int64_t places, int64_t tile) {
     const int64_t jobs = (places + tile - 1) / tile * entries;
-    return dim3(unsigned(jobs < ctas * sms ? jobs : ctas * sms));
+    return dim3(unsigned(jobs < kCtas * sms ? jobs : kCtas * sms));
   };
-  if (const int st = launch_ordered(up, grid(p.I, kUpPlaces, kUpCtas), kStreamThreads,
+  if (const int st = launch_ordered(dq4_moe_up_kernel, grid(p.I, kUpPlaces), kStreamThreads,
                                     kUpBytes + more, s, w1, p))
     return st;
-  if (const int st = launch_ordered(down, grid(p.H, kDownPlaces, kDownCtas), kStreamThreads,
+  if (const int st = launch_ordered(dq4_moe_down_kernel, grid(p.H, kDownPlaces), kStreamThreads,
                                     kDownBytes + more, s, w2, p))
     return st;
   const int64_t per = kCombineThreads * 4;
-  return launch_ordered(dq4_moe_combine_kernel, dim3(unsigned((p.H + per - 1) / per), unsigned(p.T)),
-                        kCombineThreads, 0, s, p);
+  return launch_ordered(dq4_moe_combine_kernel,
+                        dim3(unsigned((p.H + per - 1) / per), unsigned(p.T)), kCombineThreads, 0, s,
+                        p);
 }
 
 }  // namespace
@@ -553,9 +764,9 @@ int dq4_int8_moe(const void* X, int64_t row_stride, int32_t dtype, int64_t T, in
   if (misaligned(workspace, 256)) return DQ4_ERR_ALIGN;
   int dev, sms;
   if (const int st = current_device(&dev, &sms)) return st;
-  MoeArgs p = {X, row_stride, dtype == DQ4_OUT_BF16, int(T), int(E), top_k, renormalize, 0, H, I, logits,
-               W1, W2, S1, S2, ids, weights, Y, nullptr, nullptr, nullptr, nullptr,
-               nullptr, bad};
+  MoeArgs p = {X, row_stride, dtype == DQ4_OUT_BF16, int(T), int(E), top_k, renormalize, H, I,
+               logits, W1, W2, S1, S2, ids, weights, Y, nullptr, nullptr, nullptr, nullptr, nullptr,
+               bad};
   char* at = static_cast<char*>(workspace);
   p.r = reinterpret_cast<Routed*>(at);
   at += up256(sizeof(Routed));
@@ -567,10 +778,7 @@ int dq4_int8_moe(const void* X, int64_t row_stride, int32_t dtype, int64_t T, in
   at += T * top_k * up256(I / 4);
   p.out = reinterpret_cast<float*>(at);
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  // (entries of 16 pairs, two products for each weight's conversion, took more: for 64 tokens
-  // through 2 of 8 experts of 4096 x 14336, 16 pairs each, 443 us, in eights, which read the weights
-  // twice from L2, 409; for 23 tokens 302 and 237)
-  return launch_moe<1, 2, 2, 2, 2>(p, dev, sms, s);
+  return launch_moe(p, dev, sms, s);
 }
 
 }  // extern "C"

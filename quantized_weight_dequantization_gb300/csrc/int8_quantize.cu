@@ -1,12 +1,12 @@
 // Rows in 8 bits with outlier columns: dq4_int8_quantize (dq4_int8.h).
 //
 // Bound by memory: 2 bytes a value in, 1 out.  A row lies in the registers of a warp (up to 1024
-// values) or of a CTA, is read once, and its codes are written as if there were no outlier
-// columns; values past the threshold only mark their column (their own codes are nothing yet).  A
-// second, small launch lists the marked columns, takes their codes out and copies their values:
-// 2 M L scattered accesses instead of a second pass over X.  A mark is a bit set by an atomic that
-// nothing waits for, in one of 16 copies: one word takes an atomic (or a store) every 2 to 3 ns, and
-// 16384 x 1024 with 5 such columns took 31 to 37 us with a single copy.
+// values) or of a CTA, is read once, and its codes are written as if there were no outlier columns;
+// values past the threshold only mark their column (their own codes are nothing yet).  A second,
+// small launch lists the marked columns, takes their codes out and copies their values: 2 M L
+// scattered accesses instead of a second pass over X.  A mark is a bit set by an atomic that
+// nothing waits for, in one of 16 copies: one word takes an atomic (or a store) every 2 to 3 ns,
+// and 16384 x 1024 with 5 such columns took 31 to 37 us with a single copy.
 // The maximum is taken on the bits of |x|, two values an instruction: for values that are not
 // negative the order of the bits is that of the numbers, infinity and NaN last.
 #include "int8.cuh"
@@ -44,9 +44,10 @@ __device__ __forceinline__ float2 widen2(uint32_t w) {
   }
 }
 
-// x * inverse to the nearest integer, in the low byte of each half: 1.5 * 2^23 leaves no bits behind
-// the point.  (Two values an instruction.  The product is rounded on its own: ptxas makes one
-// instruction of a packed product and sum, whatever their modifiers, so the sum is an FMA by 1.)
+// x * inverse to the nearest integer, in the low byte of each half: 1.5 * 2^23 leaves no bits
+// behind the point.  (Two values an instruction.  The product is rounded on its own: ptxas makes
+// one instruction of a packed product and sum, whatever their modifiers, so the sum is an FMA by
+// 1.)
 __device__ __forceinline__ uint64_t codes_of(float2 x, uint64_t inverse2) {
   const uint64_t magic2 = 0x4B4000004B400000ull, one2 = 0x3F8000003F800000ull;
   uint64_t v;
@@ -87,7 +88,9 @@ __global__ void __launch_bounds__(kRowThreads) int8_quantize_kernel(const QuantA
       }
     }
   };
-  auto word = [&](int g, int i) { return i == 0 ? v[g].x : i == 1 ? v[g].y : i == 2 ? v[g].z : v[g].w; };
+  auto word = [&](int g, int i) {
+    return i == 0 ? v[g].x : i == 1 ? v[g].y : i == 2 ? v[g].z : v[g].w;
+  };
 
   // ---- the largest |x|
   uint32_t top = 0;
@@ -332,13 +335,15 @@ int dq4_int8_quantize(const void* X, int64_t row_stride, int32_t dtype, int64_t 
   const bool vec = K % 8 == 0 && row_stride % 8 == 0 && !misaligned(X, 16) && !misaligned(codes, 8);
   if (M > 0) {
     const bool bf16 = dtype == DQ4_OUT_BF16;
-    const int st = bf16 ? (thr ? launch_rows<true, true>(p, vec, s) : launch_rows<true, false>(p, vec, s))
+    const int st = bf16 ? (thr ? launch_rows<true, true>(p, vec, s)
+                               : launch_rows<true, false>(p, vec, s))
                         : (thr ? launch_rows<false, true>(p, vec, s)
                                : launch_rows<false, false>(p, vec, s));
     if (st || !thr) return st;
   }
   OutlierArgs o = {p.X, row_stride, M, K, p.loud, codes, scales, cols, max_cols,
-                   static_cast<uint16_t*>(outliers), count, p.marks, static_cast<int*>(workspace), 1};
+                   static_cast<uint16_t*>(outliers), count, p.marks, static_cast<int*>(workspace),
+                   1};
   // rows of a CTA: one wave of the SMs, two CTAs each
   o.rows = (M + 2 * sms - 1) / (2 * sms);
   if (o.rows < 1) o.rows = 1;
