@@ -51,7 +51,7 @@ struct Gemm {
   static constexpr int kPieces = kBarsAt / kPiece;
   static constexpr int kBars = 2 * kSlots + 2 * kRawSlots + 2 * kRing + 2 * kBuffers + 1 + kPieces;
   static constexpr int kBytes = kBarsAt + 8 * kBars + 1024;  // + alignment slack
-  static constexpr int kStatic = kBack ? 16 * kStage + 64 : 64;
+  static constexpr int kStatic = kBack ? 16 * kStage + 64 : 4 * BX + 64;
   static_assert(kBytes + kStatic <= 227 * 1024, "shared memory budget");
   static_assert(kBytes > 116 * 1024, "one CTA per SM: the TMEM allocation never waits");
 };
@@ -88,6 +88,11 @@ __device__ __forceinline__ bool all_readers(bool v) {
 __device__ __forceinline__ void commit(uint32_t bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];"
                :: "r"(bar) : "memory");
+}
+__device__ __forceinline__ int load_acquire(const int* p) {
+  int v;
+  asm volatile("ld.acquire.gpu.global.b32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+  return v;
 }
 // Four 8 x 8 matrices of 16-bit elements, transposed; a thread gives the address of a row.
 __device__ __forceinline__ void load_transposed(uint32_t addr, uint32_t* m) {
@@ -147,6 +152,7 @@ __global__ void __launch_bounds__(Gemm<BX, kBack>::kThreads, 1)
   __shared__ uint32_t s_tmem;
   __shared__ volatile int s_abort;
   __shared__ bool s_last;
+  __shared__ __align__(16) float s_unit[kBack ? 4 : BX];  // of the item's rows
   __shared__ __align__(16) float s_scale[kBack ? 4 * kStage : 4];  // two stages of each group
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
@@ -513,22 +519,24 @@ __global__ void __launch_bounds__(Gemm<BX, kBack>::kThreads, 1)
     for (int64_t walk = walk0; next_item(walk, it); ++turn) {
       const int buffer = turn % kBuffers;
       const int64_t n = it.lane0 + column, m0 = it.row0 + half * kHalf;
-      float scale = 1.f, bias = 0.f, unit[kChunks];
+      const int rank = tid - 32 * kProducers;
+      float scale = 1.f, bias = 0.f, unit = 0.f;
       if constexpr (!kBack) {
         if (n < p.lanes) {
           scale = load_global(p.SCB + n) * kRecip127;
           if (p.bias) bias = load_any(p.bias, n, p.out_dtype);
         }
-#pragma unroll
-        for (int c = 0; c < kChunks; ++c)
-          unit[c] =
-              m0 + 32 * c + lane < p.rows ? load_global(p.row_units + m0 + 32 * c + lane) : 0.f;
+        if (rank < BX && it.row0 + rank < p.rows) unit = load_global(p.row_units + it.row0 + rank);
       }
       const bool ok = !*aborted && mbar_wait(acc_full(buffer), uint32_t(turn / kBuffers) & 1u) &&
                       !*aborted;
       if (!all_readers(ok)) {
         if (!ok && lane == 0 && !*aborted) fail();
         break;
+      }
+      if constexpr (!kBack) {
+        if (rank < BX) s_unit[rank] = unit;
+        bar_readers();
       }
       asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
       const uint32_t at = tmem + (uint32_t(quad * 32) << 16) + buffer * BX + half * kHalf;
@@ -552,34 +560,50 @@ __global__ void __launch_bounds__(Gemm<BX, kBack>::kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(acc_empty(buffer));
       };
-      // 32 columns (activation rows) in the output's type, two in a word; u: their units, a lane
-      // each
-      auto finish = [&](uint32_t acc, float u, int j) {
-        if constexpr (kBack) return __uint_as_float(acc);
-        else return __uint_as_float(acc) * __shfl_sync(kAllLanes, u, j) * scale + bias;
+      // 32 columns (activation rows) finished, and in the output's type, two in a word
+      auto finish = [&](uint32_t (&v)[32], int c) {
+        if constexpr (!kBack) {
+          const float* unit = s_unit + half * kHalf + 32 * c;
+#pragma unroll
+          for (int j = 0; j < 32; j += 4) {
+            const float4 u = *reinterpret_cast<const float4*>(unit + j);
+            const float by[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              v[j + k] = __float_as_uint(__uint_as_float(v[j + k]) * by[k] * scale + bias);
+          }
+        }
       };
-      auto pack = [&](const uint32_t (&v)[32], float u, uint32_t* to) {
+      auto pack = [&](uint32_t (&v)[32], int c, uint32_t* to) {
+        finish(v, c);
 #pragma unroll
         for (int j = 0; j < 32; j += 2) {
-          const float a = finish(v[j], u, j), b = finish(v[j + 1], u, j + 1);
+          const float a = __uint_as_float(v[j]), b = __uint_as_float(v[j + 1]);
           to[j / 2] = bf16 ? pack2<DQ4_OUT_BF16>(a, b) : pack2<DQ4_OUT_F16>(a, b);
         }
       };
+      // (rows of the 32 that are there; none for a lane past the last)
+      auto rows_at = [&](int c) {
+        return n < p.lanes ? int(min(int64_t(32), p.rows - m0 - 32 * c)) : 0;
+      };
       auto store = [&](const uint32_t* from, int c) {
-        uint16_t* out = static_cast<uint16_t*>(p.out);
+        const int rows = rows_at(c);
+        if (pairs) {
+          const int odd = column & 1;
+          uint16_t* to = static_cast<uint16_t*>(p.out) + (m0 + 32 * c + odd) * p.lanes + n - odd;
 #pragma unroll
-        for (int j = 0; j < 16; ++j) {
-          const int64_t m = m0 + 32 * c + 2 * j;
-          if (pairs) {
+          for (int j = 0; j < 16; ++j, to += 2 * p.lanes) {
             const uint32_t other = __shfl_xor_sync(kAllLanes, from[j], kNext);
-            const uint32_t v = column & 1 ? __byte_perm(other, from[j], 0x7632)
-                                          : __byte_perm(from[j], other, 0x5410);
-            const int64_t row = m + (column & 1);
-            if (row < p.rows && n < p.lanes)
-              *reinterpret_cast<uint32_t*>(out + row * p.lanes + (n & ~int64_t(1))) = v;
-          } else if (n < p.lanes) {
-            if (m < p.rows) out[m * p.lanes + n] = uint16_t(from[j]);
-            if (m + 1 < p.rows) out[(m + 1) * p.lanes + n] = uint16_t(from[j] >> 16);
+            const uint32_t v = odd ? __byte_perm(other, from[j], 0x7632)
+                                   : __byte_perm(from[j], other, 0x5410);
+            if (2 * j + odd < rows) *reinterpret_cast<uint32_t*>(to) = v;
+          }
+        } else {
+          uint16_t* to = static_cast<uint16_t*>(p.out) + (m0 + 32 * c) * p.lanes + n;
+#pragma unroll
+          for (int j = 0; j < 16; ++j, to += 2 * p.lanes) {
+            if (2 * j < rows) to[0] = uint16_t(from[j]);
+            if (2 * j + 1 < rows) to[p.lanes] = uint16_t(from[j] >> 16);
           }
         }
       };
@@ -591,7 +615,7 @@ __global__ void __launch_bounds__(Gemm<BX, kBack>::kThreads, 1)
         for (int c = 0; c < kChunks; ++c) {
           uint32_t v[32];
           read(c, v);
-          pack(v, unit[c], keep + 16 * c);
+          pack(v, c, keep + 16 * c);
         }
         release();
 #pragma unroll
@@ -607,9 +631,19 @@ __global__ void __launch_bounds__(Gemm<BX, kBack>::kThreads, 1)
         return p.part + ((cta * 2 + which) * (BX / 4) + half * (kHalf / 4)) * kTileW + quad * 32 +
                lane;
       };
-      int64_t cta0 = 0;
-      int sharers = 0;
-      if (!whole) {
+      const int64_t cta0 = whole ? 0 : cta_of(it.tile * stages);
+      const int64_t cta1 = whole ? 0 : cta_of((it.tile + 1) * stages - 1);
+      const int sharers = int(cta1 - cta0) + 1, own = int(blockIdx.x - cta0);
+      // The CTA's last item: the rings are idle, and its part can stay in TMEM if the others are there,
+      // as they mostly are: they are the first items of their CTAs.
+      const bool over = !whole && walk >= walk1;
+      bool stays = false;
+      if (over) {
+        if (tid == 32 * kProducers) s_last = load_acquire(p.count + cta1) == sharers - 1;
+        bar_readers();
+        stays = s_last;
+      }
+      if (!whole && !stays) {
         float4* part = part_at(blockIdx.x, it.begin == 0);
 #pragma unroll 1
         for (int c = 0; c < kChunks; ++c) {
@@ -623,30 +657,27 @@ __global__ void __launch_bounds__(Gemm<BX, kBack>::kThreads, 1)
         }
         release();
         bar_readers();
-        const int64_t cta1 = cta_of((it.tile + 1) * stages - 1);
-        cta0 = cta_of(it.tile * stages);
-        sharers = int(cta1 - cta0) + 1;
-        if (tid == 32 * kProducers) {
-          s_last = atomic_add_acq_rel(p.count + cta1, 1) == int(cta1 - cta0);
-          if (s_last) p.count[cta1] = 0;  // ready for the next call
-        }
+        if (tid == 32 * kProducers)
+          s_last = atomic_add_acq_rel(p.count + cta1, 1) == sharers - 1;
         bar_readers();
         if (!s_last) continue;
       }
-      // The CTA's last item: the rings are idle, and the parts are copied into them, 32 columns of
-      // all of them at a time (which the first reader warp issues), the next ones ahead.
-      const bool idle = !whole && walk >= walk1 && sharers <= S::kPieces;
-      const int depth = idle ? S::kPieces / sharers : 1;
+      if (!whole && tid == 32 * kProducers) p.count[cta1] = 0;  // ready for the next call
+      // The parts are copied into the idle rings, 32 columns of all of them at a time (which the
+      // first reader warp issues), the next ones ahead.
+      const int pieces = stays ? sharers - 1 : sharers;
+      const bool idle = over && pieces <= S::kPieces;
+      const int depth = idle ? S::kPieces / pieces : 1;
       auto copy = [&](int c) {
         const uint32_t bar = piece_full(c % depth);
-        if (lane == 0) mbar_expect(bar, sharers * S::kPiece);
+        if (lane == 0) mbar_expect(bar, pieces * S::kPiece);
         __syncwarp();
-        const int q = lane >> 1, h = lane & 1;
-        if (q < sharers)
+        const int i = lane >> 1, h = lane & 1, q = stays && i >= own ? i + 1 : i;
+        if (i < pieces)
           asm volatile(
               "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes "
               "[%0], [%1], %2, [%3];"
-              :: "r"(sbase + (c % depth * sharers + q) * S::kPiece + h * (S::kPiece / 2)),
+              :: "r"(sbase + (c % depth * pieces + i) * S::kPiece + h * (S::kPiece / 2)),
                  "l"(p.part + ((cta0 + q) * 2 + (q == 0)) * (BX / 4 * kTileW) +
                      (h * (kHalf / 4) + 8 * c) * kTileW),
                  "r"(S::kPiece / 2), "r"(bar) : "memory");
@@ -664,25 +695,31 @@ __global__ void __launch_bounds__(Gemm<BX, kBack>::kThreads, 1)
           read(c, v);
         } else {
           if (idle) here = here && mbar_wait(piece_full(c % depth), uint32_t(c / depth) & 1u);
-          uint32_t at = sbase + c % depth * sharers * S::kPiece + half * (S::kPiece / 2) +
+          uint32_t at = sbase + c % depth * pieces * S::kPiece + half * (S::kPiece / 2) +
                         (quad * 32 + lane) * 16;
           float sum[32] = {};
 #pragma unroll 1
-          for (int q = 0; q < sharers; ++q, at += S::kPiece) {
-            const float4* from = part_at(cta0 + q, q == 0) + 8 * c * kTileW;
-            float more[32];
+          for (int q = 0; q < sharers; ++q) {
+            uint32_t more[32];
+            if (stays && q == own) {
+              read(c, more);
+            } else if (idle) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              if (idle) {
+              for (int j = 0; j < 8; ++j) {
                 const uint4 w = lds_v4(at + j * kTileW * 16);
                 memcpy(&more[4 * j], &w, 16);
-              } else {
+              }
+              at += S::kPiece;
+            } else {
+              const float4* from = part_at(cta0 + q, q == 0) + 8 * c * kTileW;
+#pragma unroll
+              for (int j = 0; j < 8; ++j) {
                 const float4 w = load_l2(from + j * kTileW);
                 memcpy(&more[4 * j], &w, 16);
               }
             }
 #pragma unroll
-            for (int j = 0; j < 32; ++j) sum[j] += more[j];
+            for (int j = 0; j < 32; ++j) sum[j] += __uint_as_float(more[j]);
           }
           memcpy(v, sum, sizeof(v));
           if (idle && c + depth < kChunks) {  // their place, for later ones
@@ -690,19 +727,16 @@ __global__ void __launch_bounds__(Gemm<BX, kBack>::kThreads, 1)
             if (warp == kProducers) copy(c + depth);
           }
         }
-        float u = 0.f;
-        if constexpr (!kBack)
-          if (m0 + 32 * c + lane < p.rows) u = load_global(p.row_units + m0 + 32 * c + lane);
         if (f32) {
-          float* out = static_cast<float*>(p.out) + (m0 + 32 * c) * p.lanes + n;
+          finish(v, c);
+          const int rows = rows_at(c);
+          float* to = static_cast<float*>(p.out) + (m0 + 32 * c) * p.lanes + n;
 #pragma unroll
-          for (int j = 0; j < 32; ++j) {
-            const float y = finish(v[j], u, j);
-            if (m0 + 32 * c + j < p.rows && n < p.lanes) out[j * p.lanes] = y;
-          }
+          for (int j = 0; j < 32; ++j, to += p.lanes)
+            if (j < rows) *to = __uint_as_float(v[j]);
         } else {
           uint32_t keep[16];
-          pack(v, u, keep);
+          pack(v, c, keep);
           store(keep, c);
         }
       }
