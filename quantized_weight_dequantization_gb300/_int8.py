@@ -63,18 +63,6 @@ def _need_of(index: int, name: str, *shape) -> int:
 _current_device = torch._C._cuda_getDevice
 
 
-def _on_its_device(call):
-    """A call whose tensors are on another device than the current one, with that made current."""
-    @functools.wraps(call)
-    def wrapper(first, *args, **kwargs):
-        like = first[0] if isinstance(first, tuple) else first
-        if like.is_cuda and like.get_device() != _current_device():
-            with torch.cuda.device(like.get_device()):
-                return call(first, *args, **kwargs)
-        return call(first, *args, **kwargs)
-    return wrapper
-
-
 def _on_gpu(t: torch.Tensor, name: str) -> None:
     if t.device.type != "cuda":
         raise ValueError(f"{name}: must be a CUDA tensor (the library reads device memory)")
@@ -260,7 +248,6 @@ def _scratch(workspace, need: int, what: str, like: torch.Tensor, handle):
     return ws.data_ptr(), ws.numel()
 
 
-@_on_its_device
 def int8_linear_backward(dY: torch.Tensor, CB: torch.Tensor, SCB: torch.Tensor,
                          dX: Optional[torch.Tensor] = None,
                          workspace: Optional[torch.Tensor] = None,
@@ -277,6 +264,10 @@ def int8_linear_backward(dY: torch.Tensor, CB: torch.Tensor, SCB: torch.Tensor,
         raise TypeError(f"dY: must be float16 or bfloat16, got {dY.dtype}")
     if dY.dim() != 2 or CB.dim() != 2 or dY.shape[1] != CB.shape[0]:
         raise ValueError(f"dY {tuple(dY.shape)} does not go with CB {tuple(CB.shape)}")
+    index = dY.get_device()
+    if index != _current_device():
+        with torch.cuda.device(index):
+            return int8_linear_backward(dY, CB, SCB, dX, workspace, bad, stream)
     M, N = dY.shape
     K = CB.shape[1]
     dy_ptr = _flat(dY, "dY", dY.dtype, 0, dY)
@@ -287,7 +278,6 @@ def int8_linear_backward(dY: torch.Tensor, CB: torch.Tensor, SCB: torch.Tensor,
         _shape(dX, "dX", (M, K))
     dx_ptr = _flat(dX, "dX", dY.dtype, 0, dY)
     bad_ptr = _bad(bad, dY)
-    index = dY.get_device()
     handle = _stream(stream, index)
     need = _need_of(index, "linear_backward", M, N, K)
     with _call_lock(index, handle):
@@ -300,7 +290,6 @@ def int8_linear_backward(dY: torch.Tensor, CB: torch.Tensor, SCB: torch.Tensor,
 
 
 # ------------------------------------------------------------- mixture of experts
-@_on_its_device
 def int8_moe(X: torch.Tensor, logits: torch.Tensor, w1: torch.Tensor, s1: torch.Tensor,
              w2: torch.Tensor, s2: torch.Tensor, top_k: int, renormalize: bool = True,
              return_routing: bool = False, workspace: Optional[torch.Tensor] = None,
@@ -319,6 +308,11 @@ def int8_moe(X: torch.Tensor, logits: torch.Tensor, w1: torch.Tensor, s1: torch.
     of the graph's own.
     """
     _rows(X, "X")
+    index = X.get_device()
+    if index != _current_device():
+        with torch.cuda.device(index):
+            return int8_moe(X, logits, w1, s1, w2, s2, top_k, renormalize, return_routing,
+                            workspace, bad, stream)
     T, H = X.shape
     w1_ptr, s1_ptr = _weight(w1, s1, X, "w1", 3)
     w2_ptr, s2_ptr = _weight(w2, s2, X, "w2", 3)
@@ -333,7 +327,6 @@ def int8_moe(X: torch.Tensor, logits: torch.Tensor, w1: torch.Tensor, s1: torch.
     weights = torch.empty((T, top_k), dtype=torch.float32, device=X.device)
     Y = torch.empty((T, H), dtype=X.dtype, device=X.device)
     bad_ptr = _bad(bad, X)
-    index = X.get_device()
     handle = _stream(stream, index)
     need = _need_of(index, "moe", T, H, I, top_k)
     with _call_lock(index, handle):

@@ -888,22 +888,23 @@ struct Plan {
 };
 
 // The tile's width, and whether CTAs take whole tiles or equal runs of stages, by the estimated
-// time in cycles.  A stage takes about 1000 at BX 64 and 128 and 1500 at 256 (the MMAs: 122 each,
-// at 256 181); the end of a tile 1500 where its accumulator is the only one.  Parts of tiles cost
-// their writing (40 bytes a cycle), the count (3000), and the reading of all parts of a tile by one
-// CTA, at 56 bytes a cycle: for wide tiles that few stages share, more than the SMs that whole
-// tiles leave idle.  512 rows through 4096 x 4096, in us: 256 wide in parts 37, whole 25.
-Plan plan_gemm(int64_t lanes, int64_t rows, int steps, int sms) {
+// time in cycles, from measured ones: a stage takes 840, 890 and 1350 at BX 64, 128 and 256 (of 8
+// MMAs; the gradient's 1270, 1310 and 1600), the end of a tile 1500 where its accumulator is the
+// only one.  Runs cost 12000 more, the parts' writing, counting and joining, and a part's bytes by
+// the CTAs that share a tile, which are more, and have no whole tile, where a run is shorter than a
+// tile.  In us, whole / runs: 64 rows through 4096 x 11008 19.9 / 22, through 4096 x 4096
+// 18.4 / 16.2, 14336 to 4096 55 / 28; 512 through 4096 x 11008, 256 wide, 56 / 45.
+Plan plan_gemm(int64_t lanes, int64_t rows, int steps, bool back, int sms) {
   Plan best = {};
   double best_cost = 1e300;
   const int stages = (steps + 1) / 2;
   for (int bx = 64; bx <= 256; bx *= 2) {
     const int64_t tiles_x = (rows + bx - 1) / bx;
     const int64_t tiles = tiles_x * ((lanes + kTileW - 1) / kTileW);
-    const double stage = bx < 256 ? 1000 : 1500;
-    const double end = bx == 64 ? 200 : 1500, last = bx / 64 * 700 + 5000;
-    const double rounds = double((tiles + sms - 1) / sms);
-    double cost = rounds * (stages * stage + end) + last;
+    const double stage = back ? (bx == 64 ? 1270 : bx == 128 ? 1310 : 1600)
+                              : (bx == 64 ? 840 : bx == 128 ? 890 : 1350);
+    const double end = bx == 64 ? 200 : 1500;
+    double cost = double((tiles + sms - 1) / sms) * (stages * stage + end);
     if (cost < best_cost) {
       best_cost = cost;
       best = {bx, stages, tiles_x, tiles, int(tiles < sms ? tiles : sms), false};
@@ -911,8 +912,8 @@ Plan plan_gemm(int64_t lanes, int64_t rows, int steps, int sms) {
     const int64_t units = tiles * stages;
     const int ctas = int(units < sms ? units : sms);
     const double run = double(units) / ctas, sharers = stages / run + 1;
-    cost = (run + 1) * stage + (run / stages + 1) * end + last + bx / 64 * 600 + 3000 +
-           bx * (13 + 9 * sharers);
+    cost = run * stage + (run / stages + 1) * end + 12000 +
+           bx * (9 * sharers + (run < stages ? 25 : 0));
     if (cost < best_cost) {
       best_cost = cost;
       best = {bx, stages, tiles_x, tiles, ctas, true};
@@ -956,14 +957,14 @@ int64_t part_bytes(const Plan& pl) {
 }  // namespace
 
 int64_t int8_gemm_workspace(int64_t M, int64_t N, int64_t K, int L, int sms) {
-  const Plan pl = plan_gemm(N, M, all_steps(K, L), sms);
+  const Plan pl = plan_gemm(N, M, all_steps(K, L), false, sms);
   return kInt8Counters + up256(N * k_steps(L) * kStep) + up256(M * 4) +
          up256(M * all_steps(K, L) * kStep * 2) + part_bytes(pl);
 }
 
 int launch_int8_gemm(const Int8Linear& a, int dev, int sms, void* workspace, cudaStream_t stream) {
   const int steps = all_steps(a.K, a.L);
-  const Plan pl = plan_gemm(a.N, a.M, steps, sms);
+  const Plan pl = plan_gemm(a.N, a.M, steps, false, sms);
   char* at = static_cast<char*>(workspace);
   int* count = reinterpret_cast<int*>(at);
   at += kInt8Counters;
@@ -1026,12 +1027,12 @@ int launch_int8_gemm(const Int8Linear& a, int dev, int sms, void* workspace, cud
 }
 
 int64_t int8_backward_workspace(int64_t M, int64_t N, int64_t K, int sms) {
-  return kInt8Counters + part_bytes(plan_gemm(K, M, k_steps(N), sms));
+  return kInt8Counters + part_bytes(plan_gemm(K, M, k_steps(N), true, sms));
 }
 
 int launch_int8_backward(const Int8Backward& a, int dev, int sms, void* workspace,
                          cudaStream_t stream) {
-  const Plan pl = plan_gemm(a.K, a.M, k_steps(a.N), sms);
+  const Plan pl = plan_gemm(a.K, a.M, k_steps(a.N), true, sms);
   CUtensorMap w, x;
   if (const int st = encode_2d(&w, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.CB, a.K, a.N, a.K, kTileW,
                                kStage, CU_TENSOR_MAP_SWIZZLE_128B))

@@ -369,3 +369,400 @@ def test_moe_same_expert_for_all(dq):
     w2, s2 = weight(rng, E, H, I)
     for k in (1, 2):
         check_moe(dq, x, dev(logits), w1, s1, w2, s2, k, False, "f16", k)
+
+
+# ------------------------------------------------------------- sums in parts, offsets, ends
+@pytest.mark.parametrize("M,N,K", [(40, 64, 65536), (300, 128, 20000), (70, 130, 32768),
+                                   (129, 40, 50000), (260, 1500, 8208), (18, 1500, 30000)])
+def test_few_tiles_of_long_sums(dq, M, N, K):
+    """Few tiles and a long sum: many parts to a tile, of which one joins all; and the same for
+    the gradient, twice, bit for bit."""
+    rng = np.random.default_rng(M + N + K)
+    CB, SCB = weight(rng, N, K)
+    rows = random_rows(dq, rng, M, K, 0)
+    y = check_linear(dq, rows, CB, SCB, rng.normal(size=N), "f32", (M, N, K))
+    assert y.shape == (M, N)
+    one, two = (dq.int8_linear(rows, dev(CB), dev(SCB)) for _ in range(2))
+    assert torch.equal(one, two)
+    lanes = N // 16 * 16
+    n = K // 8 * 8
+    CB, SCB = weight(rng, n, lanes)
+    dy = dev((rng.normal(size=(M, n)) * 0.05).astype(np.float32), DT["f16"])
+    dx = dq.int8_linear_backward(dy, dev(CB), dev(SCB))
+    w = defs.weight16(CB, SCB, lambda f: f.astype(np.float16).astype(np.float32))
+    want, size = defs.linear_backward(host(dy), w)
+    close(dx, want, (n / 16 + 4) * 2.0 ** -23 * size + U["f16"] * np.abs(want) + TINY["f16"],
+          (M, n, lanes))
+    assert torch.equal(dx, dq.int8_linear_backward(dy, dev(CB), dev(SCB)))
+
+
+def test_offsets_past_32_bits(dq):
+    """Operands and results of more than 2^31 values: their last rows, by the definitions."""
+    rng = np.random.default_rng(20)
+    rows_n, K = 140000, 16384
+    x = torch.randn(rows_n, K, device="cuda", dtype=torch.float16,
+                    generator=torch.Generator("cuda").manual_seed(1))
+    x[rows_n - 1, 7] = 40.0
+    rows = dq.int8_quantize(x, 20.0, 4)
+    last = slice(rows_n - 40, rows_n)
+    codes, scales, *_ = defs.quantize(host(x[last]), 20.0, 4)
+    assert rows.cols.tolist() == [7, -1, -1, -1] and rows.count.item() == 1
+    assert np.array_equal(rows.codes[last].cpu().numpy(), codes)
+    assert np.array_equal(host(rows.scales[last]), scales)
+    assert torch.equal(rows.outliers[last, 0], x[last, 7])
+    del x
+
+    def check(y, rows, CB, SCB, what):
+        want, size = defs.linear(rows.codes.cpu().numpy(), host(rows.scales), CB, SCB,
+                                 None if rows.cols is None else rows.cols.cpu().numpy(),
+                                 None if rows.cols is None else host(rows.outliers))
+        close(y, want, 2.0 ** -21 * size + U["f16"] * np.abs(want) + TINY["f16"], what)
+    CB, SCB = weight(rng, 24, K)
+    y = dq.int8_linear(rows, dev(CB), dev(SCB))
+    cut = dq.Int8Rows(rows.codes[last], rows.scales[last], rows.cols, rows.outliers[last])
+    check(y[last], cut, CB, SCB, "rows")
+    # the codes as a weight: rows past the 32-bit offset, by few and by many
+    few = dq.Int8Rows(dev(rng.integers(-127, 128, (70, K)).astype(np.int8)),
+                      dev(np.full(70, 0.7, np.float32)))
+    for M in (3, 70):
+        some = dq.Int8Rows(few.codes[:M], few.scales[:M])
+        y = dq.int8_linear(some, rows.codes, rows.scales)
+        check(y[:, last], some, rows.codes[last].cpu().numpy(),
+              host(rows.scales[last]).astype(np.float32), M)
+    del rows, y, cut
+    # results of more than 2^31 values
+    M, N, K = 140000, 16400, 16
+    CB, SCB = weight(rng, N, K)
+    rows = dq.Int8Rows(dev(rng.integers(-127, 128, (M, K)).astype(np.int8)),
+                       dev(np.full(M, 0.7, np.float32)))
+    y = dq.int8_linear(rows, dev(CB), dev(SCB))
+    last = slice(M - 40, M)
+    check(y[last], dq.Int8Rows(rows.codes[last], rows.scales[last]), CB, SCB, "results")
+    # as dY, and as rows of dX
+    dx = dq.int8_linear_backward(y, dev(CB), dev(SCB))
+    w = defs.weight16(CB, SCB, lambda f: f.astype(np.float16).astype(np.float32))
+    want, size = defs.linear_backward(host(y[last]), w)
+    close(dx[last], want, (N / 16 + 4) * 2.0 ** -23 * size + U["f16"] * np.abs(want)
+          + TINY["f16"], "dY")
+    del y, dx
+    CB, SCB = weight(rng, 16, 16400)
+    dy = torch.randn(M, 16, device="cuda", dtype=torch.float16)
+    dx = dq.int8_linear_backward(dy, dev(CB), dev(SCB))
+    w = defs.weight16(CB, SCB, lambda f: f.astype(np.float16).astype(np.float32))
+    want, size = defs.linear_backward(host(dy[last]), w)
+    close(dx[last], want, 5 * 2.0 ** -23 * size + U["f16"] * np.abs(want) + TINY["f16"], "dX")
+
+
+@pytest.mark.parametrize("M", [1, 20, 31, 40, 130])
+def test_nothing_beside_the_results_is_written(dq, M):
+    """Results and workspaces in the middle of larger buffers, at odd sizes."""
+    rng = np.random.default_rng(M)
+    lib = dq.get_lib()
+    N, K, guard = 187, 336, 4096
+
+    def inside(n, dtype):
+        buf = torch.full((n + 2 * guard,), 77, dtype=dtype, device="cuda")
+        return buf, buf[guard:guard + n]
+
+    def untouched(buf, n, what):
+        assert (buf[:guard] == 77).all() and (buf[guard + n:] == 77).all(), what
+
+    def workspace(need):
+        buf, ws = inside(need, torch.uint8)
+        ws.zero_()
+        return buf, ws
+    x = rows_of(rng, M, K, "bf16", 7)
+    dq.int8_quantize(x)  # (the first call gives the library's functions their types)
+    need = lib.dq4_int8_quantize_workspace_bytes(K)
+    wb, ws = workspace(need)
+    rows = dq.int8_quantize(x, 6.0, 9, workspace=ws)
+    untouched(wb, need, "quantize's workspace")
+    CB, SCB = weight(rng, N, K)
+    for kind in DT:
+        need = lib.dq4_int8_linear_workspace_bytes(M, N, K, 9)
+        wb, ws = workspace(need)
+        yb, y = inside(M * N, DT[kind])
+        dq.int8_linear(rows, dev(CB), dev(SCB), Y=y.view(M, N), workspace=ws if need else None)
+        untouched(wb, need, (kind, "workspace"))
+        untouched(yb, M * N, (kind, "Y"))
+        assert torch.equal(y.view(M, N), dq.int8_linear(rows, dev(CB), dev(SCB),
+                                                        out_dtype=DT[kind]))
+    # (the addresses of 16-bit rows that are odd in units of four bytes)
+    yb = torch.full((M * 188 + 1 + guard,), 77, dtype=torch.float16, device="cuda")
+    CB, SCB = weight(rng, 188, K)
+    dq.int8_linear(rows, dev(CB), dev(SCB), Y=yb[1:1 + M * 188].view(M, 188))
+    assert yb[0] == 77 and (yb[1 + M * 188:] == 77).all()
+    assert torch.equal(yb[1:1 + M * 188].view(M, 188), dq.int8_linear(rows, dev(CB), dev(SCB)))
+    N = 184
+    CB, SCB = weight(rng, N, K)
+    dy = rows_of(rng, M, N, "bf16")
+    need = lib.dq4_int8_linear_backward_workspace_bytes(M, N, K)
+    wb, ws = workspace(need)
+    xb, dx = inside(M * K, torch.bfloat16)
+    dq.int8_linear_backward(dy, dev(CB), dev(SCB), dx.view(M, K), workspace=ws)
+    untouched(wb, need, "backward's workspace")
+    untouched(xb, M * K, "dX")
+    E, H, I = 5, 80, 48
+    w1, s1 = weight(rng, E, 2 * I, H)
+    w2, s2 = weight(rng, E, H, I)
+    need = lib.dq4_int8_moe_workspace_bytes(M, H, I, 2)
+    wb, ws = workspace(need)
+    args = (rows_of(rng, M, H, "f16"), dev(rng.normal(size=(M, E)).astype(np.float32)), dev(w1),
+            dev(s1), dev(w2), dev(s2), 2)
+    y = dq.int8_moe(*args, workspace=ws)
+    untouched(wb, need, "moe's workspace")
+    assert torch.equal(y, dq.int8_moe(*args))
+
+
+def test_empty(dq):
+    """No rows, no outputs, no values."""
+    rng = np.random.default_rng(1)
+    CB, SCB = weight(rng, 24, 64)
+    rows = random_rows(dq, rng, 40, 64, 3)
+    none = dq.Int8Rows(rows.codes[:0], rows.scales[:0], rows.cols, rows.outliers[:0])
+    assert dq.int8_linear(none, dev(CB), dev(SCB)).shape == (0, 24)
+    assert dq.int8_linear(rows, dev(CB[:0]), dev(SCB[:0])).shape == (40, 0)
+    for M in (1, 40):
+        empty = dq.Int8Rows(rows.codes[:M, :0].contiguous(), rows.scales[:M])
+        bias = dev(rng.normal(size=24).astype(np.float32), torch.bfloat16)
+        y = dq.int8_linear(empty, dev(CB[:, :0]), dev(SCB), bias, torch.bfloat16)
+        assert torch.equal(y, bias.expand(M, -1))
+    dy = rows_of(rng, 40, 24, "f16")
+    assert dq.int8_linear_backward(dy[:0], dev(CB), dev(SCB)).shape == (0, 64)
+    assert dq.int8_linear_backward(dy, dev(CB[:, :0]), dev(SCB)).shape == (40, 0)
+    dx = dq.int8_linear_backward(dy[:, :0].contiguous(), dev(CB[:0]), dev(SCB[:0]))
+    assert dx.shape == (40, 64) and not dx.any()
+    w1, s1 = weight(rng, 2, 32, 48)
+    w2, s2 = weight(rng, 2, 48, 16)
+    y, ids, p = dq.int8_moe(rows_of(rng, 3, 48, "f16")[:0], torch.empty(0, 2, device="cuda"),
+                            dev(w1), dev(s1), dev(w2), dev(s2), 2, return_routing=True)
+    assert y.shape == (0, 48) and ids.shape == (0, 2) and p.shape == (0, 2)
+
+
+# ------------------------------------------------------------- together, and at the same time
+def layer(rng, dq, K, N, E=6, I=48):
+    w = [dev(a) for a in weight(rng, N, K)]
+    up = [dev(a) for a in weight(rng, E, 2 * I, N)]
+    down = [dev(a) for a in weight(rng, E, N, I)]
+    return w, up, down
+
+
+def run(dq, x, logits, w, up, down, bias):
+    """A projection, a mixture of experts on its result, and the projection's gradient."""
+    rows = dq.int8_quantize(x, 6.0, 16)
+    y = dq.int8_linear(rows, *w, bias, x.dtype)
+    z = dq.int8_moe(y[:8], logits, *up, *down, 2)
+    return rows.codes, y, z, dq.int8_linear_backward(y, *w)
+
+
+@pytest.mark.parametrize("M", [5, 21, 150])
+def test_together(dq, M):
+    """A layer as it is used, beside the operators that were there: the outlier columns of the
+    quantizer through int8_correction_prep, and the 8-bit product by hand."""
+    rng = np.random.default_rng(M)
+    K, N = 320, 144
+    (CB, SCB), up, down = layer(rng, dq, K, N)
+    x = rows_of(rng, M, K, "f16", 5)
+    bias = dev(rng.normal(size=N).astype(np.float32), torch.float16)
+    logits = dev(rng.normal(size=(min(M, 8), 6)).astype(np.float32))
+    codes, y, z, dx = run(dq, x, logits, (CB, SCB), up, down, bias)
+    rows = dq.int8_quantize(x, 6.0, 16)
+    L = rows.count.item()
+    assert 0 < L <= 16 and torch.equal(rows.codes, codes)
+    cols = rows.cols[:L].contiguous()
+    sub_a, sub_b = dq.int8_correction_prep(x, CB, SCB, cols)
+    assert torch.equal(sub_a, rows.outliers[:, :L])
+    by_hand = (host(codes) @ host(CB).T * host(rows.scales)[:, None] * host(SCB) / 127 ** 2
+               + host(sub_a) @ host(sub_b) + host(bias))
+    size = (np.abs(host(codes)) @ np.abs(host(CB)).T * host(rows.scales)[:, None] * host(SCB)
+            / 127 ** 2 + np.abs(host(sub_a)) @ np.abs(host(sub_b)) + np.abs(host(bias)))
+    # (sub_b is the weight in FP16, half a step of which is 2^-11)
+    close(y, by_hand, (2.0 ** -21 + 2.0 ** -11) * size + U["f16"] * np.abs(by_hand), M)
+    check_moe(dq, y[:8], logits, *(t.cpu().numpy() for t in up), *(t.cpu().numpy() for t in down),
+              2, True, "f16", M)
+    # the gradient against differences of the product in 64 bits, which is linear in x: along
+    # any d, (f(x + d) - f(x - d)) / 2 = <dX, d>.  A weight in FP16 is off by 2^-11 of it.
+    dy = y.double()
+    W = CB.double() * SCB.double()[:, None] / 127
+    f = lambda v: ((v @ W.T) * dy).sum(1)
+    for _ in range(4):
+        d = torch.randn(M, K, device="cuda", dtype=torch.float64)
+        d = d * (torch.rand(M, K, device="cuda") < 0.1)
+        want = (f(x.double() + d) - f(x.double() - d)) / 2
+        reach = ((dy.abs() @ W.abs()) * d.abs()).sum(1)
+        own = (dx.double().abs() * d.abs()).sum(1)
+        tol = reach * (2.0 ** -11 + (N / 16 + 4) * 2.0 ** -23) + own * 2.0 ** -11 + 1e-9 * reach
+        assert ((dx.double() * d).sum(1) - want).abs().le(tol).all()
+
+
+def test_gradient_of_codes_against_the_product(dq):
+    """The product's own differences: a step of one code moves Y by the column that dX sums."""
+    rng = np.random.default_rng(2)
+    M, K, N = 37, 64, 48
+    CB, SCB = (dev(a) for a in weight(rng, N, K))
+    codes = dev(rng.integers(-100, 101, (M, K)).astype(np.int8))
+    scales = torch.full((M,), 127.0, device="cuda")  # (a code's step is 1)
+    dy = rows_of(rng, M, N, "bf16")
+    dx = host(dq.int8_linear_backward(dy, CB, SCB))
+    for k in (0, 17, 63):
+        hi, lo = codes.clone(), codes.clone()
+        hi[:, k] += 16
+        lo[:, k] -= 16
+        step = (host(dq.int8_linear(dq.Int8Rows(hi, scales), CB, SCB, out_dtype=torch.float32))
+                - host(dq.int8_linear(dq.Int8Rows(lo, scales), CB, SCB,
+                                      out_dtype=torch.float32))) / 32
+        W = np.abs(host(CB) * host(SCB)[:, None] / 127)
+        size = np.abs(host(codes)) @ W.T + 16 * W[:, k]
+        reach = (np.abs(host(dy)) * size).sum(1)
+        # each Y is off by 2^-21 of its magnitudes; the weight in BF16 by 2^-8, dX by 2^-8
+        tol = (reach * (2.0 ** -21 + 2.0 ** -24) / 16 + (np.abs(host(dy)) @ W[:, k]) * (2.0 ** -8 + 2.0 ** -19)
+               + np.abs(dx[:, k]) * 2.0 ** -8)
+        assert (np.abs((host(dy) * step).sum(1) - dx[:, k]) <= tol).all()
+
+
+@pytest.mark.parametrize("M", [4, 24, 90])
+def test_graphs(dq, M):
+    """Two captured runs, replayed on two streams at once and in turn with eager calls, give
+    what eager calls give."""
+    rng = np.random.default_rng(M)
+    K, N = 320, 144
+    w, up, down = layer(rng, dq, K, N)
+    xs = [rows_of(rng, M, K, "bf16", 4) for _ in range(4)]
+    logits = [dev(rng.normal(size=(min(M, 8), 6)).astype(np.float32)) for _ in range(4)]
+    want = [run(dq, x, l, w, up, down, None) for x, l in zip(xs, logits)]
+    torch.cuda.synchronize()
+    graphs = []
+    for g in range(2):
+        x, l = xs[g].clone(), logits[g].clone()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            out = run(dq, x, l, w, up, down, None)
+        graphs.append((graph, x, l, out))
+    streams = [torch.cuda.Stream() for _ in graphs]
+    for turn in range(6):
+        for g, (graph, x, l, out) in enumerate(graphs):
+            at = (turn + g) % 4
+            with torch.cuda.stream(streams[g]):
+                x.copy_(xs[at])
+                l.copy_(logits[at])
+        torch.cuda.synchronize()
+        for g, (graph, *_) in enumerate(graphs):
+            with torch.cuda.stream(streams[g]):
+                graph.replay()
+        eager = run(dq, xs[3], logits[3], w, up, down, None)
+        torch.cuda.synchronize()
+        for g, (_, _, _, out) in enumerate(graphs):
+            for a, b in zip(out, want[(turn + g) % 4]):
+                assert torch.equal(a, b), (turn, g)
+        for a, b in zip(eager, want[3]):
+            assert torch.equal(a, b), turn
+
+
+@pytest.mark.parametrize("M", [4, 90])
+def test_threads_and_streams(dq, M):
+    """Four host threads, two to a stream, and a stream given by its handle."""
+    import threading
+    rng = np.random.default_rng(M)
+    K, N = 320, 144
+    w, up, down = layer(rng, dq, K, N)
+    xs = [rows_of(rng, M, K, "f16", 4) for _ in range(4)]
+    logits = [dev(rng.normal(size=(min(M, 8), 6)).astype(np.float32)) for _ in range(4)]
+    want = [run(dq, x, l, w, up, down, None) for x, l in zip(xs, logits)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    wrong = []
+
+    def work(i):
+        try:
+            with torch.cuda.stream(streams[i % 2]):
+                for turn in range(20):
+                    at = (i + turn) % 4
+                    got = run(dq, xs[at], logits[at], w, up, down, None)
+                    streams[i % 2].synchronize()
+                    if not all(torch.equal(a, b) for a, b in zip(got, want[at])):
+                        wrong.append((i, turn))
+        except Exception as e:  # noqa: BLE001
+            wrong.append((i, e))
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong
+    s = streams[0]
+    rows = dq.int8_quantize(xs[0], 6.0, 16, stream=s)
+    y = dq.int8_linear(rows, *w, out_dtype=torch.float16, stream=s)
+    dx = dq.int8_linear_backward(y, *w, stream=s)
+    s.synchronize()
+    assert torch.equal(y, want[0][1]) and torch.equal(dx, want[0][3])
+
+
+def test_repeated_expert_layer(dq):
+    """No atomic adds a value: a layer's results are the same each time."""
+    rng = np.random.default_rng(12)
+    T, H, I, E = 200, 128, 80, 7
+    w1, s1 = (dev(a) for a in weight(rng, E, 2 * I, H))
+    w2, s2 = (dev(a) for a in weight(rng, E, H, I))
+    x = rows_of(rng, T, H, "bf16")
+    logits = dev(rng.normal(size=(T, E)).astype(np.float32))
+    y = dq.int8_moe(x, logits, w1, s1, w2, s2, 3)
+    for _ in range(5):
+        assert torch.equal(y, dq.int8_moe(x, logits, w1, s1, w2, s2, 3))
+
+
+def test_refused_on_the_device(dq):
+    """What only a device's tensors show: shapes, types and strides that are refused before any
+    launch."""
+    rng = np.random.default_rng(13)
+    CB, SCB = (dev(a) for a in weight(rng, 24, 64))
+    rows = random_rows(dq, rng, 5, 64, 3)
+    E = dq.Dq4Error
+    with pytest.raises(E):  # K no multiple of 16
+        dq.int8_linear(dq.Int8Rows(rows.codes[:, :40].contiguous(), rows.scales),
+                       CB[:, :40].contiguous(), SCB)
+    with pytest.raises(E):  # codes off 16 bytes
+        off = torch.zeros(5 * 64 + 8, dtype=torch.int8, device="cuda")[8:].view(5, 64)
+        dq.int8_linear(dq.Int8Rows(off, rows.scales), CB, SCB)
+    with pytest.raises(E):  # a workspace off 256 bytes
+        many = random_rows(dq, rng, 60, 64, 0)
+        dq.int8_linear(many, CB, SCB,
+                       workspace=torch.zeros(1 << 22, dtype=torch.uint8, device="cuda")[16:])
+    with pytest.raises(ValueError):
+        dq.int8_linear(many, CB, SCB, workspace=torch.zeros(64, dtype=torch.uint8, device="cuda"))
+    for bad_call in (
+            lambda: dq.int8_linear(rows, CB.t(), SCB),
+            lambda: dq.int8_linear(rows, CB, SCB[:-1]),
+            lambda: dq.int8_linear(rows, CB, SCB, SCB[:-1].half()),
+            lambda: dq.int8_linear(rows._replace(cols=None), CB, SCB),
+            lambda: dq.int8_linear(rows._replace(outliers=rows.outliers[:, 1:]), CB, SCB),
+            lambda: dq.int8_linear(rows, CB, SCB, Y=torch.empty(5, 48, device="cuda")[:, ::2]),
+            lambda: dq.int8_quantize(torch.zeros(4, 8, device="cuda").half().t()),
+            lambda: dq.int8_quantize(torch.zeros(4, 8, device="cuda").half(), 6.0, 129),
+            lambda: dq.int8_linear_backward(torch.zeros(5, 23, device="cuda").half(), CB, SCB)):
+        with pytest.raises(ValueError):
+            bad_call()
+    for bad_call in (lambda: dq.int8_linear(rows, CB.half(), SCB),
+                     lambda: dq.int8_linear(rows, CB, SCB, out_dtype=torch.float64),
+                     lambda: dq.int8_linear(rows, CB, SCB, SCB),
+                     lambda: dq.int8_quantize(torch.zeros(4, 8, device="cuda")),
+                     lambda: dq.int8_linear_backward(torch.zeros(5, 24, device="cuda"), CB, SCB)):
+        with pytest.raises(TypeError):
+            bad_call()
+    with pytest.raises(E):  # N no multiple of 8
+        dq.int8_linear_backward(torch.zeros(5, 20, device="cuda").half(), CB[:20], SCB[:20])
+    w1, s1 = (dev(a) for a in weight(rng, 3, 32, 48))
+    w2, s2 = (dev(a) for a in weight(rng, 3, 48, 16))
+    x, logits = rows_of(rng, 4, 48, "f16"), torch.zeros(4, 3, device="cuda")
+    for bad_call in (lambda: dq.int8_moe(x, logits, w1, s1, w2, s2, 4),
+                     lambda: dq.int8_moe(x, logits, w1, s1, w2, s2, 0),
+                     lambda: dq.int8_moe(x, logits[:, :2], w1, s1, w2, s2, 2),
+                     lambda: dq.int8_moe(x, logits, w1[:, :30], s1, w2, s2, 2),
+                     lambda: dq.int8_moe(x[:, :32], logits, w1, s1, w2, s2, 2)):
+        with pytest.raises(ValueError):
+            bad_call()
+    big = torch.zeros(257, 48, device="cuda").half()
+    with pytest.raises(E):  # more tokens than the layer is for
+        dq.int8_moe(big, torch.zeros(257, 3, device="cuda"), w1, s1, w2, s2, 2)
+    # by keyword, every argument
+    dq.int8_moe(X=x, logits=logits, w1=w1, s1=s1, w2=w2, s2=s2, top_k=2)
+    dq.int8_linear_backward(dY=torch.zeros(5, 24, device="cuda").half(), CB=CB, SCB=SCB)
