@@ -248,12 +248,16 @@ __global__ void __launch_bounds__(kRowThreads) int8_outliers_kernel(const Outlie
       }
     }
   }
-  // Seldom: outlier columns past the last that is kept.  Their outliers' codes end at +-127 (they
-  // are above the scale).
+  // Outlier columns past the last that is kept: their outliers' codes end at +-127 (they are above
+  // the scale).  A warp takes 32 columns, a lane one of them.
   if (found > p.max_cols) {
-    for (int64_t col = s_cols[p.max_cols - 1] + 1; col < p.K; ++col) {
-      if (!(marks_of(col >> 5) >> (col & 31) & 1)) continue;
-      for (int r = t; r < rows; r += kRowThreads) {
+    const int64_t after = s_cols[p.max_cols - 1] + 1;
+    for (int64_t w = after / 32 + warp; w < words; w += kRowThreads / 32) {
+      const uint32_t copy = lane < kCopies ? load_global(p.marks + lane * words + w) : 0;
+      const int64_t col = w * 32 + lane;
+      if (!(__reduce_or_sync(kAllLanes, copy) >> lane & 1) || col < after) continue;
+#pragma unroll 4
+      for (int r = 0; r < rows; ++r) {
         const uint32_t b = load_global(p.X + (row0 + r) * p.row_stride + col);
         if ((b & 0x7FFFu) >= p.loud && load_global(p.scales + row0 + r) > 0.f)
           p.codes[(row0 + r) * p.K + col] = b & 0x8000u ? -127 : 127;
