@@ -17,6 +17,15 @@
 //                 copies the weight's codes, the warp that copies the activations
 // Waits are bounded; one that runs out counts into *bad, raises a flag of the CTA, and every
 // role lets its copies and MMAs finish and ends.
+//
+// What bounds it: the MMAs, 128 x BX x 16, take about 105 cycles at BX 64 and 128 and 169 at 256,
+// where 32, 64 and 128 would be the rate of the tensor cores: with A in TMEM the smaller ones are
+// no faster, and the largest shares the shared memory (activations in and out, codes in and out:
+// 160 of 181 cycles' bandwidth when it was measured) with the producers.  8191 rows through
+// 4096 x 14336: 625 to 650 us, 0.77 to 0.80 of the measured rate of the GPU; the gradient of 2047
+// rows through 11008 x 4096 146 us, 0.65: its producers' instructions, three packed ones for two
+// values.  (Pairs of CTAs with tiles of 256 x 256, the weight's values in TMEM or in shared
+// memory: 790 to 824 us.)
 #include "int8_gemm.cuh"
 
 namespace dq4d {
@@ -634,8 +643,8 @@ __global__ void __launch_bounds__(Gemm<BX, kBack>::kThreads, 1)
       const int64_t cta0 = whole ? 0 : cta_of(it.tile * stages);
       const int64_t cta1 = whole ? 0 : cta_of((it.tile + 1) * stages - 1);
       const int sharers = int(cta1 - cta0) + 1, own = int(blockIdx.x - cta0);
-      // The CTA's last item: the rings are idle, and its part can stay in TMEM if the others are there,
-      // as they mostly are: they are the first items of their CTAs.
+      // The CTA's last item: the rings are idle, and its part can stay in TMEM if the others are
+      // there, as they mostly are: they are the first items of their CTAs.
       const bool over = !whole && walk >= walk1;
       bool stays = false;
       if (over) {
@@ -772,21 +781,24 @@ struct RowArgs {
   int* bad;
 };
 
-// A row's FP16 values are its codes, times the row's unit u = scale / 127.  An outlier x takes
-// the place of its code as x / u, in two FP16 terms, the second in a column of its own past K,
-// where the weight's column stands again: the CTAs past row_ctas gather those columns (gathered
-// in the product itself, for each tile again, 4096 rows with 13 such columns through 4096 x 11008
-// took 293 us; so 274).  FP16 ends at 65504: where an outlier is above 2^15 u, the unit is 2^-15 of
-// it, and codes are rounded to FP16 with what they are in it.
+// A row's FP16 values are its codes, times the row's unit u = scale / 127.  An outlier x takes the
+// place of its code as x / u, in two FP16 terms, the second in a column of its own past K, where
+// the weight's column stands again: the CTAs past row_ctas gather those columns (gathered in the
+// product itself, for each tile again, 4096 rows with 13 such columns through 4096 x 11008 took 293
+// us; so 274).  FP16 ends at 65504: where an outlier is above 2^15 u, the unit is 2^-15 of it, and
+// codes are rounded to FP16 with what they are in it.
+// A warp takes 512 values of a row, 16 a lane (so spread, 512 rows through 4096 x 4096 take 22.8
+// us; 2048 values a warp, loaded at once, 25.4; with outlier columns, which each part looks up
+// again, 512 rows through 4096 x 11008 55.5 and 53).
+constexpr int kRowPart = 512;
 __global__ void __launch_bounds__(256) int8_rows_kernel(const RowArgs p) {
   __shared__ int64_t s_most[8];
-  __shared__ int s_col[256];
-  __shared__ uint32_t s_top[8];
+  __shared__ int s_col[256];  // of entry t, -1 if it is not used
   wait_for_stream();
   asm volatile("griddepcontrol.launch_dependents;");
-  const int t = threadIdx.x;
-  int64_t col = -1;  // of entry t, if it is used
+  const int t = threadIdx.x, lane = t & 31;
   if (p.L > 0) {
+    int64_t col = -1;
     // used: in range and above all before it (the largest so far, by warps and then over them)
     const int64_t c = t < p.L ? load_global(p.cols + t) : -1;
     int64_t run = c < p.K ? c : -1;
@@ -805,9 +817,9 @@ __global__ void __launch_bounds__(256) int8_rows_kernel(const RowArgs p) {
     s_col[t] = int(col);
     if (blockIdx.x == 0 && wrong && p.bad) atomicAdd(p.bad, 1);
   }
+  if (p.L > 0) __syncthreads();
   const int64_t codes_end = p.codes_end;
   if (blockIdx.x >= p.row_ctas) {
-    __syncthreads();
     const int64_t extra = p.width - codes_end, pieces = p.N * extra / 16;
     const int64_t step = (gridDim.x - p.row_ctas) * 256;
     for (int64_t i = (blockIdx.x - p.row_ctas) * 256 + t; i < pieces; i += step) {
@@ -825,15 +837,24 @@ __global__ void __launch_bounds__(256) int8_rows_kernel(const RowArgs p) {
     }
     return;
   }
-  for (int64_t row = blockIdx.x; row < p.M; row += p.row_ctas) {
-    float unit = load_global(p.scales + row) * kRecip127, ratio = 1.f, x = 0.f;
+  const int64_t segs = (codes_end + kRowPart - 1) / kRowPart, parts = p.M * segs;
+  for (int64_t part = blockIdx.x * 8 + t / 32; part < parts; part += p.row_ctas * 8) {
+    const int64_t row = part / segs, k0 = (part - row * segs) * kRowPart;
+    const int8_t* from = p.codes + row * p.K;
+    uint16_t* to = p.X + row * p.width;
+    const int64_t k = k0 + lane * 16;
+    uint4 c = make_uint4(0, 0, 0, 0);
+    if (k < p.K) c = load_global(reinterpret_cast<const uint4*>(from + k));
+    float unit = load_global(p.scales + row) * kRecip127, ratio = 1.f, x[kMaxOutliers / 32] = {};
     if (p.L > 0) {
-      if (col >= 0) x = load_16(p.outliers, row * p.L + t, p.bf16);
-      uint32_t top = __reduce_max_sync(kAllLanes, __float_as_uint(x) & 0x7FFFFFFFu);
-      __syncthreads();  // (the last row's has been read)
-      if ((t & 31) == 0) s_top[t >> 5] = top;
-      __syncthreads();
-      for (int w = 0; w < 8; ++w) top = max(top, s_top[w]);
+      uint32_t top = 0;
+#pragma unroll
+      for (int j = 0; j < kMaxOutliers / 32; ++j) {
+        const int l = 32 * j + lane;
+        if (s_col[l] >= 0) x[j] = load_16(p.outliers, row * p.L + l, p.bf16);
+        top = max(top, __float_as_uint(x[j]) & 0x7FFFFFFFu);
+      }
+      top = __reduce_max_sync(kAllLanes, top);
       const float own = unit;
       if (top < 0x7F800000u) {
         unit = fmaxf(fmaxf(unit, __uint_as_float(top) * 3.0517578125e-05f), 7.888609052210118e-31f);
@@ -843,11 +864,7 @@ __global__ void __launch_bounds__(256) int8_rows_kernel(const RowArgs p) {
         unit = __uint_as_float(0x7FC00000u);
       }
     }
-    uint16_t* to = p.X + row * p.width;
-    const int8_t* from = p.codes + row * p.K;
-    for (int64_t k = t * 16; k < codes_end; k += 256 * 16) {
-      uint4 c = make_uint4(0, 0, 0, 0);
-      if (k < p.K) c = load_global(reinterpret_cast<const uint4*>(from + k));
+    if (k < codes_end) {
       const uint32_t* w = reinterpret_cast<const uint32_t*>(&c);
       uint32_t o[8];
 #pragma unroll
@@ -864,14 +881,17 @@ __global__ void __launch_bounds__(256) int8_rows_kernel(const RowArgs p) {
       y[0] = make_uint4(o[0], o[1], o[2], o[3]);
       y[1] = make_uint4(o[4], o[5], o[6], o[7]);
     }
-    if (t == 0) p.units[row] = unit;
+    if (lane == 0 && k0 == 0) p.units[row] = unit;
     if (p.L > 0) {
-      __syncthreads();  // the codes are there
-      if (codes_end + t < p.width) {
-        const float v = col >= 0 ? __fdiv_rn(x, unit) : 0.f;
+      __syncwarp();  // the codes are there
+#pragma unroll
+      for (int j = 0; j < kMaxOutliers / 32; ++j) {
+        const int l = 32 * j + lane, col = s_col[l];
+        const float v = col >= 0 ? __fdiv_rn(x[j], unit) : 0.f;
         const __half high = __float2half_rn(v);
-        if (col >= 0) to[col] = __half_as_ushort(high);
-        to[codes_end + t] = __half_as_ushort(__float2half_rn(v - __half2float(high)));
+        if (col >= k0 && col < k0 + kRowPart) to[col] = __half_as_ushort(high);
+        if (k0 == 0 && codes_end + l < p.width)
+          to[codes_end + l] = __half_as_ushort(__float2half_rn(v - __half2float(high)));
       }
     }
   }
@@ -995,7 +1015,8 @@ int launch_int8_gemm(const Int8Linear& a, int dev, int sms, void* workspace, cud
   r.K = a.K;
   r.width = width;
   r.codes_end = int64_t(code_steps(a.K, a.L)) * kStep;
-  r.row_ctas = a.M < 8 * sms ? a.M : 8 * sms;
+  const int64_t parts = (r.codes_end + kRowPart - 1) / kRowPart * a.M;
+  r.row_ctas = (parts + 7) / 8 < 8 * sms ? (parts + 7) / 8 : 8 * sms;
   r.CB = a.CB;
   r.N = a.N;
   r.cols = a.cols;
