@@ -1,5 +1,6 @@
 // The gradient of the 8-bit product's input, dq4_int8_linear_backward (dq4_int8.h): the entry
-// point.  The kernel is the product's (int8_gemm.cu), the weight's columns its rows.
+// point.  The kernel is the product's (int8_gemm.cu, with what it measured), the weight's columns
+// its rows: the sum runs over the weight's rows, whose scales go into its 16-bit values.
 #include "int8_gemm.cuh"
 
 using namespace dq4d;

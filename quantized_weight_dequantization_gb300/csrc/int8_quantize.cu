@@ -9,6 +9,9 @@
 // and 16384 x 1024 with 5 such columns took 31 to 37 us with a single copy.
 // The maximum is taken on the bits of |x|, two values an instruction: for values that are not
 // negative the order of the bits is that of the numbers, infinity and NaN last.
+//
+// 2048 x 14336: 14 us, of which the bytes take 13.0 (0.93 of the copy rate); with 21 outlier
+// columns 21.7, the second launch; 1 x 4096 1.5 us, the launch.
 #include "int8.cuh"
 
 namespace dq4d {
