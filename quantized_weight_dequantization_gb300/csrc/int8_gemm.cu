@@ -788,13 +788,11 @@ struct RowArgs {
 // us; so 274).  FP16 ends at 65504: where an outlier is above 2^15 u, the unit is 2^-15 of it, and
 // codes are rounded to FP16 with what they are in it.
 // A warp takes 512 values of a row, 16 a lane (so spread, 512 rows through 4096 x 4096 take 22.8
-// us; 2048 values a warp, loaded at once, 25.4; with outlier columns, which each part looks up
-// again, 512 rows through 4096 x 11008 55.5 and 53).
+// us; 2048 values a warp, loaded at once, 25.4).
 constexpr int kRowPart = 512;
 __global__ void __launch_bounds__(256) int8_rows_kernel(const RowArgs p) {
   __shared__ int64_t s_most[8];
   __shared__ int s_col[256];  // of entry t, -1 if it is not used
-  wait_for_stream();
   asm volatile("griddepcontrol.launch_dependents;");
   const int t = threadIdx.x, lane = t & 31;
   if (p.L > 0) {
@@ -1029,9 +1027,10 @@ int launch_int8_gemm(const Int8Linear& a, int dev, int sms, void* workspace, cud
   r.bad = a.bad;
   const int64_t gathers = (a.N * extra / 16 + 255) / 256;
   const int64_t row_kernel_ctas = r.row_ctas + (gathers < 4 * sms ? gathers : 4 * sms);
-  if (const int st = launch_ordered(int8_rows_kernel, dim3(unsigned(row_kernel_ctas)), 256, 0,
-                                    stream, r))
-    return st;
+  // In full stream order: launched early, its CTAs gather on the SMs that the kernel before leaves
+  // first (512 rows with 13 outlier columns through 4096 x 11008: 55.4 us, so 47.5).
+  int8_rows_kernel<<<unsigned(row_kernel_ctas), 256, 0, stream>>>(r);
+  if (const cudaError_t e = cudaGetLastError()) return fail_cuda(DQ4_ERR_LAUNCH, e);
   GemmArgs p = {};
   p.lanes = p.N = a.N;
   p.rows = a.M;
