@@ -246,25 +246,34 @@ inline bool aligned(const void* p, uintptr_t to) { return reinterpret_cast<uintp
 // Launch on `stream` with programmatic stream serialization: the grid may be scheduled
 // while the kernel before it drains, and waits for it (wait_for_stream) before it touches
 // memory.
+// cluster: CTAs of a cluster, 1 for none.
 template <typename... KArgs, typename... Actual>
-int launch_ordered(void (*kernel)(KArgs...), dim3 grid, int threads, size_t smem,
-                   cudaStream_t stream, Actual&&... args) {
+int launch_clusters(void (*kernel)(KArgs...), dim3 grid, int threads, size_t smem,
+                    cudaStream_t stream, int cluster, Actual&&... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = unsigned(cluster);
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
   const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, std::forward<Actual>(args)...);
   if (e != cudaSuccess) {
     cudaGetLastError();
     return fail_cuda(DQ4_ERR_LAUNCH, e);
   }
   return DQ4_OK;
+}
+template <typename... KArgs, typename... Actual>
+int launch_ordered(void (*kernel)(KArgs...), dim3 grid, int threads, size_t smem,
+                   cudaStream_t stream, Actual&&... args) {
+  return launch_clusters(kernel, grid, threads, smem, stream, 1, std::forward<Actual>(args)...);
 }
 
 // Let `kernel` have `bytes` of dynamic shared memory, once for each device (bit dev of

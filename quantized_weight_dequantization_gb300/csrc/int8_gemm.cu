@@ -10,8 +10,10 @@
 // A CTA takes items (a tile, or a part of a tile's sum where there are few) in turn:
 //   warps 0..7    two groups that take alternate stages: codes from shared memory to 16-bit values
 //                 in TMEM, a thread a lane
-//   warps 8..15   read a finished tile out of TMEM, scale, store (or leave a part of the sum; the
-//                 last part's CTA adds them all, in their order)
+//   warps 8..15   read a finished tile out of TMEM, scale, store.  A part of a tile's sum is left
+//                 in shared memory for the cluster, whose CTAs each add and store a share of the
+//                 columns; or in the workspace, for the last part's CTA, which adds them all.  The
+//                 order of the parts is that of the sum, so that the same call gives the same bits
 //   then          one or two warps that issue the MMAs (alternate stages, accumulators of their
 //                 own: issuing takes a thread about 120 cycles, whatever BX is), the warp that
 //                 copies the weight's codes, the warp that copies the activations
@@ -58,7 +60,7 @@ struct Gemm {
   // where parts of a tile are joined: pieces of 32 rows (both readers' halves) in the idle rings
   static constexpr int kPiece = 2 * 32 * kTileW * 4;
   static constexpr int kPieces = kBarsAt / kPiece;
-  static constexpr int kBars = 2 * kSlots + 2 * kRawSlots + 2 * kRing + 2 * kBuffers + 1 + kPieces;
+  static constexpr int kBars = 2 * kSlots + 2 * kRawSlots + 2 * kRing + 2 * kBuffers + 2 + kPieces;
   static constexpr int kBytes = kBarsAt + 8 * kBars + 1024;  // + alignment slack
   static constexpr int kStatic = kBack ? 16 * kStage + 64 : 4 * BX + 64;
   static_assert(kBytes + kStatic <= 227 * 1024, "shared memory budget");
@@ -72,6 +74,7 @@ struct GemmArgs {
   int tiles_x;           // tiles along the activations
   int64_t tiles;
   int64_t units;         // tiles * stages, if CTAs take equal runs of them; 0: whole tiles in turn
+  int cluster;           // CTAs that share a tile's stages, and its columns at the end; 1: none
   const float* SCB;
   int64_t N;             // weight rows
   const float* row_units;  // of the activation rows
@@ -102,6 +105,30 @@ __device__ __forceinline__ int load_acquire(const int* p) {
   int v;
   asm volatile("ld.acquire.gpu.global.b32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
   return v;
+}
+// Clusters: the place in CTA r's shared memory of one in this CTA's; an arrival there, after what
+// the warp wrote; what has been written before a phase that has completed; a read; all threads.
+__device__ __forceinline__ uint32_t of_cta(uint32_t addr, int r) {
+  uint32_t there;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(there) : "r"(addr), "r"(r));
+  return there;
+}
+__device__ __forceinline__ void arrive_cluster(uint32_t bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];"
+               :: "r"(bar) : "memory");
+}
+__device__ __forceinline__ void see_cluster(uint32_t bar, uint32_t parity) {
+  asm volatile(
+      "{\n.reg .pred p;\nmbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 p, [%0], %1;\n}"
+      :: "r"(bar), "r"(parity) : "memory");
+}
+__device__ __forceinline__ void load_cluster(uint32_t addr, uint32_t* v) {
+  asm volatile("ld.shared::cluster.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void sync_cluster() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;"
+               ::: "memory");
 }
 // Four 8 x 8 matrices of 16-bit elements, transposed; a thread gives the address of a row.
 __device__ __forceinline__ void load_transposed(uint32_t addr, uint32_t* m) {
@@ -178,7 +205,8 @@ __global__ void __launch_bounds__(Gemm<BX, kBack>::kThreads, 1)
   };
   auto acc_empty = [&](int b) { return acc_full(kBuffers + b); };
   const uint32_t all_done = acc_full(2 * kBuffers);
-  auto piece_full = [&](int s) { return acc_full(2 * kBuffers + 1 + s); };
+  const uint32_t shared = acc_full(2 * kBuffers + 1);  // the cluster's accumulators can be read
+  auto piece_full = [&](int s) { return acc_full(2 * kBuffers + 2 + s); };
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   volatile int* aborted = &s_abort;
   auto fail = [&] {
@@ -209,6 +237,7 @@ __global__ void __launch_bounds__(Gemm<BX, kBack>::kThreads, 1)
         mbar_init(acc_empty(b), kReaders);
       }
       mbar_init(all_done, kIssuers);
+      mbar_init(shared, kReaders * p.cluster);
       for (int s = 0; s < S::kPieces; ++s) mbar_init(piece_full(s), 1);
       *aborted = 0;
       asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -220,6 +249,7 @@ __global__ void __launch_bounds__(Gemm<BX, kBack>::kThreads, 1)
   asm volatile("griddepcontrol.launch_dependents;");
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
   __syncthreads();
+  if (p.cluster > 1) sync_cluster();  // (the other CTAs' barriers)
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
   const uint32_t tmem = s_tmem;
 
@@ -234,8 +264,9 @@ __global__ void __launch_bounds__(Gemm<BX, kBack>::kThreads, 1)
   const int64_t ctas = gridDim.x;
   auto begin_of = [&](int64_t cta) { return cta * p.units / ctas; };
   auto cta_of = [&](int64_t u) { return ((u + 1) * ctas - 1) / p.units; };
-  const int64_t walk0 = p.units ? begin_of(blockIdx.x) : blockIdx.x;
-  const int64_t walk1 = p.units ? begin_of(blockIdx.x + 1) : p.tiles;
+  const int rank = int(blockIdx.x % p.cluster);  // of the cluster
+  const int64_t walk0 = p.units ? begin_of(blockIdx.x) : blockIdx.x / p.cluster;
+  const int64_t walk1 = p.units ? begin_of(blockIdx.x + 1) : p.cluster > 1 ? walk0 + 1 : p.tiles;
   auto next_item = [&](int64_t& at, Item& it) {
     if (at >= walk1) return false;
     it.tile = at;
@@ -247,6 +278,8 @@ __global__ void __launch_bounds__(Gemm<BX, kBack>::kThreads, 1)
       it.end = int(min(int64_t(stages), it.begin + walk1 - at));
       at += it.end - it.begin;
     } else {
+      it.begin = rank * stages / p.cluster;
+      it.end = (rank + 1) * stages / p.cluster;
       at += ctas;
     }
     const int64_t tw = it.tile / p.tiles_x;
@@ -528,14 +561,15 @@ __global__ void __launch_bounds__(Gemm<BX, kBack>::kThreads, 1)
     for (int64_t walk = walk0; next_item(walk, it); ++turn) {
       const int buffer = turn % kBuffers;
       const int64_t n = it.lane0 + column, m0 = it.row0 + half * kHalf;
-      const int rank = tid - 32 * kProducers;
+      const int reader = tid - 32 * kProducers;
       float scale = 1.f, bias = 0.f, unit = 0.f;
       if constexpr (!kBack) {
         if (n < p.lanes) {
           scale = load_global(p.SCB + n) * kRecip127;
           if (p.bias) bias = load_any(p.bias, n, p.out_dtype);
         }
-        if (rank < BX && it.row0 + rank < p.rows) unit = load_global(p.row_units + it.row0 + rank);
+        if (reader < BX && it.row0 + reader < p.rows)
+          unit = load_global(p.row_units + it.row0 + reader);
       }
       const bool ok = !*aborted && mbar_wait(acc_full(buffer), uint32_t(turn / kBuffers) & 1u) &&
                       !*aborted;
@@ -544,7 +578,7 @@ __global__ void __launch_bounds__(Gemm<BX, kBack>::kThreads, 1)
         break;
       }
       if constexpr (!kBack) {
-        if (rank < BX) s_unit[rank] = unit;
+        if (reader < BX) s_unit[reader] = unit;
         bar_readers();
       }
       asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
@@ -569,13 +603,13 @@ __global__ void __launch_bounds__(Gemm<BX, kBack>::kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(acc_empty(buffer));
       };
-      // 32 columns (activation rows) finished, and in the output's type, two in a word
-      auto finish = [&](uint32_t (&v)[32], int c) {
+      // Columns (activation rows) from `col` on: finished, in the output's type, two in a word, and
+      // stored (rows of them that are there: none for a lane past the last).
+      auto finish = [&](auto& v, int col) {
         if constexpr (!kBack) {
-          const float* unit = s_unit + half * kHalf + 32 * c;
 #pragma unroll
-          for (int j = 0; j < 32; j += 4) {
-            const float4 u = *reinterpret_cast<const float4*>(unit + j);
+          for (int j = 0; j < int(sizeof(v) / 4); j += 4) {
+            const float4 u = *reinterpret_cast<const float4*>(s_unit + col + j);
             const float by[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
             for (int k = 0; k < 4; ++k)
@@ -583,39 +617,95 @@ __global__ void __launch_bounds__(Gemm<BX, kBack>::kThreads, 1)
           }
         }
       };
-      auto pack = [&](uint32_t (&v)[32], int c, uint32_t* to) {
-        finish(v, c);
+      auto pack = [&](auto& v, int col, uint32_t* to) {
+        finish(v, col);
 #pragma unroll
-        for (int j = 0; j < 32; j += 2) {
+        for (int j = 0; j < int(sizeof(v) / 4); j += 2) {
           const float a = __uint_as_float(v[j]), b = __uint_as_float(v[j + 1]);
           to[j / 2] = bf16 ? pack2<DQ4_OUT_BF16>(a, b) : pack2<DQ4_OUT_F16>(a, b);
         }
       };
-      // (rows of the 32 that are there; none for a lane past the last)
-      auto rows_at = [&](int c) {
-        return n < p.lanes ? int(min(int64_t(32), p.rows - m0 - 32 * c)) : 0;
+      auto rows_at = [&](int col, int most) {
+        return n < p.lanes ? int(min(int64_t(most), p.rows - it.row0 - col)) : 0;
       };
-      auto store = [&](const uint32_t* from, int c) {
-        const int rows = rows_at(c);
+      auto store = [&](auto& from, int col, int at) {  // (words from `at` on, for 32 columns or all)
+        constexpr int kWords = int(sizeof(from) / 4) < 16 ? int(sizeof(from) / 4) : 16;
+        const int rows = rows_at(col, 2 * kWords);
         if (pairs) {
           const int odd = column & 1;
-          uint16_t* to = static_cast<uint16_t*>(p.out) + (m0 + 32 * c + odd) * p.lanes + n - odd;
+          uint16_t* to = static_cast<uint16_t*>(p.out) + (it.row0 + col + odd) * p.lanes + n - odd;
 #pragma unroll
-          for (int j = 0; j < 16; ++j, to += 2 * p.lanes) {
-            const uint32_t other = __shfl_xor_sync(kAllLanes, from[j], kNext);
-            const uint32_t v = odd ? __byte_perm(other, from[j], 0x7632)
-                                   : __byte_perm(from[j], other, 0x5410);
+          for (int j = 0; j < kWords; ++j, to += 2 * p.lanes) {
+            const uint32_t other = __shfl_xor_sync(kAllLanes, from[at + j], kNext);
+            const uint32_t v = odd ? __byte_perm(other, from[at + j], 0x7632)
+                                   : __byte_perm(from[at + j], other, 0x5410);
             if (2 * j + odd < rows) *reinterpret_cast<uint32_t*>(to) = v;
           }
         } else {
-          uint16_t* to = static_cast<uint16_t*>(p.out) + (m0 + 32 * c) * p.lanes + n;
+          uint16_t* to = static_cast<uint16_t*>(p.out) + (it.row0 + col) * p.lanes + n;
 #pragma unroll
-          for (int j = 0; j < 16; ++j, to += 2 * p.lanes) {
-            if (2 * j < rows) to[0] = uint16_t(from[j]);
-            if (2 * j + 1 < rows) to[p.lanes] = uint16_t(from[j] >> 16);
+          for (int j = 0; j < kWords; ++j, to += 2 * p.lanes) {
+            if (2 * j < rows) to[0] = uint16_t(from[at + j]);
+            if (2 * j + 1 < rows) to[p.lanes] = uint16_t(from[at + j] >> 16);
           }
         }
       };
+      auto put = [&](auto& v, int col) {
+        constexpr int kColumns = int(sizeof(v) / 4);
+        if (f32) {
+          finish(v, col);
+          const int rows = rows_at(col, kColumns);
+          float* to = static_cast<float*>(p.out) + (it.row0 + col) * p.lanes + n;
+#pragma unroll
+          for (int j = 0; j < kColumns; ++j, to += p.lanes)
+            if (j < rows) *to = __uint_as_float(v[j]);
+        } else {
+          uint32_t keep[kColumns / 2];
+          pack(v, col, keep);
+          store(keep, col, 0);
+        }
+      };
+      if (p.cluster > 1) {
+        // The CTA's only item: its accumulator goes into its rings, which are idle.  Each CTA then
+        // adds and stores an equal share of the columns, eight at a time.
+        uint32_t to = sbase + ((half * (kHalf / 4)) * kTileW + quad * 32 + lane) * 16;
+#pragma unroll 1
+        for (int c = 0; c < kChunks; ++c) {
+          uint32_t v[32];
+          read(c, v);
+#pragma unroll
+          for (int j = 0; j < 8; ++j, to += kTileW * 16)
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};"
+                         :: "r"(to), "r"(v[4 * j]), "r"(v[4 * j + 1]), "r"(v[4 * j + 2]),
+                            "r"(v[4 * j + 3]) : "memory");
+        }
+        __syncwarp();
+        if (lane < p.cluster) arrive_cluster(of_cta(shared, lane));
+        const bool there = mbar_wait(shared, 0) && !*aborted;
+        see_cluster(shared, 0);
+        if (!__all_sync(kAllLanes, there)) {
+          if (lane == 0 && !*aborted) fail();
+          break;
+        }
+        const int each = BX / p.cluster;
+#pragma unroll 1
+        for (int col = rank * each + half * 8; col < (rank + 1) * each; col += 16) {
+          const uint32_t from = sbase + (col / 4 * kTileW + quad * 32 + lane) * 16;
+          uint32_t v[8];
+          float sum[8] = {};
+#pragma unroll 1
+          for (int r = 0; r < p.cluster; ++r) {
+            const uint32_t there = of_cta(from, r);
+            load_cluster(there, v);
+            load_cluster(there + kTileW * 16, v + 4);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) sum[j] += __uint_as_float(v[j]);
+          }
+          memcpy(v, sum, sizeof(v));
+          put(v, col);
+        }
+        break;
+      }
       const bool whole = it.begin == 0 && it.end == stages;
       if (whole && !f32) {
         // all of the tile to registers, so that the next one can start, then the stores
@@ -624,11 +714,11 @@ __global__ void __launch_bounds__(Gemm<BX, kBack>::kThreads, 1)
         for (int c = 0; c < kChunks; ++c) {
           uint32_t v[32];
           read(c, v);
-          pack(v, c, keep + 16 * c);
+          pack(v, half * kHalf + 32 * c, keep + 16 * c);
         }
         release();
 #pragma unroll
-        for (int c = 0; c < kChunks; ++c) store(keep + 16 * c, c);
+        for (int c = 0; c < kChunks; ++c) store(keep, half * kHalf + 32 * c, 16 * c);
         continue;
       }
       // (What follows runs once or twice in a CTA: loops, as code that is fetched for the first
@@ -736,18 +826,7 @@ __global__ void __launch_bounds__(Gemm<BX, kBack>::kThreads, 1)
             if (warp == kProducers) copy(c + depth);
           }
         }
-        if (f32) {
-          finish(v, c);
-          const int rows = rows_at(c);
-          float* to = static_cast<float*>(p.out) + (m0 + 32 * c) * p.lanes + n;
-#pragma unroll
-          for (int j = 0; j < 32; ++j, to += p.lanes)
-            if (j < rows) *to = __uint_as_float(v[j]);
-        } else {
-          uint32_t keep[16];
-          pack(v, c, keep);
-          store(keep, c);
-        }
+        put(v, half * kHalf + 32 * c);
       }
       if (whole) release();
       if (!here && lane == 0) fail();
@@ -755,6 +834,7 @@ __global__ void __launch_bounds__(Gemm<BX, kBack>::kThreads, 1)
   }
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
   __syncthreads();
+  if (p.cluster > 1) sync_cluster();  // (nothing of this CTA is read any more)
   if (warp == kMmaWarp) {
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;"
@@ -902,16 +982,19 @@ struct Plan {
   int bx, stages;
   int64_t tiles_x, tiles;
   int ctas;
-  bool split;  // equal runs of stages, else whole tiles
+  bool split;   // equal runs of stages, else whole tiles,
+  int cluster;  // by so many CTAs each
 };
 
-// The tile's width, and whether CTAs take whole tiles or equal runs of stages, by the estimated
-// time in cycles, from measured ones: a stage takes 840, 890 and 1350 at BX 64, 128 and 256 (of 8
-// MMAs; the gradient's 1270, 1310 and 1600), the end of a tile 1500 where its accumulator is the
-// only one.  Runs cost 12000 more, the parts' writing, counting and joining, and a part's bytes by
+// The tile's width, and whether CTAs take whole tiles, a tile by clusters of 2, 4 or 8, or equal
+// runs of stages over all tiles, by the estimated time in cycles, from measured ones: a stage takes
+// 840, 890 and 1350 at BX 64, 128 and 256 (of 8 MMAs; the gradient's 1270, 1310 and 1600), the end
+// of a tile 1500 where its accumulator is the only one.  A cluster's exchange costs 2500, 300 a CTA
+// and 40 a column; runs cost 12000, the parts' writing, counting and joining, and a part's bytes by
 // the CTAs that share a tile, which are more, and have no whole tile, where a run is shorter than a
-// tile.  In us, whole / runs: 64 rows through 4096 x 11008 19.9 / 22, through 4096 x 4096
-// 18.4 / 16.2, 14336 to 4096 55 / 28; 512 through 4096 x 11008, 256 wide, 56 / 45.
+// tile.  In us, whole / clusters / runs: 64 rows through 4096 x 11008 20.4 / - / 21.3, through 4096
+// x 4096 19.0 / 12.1 / 15.7, 14336 to 4096 54 / 22.4 / 24.8; 512 through 4096 x 11008, 256 wide, 56
+// / - / 44.5; 256 rows' gradient through 11008 x 4096, 256 wide, 76 / 29.6 / 38.5.
 Plan plan_gemm(int64_t lanes, int64_t rows, int steps, bool back, int sms) {
   Plan best = {};
   double best_cost = 1e300;
@@ -925,7 +1008,16 @@ Plan plan_gemm(int64_t lanes, int64_t rows, int steps, bool back, int sms) {
     double cost = double((tiles + sms - 1) / sms) * (stages * stage + end);
     if (cost < best_cost) {
       best_cost = cost;
-      best = {bx, stages, tiles_x, tiles, int(tiles < sms ? tiles : sms), false};
+      best = {bx, stages, tiles_x, tiles, int(tiles < sms ? tiles : sms), false, 1};
+    }
+    // (76 clusters of two run at once, 32 of four, fewer than 16 of eight)
+    for (int c = 2; c <= 8 && c <= stages; c *= 2) {
+      if (tiles * c > (c == 2 ? sms : c == 4 ? sms * 27 / 32 : sms / 2)) continue;
+      cost = (stages + c - 1) / c * stage + end + 2500 + 300 * c + 40 * bx;
+      if (cost < best_cost) {
+        best_cost = cost;
+        best = {bx, stages, tiles_x, tiles, int(tiles) * c, false, c};
+      }
     }
     const int64_t units = tiles * stages;
     const int ctas = int(units < sms ? units : sms);
@@ -934,7 +1026,7 @@ Plan plan_gemm(int64_t lanes, int64_t rows, int steps, bool back, int sms) {
            bx * (9 * sharers + (run < stages ? 25 : 0));
     if (cost < best_cost) {
       best_cost = cost;
-      best = {bx, stages, tiles_x, tiles, ctas, true};
+      best = {bx, stages, tiles_x, tiles, ctas, true, 1};
     }
   }
   return best;
@@ -946,8 +1038,8 @@ int launch_one(const CUtensorMap& w, const CUtensorMap& x, const CUtensorMap& co
   auto kernel = dq4_int8_gemm_kernel<BX, kBack, kBF16>;
   static std::atomic<uint64_t> allowed{0};
   if (const int st = allow_smem(kernel, Gemm<BX, kBack>::kBytes, dev, &allowed)) return st;
-  return launch_ordered(kernel, dim3(unsigned(ctas)), Gemm<BX, kBack>::kThreads,
-                        Gemm<BX, kBack>::kBytes, stream, w, x, cols, p);
+  return launch_clusters(kernel, dim3(unsigned(ctas)), Gemm<BX, kBack>::kThreads,
+                         Gemm<BX, kBack>::kBytes, stream, p.cluster, w, x, cols, p);
 }
 
 template <bool kBack, bool kBF16>
@@ -956,6 +1048,7 @@ int launch_plan(const Plan& pl, const CUtensorMap& w, const CUtensorMap& x,
   p.tiles_x = int(pl.tiles_x);
   p.tiles = pl.tiles;
   p.units = pl.split ? pl.tiles * pl.stages : 0;
+  p.cluster = pl.cluster;
   p.part = static_cast<float4*>(part);
   if (pl.bx == 64) return launch_one<64, kBack, kBF16>(w, x, cols, p, dev, pl.ctas, stream);
   if (pl.bx == 128) return launch_one<128, kBack, kBF16>(w, x, cols, p, dev, pl.ctas, stream);

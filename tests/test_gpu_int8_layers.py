@@ -373,7 +373,8 @@ def test_moe_same_expert_for_all(dq):
 
 # ------------------------------------------------------------- sums in parts, offsets, ends
 @pytest.mark.parametrize("M,N,K", [(40, 64, 65536), (300, 128, 20000), (70, 130, 32768),
-                                   (129, 40, 50000), (260, 1500, 8208), (18, 1500, 30000)])
+                                   (129, 40, 50000), (260, 1500, 8208), (18, 1500, 30000),
+                                   (60, 2560, 20480)])
 def test_few_tiles_of_long_sums(dq, M, N, K):
     """Few tiles and a long sum: many parts to a tile, of which one joins all; and the same for
     the gradient, twice, bit for bit."""
@@ -394,6 +395,28 @@ def test_few_tiles_of_long_sums(dq, M, N, K):
     close(dx, want, (n / 16 + 4) * 2.0 ** -23 * size + U["f16"] * np.abs(want) + TINY["f16"],
           (M, n, lanes))
     assert torch.equal(dx, dq.int8_linear_backward(dy, dev(CB), dev(SCB)))
+
+
+@pytest.mark.parametrize("M,N,K", [(40, 1000, 4096), (63, 4001, 2064), (128, 4090, 3000),
+                                   (100, 9000, 6160), (250, 4000, 4000), (512, 4000, 8000)])
+def test_tiles_shared_by_clusters(dq, M, N, K):
+    """Tiles whose sums two, four or eight CTAs share, ragged in every direction."""
+    rng = np.random.default_rng(M + N + K)
+    K = K // 16 * 16
+    CB, SCB = weight(rng, N, K)
+    for kind, loud in (("f32", 0), ("bf16", 9)):
+        rows = random_rows(dq, rng, M, K, loud)
+        check_linear(dq, rows, CB, SCB, rng.normal(size=N), kind, (M, N, K, kind))
+        one, two = (dq.int8_linear(rows, dev(CB), dev(SCB)) for _ in range(2))
+        assert torch.equal(one, two)
+    lanes, n = N // 16 * 16, K // 8 * 8 - 8
+    CB, SCB = weight(rng, n, lanes)
+    dy = dev((rng.normal(size=(M, n)) * 0.05).astype(np.float32), DT["bf16"])
+    w = defs.weight16(CB, SCB, lambda f: torch.from_numpy(f).to(DT["bf16"]).float().numpy())
+    want, size = defs.linear_backward(host(dy), w)
+    dx = dq.int8_linear_backward(dy, dev(CB), dev(SCB))
+    close(dx, want, (n / 16 + 4) * 2.0 ** -23 * size + U["bf16"] * np.abs(want) + TINY["bf16"],
+          (M, n, lanes))
 
 
 def test_offsets_past_32_bits(dq):
