@@ -71,7 +71,10 @@ __global__ void __launch_bounds__(kStreamThreads, kFewDepth == 2 && NT < 4 ? 3 :
   const int in_cta = warp / group, member = warp - in_cta * group;
   const int64_t n0 = (int64_t(blockIdx.x) * (kStreamWarps / group) + in_cta) * kFewRows;
   uint8_t* rings = aligned_1024(smem_raw);
-  float* coef = reinterpret_cast<float*>(rings + kStreamWarps * kFewDepth * kStage);
+  // (the outliers' factors go where the rings were: with a place of their own an SM held two CTAs
+  // in place of three, 16 rows with 5 outlier columns through 4096 x 11008 took 20.6 us)
+  float* coef = reinterpret_cast<float*>(rings);
+  static_assert(kTokens * kMaxOutliers * 4 <= kStreamWarps * kFewDepth * kStage, "factors fit");
   const uint32_t ring = smem_u32(rings) + warp * kFewDepth * kStage, bars = smem_u32(s_bars[warp]);
   const uint64_t map = reinterpret_cast<uint64_t>(&map_w);
   // this warp's chunks, member + i * group for i < mine, in turn from `i0` on: warps that went
@@ -227,11 +230,12 @@ __global__ void __launch_bounds__(kStreamThreads, kFewDepth == 2 && NT < 4 ? 3 :
 
 // Whether a product goes to the kernel for few rows: up to 16, and up to 32 where the weight is
 // small.  Few / many, in us:
-//   rows          4096 x 4096    4096 to 11008   14336 to 4096   8192 to 28672
-//     16          6.6 / 16.9     14.9 / 22.7     16.1 / 30.5      50 / 60
-//     32         12.3 / 17.1     23.4 / 22.6     29.8 / 30.3      75 / 60
+//   rows          1024 x 1024   2048 to 4096   4096 x 4096   4096 to 11008   8192 to 28672
+//     16          3.2 / 8.6     3.9 / 10.4     6.6 / 11.7    14.9 / 20.2     50 / 55
+//     32          4.9 / 8.6     8.3 / 10.1    12.3 / 11.9    23.4 / 20.3     75 / 55
+// (32 rows 8192 to 2048: 9.6 / 14.9; with 5 outlier columns through 4096 x 4096 15.4 / 13.6.)
 bool few_rows(int64_t M, int64_t N, int64_t K) {
-  return M <= 16 || (M <= 32 && N * K <= 32 << 20) || K == 0;
+  return M <= 16 || (M <= 32 && N * K <= 16 << 20) || K == 0;
 }
 
 template <int NT, int kFewDepth>
@@ -240,12 +244,8 @@ int launch_few_depth(const CUtensorMap& w, const Int8Linear& p, int64_t grid, in
   auto kernel = dq4_int8_few_kernel<NT, kFewDepth>;
   constexpr int kRings = kStreamWarps * kFewDepth * kFewRows * kChunk + 1024;
   static std::atomic<uint64_t> allowed{0};
-  if (const int st = allow_smem(kernel, kRings + 8 * NT * kMaxOutliers * 4, dev, &allowed,
-                                kFewDepth == 2 ? 50 : 70))
-    return st;
-  const int tokens = int(p.M < 8 * NT ? p.M : 8 * NT);  // (more only with K = 0: none is used then)
-  return launch_ordered(kernel, dim3(unsigned(grid)), kStreamThreads, kRings + tokens * p.L * 4,
-                        stream, w, p, group);
+  if (const int st = allow_smem(kernel, kRings, dev, &allowed, kFewDepth == 2 ? 50 : 70)) return st;
+  return launch_ordered(kernel, dim3(unsigned(grid)), kStreamThreads, kRings, stream, w, p, group);
 }
 
 template <int NT>
