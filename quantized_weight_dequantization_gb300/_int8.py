@@ -18,7 +18,7 @@ from ._binding import _DTYPE_CODE, Dq4Error, _call_lock, get_lib
 
 # bytes of a new workspace that have to be zero (None: all of them)
 _COUNTERS.update({"int8 quantize": None, "int8 linear": 4096, "int8 backward": 4096,
-                  "int8 moe": 4096})
+                  "int8 moe": 0})
 
 _LIB = None
 
@@ -84,13 +84,13 @@ def _shape(t: torch.Tensor, name: str, shape) -> None:
         raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
 
 
-def _weight(CB: torch.Tensor, SCB: torch.Tensor, like: torch.Tensor, name: str, dims: int):
-    """Checked addresses of a weight's codes and scales."""
+def _weight(CB: torch.Tensor, SCB: torch.Tensor, like: torch.Tensor, name: str, dims: int) -> None:
+    """A weight's codes and scales."""
     if CB.dim() != dims:
         raise ValueError(f"{name}: must be {dims}-D, got {tuple(CB.shape)}")
     _shape(SCB, f"{name}'s scales", CB.shape[:-1])
-    return (_flat(CB, name, torch.int8, 0, like),
-            _flat(SCB, f"{name}'s scales", torch.float32, 0, like))
+    _flat(CB, name, torch.int8, 0, like)
+    _flat(SCB, f"{name}'s scales", torch.float32, 0, like)
 
 
 # ------------------------------------------------------------- rows in 8 bits
@@ -259,31 +259,38 @@ def int8_linear_backward(dY: torch.Tensor, CB: torch.Tensor, SCB: torch.Tensor,
     :func:`int8_correction_prep` has them.  N must be a multiple of 8, K of 16.  ``workspace``
     and ``bad`` as for :func:`int8_linear`.
     """
-    _on_gpu(dY, "dY")
-    if dY.dtype not in _HALF:
-        raise TypeError(f"dY: must be float16 or bfloat16, got {dY.dtype}")
-    if dY.dim() != 2 or CB.dim() != 2 or dY.shape[1] != CB.shape[0]:
-        raise ValueError(f"dY {tuple(dY.shape)} does not go with CB {tuple(CB.shape)}")
     index = dY.get_device()
+    # (first the short way that valid arguments pass, as in int8_linear)
+    if not (dY.is_cuda and CB.is_cuda and dY.dtype in _HALF and CB.dtype is torch.int8
+            and SCB.dtype is torch.float32 and dY.dim() == 2 and CB.dim() == 2
+            and CB.shape[0] == dY.shape[1] and SCB.shape == CB.shape[:1]
+            and dY.is_contiguous() and CB.is_contiguous() and SCB.is_contiguous()
+            and CB.get_device() == index and SCB.get_device() == index):
+        _on_gpu(dY, "dY")
+        if dY.dtype not in _HALF:
+            raise TypeError(f"dY: must be float16 or bfloat16, got {dY.dtype}")
+        if dY.dim() != 2 or CB.dim() != 2 or dY.shape[1] != CB.shape[0]:
+            raise ValueError(f"dY {tuple(dY.shape)} does not go with CB {tuple(CB.shape)}")
+        _flat(dY, "dY", dY.dtype, 0, dY)
+        _weight(CB, SCB, dY, "CB", 2)
     if index != _current_device():
         with torch.cuda.device(index):
             return int8_linear_backward(dY, CB, SCB, dX, workspace, bad, stream)
     M, N = dY.shape
     K = CB.shape[1]
-    dy_ptr = _flat(dY, "dY", dY.dtype, 0, dY)
-    cb_ptr, scb_ptr = _weight(CB, SCB, dY, "CB", 2)
     if dX is None:
         dX = torch.empty((M, K), dtype=dY.dtype, device=dY.device)
     else:
         _shape(dX, "dX", (M, K))
-    dx_ptr = _flat(dX, "dX", dY.dtype, 0, dY)
-    bad_ptr = _bad(bad, dY)
+        _flat(dX, "dX", dY.dtype, 0, dY)
+    bad_ptr = None if bad is None else _bad(bad, dY)
     handle = _stream(stream, index)
     need = _need_of(index, "linear_backward", M, N, K)
     with _call_lock(index, handle):
         ws_ptr, ws_bytes = _scratch(workspace, need, "int8 backward", dY, handle)
-        st = _lib().dq4_int8_linear_backward(dy_ptr, _DTYPE_CODE[dY.dtype], cb_ptr, scb_ptr, M, N,
-                                             K, dx_ptr, ws_ptr, ws_bytes, bad_ptr, handle)
+        st = _lib().dq4_int8_linear_backward(dY.data_ptr(), _DTYPE_CODE[dY.dtype], CB.data_ptr(),
+                                             SCB.data_ptr(), M, N, K, dX.data_ptr(), ws_ptr,
+                                             ws_bytes, bad_ptr, handle)
     if st:
         raise Dq4Error(st, "dq4_int8_linear_backward")
     return dX
@@ -303,38 +310,50 @@ def int8_moe(X: torch.Tensor, logits: torch.Tensor, w1: torch.Tensor, s1: torch.
     Wg, then those of Wu, ``w2`` int8 [E, H, I]; ``s1`` [E, 2 I] and ``s2`` [E, H] are float32
     scales of their rows, a value w * s / 127.  H and I are multiples of 16.  Returns Y (T x H,
     X's dtype), or (Y, ids, weights) with the choices, int32 and float32 [T, top_k].
-    ``workspace`` (uint8, zero-filled before its first use) holds the rows between the launches;
+    ``workspace`` (uint8) holds the rows between the launches;
     by default a cached buffer per (device, stream) is used, and in ``torch.cuda.graph`` memory
     of the graph's own.
     """
-    _rows(X, "X")
     index = X.get_device()
+    T, H = X.shape if X.dim() == 2 else (-1, -1)
+    E, I = (w1.shape[0], w2.shape[2]) if w1.dim() == 3 and w2.dim() == 3 else (-1, -1)
+    # (first the short way that valid arguments pass, as in int8_linear)
+    if not (X.is_cuda and X.dtype in _HALF and T >= 0 and E >= 0 and X.stride(1) == 1
+            and w1.shape == (E, 2 * I, H) and w2.shape == (E, H, I) and s1.shape == (E, 2 * I)
+            and s2.shape == (E, H) and logits.shape == (T, E) and w1.dtype is torch.int8
+            and w2.dtype is torch.int8 and s1.dtype is torch.float32
+            and s2.dtype is torch.float32 and logits.dtype is torch.float32
+            and w1.is_contiguous() and w2.is_contiguous() and s1.is_contiguous()
+            and s2.is_contiguous() and logits.is_contiguous() and w1.get_device() == index
+            and w2.get_device() == index and s1.get_device() == index
+            and s2.get_device() == index and logits.get_device() == index):
+        _rows(X, "X")
+        _weight(w1, s1, X, "w1", 3)
+        _weight(w2, s2, X, "w2", 3)
+        _shape(w1, "w1", (E, 2 * I, H))
+        _shape(w2, "w2", (E, H, I))
+        _shape(logits, "logits", (T, E))
+        _flat(logits, "logits", torch.float32, 0, X)
     if index != _current_device():
         with torch.cuda.device(index):
             return int8_moe(X, logits, w1, s1, w2, s2, top_k, renormalize, return_routing,
                             workspace, bad, stream)
-    T, H = X.shape
-    w1_ptr, s1_ptr = _weight(w1, s1, X, "w1", 3)
-    w2_ptr, s2_ptr = _weight(w2, s2, X, "w2", 3)
-    E, I = w1.shape[0], w2.shape[2]
-    _shape(w1, "w1", (E, 2 * I, H))
-    _shape(w2, "w2", (E, H, I))
-    _shape(logits, "logits", (T, E))
-    logits_ptr = _flat(logits, "logits", torch.float32, 0, X)
     if not 1 <= top_k <= min(E, 16):
         raise ValueError(f"top_k must be 1 .. {min(E, 16)}, got {top_k}")
-    ids = torch.empty((T, top_k), dtype=torch.int32, device=X.device)
-    weights = torch.empty((T, top_k), dtype=torch.float32, device=X.device)
-    Y = torch.empty((T, H), dtype=X.dtype, device=X.device)
-    bad_ptr = _bad(bad, X)
+    device = X.device
+    ids = torch.empty((T, top_k), dtype=torch.int32, device=device)
+    weights = torch.empty((T, top_k), dtype=torch.float32, device=device)
+    Y = torch.empty((T, H), dtype=X.dtype, device=device)
+    bad_ptr = None if bad is None else _bad(bad, X)
     handle = _stream(stream, index)
     need = _need_of(index, "moe", T, H, I, top_k)
     with _call_lock(index, handle):
         ws_ptr, ws_bytes = _scratch(workspace, need, "int8 moe", X, handle)
         st = _lib().dq4_int8_moe(X.data_ptr(), X.stride(0), _DTYPE_CODE[X.dtype], T, H, I, E,
-                                 logits_ptr, top_k, renormalize, w1_ptr, s1_ptr, w2_ptr, s2_ptr,
-                                 ids.data_ptr(), weights.data_ptr(), Y.data_ptr(), ws_ptr,
-                                 ws_bytes, bad_ptr, handle)
+                                 logits.data_ptr(), top_k, renormalize, w1.data_ptr(),
+                                 s1.data_ptr(), w2.data_ptr(), s2.data_ptr(), ids.data_ptr(),
+                                 weights.data_ptr(), Y.data_ptr(), ws_ptr, ws_bytes, bad_ptr,
+                                 handle)
     if st:
         raise Dq4Error(st, "dq4_int8_moe")
     return (Y, ids, weights) if return_routing else Y
