@@ -419,6 +419,41 @@ def test_tiles_shared_by_clusters(dq, M, N, K):
           (M, n, lanes))
 
 
+@pytest.mark.parametrize("M,N,K", [(64, 4096, 4096), (200, 4096, 2048), (700, 4096, 1024)])
+def test_many_rows_in_graphs_on_two_streams(dq, M, N, K):
+    """Products of many rows captured twice and replayed on two streams at once, beside eager
+    calls on a third, bit for bit what they give alone."""
+    rng = np.random.default_rng(M)
+    CB, SCB = (dev(a) for a in weight(rng, N, K))
+    rows = [random_rows(dq, rng, M, K, 4 * i) for i in range(3)]
+    dys = [rows_of(rng, M, N, "bf16") for _ in range(3)]
+
+    def both(i):
+        return dq.int8_linear(rows[i], CB, SCB), dq.int8_linear_backward(dys[i], CB, SCB)
+    want = [both(i) for i in range(3)]
+    torch.cuda.synchronize()
+    graphs, outs = [], []
+    for i in range(2):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            outs.append(both(i))
+        graphs.append(graph)
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    for _ in range(10):
+        for i in range(2):
+            for t in outs[i]:
+                t.zero_()
+        torch.cuda.synchronize()
+        for i in range(2):
+            with torch.cuda.stream(streams[i]):
+                graphs[i].replay()
+        with torch.cuda.stream(streams[2]):
+            got = both(2)
+        torch.cuda.synchronize()
+        for a, b in zip((*outs[0], *outs[1], *got), (*want[0], *want[1], *want[2])):
+            assert torch.equal(a, b)
+
+
 def test_offsets_past_32_bits(dq):
     """Operands and results of more than 2^31 values: their last rows, by the definitions."""
     rng = np.random.default_rng(20)
