@@ -63,7 +63,7 @@ struct Gemm {
   static constexpr int kBars = 2 * kSlots + 2 * kRawSlots + 2 * kRing + 2 * kBuffers + 2 + kPieces;
   static constexpr int kBytes = kBarsAt + 8 * kBars + 1024;  // + alignment slack
   static constexpr int kStatic = kBack ? 16 * kStage + 64 : 4 * BX + 64;
-  static_assert(kBytes + kStatic <= 227 * 1024, "shared memory budget");
+  static_assert(kBytes + kStatic <= 227 * 1024, "shared memory");
   static_assert(kBytes > 116 * 1024, "one CTA per SM: the TMEM allocation never waits");
 };
 

@@ -108,7 +108,6 @@ __global__ void __launch_bounds__(kStreamThreads, kFewDepth == 2 && NT < 4 ? 3 :
   const float sn = load_ahead(p.SCB + n_in);
   uint32_t ahead[kAhead];
   int used = 0;
-  if (p.L > 0 && warp == 0) list_columns(p, &s_cols);  // (while the first codes are on their way)
   const int8_t* tok[NT];
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt)
@@ -131,6 +130,7 @@ __global__ void __launch_bounds__(kStreamThreads, kFewDepth == 2 && NT < 4 ? 3 :
       }
   };
   fetch(0);
+  if (p.L > 0 && warp == 0) list_columns(p, &s_cols);  // (while the first codes are on their way)
 #pragma unroll 1
   for (; i < mine; ++i) {
     uint4 x[NT][2];
