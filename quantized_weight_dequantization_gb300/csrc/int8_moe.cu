@@ -6,7 +6,8 @@
 //           each expert's (token, choice) pairs, by entries of up to 8
 //   up      a job is 16 inner places of an entry's expert, gate and up rows together: inner =
 //           silu(g) * u in FP16, scaled by a power of two for each 16 places of a pair, and the
-//           largest of each pair's row
+//           largest of each pair's row.  One rounding to 11 bits there is as much as FP16 results
+//           have of their own, so those get what it leaves as a second term; BF16 ones do without
 //   down    a job is 32 output places of an entry's expert; inner values are brought to a scale for
 //           their row on their way in, exactly (powers of two)
 //   combine each token's results by their weights
@@ -14,7 +15,7 @@
 //
 // Of 4096 x 14336: one token through 2 of 8 experts 70.5 us, where the bytes take 52 (alone, the
 // four take 5.6, 41.6, 25.5 and 4 us: the two products 0.83 and 0.68 of the copy rate), 23 tokens
-// 240 of 208; of 2048 x 1408, 16 tokens through 6 of 64, 92 of 65.  What is left is the ends of
+// 240 of 208 (in FP16 254); of 2048 x 1408, 16 tokens through 6 of 64, 92 of 65.  What is left is the ends of
 // the four launches, about 4 us each.
 #include "int8.cuh"
 
@@ -56,6 +57,7 @@ struct MoeArgs {
   Routed* r;
   uint16_t* xs;     // [pairs][H] FP16
   uint16_t* inner;  // [pairs][I] FP16, scaled for each tile of 16
+  uint16_t* inner_low;  // and what that leaves, for FP16 results; else none
   float* inner_by;  // [pairs][I / 16] what a tile has to be multiplied by
   float* out;       // [pairs][H]
   int* bad;
@@ -266,10 +268,15 @@ __global__ void __launch_bounds__(kRouteThreads) dq4_moe_route_kernel(const MoeA
 // Rings of four chunks leave the tokens less of L1: 16 tokens, 6 of 64 experts, took 97 us, so 92.
 //
 // kBoxes: boxes of weight rows of a chunk.  kScaled: tokens have factors, one for each 16 values.
+// kTerms: FP16 terms of a token's value, the second in an array of its own.  With two a chunk's
+// tokens are fetched while its weights are waited for, not a chunk ahead: there are no registers
+// for 64 words (going through a chunk once for each term took 298 us for 23 tokens through 2 of 8
+// experts of 4096 x 14336; so 254, and one term 240).
 // Jobs:
 //   places(job, y)          the first row of each box of weights
 //   tokens(job)             this lane's token (for one that is not there any other, whose results
 //                           are not used), advanced to its 32 c
+//   second()                how far its second term is from it
 //   scales(job, k, f)       with kScaled: the factors of values k .. k + 15 and the 16 after them
 //   begin(job, t)           before a job's products, thread t of its group
 //   finish(job, part, ...)  the group's sums (sum(part, warps, token, row)), thread t of `threads`
@@ -298,7 +305,7 @@ __device__ __forceinline__ int group_warps(uint32_t jobs, uint32_t chunks, uint3
   return best;
 }
 
-template <int kBoxes, bool kScaled>
+template <int kBoxes, bool kScaled, int kTerms>
 struct Streamed {
   static constexpr int kStage = kJobRows * kChunk;
   static constexpr int kPart = kJobRows * kEntry;  // sums of a warp
@@ -354,7 +361,7 @@ struct Streamed {
     for (int i = 0; i < kDepth; ++i) issue();
     // ---- the tokens: those of the next chunk
     const uint16_t* tok;
-    uint4 x[4];
+    uint4 x[kTerms][4];
     float f[2];
     int64_t tok_job = mine > 0 ? first : all;
     int tok_chunk = 0, tok_left = mine;
@@ -368,9 +375,15 @@ struct Streamed {
       if (tok_job >= all) return;
       const int64_t k = int64_t(member + tok_chunk * group) * kChunk;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        x[i] = make_uint4(0, 0, 0, 0);  // (past the end)
-        if (k + 32 * c + 8 * i < K) x[i] = load_ahead(reinterpret_cast<const uint4*>(tok + k) + i);
+      for (int t = 0; t < kTerms; ++t) {
+        const uint16_t* from = tok + k;
+        if constexpr (kTerms > 1)
+          if (t) from += jobs.second();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          x[t][i] = make_uint4(0, 0, 0, 0);  // (past the end)
+          if (k + 32 * c + 8 * i < K) x[t][i] = load_ahead(reinterpret_cast<const uint4*>(from) + i);
+        }
       }
       if constexpr (kScaled) jobs.scales(tok_job, k + 32 * c, f);
       if (++tok_chunk == mine) tok_chunk = 0;
@@ -380,7 +393,7 @@ struct Streamed {
         tok_open();
       }
     };
-    fetch();
+    if constexpr (kTerms == 1) fetch();
     auto join = [&] {  // the group's threads
       if (group == 1)
         __syncwarp();
@@ -395,21 +408,27 @@ struct Streamed {
       float acc[2][4] = {};
 #pragma unroll 1
       for (int i = 0; i < mine && ok; ++i) {
-        // the tokens' operand words, which frees the registers for the next chunk's
-        uint32_t b[16];
+        // the tokens' operand words: with one term before the next chunk's are fetched
+        uint32_t b[kTerms][16];
+        auto words = [&] {
 #pragma unroll
-        for (int s = 0; s < 16; ++s) {
-          b[s] = reinterpret_cast<const uint32_t*>(x)[s];
-          if constexpr (kScaled) {
-            __half2 v;
-            memcpy(&v, &b[s], 4);
-            v = __hmul2(v, __float2half2_rn(f[s >> 3]));
-            memcpy(&b[s], &v, 4);
-          }
-        }
+          for (int t = 0; t < kTerms; ++t)
+#pragma unroll
+            for (int s = 0; s < 16; ++s) {
+              b[t][s] = reinterpret_cast<const uint32_t*>(x[t])[s];
+              if constexpr (kScaled) {
+                __half2 v;
+                memcpy(&v, &b[t][s], 4);
+                v = __hmul2(v, __float2half2_rn(f[s >> 3]));
+                memcpy(&b[t][s], &v, 4);
+              }
+            }
+        };
+        if constexpr (kTerms == 1) words();
         fetch();
         ok = __all_sync(kAllLanes, mbar_wait(bars + 8 * slot, phase));
         if (!ok) break;
+        if constexpr (kTerms > 1) words();
         const uint32_t at = ring + slot * kStage;
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
@@ -427,8 +446,10 @@ struct Streamed {
               uint32_t a[4];
               codes_f16(reinterpret_cast<const uint32_t*>(&w[rt][0])[s], a[0], a[2]);
               codes_f16(reinterpret_cast<const uint32_t*>(&w[rt][1])[s], a[1], a[3]);
-              mma_16816(acc[rt], a[0], a[1], a[2], a[3], b[8 * half + 2 * s],
-                        b[8 * half + 2 * s + 1]);
+#pragma unroll
+              for (int t = 0; t < kTerms; ++t)
+                mma_16816(acc[rt], a[0], a[1], a[2], a[3], b[t][8 * half + 2 * s],
+                          b[t][8 * half + 2 * s + 1]);
             }
         }
         __syncwarp();  // every lane has read the chunk
@@ -518,7 +539,7 @@ __device__ __forceinline__ Entries load_entries(const MoeArgs& p, uint8_t* smem)
 
 // ---------------------------------------------------------------------------- up
 struct UpJobs {
-  using S = Streamed<2, false>;
+  using S = Streamed<2, false, 1>;
   const MoeArgs& p;
   Entries s;
   float s_gate, s_up;  // scales of this thread's place
@@ -570,7 +591,11 @@ struct UpJobs {
         float up, down;
         pow2_scaling(__uint_as_float(top), up, down);
         const int64_t at = first + j;
-        p.inner[at * p.I + tile * kUpPlaces + place] = __half_as_ushort(__float2half_rn(v * up));
+        const __half high = __float2half_rn(v * up);
+        p.inner[at * p.I + tile * kUpPlaces + place] = __half_as_ushort(high);
+        if (p.inner_low)
+          p.inner_low[at * p.I + tile * kUpPlaces + place] =
+              __half_as_ushort(__float2half_rn(v * up - __half2float(high)));
         if (place == 0) {
           p.inner_by[at * (p.I / kUpPlaces) + tile] = down;
           atomicMax(p.r->top + at, top);
@@ -593,8 +618,9 @@ __global__ void __launch_bounds__(kStreamThreads, kCtas)
 }
 
 // -------------------------------------------------------------------------- down
+template <int kTerms>
 struct DownJobs {
-  using S = Streamed<1, true>;
+  using S = Streamed<1, true, kTerms>;
   const MoeArgs& p;
   Entries s;
   float s_place;  // scale of this thread's place
@@ -619,6 +645,7 @@ struct DownJobs {
   __device__ __forceinline__ const uint16_t* tokens(int64_t job) const {
     return p.inner + pair_of(job) * p.I + 32 * (threadIdx.x & 3);
   }
+  __device__ __forceinline__ int64_t second() const { return p.inner_low - p.inner; }
   // A tile's FP16 values in the row's unit: powers of two, both.
   __device__ __forceinline__ void scales(int64_t job, int64_t k, float (&f)[2]) const {
     const int at = pair_of(job);
@@ -649,10 +676,11 @@ struct DownJobs {
   }
 };
 
+template <int kTerms>
 __global__ void __launch_bounds__(kStreamThreads, kCtas)
     dq4_moe_down_kernel(const __grid_constant__ CUtensorMap map_w, const MoeArgs p) {
   extern __shared__ uint8_t smem_raw[];
-  using Jobs = DownJobs;
+  using Jobs = DownJobs<kTerms>;
   uint8_t* smem = aligned_1024(smem_raw);
   Jobs::S::setup(smem, map_w);
   wait_for_stream();
@@ -696,16 +724,18 @@ int launch_moe(const MoeArgs& p, int dev, int sms, cudaStream_t s) {
   const int64_t entries = most_entries(p.E, pairs);
   const int more = int(entry_bytes(entries, pairs));
   constexpr int kMore = kMaxPairs * 8 + kMaxEntries * 4 + 2;
-  constexpr int kUpBytes = UpJobs::S::kBytes + 1024, kDownBytes = DownJobs::S::kBytes + 1024;
+  constexpr int kUpBytes = UpJobs::S::kBytes + 1024, kDownBytes = DownJobs<1>::S::kBytes + 1024;
   static_assert(kUpBytes + kMore <= 227 * 1024 && kDownBytes + kMore <= 227 * 1024,
                 "shared memory");
   const int keys = kRouteThreads / 32 * p.E * 4;
-  static std::atomic<uint64_t> allowed_route{0}, allowed_up{0}, allowed_down{0};
+  static std::atomic<uint64_t> allowed_route{0}, allowed_up{0}, allowed_down[2] = {};
   if (const int st = allow_smem(dq4_moe_route_kernel, kRouteThreads / 32 * kMaxExperts * 4, dev,
                                 &allowed_route))
     return st;
   if (const int st = allow_smem(dq4_moe_up_kernel, kUpBytes + kMore, dev, &allowed_up)) return st;
-  if (const int st = allow_smem(dq4_moe_down_kernel, kDownBytes + kMore, dev, &allowed_down))
+  const auto down = p.inner_low ? dq4_moe_down_kernel<2> : dq4_moe_down_kernel<1>;
+  if (const int st = allow_smem(down, kDownBytes + kMore, dev,
+                                &allowed_down[p.inner_low != nullptr]))
     return st;
   CUtensorMap w1, w2;
   if (const int st = encode_2d(&w1, CU_TENSOR_MAP_DATA_TYPE_UINT8, p.W1, p.H, 2 * p.I * p.E, p.H,
@@ -725,7 +755,7 @@ int launch_moe(const MoeArgs& p, int dev, int sms, cudaStream_t s) {
   if (const int st = launch_ordered(dq4_moe_up_kernel, grid(p.I, kUpPlaces), kStreamThreads,
                                     kUpBytes + more, s, w1, p))
     return st;
-  if (const int st = launch_ordered(dq4_moe_down_kernel, grid(p.H, kDownPlaces), kStreamThreads,
+  if (const int st = launch_ordered(down, grid(p.H, kDownPlaces), kStreamThreads,
                                     kDownBytes + more, s, w2, p))
     return st;
   const int64_t per = kCombineThreads * 4;
@@ -746,7 +776,7 @@ int64_t dq4_int8_moe_workspace_bytes(int64_t T, int64_t H, int64_t I, int32_t to
       H > kMaxHidden || I > kMaxInner)
     return 0;
   return up256(sizeof(Routed)) +
-         T * top_k * (up256(H * 2) + up256(I * 2) + up256(I / 4) + up256(H * 4));
+         T * top_k * (up256(H * 2) + 2 * up256(I * 2) + up256(I / 4) + up256(H * 4));
 }
 
 int dq4_int8_moe(const void* X, int64_t row_stride, int32_t dtype, int64_t T, int64_t H, int64_t I,
@@ -773,13 +803,15 @@ int dq4_int8_moe(const void* X, int64_t row_stride, int32_t dtype, int64_t T, in
   if (const int st = current_device(&dev, &sms)) return st;
   MoeArgs p = {X, row_stride, dtype == DQ4_OUT_BF16, int(T), int(E), top_k, renormalize, H, I,
                logits, W1, W2, S1, S2, ids, weights, Y, nullptr, nullptr, nullptr, nullptr, nullptr,
-               bad};
+               nullptr, bad};
   char* at = static_cast<char*>(workspace);
   p.r = reinterpret_cast<Routed*>(at);
   at += up256(sizeof(Routed));
   p.xs = reinterpret_cast<uint16_t*>(at);
   at += T * top_k * up256(H * 2);
   p.inner = reinterpret_cast<uint16_t*>(at);
+  at += T * top_k * up256(I * 2);
+  if (!p.bf16) p.inner_low = reinterpret_cast<uint16_t*>(at);
   at += T * top_k * up256(I * 2);
   p.inner_by = reinterpret_cast<float*>(at);
   at += T * top_k * up256(I / 4);

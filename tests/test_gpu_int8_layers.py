@@ -303,6 +303,28 @@ def test_moe(dq, T, H, I, E, k):
     check_moe(dq, x, logits, w1, s1, w2, s2, k, T % 2 == 0, kind, (T, H, I, E, k))
 
 
+@pytest.mark.parametrize("T", [1, 4, 23, 60])
+def test_moe_holds_more_than_its_results(dq, T):
+    """FP16 results: the inner values' two terms hold 2^-22 of them, which leaves the results' own
+    rounding and FP32 sums."""
+    rng = np.random.default_rng(T)
+    H, I, E, k = 256, 1424, 8, 2
+    w1, s1 = weight(rng, E, 2 * I, H)
+    w2, s2 = weight(rng, E, H, I)
+    x = rows_of(rng, T, H, "f16")
+    logits = dev(rng.normal(size=(T, E)).astype(np.float32))
+    y = dq.int8_moe(x, logits, dev(w1), dev(s1), dev(w2), dev(s2), k)
+    want, _, _, size, unit = defs.moe(host(x), host(logits), w1, s1, w2, s2, k, True)
+    tol = (unit * (H / 16 * 2.0 ** -23 + 2.0 ** -20)
+           + size * (2.0 ** -22 + I / 16 * 2.0 ** -23 + 2.0 ** -19) + U["f16"] * np.abs(want)
+           + TINY["f16"])
+    close(y, want, tol, T)
+    # over all, the rounding of the results is all that is seen: a value's is at most 2^-11 of it
+    # and 2^-11 / sqrt(3) in the mean square at most
+    off = host(y) - want
+    assert np.sqrt((off ** 2).sum() / (want ** 2).sum()) < 2.0 ** -11 / np.sqrt(3)
+
+
 def test_moe_routing(dq):
     """Ties, NaN, infinities, masked experts, rows whose mask leaves nothing."""
     rng = np.random.default_rng(8)
