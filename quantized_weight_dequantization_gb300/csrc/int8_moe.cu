@@ -259,8 +259,8 @@ __global__ void __launch_bounds__(kRouteThreads) dq4_moe_route_kernel(const MoeA
 // codes of rows g and g + 8 of each 16, and the same places of token g, and eight products take
 // them four at a time.  The weights come by TMA into a ring of the warp's own in shared memory, two
 // chunks ahead, across the ends of jobs (lane 0 issues, all lanes consume); the tokens, which every
-// job of an entry reads, from L2 into registers, a chunk ahead.  Nothing else synchronizes warps
-// before a job's end.  A job starts at a chunk of its own, so that warps do not go through the
+// job of an entry reads, from L2 into registers, while a chunk's weights are waited for (a chunk
+// ahead took 1 % more).  Nothing else synchronizes warps before a job's end.  A job starts at a chunk of its own, so that warps do not go through the
 // tokens side by side and queue at single lines of L2.
 // Copies of 128-byte rows: the TMA takes about 3.5 cycles for a row whatever its width, and at 64
 // bytes a row that bounds the weight's bytes (one token through 11008 x 4096, whose weight alone
@@ -268,10 +268,9 @@ __global__ void __launch_bounds__(kRouteThreads) dq4_moe_route_kernel(const MoeA
 // Rings of four chunks leave the tokens less of L1: 16 tokens, 6 of 64 experts, took 97 us, so 92.
 //
 // kBoxes: boxes of weight rows of a chunk.  kScaled: tokens have factors, one for each 16 values.
-// kTerms: FP16 terms of a token's value, the second in an array of its own.  With two a chunk's
-// tokens are fetched while its weights are waited for, not a chunk ahead: there are no registers
-// for 64 words (going through a chunk once for each term took 298 us for 23 tokens through 2 of 8
-// experts of 4096 x 14336; so 254, and one term 240).
+// kTerms: FP16 terms of a token's value, the second in an array of its own (going through a chunk
+// once for each, with half of the registers, took 298 us for 23 tokens through 2 of 8 experts of
+// 4096 x 14336; so 254, and one term 240).
 // Jobs:
 //   places(job, y)          the first row of each box of weights
 //   tokens(job)             this lane's token (for one that is not there any other, whose results
@@ -359,7 +358,7 @@ struct Streamed {
     };
 #pragma unroll 1
     for (int i = 0; i < kDepth; ++i) issue();
-    // ---- the tokens: those of the next chunk
+    // ---- the tokens, of the next chunk
     const uint16_t* tok;
     uint4 x[kTerms][4];
     float f[2];
@@ -393,7 +392,6 @@ struct Streamed {
         tok_open();
       }
     };
-    if constexpr (kTerms == 1) fetch();
     auto join = [&] {  // the group's threads
       if (group == 1)
         __syncwarp();
@@ -408,27 +406,22 @@ struct Streamed {
       float acc[2][4] = {};
 #pragma unroll 1
       for (int i = 0; i < mine && ok; ++i) {
-        // the tokens' operand words: with one term before the next chunk's are fetched
-        uint32_t b[kTerms][16];
-        auto words = [&] {
-#pragma unroll
-          for (int t = 0; t < kTerms; ++t)
-#pragma unroll
-            for (int s = 0; s < 16; ++s) {
-              b[t][s] = reinterpret_cast<const uint32_t*>(x[t])[s];
-              if constexpr (kScaled) {
-                __half2 v;
-                memcpy(&v, &b[t][s], 4);
-                v = __hmul2(v, __float2half2_rn(f[s >> 3]));
-                memcpy(&b[t][s], &v, 4);
-              }
-            }
-        };
-        if constexpr (kTerms == 1) words();
         fetch();
         ok = __all_sync(kAllLanes, mbar_wait(bars + 8 * slot, phase));
         if (!ok) break;
-        if constexpr (kTerms > 1) words();
+        uint32_t b[kTerms][16];  // the tokens' operand words
+#pragma unroll
+        for (int t = 0; t < kTerms; ++t)
+#pragma unroll
+          for (int s = 0; s < 16; ++s) {
+            b[t][s] = reinterpret_cast<const uint32_t*>(x[t])[s];
+            if constexpr (kScaled) {
+              __half2 v;
+              memcpy(&v, &b[t][s], 4);
+              v = __hmul2(v, __float2half2_rn(f[s >> 3]));
+              memcpy(&b[t][s], &v, 4);
+            }
+          }
         const uint32_t at = ring + slot * kStage;
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
