@@ -60,8 +60,10 @@ __device__ __forceinline__ uint64_t codes_of(float2 x, uint64_t inverse2) {
   return v;
 }
 
-// kRow threads a row, kGroups groups of 8 values for each at a time.  kVec: groups are whole and
-// aligned.  Rows longer than the registers hold are read twice (the second time from L2).
+// kRow threads a row, kGroups groups of 8 values for each at a time: 8 that follow one another,
+// where they are whole and aligned (kVec), else every kRow-th, so that a warp's loads follow one
+// another.  (8000 x 1001: 24 us with 8 that follow one another and a CTA a row, so 7.8.)  Rows
+// longer than the registers hold are read twice (the second time from L2).
 template <bool kBf16, bool kVec, bool kThr, int kRow, int kGroups>
 __global__ void __launch_bounds__(kRowThreads) int8_quantize_kernel(const QuantArgs p) {
   constexpr uint32_t kInf = kBf16 ? 0x7F80u : 0x7C00u;
@@ -75,10 +77,13 @@ __global__ void __launch_bounds__(kRowThreads) int8_quantize_kernel(const QuantA
   const uint16_t* x = p.X + row * p.row_stride;
   uint32_t* marks = p.marks + (blockIdx.x % kCopies) * ((p.K + 31) / 32);
   uint4 v[kGroups];
+  auto column_of = [&](int64_t base, int g, int i) {
+    return kVec ? base + (g * kRow + t) * 8 + i : base + (g * 8 + i) * kRow + t;
+  };
   auto load = [&](int64_t base) {
 #pragma unroll
     for (int g = 0; g < kGroups; ++g) {
-      const int64_t e = base + (int64_t(g) * kRow + t) * 8;
+      const int64_t e = column_of(base, g, 0);
       v[g] = make_uint4(0, 0, 0, 0);
       if constexpr (kVec) {
         if (e < p.K) v[g] = load_global(reinterpret_cast<const uint4*>(x + e));
@@ -86,7 +91,8 @@ __global__ void __launch_bounds__(kRowThreads) int8_quantize_kernel(const QuantA
         uint32_t w[4] = {0, 0, 0, 0};
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-          if (e + i < p.K) w[i / 2] |= uint32_t(load_global(x + e + i)) << (16 * (i & 1));
+          if (e + i * kRow < p.K)
+            w[i / 2] |= uint32_t(load_global(x + e + i * kRow)) << (16 * (i & 1));
         v[g] = make_uint4(w[0], w[1], w[2], w[3]);
       }
     }
@@ -120,7 +126,7 @@ __global__ void __launch_bounds__(kRowThreads) int8_quantize_kernel(const QuantA
           if (b < p.loud || b > kInf) {
             most = max(most, b);
           } else {
-            const int64_t col = base + (int64_t(g) * kRow + t) * 8 + i;
+            const int64_t col = column_of(base, g, i);
             atomicOr(marks + (col >> 5), 1u << (col & 31));
           }
         }
@@ -148,7 +154,7 @@ __global__ void __launch_bounds__(kRowThreads) int8_quantize_kernel(const QuantA
     if (p.K > kSpan) load(base);
 #pragma unroll
     for (int g = 0; g < kGroups; ++g) {
-      const int64_t e = base + (int64_t(g) * kRow + t) * 8;
+      const int64_t e = column_of(base, g, 0);
       uint32_t c[2];
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
@@ -163,7 +169,7 @@ __global__ void __launch_bounds__(kRowThreads) int8_quantize_kernel(const QuantA
       } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-          if (e + i < p.K) to[e + i] = int8_t(c[i / 4] >> (8 * (i & 3)));
+          if (e + i * kRow < p.K) to[e + i * kRow] = int8_t(c[i / 4] >> (8 * (i & 3)));
       }
     }
   }
@@ -252,18 +258,30 @@ __global__ void __launch_bounds__(kRowThreads) int8_outliers_kernel(const Outlie
     }
   }
   // Outlier columns past the last that is kept: their outliers' codes end at +-127 (they are above
-  // the scale).  A warp takes 32 columns, a lane one of them.
+  // the scale).  A warp looks at 32 words of marks, and takes the columns of a word side by side,
+  // or, where they are few, the rows of one.
   if (found > p.max_cols) {
     const int64_t after = s_cols[p.max_cols - 1] + 1;
-    for (int64_t w = after / 32 + warp; w < words; w += kRowThreads / 32) {
-      const uint32_t copy = lane < kCopies ? load_global(p.marks + lane * words + w) : 0;
-      const int64_t col = w * 32 + lane;
-      if (!(__reduce_or_sync(kAllLanes, copy) >> lane & 1) || col < after) continue;
+    auto clip = [&](int64_t row, int64_t col) {
+      const uint32_t b = load_global(p.X + row * p.row_stride + col);
+      if ((b & 0x7FFFu) >= p.loud && load_global(p.scales + row) > 0.f)
+        p.codes[row * p.K + col] = b & 0x8000u ? -127 : 127;
+    };
+    for (int64_t w0 = after / 32 + warp * 32; w0 < words; w0 += kRowThreads) {
+      uint32_t own = w0 + lane < words ? marks_of(w0 + lane) : 0;
+      if (w0 + lane == after / 32) own &= 0xFFFFFFFFu << (after & 31);
+      for (uint32_t some = __ballot_sync(kAllLanes, own != 0); some != 0; some &= some - 1) {
+        const int at = __ffs(some) - 1;
+        uint32_t m = __shfl_sync(kAllLanes, own, at);
+        const int64_t col = (w0 + at) * 32;
+        if (__popc(m) >= 8) {
+          if (m >> lane & 1)
 #pragma unroll 4
-      for (int r = 0; r < rows; ++r) {
-        const uint32_t b = load_global(p.X + (row0 + r) * p.row_stride + col);
-        if ((b & 0x7FFFu) >= p.loud && load_global(p.scales + row0 + r) > 0.f)
-          p.codes[(row0 + r) * p.K + col] = b & 0x8000u ? -127 : 127;
+            for (int r = 0; r < rows; ++r) clip(row0 + r, col + lane);
+        } else {
+          for (; m != 0; m &= m - 1)
+            for (int r = lane; r < rows; r += 32) clip(row0 + r, col + __ffs(m) - 1);
+        }
       }
     }
   }
@@ -286,6 +304,8 @@ int launch_rows(const QuantArgs& p, bool vec, cudaStream_t stream) {
     return launch_ordered(kernel, dim3(unsigned((p.M + rows - 1) / rows)), kRowThreads, 0, stream,
                           p);
   };
+  if (!vec && p.K <= 1024)
+    return go(int8_quantize_kernel<kBf16, false, kThr, 32, 4>, kRowThreads / 32);
   if (!vec) return go(int8_quantize_kernel<kBf16, false, kThr, 256, 2>, 1);
   if (p.K <= 1024) return go(int8_quantize_kernel<kBf16, true, kThr, 32, 4>, kRowThreads / 32);
   if (p.K <= 4096) return go(int8_quantize_kernel<kBf16, true, kThr, 256, 2>, 1);
