@@ -6,8 +6,9 @@
 //           each expert's (token, choice) pairs, by entries of up to 8
 //   up      a job is 16 inner places of an entry's expert, gate and up rows together: inner =
 //           silu(g) * u in FP16, scaled by a power of two for each 16 places of a pair, and the
-//           largest of each pair's row.  One rounding to 11 bits there is as much as FP16 results
-//           have of their own, so those get what it leaves as a second term; BF16 ones do without
+//           largest of each pair's row.  One rounding to 11 bits there would be as much as FP16
+//           results have of their own, and move one BF16 result in ten to its neighbour, so what it
+//           leaves is a second term
 //   down    a job is 32 output places of an entry's expert; inner values are brought to a scale for
 //           their row on their way in, exactly (powers of two)
 //   combine each token's results by their weights
@@ -57,7 +58,7 @@ struct MoeArgs {
   Routed* r;
   uint16_t* xs;     // [pairs][H] FP16
   uint16_t* inner;  // [pairs][I] FP16, scaled for each tile of 16
-  uint16_t* inner_low;  // and what that leaves, for FP16 results; else none
+  uint16_t* inner_low;  // and what that leaves
   float* inner_by;  // [pairs][I / 16] what a tile has to be multiplied by
   float* out;       // [pairs][H]
   int* bad;
@@ -586,9 +587,8 @@ struct UpJobs {
         const int64_t at = first + j;
         const __half high = __float2half_rn(v * up);
         p.inner[at * p.I + tile * kUpPlaces + place] = __half_as_ushort(high);
-        if (p.inner_low)
-          p.inner_low[at * p.I + tile * kUpPlaces + place] =
-              __half_as_ushort(__float2half_rn(v * up - __half2float(high)));
+        p.inner_low[at * p.I + tile * kUpPlaces + place] =
+            __half_as_ushort(__float2half_rn(v * up - __half2float(high)));
         if (place == 0) {
           p.inner_by[at * (p.I / kUpPlaces) + tile] = down;
           atomicMax(p.r->top + at, top);
@@ -611,9 +611,8 @@ __global__ void __launch_bounds__(kStreamThreads, kCtas)
 }
 
 // -------------------------------------------------------------------------- down
-template <int kTerms>
 struct DownJobs {
-  using S = Streamed<1, true, kTerms>;
+  using S = Streamed<1, true, 2>;
   const MoeArgs& p;
   Entries s;
   float s_place;  // scale of this thread's place
@@ -669,11 +668,10 @@ struct DownJobs {
   }
 };
 
-template <int kTerms>
 __global__ void __launch_bounds__(kStreamThreads, kCtas)
     dq4_moe_down_kernel(const __grid_constant__ CUtensorMap map_w, const MoeArgs p) {
   extern __shared__ uint8_t smem_raw[];
-  using Jobs = DownJobs<kTerms>;
+  using Jobs = DownJobs;
   uint8_t* smem = aligned_1024(smem_raw);
   Jobs::S::setup(smem, map_w);
   wait_for_stream();
@@ -717,18 +715,16 @@ int launch_moe(const MoeArgs& p, int dev, int sms, cudaStream_t s) {
   const int64_t entries = most_entries(p.E, pairs);
   const int more = int(entry_bytes(entries, pairs));
   constexpr int kMore = kMaxPairs * 8 + kMaxEntries * 4 + 2;
-  constexpr int kUpBytes = UpJobs::S::kBytes + 1024, kDownBytes = DownJobs<1>::S::kBytes + 1024;
+  constexpr int kUpBytes = UpJobs::S::kBytes + 1024, kDownBytes = DownJobs::S::kBytes + 1024;
   static_assert(kUpBytes + kMore <= 227 * 1024 && kDownBytes + kMore <= 227 * 1024,
                 "shared memory");
   const int keys = kRouteThreads / 32 * p.E * 4;
-  static std::atomic<uint64_t> allowed_route{0}, allowed_up{0}, allowed_down[2] = {};
+  static std::atomic<uint64_t> allowed_route{0}, allowed_up{0}, allowed_down{0};
   if (const int st = allow_smem(dq4_moe_route_kernel, kRouteThreads / 32 * kMaxExperts * 4, dev,
                                 &allowed_route))
     return st;
   if (const int st = allow_smem(dq4_moe_up_kernel, kUpBytes + kMore, dev, &allowed_up)) return st;
-  const auto down = p.inner_low ? dq4_moe_down_kernel<2> : dq4_moe_down_kernel<1>;
-  if (const int st = allow_smem(down, kDownBytes + kMore, dev,
-                                &allowed_down[p.inner_low != nullptr]))
+  if (const int st = allow_smem(dq4_moe_down_kernel, kDownBytes + kMore, dev, &allowed_down))
     return st;
   CUtensorMap w1, w2;
   if (const int st = encode_2d(&w1, CU_TENSOR_MAP_DATA_TYPE_UINT8, p.W1, p.H, 2 * p.I * p.E, p.H,
@@ -748,8 +744,8 @@ int launch_moe(const MoeArgs& p, int dev, int sms, cudaStream_t s) {
   if (const int st = launch_ordered(dq4_moe_up_kernel, grid(p.I, kUpPlaces), kStreamThreads,
                                     kUpBytes + more, s, w1, p))
     return st;
-  if (const int st = launch_ordered(down, grid(p.H, kDownPlaces), kStreamThreads,
-                                    kDownBytes + more, s, w2, p))
+  if (const int st = launch_ordered(dq4_moe_down_kernel, grid(p.H, kDownPlaces),
+                                    kStreamThreads, kDownBytes + more, s, w2, p))
     return st;
   const int64_t per = kCombineThreads * 4;
   return launch_ordered(dq4_moe_combine_kernel,
@@ -804,7 +800,7 @@ int dq4_int8_moe(const void* X, int64_t row_stride, int32_t dtype, int64_t T, in
   at += T * top_k * up256(H * 2);
   p.inner = reinterpret_cast<uint16_t*>(at);
   at += T * top_k * up256(I * 2);
-  if (!p.bf16) p.inner_low = reinterpret_cast<uint16_t*>(at);
+  p.inner_low = reinterpret_cast<uint16_t*>(at);
   at += T * top_k * up256(I * 2);
   p.inner_by = reinterpret_cast<float*>(at);
   at += T * top_k * up256(I / 4);
