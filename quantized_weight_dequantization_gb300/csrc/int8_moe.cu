@@ -5,19 +5,19 @@
 //           scaled by a power of two, and puts it at the places of its choices; the first lists
 //           each expert's (token, choice) pairs, by entries of up to 8
 //   up      a job is 16 inner places of an entry's expert, gate and up rows together: inner =
-//           silu(g) * u in FP16, scaled by a power of two for each 16 places of a pair, and the
-//           largest of each pair's row.  One rounding to 11 bits there would be as much as FP16
-//           results have of their own, and move one BF16 result in ten to its neighbour, so what it
-//           leaves is a second term
-//   down    a job is 32 output places of an entry's expert; inner values are brought to a scale for
-//           their row on their way in, exactly (powers of two)
+//           silu(g) * u in FP32, and the largest of each pair's row
+//   down    a job is 32 output places of an entry's expert; inner values become two terms of FP16 on
+//           their way in, in units of a power of two for their row.  That holds 22 bits of a value, or
+//           2^-39 of its row's largest, where FP16 ends.  (One term's 11 bits are as much as FP16
+//           results have, and move one BF16 result in ten to its neighbour.  A power of two for each
+//           16 places, brought to the row's in FP16, lost what is below 2^-25 of the row.)
 //   combine each token's results by their weights
 // Experts that no token chose have no jobs.  No atomic adds a value.
 //
-// Of 4096 x 14336: one token through 2 of 8 experts 70.5 us, where the bytes take 52 (alone, the
-// four take 5.6, 41.6, 25.5 and 4 us: the two products 0.83 and 0.68 of the copy rate), 23 tokens
-// 240 of 208 (in FP16 254); of 2048 x 1408, 16 tokens through 6 of 64, 92 of 65.  What is left is the ends of
-// the four launches, about 4 us each.
+// Of 4096 x 14336: one token through 2 of 8 experts 73.5 us, where the bytes take 52, 23 tokens 255
+// of 208; of 2048 x 1408, 16 tokens through 6 of 64, 96 of 65.  What is left is the ends of the four
+// launches, about 4 us each, and the second product's (0.68 of the copy rate for one token with one
+// term, where the first has 0.83).
 #include "int8.cuh"
 
 namespace dq4d {
@@ -57,9 +57,7 @@ struct MoeArgs {
   void* Y;
   Routed* r;
   uint16_t* xs;     // [pairs][H] FP16
-  uint16_t* inner;  // [pairs][I] FP16, scaled for each tile of 16
-  uint16_t* inner_low;  // and what that leaves
-  float* inner_by;  // [pairs][I / 16] what a tile has to be multiplied by
+  float* inner;     // [pairs][I in whole chunks], see inner_at
   float* out;       // [pairs][H]
   int* bad;
 };
@@ -261,23 +259,24 @@ __global__ void __launch_bounds__(kRouteThreads) dq4_moe_route_kernel(const MoeA
 // them four at a time.  The weights come by TMA into a ring of the warp's own in shared memory, two
 // chunks ahead, across the ends of jobs (lane 0 issues, all lanes consume); the tokens, which every
 // job of an entry reads, from L2 into registers, while a chunk's weights are waited for (a chunk
-// ahead took 1 % more).  Nothing else synchronizes warps before a job's end.  A job starts at a chunk of its own, so that warps do not go through the
-// tokens side by side and queue at single lines of L2.
+// ahead took 1 % more).  Nothing else synchronizes warps before a job's end.  A job starts at a
+// chunk of its own, so that warps do not go through the tokens side by side and queue at single
+// lines of L2.
 // Copies of 128-byte rows: the TMA takes about 3.5 cycles for a row whatever its width, and at 64
 // bytes a row that bounds the weight's bytes (one token through 11008 x 4096, whose weight alone
 // takes 10.4 us to read: 23.7 us).  Copies of 16 bytes a lane, cp.async, took 13.4 us there.
 // Rings of four chunks leave the tokens less of L1: 16 tokens, 6 of 64 experts, took 97 us, so 92.
 //
-// kBoxes: boxes of weight rows of a chunk.  kScaled: tokens have factors, one for each 16 values.
-// kTerms: FP16 terms of a token's value, the second in an array of its own (going through a chunk
-// once for each, with half of the registers, took 298 us for 23 tokens through 2 of 8 experts of
-// 4096 x 14336; so 254, and one term 240).
+// kBoxes: boxes of weight rows of a chunk.  kTwo: tokens are FP32, and become two terms (23 tokens
+// through 2 of 8 experts of 4096 x 14336 254 us; 298 by going through a chunk once for each, with
+// half of the registers; 259 where they become that before the weights' wait, which spills; 240 with
+// one term).
 // Jobs:
 //   places(job, y)          the first row of each box of weights
 //   tokens(job)             this lane's token (for one that is not there any other, whose results
-//                           are not used), advanced to its 32 c
-//   second()                how far its second term is from it
-//   scales(job, k, f)       with kScaled: the factors of values k .. k + 15 and the 16 after them
+//                           are not used), advanced to its 32 c; its loads are kLoadStep apart
+//   unit(job)               with kTwo: what its values are multiplied by, a power of two that
+//                           brings them into FP16's upper range
 //   begin(job, t)           before a job's products, thread t of its group
 //   finish(job, part, ...)  the group's sums (sum(part, warps, token, row)), thread t of `threads`
 //
@@ -305,8 +304,25 @@ __device__ __forceinline__ int group_warps(uint32_t jobs, uint32_t chunks, uint3
   return best;
 }
 
-template <int kBoxes, bool kScaled, int kTerms>
+// Two values times `unit`: in FP16, and what that leaves.
+__device__ __forceinline__ void two_terms(uint32_t a, uint32_t b, float unit, uint32_t& high,
+                                          uint32_t& low) {
+  const uint64_t minus_one = 0xBF800000BF800000ull;
+  const uint32_t u = __float_as_uint(unit);
+  uint64_t x = uint64_t(b) << 32 | a, left;
+  asm("mul.rn.f32x2 %0, %0, %1;" : "+l"(x) : "l"(uint64_t(u) << 32 | u));
+  high = pack2<DQ4_OUT_F16>(__uint_as_float(uint32_t(x)), __uint_as_float(uint32_t(x >> 32)));
+  __half2 h;
+  memcpy(&h, &high, 4);
+  const float2 f = __half22float2(h);
+  memcpy(&left, &f, 8);
+  asm("fma.rn.f32x2 %0, %0, %1, %2;" : "+l"(left) : "l"(minus_one), "l"(x));
+  low = pack2<DQ4_OUT_F16>(__uint_as_float(uint32_t(left)), __uint_as_float(uint32_t(left >> 32)));
+}
+
+template <int kBoxes, bool kTwo>
 struct Streamed {
+  using Token = std::conditional_t<kTwo, float, uint16_t>;
   static constexpr int kStage = kJobRows * kChunk;
   static constexpr int kPart = kJobRows * kEntry;  // sums of a warp
   static constexpr int kBarsAt = kStreamWarps * kDepth * kStage;
@@ -360,32 +376,29 @@ struct Streamed {
 #pragma unroll 1
     for (int i = 0; i < kDepth; ++i) issue();
     // ---- the tokens, of the next chunk
-    const uint16_t* tok;
-    uint4 x[kTerms][4];
-    float f[2];
+    constexpr int kLoad = 16 / int(sizeof(Token)), kLoads = 32 / kLoad;  // values of a load
+    const Token* tok;
+    uint4 x[kLoads];
+    float unit = 0.f, next_unit = 0.f;
     int64_t tok_job = mine > 0 ? first : all;
     int tok_chunk = 0, tok_left = mine;
     auto tok_open = [&] {
       if (tok_job >= all) return;
       tok = jobs.tokens(tok_job);
+      if constexpr (kTwo) next_unit = jobs.unit(tok_job);
       tok_chunk = start_of(tok_job);
     };
     tok_open();
     auto fetch = [&] {
       if (tok_job >= all) return;
       const int64_t k = int64_t(member + tok_chunk * group) * kChunk;
+      unit = next_unit;
 #pragma unroll
-      for (int t = 0; t < kTerms; ++t) {
-        const uint16_t* from = tok + k;
-        if constexpr (kTerms > 1)
-          if (t) from += jobs.second();
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          x[t][i] = make_uint4(0, 0, 0, 0);  // (past the end)
-          if (k + 32 * c + 8 * i < K) x[t][i] = load_ahead(reinterpret_cast<const uint4*>(from) + i);
-        }
+      for (int i = 0; i < kLoads; ++i) {
+        x[i] = make_uint4(0, 0, 0, 0);  // (past the end)
+        if (k + 32 * c + kLoad * i < K)
+          x[i] = load_ahead(reinterpret_cast<const uint4*>(tok + k) + Jobs::kLoadStep * i);
       }
-      if constexpr (kScaled) jobs.scales(tok_job, k + 32 * c, f);
       if (++tok_chunk == mine) tok_chunk = 0;
       if (--tok_left == 0) {
         tok_left = mine;
@@ -404,6 +417,7 @@ struct Streamed {
     bool ok = true;
     for (int64_t job = first; job < all; job += stride) {
       jobs.begin(job, 32 * member + lane);
+      constexpr int kTerms = kTwo ? 2 : 1;
       float acc[2][4] = {};
 #pragma unroll 1
       for (int i = 0; i < mine && ok; ++i) {
@@ -412,17 +426,13 @@ struct Streamed {
         if (!ok) break;
         uint32_t b[kTerms][16];  // the tokens' operand words
 #pragma unroll
-        for (int t = 0; t < kTerms; ++t)
-#pragma unroll
-          for (int s = 0; s < 16; ++s) {
-            b[t][s] = reinterpret_cast<const uint32_t*>(x[t])[s];
-            if constexpr (kScaled) {
-              __half2 v;
-              memcpy(&v, &b[t][s], 4);
-              v = __hmul2(v, __float2half2_rn(f[s >> 3]));
-              memcpy(&b[t][s], &v, 4);
-            }
-          }
+        for (int s = 0; s < 16; ++s) {
+          const uint32_t* w = reinterpret_cast<const uint32_t*>(x);
+          if constexpr (kTwo)
+            two_terms(w[2 * s], w[2 * s + 1], unit, b[0][s], b[1][s]);
+          else
+            b[0][s] = w[s];
+        }
         const uint32_t at = ring + slot * kStage;
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
@@ -531,9 +541,20 @@ __device__ __forceinline__ Entries load_entries(const MoeArgs& p, uint8_t* smem)
   return s;
 }
 
+// Inner values lie as they are read: of a chunk lane c's i-th four, 32 c + 4 i, stand beside those of
+// the other lanes, so that a load takes one line of a token.  (In their own order it took four, and
+// 23 tokens through 2 of 8 experts of 4096 x 14336 took 26 us more.)
+__device__ __forceinline__ int64_t inner_at(int64_t k) {
+  return (k & ~int64_t(kChunk - 1)) + ((k >> 2 & 7) << 4) + ((k >> 5 & 3) << 2) + (k & 3);
+}
+__host__ __device__ __forceinline__ int64_t inner_width(int64_t I) {
+  return (I + kChunk - 1) / kChunk * kChunk;
+}
+
 // ---------------------------------------------------------------------------- up
 struct UpJobs {
-  using S = Streamed<2, false, 1>;
+  using S = Streamed<2, false>;
+  static constexpr int kLoadStep = 1;
   const MoeArgs& p;
   Entries s;
   float s_gate, s_up;  // scales of this thread's place
@@ -582,17 +603,9 @@ struct UpJobs {
 #pragma unroll
       for (int o = 8; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(kAllLanes, top, o));
       if (j < count) {
-        float up, down;
-        pow2_scaling(__uint_as_float(top), up, down);
         const int64_t at = first + j;
-        const __half high = __float2half_rn(v * up);
-        p.inner[at * p.I + tile * kUpPlaces + place] = __half_as_ushort(high);
-        p.inner_low[at * p.I + tile * kUpPlaces + place] =
-            __half_as_ushort(__float2half_rn(v * up - __half2float(high)));
-        if (place == 0) {
-          p.inner_by[at * (p.I / kUpPlaces) + tile] = down;
-          atomicMax(p.r->top + at, top);
-        }
+        p.inner[at * inner_width(p.I) + inner_at(tile * kUpPlaces + place)] = v;
+        if (place == 0) atomicMax(p.r->top + at, top);
       }
     }
   }
@@ -612,7 +625,8 @@ __global__ void __launch_bounds__(kStreamThreads, kCtas)
 
 // -------------------------------------------------------------------------- down
 struct DownJobs {
-  using S = Streamed<1, true, 2>;
+  using S = Streamed<1, true>;
+  static constexpr int kLoadStep = 4;
   const MoeArgs& p;
   Entries s;
   float s_place;  // scale of this thread's place
@@ -634,19 +648,10 @@ struct DownJobs {
     const int entry = entry_of(job, tile);
     return min(s.first[entry] + (int(threadIdx.x & 31) >> 2), s.first[entry + 1] - 1);
   }
-  __device__ __forceinline__ const uint16_t* tokens(int64_t job) const {
-    return p.inner + pair_of(job) * p.I + 32 * (threadIdx.x & 3);
+  __device__ __forceinline__ const float* tokens(int64_t job) const {
+    return p.inner + pair_of(job) * inner_width(p.I) + 4 * (threadIdx.x & 3);
   }
-  __device__ __forceinline__ int64_t second() const { return p.inner_low - p.inner; }
-  // A tile's FP16 values in the row's unit: powers of two, both.
-  __device__ __forceinline__ void scales(int64_t job, int64_t k, float (&f)[2]) const {
-    const int at = pair_of(job);
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-      f[h] = k + 16 * h < p.I
-                 ? load_ahead(p.inner_by + at * (p.I / kUpPlaces) + k / kUpPlaces + h) * s.up[at]
-                 : 0.f;
-  }
+  __device__ __forceinline__ float unit(int64_t job) const { return s.up[pair_of(job)]; }
   __device__ __forceinline__ void begin(int64_t job, int t) {
     int tile;
     const int entry = entry_of(job, tile);
@@ -765,7 +770,7 @@ int64_t dq4_int8_moe_workspace_bytes(int64_t T, int64_t H, int64_t I, int32_t to
       H > kMaxHidden || I > kMaxInner)
     return 0;
   return up256(sizeof(Routed)) +
-         T * top_k * (up256(H * 2) + 2 * up256(I * 2) + up256(I / 4) + up256(H * 4));
+         T * top_k * (up256(H * 2) + inner_width(I) * 4 + up256(H * 4));
 }
 
 int dq4_int8_moe(const void* X, int64_t row_stride, int32_t dtype, int64_t T, int64_t H, int64_t I,
@@ -791,19 +796,14 @@ int dq4_int8_moe(const void* X, int64_t row_stride, int32_t dtype, int64_t T, in
   int dev, sms;
   if (const int st = current_device(&dev, &sms)) return st;
   MoeArgs p = {X, row_stride, dtype == DQ4_OUT_BF16, int(T), int(E), top_k, renormalize, H, I,
-               logits, W1, W2, S1, S2, ids, weights, Y, nullptr, nullptr, nullptr, nullptr, nullptr,
-               nullptr, bad};
+               logits, W1, W2, S1, S2, ids, weights, Y, nullptr, nullptr, nullptr, nullptr, bad};
   char* at = static_cast<char*>(workspace);
   p.r = reinterpret_cast<Routed*>(at);
   at += up256(sizeof(Routed));
   p.xs = reinterpret_cast<uint16_t*>(at);
   at += T * top_k * up256(H * 2);
-  p.inner = reinterpret_cast<uint16_t*>(at);
-  at += T * top_k * up256(I * 2);
-  p.inner_low = reinterpret_cast<uint16_t*>(at);
-  at += T * top_k * up256(I * 2);
-  p.inner_by = reinterpret_cast<float*>(at);
-  at += T * top_k * up256(I / 4);
+  p.inner = reinterpret_cast<float*>(at);
+  at += T * top_k * inner_width(I) * 4;
   p.out = reinterpret_cast<float*>(at);
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   return launch_moe(p, dev, sms, s);

@@ -56,3 +56,30 @@ def test_moe_results_are_rounded_once(dq, kind, I):
     y = dq.int8_moe(x, logits, dev(w1), dev(s1), dev(w2), dev(s2), 1)
     want, _, _, size, unit = defs.moe(host(x), host(logits), w1, s1, w2, s2, 1, True)
     rounded_once(y, want, moe_off(unit, size, H, I), kind, (kind, I))
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f16"])
+@pytest.mark.parametrize("spread", [12, 18, 24, 27, 33])
+def test_moe_small_inner_values_beside_large_ones(dq, kind, spread):
+    """Inner values 2^spread below their row's largest, and results that take the small ones alone
+    (codes of 0 at the others): held to 2^-22, or to 2^-39 of the row's largest."""
+    rng = np.random.default_rng(spread)
+    T, H, I, E = 19, 64, 96, 2
+    x = dev(rng.normal(size=(T, H)).astype(np.float32), DT[kind])
+    logits = dev(rng.normal(size=(T, E)).astype(np.float32))
+    w1, s1 = weight(rng, E, 2 * I, H)
+    w2, s2 = weight(rng, E, H, I)
+    s1[:, I:] *= 2.0 ** -spread  # of the rows of Wu,
+    s1[:, I:I + 5] *= 2.0 ** spread  # all but a few places of one tile
+    w2[:, 16:, :5] = 0
+    s2[:, 16:] *= 2.0 ** spread
+    y = dq.int8_moe(x, logits, dev(w1), dev(s1), dev(w2), dev(s2), 2)
+    want, ids, weights, size, unit = defs.moe(host(x), host(logits), w1, s1, w2, s2, 2, True)
+    floor = np.zeros_like(want)
+    for t in range(T):
+        for e, p in zip(ids[t], weights[t]):
+            both = (w1[e] * (s1[e].astype(np.float64)[:, None] / 127)) @ host(x)[t]
+            top = np.abs(both[:I] / (1 + np.exp(-both[:I])) * both[I:]).max()
+            v = np.abs(w2[e].astype(np.float64)) * (s2[e].astype(np.float64)[:, None] / 127)
+            floor[t] += p * 2.0 ** -39 * top * v.sum(1)
+    rounded_once(y, want, moe_off(unit, size, H, I) + floor, kind, (kind, spread))
