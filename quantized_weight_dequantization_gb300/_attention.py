@@ -77,10 +77,13 @@ def _workspace(workspace, need: int, what: str, like: torch.Tensor, handle) -> t
     index = like.get_device()
     if handle == torch._C._cuda_getCurrentRawStream(index):
         return _stream_workspace(need, what, like, index, handle)
-    stream = (torch.cuda.ExternalStream(handle, index) if handle else
-              torch.cuda.default_stream(index))
-    with torch.cuda.stream(stream):
+    with torch.cuda.stream(_stream_of(handle, index)):
         return _stream_workspace(need, what, like, index, handle)
+
+
+def _stream_of(handle: int, index: int):
+    return (torch.cuda.ExternalStream(handle, index) if handle else
+            torch.cuda.default_stream(index))
 
 
 def _stream_workspace(need: int, what: str, like: torch.Tensor, index: int, handle):

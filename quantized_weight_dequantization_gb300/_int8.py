@@ -13,7 +13,7 @@ from typing import NamedTuple, Optional
 
 import torch
 
-from ._attention import _COUNTERS, _HALF, _bad, _flat, _stream, _workspace
+from ._attention import _COUNTERS, _HALF, _bad, _flat, _stream, _stream_of, _workspace
 from ._binding import _DTYPE_CODE, Dq4Error, _call_lock, get_lib
 
 # bytes of a new workspace that have to be zero (None: all of them)
@@ -297,6 +297,11 @@ def int8_linear_backward(dY: torch.Tensor, CB: torch.Tensor, SCB: torch.Tensor,
 
 
 # ------------------------------------------------------------- mixture of experts
+def _routing(T: int, top_k: int, like: torch.Tensor):
+    return (torch.empty((T, top_k), dtype=torch.int32, device=like.device),
+            torch.empty((T, top_k), dtype=torch.float32, device=like.device))
+
+
 def int8_moe(X: torch.Tensor, logits: torch.Tensor, w1: torch.Tensor, s1: torch.Tensor,
              w2: torch.Tensor, s2: torch.Tensor, top_k: int, renormalize: bool = True,
              return_routing: bool = False, workspace: Optional[torch.Tensor] = None,
@@ -340,12 +345,14 @@ def int8_moe(X: torch.Tensor, logits: torch.Tensor, w1: torch.Tensor, s1: torch.
                             workspace, bad, stream)
     if not 1 <= top_k <= min(E, 16):
         raise ValueError(f"top_k must be 1 .. {min(E, 16)}, got {top_k}")
-    device = X.device
-    ids = torch.empty((T, top_k), dtype=torch.int32, device=device)
-    weights = torch.empty((T, top_k), dtype=torch.float32, device=device)
-    Y = torch.empty((T, H), dtype=X.dtype, device=device)
     bad_ptr = None if bad is None else _bad(bad, X)
     handle = _stream(stream, index)
+    Y = torch.empty((T, H), dtype=X.dtype, device=X.device)
+    if return_routing or handle == torch._C._cuda_getCurrentRawStream(index):
+        ids, weights = _routing(T, top_k, X)
+    else:  # nobody else holds them: memory of the stream that uses them, which is given back to it
+        with torch.cuda.stream(_stream_of(handle, index)):
+            ids, weights = _routing(T, top_k, X)
     need = _need_of(index, "moe", T, H, I, top_k)
     with _call_lock(index, handle):
         ws_ptr, ws_bytes = _scratch(workspace, need, "int8 moe", X, handle)

@@ -83,3 +83,29 @@ def test_moe_small_inner_values_beside_large_ones(dq, kind, spread):
             v = np.abs(w2[e].astype(np.float64)) * (s2[e].astype(np.float64)[:, None] / 127)
             floor[t] += p * 2.0 ** -39 * top * v.sum(1)
     rounded_once(y, want, moe_off(unit, size, H, I) + floor, kind, (kind, spread))
+
+
+def test_moe_on_a_stream_of_its_own(dq):
+    """What the call alone holds stays its own until the stream given is done with it, whatever the
+    current stream allocates and writes meanwhile."""
+    rng = np.random.default_rng(3)
+    T, H, I, E, k = 8, 64, 32, 6, 2
+    args = [dev(rng.normal(size=(T, H)).astype(np.float32), torch.float16),
+            dev(rng.normal(size=(T, E)).astype(np.float32)),
+            *(dev(a) for a in weight(rng, E, 2 * I, H)), *(dev(a) for a in weight(rng, E, H, I))]
+    want = dq.int8_moe(*args, k)
+    stream = torch.cuda.Stream()
+    dq.int8_moe(*args, k, stream=stream)  # (the stream's workspace is there)
+    torch.cuda.synchronize()
+    for _ in range(3):
+        with torch.cuda.stream(stream):
+            torch.cuda._sleep(20_000_000)  # (about 10 ms)
+        y = dq.int8_moe(*args, k, stream=stream)
+        others = [torch.full((T, k), 77, dtype=torch.int32, device="cuda") for _ in range(64)]
+        torch.cuda.synchronize()
+        assert torch.equal(y, want)
+        assert all((t == 77).all() for t in others)
+        y, ids, weights = dq.int8_moe(*args, k, return_routing=True, stream=stream)
+        stream.synchronize()
+        assert torch.equal(y, want) and ids.shape == weights.shape == (T, k)
+        assert torch.allclose(weights.sum(1), torch.ones(T, device="cuda"))
