@@ -74,8 +74,10 @@ int64_t dq4_int8_quantize_workspace_bytes(int64_t K);
  *   bias      `out_dtype`[N] or NULL
  *   Y         `out_dtype` (FP16, BF16 or FP32) [M][N], row-major
  * The sum over codes is exact while it and its parts stay below 2^24 (always up to K = 1040),
- * beyond that rounded as FP32 sums are; outlier products are exact to 2^-22.  A row whose scale
- * is NaN, or with an outlier that is not finite, is NaN.
+ * beyond that, and together with outliers, rounded as FP32 sums are.  In products of many rows an
+ * outlier is held to 2^-22 of it, or 2^-25 of the larger of scales[m] / 127 and 2^-14 of the
+ * row's largest outlier, and codes beside one above 2^32 scales[m] to 2^-39 of it; products of few
+ * rows hold both to FP32.  A row whose scale is NaN, or with an outlier that is not finite, is NaN.
  * K % 16 == 0, codes and CB 16-byte aligned, M, N, K < 2^31, M * K and N * K < 2^47.
  */
 int dq4_int8_linear(const int8_t* codes, const float* scales, const int8_t* CB, const float* SCB,

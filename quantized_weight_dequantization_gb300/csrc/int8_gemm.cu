@@ -865,8 +865,8 @@ struct RowArgs {
 // place of its code as x / u, in two FP16 terms, the second in a column of its own past K, where
 // the weight's column stands again: the CTAs past row_ctas gather those columns (gathered in the
 // product itself, for each tile again, 4096 rows with 13 such columns through 4096 x 11008 took 293
-// us; so 274).  FP16 ends at 65504: where an outlier is above 2^15 u, the unit is 2^-15 of it, and
-// codes are rounded to FP16 with what they are in it.
+// us; so 274).  FP16 ends at 65504 and 2^-24: where an outlier is above 2^15 u, the unit is 2^e u, the
+// least that it is not above 2^15 of, and codes are 2^-e of theirs, exactly up to e = 24.
 // A warp takes 512 values of a row, 16 a lane (so spread, 512 rows through 4096 x 4096 take 22.8
 // us; 2048 values a warp, loaded at once, 25.4).
 constexpr int kRowPart = 512;
@@ -933,13 +933,17 @@ __global__ void __launch_bounds__(256) int8_rows_kernel(const RowArgs p) {
         top = max(top, __float_as_uint(x[j]) & 0x7FFFFFFFu);
       }
       top = __reduce_max_sync(kAllLanes, top);
-      const float own = unit;
-      if (top < 0x7F800000u) {
-        unit = fmaxf(fmaxf(unit, __uint_as_float(top) * 3.0517578125e-05f), 7.888609052210118e-31f);
-        ratio = own == unit ? 1.f : __fdiv_rn(own, unit);
-        if (own != own) unit = own;
-      } else {
+      const float most = __uint_as_float(top) * 3.0517578125e-05f;  // 2^-15 of the largest outlier
+      if (top >= 0x7F800000u) {
         unit = __uint_as_float(0x7FC00000u);
+      } else if (unit == 0.f) {  // (a scale of 0: codes count for nothing)
+        unit = fmaxf(most, 1.17549435e-38f);
+        ratio = 0.f;
+      } else if (fabsf(unit) < most) {
+        int e = ilogbf(most) - ilogbf(unit);
+        if (fabsf(scalbnf(unit, e)) < most) ++e;
+        unit = scalbnf(unit, e);
+        ratio = scalbnf(1.f, -e);
       }
     }
     if (k < codes_end) {

@@ -109,3 +109,81 @@ def test_moe_on_a_stream_of_its_own(dq):
         stream.synchronize()
         assert torch.equal(y, want) and ids.shape == weights.shape == (T, k)
         assert torch.allclose(weights.sum(1), torch.ones(T, device="cuda"))
+
+
+# ------------------------------------------------------------- the product
+def integer_rows(rng, M, N, K, cols, largest, kind):
+    """Codes, weight codes and outliers whose products all are whole numbers, with the result: with
+    scales of 127 and 127 a code's and a weight's unit are 1 (127 RN32(1/127) is 1)."""
+    codes = rng.integers(-127, 128, (M, K)).astype(np.int8)
+    CB = rng.integers(-127, 128, (N, K)).astype(np.int8)
+    scale = np.full(M, 127, np.float32), np.full(N, 127, np.float32)
+    if not cols:
+        return codes, CB, scale, None, codes.astype(np.int64) @ CB.astype(np.int64).T
+    codes[:, cols] = 0
+    CB[:, cols] = rng.integers(-3, 4, (N, len(cols)))
+    out = np.rint(rng.uniform(-largest, largest, (M, len(cols))))
+    out[:, 0] = largest
+    out = host(dev(out.astype(np.float32), DT[kind])).astype(np.int64)
+    y = codes.astype(np.int64) @ CB.astype(np.int64).T + out @ CB[:, cols].astype(np.int64).T
+    return codes, CB, scale, out, y
+
+
+@pytest.mark.parametrize("M", [1, 16, 17, 40, 129, 300])
+@pytest.mark.parametrize("K", [16, 208, 1040])
+@pytest.mark.parametrize("largest,kind", [(0, "f16"), (300, "f16"), (40000, "f16"),
+                                          (65504, "f16"), (3 << 16, "bf16"), (1 << 20, "bf16")])
+def test_linear_whole_numbers(dq, M, K, largest, kind):
+    """Sums of codes are exact up to K = 1040, and so they are beside outliers far above them: FP32
+    results bit for bit.  (Everything is a whole number below 2^24.)"""
+    rng = np.random.default_rng(M + K + largest)
+    cols = [1, K - 3] if largest else []
+    codes, CB, (scales, SCB), out, want = integer_rows(rng, M, 150, K, cols, largest, kind)
+    assert np.abs(want).max() < 1 << 24
+    rows = dq.Int8Rows(dev(codes), dev(scales))
+    if cols:
+        rows = rows._replace(cols=dev(np.array(cols)), outliers=dev(out.astype(np.float32), DT[kind]))
+    y = dq.int8_linear(rows, dev(CB), dev(SCB), out_dtype=torch.float32)
+    assert np.array_equal(host(y), want), np.abs(host(y) - want).max()
+
+
+@pytest.mark.parametrize("M", [8, 50])
+@pytest.mark.parametrize("top", [300.0, 1000.0, 3000.0, 60000.0])
+def test_linear_codes_beside_a_large_outlier(dq, M, top):
+    """Results that take the codes alone (a weight of 0 at the outlier) keep 2^-21 of them; those
+    that take both are FP32 sums of K / 16 steps beside it."""
+    rng = np.random.default_rng(int(top))
+    K, N = 1040, 130
+    CB, SCB = weight(rng, N, K)
+    x = rng.uniform(-1, 1, (M, K))
+    x[:, 7], x[0, 7] = top * rng.uniform(0.5, 1, M), 0.0
+    CB[::2, 7] = 0
+    CB[1::4, 7] = 1
+    rows = dq.int8_quantize(dev(x.astype(np.float32), torch.float16), 6.0, 8)
+    y = dq.int8_linear(rows, dev(CB), dev(SCB), out_dtype=torch.float32)
+    want, size = defs.linear(rows.codes.cpu().numpy(), host(rows.scales), CB, SCB,
+                             rows.cols.cpu().numpy(), host(rows.outliers))
+    tol = (2.0 ** -21 + np.where(CB[:, 7] != 0, K / 16 * 2.0 ** -23, 0)) * size
+    assert (np.abs(host(y) - want) <= tol).all(), np.abs((host(y) - want) / size).max(0)
+
+
+@pytest.mark.parametrize("M", [5, 60])
+def test_linear_scales_far_from_one(dq, M):
+    """Scales that only a caller's own rows have, beside outliers: of 0, negative, the smallest of
+    the quantizer's and below; rows without a value above 0."""
+    rng = np.random.default_rng(M)
+    K, N = 96, 40
+    CB, SCB = weight(rng, N, K)
+    codes = rng.integers(-127, 128, (M, K)).astype(np.int8)
+    scales = rng.uniform(0.5, 2, M).astype(np.float32)
+    out = rng.normal(size=(M, 4)) * 20
+    scales[0], scales[1], scales[2], scales[3] = 0.0, -1.5, 2.0 ** -100, 1e-35
+    out[2:4] = out[2:4] * 1e-30
+    scales[4], out[4] = 0.0, 0.0
+    cols = np.array([0, 5, 64, 95])
+    rows = dq.Int8Rows(dev(codes), dev(scales), dev(cols),
+                       dev(out.astype(np.float32), torch.bfloat16))
+    y = dq.int8_linear(rows, dev(CB), dev(SCB), out_dtype=torch.float32)
+    want, size = defs.linear(codes, scales, CB, SCB, cols, host(rows.outliers))
+    tol = (2.0 ** -21 + (K / 16 + 4) * 2.0 ** -23) * size
+    assert (np.abs(host(y) - want) <= tol).all(), np.abs((host(y) - want) / (size + 1e-300)).max(1)
