@@ -16,15 +16,14 @@
  * same: codes int8[M][K], scales FP32[M].
  *
  * Workspaces: device memory, 256-byte aligned, of at least the bytes that the function beside
- * the entry point gives (-DQ4_ERR_DEVICE if no device answers), zero before their first use (the
- * quantizer's all of it, the products' first 4096 bytes; the expert layer's holds anything); a
- * completed call leaves a workspace ready for later calls of the same entry point, of any shape
- * that it is large enough for, in the same stream (not for concurrent calls or replays of
- * captured ones).
+ * the entry point gives (-DQ4_ERR_DEVICE if no device answers), the quantizer's zero before its
+ * first use (the others hold anything); a completed call leaves a workspace ready for later calls
+ * of the same entry point, of any shape that it is large enough for, in the same stream (not for
+ * concurrent calls or replays of captured ones).
  *
  * `bad` is an optional device int (NULL to skip) that counts what a call could not do, as each
- * entry point says, and waits inside a kernel that ran out (never expected; the workspace must
- * then be cleared again); it stays 0 for valid inputs.
+ * entry point says, and waits inside a kernel that ran out (never expected; results of that call
+ * are not to be used); it stays 0 for valid inputs.
  */
 #ifndef DQ4_INT8_H
 #define DQ4_INT8_H

@@ -17,8 +17,7 @@ from ._attention import _COUNTERS, _HALF, _bad, _flat, _stream, _stream_of, _wor
 from ._binding import _DTYPE_CODE, Dq4Error, _call_lock, get_lib
 
 # bytes of a new workspace that have to be zero (None: all of them)
-_COUNTERS.update({"int8 quantize": None, "int8 linear": 4096, "int8 backward": 4096,
-                  "int8 moe": 0})
+_COUNTERS.update({"int8 quantize": None, "int8 linear": 0, "int8 backward": 0, "int8 moe": 0})
 
 _LIB = None
 
@@ -167,9 +166,10 @@ def int8_linear(X: Int8Rows, CB: torch.Tensor, SCB: torch.Tensor,
 
     Outlier columns of X multiply W's values as the 16-bit numbers they are.  ``bias`` ([N]) and
     Y are of ``out_dtype`` (float16, bfloat16 or float32).  K must be a multiple of 16.
-    ``workspace`` (uint8, zero-filled before its first use) holds X in 16 bits and partial sums;
-    by default a cached buffer per (device, stream) is used, and in ``torch.cuda.graph`` memory
-    of the graph's own.  ``bad`` (int32) counts columns that cannot be used.
+    ``workspace`` (uint8) holds X in 16 bits and partial sums; by default a cached buffer per
+    (device, stream) is used, and in ``torch.cuda.graph`` memory of the graph's own.  ``bad``
+    (int32) counts columns that cannot be used, and waits inside a kernel that ran out, after which
+    Y is not to be used.
     """
     codes, scales, cols, outliers, _ = X
     M, K = codes.shape if codes.dim() == 2 else (-1, -1)
@@ -257,7 +257,7 @@ def int8_linear_backward(dY: torch.Tensor, CB: torch.Tensor, SCB: torch.Tensor,
 
     dY is M x N (float16 or bfloat16, contiguous); W's values are rounded to its type, as
     :func:`int8_correction_prep` has them.  N must be a multiple of 8, K of 16.  ``workspace``
-    and ``bad`` as for :func:`int8_linear`.
+    (of partial sums) and ``bad`` as for :func:`int8_linear`.
     """
     index = dY.get_device()
     # (first the short way that valid arguments pass, as in int8_linear)
@@ -315,9 +315,9 @@ def int8_moe(X: torch.Tensor, logits: torch.Tensor, w1: torch.Tensor, s1: torch.
     Wg, then those of Wu, ``w2`` int8 [E, H, I]; ``s1`` [E, 2 I] and ``s2`` [E, H] are float32
     scales of their rows, a value w * s / 127.  H and I are multiples of 16.  Returns Y (T x H,
     X's dtype), or (Y, ids, weights) with the choices, int32 and float32 [T, top_k].
-    ``workspace`` (uint8) holds the rows between the launches;
-    by default a cached buffer per (device, stream) is used, and in ``torch.cuda.graph`` memory
-    of the graph's own.
+    ``workspace`` (uint8) holds the rows between the launches; by default a cached buffer per
+    (device, stream) is used, and in ``torch.cuda.graph`` memory of the graph's own.  ``bad``
+    (int32) counts waits inside a kernel that ran out, after which Y is not to be used.
     """
     index = X.get_device()
     T, H = X.shape if X.dim() == 2 else (-1, -1)

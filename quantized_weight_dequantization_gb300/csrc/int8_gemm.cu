@@ -858,6 +858,8 @@ struct RowArgs {
   uint16_t* X;     // [M][width]
   float* units;    // [M]
   int8_t* columns; // [N][width - codes_end] the weight's columns of the outliers' second terms
+  int* count;      // [counts] the product's counters, to be cleared
+  int counts;
   int* bad;
 };
 
@@ -875,6 +877,8 @@ __global__ void __launch_bounds__(256) int8_rows_kernel(const RowArgs p) {
   __shared__ int s_col[256];  // of entry t, -1 if it is not used
   asm volatile("griddepcontrol.launch_dependents;");
   const int t = threadIdx.x, lane = t & 31;
+  if (blockIdx.x == 0)
+    for (int i = t; i < p.counts; i += 256) p.count[i] = 0;
   if (p.L > 0) {
     int64_t col = -1;
     // used: in range and above all before it (the largest so far, by warps and then over them)
@@ -1065,6 +1069,10 @@ int k_steps(int64_t K) { return int((K + kStep - 1) / kStep); }
 int code_steps(int64_t K, int L) { return L > 0 ? (k_steps(K) + 1) / 2 * 2 : k_steps(K); }
 int all_steps(int64_t K, int L) { return code_steps(K, L) + k_steps(L); }
 
+// The counters of parts that the product uses.  A call that completes leaves them at 0; they are
+// cleared all the same, so that one whose waits ran out costs nothing but its own results.
+int counters(const Plan& pl) { return pl.split ? pl.ctas : 0; }
+
 int64_t part_bytes(const Plan& pl) {
   return pl.split ? int64_t(pl.ctas) * 2 * pl.bx * kTileW * 4 : 0;
 }
@@ -1121,6 +1129,8 @@ int launch_int8_gemm(const Int8Linear& a, int dev, int sms, void* workspace, cud
   r.X = X;
   r.units = units;
   r.columns = columns;
+  r.count = count;
+  r.counts = counters(pl);
   r.bad = a.bad;
   const int64_t gathers = (a.N * extra / 16 + 255) / 256;
   const int64_t row_kernel_ctas = r.row_ctas + (gathers < 4 * sms ? gathers : 4 * sms);
@@ -1169,6 +1179,9 @@ int launch_int8_backward(const Int8Backward& a, int dev, int sms, void* workspac
   p.count = static_cast<int*>(workspace);
   p.bad = a.bad;
   char* part = static_cast<char*>(workspace) + kInt8Counters;
+  if (pl.split)
+    if (const cudaError_t e = cudaMemsetAsync(p.count, 0, size_t(counters(pl)) * 4, stream))
+      return fail_cuda(DQ4_ERR_LAUNCH, e);
   return a.bf16 ? launch_plan<true, true>(pl, w, x, w, p, dev, part, stream)
                 : launch_plan<true, false>(pl, w, x, w, p, dev, part, stream);
 }

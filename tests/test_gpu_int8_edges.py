@@ -142,7 +142,8 @@ def test_linear_whole_numbers(dq, M, K, largest, kind):
     assert np.abs(want).max() < 1 << 24
     rows = dq.Int8Rows(dev(codes), dev(scales))
     if cols:
-        rows = rows._replace(cols=dev(np.array(cols)), outliers=dev(out.astype(np.float32), DT[kind]))
+        rows = rows._replace(cols=dev(np.array(cols)),
+                             outliers=dev(out.astype(np.float32), DT[kind]))
     y = dq.int8_linear(rows, dev(CB), dev(SCB), out_dtype=torch.float32)
     assert np.array_equal(host(y), want), np.abs(host(y) - want).max()
 
@@ -187,3 +188,69 @@ def test_linear_scales_far_from_one(dq, M):
     want, size = defs.linear(codes, scales, CB, SCB, cols, host(rows.outliers))
     tol = (2.0 ** -21 + (K / 16 + 4) * 2.0 ** -23) * size
     assert (np.abs(host(y) - want) <= tol).all(), np.abs((host(y) - want) / (size + 1e-300)).max(1)
+
+
+# ------------------------------------------------------------- equal runs of stages
+def up256(n):
+    return (n + 255) // 256 * 256
+
+
+def steps_of(n):
+    return -(-n // 64)
+
+
+def width_of_runs(need, before, lanes, M, steps):
+    """The tile width of a product whose CTAs take equal runs of stages, by the size of its
+    workspace, which then has two parts of a tile for each CTA behind `before` bytes; else 0."""
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    if need == before:
+        return 0
+    for width in (64, 128, 256):
+        tiles = -(-M // width) * -(-lanes // 128)
+        if need - before == min(tiles * (-(-steps // 2)), sms) * 2 * width * 128 * 4:
+            return width
+    raise AssertionError((need, before))
+
+
+def linear_runs(dq, M, N, K, L):
+    code_steps = steps_of(K) if L == 0 else (steps_of(K) + 1) // 2 * 2
+    steps = code_steps + steps_of(L)
+    before = 4096 + up256(N * steps_of(L) * 64) + up256(M * 4) + up256(M * steps * 128)
+    need = dq.get_lib().dq4_int8_linear_workspace_bytes(M, N, K, L)
+    return width_of_runs(need, before, N, M, steps)
+
+
+def backward_runs(dq, M, N, K):
+    need = dq.get_lib().dq4_int8_linear_backward_workspace_bytes(M, N, K)
+    return width_of_runs(need, 4096, K, M, steps_of(N))
+
+
+def gpu_weight(N, K, seed):
+    gen = torch.Generator("cuda").manual_seed(seed)
+    CB = torch.randint(-127, 128, (N, K), dtype=torch.int8, device="cuda", generator=gen)
+    return CB, (0.5 + torch.rand(N, device="cuda", generator=gen)) * (4 / K ** 0.5)
+
+
+def gpu_rows(dq, M, K, loud, seed, kind=torch.bfloat16, most=24):
+    gen = torch.Generator("cuda").manual_seed(seed)
+    x = torch.randn(M, K, device="cuda", generator=gen) * 0.8
+    x[:, torch.randperm(K, device="cuda", generator=gen)[:loud]] *= 12
+    return dq.int8_quantize(x.to(kind), 6.0 if loud else 0.0, most)
+
+
+def test_counters_that_a_call_left_behind(dq):
+    """A call whose wait ran out may leave counts of a tile's parts: the next one does without."""
+    M, N, K = 60, 20000, 3008
+    assert linear_runs(dq, M, N, K, 0) and backward_runs(dq, M, 22000, 3008)
+    CB, SCB = gpu_weight(N, K, 1)
+    rows = gpu_rows(dq, M, K, 0, 2)
+    dy = torch.randn(M, 22000, device="cuda").half()
+    W = gpu_weight(22000, 3008, 3)
+    want = dq.int8_linear(rows, CB, SCB), dq.int8_linear_backward(dy, *W)
+    ws = torch.zeros(1 << 26, dtype=torch.uint8, device="cuda")
+    for left in (1, 7):
+        for call, is_ in ((lambda: dq.int8_linear(rows, CB, SCB, workspace=ws), want[0]),
+                          (lambda: dq.int8_linear_backward(dy, *W, workspace=ws), want[1])):
+            ws[:4096].view(torch.int32).fill_(left)
+            for _ in range(2):
+                assert torch.equal(call(), is_), left
