@@ -115,8 +115,8 @@ int64_t dq4_int8_linear_backward_workspace_bytes(int64_t M, int64_t N, int64_t K
  * Activations are FP16 in the products, a power of two for each row keeping them in its range
  * (BF16 rows lose nothing down to 2^-31 of their largest value); the inner values are held in
  * two terms of 11 bits: to 2^-22 of them, or 2^-39 of the largest of their row.
- * T 0 .. 256, E 1 .. 1024, top_k 1 .. min(E, 16), H up to 32768 and I up to 2^20, both multiples
- * of 16, E * I * H < 2^47; weights 16-byte aligned, X 16-byte aligned with row_stride % 8 == 0.
+ * T 0 .. 256, E 1 .. 1024, top_k 1 .. min(E, 16), H 16 .. 32768 and I 16 .. 2^20, both multiples
+ * of 16, E * I * H < 2^47 (H and I may be 0 without tokens); weights 16-byte aligned, X 16-byte aligned with row_stride % 8 == 0.
  */
 int dq4_int8_moe(const void* X, int64_t row_stride, int32_t dtype, int64_t T, int64_t H, int64_t I,
                  int64_t E, const float* logits, int32_t top_k, int32_t renormalize,

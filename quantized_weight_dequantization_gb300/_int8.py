@@ -313,8 +313,9 @@ def int8_moe(X: torch.Tensor, logits: torch.Tensor, w1: torch.Tensor, s1: torch.
     equal, weighted by their softmax over the chosen ones (``renormalize``) or over all:
     ``y = sum p_e W2_e (silu(Wg_e x) * (Wu_e x))``.  ``w1`` int8 [E, 2 I, H] holds the rows of
     Wg, then those of Wu, ``w2`` int8 [E, H, I]; ``s1`` [E, 2 I] and ``s2`` [E, H] are float32
-    scales of their rows, a value w * s / 127.  H and I are multiples of 16.  Returns Y (T x H,
-    X's dtype), or (Y, ids, weights) with the choices, int32 and float32 [T, top_k].
+    scales of their rows, a value w * s / 127.  H and I are multiples of 16, and not 0 with tokens.
+    Returns Y (T x H, X's dtype), or (Y, ids, weights) with the choices, int32 and float32
+    [T, top_k].
     ``workspace`` (uint8) holds the rows between the launches; by default a cached buffer per
     (device, stream) is used, and in ``torch.cuda.graph`` memory of the graph's own.  ``bad``
     (int32) counts waits inside a kernel that ran out, after which Y is not to be used.

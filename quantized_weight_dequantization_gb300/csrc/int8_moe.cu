@@ -783,8 +783,8 @@ int dq4_int8_moe(const void* X, int64_t row_stride, int32_t dtype, int64_t T, in
       I % 16 != 0 || E * H * I >= int64_t(1) << 47)
     return DQ4_ERR_N;
   if (!valid_dtype(dtype, false)) return DQ4_ERR_DTYPE;
-  if (T == 0 || H == 0) return DQ4_OK;
-  if (I == 0) return DQ4_ERR_N;
+  if (T == 0) return DQ4_OK;
+  if (H == 0 || I == 0) return DQ4_ERR_N;
   if (!X || !logits || !W1 || !S1 || !W2 || !S2 || !ids || !weights || !Y) return DQ4_ERR_NULL;
   if (misaligned(X, 16) || row_stride % 8 != 0 || misaligned(logits, 4) || misaligned(W1, 16) ||
       misaligned(W2, 16) || misaligned(S1, 4) || misaligned(S2, 4) || misaligned(ids, 4) ||
