@@ -109,6 +109,20 @@ class Int8Rows(NamedTuple):
     count: Optional[torch.Tensor] = None
 
 
+@functools.lru_cache(maxsize=64)
+def _threshold(threshold: float) -> float:
+    """The least FP32 number that is not below the threshold: what 16-bit values are at or above of
+    one are so of the other, and a threshold above 0 stays one."""
+    if threshold < 0:
+        return -1.0  # (refused by the library, which would take some of them for 0)
+    near = ctypes.c_float(threshold)
+    if not near.value < threshold:
+        return near.value
+    bits = ctypes.c_uint32.from_buffer(near)  # (towards 0 from a positive number: the next)
+    bits.value += 1
+    return near.value
+
+
 def int8_quantize(X: torch.Tensor, threshold: float = 0.0, max_outliers: int = 64,
                   workspace: Optional[torch.Tensor] = None, stream=None) -> Int8Rows:
     """Rows of X (M x K, float16 or bfloat16, any row stride) in 8 bits, as LLM.int8 has them.
@@ -148,8 +162,9 @@ def int8_quantize(X: torch.Tensor, threshold: float = 0.0, max_outliers: int = 6
     with _call_lock(index, handle):
         ws_ptr, ws_bytes = _scratch(workspace, need, "int8 quantize", X, handle)
         st = _lib().dq4_int8_quantize(X.data_ptr(), X.stride(0), _DTYPE_CODE[X.dtype], M, K,
-                                      threshold, codes.data_ptr(), scales.data_ptr(),
-                                      cols.data_ptr(), max_outliers, outliers.data_ptr(),
+                                      _threshold(float(threshold)), codes.data_ptr(),
+                                      scales.data_ptr(), cols.data_ptr(), max_outliers,
+                                      outliers.data_ptr(),
                                       count.data_ptr(), ws_ptr, ws_bytes, handle)
     if st:
         raise Dq4Error(st, "dq4_int8_quantize")

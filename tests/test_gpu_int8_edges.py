@@ -254,3 +254,27 @@ def test_counters_that_a_call_left_behind(dq):
             ws[:4096].view(torch.int32).fill_(left)
             for _ in range(2):
                 assert torch.equal(call(), is_), left
+
+
+# ------------------------------------------------------------- rows in 8 bits
+@pytest.mark.parametrize("kind", ["bf16", "f16"])
+def test_quantize_thresholds_between_numbers(dq, kind):
+    """A threshold means what it says: not the FP32 number next to it, which may be a value's own, or
+    0 (no threshold at all)."""
+    rng = np.random.default_rng(7)
+    x = rng.normal(size=(9, 200)) * 2
+    x[3, 5], x[4, 6], x[5, 7] = 6.0, -6.0, 6.03125
+    x[6] = 0
+    x = dev(x.astype(np.float32), DT[kind])
+    for threshold in (6.0 + 1e-9, 6.0 - 1e-9, 6.0, 1e-60, 5e-324, 1e-45, 6.03125 * (1 + 1e-15),
+                      1e39, 1e300, 3.4028235677973366e38):
+        rows = dq.int8_quantize(x, threshold, 128)
+        codes, scales, cols, outliers, count = defs.quantize(host(x), threshold, 128)
+        assert rows.count.item() == count, threshold
+        assert np.array_equal(rows.cols.cpu().numpy(), cols), threshold
+        assert np.array_equal(rows.codes.cpu().numpy(), codes), threshold
+        assert np.array_equal(host(rows.scales), scales), threshold
+        assert np.array_equal(host(rows.outliers), outliers), threshold
+    for threshold in (-1e-60, -1.0, float("nan")):
+        with pytest.raises(dq.Dq4Error):
+            dq.int8_quantize(x, threshold)

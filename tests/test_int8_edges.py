@@ -21,3 +21,21 @@ def test_moe_without_hidden_values(lib):
                                 None)
     assert call(4, 0, 32) == N_ and call(4, 64, 0) == N_ and call(4, 0, 0) == N_
     assert call(0, 0, 32) == OK and call(0, 64, 0) == OK
+
+
+def test_thresholds_keep_their_side():
+    """The library's FP32 threshold is the least that is not below the caller's, and never 0 for one
+    that is not; negative ones and NaN stay what it refuses."""
+    import math
+
+    import numpy as np
+
+    from quantized_weight_dequantization_gb300._int8 import _threshold
+    for v in (6.0, 6.0 + 1e-9, 6.0 - 1e-9, 1e-60, 5e-324, 1e-45, 2.0 ** -149, 1e39, 1e300, math.inf,
+              3.4028235677973366e38, 3.4028234663852886e38, 65504.1):
+        f = _threshold(v)
+        with np.errstate(over="ignore"):
+            assert np.float32(f) == f and f >= v and f > 0, v
+            assert float(np.nextafter(np.float32(f), np.float32(0))) < v, v
+    assert all(_threshold(v) < 0 for v in (-1.0, -1e-60, -math.inf))
+    assert math.isnan(_threshold(math.nan))
