@@ -71,10 +71,11 @@ __global__ void __launch_bounds__(kStreamThreads, kFewDepth == 2 && NT < 4 ? 3 :
   const int in_cta = warp / group, member = warp - in_cta * group;
   const int64_t n0 = (int64_t(blockIdx.x) * (kStreamWarps / group) + in_cta) * kFewRows;
   uint8_t* rings = aligned_1024(smem_raw);
-  // (the outliers' factors go where the rings were: with a place of their own an SM held two CTAs
-  // in place of three, 16 rows with 5 outlier columns through 4096 x 11008 took 20.6 us)
-  float* coef = reinterpret_cast<float*>(rings);
-  static_assert(kTokens * kMaxOutliers * 4 <= kStreamWarps * kFewDepth * kStage, "factors fit");
+  // (the outliers, with the codes in whose place they are, go where the rings were: with a place of
+  // their own an SM held two CTAs in place of three, 16 rows with 5 outlier columns through 4096 x
+  // 11008 took 20.6 us)
+  float2* coef = reinterpret_cast<float2*>(rings);
+  static_assert(kTokens * kMaxOutliers * 8 <= kStreamWarps * kFewDepth * kStage, "factors fit");
   const uint32_t ring = smem_u32(rings) + warp * kFewDepth * kStage, bars = smem_u32(s_bars[warp]);
   const uint64_t map = reinterpret_cast<uint64_t>(&map_w);
   // this warp's chunks, member + i * group for i < mine, in turn from `i0` on: warps that went
@@ -195,9 +196,8 @@ __global__ void __launch_bounds__(kStreamThreads, kFewDepth == 2 && NT < 4 ? 3 :
     for (int i = threadIdx.x; i < used * int(p.M); i += kStreamThreads) {
       const int u = i / int(p.M), m = i - u * int(p.M);
       const float x = load_16(p.outliers, int64_t(m) * p.L + s_cols.entry[u], p.outliers_bf16);
-      const float code = p.codes[m * p.K + s_cols.col[u]];
-      // in the place of its code's value; not finite: NaN
-      coef[i] = x + (x - x) - code * (load_global(p.scales + m) * kRecip127);
+      // (not finite: NaN)
+      coef[i] = make_float2(x + (x - x), float(load_global(p.codes + m * p.K + s_cols.col[u])));
     }
     __syncthreads();
   } else if (group == 1) {
@@ -214,15 +214,24 @@ __global__ void __launch_bounds__(kStreamThreads, kFewDepth == 2 && NT < 4 ? 3 :
     if (m < kTokens)  // (more rows only without codes, K = 0)
       for (int w = 0; w < group; ++w)
         sum += s_part[in_cta * group + w][m * kFewRows + t % kFewRows];
-    float y = sum * (load_global(p.scales + m) * kRecip127) * s_n;
+    const float s_m = load_global(p.scales + m) * kRecip127;
+    float y;
     if (used > 0) {
-      float more = 0.f;
+      float more = 0.f, instead = 0.f;  // the outliers' sum, and that of the codes where they are
+      auto add = [&](int u, float w) {
+        const float2 x = coef[u * int(p.M) + m];
+        more += w * x.x;
+        instead += w * x.y;
+      };
 #pragma unroll
       for (int u = 0; u < kAhead; ++u)
-        if (u < used) more += float(int(ahead[u])) * coef[u * int(p.M) + m];
+        if (u < used) add(u, float(int(ahead[u])));
       for (int u = kAhead; u < used; ++u)
-        more += float(load_global(p.CB + n * p.K + s_cols.col[u])) * coef[u * int(p.M) + m];
-      y += more * s_n;
+        add(u, float(load_global(p.CB + n * p.K + s_cols.col[u])));
+      // (whole numbers, sum and instead: their difference is as exact as the sum)
+      y = (sum - instead) * s_m * s_n + more * s_n;
+    } else {
+      y = sum * s_m * s_n;
     }
     store_any(p.Y, m * p.N + n, y + bias, p.out_dtype);
   }

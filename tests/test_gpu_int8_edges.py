@@ -278,3 +278,20 @@ def test_quantize_thresholds_between_numbers(dq, kind):
     for threshold in (-1e-60, -1.0, float("nan")):
         with pytest.raises(dq.Dq4Error):
             dq.int8_quantize(x, threshold)
+
+
+@pytest.mark.parametrize("M", [1, 9, 24, 60])
+def test_linear_codes_of_used_columns_leave_nothing(dq, M):
+    """Codes of columns whose outliers are used do not count, however far above them they are: whole
+    numbers, and outliers of 2^-20 of a code."""
+    rng = np.random.default_rng(M)
+    K, N, cols = 64, 33, [0, 9, 31, 32, 63]
+    codes, CB = np.zeros((M, K), np.int8), rng.integers(-127, 128, (N, K)).astype(np.int8)
+    codes[:, cols] = rng.integers(1, 128, (M, len(cols)))
+    out = rng.integers(-100, 101, (M, len(cols))) * 2.0 ** -20
+    rows = dq.Int8Rows(dev(codes), dev(np.full(M, 127, np.float32)), dev(np.array(cols)),
+                       dev(out.astype(np.float32), torch.bfloat16))
+    y = dq.int8_linear(rows, dev(CB), dev(np.full(N, 127, np.float32)), out_dtype=torch.float32)
+    # (for many rows an outlier is two FP16 numbers, which end at 2^-24 of a unit)
+    tol = 0 if M <= 16 else 2.0 ** -25 * np.abs(CB[:, cols].astype(int)).sum(1)
+    assert (np.abs(host(y) - out @ CB[:, cols].T) <= tol).all()
