@@ -613,7 +613,8 @@ __global__ void __launch_bounds__(Gemm<BX, kBack>::kThreads, 1)
             const float by[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-              v[j + k] = __float_as_uint(__uint_as_float(v[j + k]) * by[k] * scale + bias);
+              // (the weight's scale first: rows may be near FP32's largest number)
+              v[j + k] = __float_as_uint(__uint_as_float(v[j + k]) * scale * by[k] + bias);
           }
         }
       };

@@ -214,13 +214,14 @@ __global__ void __launch_bounds__(kStreamThreads, kFewDepth == 2 && NT < 4 ? 3 :
     if (m < kTokens)  // (more rows only without codes, K = 0)
       for (int w = 0; w < group; ++w)
         sum += s_part[in_cta * group + w][m * kFewRows + t % kFewRows];
+    // (the weight's scale first: rows may be near FP32's largest number, their results not)
     const float s_m = load_global(p.scales + m) * kRecip127;
     float y;
     if (used > 0) {
       float more = 0.f, instead = 0.f;  // the outliers' sum, and that of the codes where they are
       auto add = [&](int u, float w) {
         const float2 x = coef[u * int(p.M) + m];
-        more += w * x.x;
+        more += w * s_n * x.x;
         instead += w * x.y;
       };
 #pragma unroll
@@ -229,9 +230,9 @@ __global__ void __launch_bounds__(kStreamThreads, kFewDepth == 2 && NT < 4 ? 3 :
       for (int u = kAhead; u < used; ++u)
         add(u, float(load_global(p.CB + n * p.K + s_cols.col[u])));
       // (whole numbers, sum and instead: their difference is as exact as the sum)
-      y = (sum - instead) * s_m * s_n + more * s_n;
+      y = (sum - instead) * s_n * s_m + more;
     } else {
-      y = sum * s_m * s_n;
+      y = sum * s_n * s_m;
     }
     store_any(p.Y, m * p.N + n, y + bias, p.out_dtype);
   }

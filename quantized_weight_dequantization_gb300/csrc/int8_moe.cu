@@ -594,9 +594,10 @@ struct UpJobs {
     for (int j = t / kUpPlaces; j < (count + 1) / 2 * 2; j += threads / kUpPlaces) {
       float v = 0.f;
       if (j < count) {
-        const float down = s.down[first + j] * kRecip127;
-        const float gate = S::sum(part, warps, j, place) * down * s_gate;
-        const float up = S::sum(part, warps, j, 16 + place) * down * s_up;
+        // (the weights' scales first: rows may be near FP32's largest number)
+        const float down = s.down[first + j];
+        const float gate = S::sum(part, warps, j, place) * (s_gate * kRecip127) * down;
+        const float up = S::sum(part, warps, j, 16 + place) * (s_up * kRecip127) * down;
         v = __fdiv_rn(gate, 1.f + expf(-gate)) * up;
       }
       uint32_t top = __float_as_uint(v) & 0x7FFFFFFFu;
@@ -668,7 +669,7 @@ struct DownJobs {
     if (n >= p.H) return;
     const float scale = s_place * kRecip127;
     for (int j = t / kDownPlaces; j < count; j += threads / kDownPlaces) {
-      p.out[(first + j) * p.H + n] = S::sum(part, warps, j, place) * s.down[first + j] * scale;
+      p.out[(first + j) * p.H + n] = S::sum(part, warps, j, place) * scale * s.down[first + j];
     }
   }
 };

@@ -295,3 +295,43 @@ def test_linear_codes_of_used_columns_leave_nothing(dq, M):
     # (for many rows an outlier is two FP16 numbers, which end at 2^-24 of a unit)
     tol = 0 if M <= 16 else 2.0 ** -25 * np.abs(CB[:, cols].astype(int)).sum(1)
     assert (np.abs(host(y) - out @ CB[:, cols].T) <= tol).all()
+
+
+@pytest.mark.parametrize("M", [3, 50])
+@pytest.mark.parametrize("loud", [0, 3])
+def test_linear_rows_near_the_largest_number(dq, M, loud):
+    """Rows up to BF16's largest value through a weight that brings them back: no factor of the
+    result is past FP32 on its way."""
+    rng = np.random.default_rng(M + loud)
+    K, N = 512, 70
+    CB, SCB = weight(rng, N, K)
+    SCB = (SCB * 1e-4).astype(np.float32)
+    x = rng.uniform(-1, 1, (M, K)) * 2.0 ** 127 * (1 - 2.0 ** -9)
+    if loud:
+        x[:, loud:] *= 2.0 ** -20
+    rows = dq.int8_quantize(dev(x.astype(np.float32), torch.bfloat16), 2.0 ** 108 if loud else 0.0, 8)
+    y = dq.int8_linear(rows, dev(CB), dev(SCB), out_dtype=torch.float32)
+    want, size = defs.linear(rows.codes.cpu().numpy(), host(rows.scales), CB, SCB,
+                             rows.cols.cpu().numpy() if loud else None,
+                             host(rows.outliers) if loud else None)
+    tol = (2.0 ** -21 + (K / 16 + 4) * 2.0 ** -23) * size
+    assert np.isfinite(want.astype(np.float32)).all() and np.isfinite(host(y)).all()
+    assert (np.abs(host(y) - want) <= tol).all()
+
+
+def test_moe_rows_near_the_largest_number(dq):
+    """Rows of 2^114 and inner values of 2^120 through weights that bring them back: sums of 512
+    products with codes of 127, in the row's unit times that unit, would be past 2^128."""
+    rng = np.random.default_rng(120)
+    T, H, I, E = 5, 512, 32, 3
+    x = dev((rng.uniform(0.5, 1, (T, H)) * 2.0 ** 114).astype(np.float32), torch.bfloat16)
+    logits = dev(rng.normal(size=(T, E)).astype(np.float32))
+    w1, s1 = weight(rng, E, 2 * I, H)
+    w2, s2 = weight(rng, E, H, I)
+    w1[:], w2[:, ::2] = 127, 127
+    s1[:, :I] *= np.float32(2.0 ** -114)
+    s1[:, I:] *= np.float32(2.0 ** -6)
+    s2 *= np.float32(2.0 ** -108)
+    y = dq.int8_moe(x, logits, dev(w1), dev(s1), dev(w2), dev(s2), 2)
+    want, _, _, size, unit = defs.moe(host(x), host(logits), w1, s1, w2, s2, 2, True)
+    rounded_once(y, want, moe_off(unit, size, H, I), "bf16", "near the largest")
