@@ -239,13 +239,23 @@ __global__ void __launch_bounds__(kStreamThreads, kFewDepth == 2 && NT < 4 ? 3 :
 }
 
 // Whether a product goes to the kernel for few rows: up to 16, and up to 32 where the weight is
-// small.  Few / many, in us:
-//   rows          1024 x 1024   2048 to 4096   4096 x 4096   4096 to 11008   8192 to 28672
-//     16          3.2 / 8.6     3.9 / 10.4     6.6 / 11.7    14.9 / 20.2     50 / 55
-//     32          4.9 / 8.6     8.3 / 10.1    12.3 / 11.9    23.4 / 20.3     75 / 55
-// (32 rows 8192 to 2048: 9.6 / 14.9; with 5 outlier columns through 4096 x 4096 15.4 / 13.6.)
-bool few_rows(int64_t M, int64_t N, int64_t K) {
-  return M <= 16 || (M <= 32 && N * K <= 16 << 20) || K == 0;
+// small; with outlier columns, whose sums are N M for each that is used, where N is, too.  Few / many,
+// in us, for 16 rows, K to N:
+//   1024 to 1024   2048 to 2048   4096 to 4096   4096 to 11008   8192 to 28672
+//    3.2 / 8.6      3.9 / 10.4     6.6 / 11.7     14.4 / 20.2     49 / 55
+// and for 17 to 32 rows, without, with 5 and with 30 outlier columns:
+//   1024 to 4096    4.5 to 4.9 / 8.5     6.6 to 7.3 / 9.9    11.4 to 15.7 / 10.1
+//   4096 to 256     5.6 to 6.0 / 10.1    7.4 to 7.9 / 11.3   10.3 to 12.7 / 11.5
+//   4096 to 2048    5.9 to 6.4 / 11.3    7.7 to 8.1 / 12.6   10.6 to 13.0 / 12.8
+//   8192 to 2048    9.5 to 9.6 / 14.8   11.2 to 11.3 / 16.2  14.3 to 16.2 / 16.8
+//  16384 to 1024   15.9 / 15.9          17.4 to 17.6 / 17.2  20.6 to 22.4 / 17.7
+//   2048 to 4096    7.9 / 10.5          11.5 to 11.9 / 11.6  17.3 to 21.2 / 11.9
+//   4096 to 4096   11.4 to 12.1 / 12.1  15.0 to 15.8 / 13.5  20.7 to 25.4 / 14.4
+//   1024 to 11008   9.2 to 10.3 / 8.8   14.8 to 16.8 / 11.2  26.4 to 38.5 / 12.0
+bool few_rows(int64_t M, int64_t N, int64_t K, int L) {
+  if (M <= 16 || K == 0) return true;
+  return M <= 32 && N <= 4096 && N * K <= 16 << 20 &&
+         (L == 0 || N <= 2048 || N * K <= 4 << 20);
 }
 
 template <int NT, int kFewDepth>
@@ -289,7 +299,7 @@ extern "C" {
 
 int64_t dq4_int8_linear_workspace_bytes(int64_t M, int64_t N, int64_t K, int32_t L) {
   if (M <= 0 || N <= 0 || K < 0 || L < 0 || L > kMaxOutliers || M > INT32_MAX || N > INT32_MAX ||
-      K > INT32_MAX || few_rows(M, N, K))
+      K > INT32_MAX || few_rows(M, N, K, L))
     return 0;
   int dev, sms;
   if (current_device(&dev, &sms) != DQ4_OK) return -DQ4_ERR_DEVICE;
@@ -319,7 +329,7 @@ int dq4_int8_linear(const int8_t* codes, const float* scales, const int8_t* CB, 
   const Int8Linear p = {codes, scales, CB, SCB, M, N, K, cols, outliers, L,
                         L > 0 && outlier_dtype == DQ4_OUT_BF16, bias, out_dtype, Y, bad};
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (!few_rows(M, N, K)) {
+  if (!few_rows(M, N, K, L)) {
     if (!workspace || workspace_bytes < int8_gemm_workspace(M, N, K, L, sms))
       return DQ4_ERR_WORKSPACE;
     if (misaligned(workspace, 256)) return DQ4_ERR_ALIGN;

@@ -335,3 +335,33 @@ def test_moe_rows_near_the_largest_number(dq):
     y = dq.int8_moe(x, logits, dev(w1), dev(s1), dev(w2), dev(s2), 2)
     want, _, _, size, unit = defs.moe(host(x), host(logits), w1, s1, w2, s2, 2, True)
     rounded_once(y, want, moe_off(unit, size, H, I), "bf16", "near the largest")
+
+
+def close_on_gpu(y, rows, CB, SCB, bias, steps, u, what):
+    """By the definition, in 64 bits on the GPU: for results too many for the host."""
+    a = rows.codes.double() * (rows.scales.double()[:, None] / 127)
+    if rows.cols is not None:
+        for at, c in enumerate(rows.cols.tolist()):
+            if c >= 0:
+                a[:, c] = rows.outliers[:, at].double()
+    w = CB.double() * (SCB.double()[:, None] / 127)
+    want, size = a @ w.T, a.abs() @ w.abs().T
+    if bias is not None:
+        want, size = want + bias.double(), size + bias.double().abs()
+    off = (y.double() - want).abs() - (2.0 ** -21 + steps * 2.0 ** -23) * size - u * want.abs()
+    assert off.max() <= 2.0 ** -25, (what, off.max().item())
+
+
+@pytest.mark.parametrize("N,K,L,few", [(4096, 4096, 0, 32), (4096, 4096, 5, 16), (4100, 512, 0, 16),
+                                       (2048, 8192, 5, 32), (2064, 2048, 5, 16),
+                                       (4096, 1024, 5, 32), (11008, 1024, 0, 16)])
+def test_linear_on_both_sides_of_its_kernels(dq, N, K, L, few):
+    """The change from the kernel for few rows, which needs no workspace, to that for many."""
+    need = dq.get_lib().dq4_int8_linear_workspace_bytes
+    CB, SCB = gpu_weight(N, K, N + K)
+    for M in (16, 17, 32, 33):
+        rows = gpu_rows(dq, M, K, L, M)
+        most = 24 if L else 0
+        assert (need(M, N, K, most) == 0) == (M <= few), M
+        y = dq.int8_linear(rows, CB, SCB, out_dtype=torch.float32)
+        close_on_gpu(y, rows, CB, SCB, None, K / 16 if L or K > 1040 else 0, 0, (M, N, K))
