@@ -239,8 +239,8 @@ __global__ void __launch_bounds__(kStreamThreads, kFewDepth == 2 && NT < 4 ? 3 :
 }
 
 // Whether a product goes to the kernel for few rows: up to 16, and up to 32 where the weight is
-// small; with outlier columns, whose sums are N M for each that is used, where N is, too.  Few / many,
-// in us, for 16 rows, K to N:
+// small; with outlier columns, whose sums are N M for each that is used, where N is, too.
+// Few / many, in us, for 16 rows, K to N:
 //   1024 to 1024   2048 to 2048   4096 to 4096   4096 to 11008   8192 to 28672
 //    3.2 / 8.6      3.9 / 10.4     6.6 / 11.7     14.4 / 20.2     49 / 55
 // and for 17 to 32 rows, without, with 5 and with 30 outlier columns:
