@@ -563,3 +563,40 @@ def test_runs_stay_in_their_workspace(dq, in_runs):
     for i in range(3):
         assert same(call(i, workspace=buf[guard:guard + need]), want[i])
     assert (buf[:guard] == 0xA5).all() and (buf[guard + need:] == 0xA5).all()
+
+
+# ------------------------------------------------------------- as the README has it
+@pytest.mark.parametrize("M", [7, 90])
+def test_readme_function_trains_what_comes_before(dq, M):
+    """The autograd function of the README: gradients of an adapter before a frozen weight, by the
+    formula and by differences of the loss in 64 bits."""
+    import os
+    import re
+    text = open(os.path.join(os.path.dirname(os.path.dirname(__file__)), "README.md")).read()
+    code = [c for c in re.findall(r"```python\n(.*?)```", text, flags=re.S) if "class Frozen" in c]
+    scope = {"torch": torch, "dq": dq}
+    exec(code[0], scope)
+    N, K, R = 96, 128, 8
+    CB, SCB = gpu_weight(N, K, M)
+    gen = torch.Generator("cuda").manual_seed(M)
+    x = torch.randn(M, R, device="cuda", generator=gen)
+    A = (torch.randn(R, K, device="cuda", generator=gen) * 0.5).requires_grad_()
+    g = torch.randn(M, N, device="cuda", generator=gen).bfloat16()
+    h = (x @ A).bfloat16()
+    h.retain_grad()
+    y = scope["Frozen"].apply(h, CB, SCB)
+    assert torch.equal(y, dq.int8_linear(dq.int8_quantize(h.detach(), 6.0), CB, SCB,
+                                         out_dtype=torch.bfloat16))
+    (y.float() * g.float()).sum().backward()
+    want, size = backward_by_definition(g, CB, SCB)
+    off = (h.grad.double() - want).abs()
+    assert (off <= 2.0 ** -8 * want.abs() + (N / 16 + 4) * 2.0 ** -23 * size).all()
+    # A's own: x^T dh.  The loss is linear in A but for roundings, so a difference of it in 64 bits,
+    # the weight as it is, is <dA, D>; the weight in BF16 and dh are off by 2^-8 of their terms each
+    W = CB.double() * (SCB.double()[:, None] / 127)
+    loss = lambda a: ((x.double() @ a) @ W.T * g.double()).sum()
+    for _ in range(3):
+        D = torch.randn(R, K, device="cuda", dtype=torch.float64, generator=gen)
+        slope = (loss(A.detach().double() + D) - loss(A.detach().double() - D)) / 2
+        reach = (x.double().abs().T @ (g.double().abs() @ W.abs()) * D.abs()).sum()
+        assert ((A.grad.double() * D).sum() - slope).abs() <= (2.0 ** -7 + 2.0 ** -14) * reach
