@@ -249,12 +249,13 @@ __global__ void __launch_bounds__(kStreamThreads, kFewDepth == 2 && NT < 4 ? 3 :
 //   4096 to 2048    5.9 to 6.4 / 11.3    7.7 to 8.1 / 12.6   10.6 to 13.0 / 12.8
 //   8192 to 2048    9.5 to 9.6 / 14.8   11.2 to 11.3 / 16.2  14.3 to 16.2 / 16.8
 //  16384 to 1024   15.9 / 15.9          17.4 to 17.6 / 17.2  20.6 to 22.4 / 17.7
+//  65536 to 256    54.9 / 36.7          56.4 / 38.0          (a CTA takes 16 weight rows' whole sum)
 //   2048 to 4096    7.9 / 10.5          11.5 to 11.9 / 11.6  17.3 to 21.2 / 11.9
 //   4096 to 4096   11.4 to 12.1 / 12.1  15.0 to 15.8 / 13.5  20.7 to 25.4 / 14.4
 //   1024 to 11008   9.2 to 10.3 / 8.8   14.8 to 16.8 / 11.2  26.4 to 38.5 / 12.0
 bool few_rows(int64_t M, int64_t N, int64_t K, int L) {
   if (M <= 16 || K == 0) return true;
-  return M <= 32 && N <= 4096 && N * K <= 16 << 20 &&
+  return M <= 32 && N <= 4096 && K < 16384 && N * K <= 16 << 20 &&
          (L == 0 || N <= 2048 || N * K <= 4 << 20);
 }
 

@@ -356,7 +356,8 @@ def close_on_gpu(y, rows, CB, SCB, bias, steps, u, what):
 
 @pytest.mark.parametrize("N,K,L,few", [(4096, 4096, 0, 32), (4096, 4096, 5, 16), (4100, 512, 0, 16),
                                        (2048, 8192, 5, 32), (2064, 2048, 5, 16),
-                                       (4096, 1024, 5, 32), (11008, 1024, 0, 16)])
+                                       (4096, 1024, 5, 32), (11008, 1024, 0, 16),
+                                       (256, 16384, 0, 16), (256, 16368, 5, 32)])
 def test_linear_on_both_sides_of_its_kernels(dq, N, K, L, few):
     """The change from the kernel for few rows, which needs no workspace, to that for many."""
     need = dq.get_lib().dq4_int8_linear_workspace_bytes
