@@ -24,8 +24,8 @@
 // where 32, 64 and 128 would be the rate of the tensor cores: with A in TMEM the smaller ones are
 // no faster, and the largest shares the shared memory with the copies and the producers
 // (activations in and out, codes in and out: 160 cycles at 128 bytes a cycle).  8191 rows through
-// 4096 x 14336: 613 to 640 us, 0.78 to 0.81 of the measured rate of the GPU; the gradient of 2047
-// rows through 11008 x 4096 146 us, 0.65: its producers' instructions, three packed ones for two
+// 4096 x 14336: 610 to 653 us, 0.76 to 0.82 of the measured rate of the GPU; the gradient of 2047
+// rows through 11008 x 4096 150 us, 0.64: its producers' instructions, three packed ones for two
 // values.  (Pairs of CTAs with tiles of 256 x 256, the weight's values in TMEM or in shared
 // memory: 790 to 824 us for the 8191 rows.)
 #include "int8_gemm.cuh"

@@ -265,7 +265,7 @@ __global__ void __launch_bounds__(kRouteThreads) dq4_moe_route_kernel(const MoeA
 // Copies of 128-byte rows: the TMA takes about 3.5 cycles for a row whatever its width, and at 64
 // bytes a row that bounds the weight's bytes (one token through 11008 x 4096, whose weight alone
 // takes 10.4 us to read: 23.7 us).  Copies of 16 bytes a lane, cp.async, took 13.4 us there.
-// Rings of four chunks leave the tokens less of L1: 16 tokens, 6 of 64 experts, took 97 us, so 92.
+// Rings of four chunks leave the tokens less of L1: 16 tokens, 6 of 64 experts, took 5 us more.
 //
 // kBoxes: boxes of weight rows of a chunk.  kTwo: tokens are FP32, and become two terms (23 tokens
 // through 2 of 8 experts of 4096 x 14336 254 us; 298 by going through a chunk once for each, with
@@ -280,9 +280,9 @@ __global__ void __launch_bounds__(kRouteThreads) dq4_moe_route_kernel(const MoeA
 //   begin(job, t)           before a job's products, thread t of its group
 //   finish(job, part, ...)  the group's sums (sum(part, warps, token, row)), thread t of `threads`
 //
-// (Entries of 16 pairs, two products for each weight's conversion, took more: 64 tokens through 2
-// of 8 experts of 4096 x 14336, 16 pairs each, 443 us, in eights, which read the weights twice from
-// L2, 409; 23 tokens 302 and 237.)
+// (Entries of 16 pairs, two products for each weight's conversion, took more: with one term, 64
+// tokens through 2 of 8 experts of 4096 x 14336, 16 pairs each, 443 us, in eights, which read the
+// weights twice from L2, 409, with two terms 443; 23 tokens 302 and 237.)
 constexpr int kJobRows = 32;
 constexpr int kDepth = 2;  // chunks of a ring
 constexpr int kCtas = 2;   // of an SM
