@@ -54,7 +54,8 @@ extern "C" {
  *   codes     int8[M][K], scales FP32[M]
  * threshold == 0: cols, outliers, count and workspace are not used (NULL).  threshold < 0
  * or NaN, max_cols outside 1 .. 128, M or K < 0: DQ4_ERR_N.
- * Fastest where K and row_stride are multiples of 8, X 16-byte and codes 8-byte aligned.
+ * Fastest where K and row_stride (of several rows) are multiples of 8, X 16-byte and codes 8-byte
+ * aligned.
  */
 int dq4_int8_quantize(const void* X, int64_t row_stride, int32_t dtype, int64_t M, int64_t K,
                       float threshold, int8_t* codes, float* scales, int64_t* cols,
@@ -116,7 +117,8 @@ int64_t dq4_int8_linear_backward_workspace_bytes(int64_t M, int64_t N, int64_t K
  * (BF16 rows lose nothing down to 2^-31 of their largest value); the inner values are held in
  * two terms of 11 bits: to 2^-22 of them, or 2^-39 of the largest of their row.
  * T 0 .. 256, E 1 .. 1024, top_k 1 .. min(E, 16), H 16 .. 32768 and I 16 .. 2^20, both multiples
- * of 16, E * I * H < 2^47 (H and I may be 0 without tokens); weights 16-byte aligned, X 16-byte aligned with row_stride % 8 == 0.
+ * of 16, E * I * H < 2^47 (H and I may be 0 without tokens); weights 16-byte aligned, X 16-byte
+ * aligned, with row_stride % 8 == 0 where there are several tokens.
  */
 int dq4_int8_moe(const void* X, int64_t row_stride, int32_t dtype, int64_t T, int64_t H, int64_t I,
                  int64_t E, const float* logits, int32_t top_k, int32_t renormalize,

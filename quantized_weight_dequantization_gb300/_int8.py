@@ -323,9 +323,10 @@ def int8_moe(X: torch.Tensor, logits: torch.Tensor, w1: torch.Tensor, s1: torch.
              bad: Optional[torch.Tensor] = None, stream=None):
     """A mixture-of-experts layer for few tokens (256 at most) over 8-bit weights.
 
-    X is T x H (float16 or bfloat16), ``logits`` T x E (float32).  Each token goes through the
-    ``top_k`` experts (16 at most) with its largest logits, the lower index first where they are
-    equal, weighted by their softmax over the chosen ones (``renormalize``) or over all:
+    X is T x H (float16 or bfloat16, its rows 16-byte aligned), ``logits`` T x E (float32).  Each
+    token goes through the ``top_k`` experts (16 at most) with its largest logits, the lower index
+    first where they are equal, weighted by their softmax over the chosen ones (``renormalize``) or
+    over all:
     ``y = sum p_e W2_e (silu(Wg_e x) * (Wu_e x))``.  ``w1`` int8 [E, 2 I, H] holds the rows of
     Wg, then those of Wu, ``w2`` int8 [E, H, I]; ``s1`` [E, 2 I] and ``s2`` [E, H] are float32
     scales of their rows, a value w * s / 127.  H and I are multiples of 16, and not 0 with tokens.

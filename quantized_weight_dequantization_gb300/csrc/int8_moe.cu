@@ -787,7 +787,7 @@ int dq4_int8_moe(const void* X, int64_t row_stride, int32_t dtype, int64_t T, in
   if (T == 0) return DQ4_OK;
   if (H == 0 || I == 0) return DQ4_ERR_N;
   if (!X || !logits || !W1 || !S1 || !W2 || !S2 || !ids || !weights || !Y) return DQ4_ERR_NULL;
-  if (misaligned(X, 16) || row_stride % 8 != 0 || misaligned(logits, 4) || misaligned(W1, 16) ||
+  if (misaligned(X, 16) || (T > 1 && row_stride % 8 != 0) || misaligned(logits, 4) || misaligned(W1, 16) ||
       misaligned(W2, 16) || misaligned(S1, 4) || misaligned(S2, 4) || misaligned(ids, 4) ||
       misaligned(weights, 4) || misaligned(Y, 2) || misaligned(bad, 4))
     return DQ4_ERR_ALIGN;

@@ -359,7 +359,8 @@ int dq4_int8_quantize(const void* X, int64_t row_stride, int32_t dtype, int64_t 
     }
     p.marks = reinterpret_cast<uint32_t*>(static_cast<char*>(workspace) + kMarksAt);
   }
-  const bool vec = K % 8 == 0 && row_stride % 8 == 0 && !misaligned(X, 16) && !misaligned(codes, 8);
+  const bool vec = K % 8 == 0 && (M <= 1 || row_stride % 8 == 0) && !misaligned(X, 16) &&
+                   !misaligned(codes, 8);
   if (M > 0) {
     const bool bf16 = dtype == DQ4_OUT_BF16;
     const int st = bf16 ? (thr ? launch_rows<true, true>(p, vec, s)

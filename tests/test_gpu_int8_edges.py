@@ -601,3 +601,18 @@ def test_readme_function_trains_what_comes_before(dq, M):
         slope = (loss(A.detach().double() + D) - loss(A.detach().double() - D)) / 2
         reach = (x.double().abs().T @ (g.double().abs() @ W.abs()) * D.abs()).sum()
         assert ((A.grad.double() * D).sum() - slope).abs() <= (2.0 ** -7 + 2.0 ** -14) * reach
+
+
+def test_single_rows_of_any_stride(dq):
+    """A column turned into a row: its values follow one another, its stride to a next row is 1."""
+    rng = np.random.default_rng(1)
+    H, I, E = 1024, 32, 3
+    x = dev(rng.normal(size=H).astype(np.float32), torch.bfloat16)
+    row, view = x[None], x[:, None].t()
+    assert view.stride() == (1, 1)
+    args = (dev(rng.normal(size=(1, E)).astype(np.float32)),
+            *(dev(a) for a in weight(rng, E, 2 * I, H)), *(dev(a) for a in weight(rng, E, H, I)), 2)
+    assert torch.equal(dq.int8_moe(view, *args), dq.int8_moe(row, *args))
+    for threshold in (0.0, 2.0):
+        for a, b in zip(dq.int8_quantize(view, threshold), dq.int8_quantize(row, threshold)):
+            assert a is b is None or torch.equal(a, b)

@@ -3,7 +3,7 @@
 import pytest
 
 P = 1 << 12  # a fake aligned pointer, never followed on these paths
-OK, N_ = 0, 2
+OK, N_, ALIGN, WORKSPACE = 0, 2, 6, 15
 
 
 @pytest.fixture(scope="module")
@@ -39,3 +39,12 @@ def test_thresholds_keep_their_side():
             assert float(np.nextafter(np.float32(f), np.float32(0))) < v, v
     assert all(_threshold(v) < 0 for v in (-1.0, -1e-60, -math.inf))
     assert math.isnan(_threshold(math.nan))
+
+
+def test_moe_single_row_has_no_stride(lib):
+    """The stride to a next row says nothing where there is none (the next check is the workspace's)."""
+    def call(T, stride, X=P):
+        return lib.dq4_int8_moe(X, stride, 0, T, 64, 32, 8, P, 2, 1, P, P, P, P, P, P, P, None, 0, P,
+                                None)
+    assert call(1, 1) == call(1, 64) == call(2, 64) == WORKSPACE
+    assert call(2, 1) == call(2, 68) == call(1, 1, P + 8) == ALIGN
