@@ -629,7 +629,7 @@ __global__ void __launch_bounds__(Gemm<BX, kBack>::kThreads, 1)
       auto rows_at = [&](int col, int most) {
         return n < p.lanes ? int(min(int64_t(most), p.rows - it.row0 - col)) : 0;
       };
-      auto store = [&](auto& from, int col, int at) {  // (words from `at` on, for 32 columns or all)
+      auto store = [&](auto& from, int col, int at) {  // (words from `at` on: 32 columns or all)
         constexpr int kWords = int(sizeof(from) / 4) < 16 ? int(sizeof(from) / 4) : 16;
         const int rows = rows_at(col, 2 * kWords);
         if (pairs) {
@@ -868,8 +868,8 @@ struct RowArgs {
 // place of its code as x / u, in two FP16 terms, the second in a column of its own past K, where
 // the weight's column stands again: the CTAs past row_ctas gather those columns (gathered in the
 // product itself, for each tile again, 4096 rows with 13 such columns through 4096 x 11008 took 293
-// us; so 274).  FP16 ends at 65504 and 2^-24: where an outlier is above 2^15 u, the unit is 2^e u, the
-// least that it is not above 2^15 of, and codes are 2^-e of theirs, exactly up to e = 24.
+// us; so 274).  FP16 ends at 65504 and 2^-24: where an outlier is above 2^15 u, the unit is 2^e u,
+// the least that it is not above 2^15 of, and codes are 2^-e of theirs, exactly up to e = 24.
 // A warp takes 512 values of a row, 16 a lane (so spread, 512 rows through 4096 x 4096 take 22.8
 // us; 2048 values a warp, loaded at once, 25.4).
 constexpr int kRowPart = 512;

@@ -241,15 +241,15 @@ __global__ void __launch_bounds__(kStreamThreads, kFewDepth == 2 && NT < 4 ? 3 :
 // Whether a product goes to the kernel for few rows: up to 16, and up to 32 where the weight is
 // small; with outlier columns, whose sums are N M for each that is used, where N is, too.
 // Few / many, in us, for 16 rows, K to N:
-//   1024 to 1024   2048 to 2048   4096 to 4096   4096 to 11008   8192 to 28672
-//    3.2 / 8.6      3.9 / 10.4     6.6 / 11.7     14.4 / 20.2     49 / 55
+//   1024 to 1024   2048 to 2048   4096 to 4096   4096 to 11008   8192 to 28672   65536 to 256
+//    3.2 / 8.6      3.9 / 10.4     6.6 / 11.7     14.4 / 20.2     49 / 55         35.2 / 36.3
 // and for 17 to 32 rows, without, with 5 and with 30 outlier columns:
 //   1024 to 4096    4.5 to 4.9 / 8.5     6.6 to 7.3 / 9.9    11.4 to 15.7 / 10.1
 //   4096 to 256     5.6 to 6.0 / 10.1    7.4 to 7.9 / 11.3   10.3 to 12.7 / 11.5
 //   4096 to 2048    5.9 to 6.4 / 11.3    7.7 to 8.1 / 12.6   10.6 to 13.0 / 12.8
 //   8192 to 2048    9.5 to 9.6 / 14.8   11.2 to 11.3 / 16.2  14.3 to 16.2 / 16.8
 //  16384 to 1024   15.9 / 15.9          17.4 to 17.6 / 17.2  20.6 to 22.4 / 17.7
-//  65536 to 256    54.9 / 36.7          56.4 / 38.0          (a CTA takes 16 weight rows' whole sum)
+//  65536 to 256    54.9 / 36.7          56.4 / 38.0          (a CTA takes a sum of 65536)
 //   2048 to 4096    7.9 / 10.5          11.5 to 11.9 / 11.6  17.3 to 21.2 / 11.9
 //   4096 to 4096   11.4 to 12.1 / 12.1  15.0 to 15.8 / 13.5  20.7 to 25.4 / 14.4
 //   1024 to 11008   9.2 to 10.3 / 8.8   14.8 to 16.8 / 11.2  26.4 to 38.5 / 12.0

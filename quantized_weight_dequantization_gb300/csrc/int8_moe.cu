@@ -6,18 +6,18 @@
 //           each expert's (token, choice) pairs, by entries of up to 8
 //   up      a job is 16 inner places of an entry's expert, gate and up rows together: inner =
 //           silu(g) * u in FP32, and the largest of each pair's row
-//   down    a job is 32 output places of an entry's expert; inner values become two terms of FP16 on
-//           their way in, in units of a power of two for their row.  That holds 22 bits of a value, or
-//           2^-39 of its row's largest, where FP16 ends.  (One term's 11 bits are as much as FP16
-//           results have, and move one BF16 result in ten to its neighbour.  A power of two for each
-//           16 places, brought to the row's in FP16, lost what is below 2^-25 of the row.)
+//   down    a job is 32 output places of an entry's expert; inner values become two terms of FP16
+//           on their way in, in units of a power of two for their row.  That holds 22 bits of a
+//           value, or 2^-39 of its row's largest, where FP16 ends.  (One term's 11 bits are as much
+//           as FP16 results have, and move one BF16 result in ten to its neighbour.  A power of two
+//           for each 16 places, brought to the row's in FP16, lost what is below 2^-25 of the row.)
 //   combine each token's results by their weights
 // Experts that no token chose have no jobs.  No atomic adds a value.
 //
 // Of 4096 x 14336: one token through 2 of 8 experts 73.5 us, where the bytes take 52, 23 tokens 255
-// of 208; of 2048 x 1408, 16 tokens through 6 of 64, 96 of 65.  What is left is the ends of the four
-// launches, about 4 us each, and the second product's (0.68 of the copy rate for one token with one
-// term, where the first has 0.83).
+// of 208; of 2048 x 1408, 16 tokens through 6 of 64, 96 of 65.  What is left is the ends of the
+// four launches, about 4 us each, and the second product, which for one token ran at 0.68 of the
+// copy rate with one term, where the first runs at 0.83.
 #include "int8.cuh"
 
 namespace dq4d {
@@ -269,8 +269,8 @@ __global__ void __launch_bounds__(kRouteThreads) dq4_moe_route_kernel(const MoeA
 //
 // kBoxes: boxes of weight rows of a chunk.  kTwo: tokens are FP32, and become two terms (23 tokens
 // through 2 of 8 experts of 4096 x 14336 254 us; 298 by going through a chunk once for each, with
-// half of the registers; 259 where they become that before the weights' wait, which spills; 240 with
-// one term).
+// half of the registers; 259 where they become that before the weights' wait, which spills; 240
+// with one term).
 // Jobs:
 //   places(job, y)          the first row of each box of weights
 //   tokens(job)             this lane's token (for one that is not there any other, whose results
@@ -541,9 +541,9 @@ __device__ __forceinline__ Entries load_entries(const MoeArgs& p, uint8_t* smem)
   return s;
 }
 
-// Inner values lie as they are read: of a chunk lane c's i-th four, 32 c + 4 i, stand beside those of
-// the other lanes, so that a load takes one line of a token.  (In their own order it took four, and
-// 23 tokens through 2 of 8 experts of 4096 x 14336 took 26 us more.)
+// Inner values lie as they are read: of a chunk lane c's i-th four, 32 c + 4 i, stand beside those
+// of the other lanes, so that a load takes one line of a token.  (In their own order it took four,
+// and 23 tokens through 2 of 8 experts of 4096 x 14336 took 26 us more.)
 __device__ __forceinline__ int64_t inner_at(int64_t k) {
   return (k & ~int64_t(kChunk - 1)) + ((k >> 2 & 7) << 4) + ((k >> 5 & 3) << 2) + (k & 3);
 }
@@ -787,9 +787,9 @@ int dq4_int8_moe(const void* X, int64_t row_stride, int32_t dtype, int64_t T, in
   if (T == 0) return DQ4_OK;
   if (H == 0 || I == 0) return DQ4_ERR_N;
   if (!X || !logits || !W1 || !S1 || !W2 || !S2 || !ids || !weights || !Y) return DQ4_ERR_NULL;
-  if (misaligned(X, 16) || (T > 1 && row_stride % 8 != 0) || misaligned(logits, 4) || misaligned(W1, 16) ||
-      misaligned(W2, 16) || misaligned(S1, 4) || misaligned(S2, 4) || misaligned(ids, 4) ||
-      misaligned(weights, 4) || misaligned(Y, 2) || misaligned(bad, 4))
+  if (misaligned(X, 16) || (T > 1 && row_stride % 8 != 0) || misaligned(logits, 4) ||
+      misaligned(W1, 16) || misaligned(W2, 16) || misaligned(S1, 4) || misaligned(S2, 4) ||
+      misaligned(ids, 4) || misaligned(weights, 4) || misaligned(Y, 2) || misaligned(bad, 4))
     return DQ4_ERR_ALIGN;
   if (!workspace || workspace_bytes < dq4_int8_moe_workspace_bytes(T, H, I, top_k))
     return DQ4_ERR_WORKSPACE;

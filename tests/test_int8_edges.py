@@ -1,4 +1,4 @@
-"""The operators with 8-bit weights without a GPU: refusals that test_int8_layers.py does not have."""
+"""The operators with 8-bit weights without a GPU: what test_int8_layers.py does not ask."""
 
 import pytest
 
@@ -42,9 +42,9 @@ def test_thresholds_keep_their_side():
 
 
 def test_moe_single_row_has_no_stride(lib):
-    """The stride to a next row says nothing where there is none (the next check is the workspace's)."""
+    """The stride to a next row says nothing where there is none (the workspace is checked next)."""
     def call(T, stride, X=P):
-        return lib.dq4_int8_moe(X, stride, 0, T, 64, 32, 8, P, 2, 1, P, P, P, P, P, P, P, None, 0, P,
-                                None)
+        return lib.dq4_int8_moe(X, stride, 0, T, 64, 32, 8, P, 2, 1, P, P, P, P, P, P, P, None, 0,
+                                P, None)
     assert call(1, 1) == call(1, 64) == call(2, 64) == WORKSPACE
     assert call(2, 1) == call(2, 68) == call(1, 1, P + 8) == ALIGN
